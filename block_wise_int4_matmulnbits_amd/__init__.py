@@ -1,5 +1,5 @@
-"""Python binding of libmnb, the block-wise INT4 MatMulNBits decode GEMV for
-MI355X (gfx950).
+"""Python binding of libmnb, the block-wise INT4 MatMulNBits products, 8-bit
+products and 4-bit expert layers for MI355X (gfx950).
 
 Argument marshalling only: every step of the computation runs in the HIP
 kernels of ``libmnb.so`` (built in-tree by ``build.py``).  Functions carry the
@@ -18,9 +18,16 @@ LIB_PATH = os.path.join(_HERE, "libmnb.so")
 
 MNB_F16 = 0
 MNB_BF16 = 1
+MNB_F32 = 2              # router logits of moe_nbits
+MNB_I8 = 3               # quantised rows of matmul_int8
 MNB_MAX_M = 8            # decode kernels; prefill up to MNB_MAX_ROWS
 MNB_MAX_ROWS = 1 << 20
 MNB_MAX_SPLIT_WORKSPACE = 32 << 20   # bytes of K-split partial sums a default plan may take
+MNB_MAX_K_INT8 = 131056
+MNB_MOE_MAX_TOKENS = 64
+MNB_MOE_MAX_EXPERTS = 512
+MNB_MOE_MAX_TOP_K = 16
+MNB_MOE_MAX_WIDTH = 65536
 MNB_LAYOUT_NATURAL = 0   # stored weight layouts (mnb_repack_weights)
 MNB_LAYOUT_EVEN_ODD = 1
 
@@ -28,6 +35,7 @@ STATUS = {
     0: "MNB_OK", 1: "MNB_ERR_NULL", 2: "MNB_ERR_SHAPE", 3: "MNB_ERR_BLOCK",
     4: "MNB_ERR_DTYPE", 5: "MNB_ERR_ALIGN", 6: "MNB_ERR_M_RANGE",
     7: "MNB_ERR_HIP", 8: "MNB_ERR_ALIAS", 9: "MNB_ERR_PLAN", 10: "MNB_ERR_LAYOUT",
+    11: "MNB_ERR_WORKSPACE",
 }
 
 
@@ -80,13 +88,22 @@ class mnb_kernel_info(ctypes.Structure):
         return {f: getattr(self, f) for f, _ in self._fields_}
 
 
+class mnb_moe_weights(ctypes.Structure):
+    _fields_ = [("experts", ctypes.c_int64), ("hidden", ctypes.c_int64), ("inter", ctypes.c_int64),
+                ("gate_up", ctypes.c_void_p), ("gate_up_scales", ctypes.c_void_p),
+                ("gate_up_zero_points", ctypes.c_void_p),
+                ("down", ctypes.c_void_p), ("down_scales", ctypes.c_void_p),
+                ("down_zero_points", ctypes.c_void_p), ("block", ctypes.c_int32)]
+
+
 _lock = threading.Lock()
 _lib = None
 
 EXPORTS = ("matmul_nbits", "matmul_nbits_planned", "matmul_nbits_noalloc", "mnb_plan_default",
            "mnb_plan_check", "mnb_counters_get", "mnb_counters_reset",
            "mnb_get_kernel_info", "mnb_status_string", "mnb_last_hip_error",
-           "mnb_abi_version", "mnb_repack_weights")
+           "mnb_abi_version", "mnb_repack_weights", "quantize_rows_int8", "matmul_int8",
+           "mnb_int8_workspace", "moe_nbits", "mnb_moe_workspace")
 
 
 def lib():
@@ -128,6 +145,18 @@ def lib():
         L.mnb_abi_version.argtypes = []
         L.mnb_repack_weights.restype = i32
         L.mnb_repack_weights.argtypes = [vp, i32, vp, i32, i64, i64, vp]
+        L.quantize_rows_int8.restype = i32
+        L.quantize_rows_int8.argtypes = [vp, i32, i64, i64, vp, vp, vp]
+        L.matmul_int8.restype = i32
+        L.matmul_int8.argtypes = [vp, i32, vp, i64, i64, i64, vp, vp, vp, vp, i32, vp,
+                                  ctypes.c_size_t, vp]
+        L.mnb_int8_workspace.restype = ctypes.c_size_t
+        L.mnb_int8_workspace.argtypes = [i32, i64, i64, i64]
+        L.moe_nbits.restype = i32
+        L.moe_nbits.argtypes = [vp, i32, i64, vp, i32, i32, i32, ctypes.POINTER(mnb_moe_weights),
+                                vp, i32, vp, vp, vp, ctypes.c_size_t, vp]
+        L.mnb_moe_workspace.restype = ctypes.c_size_t
+        L.mnb_moe_workspace.argtypes = [i64, i64, i64, i64, i32]
         _lib = L
         return L
 
@@ -248,6 +277,184 @@ def mnb_repack_weights(src, src_layout, dst, dst_layout, stream=None):
                               _stream_handle(stream, src.device))
     _check(st, L)
     return dst
+
+
+# ------------------------------------------- 8-bit products and expert layers
+def _device_of(named):
+    """The one GPU that all the given (name, tensor) pairs are on; every
+    tensor must be contiguous."""
+    device = None
+    for name, t in named:
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError("%s must be on the GPU" % name)
+        if device is None:
+            device = t.device
+        elif t.device != device:
+            raise ValueError("%s is on %s, not on %s" % (name, t.device, device))
+        if not t.is_contiguous():
+            raise ValueError("%s must be contiguous" % name)
+    return device
+
+
+def _expect(name, t, shape, *dtypes):
+    if t.dtype not in dtypes:
+        raise TypeError("%s must be %s, got %s" % (name, " or ".join(str(d) for d in dtypes), t.dtype))
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError("%s must be %s, got %s" % (name, list(shape), list(t.shape)))
+
+
+def _launch(device, stream, workspace, need, call):
+    """call(workspace address, workspace bytes, stream handle) with ``device``
+    current.  Without a workspace of the caller's, one is taken from torch's
+    allocator on the call's stream (inside a graph capture: from the graph's
+    own pool), so calls on several streams and captured graphs never share
+    one."""
+    import torch
+    L = lib()
+    if torch.cuda.current_device() != device.index:
+        with torch.cuda.device(device):
+            return _launch(device, stream, workspace, need, call)
+    size = 0
+    if workspace is not None:
+        if workspace.device != device or not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous tensor on %s" % device)
+        size = workspace.numel() * workspace.element_size()
+    elif need:
+        if stream is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=device)
+        else:
+            on = torch.cuda.ExternalStream(stream, device=device) if isinstance(stream, int) else stream
+            with torch.cuda.stream(on):
+                workspace = torch.empty(need, dtype=torch.uint8, device=device)
+        size = need
+    _check(call(workspace.data_ptr() if size else None, size, _stream_handle(stream, device)), L)
+
+
+def quantize_rows_int8(A, q, scales, stream=None):
+    """Rows of A to 8-bit integers with one scale per row: scales[r] =
+    max|A[r]| / 127 and q[r] = rint(127 A[r] / max|A[r]|).
+
+    A: fp16/bf16 [m, K], K a multiple of 16; q: int8 [m, K]; scales: fp32 [m].
+    Queued on ``stream`` (default: torch's current stream on A's device);
+    returns ``(q, scales)``.
+    """
+    import torch
+    L = lib()
+    if A.dim() != 2:
+        raise ValueError("A must be 2-D")
+    m, K = A.shape
+    device = _device_of((("A", A), ("q", q), ("scales", scales)))
+    _expect("q", q, (m, K), torch.int8)
+    _expect("scales", scales, (m,), torch.float32)
+    a_dt = _dtype_code(A)
+    _launch(device, stream, None, 0, lambda ws, size, s: L.quantize_rows_int8(
+        A.data_ptr(), a_dt, m, K, q.data_ptr(), scales.data_ptr(), s))
+    return q, scales
+
+
+def matmul_int8(A, a_scales, B, b_scales, bias, out, workspace=None, stream=None):
+    """out[m, N] = (A_q[m, K] @ B[N, K]^T) * a_scales[m] * b_scales[N] + bias[N].
+
+    A: int8 [m, K] with a_scales fp32 [m], or fp16/bf16 [m, K] with a_scales
+    None (quantised in the call by quantize_rows_int8's rule); K a multiple of
+    16; B: int8 [N, K]; b_scales: fp32 [N]; bias: fp32 [N] or None; out:
+    fp16/bf16 [m, N], fully overwritten.  workspace: a tensor of at least
+    mnb_int8_workspace(...) bytes, or None for one of torch's allocator.
+    Queued on ``stream``; returns ``out``.
+    """
+    import torch
+    L = lib()
+    if A.dim() != 2 or B.dim() != 2:
+        raise ValueError("A and B must be 2-D")
+    m, K = A.shape
+    N = B.shape[0]
+    device = _device_of((("A", A), ("a_scales", a_scales), ("B", B), ("b_scales", b_scales), ("bias", bias),
+                         ("out", out)))
+    _expect("B", B, (N, K), torch.int8)
+    _expect("b_scales", b_scales, (N,), torch.float32)
+    _expect("out", out, (m, N), torch.float16, torch.bfloat16)
+    if bias is not None:
+        _expect("bias", bias, (N,), torch.float32)
+    if A.dtype == torch.int8:
+        a_dt = MNB_I8
+        if a_scales is None:
+            raise ValueError("int8 rows need a_scales")
+        _expect("a_scales", a_scales, (m,), torch.float32)
+    else:
+        a_dt = _dtype_code(A)
+        if a_scales is not None:
+            raise ValueError("a_scales must be None with fp16 or bf16 rows")
+    need = L.mnb_int8_workspace(a_dt, m, K, N) if workspace is None else 0
+    _launch(device, stream, workspace, need, lambda ws, size, s: L.matmul_int8(
+        A.data_ptr(), a_dt, None if a_scales is None else a_scales.data_ptr(), m, K, N, B.data_ptr(),
+        b_scales.data_ptr(), None if bias is None else bias.data_ptr(), out.data_ptr(), _dtype_code(out),
+        ws, size, s))
+    return out
+
+
+def mnb_int8_workspace(a_dtype, m, K, N):
+    """Workspace bytes of matmul_int8 (a_dtype: MNB_I8, MNB_F16 or MNB_BF16)."""
+    return lib().mnb_int8_workspace(a_dtype, m, K, N)
+
+
+def moe_nbits(x, router_logits, gate_up, gate_up_scales, gate_up_zero_points, down, down_scales, down_zero_points,
+              out, top_k, renormalize=True, expert_ids=None, expert_weights=None, block=32, workspace=None,
+              stream=None):
+    """out[T, H] = the weighted sum of each token's top_k experts, Down(silu(Gate x) * Up x).
+
+    x: fp16/bf16 [T, H], T <= MNB_MOE_MAX_TOKENS; router_logits: fp32, fp16 or
+    bf16 [T, E]; gate_up: uint8 [E, 2I, H/2] (the gate's rows first) with
+    scales fp16 [E, 2I, H/32] and zero points uint8 [E, 2I, ceil(H/64)] or
+    None; down: uint8 [E, H, I/2], likewise; out: fp16/bf16 [T, H], fully
+    overwritten.  expert_ids: int32 [T, top_k] and expert_weights: fp32
+    [T, top_k] receive the routing where given.  workspace: a tensor of at
+    least mnb_moe_workspace(...) bytes, or None for one of torch's
+    allocator.  Queued on ``stream``; returns ``out``.
+    """
+    import torch
+    L = lib()
+    if x.dim() != 2 or router_logits.dim() != 2 or gate_up.dim() != 3 or down.dim() != 3:
+        raise ValueError("x and router_logits must be 2-D, gate_up and down 3-D")
+    T, H = x.shape
+    E, I = gate_up.shape[0], gate_up.shape[1] // 2
+    device = _device_of((("x", x), ("router_logits", router_logits), ("gate_up", gate_up),
+                         ("gate_up_scales", gate_up_scales), ("gate_up_zero_points", gate_up_zero_points),
+                         ("down", down), ("down_scales", down_scales), ("down_zero_points", down_zero_points),
+                         ("out", out), ("expert_ids", expert_ids), ("expert_weights", expert_weights)))
+    _expect("router_logits", router_logits, (T, E), torch.float32, torch.float16, torch.bfloat16)
+    _expect("gate_up", gate_up, (E, 2 * I, H // 2), torch.uint8)
+    _expect("gate_up_scales", gate_up_scales, (E, 2 * I, H // 32), torch.float16)
+    _expect("down", down, (E, H, I // 2), torch.uint8)
+    _expect("down_scales", down_scales, (E, H, I // 32), torch.float16)
+    _expect("out", out, (T, H), torch.float16, torch.bfloat16)
+    if gate_up_zero_points is not None:
+        _expect("gate_up_zero_points", gate_up_zero_points, (E, 2 * I, (H // 32 + 1) // 2), torch.uint8)
+    if down_zero_points is not None:
+        _expect("down_zero_points", down_zero_points, (E, H, (I // 32 + 1) // 2), torch.uint8)
+    if expert_ids is not None:
+        _expect("expert_ids", expert_ids, (T, top_k), torch.int32)
+    if expert_weights is not None:
+        _expect("expert_weights", expert_weights, (T, top_k), torch.float32)
+
+    def address(t):
+        return None if t is None else t.data_ptr()
+
+    w = mnb_moe_weights(E, H, I, gate_up.data_ptr(), gate_up_scales.data_ptr(), address(gate_up_zero_points),
+                        down.data_ptr(), down_scales.data_ptr(), address(down_zero_points), block)
+    x_dt, out_dt = _dtype_code(x), _dtype_code(out)
+    l_dt = MNB_F32 if router_logits.dtype == torch.float32 else _dtype_code(router_logits)
+    need = L.mnb_moe_workspace(T, H, I, E, top_k) if workspace is None else 0
+    _launch(device, stream, workspace, need, lambda ws, size, s: L.moe_nbits(
+        x.data_ptr(), x_dt, T, router_logits.data_ptr(), l_dt, top_k, int(bool(renormalize)), ctypes.byref(w),
+        out.data_ptr(), out_dt, address(expert_ids), address(expert_weights), ws, size, s))
+    return out
+
+
+def mnb_moe_workspace(tokens, hidden, inter, experts, top_k):
+    """Workspace bytes of moe_nbits."""
+    return lib().mnb_moe_workspace(tokens, hidden, inter, experts, top_k)
 
 
 def mnb_plan_default(m, K, N, num_cus, wgs_per_cu=0):

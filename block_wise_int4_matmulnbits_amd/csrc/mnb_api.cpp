@@ -103,6 +103,62 @@ void log_plan(int64_t m, int64_t K, int64_t N, int a_dtype, int out_dtype, const
             (long long)launches, fixed_scratch ? " fixed-scratch" : "");
 }
 
+constexpr int kNoDevice = 100;   // hipErrorNoDevice: a build without the kernels
+
+const char* dtype_name(int dtype)
+{
+    static const char* const names[] = {"f16", "bf16", "f32", "i8"};
+    return names[dtype];
+}
+
+// A buffer of a call; null or empty ones overlap nothing.
+struct Span {
+    const void* p;
+    int64_t bytes;
+};
+
+// Whether a written buffer overlaps an input or another written buffer.
+bool aliased(const Span* in, int n_in, const Span* wr, int n_wr)
+{
+    for (int i = 0; i < n_wr; ++i) {
+        for (int j = 0; j < n_in; ++j)
+            if (overlaps(wr[i].p, wr[i].bytes, in[j].p, in[j].bytes)) return true;
+        for (int j = 0; j < i; ++j)
+            if (overlaps(wr[i].p, wr[i].bytes, wr[j].p, wr[j].bytes)) return true;
+    }
+    return false;
+}
+
+// The end of a call that queued `launches` kernels with status e (a hipError_t).
+int finish_launches(int e, int launches)
+{
+    g_launches.fetch_add((uint64_t)launches, std::memory_order_relaxed);
+    if (e != 0) {
+        t_last_hip_error = e;
+        return MNB_ERR_HIP;
+    }
+    g_calls.fetch_add(1, std::memory_order_relaxed);
+    return MNB_OK;
+}
+
+int check_int8_shape(int a_dtype, int64_t m, int64_t K, int64_t N)
+{
+    if (m < 0 || m > MNB_MAX_ROWS) return MNB_ERR_M_RANGE;
+    if (K < 0 || N < 0 || K % 16 || K > MNB_MAX_K_INT8 || N > INT32_MAX) return MNB_ERR_SHAPE;
+    if (a_dtype != MNB_F16 && a_dtype != MNB_BF16 && a_dtype != MNB_I8) return MNB_ERR_DTYPE;
+    return MNB_OK;
+}
+
+int check_moe_shape(int64_t tokens, int64_t hidden, int64_t inter, int64_t experts, int top_k)
+{
+    if (tokens < 0 || tokens > MNB_MOE_MAX_TOKENS) return MNB_ERR_M_RANGE;
+    if (hidden < 32 || hidden % 32 || hidden > MNB_MOE_MAX_WIDTH || inter < 32 || inter % 32 ||
+        inter > MNB_MOE_MAX_WIDTH || experts < 1 || experts > MNB_MOE_MAX_EXPERTS || top_k < 1 ||
+        top_k > MNB_MOE_MAX_TOP_K || top_k > experts)
+        return MNB_ERR_SHAPE;
+    return MNB_OK;
+}
+
 int run(const void* A, int a_dtype, int64_t m, int64_t K, int64_t N,
         const uint8_t* Bpacked, const uint16_t* scales, const uint8_t* zero_points,
         int block, void* out, int out_dtype, void* stream, const mnb_plan* explicit_plan,
@@ -358,6 +414,22 @@ int prefill_plan(const Tiling& t, int64_t m, int64_t K, int64_t N, int num_cus, 
 }
 
 }  // namespace
+
+namespace mnb {
+
+size_t int8_workspace_bytes(int a_dtype, int64_t m, int64_t K, int64_t)
+{
+    if (a_dtype == MNB_I8) return 0;
+    return (size_t)(m * K) + (size_t)(m * 4);   // rows (a multiple of 16 bytes), then scales
+}
+
+size_t moe_workspace_bytes(int64_t T, int64_t H, int64_t I, int64_t E, int top_k)
+{
+    (void)H, (void)E;
+    return (size_t)(T * top_k) * (size_t)(8 + 4 * I);
+}
+
+}  // namespace mnb
 
 extern "C" {
 
@@ -690,6 +762,110 @@ int mnb_repack_weights(const uint8_t* src, int src_layout, uint8_t* dst, int dst
     return MNB_OK;
 }
 
+int quantize_rows_int8(const void* A, int a_dtype, int64_t m, int64_t K, int8_t* q, float* scales, void* stream)
+{
+    if (m < 0 || m > MNB_MAX_ROWS) return MNB_ERR_M_RANGE;
+    if (K < 0 || K % 16 || K > MNB_MAX_K) return MNB_ERR_SHAPE;
+    if (a_dtype != MNB_F16 && a_dtype != MNB_BF16) return MNB_ERR_DTYPE;
+    if (m == 0) return finish_launches(0, 0);
+    if (!scales || (K > 0 && (!A || !q))) return MNB_ERR_NULL;
+    if (((uintptr_t)A & 15) || ((uintptr_t)q & 15) || ((uintptr_t)scales & 3)) return MNB_ERR_ALIGN;
+    const Span in[] = {{A, m * K * 2}}, wr[] = {{q, m * K}, {scales, m * 4}};
+    if (aliased(in, 1, wr, 2)) return MNB_ERR_ALIAS;
+    if (log_enabled())
+        fprintf(stderr, "mnb: quantize_rows_int8 m=%lld K=%lld a=%s launches=1\n", (long long)m, (long long)K,
+                dtype_name(a_dtype));
+    if (!mnb::launch_quantize_rows) return finish_launches(kNoDevice, 0);
+    const int e = mnb::launch_quantize_rows(A, a_dtype == MNB_BF16, m, K, q, scales, stream);
+    return finish_launches(e, 1);
+}
+
+size_t mnb_int8_workspace(int a_dtype, int64_t m, int64_t K, int64_t N)
+{
+    if (check_int8_shape(a_dtype, m, K, N) != MNB_OK || m == 0 || N == 0) return 0;
+    return mnb::int8_workspace_bytes(a_dtype, m, K, N);
+}
+
+int matmul_int8(const void* A, int a_dtype, const float* a_scales, int64_t m, int64_t K, int64_t N,
+                const int8_t* B, const float* b_scales, const float* bias, void* out, int out_dtype,
+                void* workspace, size_t workspace_bytes, void* stream)
+{
+    int st = check_int8_shape(a_dtype, m, K, N);
+    if (st != MNB_OK) return st;
+    if (out_dtype != MNB_F16 && out_dtype != MNB_BF16) return MNB_ERR_DTYPE;
+    if (m == 0 || N == 0) return finish_launches(0, 0);
+    const bool rows8 = a_dtype == MNB_I8;
+    if (!out || !b_scales || (K > 0 && (!A || !B)) || (rows8 && !a_scales)) return MNB_ERR_NULL;
+    if (((uintptr_t)A & 15) || ((uintptr_t)B & 15) || ((uintptr_t)a_scales & 3) || ((uintptr_t)b_scales & 3) ||
+        ((uintptr_t)bias & 3) || ((uintptr_t)out & 1) || ((uintptr_t)workspace & 15))
+        return MNB_ERR_ALIGN;
+    const size_t need = mnb::int8_workspace_bytes(a_dtype, m, K, N);
+    if (need && !workspace) return MNB_ERR_NULL;
+    if (need > workspace_bytes) return MNB_ERR_WORKSPACE;
+    const Span in[] = {{A, m * K * (rows8 ? 1 : 2)}, {rows8 ? a_scales : nullptr, m * 4}, {B, N * K},
+                       {b_scales, N * 4}, {bias, N * 4}};
+    const Span wr[] = {{out, m * N * 2}, {workspace, (int64_t)need}};
+    if (aliased(in, 5, wr, 2)) return MNB_ERR_ALIAS;
+    if (!mnb::launch_int8) return finish_launches(kNoDevice, 0);
+    const mnb::Int8Args args{A, a_scales, B, b_scales, bias, out, m, K, N, a_dtype, out_dtype == MNB_BF16, workspace};
+    int launches = 0;
+    const int e = mnb::launch_int8(args, stream, &launches);
+    if (log_enabled())
+        fprintf(stderr, "mnb: matmul_int8 m=%lld K=%lld N=%lld a=%s out=%s bias=%d launches=%d\n", (long long)m,
+                (long long)K, (long long)N, dtype_name(a_dtype), dtype_name(out_dtype), bias != nullptr, launches);
+    return finish_launches(e, launches);
+}
+
+size_t mnb_moe_workspace(int64_t tokens, int64_t hidden, int64_t inter, int64_t experts, int top_k)
+{
+    if (check_moe_shape(tokens, hidden, inter, experts, top_k) != MNB_OK || tokens == 0) return 0;
+    return mnb::moe_workspace_bytes(tokens, hidden, inter, experts, top_k);
+}
+
+int moe_nbits(const void* x, int x_dtype, int64_t tokens, const void* router_logits, int logits_dtype, int top_k,
+              int renormalize, const mnb_moe_weights* weights, void* out, int out_dtype, int32_t* expert_ids,
+              float* expert_weights, void* workspace, size_t workspace_bytes, void* stream)
+{
+    if (!weights) return MNB_ERR_NULL;
+    const mnb_moe_weights& w = *weights;
+    int st = check_moe_shape(tokens, w.hidden, w.inter, w.experts, top_k);
+    if (st != MNB_OK) return st;
+    if (w.block != 32) return MNB_ERR_BLOCK;
+    if ((x_dtype != MNB_F16 && x_dtype != MNB_BF16) || (out_dtype != MNB_F16 && out_dtype != MNB_BF16) ||
+        (logits_dtype != MNB_F32 && logits_dtype != MNB_F16 && logits_dtype != MNB_BF16))
+        return MNB_ERR_DTYPE;
+    if (tokens == 0) return finish_launches(0, 0);
+    if (!x || !router_logits || !w.gate_up || !w.gate_up_scales || !w.down || !w.down_scales || !out || !workspace)
+        return MNB_ERR_NULL;
+    const int64_t lsize = logits_dtype == MNB_F32 ? 4 : 2;
+    if (((uintptr_t)x & 15) || ((uintptr_t)router_logits & (lsize - 1)) || ((uintptr_t)w.gate_up & 15) ||
+        ((uintptr_t)w.gate_up_scales & 1) || ((uintptr_t)w.down & 15) || ((uintptr_t)w.down_scales & 1) ||
+        ((uintptr_t)out & 1) || ((uintptr_t)expert_ids & 3) || ((uintptr_t)expert_weights & 3) ||
+        ((uintptr_t)workspace & 15))
+        return MNB_ERR_ALIGN;
+    const size_t need = mnb::moe_workspace_bytes(tokens, w.hidden, w.inter, w.experts, top_k);
+    if (need > workspace_bytes) return MNB_ERR_WORKSPACE;
+    const int64_t E = w.experts, H = w.hidden, I = w.inter, hb = H / 32, ib = I / 32;
+    const Span in[] = {{x, tokens * H * 2}, {router_logits, tokens * E * lsize},
+                       {w.gate_up, E * I * H}, {w.gate_up_scales, E * 2 * I * hb * 2},
+                       {w.gate_up_zero_points, E * 2 * I * ((hb + 1) / 2)},
+                       {w.down, E * H * (I / 2)}, {w.down_scales, E * H * ib * 2},
+                       {w.down_zero_points, E * H * ((ib + 1) / 2)}};
+    const Span wr[] = {{out, tokens * H * 2}, {expert_ids, tokens * top_k * 4}, {expert_weights, tokens * top_k * 4},
+                       {workspace, (int64_t)need}};
+    if (aliased(in, 8, wr, 4)) return MNB_ERR_ALIAS;
+    if (!mnb::launch_moe) return finish_launches(kNoDevice, 0);
+    const mnb::MoeArgs args{x, router_logits, w, out, expert_ids, expert_weights, (int32_t)tokens, top_k,
+                            x_dtype == MNB_BF16, logits_dtype, renormalize != 0, out_dtype == MNB_BF16, workspace};
+    int launches = 0;
+    const int e = mnb::launch_moe(args, stream, &launches);
+    if (log_enabled())
+        fprintf(stderr, "mnb: moe_nbits tokens=%lld hidden=%lld inter=%lld experts=%lld top_k=%d x=%s logits=%s "
+                "out=%s launches=%d\n", (long long)tokens, (long long)H, (long long)I, (long long)E, top_k,
+                dtype_name(x_dtype), dtype_name(logits_dtype), dtype_name(out_dtype), launches);
+    return finish_launches(e, launches);
+}
+
 void mnb_counters_get(mnb_counters* out)
 {
     if (!out) return;
@@ -729,16 +905,16 @@ const char* mnb_status_string(int status)
     switch (status) {
     case MNB_OK: return "ok";
     case MNB_ERR_NULL: return "a required pointer is NULL";
-    case MNB_ERR_SHAPE: return "bad shape (K must be a non-negative multiple of 32, N >= 0, within limits)";
+    case MNB_ERR_SHAPE: return "bad shape (matmul_nbits: K must be a non-negative multiple of 32, N >= 0, within limits)";
     case MNB_ERR_BLOCK: return "block size must be 32";
-    case MNB_ERR_DTYPE: return "dtype must be MNB_F16 or MNB_BF16";
-    case MNB_ERR_ALIGN: return "A and Bpacked must be 16-byte aligned, scales and out 2-byte aligned";
-    case MNB_ERR_M_RANGE: return "m must be in [0, MNB_MAX_ROWS]";
+    case MNB_ERR_DTYPE: return "an element type the call does not take (matmul_nbits: MNB_F16 or MNB_BF16)";
+    case MNB_ERR_ALIGN: return "a buffer is not aligned (matmul_nbits: A and Bpacked to 16 bytes, scales and out to 2)";
+    case MNB_ERR_M_RANGE: return "m must be in [0, MNB_MAX_ROWS], tokens of the expert layer in [0, MNB_MOE_MAX_TOKENS]";
     case MNB_ERR_HIP: return "HIP runtime error (see mnb_last_hip_error)";
-    case MNB_ERR_ALIAS: return "out overlaps an input";
+    case MNB_ERR_ALIAS: return "a written buffer overlaps an input or another written buffer";
     case MNB_ERR_PLAN: return "launch plan not supported";
     case MNB_ERR_LAYOUT: return "unknown weight layout";
-    case MNB_ERR_WORKSPACE: return "the plan needs more workspace than matmul_nbits_noalloc's fixed buffer holds";
+    case MNB_ERR_WORKSPACE: return "the call needs more workspace than it was given (matmul_nbits_noalloc: than its fixed buffer holds)";
     }
     return "unknown status";
 }

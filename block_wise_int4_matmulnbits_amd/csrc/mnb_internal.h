@@ -1,5 +1,5 @@
 // Internal interface between the host front end (mnb_api.cpp, plain C++)
-// and the HIP side (mnb_gemv.hip).  Not installed; not part of the C ABI.
+// and the HIP side (mnb_gemv.hip and the other .hip files).  Not installed; not part of the C ABI.
 #pragma once
 
 #include <stddef.h>
@@ -97,5 +97,50 @@ int64_t gemv_lds_bytes(int64_t m, int64_t N, const mnb_plan& plan, int32_t* tcap
 // Code-object facts of the variant (m, K and the plan select it).  Returns a hipError_t, or -1 when no
 // variant matches.
 int kernel_info(int64_t m, int64_t K, const mnb_plan& plan, mnb_kernel_info* info);
+
+// The launchers below are weak: a build of the front end alone (the host-only
+// builds of the tests) links without them, and its calls report that no
+// device is present.
+#define MNB_WEAK __attribute__((weak))
+
+// 8-bit products (mnb_int8.hip).  Arguments have passed the front end's
+// checks; m, N > 0.  Each returns a hipError_t and, in *launches, the kernels
+// it queued.
+struct Int8Args {
+    const void* A;           // [m][K], a_dtype
+    const float* a_scales;   // [m] with MNB_I8 rows
+    const int8_t* B;         // [N][K]
+    const float* b_scales;   // [N]
+    const float* bias;       // [N] or null
+    void* out;               // [m][N]
+    int64_t m, K, N;
+    int a_dtype, out_bf16;
+    void* ws;                // int8_workspace_bytes()
+};
+int launch_quantize_rows(const void* A, int a_bf16, int64_t m, int64_t K, int8_t* q, float* scales, void* stream)
+    MNB_WEAK;
+int launch_int8(const Int8Args& args, void* stream, int* launches) MNB_WEAK;
+
+// Workspace of an 8-bit product: the quantised rows and their scales where the
+// rows come as fp16 or bf16.  Host-only arithmetic (mnb_api.cpp).
+size_t int8_workspace_bytes(int a_dtype, int64_t m, int64_t K, int64_t N);
+
+// The expert layer (mnb_moe.hip).
+struct MoeArgs {
+    const void* x;           // [T][H]
+    const void* logits;      // [T][E]
+    mnb_moe_weights w;
+    void* out;               // [T][H]
+    int32_t* ids;            // [T][top_k] or null
+    float* probs;            // [T][top_k] or null
+    int32_t T, top_k;
+    int x_bf16, logits_dtype, renormalize, out_bf16;
+    void* ws;                // moe_workspace_bytes()
+};
+int launch_moe(const MoeArgs& args, void* stream, int* launches) MNB_WEAK;
+
+// Workspace of the expert layer: see MoeLayout in mnb_moe.hip.  Host-only
+// arithmetic (mnb_api.cpp).
+size_t moe_workspace_bytes(int64_t T, int64_t H, int64_t I, int64_t E, int top_k);
 
 }  // namespace mnb

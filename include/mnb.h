@@ -32,10 +32,11 @@
 extern "C" {
 #endif
 
-#define MNB_ABI_VERSION 6
+#define MNB_ABI_VERSION 7
 
-/* Element types of A and of the output. */
-typedef enum { MNB_F16 = 0, MNB_BF16 = 1 } mnb_dtype;
+/* Element types.  matmul_nbits takes MNB_F16 and MNB_BF16; the 8-bit product
+ * also takes MNB_I8 rows and the expert layer MNB_F32 router logits. */
+typedef enum { MNB_F16 = 0, MNB_BF16 = 1, MNB_F32 = 2, MNB_I8 = 3 } mnb_dtype;
 
 /* Status codes.  On any code other than MNB_OK nothing was launched, except
  * MNB_ERR_HIP, which reports that the HIP launch itself failed. */
@@ -44,17 +45,19 @@ typedef enum {
     MNB_ERR_NULL = 1,     /* a required pointer is NULL                      */
     MNB_ERR_SHAPE = 2,    /* K < 0, N < 0, K not a multiple of 32, too large  */
     MNB_ERR_BLOCK = 3,    /* block != 32                                     */
-    MNB_ERR_DTYPE = 4,    /* a_dtype or out_dtype not MNB_F16 / MNB_BF16      */
+    MNB_ERR_DTYPE = 4,    /* an element type the call does not take           */
     MNB_ERR_ALIGN = 5,    /* A or Bpacked not 16-byte aligned, scales or out
                              not 2-byte aligned                              */
-    MNB_ERR_M_RANGE = 6,  /* m < 0 or m > MNB_MAX_ROWS                        */
+    MNB_ERR_M_RANGE = 6,  /* m < 0 or m > MNB_MAX_ROWS (tokens of the expert
+                             layer: > MNB_MOE_MAX_TOKENS)                     */
     MNB_ERR_HIP = 7,      /* the HIP runtime reported an error; see
                              mnb_last_hip_error()                            */
     MNB_ERR_ALIAS = 8,    /* out overlaps an input buffer                    */
     MNB_ERR_PLAN = 9,     /* an explicit plan is not one the library runs   */
     MNB_ERR_LAYOUT = 10,  /* unknown weight layout                            */
     MNB_ERR_WORKSPACE = 11 /* matmul_nbits_noalloc: the plan needs more than its
-                              fixed workspace (MNB_MAX_SPLIT_WORKSPACE)       */
+                              fixed workspace (MNB_MAX_SPLIT_WORKSPACE); calls
+                              that take a workspace: it is too small          */
 } mnb_status;
 
 /*
@@ -278,10 +281,154 @@ int mnb_repack_weights(const uint8_t* src, int src_layout, uint8_t* dst, int dst
                        int64_t N, int64_t K, void* stream);
 
 /*
+ * quantize_rows_int8 -- rows of activations to 8-bit integers with one scale
+ * per row, one launch on `stream`:
+ *
+ *   scale[r] = max_k |a[r][k]| / 127,   q[r][k] = rint(127 a[r][k] / max_k |a[r][k]|)
+ *
+ * with the exact quotient rounded to the nearest integer, ties to even (the
+ * scale is rounded to fp32 once).  q lies in [-127, 127].  A row of zeros
+ * gives scale 0 and q 0; a row with an infinity or a NaN gives a NaN scale
+ * and q 0, so that every product with it is NaN.
+ *
+ *   A        device, [m][K] row-major, fp16 or bf16 per a_dtype; 16-byte
+ *            aligned.
+ *   m, K     0 <= m <= MNB_MAX_ROWS; K a multiple of 16, 0 <= K <= MNB_MAX_K
+ *            (K == 0 gives scale 0).
+ *   q        device, [m][K] int8; 16-byte aligned.
+ *   scales   device, [m] fp32; 4-byte aligned.
+ *   stream   hipStream_t, or NULL for the default stream.
+ *
+ * q and scales must not overlap A or each other.  Asynchronous; allocates
+ * nothing.  The results depend on the row alone (not on m or the device).
+ */
+int quantize_rows_int8(const void* A, int a_dtype, int64_t m, int64_t K, int8_t* q, float* scales,
+                       void* stream);
+
+/* Largest K of the 8-bit product: every partial sum of K products of two
+ * 8-bit integers stays below 2^31 (K * 128 * 128 < 2^31; K is a multiple of
+ * 16). */
+#define MNB_MAX_K_INT8 131056
+
+/*
+ * matmul_int8 -- product of 8-bit rows and 8-bit weights:
+ *
+ *   out[r][n] = (sum_k q[r][k] w[n][k]) * a_scales[r] * b_scales[n] + bias[n]
+ *
+ *   A            device, [m][K] row-major; 16-byte aligned.  MNB_I8: the rows
+ *                q themselves.  MNB_F16 / MNB_BF16: activations, quantised
+ *                within the call by quantize_rows_int8's rule (same bits as
+ *                that call followed by this one).
+ *   a_scales     device, [m] fp32, 4-byte aligned, with MNB_I8; NULL otherwise
+ *                (the call derives the scales).
+ *   m, K, N      0 <= m <= MNB_MAX_ROWS; K a multiple of 16, 0 <= K <=
+ *                MNB_MAX_K_INT8; 0 <= N <= INT32_MAX.
+ *   B            device, [N][K] int8, row-major; 16-byte aligned.  All 256
+ *                values are taken, here and in A.
+ *   b_scales     device, [N] fp32; 4-byte aligned.
+ *   bias         device, [N] fp32, 4-byte aligned; NULL for none.
+ *   out          device, [m][N] row-major, fp16 or bf16 per out_dtype; 2-byte
+ *                aligned; every element is overwritten.
+ *   workspace    device, mnb_int8_workspace(a_dtype, m, K, N) bytes at least,
+ *                16-byte aligned (NULL where that is 0); its contents need no
+ *                preparation and mean nothing afterwards.  Calls whose work
+ *                may overlap need a workspace each (a captured graph keeps the
+ *                one it was captured with).
+ *   stream       hipStream_t, or NULL for the default stream.
+ *
+ * Numerics: the integer sum is exact (int32), converted to fp32 (one
+ * rounding), multiplied by b_scales[n] and then a_scales[r] in fp32, the bias
+ * added in fp32, and the result rounded once to fp16 or bf16 (RNE).  The bits
+ * do not depend on m, N, the plan or the device.  out and workspace must not
+ * overlap the inputs or each other.  Asynchronous; allocates nothing; one or
+ * two launches.
+ */
+int matmul_int8(const void* A, int a_dtype, const float* a_scales, int64_t m, int64_t K, int64_t N,
+                const int8_t* B, const float* b_scales, const float* bias, void* out, int out_dtype,
+                void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace bytes matmul_int8 needs for these arguments (0 for none, or where
+ * matmul_int8 would reject them).  Host-only. */
+size_t mnb_int8_workspace(int a_dtype, int64_t m, int64_t K, int64_t N);
+
+/* Bounds of the expert layer. */
+#define MNB_MOE_MAX_TOKENS 64
+#define MNB_MOE_MAX_EXPERTS 512
+#define MNB_MOE_MAX_TOP_K 16
+#define MNB_MOE_MAX_WIDTH 65536   /* hidden and inter */
+
+/* Weights of a mixture-of-experts layer: per expert a fused gate and up
+ * matrix and a down matrix, each in matmul_nbits' natural layout (packed
+ * 4-bit weights in blocks of 32 along the reduction, an fp16 scale and a
+ * 4-bit zero point per block), experts one after another. */
+typedef struct {
+    int64_t experts;   /* 1 .. MNB_MOE_MAX_EXPERTS                                     */
+    int64_t hidden;    /* H: multiple of 32, 32 .. MNB_MOE_MAX_WIDTH                   */
+    int64_t inter;     /* I: multiple of 32, 32 .. MNB_MOE_MAX_WIDTH                   */
+    const uint8_t* gate_up;               /* device, [experts][2 I][H/2]: rows 0 .. I-1 the
+                                             gate, I .. 2I-1 the up projection; 16-byte aligned */
+    const uint16_t* gate_up_scales;       /* device, [experts][2 I][H/32]; 2-byte aligned */
+    const uint8_t* gate_up_zero_points;   /* device, [experts][2 I][ceil(H/64)], or NULL
+                                             for zero point 8                             */
+    const uint8_t* down;                  /* device, [experts][H][I/2]; 16-byte aligned   */
+    const uint16_t* down_scales;          /* device, [experts][H][I/32]; 2-byte aligned   */
+    const uint8_t* down_zero_points;      /* device, [experts][H][ceil(I/64)], or NULL    */
+    int32_t block;                        /* must be 32                                   */
+} mnb_moe_weights;
+
+/*
+ * moe_nbits -- a mixture-of-experts layer for a few tokens, from the router's
+ * logits to the weighted sum of the experts:
+ *
+ *   out[t] = sum_j p[t][j] * Down_e( silu(Gate_e x[t]) * (Up_e x[t]) ),  e = ids[t][j]
+ *
+ *   x              device, [tokens][H] row-major, fp16 or bf16; 16-byte aligned;
+ *                  finite in fp16 (bf16 is rounded to fp16, as in matmul_nbits).
+ *   tokens         0 .. MNB_MOE_MAX_TOKENS.
+ *   router_logits  device, [tokens][experts], MNB_F32, MNB_F16 or MNB_BF16;
+ *                  aligned to its element.
+ *   top_k          1 .. min(experts, MNB_MOE_MAX_TOP_K).
+ *   renormalize    nonzero: p is the softmax over the selected experts' logits;
+ *                  0: over all experts' logits.
+ *   out            device, [tokens][H], fp16 or bf16; 2-byte aligned.
+ *   expert_ids     device, [tokens][top_k] int32, or NULL: the selected experts.
+ *   expert_weights device, [tokens][top_k] fp32, or NULL: their p.
+ *   workspace      device, mnb_moe_workspace(...) bytes at least, 16-byte
+ *                  aligned; rules as for matmul_int8.
+ *
+ * Routing: the top_k largest logits in falling order, equal logits in rising
+ * order of the expert's number.  An expert whose logit is -infinity is never
+ * selected: where fewer than top_k remain, the rest of the row's ids are -1
+ * and their weights 0, and a token with no expert left (padding) gets a row
+ * of zeros.  A token whose logits hold a NaN or +infinity gets ids -1 and NaN
+ * in its weights and its output row.
+ * Numerics: products of fp16 activations with the exact q - z, summed in fp32
+ * per block and scaled by the block's scale in fp32; softmax, silu and the
+ * sum over the experts in fp32 (in the order of the experts' numbers), one
+ * rounding to fp16 or bf16 (RNE).  The activations between the two products
+ * are held in fp16 with a power-of-two scale per token, expert and block of
+ * 32, so they neither overflow nor lose more than fp16's half step (2^-11)
+ * of the block's largest.
+ * A token's results depend on the batch only through the order in which
+ * fp32 sums run.  Equal calls give equal bits.  out, expert_ids, expert_weights
+ * and workspace must not overlap the inputs or each other.  Asynchronous;
+ * allocates nothing; two launches.
+ */
+int moe_nbits(const void* x, int x_dtype, int64_t tokens, const void* router_logits, int logits_dtype,
+              int top_k, int renormalize, const mnb_moe_weights* weights, void* out, int out_dtype,
+              int32_t* expert_ids, float* expert_weights, void* workspace, size_t workspace_bytes,
+              void* stream);
+
+/* Workspace bytes moe_nbits needs (0 where it would reject the sizes).
+ * Host-only. */
+size_t mnb_moe_workspace(int64_t tokens, int64_t hidden, int64_t inter, int64_t experts, int top_k);
+
+/*
  * Environment: MNB_LOG set to anything but "0" (read once per process)
  * prints one line per call to stderr, once its plan is fixed and before
  * its launches: the shape, the types, whether the plan was explicit or the
- * default, every plan field, and the number of launches.
+ * default, every plan field, and the number of launches (the 8-bit and expert
+ * calls: the operator's name, shape, types and number of launches).
  */
 
 /*
@@ -294,9 +441,10 @@ int mnb_repack_weights(const uint8_t* src, int src_layout, uint8_t* dst, int dst
  * (first page, "Tests" paragraph: the direct-store counter).
  */
 typedef struct {
-    uint64_t calls;                /* matmul_nbits* calls that returned MNB_OK */
+    uint64_t calls;                /* calls of the product, quantising and expert entry
+                                      points that returned MNB_OK              */
     uint64_t launches;             /* kernel launches                          */
-    uint64_t elements_f16;         /* outputs stored as fp16                   */
+    uint64_t elements_f16;         /* matmul_nbits* outputs stored as fp16     */
     uint64_t elements_bf16_direct; /* outputs narrowed and stored as bf16 by the
                                       GEMV epilogue itself                     */
     uint64_t row_batched_launches; /* launches that served m > 1 rows at once  */
