@@ -423,10 +423,27 @@ size_t int8_workspace_bytes(int a_dtype, int64_t m, int64_t K, int64_t)
     return (size_t)(m * K) + (size_t)(m * 4);   // rows (a multiple of 16 bytes), then scales
 }
 
-size_t moe_workspace_bytes(int64_t T, int64_t H, int64_t I, int64_t E, int top_k)
+MoeLayout moe_layout(int64_t T, int64_t H, int64_t I, int64_t E, int top_k)
 {
-    (void)H, (void)E;
-    return (size_t)(T * top_k) * (size_t)(8 + 4 * I);
+    (void)H;
+    const int64_t pairs = T * top_k;
+    MoeLayout l;
+    // Rows of a batch: two quads once the experts see more than four tokens
+    // on average.
+    l.rq = pairs > 4 * E ? 2 : 1;
+    // Every expert has at most one batch that is not full.
+    const int64_t rows = 4 * l.rq;
+    int64_t batches = std::min(pairs, E) + pairs / rows;
+    if (batches > pairs) batches = pairs;
+    l.batches = (int)batches;
+    auto align = [](size_t x) { return (x + 255) & ~(size_t)255; };
+    l.batch_e = align((size_t)(1 + T) * 4);
+    l.row_token = l.batch_e + align((size_t)batches * 4);
+    l.row_p = l.row_token + align((size_t)(batches * rows) * 4);
+    l.hs = l.row_p + align((size_t)(batches * rows) * 4);
+    l.h = l.hs + align((size_t)(batches * rows * (I / 32)) * 4);
+    l.bytes = l.h + (size_t)(batches * rows * I) * 2;
+    return l;
 }
 
 }  // namespace mnb
@@ -819,7 +836,7 @@ int matmul_int8(const void* A, int a_dtype, const float* a_scales, int64_t m, in
 size_t mnb_moe_workspace(int64_t tokens, int64_t hidden, int64_t inter, int64_t experts, int top_k)
 {
     if (check_moe_shape(tokens, hidden, inter, experts, top_k) != MNB_OK || tokens == 0) return 0;
-    return mnb::moe_workspace_bytes(tokens, hidden, inter, experts, top_k);
+    return mnb::moe_layout(tokens, hidden, inter, experts, top_k).bytes;
 }
 
 int moe_nbits(const void* x, int x_dtype, int64_t tokens, const void* router_logits, int logits_dtype, int top_k,
@@ -843,7 +860,7 @@ int moe_nbits(const void* x, int x_dtype, int64_t tokens, const void* router_log
         ((uintptr_t)out & 1) || ((uintptr_t)expert_ids & 3) || ((uintptr_t)expert_weights & 3) ||
         ((uintptr_t)workspace & 15))
         return MNB_ERR_ALIGN;
-    const size_t need = mnb::moe_workspace_bytes(tokens, w.hidden, w.inter, w.experts, top_k);
+    const size_t need = mnb::moe_layout(tokens, w.hidden, w.inter, w.experts, top_k).bytes;
     if (need > workspace_bytes) return MNB_ERR_WORKSPACE;
     const int64_t E = w.experts, H = w.hidden, I = w.inter, hb = H / 32, ib = I / 32;
     const Span in[] = {{x, tokens * H * 2}, {router_logits, tokens * E * lsize},

@@ -135,12 +135,17 @@ struct MoeArgs {
     float* probs;            // [T][top_k] or null
     int32_t T, top_k;
     int x_bf16, logits_dtype, renormalize, out_bf16;
-    void* ws;                // moe_workspace_bytes()
+    void* ws;                // moe_layout().bytes
 };
 int launch_moe(const MoeArgs& args, void* stream, int* launches) MNB_WEAK;
 
-// Workspace of the expert layer: see MoeLayout in mnb_moe.hip.  Host-only
-// arithmetic (mnb_api.cpp).
-size_t moe_workspace_bytes(int64_t T, int64_t H, int64_t I, int64_t E, int top_k);
+// Layout of the expert layer's workspace (byte offsets; the head, the count
+// of batches and a word per token, comes first) and the row quads of a batch.
+// Host-only arithmetic (mnb_api.cpp).
+struct MoeLayout {
+    int rq, batches;         // row quads of a batch; the most batches there can be
+    size_t batch_e, row_token, row_p, hs, h, bytes;
+};
+MoeLayout moe_layout(int64_t T, int64_t H, int64_t I, int64_t E, int top_k);
 
 }  // namespace mnb
