@@ -442,7 +442,7 @@ MoeLayout moe_layout(int64_t T, int64_t H, int64_t I, int64_t E, int top_k)
     l.row_p = l.row_token + align((size_t)(batches * rows) * 4);
     l.hs = l.row_p + align((size_t)(batches * rows) * 4);
     l.h = l.hs + align((size_t)(batches * rows * (I / 32)) * 4);
-    l.bytes = l.h + (size_t)(batches * rows * I) * 2;
+    l.bytes = l.h + (size_t)(batches * rows * ((I / 32 + 15) / 16 * 512)) * 2;   // blocks of I in groups of 16
     return l;
 }
 

@@ -24,9 +24,12 @@
 // Between the launches the activations h = silu(g) u lie in the workspace as
 // fp16, scaled by a power of two per row and block of 32 (so that no h
 // overflows and small ones keep their precision), in the order in which the
-// second launch's lanes load them: [batch][row quad][block][row of 4][32].
+// second launch's lanes load them, 1 KB or less in one piece per load:
+// [batch][row quad][16 blocks][piece of 8][block of 16][row][8], with as many
+// rows as the quad has.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
+#include <algorithm>
 
 #include "mnb.h"
 #include "mnb_device.h"
@@ -35,8 +38,14 @@
 namespace mnb {
 namespace {
 
-constexpr int kMaxPairs = MNB_MOE_MAX_TOKENS * MNB_MOE_MAX_TOP_K;
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+
 constexpr int kMaxSlots = MNB_MOE_MAX_EXPERTS / 64;   // experts per lane of a routing wave
+// First launch: 4 column waves by 2 slices of K, loads two steps ahead.  HBM sets
+// the pace of its loop (5.8 TB/s, 64 KB in flight per CU): 12 waves or three or
+// four steps ahead gained nothing, 16 waves (128 registers) spilled and cost
+// 40%, 4 waves with 4 steps ahead 20%.
+constexpr int kUpWaves = 8, kUpRing = 2;
 constexpr int kPadToken = 255;                        // a batch's unused rows
 
 struct MoeParams {
@@ -52,11 +61,12 @@ struct MoeParams {
     int32_t* batch_e;    // expert of each batch, and its rows << 16
     int32_t* row_token;  // [batch][4 RQ]: token, -1 for unused rows
     float* row_p;        // its weight
-    uint16_t* h;         // [batch][RQ][I/32][4][32]
+    uint16_t* h;         // [batch][RQ], 128 * ceil16(I/32) each: see above
     float* hs;           // [batch][RQ][I/32][4]: powers of two
     int32_t T, H, I, E, top_k;
     int32_t x_bf16, logits_dtype, renormalize, out_bf16;
     int32_t batch_cap;      // batches the workspace holds
+    int32_t h_quad;         // elements of a row quad in h
     int32_t stage_blocks;   // first launch: blocks of K staged in LDS at a time
     uint32_t zero;          // always 0 (see vgpr_constant)
 };
@@ -102,74 +112,96 @@ __device__ __forceinline__ float wave_sum(float f)
     return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(f), 63));
 }
 
-// The routing tables of a workgroup.
+// The routing tables of a workgroup, in dynamic LDS.
 struct Routing {
-    uint64_t mask[MNB_MOE_MAX_EXPERTS];          // tokens that selected expert e
-    uint16_t first[MNB_MOE_MAX_EXPERTS];         // its first batch
-    int16_t sel[kMaxPairs];                      // [t][top_k]: expert, or -1
-    float p[kMaxPairs];
-    uint16_t batch_e[kMaxPairs];
-    uint8_t token[4 * kMaxPairs];                // [batch][4 RQ]
-    int32_t batches;
+    uint64_t* mask;      // [E]: tokens that selected expert e
+    float* p;            // [T][top_k]
+    uint32_t* token4;    // [batch][RQ]: four rows' tokens
+    uint16_t* first;     // [E]: first batch
+    int16_t* sel;        // [T][top_k]: expert, or -1
+    uint16_t* batch_e;   // [batch]
+    __device__ uint8_t* token() const { return reinterpret_cast<uint8_t*>(token4); }   // [batch][4 RQ]
 };
+__host__ __device__ inline uint32_t routing_bytes(int E, int pairs, int cap, int rq)
+{
+    return (uint32_t)(8 * E + 4 * pairs + 4 * cap * rq + 2 * E + 2 * pairs + 2 * cap + 15) & ~15u;
+}
+__device__ __forceinline__ Routing routing_tables(uint8_t* lds, int E, int pairs, int cap, int rq)
+{
+    Routing r;
+    r.mask = reinterpret_cast<uint64_t*>(lds);
+    r.p = reinterpret_cast<float*>(r.mask + E);
+    r.token4 = reinterpret_cast<uint32_t*>(r.p + pairs);
+    r.first = reinterpret_cast<uint16_t*>(r.token4 + cap * rq);
+    r.sel = reinterpret_cast<int16_t*>(r.first + E);
+    r.batch_e = reinterpret_cast<uint16_t*>(r.sel + pairs);
+    return r;
+}
 
-// One wave routes token t.  Logits become 32-bit keys in the order of their
-// values (-0 first becomes +0); 0 marks a selected or missing expert, and
-// no key of -infinity or below is selected.
-__device__ __forceinline__ void route_token(const MoeParams& p, int t, Routing& r)
+// One wave routes token t; lane l holds experts l, 64 + l, ... (NS of them).
+// Logits become 32-bit keys in the order of their values (-0 first becomes
+// +0); 0 marks a selected or missing expert, and no key of -infinity or below
+// is selected.  top_k rounds of a wave maximum: with a few experts per lane a
+// round is some 25 instructions.
+template <int NS>
+__device__ __forceinline__ void route_token(const MoeParams& p, int t, const Routing& r)
 {
     const int lane = threadIdx.x & 63;
-    const int64_t base = (int64_t)t * p.E;
     constexpr uint32_t kNegInf = 0x007FFFFFu;    // the key of -infinity
-    uint32_t key[kMaxSlots];
+    const uint32_t size = p.logits_dtype == MNB_F32 ? 4 : 2;
+    const __amdgpu_buffer_rsrc_t rL =
+        make_rsrc_small(static_cast<const uint8_t*>(p.logits) + (int64_t)t * p.E * size, (uint32_t)p.E * size);
+    uint32_t raw[NS], key[NS];
+    if (size == 4) {
+#pragma unroll
+        for (int i = 0; i < NS; ++i) raw[i] = __builtin_amdgcn_raw_buffer_load_b32(rL, 4 * (64 * i + lane), 0, 0);
+    } else {
+#pragma unroll
+        for (int i = 0; i < NS; ++i) raw[i] = __builtin_amdgcn_raw_buffer_load_b16(rL, 2 * (64 * i + lane), 0, 0);
+    }
     bool bad = false;
 #pragma unroll
-    for (int i = 0; i < kMaxSlots; ++i) {
-        const int e = 64 * i + lane;
-        float l = -__builtin_inff();
-        if (e < p.E)
-            l = p.logits_dtype == MNB_F32 ? static_cast<const float*>(p.logits)[base + e]
-                                          : widen16(static_cast<const uint16_t*>(p.logits)[base + e],
-                                                    p.logits_dtype == MNB_BF16);
-        bad |= !(l < __builtin_inff());
+    for (int i = 0; i < NS; ++i) {
+        const bool there = 64 * i + lane < p.E;
+        const float l = size == 4 ? __uint_as_float(raw[i]) : widen16(raw[i], p.logits_dtype == MNB_BF16);
+        bad |= there && !(l < __builtin_inff());
         const uint32_t b = __float_as_uint(l + 0.0f);
-        key[i] = e < p.E ? b ^ ((b >> 31) ? 0xFFFFFFFFu : 0x80000000u) : 0u;
+        key[i] = there ? b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u) : 0u;
     }
     bad = __any(bad);
-    auto value = [](uint32_t k) { return __uint_as_float(k ^ ((k >> 31) ? 0x80000000u : 0xFFFFFFFFu)); };
+    auto value = [](uint32_t k) { return __uint_as_float(k ^ (~(uint32_t)((int32_t)k >> 31) | 0x80000000u)); };
     float peak = 0.f, mass = 0.f, mine_w = 0.f;
     int mine_e = -1;                             // lane j: slot j
-    for (int j = 0; j < p.top_k; ++j) {
-        uint32_t top = 0;
+    for (int j = 0; j < p.top_k && !bad; ++j) {
+        uint32_t top = key[0];
 #pragma unroll
-        for (int i = 0; i < kMaxSlots; ++i) top = key[i] > top ? key[i] : top;
+        for (int i = 1; i < NS; ++i) top = key[i] > top ? key[i] : top;
         top = wave_max(top);
+        if (top <= kNegInf) break;
         if (j == 0) {
             peak = value(top);
-            if (!p.renormalize && !bad && top > kNegInf) {
+            if (!p.renormalize) {
                 float m = 0.f;
 #pragma unroll
-                for (int i = 0; i < kMaxSlots; ++i)
-                    if (key[i] > kNegInf) m += __expf(value(key[i]) - peak);
+                for (int i = 0; i < NS; ++i) m += key[i] > kNegInf ? __expf(value(key[i]) - peak) : 0.f;
                 mass = wave_sum(m);
             }
         }
-        if (bad || top <= kNegInf) break;
-        int e = -1;
+        int e = 0;
+        bool found = false;
 #pragma unroll
-        for (int i = 0; i < kMaxSlots; ++i) {
+        for (int i = 0; i < NS; ++i) {           // the lowest expert of this value
             const uint64_t at = __ballot(key[i] == top);
-            if (e < 0 && at) {
-                e = 64 * i + __builtin_ctzll(at);
-                if (lane == (e & 63)) key[i] = 0;
-            }
+            const int bit = __builtin_ctzll(at | (1ull << 63));
+            const bool take = !found && at;
+            e = take ? 64 * i + bit : e;
+            key[i] = take && lane == bit ? 0u : key[i];
+            found |= take;
         }
         const float w = __expf(value(top) - peak);
         if (p.renormalize) mass += w;
-        if (lane == j) {
-            mine_e = e;
-            mine_w = w;
-        }
+        mine_e = lane == j ? e : mine_e;
+        mine_w = lane == j ? w : mine_w;
     }
     if (lane < p.top_k) {
         const int s = t * p.top_k + lane;
@@ -180,52 +212,66 @@ __device__ __forceinline__ void route_token(const MoeParams& p, int t, Routing& 
     }
 }
 
+// First batch of every expert, and the count of batches; lane l of a wave takes
+// experts NS l .. NS l + NS - 1.  Every wave does this for itself.
+template <int NS>
+__device__ __forceinline__ int place_batches(const MoeParams& p, int rows, const Routing& r)
+{
+    const int lane = threadIdx.x & 63;
+    int n[NS], sum = 0;
+#pragma unroll
+    for (int i = 0; i < NS; ++i) {
+        const int e = NS * lane + i;
+        n[i] = e < p.E ? ((int)__popcll(r.mask[e]) + rows - 1) / rows : 0;
+        sum += n[i];
+    }
+    uint32_t upto = (uint32_t)sum;               // inclusive sum over the lanes
+    upto += dpp_u32<0x111, 0xF>(upto);
+    upto += dpp_u32<0x112, 0xF>(upto);
+    upto += dpp_u32<0x114, 0xF>(upto);
+    upto += dpp_u32<0x118, 0xF>(upto);
+    upto += dpp_u32<0x142, 0xA>(upto);
+    upto += dpp_u32<0x143, 0xC>(upto);
+    int first = (int)upto - sum;
+#pragma unroll
+    for (int i = 0; i < NS; ++i) {
+        const int e = NS * lane + i;
+        if (e < p.E) r.first[e] = (uint16_t)first;
+        first += n[i];
+    }
+    return __builtin_amdgcn_readlane((int)upto, 63);
+}
+
 // All tokens, the batches in the order of the experts' numbers, and each
-// batch's rows in the order of the tokens.  Workgroup 0 writes the tables for
-// the second launch and the caller's ids and weights.
-template <int RQ>
-__device__ void route(const MoeParams& p, Routing& r)
+// batch's rows in the order of the tokens; the count of batches.  Workgroup 0 writes the tables for
+// the second launch and the caller's ids and weights.  `meanwhile` is run by
+// the waves that have no token to route, before the routing is complete.
+template <int RQ, typename F>
+__device__ __forceinline__ int route(const MoeParams& p, const Routing& r, F meanwhile)
 {
     const int tid = threadIdx.x, threads = blockDim.x;
-    const int wv = __builtin_amdgcn_readfirstlane(tid >> 6), waves = threads >> 6, lane = tid & 63;
+    const int wv = __builtin_amdgcn_readfirstlane(tid >> 6), waves = threads >> 6;
     for (int e = tid; e < p.E; e += threads) r.mask[e] = 0;
+    for (int i = tid; i < p.batch_cap * RQ; i += threads) r.token4[i] = 0xFFFFFFFFu;
     __syncthreads();
-    for (int t = wv; t < p.T; t += waves) route_token(p, t, r);
-    __syncthreads();
-    if (wv == 0) {
-        // Lane l counts the batches of experts 8 l .. 8 l + 7.
-        int n[kMaxSlots], sum = 0;
-#pragma unroll
-        for (int i = 0; i < kMaxSlots; ++i) {
-            const int e = kMaxSlots * lane + i;
-            n[i] = e < p.E ? ((int)__popcll(r.mask[e]) + 4 * RQ - 1) / (4 * RQ) : 0;
-            sum += n[i];
-        }
-        int upto = sum;
-        for (int d = 1; d < 64; d <<= 1) {
-            const int o = __shfl_up(upto, d);
-            if (lane >= d) upto += o;
-        }
-        if (lane == 63) r.batches = upto;
-        upto -= sum;
-#pragma unroll
-        for (int i = 0; i < kMaxSlots; ++i) {
-            const int e = kMaxSlots * lane + i;
-            if (e < p.E) r.first[e] = (uint16_t)upto;
-            upto += n[i];
-        }
+    for (int t = wv; t < p.T; t += waves) {
+        if (p.E <= 64) route_token<1>(p, t, r);
+        else if (p.E <= 128) route_token<2>(p, t, r);
+        else route_token<kMaxSlots>(p, t, r);
     }
+    meanwhile();
     __syncthreads();
-    const int batches = r.batches, pairs = p.T * p.top_k;
-    for (int i = tid; i < batches * RQ; i += threads) reinterpret_cast<uint32_t*>(r.token)[i] = 0xFFFFFFFFu;
-    __syncthreads();
+    // (Every wave writes the same values of `first`, and reads its own.)
+    const int batches = p.E <= 64 ? place_batches<1>(p, 4 * RQ, r) : place_batches<kMaxSlots>(p, 4 * RQ, r);
+    __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
     const bool tell = blockIdx.x == 0;
+    const int pairs = p.T * p.top_k;
     for (int s = tid; s < pairs; s += threads) {
         const int e = r.sel[s], t = s / p.top_k;
         if (e >= 0) {
             const int rank = __popcll(r.mask[e] & ((1ull << t) - 1));
             const int b = r.first[e] + rank / (4 * RQ), row = b * 4 * RQ + rank % (4 * RQ);
-            r.token[row] = (uint8_t)t;
+            r.token()[row] = (uint8_t)t;
             if (rank % (4 * RQ) == 0) r.batch_e[b] = (uint16_t)e;
             if (tell) p.row_p[row] = r.p[s];
         }
@@ -241,7 +287,86 @@ __device__ void route(const MoeParams& p, Routing& r)
             p.batch_e[b] = e | (left < 4 * RQ ? left : 4 * RQ) << 16;
         }
         for (int i = tid; i < batches * 4 * RQ; i += threads)
-            p.row_token[i] = r.token[i] == kPadToken ? -1 : r.token[i];
+            p.row_token[i] = r.token()[i] == kPadToken ? -1 : r.token()[i];
+    }
+    return batches;
+}
+
+// Scales and zero points of a wave's step: 16 blocks (one per lane group) of
+// 4 NC columns.  Lane l loads those of BPP = NC consecutive blocks of column
+// l / (16 / NC): one load of scales and one of zero points per wave and step
+// where a row's blocks come in whole groups of BPP and the arrays are aligned
+// to them (VEC), in single loads otherwise.  They reach the lanes that need
+// them through a wave-private piece of LDS (a 2-byte and a 1-byte load per
+// lane, block and column took four times as many instructions as the weights
+// themselves, and they, not HBM, set the pace: the first steps' loads alone
+// took 5.7 us to issue at 16 waves per CU).
+template <int NC, bool VEC>
+struct StepScales {
+    static constexpr int NSV = VEC ? (NC + 1) / 2 : NC, NZV = VEC ? 1 : (NC + 1) / 2;
+    uint32_t s[NSV], z[NZV];
+};
+// Bytes of a wave's piece: [4 NC columns][16 fp16], then [4 NC columns][8].
+template <int NC>
+constexpr int kScaleBytes = 4 * NC * 40;
+
+// so, zo: byte offsets of this lane's first block in rS and rZ (uniform part in
+// ss, zs); blk: that block's number; nb: blocks of a row.  Loaded with the default
+// cache policy: a wave takes 32 and 8 bytes of a line whose rest other waves
+// and steps take.
+template <int NC, bool VEC>
+__device__ __forceinline__ void load_scales(StepScales<NC, VEC>& v, __amdgpu_buffer_rsrc_t rS, __amdgpu_buffer_rsrc_t rZ,
+                                            uint32_t so, uint32_t zo, uint32_t ss, uint32_t zs, int blk, int nb)
+{
+    if constexpr (VEC) {
+        const uint32_t s = blk < nb ? so : kOutOfRange, z = blk < nb ? zo : kOutOfRange;
+        if constexpr (NC == 4) {
+            const u32x2 t = __builtin_amdgcn_raw_buffer_load_b64(rS, s, ss, 0);
+            v.s[0] = t[0];
+            v.s[1] = t[1];
+            v.z[0] = __builtin_amdgcn_raw_buffer_load_b16(rZ, z, zs, 0);
+        } else {
+            if constexpr (NC == 2) v.s[0] = __builtin_amdgcn_raw_buffer_load_b32(rS, s, ss, 0);
+            else v.s[0] = __builtin_amdgcn_raw_buffer_load_b16(rS, s, ss, 0);
+            v.z[0] = __builtin_amdgcn_raw_buffer_load_b8(rZ, z, zs, 0);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < NC; ++i)
+            v.s[i] = __builtin_amdgcn_raw_buffer_load_b16(rS, blk + i < nb ? so + 2 * i : kOutOfRange, ss, 0);
+#pragma unroll
+        for (int i = 0; i < (NC + 1) / 2; ++i)
+            v.z[i] = __builtin_amdgcn_raw_buffer_load_b8(rZ, blk + 2 * i < nb ? zo + i : kOutOfRange, zs, 0);
+    }
+}
+
+// Through LDS: s[n], z[n] become the scale and the zero-point byte of column
+// 4 n + qi, block g.
+template <int NC, bool VEC>
+__device__ __forceinline__ void spread_scales(const StepScales<NC, VEC>& v, uint8_t* lds, uint32_t (&s)[NC],
+                                              uint32_t (&z)[NC])
+{
+    const int lane = threadIdx.x & 63, qi = lane & 3, g = lane >> 2;
+    const int c = lane / (16 / NC), part = lane % (16 / NC);
+    uint8_t* const zl = lds + 4 * NC * 32;
+    __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
+    if constexpr (NC == 4) {
+        const u32x2 t = VEC ? u32x2{v.s[0], v.s[1]}
+                            : u32x2{v.s[0] | (v.s[VEC ? 0 : 1] << 16), v.s[VEC ? 0 : 2] | (v.s[VEC ? 0 : 3] << 16)};
+        *reinterpret_cast<u32x2*>(lds + 32 * c + 8 * part) = t;
+        *reinterpret_cast<uint16_t*>(zl + 8 * c + 2 * part) = (uint16_t)(VEC ? v.z[0] : v.z[0] | (v.z[VEC ? 0 : 1] << 8));
+    } else if constexpr (NC == 2) {
+        *reinterpret_cast<uint32_t*>(lds + 32 * c + 4 * part) = VEC ? v.s[0] : v.s[0] | (v.s[VEC ? 0 : 1] << 16);
+        zl[8 * c + part] = (uint8_t)v.z[0];
+    } else {
+        *reinterpret_cast<uint16_t*>(lds + 32 * c + 2 * part) = (uint16_t)v.s[0];
+        if (!(part & 1)) zl[8 * c + part / 2] = (uint8_t)v.z[0];
+    }
+    __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
+#pragma unroll
+    for (int n = 0; n < NC; ++n) {
+        s[n] = *reinterpret_cast<const uint16_t*>(lds + 32 * (4 * n + qi) + 2 * g);
+        z[n] = zl[8 * (4 * n + qi) + g / 2];
     }
 }
 
@@ -300,14 +425,14 @@ __device__ __forceinline__ void block_products(const u32x4 (&w)[NC], const uint3
 // quads of the same columns) and, of every 4 W blocks of K, the 16 from 16 ks.
 // The rows' activations are staged in LDS as fp16 in the unpack's order, rows
 // 16 bytes apart modulo 128 so that eight lanes' reads fall on distinct banks.
-template <int RQ, int W>
-__global__ __launch_bounds__(64 * W) void mnb_moe_up_kernel(MoeParams p)
+template <int RQ, bool VEC>
+__global__ __launch_bounds__(64 * kUpWaves) void mnb_moe_up_kernel(MoeParams p)
 {
-    constexpr int NC = 4, R = 4 * RQ;
+    constexpr int NC = 4, R = 4 * RQ, W = kUpWaves, P = kUpRing;
     constexpr int SB = 16 * (W / 4);                 // blocks of K of a step, 16 per slice
-    __shared__ Routing rt;
     __shared__ float part[2][W][NC * RQ * 16];
-    extern __shared__ u32x4 stage[];                 // [rows][4 stage_blocks + 1]
+    __shared__ u32x2 scale_lds[W][kScaleBytes<NC> / 8];
+    extern __shared__ u32x4 up_lds[];                // routing tables, then the stage
     const int tid = threadIdx.x, lane = tid & 63;
     const int wv = __builtin_amdgcn_readfirstlane(tid >> 6), cw = wv & 3, ks = wv >> 2;
     const int qi = lane & 3, g = lane >> 2;
@@ -317,11 +442,15 @@ __global__ __launch_bounds__(64 * W) void mnb_moe_up_kernel(MoeParams p)
     const uint32_t magic = vgpr_constant(0x64006400u, p.zero);
     const int chunks = (nb + p.stage_blocks - 1) / p.stage_blocks;
     const bool all = p.T <= R;                       // every token staged once, rows by token
+    const int pairs = p.T * p.top_k;
+    const Routing rt = routing_tables(reinterpret_cast<uint8_t*>(up_lds), p.E, pairs, p.batch_cap, RQ);
+    u32x4* const stage = up_lds + routing_bytes(p.E, pairs, p.batch_cap, RQ) / 16;   // [rows][4 stage_blocks + 1]
 
-    // Rows [0, n) of the stage from tokens tok(row), blocks [b0, b0 + stage_blocks) of K.
-    auto fill = [&](int n, int b0, auto tok) {
+    // Rows [0, n) of the stage from tokens tok(row), blocks [b0, b0 +
+    // stage_blocks) of K, by threads tid0, tid0 + 1, ...
+    auto fill = [&](int n, int b0, int tid0, auto tok) {
         const int per_row = 4 * p.stage_blocks;
-        for (int i = tid; i < n * per_row; i += 64 * W) {
+        for (int i = tid - tid0; i < n * per_row; i += 64 * W - tid0) {
             const int row = i / per_row, pc = i - row * per_row, t = tok(row);
             u32x4 v = {0, 0, 0, 0};
             if (t != kPadToken && b0 + pc / 4 < nb)
@@ -329,28 +458,53 @@ __global__ __launch_bounds__(64 * W) void mnb_moe_up_kernel(MoeParams p)
             stage[row * row_pieces + pc] = f16_pairs(v, p.x_bf16, 0);
         }
     };
-    if (all && chunks == 1) fill(p.T, 0, [](int row) { return row; });
-    route<RQ>(p, rt);
+    const int batches = route<RQ>(p, rt, [&] {
+        if (all && chunks == 1 && wv >= W / 4) fill(p.T, 0, 16 * W, [](int row) { return row; });
+    });
 
-    const int batches = rt.batches;
     const int64_t units = (int64_t)batches * hblocks;   // at most 2^21
-    const int u0 = (int)(units * blockIdx.x / gridDim.x), u1 = (int)(units * (blockIdx.x + 1) / gridDim.x);
+    // As few units for every workgroup as the busiest one needs: HBM, not the
+    // CUs, sets the pace, and what counts is that all end together (896 units
+    // on 256 workgroups: 4 each on 224 of them against 3 or 4 on all: 32.3 ->
+    // 31.5 us).
+    const int per = (int)((units + gridDim.x - 1) / gridDim.x);
+    const int u0 = std::min<int>((int)blockIdx.x * per, (int)units), u1 = std::min<int>(u0 + per, (int)units);
     const int steps = (nb + SB - 1) / SB;            // of a unit
     const int chunk_steps = p.stage_blocks / SB;
 
     struct Step {
         u32x4 w[NC];
-        uint32_t s[NC], z[NC];
+        StepScales<NC, VEC> sz;
     };
     const uint32_t row_bytes = (uint32_t)p.H / 2;
-    // The loads run two steps ahead of use, across the units.
+    // This lane's weights: block 16 ks + g of every step, columns qi and 4 +
+    // qi; its scales: blocks 16 ks + 4 (lane % 4) .. of column lane / 4 (gate
+    // columns first, then up).
+    const int wblk = 16 * ks + g, sblk = 16 * ks + 4 * (lane & 3);
+    const uint32_t wo = (uint32_t)qi * row_bytes + 16 * (uint32_t)wblk;
+    const uint32_t srow = (uint32_t)((lane >> 2) & 7) + (lane >> 5) * (uint32_t)p.I;
+    const uint32_t so = 2 * (srow * (uint32_t)nb + (uint32_t)sblk), zo = srow * (uint32_t)zb + (uint32_t)sblk / 2;
+    const uint32_t rows = (uint32_t)p.I + 8;         // from a wave's first gate row to its last up row
+    // The loads run P steps ahead of use, across the units.
     int left = (u1 - u0) * steps, nbatch = u0 / hblocks, nhb = u0 - nbatch * hblocks, nstep = 0;
     auto next = [&](Step& st) {
         const bool live = left-- > 0;
         const int64_t e = live ? __builtin_amdgcn_readfirstlane(rt.batch_e[nbatch]) : 0;
-        const int hb = live ? nhb : 0;
-        const int blk = SB * nstep + 16 * ks + g;
-        const bool in = live && blk < nb;
+        const int64_t row0 = e * 2 * p.I + (live ? 32 * nhb + 8 * cw : 0);
+        const int end = live ? nb : 0;               // nothing behind the last unit
+        const __amdgpu_buffer_rsrc_t rW = make_rsrc_small(p.w1 + row0 * row_bytes, rows * row_bytes);
+        const __amdgpu_buffer_rsrc_t rS = make_rsrc_small(p.s1 + row0 * nb, 2 * rows * (uint32_t)nb);
+        const __amdgpu_buffer_rsrc_t rZ =
+            make_rsrc_small(p.z1 ? p.z1 + row0 * zb : p.w1, p.z1 ? rows * (uint32_t)zb : 0u);
+        const uint32_t at = SB * (uint32_t)nstep;
+        const uint32_t v = wblk + (int)at < end ? wo : kOutOfRange;
+        const uint32_t up = (uint32_t)p.I * row_bytes + 16 * at;
+        const uint32_t v4 = wblk + (int)at < end ? wo + 4 * row_bytes : kOutOfRange;
+        st.w[0] = __builtin_amdgcn_raw_buffer_load_b128(rW, v, 16 * at, kNontemporal);
+        st.w[1] = __builtin_amdgcn_raw_buffer_load_b128(rW, v4, 16 * at, kNontemporal);
+        st.w[2] = __builtin_amdgcn_raw_buffer_load_b128(rW, v, up, kNontemporal);
+        st.w[3] = __builtin_amdgcn_raw_buffer_load_b128(rW, v4, up, kNontemporal);
+        load_scales<NC, VEC>(st.sz, rS, rZ, so, zo, 2 * at, at / 2, sblk + (int)at, end);
         if (++nstep == steps) {
             nstep = 0;
             if (++nhb == hblocks) {
@@ -358,38 +512,23 @@ __global__ __launch_bounds__(64 * W) void mnb_moe_up_kernel(MoeParams p)
                 ++nbatch;
             }
         }
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {       // gate, up
-            const int64_t row0 = (e * 2 + half) * p.I + 32 * hb + 8 * cw;
-            const __amdgpu_buffer_rsrc_t rW = make_rsrc_small(p.w1 + row0 * row_bytes, 8 * row_bytes);
-            const __amdgpu_buffer_rsrc_t rS = make_rsrc_small(p.s1 + row0 * nb, 16 * (uint32_t)nb);
-            const __amdgpu_buffer_rsrc_t rZ =
-                make_rsrc_small(p.z1 ? p.z1 + row0 * zb : p.w1, p.z1 ? 8 * (uint32_t)zb : 0u);
-#pragma unroll
-            for (int n = 0; n < 2; ++n) {
-                const uint32_t c = (uint32_t)(4 * n + qi);
-                st.w[2 * half + n] = __builtin_amdgcn_raw_buffer_load_b128(
-                    rW, in ? c * row_bytes + 16 * (uint32_t)blk : kOutOfRange, 0, kNontemporal);
-                st.s[2 * half + n] = __builtin_amdgcn_raw_buffer_load_b16(
-                    rS, in ? 2 * (c * (uint32_t)nb + (uint32_t)blk) : kOutOfRange, 0, kNontemporal);
-                st.z[2 * half + n] = __builtin_amdgcn_raw_buffer_load_b8(
-                    rZ, in ? c * (uint32_t)zb + (uint32_t)blk / 2 : kOutOfRange, 0, kNontemporal);
-            }
-        }
     };
-
-    Step ring[2];
-    next(ring[0]);
-    next(ring[1]);
+    Step ring[P];
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+        next(ring[i]);
+        __builtin_amdgcn_sched_barrier(0);
+    }
     int staged = all && chunks == 1 ? -2 : -1;       // batch in the stage (-2: every token, -1: none)
     int buf = 0;
     float4_t acc[NC][RQ] = {};
     int b = u0 / hblocks, hb = u0 - b * hblocks, step = 0;   // the unit in work
     const float4_t no_f[RQ] = {};
+    int todo = (u1 - u0) * steps;
     auto run = [&](Step& st) {
         if (staged != -2 && step % chunk_steps == 0 && (chunks > 1 || staged != b)) {
             __syncthreads();
-            fill(R, SB * step, [&](int row) { return (int)rt.token[b * R + row]; });
+            fill(R, SB * step, 0, [&](int row) { return (int)rt.token()[b * R + row]; });
             __syncthreads();
             staged = b;
         }
@@ -398,15 +537,18 @@ __global__ __launch_bounds__(64 * W) void mnb_moe_up_kernel(MoeParams p)
         for (int rq = 0; rq < RQ; ++rq) {
             int row = 4 * rq + qi;
             if (staged == -2) {
-                const int t = rt.token[b * R + row];
+                const int t = rt.token()[b * R + row];
                 row = t == kPadToken ? 0 : t;
             }
             const u32x4* src = stage + row * row_pieces + 4 * (SB * (step % chunk_steps) + 16 * ks + g);
 #pragma unroll
             for (int pc = 0; pc < 4; ++pc) act[rq][pc] = src[pc];
         }
-        block_products<NC, RQ, false>(st.w, st.s, st.z, 4 * (g & 1), zdef, magic, act, no_f, acc);
+        uint32_t sc[NC], zc[NC];
+        spread_scales<NC, VEC>(st.sz, reinterpret_cast<uint8_t*>(scale_lds[wv]), sc, zc);
+        block_products<NC, RQ, false>(st.w, sc, zc, 4 * (g & 1), zdef, magic, act, no_f, acc);
         next(st);
+        const bool live = todo-- > 0;
         if (++step < steps) return;
         step = 0;
         // Sums over the lane groups, then over the K slices in LDS.
@@ -441,23 +583,29 @@ __global__ __launch_bounds__(64 * W) void mnb_moe_up_kernel(MoeParams p)
             // or not finite).
             int ex = (int)(top >> 23) - 127 - 13;
             ex = top == 0 || top >= 0x7F800000u ? 0 : ex < -110 ? -110 : ex;
-            if (rt.token[b * R + row] != kPadToken) {
-                const int64_t at_h = (((int64_t)b * RQ + (row >> 2)) * hblocks + hb) * 4 + (row & 3);
-                const int pos = (c & ~7) | ((c & 3) << 1) | (c >> 2 & 1);   // the unpack's pair order
-                p.h[at_h * 32 + pos] = __builtin_bit_cast(uint16_t, (_Float16)ldexpf(h, -ex));
-                if (c == 0) p.hs[at_h] = ldexpf(1.f, ex);
+            if (live && rt.token()[b * R + row] != kPadToken) {
+                const int64_t quad = (int64_t)b * RQ + (row >> 2);
+                // Its rows: a prefix of the four (tokens are below 64, unused rows 255).
+                const int rows = 4 - __popc(rt.token4[quad] & 0x80808080u);
+                const int piece = ((hb & ~15) * 4 + (c >> 3) * 16 + (hb & 15)) * rows + (row & 3);
+                const int pos = ((c & 3) << 1) | (c >> 2 & 1);   // the unpack's pair order
+                p.h[quad * p.h_quad + piece * 8 + pos] = __builtin_bit_cast(uint16_t, (_Float16)ldexpf(h, -ex));
+                if (c == 0) p.hs[(quad * hblocks + hb) * 4 + (row & 3)] = ldexpf(1.f, ex);
             }
         }
         buf ^= 1;
-        if (++hb == hblocks) {
+        if (todo > 0 && ++hb == hblocks) {
             hb = 0;
             ++b;
         }
     };
-    const int total = (u1 - u0) * steps;
-    for (int i = 0; i < total; i += 2) {
-        run(ring[0]);
-        if (i + 1 < total) run(ring[1]);
+    // P steps at a time, without a way out between them (that would be, to the
+    // compiler, a path from one slot of the ring round to itself, and it
+    // would wait there for the loads of all the others): steps behind the
+    // last one run on zeros.
+    while (todo > 0) {
+#pragma unroll
+        for (int j = 0; j < P; ++j) run(ring[j]);
     }
 }
 
@@ -466,10 +614,11 @@ __global__ __launch_bounds__(64 * W) void mnb_moe_up_kernel(MoeParams p)
 // blocks of K each, are dealt to its waves in contiguous runs; a wave adds
 // each batch's products, weighted, to its own rows of y in LDS, and the
 // waves' rows are added in wave order at the end.
-template <int RQ, int NC, int W>
+template <int RQ, int NC, int W, bool VEC>
 __global__ __launch_bounds__(64 * W) void mnb_moe_down_kernel(MoeParams p)
 {
     constexpr int R = 4 * RQ, C = 4 * NC;
+    __shared__ u32x2 scale_lds[W][kScaleBytes<NC> / 8];
     // y of each wave [W][T][C], then the tables: rows' weights and tokens and
     // the batches (expert | rows << 16), batch_cap of them.
     extern __shared__ float y_lds[];
@@ -500,9 +649,13 @@ __global__ __launch_bounds__(64 * W) void mnb_moe_down_kernel(MoeParams p)
 
     struct Step {
         u32x4 w[NC], a[RQ][4];
-        uint32_t s[NC], z[NC];
+        StepScales<NC, VEC> sz;
         float4_t f[RQ];
     };
+    const int scol = lane / (16 / NC), sblk = NC * (lane % (16 / NC));   // this lane's scales of a step
+    const uint32_t so = 2 * ((uint32_t)scol * (uint32_t)nb + (uint32_t)sblk);
+    const uint32_t zo = (uint32_t)scol * (uint32_t)zb + (uint32_t)sblk / 2;
+    const uint32_t wo = (uint32_t)qi * row_bytes + 16 * (uint32_t)g;
     int nbatch = i0 / steps, nstep = i0 - nbatch * steps;
     auto next = [&](Step& st, bool live) {
         const int b = live ? nbatch : 0;
@@ -517,27 +670,26 @@ __global__ __launch_bounds__(64 * W) void mnb_moe_down_kernel(MoeParams p)
         const __amdgpu_buffer_rsrc_t rZ =
             make_rsrc_small(p.z2 ? p.z2 + row0 * zb : p.w2, p.z2 ? C * (uint32_t)zb : 0u);
         const __amdgpu_buffer_rsrc_t rA =
-            make_rsrc_small(p.h + (int64_t)b * RQ * nb * 128, live ? RQ * (uint32_t)nb * 256 : 0u);
+            make_rsrc_small(p.h + (int64_t)b * RQ * p.h_quad, live ? 2 * RQ * (uint32_t)p.h_quad : 0u);
         const __amdgpu_buffer_rsrc_t rF = make_rsrc_small(p.hs + (int64_t)b * RQ * nb * 4, live ? RQ * (uint32_t)nb * 16 : 0u);
 #pragma unroll
         for (int n = 0; n < NC; ++n) {
-            const uint32_t c = (uint32_t)(4 * n + qi);
-            st.w[n] = __builtin_amdgcn_raw_buffer_load_b128(rW, in ? c * row_bytes + 16 * (uint32_t)blk : kOutOfRange, 0,
-                                                            kNontemporal);
-            st.s[n] = __builtin_amdgcn_raw_buffer_load_b16(
-                rS, in ? 2 * (c * (uint32_t)nb + (uint32_t)blk) : kOutOfRange, 0, kNontemporal);
-            st.z[n] = __builtin_amdgcn_raw_buffer_load_b8(rZ, in ? c * (uint32_t)zb + (uint32_t)blk / 2 : kOutOfRange, 0,
-                                                          kNontemporal);
+            st.w[n] = __builtin_amdgcn_raw_buffer_load_b128(rW, in ? wo + 4 * n * row_bytes : kOutOfRange,
+                                                            256 * (uint32_t)nstep, kNontemporal);
         }
+        load_scales<NC, VEC>(st.sz, rS, rZ, so, zo, 32 * (uint32_t)nstep, 8 * (uint32_t)nstep, 16 * nstep + sblk,
+                             live ? nb : 0);
 #pragma unroll
         for (int rq = 0; rq < RQ; ++rq) {
             // Unused rows load zeros.
-            const bool used = in && 4 * rq + qi < rows;
+            const int n4 = rows - 4 * rq < 4 ? rows - 4 * rq : 4;   // rows of the quad
+            const bool used = in && qi < n4;
             const uint32_t at = (uint32_t)(rq * nb + blk);
+            const uint32_t to = 2 * rq * (uint32_t)p.h_quad + 16 * ((64 * (uint32_t)nstep + g) * (uint32_t)n4 + qi);
 #pragma unroll
             for (int pc = 0; pc < 4; ++pc)
                 st.a[rq][pc] = __builtin_amdgcn_raw_buffer_load_b128(
-                    rA, used ? at * 256 + 64 * (uint32_t)qi + 16 * pc : kOutOfRange, 0, 0);
+                    rA, used ? to + 256 * pc * (uint32_t)n4 : kOutOfRange, 0, 0);
             st.f[rq] = __builtin_bit_cast(float4_t, __builtin_amdgcn_raw_buffer_load_b128(rF, in ? at * 16 : kOutOfRange, 0, 0));
         }
         if (++nstep == steps) {
@@ -551,7 +703,9 @@ __global__ __launch_bounds__(64 * W) void mnb_moe_down_kernel(MoeParams p)
     int bt = i0 / steps;
     float4_t acc[NC][RQ] = {};
     auto run = [&](Step& st, int i) {
-        block_products<NC, RQ, true>(st.w, st.s, st.z, 4 * (g & 1), zdef, magic, st.a, st.f, acc);
+        uint32_t sc[NC], zc[NC];
+        spread_scales<NC, VEC>(st.sz, reinterpret_cast<uint8_t*>(scale_lds[wv]), sc, zc);
+        block_products<NC, RQ, true>(st.w, sc, zc, 4 * (g & 1), zdef, magic, st.a, st.f, acc);
         next(st, i + 2 < i1);
         if (i + 1 < i1 && (i + 1) % steps) return;
         // The batch ends for this wave: weighted rows to its y.
@@ -570,9 +724,11 @@ __global__ __launch_bounds__(64 * W) void mnb_moe_down_kernel(MoeParams p)
         }
         ++bt;
     };
-    for (int i = i0; i < i1; i += 2) {
+    for (int i = i0; i < i1;) {   // ends right behind an item, as above
         run(ring[0], i);
-        if (i + 1 < i1) run(ring[1], i + 1);
+        if (++i >= i1) break;
+        run(ring[1], i);
+        ++i;
     }
     __syncthreads();
     for (int i = tid; i < p.T * C; i += 64 * W) {
@@ -584,30 +740,44 @@ __global__ __launch_bounds__(64 * W) void mnb_moe_down_kernel(MoeParams p)
     }
 }
 
-template <int RQ, int W>
-hipError_t queue_up(const MoeParams& p, int cus, hipStream_t s)
+// Whether a matrix's scales and zero points can be loaded for `blocks`
+// consecutive blocks at a time.
+bool vec_ok(int64_t K, const uint16_t* scales, const uint8_t* zp, int blocks)
 {
-    const size_t lds = (size_t)4 * RQ * (4 * p.stage_blocks + 1) * 16;
-    const void* fn = reinterpret_cast<const void*>(mnb_moe_up_kernel<RQ, W>);
+    return (K / 32) % blocks == 0 && ((uintptr_t)scales & (2 * blocks - 1)) == 0 &&
+           (blocks < 4 || ((uintptr_t)zp & (blocks / 2 - 1)) == 0);
+}
+
+hipError_t queue(const void* fn, const MoeParams& p, unsigned grid, int threads, size_t lds, hipStream_t s)
+{
     hipError_t e = hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
     if (e != hipSuccess) return e;
-    const int64_t most = (int64_t)p.T * p.top_k * (p.I / 32);
-    const unsigned grid = (unsigned)(most < cus ? most : cus);
     MoeParams q = p;
     void* args[] = {&q};
-    return hipLaunchKernel(fn, dim3(grid), dim3(64 * W), args, lds, s);
+    return hipLaunchKernel(fn, dim3(grid), dim3((unsigned)threads), args, lds, s);
+}
+
+template <int RQ>
+hipError_t queue_up(const MoeParams& p, int cus, hipStream_t s)
+{
+    // Every token, where they are few and K is staged whole; else one batch.
+    const int rows = p.T < 4 * RQ && p.H <= 32 * p.stage_blocks ? p.T : 4 * RQ;
+    const size_t lds = routing_bytes(p.E, p.T * p.top_k, p.batch_cap, RQ) + (size_t)rows * (4 * p.stage_blocks + 1) * 16;
+    const int64_t units = (int64_t)p.T * p.top_k * (p.I / 32);
+    const bool vec = vec_ok(p.H, p.s1, p.z1, 4);
+    const void* fn = vec ? reinterpret_cast<const void*>(mnb_moe_up_kernel<RQ, true>)
+                         : reinterpret_cast<const void*>(mnb_moe_up_kernel<RQ, false>);
+    return queue(fn, p, (unsigned)(units < cus ? units : cus), 64 * kUpWaves, lds, s);
 }
 
 template <int RQ, int NC, int W>
 hipError_t queue_down(const MoeParams& p, hipStream_t s)
 {
     const size_t lds = ((size_t)W * p.T * 4 * NC + (size_t)p.batch_cap * (8 * RQ + 1)) * 4;
-    const void* fn = reinterpret_cast<const void*>(mnb_moe_down_kernel<RQ, NC, W>);
-    hipError_t e = hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
-    if (e != hipSuccess) return e;
-    MoeParams q = p;
-    void* args[] = {&q};
-    return hipLaunchKernel(fn, dim3((unsigned)(p.H / (4 * NC))), dim3(64 * W), args, lds, s);
+    const bool vec = vec_ok(p.I, p.s2, p.z2, NC);
+    const void* fn = vec ? reinterpret_cast<const void*>(mnb_moe_down_kernel<RQ, NC, W, true>)
+                         : reinterpret_cast<const void*>(mnb_moe_down_kernel<RQ, NC, W, false>);
+    return queue(fn, p, (unsigned)(p.H / (4 * NC)), 64 * W, lds, s);
 }
 
 }  // namespace
@@ -648,11 +818,12 @@ int launch_moe(const MoeArgs& a, void* stream, int* launches)
     p.out_bf16 = a.out_bf16;
     p.zero = 0;
     p.batch_cap = lay.batches;
+    p.h_quad = 128 * ((p.I / 32 + 15) / 16 * 16);
     // The first launch stages whole rows where they fit, else spans of K.
-    const int blocks = (p.H / 32 + 63) / 64 * 64, most = lay.rq == 1 ? 512 : 192;
+    const int blocks = (p.H / 32 + 63) / 64 * 64, most = lay.rq == 1 ? 448 : 192;
     p.stage_blocks = blocks < most ? blocks : most;
     const hipStream_t s = static_cast<hipStream_t>(stream);
-    hipError_t he = lay.rq == 1 ? queue_up<1, 16>(p, cus, s) : queue_up<2, 8>(p, cus, s);
+    hipError_t he = lay.rq == 1 ? queue_up<1>(p, cus, s) : queue_up<2>(p, cus, s);
     if (he != hipSuccess) return (int)he;
     ++*launches;
     // Columns of a workgroup: as few as fill the device.
