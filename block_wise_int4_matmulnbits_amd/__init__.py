@@ -280,56 +280,61 @@ def mnb_repack_weights(src, src_layout, dst, dst_layout, stream=None):
 
 
 # ------------------------------------------- 8-bit products and expert layers
-def _device_of(named):
-    """The one GPU that all the given (name, tensor) pairs are on; every
-    tensor must be contiguous."""
-    device = None
-    for name, t in named:
-        if t is None:
-            continue
-        if not t.is_cuda:
-            raise ValueError("%s must be on the GPU" % name)
-        if device is None:
-            device = t.device
-        elif t.device != device:
-            raise ValueError("%s is on %s, not on %s" % (name, t.device, device))
-        if not t.is_contiguous():
-            raise ValueError("%s must be contiguous" % name)
-    return device
-
-
-def _expect(name, t, shape, *dtypes):
-    if t.dtype not in dtypes:
-        raise TypeError("%s must be %s, got %s" % (name, " or ".join(str(d) for d in dtypes), t.dtype))
-    if tuple(t.shape) != tuple(shape):
+# These are called once per layer and token, so their checks are kept to a few
+# attribute reads per tensor.
+def _expect(name, t, shape, dtype, index):
+    """t has this shape and type, and is contiguous and on GPU ``index``."""
+    if t.dtype != dtype:
+        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if t.shape != shape:
         raise ValueError("%s must be %s, got %s" % (name, list(shape), list(t.shape)))
+    if t.get_device() != index:
+        raise ValueError("%s must be on the GPU of the first argument, got %s" % (name, t.device))
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
 
 
-def _launch(device, stream, workspace, need, call):
-    """call(workspace address, workspace bytes, stream handle) with ``device``
-    current.  Without a workspace of the caller's, one is taken from torch's
-    allocator on the call's stream (inside a graph capture: from the graph's
-    own pool), so calls on several streams and captured graphs never share
-    one."""
+def _first(name, t, dim):
+    """Index of the GPU that t is on; t must be contiguous and of ``dim`` dimensions."""
+    if t.dim() != dim:
+        raise ValueError("%s must be %d-D" % (name, dim))
+    index = t.get_device()
+    if index < 0:
+        raise ValueError("%s must be on the GPU" % name)
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+    return index
+
+
+def _workspace(t, need, workspace, stream, index):
+    """A tensor for a call's workspace: the caller's, or one of torch's
+    allocator on the call's stream (inside a graph capture: of the graph's own
+    pool), so that calls on several streams and captured graphs never share
+    one.  The allocator hands its memory on only to later work of that
+    stream."""
     import torch
-    L = lib()
-    if torch.cuda.current_device() != device.index:
-        with torch.cuda.device(device):
-            return _launch(device, stream, workspace, need, call)
-    size = 0
     if workspace is not None:
-        if workspace.device != device or not workspace.is_contiguous():
-            raise ValueError("workspace must be a contiguous tensor on %s" % device)
-        size = workspace.numel() * workspace.element_size()
-    elif need:
-        if stream is None:
-            workspace = torch.empty(need, dtype=torch.uint8, device=device)
-        else:
-            on = torch.cuda.ExternalStream(stream, device=device) if isinstance(stream, int) else stream
-            with torch.cuda.stream(on):
-                workspace = torch.empty(need, dtype=torch.uint8, device=device)
-        size = need
-    _check(call(workspace.data_ptr() if size else None, size, _stream_handle(stream, device)), L)
+        if workspace.get_device() != index or not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous tensor on the GPU of the first argument")
+        return workspace
+    if stream is None:
+        return t.new_empty(need, dtype=torch.uint8)
+    on = torch.cuda.ExternalStream(stream, device=t.device) if isinstance(stream, int) else stream
+    with torch.cuda.stream(on):
+        return t.new_empty(need, dtype=torch.uint8)
+
+
+def _on_device(index, stream, call, *args):
+    """call(*args, stream handle) with GPU ``index`` current."""
+    import torch
+    if torch._C._cuda_getDevice() != index:
+        with torch.cuda.device(index):
+            return _on_device(index, stream, call, *args)
+    if stream is None:
+        handle = torch._C._cuda_getCurrentRawStream(index)
+    else:
+        handle = stream if isinstance(stream, int) else stream.cuda_stream
+    _check(call(*args, handle), _lib)
 
 
 def quantize_rows_int8(A, q, scales, stream=None):
@@ -341,16 +346,13 @@ def quantize_rows_int8(A, q, scales, stream=None):
     returns ``(q, scales)``.
     """
     import torch
-    L = lib()
-    if A.dim() != 2:
-        raise ValueError("A must be 2-D")
+    L = _lib or lib()
+    index = _first("A", A, 2)
     m, K = A.shape
-    device = _device_of((("A", A), ("q", q), ("scales", scales)))
-    _expect("q", q, (m, K), torch.int8)
-    _expect("scales", scales, (m,), torch.float32)
-    a_dt = _dtype_code(A)
-    _launch(device, stream, None, 0, lambda ws, size, s: L.quantize_rows_int8(
-        A.data_ptr(), a_dt, m, K, q.data_ptr(), scales.data_ptr(), s))
+    _expect("q", q, (m, K), torch.int8, index)
+    _expect("scales", scales, (m,), torch.float32, index)
+    _on_device(index, stream, L.quantize_rows_int8, A.data_ptr(), _dtype_code(A), m, K, q.data_ptr(),
+               scales.data_ptr())
     return q, scales
 
 
@@ -365,32 +367,32 @@ def matmul_int8(A, a_scales, B, b_scales, bias, out, workspace=None, stream=None
     Queued on ``stream``; returns ``out``.
     """
     import torch
-    L = lib()
-    if A.dim() != 2 or B.dim() != 2:
-        raise ValueError("A and B must be 2-D")
+    L = _lib or lib()
+    index = _first("A", A, 2)
     m, K = A.shape
+    if B.dim() != 2:
+        raise ValueError("B must be 2-D")
     N = B.shape[0]
-    device = _device_of((("A", A), ("a_scales", a_scales), ("B", B), ("b_scales", b_scales), ("bias", bias),
-                         ("out", out)))
-    _expect("B", B, (N, K), torch.int8)
-    _expect("b_scales", b_scales, (N,), torch.float32)
-    _expect("out", out, (m, N), torch.float16, torch.bfloat16)
+    _expect("B", B, (N, K), torch.int8, index)
+    _expect("b_scales", b_scales, (N,), torch.float32, index)
+    _expect("out", out, (m, N), out.dtype, index)
+    o_dt = _dtype_code(out)
     if bias is not None:
-        _expect("bias", bias, (N,), torch.float32)
+        _expect("bias", bias, (N,), torch.float32, index)
     if A.dtype == torch.int8:
         a_dt = MNB_I8
         if a_scales is None:
             raise ValueError("int8 rows need a_scales")
-        _expect("a_scales", a_scales, (m,), torch.float32)
+        _expect("a_scales", a_scales, (m,), torch.float32, index)
     else:
         a_dt = _dtype_code(A)
         if a_scales is not None:
             raise ValueError("a_scales must be None with fp16 or bf16 rows")
     need = L.mnb_int8_workspace(a_dt, m, K, N) if workspace is None else 0
-    _launch(device, stream, workspace, need, lambda ws, size, s: L.matmul_int8(
-        A.data_ptr(), a_dt, None if a_scales is None else a_scales.data_ptr(), m, K, N, B.data_ptr(),
-        b_scales.data_ptr(), None if bias is None else bias.data_ptr(), out.data_ptr(), _dtype_code(out),
-        ws, size, s))
+    ws = _workspace(A, need, workspace, stream, index) if need or workspace is not None else None
+    _on_device(index, stream, L.matmul_int8, A.data_ptr(), a_dt, None if a_scales is None else a_scales.data_ptr(),
+               m, K, N, B.data_ptr(), b_scales.data_ptr(), None if bias is None else bias.data_ptr(), out.data_ptr(),
+               o_dt, None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel() * ws.element_size())
     return out
 
 
@@ -414,41 +416,41 @@ def moe_nbits(x, router_logits, gate_up, gate_up_scales, gate_up_zero_points, do
     allocator.  Queued on ``stream``; returns ``out``.
     """
     import torch
-    L = lib()
-    if x.dim() != 2 or router_logits.dim() != 2 or gate_up.dim() != 3 or down.dim() != 3:
-        raise ValueError("x and router_logits must be 2-D, gate_up and down 3-D")
+    L = _lib or lib()
+    index = _first("x", x, 2)
     T, H = x.shape
+    if router_logits.dim() != 2 or gate_up.dim() != 3 or down.dim() != 3:
+        raise ValueError("router_logits must be 2-D, gate_up and down 3-D")
     E, I = gate_up.shape[0], gate_up.shape[1] // 2
-    device = _device_of((("x", x), ("router_logits", router_logits), ("gate_up", gate_up),
-                         ("gate_up_scales", gate_up_scales), ("gate_up_zero_points", gate_up_zero_points),
-                         ("down", down), ("down_scales", down_scales), ("down_zero_points", down_zero_points),
-                         ("out", out), ("expert_ids", expert_ids), ("expert_weights", expert_weights)))
-    _expect("router_logits", router_logits, (T, E), torch.float32, torch.float16, torch.bfloat16)
-    _expect("gate_up", gate_up, (E, 2 * I, H // 2), torch.uint8)
-    _expect("gate_up_scales", gate_up_scales, (E, 2 * I, H // 32), torch.float16)
-    _expect("down", down, (E, H, I // 2), torch.uint8)
-    _expect("down_scales", down_scales, (E, H, I // 32), torch.float16)
-    _expect("out", out, (T, H), torch.float16, torch.bfloat16)
+    u8, f16 = torch.uint8, torch.float16
+    _expect("router_logits", router_logits, (T, E), router_logits.dtype, index)
+    _expect("gate_up", gate_up, (E, 2 * I, H // 2), u8, index)
+    _expect("gate_up_scales", gate_up_scales, (E, 2 * I, H // 32), f16, index)
+    _expect("down", down, (E, H, I // 2), u8, index)
+    _expect("down_scales", down_scales, (E, H, I // 32), f16, index)
+    _expect("out", out, (T, H), out.dtype, index)
+    z1 = z2 = ids = weights = None
     if gate_up_zero_points is not None:
-        _expect("gate_up_zero_points", gate_up_zero_points, (E, 2 * I, (H // 32 + 1) // 2), torch.uint8)
+        _expect("gate_up_zero_points", gate_up_zero_points, (E, 2 * I, (H // 32 + 1) // 2), u8, index)
+        z1 = gate_up_zero_points.data_ptr()
     if down_zero_points is not None:
-        _expect("down_zero_points", down_zero_points, (E, H, (I // 32 + 1) // 2), torch.uint8)
+        _expect("down_zero_points", down_zero_points, (E, H, (I // 32 + 1) // 2), u8, index)
+        z2 = down_zero_points.data_ptr()
     if expert_ids is not None:
-        _expect("expert_ids", expert_ids, (T, top_k), torch.int32)
+        _expect("expert_ids", expert_ids, (T, top_k), torch.int32, index)
+        ids = expert_ids.data_ptr()
     if expert_weights is not None:
-        _expect("expert_weights", expert_weights, (T, top_k), torch.float32)
-
-    def address(t):
-        return None if t is None else t.data_ptr()
-
-    w = mnb_moe_weights(E, H, I, gate_up.data_ptr(), gate_up_scales.data_ptr(), address(gate_up_zero_points),
-                        down.data_ptr(), down_scales.data_ptr(), address(down_zero_points), block)
-    x_dt, out_dt = _dtype_code(x), _dtype_code(out)
+        _expect("expert_weights", expert_weights, (T, top_k), torch.float32, index)
+        weights = expert_weights.data_ptr()
+    w = mnb_moe_weights(E, H, I, gate_up.data_ptr(), gate_up_scales.data_ptr(), z1, down.data_ptr(),
+                        down_scales.data_ptr(), z2, block)
+    x_dt, o_dt = _dtype_code(x), _dtype_code(out)
     l_dt = MNB_F32 if router_logits.dtype == torch.float32 else _dtype_code(router_logits)
     need = L.mnb_moe_workspace(T, H, I, E, top_k) if workspace is None else 0
-    _launch(device, stream, workspace, need, lambda ws, size, s: L.moe_nbits(
-        x.data_ptr(), x_dt, T, router_logits.data_ptr(), l_dt, top_k, int(bool(renormalize)), ctypes.byref(w),
-        out.data_ptr(), out_dt, address(expert_ids), address(expert_weights), ws, size, s))
+    ws = _workspace(x, need, workspace, stream, index) if need or workspace is not None else None
+    _on_device(index, stream, L.moe_nbits, x.data_ptr(), x_dt, T, router_logits.data_ptr(), l_dt, top_k,
+               1 if renormalize else 0, ctypes.byref(w), out.data_ptr(), o_dt, ids, weights,
+               None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel() * ws.element_size())
     return out
 
 

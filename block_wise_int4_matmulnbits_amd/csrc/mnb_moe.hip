@@ -750,11 +750,10 @@ bool vec_ok(int64_t K, const uint16_t* scales, const uint8_t* zp, int blocks)
 
 hipError_t queue(const void* fn, const MoeParams& p, unsigned grid, int threads, size_t lds, hipStream_t s)
 {
-    hipError_t e = hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
-    if (e != hipSuccess) return e;
     MoeParams q = p;
     void* args[] = {&q};
-    return hipLaunchKernel(fn, dim3(grid), dim3((unsigned)threads), args, lds, s);
+    const hipError_t e = hipLaunchKernel(fn, dim3(grid), dim3((unsigned)threads), args, lds, s);
+    return e != hipSuccess ? e : hipGetLastError();
 }
 
 template <int RQ>
