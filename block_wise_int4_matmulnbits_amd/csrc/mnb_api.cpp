@@ -419,7 +419,7 @@ namespace mnb {
 
 size_t int8_workspace_bytes(int a_dtype, int64_t m, int64_t K, int64_t)
 {
-    if (a_dtype == MNB_I8) return 0;
+    if (a_dtype == MNB_I8 || int8_fused(a_dtype, m, K)) return 0;
     return (size_t)(m * K) + (size_t)(m * 4);   // rows (a multiple of 16 bytes), then scales
 }
 

@@ -11,6 +11,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 #include "mnb.h"
 #include "mnb_device.h"
 #include "mnb_internal.h"
@@ -171,6 +173,7 @@ __device__ __forceinline__ uint16_t narrow16(float v, int bf16)
 
 struct Int8Params {
     const int8_t* A;        // [M][K]
+    const uint16_t* A16;    // the rows as fp16 or bf16, quantised by the kernel
     const float* a_scales;  // [M]
     const int8_t* B;        // [N][K]
     const float* b_scales;  // [N]
@@ -178,38 +181,348 @@ struct Int8Params {
     uint16_t* out;          // [M][N]
     int64_t M, N;
     int32_t K;
-    int32_t out_bf16;
+    int32_t a_bf16, out_bf16;
 };
 
-// A wave owns 16 rows by 16 columns.  v_mfma_i32_16x16x64_i8: lane (j, g)
-// supplies 16 k of row j and of column j and receives column j, rows 4 g ..
-// 4 g + 3.
-__global__ __launch_bounds__(256) void mnb_int8_kernel(Int8Params p)
+// The result of one output from its exact sum.
+__device__ __forceinline__ uint16_t finish(int sum, float a_scale, float b_scale, float bias, int out_bf16)
 {
-    const int lane = threadIdx.x & 63, j = lane & 15, g = lane >> 4;
-    const int64_t tiles_n = (p.N + 15) / 16, tiles = tiles_n * ((p.M + 15) / 16);
-    for (int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); t < tiles; t += (int64_t)gridDim.x * 4) {
-        const int64_t r0 = t / tiles_n * 16, c0 = t % tiles_n * 16;
-        const int64_t rows = p.M - r0 < 16 ? p.M - r0 : 16, cols = p.N - c0 < 16 ? p.N - c0 : 16;
-        const __amdgpu_buffer_rsrc_t rA = make_rsrc(p.A + r0 * p.K, (uint64_t)rows * p.K);
-        const __amdgpu_buffer_rsrc_t rB = make_rsrc(p.B + c0 * p.K, (uint64_t)cols * p.K);
-        i32x4 acc = {0, 0, 0, 0};
-        for (int k = 16 * g; k - 16 * g < p.K; k += 64) {
-            const uint32_t off = k < p.K ? (uint32_t)j * p.K + k : kOutOfRange;
-            const u32x4 a = __builtin_amdgcn_raw_buffer_load_b128(rA, off, 0, 0);
-            const u32x4 b = __builtin_amdgcn_raw_buffer_load_b128(rB, off, 0, 0);
-            acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, a), __builtin_bit_cast(i32x4, b),
-                                                        acc, 0, 0, 0);
+    return narrow16((float)sum * b_scale * a_scale + bias, out_bf16);
+}
+
+// Few rows (m <= 16, K <= 16384): one pass over the weights, which HBM bounds.
+//
+// A workgroup keeps the rows in LDS and walks its tiles of 16 columns.  Its
+// waves split K: wave w takes every W-th 128 bytes of it, NU of them, whose
+// weights it loads one tile ahead (16 KB to 256 KB under way per workgroup).
+// v_mfma_i32_16x16x64_i8: lane (j, g) supplies 16 k of row j and of column j.  The
+// waves' sums of a tile meet in LDS.  FUSE: the rows come as fp16 or bf16 and
+// the workgroup quantises them itself, which spares a launch.
+//
+// LDS: rows [M][K + 16] (lanes j read rows 16 bytes apart modulo 128), then the
+// sums of two tiles [2][W][64] x 16 bytes.
+inline size_t rows_lds(int64_t m, int64_t K, int waves) { return (size_t)(m * (K + 16)) + (size_t)waves * 2048; }
+
+template <int NU, bool FUSE>
+__global__ __launch_bounds__(1024) void mnb_int8_rows_kernel(Int8Params p)
+{
+    extern __shared__ u32x4 rows_lds_buf[];
+    __shared__ float row_scales[16];
+    const int tid = threadIdx.x, lane = tid & 63, j = lane & 15, g = lane >> 4;
+    const int wv = __builtin_amdgcn_readfirstlane(tid >> 6), threads = (int)blockDim.x, W = threads >> 6;
+    const int M = (int)p.M;
+    const uint32_t K = (uint32_t)p.K, stride = K + 16;
+    char* const rows = reinterpret_cast<char*>(rows_lds_buf);
+    i32x4* const part = reinterpret_cast<i32x4*>(rows + (uint32_t)M * stride);   // [2][W][64]
+
+    // This workgroup's tiles: as few for each as the busiest one needs.
+    const int tiles = (int)((p.N + 15) / 16), per = (tiles + (int)gridDim.x - 1) / (int)gridDim.x;
+    const int t0 = (int)blockIdx.x * per < tiles ? (int)blockIdx.x * per : tiles;
+    const int t1 = t0 + per < tiles ? t0 + per : tiles;
+
+    u32x4 b[NU][2];
+    // Piece (u, d) of a tile: 16 bytes of column j from 128 (wv + W u) + 64 d + 16 g.
+    auto offset = [&](int u, int d) { return 128u * (uint32_t)(wv + W * u) + 64u * d + 16u * (uint32_t)g; };
+    auto issue = [&](int t, int u) {
+        const int64_t c0 = (int64_t)t * 16, left = p.N - c0;
+        const uint32_t cols = t >= t1 ? 0u : left < 16 ? (uint32_t)left : 16u;
+        const __amdgpu_buffer_rsrc_t rB = make_rsrc_small(p.B + (t < t1 ? c0 * K : 0), cols * K);
+#pragma unroll
+        for (int d = 0; d < 2; ++d) {
+            const uint32_t k = offset(u, d);
+            b[u][d] = __builtin_amdgcn_raw_buffer_load_b128(rB, k < K ? (uint32_t)j * K + k : kOutOfRange, 0, kNontemporal);
         }
-        if (j < cols)
-            for (int i = 0; i < 4; ++i) {
-                const int64_t r = r0 + 4 * g + i;
-                if (r >= p.M) continue;
-                float v = (float)acc[i] * p.b_scales[c0 + j] * p.a_scales[r];
-                if (p.bias) v += p.bias[c0 + j];
-                p.out[r * p.N + c0 + j] = narrow16(v, p.out_bf16);
+    };
+#pragma unroll
+    for (int u = 0; u < NU; ++u) issue(t0, u);
+
+    if constexpr (FUSE) {
+        // Each row is one wave's, or with more waves than rows that of WR
+        // waves.  A lane holds eight pieces of eight elements; what a row has
+        // beyond that is read again.
+        const int pieces = (int)K / 8;
+        u32x4 v[8];
+        auto load = [&](int r, int at, int step) {
+            const __amdgpu_buffer_rsrc_t rA = make_rsrc_small(p.A16 + (int64_t)r * K, 2 * K);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                v[i] = __builtin_amdgcn_raw_buffer_load_b128(rA, 16 * (uint32_t)(at + i * step), 0, 0);
+        };
+        auto largest = [&](int r, int first, int step) {
+            uint32_t top2 = 0;
+            for (int at = first; at < pieces; at += 8 * step) {
+                load(r, at, step);
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+#pragma unroll
+                    for (int d = 0; d < 4; ++d) top2 = max_u16x2(top2, v[i][d] & 0x7FFF7FFFu);
+            }
+            uint32_t top = (top2 & 0xFFFFu) > (top2 >> 16) ? top2 & 0xFFFFu : top2 >> 16;
+#pragma unroll
+            for (int d = 32; d; d >>= 1) {
+                const uint32_t o = __shfl_xor(top, d);
+                top = o > top ? o : top;
+            }
+            return top;
+        };
+        auto store = [&](int r, uint32_t top, int first, int step) {
+            const RowScale rs = row_scale(top, p.a_bf16);
+            if (first == 0) row_scales[r] = rs.scale;
+            for (int at = first; at < pieces; at += 8 * step) {
+                if (pieces > 8 * step) load(r, at, step);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int k = at + i * step;
+                    if (k < pieces)
+                        *reinterpret_cast<u32x2*>(rows + (uint32_t)r * stride + 8 * k) = quantize_piece(v[i], rs, p.a_bf16);
+                }
+            }
+        };
+        if (M >= W) {
+            for (int r = wv; r < M; r += W) store(r, largest(r, lane, 64), lane, 64);
+        } else {
+            const int WR = W / M, r = wv / WR, first = (wv - r * WR) * 64 + lane, step = 64 * WR;
+            uint32_t* const tops = reinterpret_cast<uint32_t*>(part);   // [row][WR]
+            const uint32_t mine = r < M ? largest(r, first, step) : 0u;
+            if (lane == 0 && r < M) tops[wv] = mine;
+            __syncthreads();
+            if (r < M) {
+                uint32_t top = 0;
+                for (int w = 0; w < WR; ++w) top = tops[r * WR + w] > top ? tops[r * WR + w] : top;
+                store(r, top, first, step);
+            }
+        }
+    } else {
+        const int pieces = (int)K / 16;
+        for (int i = tid; i < M * pieces; i += threads) {
+            const int r = i / pieces;
+            *reinterpret_cast<u32x4*>(rows + 16 * (uint32_t)(i + r)) = *reinterpret_cast<const u32x4*>(p.A + 16 * (int64_t)i);
+        }
+    }
+    __syncthreads();
+
+    // Lanes of rows past M read row 0; their results are not used.
+    const char* const mine = rows + (j < M ? (uint32_t)j * stride : 0u);
+    for (int t = t0; t < t1; ++t) {
+        i32x4 acc = {0, 0, 0, 0};
+#pragma unroll
+        for (int u = 0; u < NU; ++u) {
+#pragma unroll
+            for (int d = 0; d < 2; ++d) {
+                // (Past K the weights are zeros, and the row's bytes anything.)
+                const uint32_t k = offset(u, d);
+                const i32x4 a = *reinterpret_cast<const i32x4*>(mine + (k < K ? k : 0u));
+                acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(a, __builtin_bit_cast(i32x4, b[u][d]), acc, 0, 0, 0);
+            }
+            issue(t + 1, u);
+        }
+        // Lane (j, g) holds rows 4 g .. 4 g + 3 of column j.
+        i32x4* const now = part + (t & 1) * W * 64;
+        if (4 * g < M) now[wv * 64 + lane] = acc;
+        __syncthreads();
+        // Output (row, column) by thread: the waves' sums.
+        const int* const sums = reinterpret_cast<const int*>(now);
+        for (int o = tid; o < 16 * M; o += threads) {
+            const int row = o >> 4, c = o & 15;
+            const int at = ((row >> 2) * 16 + c) * 4 + (row & 3);
+            int sum = 0;
+            for (int w = 0; w < W; ++w) sum += sums[w * 256 + at];
+            const int64_t col = (int64_t)t * 16 + c;
+            if (col < p.N)
+                p.out[row * p.N + col] = finish(sum, FUSE ? row_scales[row] : p.a_scales[row], p.b_scales[col],
+                                                p.bias ? p.bias[col] : 0.f, p.out_bf16);
+        }
+    }
+}
+
+// Sixteen bytes per lane from global memory straight into LDS (lane l to lds +
+// 16 l).  Written as assembly because the compiler makes every LDS read that
+// follows the builtin wait for the transfer; here the caller waits, once per
+// stage (wait_stage).  It has no result registers.
+__device__ __forceinline__ void load_to_lds(i32x4 rsrc, uint32_t voffset, uint32_t soffset, uint32_t lds)
+{
+    asm volatile("s_mov_b32 m0, %3\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds"
+                 :: "v"(voffset), "s"(rsrc), "s"(soffset), "s"(lds) : "memory");
+}
+
+__device__ __forceinline__ i32x4 rsrc_words(const void* base, uint32_t bytes)
+{
+    const uint64_t b = (uint64_t)(uintptr_t)base;
+    return i32x4{(int)(uint32_t)b, (int)(uint32_t)((b >> 32) & 0xFFFFu), (int)bytes, kRsrcWord3};
+}
+
+// A workgroup tile of BM rows by BN columns: WM x WN waves of (BM / WM) x (BN /
+// WN) each, and KS such sets that split each stage's K.  A stage is 128 KS
+// bytes of every row and column, NS of them in LDS: the transfers of stage t +
+// NS - 1 start when every wave is done with stage t - 1, whose place they take.
+// Rows are 128 bytes apart; 16-byte piece c of row r lies in slot c ^ (r & 7), so
+// the eight rows that one LDS access of a fragment covers lie in distinct banks.
+template <int BM, int BN, int WM, int WN, int KS, int NS>
+__global__ __launch_bounds__(64 * WM * WN * KS) void mnb_int8_tile_kernel(Int8Params p)
+{
+    constexpr int W = WM * WN * KS, RT = BM / WM / 32, CT = BN / WN / 32;
+    constexpr int PA = BM * KS / 8 / W, PB = BN * KS / 8 / W;      // transfers of a wave and stage
+    static_assert(PA * 8 * W == BM * KS && PB * 8 * W == BN * KS, "whole transfers per wave");
+    constexpr uint32_t kStage = (BM + BN) * KS * 128u;
+    static_assert((KS - 1) * WM * WN * RT * CT * 4096u <= NS * kStage, "partial sums fit the stages");
+    extern __shared__ u32x4 tile_lds[];
+    const int tid = threadIdx.x, lane = tid & 63, j = lane & 31, h = lane >> 5;
+    const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int ks = wv / (WM * WN), wm = wv / WN % WM, wn = wv % WN;
+    const uint32_t K = (uint32_t)p.K;
+    const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)tile_lds;
+
+    // Consecutive tiles share their columns; each of the 8 dies (workgroups
+    // are dealt to them in turn) gets a contiguous run of tiles, so that its
+    // L2 holds few columns at a time.
+    const int tiles_m = (int)((p.M + BM - 1) / BM);
+    const int64_t tiles = (int64_t)gridDim.x, share = tiles / 8, extra = tiles % 8;
+    const int64_t die = blockIdx.x & 7, in_die = blockIdx.x >> 3;
+    const int64_t tile = die * share + (die < extra ? die : extra) + in_die;
+    const int64_t r0 = tile % tiles_m * BM, c0 = tile / tiles_m * BN;
+    const int rows = (int)(p.M - r0 < BM ? p.M - r0 : BM), cols = (int)(p.N - c0 < BN ? p.N - c0 : BN);
+    const i32x4 rA = rsrc_words(p.A + r0 * K, (uint32_t)rows * K), rB = rsrc_words(p.B + c0 * K, (uint32_t)cols * K);
+
+    // This lane's part of the wave's transfers: slot lane % 8 of one of eight
+    // rows; rows past the last repeat it (their results are not stored).
+    const uint32_t piece = 16u * (uint32_t)((lane & 7) ^ (lane >> 3));
+    uint32_t oa[PA], ob[PB];
+#pragma unroll
+    for (int i = 0; i < PA; ++i) {
+        const int q = (wv * PA + i) * 8, r = q % BM + (lane >> 3);
+        oa[i] = (uint32_t)(r < rows ? r : rows - 1) * K + 128u * (q / BM) + piece;
+    }
+#pragma unroll
+    for (int i = 0; i < PB; ++i) {
+        const int q = (wv * PB + i) * 8, r = q % BN + (lane >> 3);
+        ob[i] = (uint32_t)(r < cols ? r : cols - 1) * K + 128u * (q / BN) + piece;
+    }
+    const int stages = (int)((K + 128u * KS - 1) / (128u * KS));
+    auto fetch = [&](int st) {
+        const uint32_t k0 = 128u * KS * (uint32_t)st, base = lds0 + (uint32_t)(st % NS) * kStage;
+#pragma unroll
+        for (int i = 0; i < PA; ++i) {
+            const int q = (wv * PA + i) * 8;
+            load_to_lds(rA, k0 + 128u * (q / BM) + piece < K ? oa[i] : kOutOfRange, k0, base + 128u * q);
+        }
+#pragma unroll
+        for (int i = 0; i < PB; ++i) {
+            const int q = (wv * PB + i) * 8;
+            load_to_lds(rB, k0 + 128u * (q / BN) + piece < K ? ob[i] : kOutOfRange, k0, base + 128u * (BM * KS + q));
+        }
+    };
+
+    typedef int i32x16 __attribute__((ext_vector_type(16)));
+    i32x16 acc[RT][CT];
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+            for (int q = 0; q < 16; ++q) acc[rt][ct][q] = 0;
+
+    // Fragment v (32 of a stage's 128 k): piece 2 v + h of row j of each tile.
+    const char* const lds = reinterpret_cast<const char*>(tile_lds);
+    const uint32_t fa = 128u * (uint32_t)(ks * BM + wm * (BM / WM) + j);
+    const uint32_t fb = 128u * (uint32_t)(BM * KS + ks * BN + wn * (BN / WN) + j);
+    auto compute = [&](int st) {
+        const char* const base = lds + (uint32_t)(st % NS) * kStage;
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+            const uint32_t slot = 16u * (uint32_t)((2 * v + h) ^ (j & 7));
+            i32x4 a[RT], b[CT];
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) a[rt] = *reinterpret_cast<const i32x4*>(base + fa + 4096 * rt + slot);
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct) b[ct] = *reinterpret_cast<const i32x4*>(base + fb + 4096 * ct + slot);
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct)
+                    acc[rt][ct] = __builtin_amdgcn_mfma_i32_32x32x32_i8(a[rt], b[ct], acc[rt][ct], 0, 0, 0);
+        }
+    };
+    constexpr int PER = PA + PB;
+#pragma unroll
+    for (int st = 0; st < NS - 1; ++st) fetch(st);       // stages past K transfer zeros
+    for (int st = 0; st < stages; ++st) {
+        // This wave's transfers of stage st are complete (those of NS - 2 later
+        // stages may be under way), its reads of stage st - 1 too; then every wave's.
+        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"i"((NS - 2) * PER) : "memory");
+        fetch(st + NS - 1);
+        compute(st);
+    }
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+
+    if constexpr (KS > 1) {
+        // Sets 1 .. KS - 1 leave their sums in LDS; set 0 adds them.
+        i32x16* const part = reinterpret_cast<i32x16*>(tile_lds);
+        auto at = [&](int k, int rt, int ct) { return ((((k - 1) * WM * WN + wm * WN + wn) * RT + rt) * CT + ct) * 64 + lane; };
+        if (ks > 0) {
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct) part[at(ks, rt, ct)] = acc[rt][ct];
+        }
+        __syncthreads();
+        if (ks > 0) return;
+#pragma unroll
+        for (int k = 1; k < KS; ++k)
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct) acc[rt][ct] += part[at(k, rt, ct)];
+    }
+
+    // Element q of lane (j, h) is row (q % 4) + 4 h + 8 (q / 4), column j.
+#pragma unroll
+    for (int ct = 0; ct < CT; ++ct) {
+        const int c = wn * (BN / WN) + 32 * ct + j;
+        if (c >= cols) continue;
+        const float bs = p.b_scales[c0 + c], bias = p.bias ? p.bias[c0 + c] : 0.f;
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+            for (int q = 0; q < 16; ++q) {
+                const int r = wm * (BM / WM) + 32 * rt + (q & 3) + 4 * h + 8 * (q >> 2);
+                if (r < rows)
+                    p.out[(r0 + r) * p.N + c0 + c] = finish(acc[rt][ct][q], p.a_scales[r0 + r], bs, bias, p.out_bf16);
             }
     }
+}
+
+typedef void (*Int8Fn)(Int8Params);
+
+template <bool FUSE>
+Int8Fn rows_kernel(int nu)
+{
+    switch (nu) {
+    case 1: return mnb_int8_rows_kernel<1, FUSE>;
+    case 2: return mnb_int8_rows_kernel<2, FUSE>;
+    case 3: return mnb_int8_rows_kernel<3, FUSE>;
+    case 4: return mnb_int8_rows_kernel<4, FUSE>;
+    case 5: return mnb_int8_rows_kernel<5, FUSE>;
+    case 6: return mnb_int8_rows_kernel<6, FUSE>;
+    case 7: return mnb_int8_rows_kernel<7, FUSE>;
+    default: return mnb_int8_rows_kernel<8, FUSE>;
+    }
+}
+
+hipError_t queue(Int8Fn fn, const Int8Params& p, int64_t grid, int threads, size_t lds, hipStream_t s)
+{
+    Int8Params q = p;
+    void* args[] = {&q};
+    const hipError_t e = hipLaunchKernel(reinterpret_cast<const void*>(fn), dim3((unsigned)grid), dim3((unsigned)threads),
+                                         args, lds, s);
+    return e != hipSuccess ? e : hipGetLastError();
+}
+
+template <int BM, int BN, int WM, int WN, int KS, int NS>
+hipError_t queue_tile(const Int8Params& p, hipStream_t s)
+{
+    const int64_t tiles = ((p.M + BM - 1) / BM) * ((p.N + BN - 1) / BN);
+    return queue(mnb_int8_tile_kernel<BM, BN, WM, WN, KS, NS>, p, tiles, 64 * WM * WN * KS,
+                 (size_t)NS * (BM + BN) * KS * 128, s);
 }
 
 }  // namespace
@@ -237,13 +550,20 @@ int launch_quantize_rows(const void* A, int a_bf16, int64_t m, int64_t K, int8_t
 
 int launch_int8(const Int8Args& a, void* stream, int* launches)
 {
-    Int8Params p;
+    int cus = 0;
+    int e = current_device_cus(&cus);
+    if (e != 0) return e;
+    const hipStream_t s = static_cast<hipStream_t>(stream);
+    const bool fuse = int8_fused(a.a_dtype, a.m, a.K);
+    Int8Params p{};
     p.A = static_cast<const int8_t*>(a.A);
+    p.A16 = static_cast<const uint16_t*>(a.A);
     p.a_scales = a.a_scales;
-    if (a.a_dtype != MNB_I8) {
+    p.a_bf16 = a.a_dtype == MNB_BF16;
+    if (a.a_dtype != MNB_I8 && !fuse) {
         int8_t* q = static_cast<int8_t*>(a.ws);
         float* scales = reinterpret_cast<float*>(q + a.m * a.K);
-        const int e = launch_quantize_rows(a.A, a.a_dtype == MNB_BF16, a.m, a.K, q, scales, stream);
+        e = launch_quantize_rows(a.A, p.a_bf16, a.m, a.K, q, scales, stream);
         if (e != 0) return e;
         ++*launches;
         p.A = q;
@@ -257,12 +577,30 @@ int launch_int8(const Int8Args& a, void* stream, int* launches)
     p.N = a.N;
     p.K = (int32_t)a.K;
     p.out_bf16 = a.out_bf16;
-    const int64_t tiles = ((a.m + 15) / 16) * ((a.N + 15) / 16), wgs = (tiles + 3) / 4;
-    hipLaunchKernelGGL(mnb_int8_kernel, dim3((unsigned)(wgs < 65536 ? wgs : 65536)), dim3(256), 0,
-                       static_cast<hipStream_t>(stream), p);
-    const int e = (int)hipGetLastError();
-    if (e == 0) ++*launches;
-    return e;
+    const int64_t units = std::max<int64_t>((a.K + 127) / 128, 1);
+    hipError_t he;
+    if (a.m <= 16 && a.K <= kInt8RowsK && rows_lds(a.m, a.K, 16) <= kInt8RowsLds) {
+        // Eight waves, two workgroups a CU, where eight units a wave cover K,
+        // both fit LDS and there is work for them; sixteen otherwise.
+        const int64_t tiles = (a.N + 15) / 16;
+        int64_t w = units <= 64 && tiles > cus && 2 * rows_lds(a.m, a.K, 8) <= kInt8RowsLds ? 8 : 16;
+        if (w > units) w = units;
+        const int nu = (int)((units + w - 1) / w);
+        w = (units + nu - 1) / nu;
+        const int64_t slots = (w <= 8 ? 2 : 1) * (int64_t)cus;
+        he = queue(fuse ? rows_kernel<true>(nu) : rows_kernel<false>(nu), p, tiles < slots ? tiles : slots,
+                   (int)(64 * w), rows_lds(a.m, a.K, (int)w), s);
+    } else if (a.m <= 32) {
+        he = queue_tile<32, 64, 1, 2, 4, 3>(p, s);
+    } else if (a.m <= 64) {
+        he = queue_tile<64, 64, 2, 2, 2, 3>(p, s);
+    } else if (a.m <= 256) {
+        he = queue_tile<128, 128, 2, 2, 2, 2>(p, s);
+    } else {
+        he = queue_tile<256, 256, 2, 4, 1, 2>(p, s);
+    }
+    if (he == hipSuccess) ++*launches;
+    return (int)he;
 }
 
 }  // namespace mnb

@@ -121,6 +121,18 @@ int launch_quantize_rows(const void* A, int a_bf16, int64_t m, int64_t K, int8_t
     MNB_WEAK;
 int launch_int8(const Int8Args& args, void* stream, int* launches) MNB_WEAK;
 
+// The kernel for few rows takes up to 16 of them where they fit its LDS with
+// the sums of its (at most 16) waves, and K up to 16 waves of eight 128-byte
+// units.
+constexpr int64_t kInt8RowsK = 16 * 8 * 128;
+constexpr size_t kInt8RowsLds = 160 * 1024 - 128;
+// Whether it also quantises fp16 or bf16 rows itself, in one launch: every
+// workgroup then reads all of them.
+inline bool int8_fused(int a_dtype, int64_t m, int64_t K)
+{
+    return a_dtype != MNB_I8 && m <= 16 && K <= kInt8RowsK && m * K <= 32768;
+}
+
 // Workspace of an 8-bit product: the quantised rows and their scales where the
 // rows come as fp16 or bf16.  Host-only arithmetic (mnb_api.cpp).
 size_t int8_workspace_bytes(int a_dtype, int64_t m, int64_t K, int64_t N);
