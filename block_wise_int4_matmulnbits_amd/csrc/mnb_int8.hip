@@ -364,8 +364,10 @@ __global__ __launch_bounds__(64 * WM * WN * KS) void mnb_int8_tile_kernel(Int8Pa
     constexpr int PA = BM * KS / 8 / W, PB = BN * KS / 8 / W;      // transfers of a wave and stage
     static_assert(PA * 8 * W == BM * KS && PB * 8 * W == BN * KS, "whole transfers per wave");
     constexpr uint32_t kStage = (BM + BN) * KS * 128u;
-    static_assert((KS - 1) * WM * WN * RT * CT * 4096u <= NS * kStage, "partial sums fit the stages");
+    static_assert((KS - 1) * WM * WN * RT * CT * 4096u + WM * WN * 32 * (2 * BN / WN + 16) <= NS * kStage,
+                  "partial sums and turned rows fit the stages");
     extern __shared__ u32x4 tile_lds[];
+    __shared__ float scale_lds[BN], bias_lds[BN];
     const int tid = threadIdx.x, lane = tid & 63, j = lane & 31, h = lane >> 5;
     const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int ks = wv / (WM * WN), wm = wv / WN % WM, wn = wv % WN;
@@ -382,6 +384,11 @@ __global__ __launch_bounds__(64 * WM * WN * KS) void mnb_int8_tile_kernel(Int8Pa
     const int64_t r0 = tile % tiles_m * BM, c0 = tile / tiles_m * BN;
     const int rows = (int)(p.M - r0 < BM ? p.M - r0 : BM), cols = (int)(p.N - c0 < BN ? p.N - c0 : BN);
     const i32x4 rA = rsrc_words(p.A + r0 * K, (uint32_t)rows * K), rB = rsrc_words(p.B + c0 * K, (uint32_t)cols * K);
+
+    for (int c = tid; c < BN; c += 64 * W) {
+        scale_lds[c] = c < cols ? p.b_scales[c0 + c] : 0.f;
+        bias_lds[c] = c < cols && p.bias ? p.bias[c0 + c] : 0.f;
+    }
 
     // This lane's part of the wave's transfers: slot lane % 8 of one of eight
     // rows; rows past the last repeat it (their results are not stored).
@@ -439,7 +446,7 @@ __global__ __launch_bounds__(64 * WM * WN * KS) void mnb_int8_tile_kernel(Int8Pa
             for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
                 for (int ct = 0; ct < CT; ++ct)
-                    acc[rt][ct] = __builtin_amdgcn_mfma_i32_32x32x32_i8(a[rt], b[ct], acc[rt][ct], 0, 0, 0);
+                    acc[rt][ct] = __builtin_amdgcn_mfma_i32_32x32x32_i8(b[ct], a[rt], acc[rt][ct], 0, 0, 0);
         }
     };
     constexpr int PER = PA + PB;
@@ -474,20 +481,51 @@ __global__ __launch_bounds__(64 * WM * WN * KS) void mnb_int8_tile_kernel(Int8Pa
                 for (int ct = 0; ct < CT; ++ct) acc[rt][ct] += part[at(k, rt, ct)];
     }
 
-    // Element q of lane (j, h) is row (q % 4) + 4 h + 8 (q / 4), column j.
+    // The weights are the product's first operand, so element q of lane (j,
+    // h) is row j, column (q % 4) + 4 h + 8 (q / 4): four neighbours of one row
+    // at a time.  A wave turns each 32 rows of its part through LDS into whole
+    // 16-byte pieces of rows (one 2-byte store per element had cost the 256 x
+    // 128 tile 10 us).
+    constexpr int CW = BN / WN, kPitch = 2 * CW + 16;   // bytes of a turned row
+    char* const turn = reinterpret_cast<char*>(tile_lds) + (KS - 1) * WM * WN * RT * CT * 4096 + (wm * WN + wn) * 32 * kPitch;
+    const bool pieces_ok = (p.N & 7) == 0 && ((uintptr_t)p.out & 15) == 0;
+    const int wc = wn * CW, width = cols - wc < CW ? cols - wc : CW;   // the wave's columns
 #pragma unroll
-    for (int ct = 0; ct < CT; ++ct) {
-        const int c = wn * (BN / WN) + 32 * ct + j;
-        if (c >= cols) continue;
-        const float bs = p.b_scales[c0 + c], bias = p.bias ? p.bias[c0 + c] : 0.f;
+    for (int rt = 0; rt < RT; ++rt) {
+        const int wr = wm * (BM / WM) + 32 * rt;
+        const float as = p.a_scales[r0 + (wr + j < rows ? wr + j : rows - 1)];
 #pragma unroll
-        for (int rt = 0; rt < RT; ++rt)
+        for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
-            for (int q = 0; q < 16; ++q) {
-                const int r = wm * (BM / WM) + 32 * rt + (q & 3) + 4 * h + 8 * (q >> 2);
-                if (r < rows)
-                    p.out[(r0 + r) * p.N + c0 + c] = finish(acc[rt][ct][q], p.a_scales[r0 + r], bs, bias, p.out_bf16);
+            for (int q4 = 0; q4 < 4; ++q4) {
+                const int c = 32 * ct + 8 * q4 + 4 * h;
+                const float4_t bs = *reinterpret_cast<const float4_t*>(&scale_lds[wc + c]);
+                const float4_t bias = *reinterpret_cast<const float4_t*>(&bias_lds[wc + c]);
+                uint32_t o[2];
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    o[i] = finish(acc[rt][ct][4 * q4 + 2 * i], as, bs[2 * i], bias[2 * i], p.out_bf16) |
+                           (uint32_t)finish(acc[rt][ct][4 * q4 + 2 * i + 1], as, bs[2 * i + 1], bias[2 * i + 1], p.out_bf16) << 16;
+                *reinterpret_cast<u32x2*>(turn + j * kPitch + 2 * c) = u32x2{o[0], o[1]};
             }
+        __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
+        if (pieces_ok) {
+            constexpr int LPR = CW / 8;                 // lanes of a row
+#pragma unroll
+            for (int i = 0; i < 32 * LPR / 64; ++i) {
+                const int r = i * (64 / LPR) + lane / LPR, c = lane % LPR * 8;
+                if (wr + r < rows && c < width)
+                    *reinterpret_cast<u32x4*>(p.out + (r0 + wr + r) * p.N + c0 + wc + c) =
+                        *reinterpret_cast<const u32x4*>(turn + r * kPitch + 2 * c);
+            }
+        } else {
+            for (int i = lane; i < 32 * CW; i += 64) {
+                const int r = i / CW, c = i % CW;
+                if (wr + r < rows && c < width)
+                    p.out[(r0 + wr + r) * p.N + c0 + wc + c] = *reinterpret_cast<const uint16_t*>(turn + r * kPitch + 2 * c);
+            }
+        }
+        __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
     }
 }
 
