@@ -351,21 +351,27 @@ __device__ __forceinline__ i32x4 rsrc_words(const void* base, uint32_t bytes)
     return i32x4{(int)(uint32_t)b, (int)(uint32_t)((b >> 32) & 0xFFFFu), (int)bytes, kRsrcWord3};
 }
 
+// Sixteen bytes at any even address (rows of an odd number of columns).
+struct __attribute__((packed, aligned(2))) Loose16 {
+    u32x4 v;
+};
+
 // A workgroup tile of BM rows by BN columns: WM x WN waves of (BM / WM) x (BN /
-// WN) each, and KS such sets that split each stage's K.  A stage is 128 KS
-// bytes of every row and column, NS of them in LDS: the transfers of stage t +
-// NS - 1 start when every wave is done with stage t - 1, whose place they take.
-// Rows are 128 bytes apart; 16-byte piece c of row r lies in slot c ^ (r & 7), so
-// the eight rows that one LDS access of a fragment covers lie in distinct banks.
-template <int BM, int BN, int WM, int WN, int KS, int NS>
+// WN) each, and KS such sets that split each stage's K.  A stage is KB (64 or
+// 128) bytes of every row and column for each set, NS of them in LDS.  Rows lie KB bytes apart; 16-byte piece c of row r in
+// slot c ^ swizzle(r), so that the eight rows that one LDS access of a fragment
+// covers lie in distinct banks.
+template <int BM, int BN, int WM, int WN, int KS, int NS, int KB>
 __global__ __launch_bounds__(64 * WM * WN * KS) void mnb_int8_tile_kernel(Int8Params p)
 {
     constexpr int W = WM * WN * KS, RT = BM / WM / 32, CT = BN / WN / 32;
-    constexpr int PA = BM * KS / 8 / W, PB = BN * KS / 8 / W;      // transfers of a wave and stage
-    static_assert(PA * 8 * W == BM * KS && PB * 8 * W == BN * KS, "whole transfers per wave");
-    constexpr uint32_t kStage = (BM + BN) * KS * 128u;
+    constexpr int LR = KB / 16, RR = 64 / LR;                        // lanes of a row, rows of a transfer
+    constexpr int PA = BM * KS / RR / W, PB = BN * KS / RR / W;      // transfers of a wave and stage
+    static_assert(PA * RR * W == BM * KS && PB * RR * W == BN * KS, "whole transfers per wave");
+    constexpr uint32_t kStage = (BM + BN) * KS * KB;
     static_assert((KS - 1) * WM * WN * RT * CT * 4096u + WM * WN * 32 * (2 * BN / WN + 16) <= NS * kStage,
                   "partial sums and turned rows fit the stages");
+    auto swizzle = [](int r) { return KB == 128 ? r & 7 : (r >> 1) & 3; };
     extern __shared__ u32x4 tile_lds[];
     __shared__ float scale_lds[BN], bias_lds[BN];
     const int tid = threadIdx.x, lane = tid & 63, j = lane & 31, h = lane >> 5;
@@ -390,32 +396,36 @@ __global__ __launch_bounds__(64 * WM * WN * KS) void mnb_int8_tile_kernel(Int8Pa
         bias_lds[c] = c < cols && p.bias ? p.bias[c0 + c] : 0.f;
     }
 
-    // This lane's part of the wave's transfers: slot lane % 8 of one of eight
-    // rows; rows past the last repeat it (their results are not stored).
-    const uint32_t piece = 16u * (uint32_t)((lane & 7) ^ (lane >> 3));
+    // This lane's part of the wave's transfers: one slot of one of RR rows;
+    // rows past the last repeat it (their results are not stored).
+    const uint32_t piece = 16u * (uint32_t)((lane % LR) ^ swizzle(lane / LR));
     uint32_t oa[PA], ob[PB];
 #pragma unroll
     for (int i = 0; i < PA; ++i) {
-        const int q = (wv * PA + i) * 8, r = q % BM + (lane >> 3);
-        oa[i] = (uint32_t)(r < rows ? r : rows - 1) * K + 128u * (q / BM) + piece;
+        const int q = (wv * PA + i) * RR, r = q % BM + lane / LR;
+        oa[i] = (uint32_t)(r < rows ? r : rows - 1) * K + KB * (q / BM) + piece;
     }
 #pragma unroll
     for (int i = 0; i < PB; ++i) {
-        const int q = (wv * PB + i) * 8, r = q % BN + (lane >> 3);
-        ob[i] = (uint32_t)(r < cols ? r : cols - 1) * K + 128u * (q / BN) + piece;
+        const int q = (wv * PB + i) * RR, r = q % BN + lane / LR;
+        ob[i] = (uint32_t)(r < cols ? r : cols - 1) * K + KB * (q / BN) + piece;
     }
-    const int stages = (int)((K + 128u * KS - 1) / (128u * KS));
-    auto fetch = [&](int st) {
-        const uint32_t k0 = 128u * KS * (uint32_t)st, base = lds0 + (uint32_t)(st % NS) * kStage;
+    const int stages = (int)((K + KB * KS - 1) / (KB * KS));
+    // Transfers [i0, i1) of the wave's PER of stage st.
+    constexpr int PER = PA + PB, V = KB / 32;
+    auto fetch = [&](int st, int i0, int i1) {
+        const uint32_t k0 = KB * KS * (uint32_t)st, base = lds0 + (uint32_t)(st % NS) * kStage;
 #pragma unroll
         for (int i = 0; i < PA; ++i) {
-            const int q = (wv * PA + i) * 8;
-            load_to_lds(rA, k0 + 128u * (q / BM) + piece < K ? oa[i] : kOutOfRange, k0, base + 128u * q);
+            const int q = (wv * PA + i) * RR;
+            if (i >= i0 && i < i1)
+                load_to_lds(rA, k0 + KB * (q / BM) + piece < K ? oa[i] : kOutOfRange, k0, base + KB * q);
         }
 #pragma unroll
         for (int i = 0; i < PB; ++i) {
-            const int q = (wv * PB + i) * 8;
-            load_to_lds(rB, k0 + 128u * (q / BN) + piece < K ? ob[i] : kOutOfRange, k0, base + 128u * (BM * KS + q));
+            const int q = (wv * PB + i) * RR;
+            if (PA + i >= i0 && PA + i < i1)
+                load_to_lds(rB, k0 + KB * (q / BN) + piece < K ? ob[i] : kOutOfRange, k0, base + KB * (BM * KS + q));
         }
     };
 
@@ -428,36 +438,51 @@ __global__ __launch_bounds__(64 * WM * WN * KS) void mnb_int8_tile_kernel(Int8Pa
 #pragma unroll
             for (int q = 0; q < 16; ++q) acc[rt][ct][q] = 0;
 
-    // Fragment v (32 of a stage's 128 k): piece 2 v + h of row j of each tile.
+    // Fragment v (32 of a stage's k): piece 2 v + h of row j of each tile.
     const char* const lds = reinterpret_cast<const char*>(tile_lds);
-    const uint32_t fa = 128u * (uint32_t)(ks * BM + wm * (BM / WM) + j);
-    const uint32_t fb = 128u * (uint32_t)(BM * KS + ks * BN + wn * (BN / WN) + j);
-    auto compute = [&](int st) {
-        const char* const base = lds + (uint32_t)(st % NS) * kStage;
+    const uint32_t fa = KB * (uint32_t)(ks * BM + wm * (BM / WM) + j);
+    const uint32_t fb = KB * (uint32_t)(BM * KS + ks * BN + wn * (BN / WN) + j);
+    auto read = [&](int st, int v, i32x4 (&a)[RT], i32x4 (&b)[CT]) {
+        const char* const base = lds + (uint32_t)(st % NS) * kStage + 16u * (uint32_t)((2 * v + h) ^ swizzle(j));
 #pragma unroll
-        for (int v = 0; v < 4; ++v) {
-            const uint32_t slot = 16u * (uint32_t)((2 * v + h) ^ (j & 7));
-            i32x4 a[RT], b[CT];
+        for (int ct = 0; ct < CT; ++ct) b[ct] = *reinterpret_cast<const i32x4*>(base + fb + 32 * KB * ct);
 #pragma unroll
-            for (int rt = 0; rt < RT; ++rt) a[rt] = *reinterpret_cast<const i32x4*>(base + fa + 4096 * rt + slot);
+        for (int rt = 0; rt < RT; ++rt) a[rt] = *reinterpret_cast<const i32x4*>(base + fa + 32 * KB * rt);
+    };
+    // Each of a stage's V fragments multiplies while the next one's operands
+    // are read.  Stage st + 1 is waited for, and its first operands are read,
+    // before the last products of stage st, which cover that: this wave's
+    // transfers of it are complete (later ones may be under way) and its
+    // reads of stage st too, then every wave's.  From there on stage st + NS
+    // takes the place of stage st, a part of its transfers with each
+    // fragment: all at once they hold up the waves, which issue in order
+    // behind them (256 x 128 on 2048 x 14336 x 4096: 121 -> 115 us; without any
+    // transfers 96, with the products alone 85).
+    // (Stages past K transfer zeros.)
+    i32x4 a[2][RT], b[2][CT];
+    auto turn_over = [&](int st) {
+        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier"
+                     ::"i"((NS - 3) * PER + PER * (V - 1) / V) : "memory");
+        read(st + 1, 0, a[0], b[0]);
+    };
+    static_assert(NS >= 3, "a stage's transfers are issued over the length of one");
 #pragma unroll
-            for (int ct = 0; ct < CT; ++ct) b[ct] = *reinterpret_cast<const i32x4*>(base + fb + 4096 * ct + slot);
+    for (int st = 0; st < NS - 2; ++st) fetch(st, 0, PER);
+    fetch(NS - 2, 0, PER * (V - 1) / V);
+    turn_over(-1);
+    fetch(NS - 2, PER * (V - 1) / V, PER);
+    for (int st = 0; st < stages; ++st) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            if (v + 1 < V) read(st, v + 1, a[(v + 1) & 1], b[(v + 1) & 1]);
+            else turn_over(st);
+            fetch(st + NS - 1, PER * v / V, PER * (v + 1) / V);
 #pragma unroll
             for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
                 for (int ct = 0; ct < CT; ++ct)
-                    acc[rt][ct] = __builtin_amdgcn_mfma_i32_32x32x32_i8(b[ct], a[rt], acc[rt][ct], 0, 0, 0);
+                    acc[rt][ct] = __builtin_amdgcn_mfma_i32_32x32x32_i8(b[v & 1][ct], a[v & 1][rt], acc[rt][ct], 0, 0, 0);
         }
-    };
-    constexpr int PER = PA + PB;
-#pragma unroll
-    for (int st = 0; st < NS - 1; ++st) fetch(st);       // stages past K transfer zeros
-    for (int st = 0; st < stages; ++st) {
-        // This wave's transfers of stage st are complete (those of NS - 2 later
-        // stages may be under way), its reads of stage st - 1 too; then every wave's.
-        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"i"((NS - 2) * PER) : "memory");
-        fetch(st + NS - 1);
-        compute(st);
     }
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
 
@@ -488,7 +513,6 @@ __global__ __launch_bounds__(64 * WM * WN * KS) void mnb_int8_tile_kernel(Int8Pa
     // 128 tile 10 us).
     constexpr int CW = BN / WN, kPitch = 2 * CW + 16;   // bytes of a turned row
     char* const turn = reinterpret_cast<char*>(tile_lds) + (KS - 1) * WM * WN * RT * CT * 4096 + (wm * WN + wn) * 32 * kPitch;
-    const bool pieces_ok = (p.N & 7) == 0 && ((uintptr_t)p.out & 15) == 0;
     const int wc = wn * CW, width = cols - wc < CW ? cols - wc : CW;   // the wave's columns
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
@@ -509,20 +533,17 @@ __global__ __launch_bounds__(64 * WM * WN * KS) void mnb_int8_tile_kernel(Int8Pa
                 *reinterpret_cast<u32x2*>(turn + j * kPitch + 2 * c) = u32x2{o[0], o[1]};
             }
         __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
-        if (pieces_ok) {
-            constexpr int LPR = CW / 8;                 // lanes of a row
+        constexpr int LPR = CW / 8;                     // lanes of a row
 #pragma unroll
-            for (int i = 0; i < 32 * LPR / 64; ++i) {
-                const int r = i * (64 / LPR) + lane / LPR, c = lane % LPR * 8;
-                if (wr + r < rows && c < width)
-                    *reinterpret_cast<u32x4*>(p.out + (r0 + wr + r) * p.N + c0 + wc + c) =
-                        *reinterpret_cast<const u32x4*>(turn + r * kPitch + 2 * c);
-            }
-        } else {
-            for (int i = lane; i < 32 * CW; i += 64) {
-                const int r = i / CW, c = i % CW;
-                if (wr + r < rows && c < width)
-                    p.out[(r0 + wr + r) * p.N + c0 + wc + c] = *reinterpret_cast<const uint16_t*>(turn + r * kPitch + 2 * c);
+        for (int i = 0; i < 32 * LPR / 64; ++i) {
+            const int r = i * (64 / LPR) + lane / LPR, c = lane % LPR * 8;
+            if (wr + r >= rows || c >= width) continue;
+            uint16_t* const out = p.out + (r0 + wr + r) * p.N + c0 + wc + c;
+            const uint16_t* const from = reinterpret_cast<const uint16_t*>(turn + r * kPitch + 2 * c);
+            if (c + 8 <= width) {
+                reinterpret_cast<Loose16*>(out)->v = *reinterpret_cast<const u32x4*>(from);
+            } else {
+                for (int k = 0; k < width - c; ++k) out[k] = from[k];
             }
         }
         __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
@@ -555,12 +576,43 @@ hipError_t queue(Int8Fn fn, const Int8Params& p, int64_t grid, int threads, size
     return e != hipSuccess ? e : hipGetLastError();
 }
 
-template <int BM, int BN, int WM, int WN, int KS, int NS>
+// The tile with the least time: rounds of one tile per CU, each a fixed part
+// (filling the stages, the epilogue) and one that grows with K, us and us per
+// 1024 of K.  Fitted to the seven tiles' times on 72 shapes (m = 17 .. 2048; K
+// x N = 4096 x 4096, 4096 x 28672, 14336 x 4096, 4112 x 5999, 1024 x 8192, 8192 x
+// 1024); its choice is 0.4% slower than the fastest tile on average, at most
+// 12% (8.1 against 7.3 us, 32 x 1024 x 8192).  256 x 256 against 256 x 128 on 2048 x
+// 4096 x 28672: 250 and 260 us, on 2048 x 14336 x 4096: 158 and 113; 32 x 32
+// against 64 x 64 on 32 x 14336 x 4096: 21 and 38, on 256 x 4096 x 4096: 24 and 14.
+struct TileCost {
+    int bm, bn;
+    double fixed, per_k;
+};
+constexpr TileCost kTiles[] = {{256, 256, 8.0, 13.4}, {256, 128, 8.0, 7.2}, {128, 128, 4.5, 4.4}, {128, 64, 5.5, 2.85},
+                               {64, 64, 5.0, 2.33},   {64, 32, 4.8, 1.42},  {32, 32, 4.5, 0.98}};
+
+int cheapest_tile(int64_t m, int64_t K, int64_t N, int cus)
+{
+    int best = 0;
+    double least = 0;
+    for (int t = 0; t < (int)(sizeof(kTiles) / sizeof(kTiles[0])); ++t) {
+        const TileCost& c = kTiles[t];
+        const int64_t tiles = ((m + c.bm - 1) / c.bm) * ((N + c.bn - 1) / c.bn), rounds = (tiles + cus - 1) / cus;
+        const double us = (double)rounds * (c.fixed + c.per_k * (double)K / 1024);
+        if (t == 0 || us < least) {
+            best = t;
+            least = us;
+        }
+    }
+    return best;
+}
+
+template <int BM, int BN, int WM, int WN, int KS, int NS, int KB>
 hipError_t queue_tile(const Int8Params& p, hipStream_t s)
 {
     const int64_t tiles = ((p.M + BM - 1) / BM) * ((p.N + BN - 1) / BN);
-    return queue(mnb_int8_tile_kernel<BM, BN, WM, WN, KS, NS>, p, tiles, 64 * WM * WN * KS,
-                 (size_t)NS * (BM + BN) * KS * 128, s);
+    return queue(mnb_int8_tile_kernel<BM, BN, WM, WN, KS, NS, KB>, p, tiles, 64 * WM * WN * KS,
+                 (size_t)NS * (BM + BN) * KS * KB, s);
 }
 
 }  // namespace
@@ -628,14 +680,16 @@ int launch_int8(const Int8Args& a, void* stream, int* launches)
         const int64_t slots = (w <= 8 ? 2 : 1) * (int64_t)cus;
         he = queue(fuse ? rows_kernel<true>(nu) : rows_kernel<false>(nu), p, tiles < slots ? tiles : slots,
                    (int)(64 * w), rows_lds(a.m, a.K, (int)w), s);
-    } else if (a.m <= 32) {
-        he = queue_tile<32, 64, 1, 2, 4, 3>(p, s);
-    } else if (a.m <= 64) {
-        he = queue_tile<64, 64, 2, 2, 2, 3>(p, s);
-    } else if (a.m <= 256) {
-        he = queue_tile<128, 128, 2, 2, 2, 2>(p, s);
     } else {
-        he = queue_tile<256, 256, 2, 4, 1, 2>(p, s);
+        switch (cheapest_tile(a.m, a.K, a.N, cus)) {
+        case 0: he = queue_tile<256, 256, 2, 4, 1, 4, 64>(p, s); break;
+        case 1: he = queue_tile<256, 128, 4, 2, 1, 3, 128>(p, s); break;
+        case 2: he = queue_tile<128, 128, 2, 4, 1, 4, 128>(p, s); break;
+        case 3: he = queue_tile<128, 64, 2, 2, 2, 3, 128>(p, s); break;
+        case 4: he = queue_tile<64, 64, 2, 2, 2, 3, 128>(p, s); break;
+        case 5: he = queue_tile<64, 32, 2, 1, 4, 3, 128>(p, s); break;
+        default: he = queue_tile<32, 32, 1, 1, 4, 4, 128>(p, s); break;
+        }
     }
     if (he == hipSuccess) ++*launches;
     return (int)he;
