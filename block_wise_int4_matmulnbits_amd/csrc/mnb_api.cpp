@@ -425,24 +425,43 @@ size_t int8_workspace_bytes(int a_dtype, int64_t m, int64_t K, int64_t)
 
 MoeLayout moe_layout(int64_t T, int64_t H, int64_t I, int64_t E, int top_k)
 {
-    (void)H;
     const int64_t pairs = T * top_k;
-    MoeLayout l;
-    // Rows of a batch: two quads once the experts see more than four tokens
-    // on average.
-    l.rq = pairs > 4 * E ? 2 : 1;
+    MoeLayout l{};
+    // The kernels and the rows of a batch, by the tokens an expert sees on
+    // average (us, narrow with 4 or 8 rows against wide with 16 or 32): 6
+    // tokens (24 tokens, 2 of 8 experts of 4096, 14336) 219 against 248 and
+    // 286; 8 (32 tokens) 312 against 252 and 293, (64 tokens, 8 of 64 of 2048,
+    // 768) 97 against 101 and 125; 16 (64 tokens, 2 of 8) 451 against 400 and
+    // 337, (64 tokens, 8 of 32 of 2048, 768) 87 against 86 and 84.
+    l.wide = pairs > 12 * E ? 2 : pairs >= 8 * E ? 1 : 0;
+    l.rq = l.wide ? 4 * l.wide : pairs > 4 * E ? 2 : 1;
     // Every expert has at most one batch that is not full.
     const int64_t rows = 4 * l.rq;
     int64_t batches = std::min(pairs, E) + pairs / rows;
     if (batches > pairs) batches = pairs;
     l.batches = (int)batches;
-    auto align = [](size_t x) { return (x + 255) & ~(size_t)255; };
-    l.batch_e = align((size_t)(1 + T) * 4);
-    l.row_token = l.batch_e + align((size_t)batches * 4);
-    l.row_p = l.row_token + align((size_t)(batches * rows) * 4);
-    l.hs = l.row_p + align((size_t)(batches * rows) * 4);
-    l.h = l.hs + align((size_t)(batches * rows * (I / 32)) * 4);
-    l.bytes = l.h + (size_t)(batches * rows * ((I / 32 + 15) / 16 * 512)) * 2;   // blocks of I in groups of 16
+    size_t at = 0;
+    auto take = [&](int64_t bytes) {
+        const size_t here = at;
+        at = (at + (size_t)bytes + 255) & ~(size_t)255;
+        return here;
+    };
+    take((1 + T) * 4);
+    l.batch_e = take(batches * 4);
+    l.row_token = take(batches * rows * 4);
+    l.row_p = take(batches * rows * 4);
+    if (l.wide) {
+        l.hs = take(batches * rows * 4);
+        l.h = take(batches * rows * I * 2);
+        l.pair_row = take(pairs * 4);
+        l.xs = take(T * H * 2);
+        l.hf = take(batches * rows * I * 4);
+        l.y = take(batches * rows * H * 4);
+    } else {
+        l.hs = take(batches * rows * (I / 32) * 4);
+        l.h = take(batches * rows * ((I / 32 + 15) / 16 * 512) * 2);   // blocks of I in groups of 16
+    }
+    l.bytes = at;
     return l;
 }
 

@@ -1,5 +1,6 @@
-// A mixture-of-experts layer of 4-bit weights for a few tokens (gfx950), in two
-// launches.
+// A mixture-of-experts layer of 4-bit weights for a few tokens (gfx950): two
+// launches of narrow kernels (described here), or five of wide ones where the
+// experts see eight tokens or more on average (moe_layout; further down).
 //
 //   out[t] = sum_j p[t][j] * Down_e( silu(Gate_e x[t]) * (Up_e x[t]) ),  e = ids[t][j]
 //
@@ -39,6 +40,7 @@ namespace mnb {
 namespace {
 
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 half8_t __attribute__((ext_vector_type(8)));
 
 constexpr int kMaxSlots = MNB_MOE_MAX_EXPERTS / 64;   // experts per lane of a routing wave
 // First launch: 4 column waves by 2 slices of K, loads two steps ahead.  HBM sets
@@ -46,6 +48,9 @@ constexpr int kMaxSlots = MNB_MOE_MAX_EXPERTS / 64;   // experts per lane of a r
 // four steps ahead gained nothing, 16 waves (128 registers) spilled and cost
 // 40%, 4 waves with 4 steps ahead 20%.
 constexpr int kUpWaves = 8, kUpRing = 2;
+constexpr size_t kLdsBytes = 160 * 1024;
+// Static LDS of the first launch: two units' partial sums, the waves' scales.
+constexpr size_t up_static_lds(int rq) { return (size_t)2 * kUpWaves * 64 * rq * 4 + kUpWaves * 640; }
 constexpr int kPadToken = 255;                        // a batch's unused rows
 
 struct MoeParams {
@@ -63,6 +68,12 @@ struct MoeParams {
     float* row_p;        // its weight
     uint16_t* h;         // [batch][RQ], 128 * ceil16(I/32) each: see above
     float* hs;           // [batch][RQ][I/32][4]: powers of two
+    // Workspace of the wide kernels.
+    int32_t* pair_row;   // [T][top_k]: row of the batches, or -1
+    uint16_t* xs;        // [T][H]: activations as fp16, in the unpack's order
+    float* hf;           // [row][I]: silu(g) u
+    uint16_t* hq;        // [row][I]: its fp16 form, in the unpack's order
+    float* y;            // [row][H]: weighted outputs of the rows
     int32_t T, H, I, E, top_k;
     int32_t x_bf16, logits_dtype, renormalize, out_bf16;
     int32_t batch_cap;      // batches the workspace holds
@@ -268,13 +279,16 @@ __device__ __forceinline__ int route(const MoeParams& p, const Routing& r, F mea
     const int pairs = p.T * p.top_k;
     for (int s = tid; s < pairs; s += threads) {
         const int e = r.sel[s], t = s / p.top_k;
+        int row = -1;
         if (e >= 0) {
             const int rank = __popcll(r.mask[e] & ((1ull << t) - 1));
-            const int b = r.first[e] + rank / (4 * RQ), row = b * 4 * RQ + rank % (4 * RQ);
+            const int b = r.first[e] + rank / (4 * RQ);
+            row = b * 4 * RQ + rank % (4 * RQ);
             r.token()[row] = (uint8_t)t;
             if (rank % (4 * RQ) == 0) r.batch_e[b] = (uint16_t)e;
             if (tell) p.row_p[row] = r.p[s];
         }
+        if (tell && p.pair_row) p.pair_row[s] = row;
         if (tell && p.ids_out) p.ids_out[s] = e;
         if (tell && p.probs_out) p.probs_out[s] = r.p[s];
     }
@@ -740,6 +754,315 @@ __global__ __launch_bounds__(64 * W) void mnb_moe_down_kernel(MoeParams p)
     }
 }
 
+// More rows per expert: the same layer on v_mfma_f32_16x16x32_f16, in five
+// launches.  The 4x4x4 product's four rows per instruction make the matrix
+// cores the bound from some eight rows on; here sixteen rows cost one
+// 16-cycle product per 256 bytes of weights, and what bounds the loop is the
+// unpacking.  Lane (j, g) supplies 8 k of column j and of row j and receives
+// column j, rows 4 g .. 4 g + 3; one product spans one 32-weight block, whose
+// scale is applied to its result, as above.
+//
+// A unit is one batch (16 RT rows of one expert) by 64 columns of weights: 32
+// gate and the same 32 up columns, or 64 down columns.  The eight waves of a
+// workgroup split K, and each takes all 64 columns of its part, so a row's
+// activations are read once per unit, straight into registers in the
+// product's order, and LDS holds only the waves' sums.  The activations h go
+// through fp32 to fp16 with one power of two per row (scale_rows): with a
+// scale per block, as in the narrow kernels, every product would need the
+// scales of its four rows.
+constexpr int kWideWaves = 8;
+constexpr uint32_t kPastRows = 0xF0000000u;   // out of range, also with a small offset added
+
+// Launch 1: the tables (workgroup 0) and x as fp16 in the unpack's order.
+template <int RT>
+__global__ __launch_bounds__(512) void mnb_moe_prepare_kernel(MoeParams p)
+{
+    extern __shared__ u32x4 prepare_lds[];
+    const int64_t pieces = (int64_t)p.T * p.H / 8;
+    for (int64_t i = (int64_t)blockIdx.x * 512 + threadIdx.x; i < pieces; i += (int64_t)gridDim.x * 512)
+        reinterpret_cast<u32x4*>(p.xs)[i] = f16_pairs(reinterpret_cast<const u32x4*>(p.x)[i], p.x_bf16, 0);
+    if (blockIdx.x != 0) return;
+    const Routing rt = routing_tables(reinterpret_cast<uint8_t*>(prepare_lds), p.E, p.T * p.top_k, p.batch_cap, 4 * RT);
+    route<4 * RT>(p, rt, [] {});
+}
+
+// Launches 2 (UP: x through gate and up to hf) and 4 (h through down to y).
+template <int RT, bool UP, int VEC>
+__global__ __launch_bounds__(64 * kWideWaves) void mnb_moe_wide_kernel(MoeParams p)
+{
+    constexpr int R = 16 * RT, CT = 4, W = kWideWaves;
+    __shared__ float part[W][CT * RT * 4][64];
+    __shared__ u32x4 scale_lds[W][64 * 20 / 16];    // of two steps: [64 columns][8 fp16], then [64][4]
+    // The tables, so that the loop reads none from memory (it would wait for
+    // its own loads ahead): the batches, then each row's token (UP) or scale.
+    extern __shared__ int wide_lds[];
+    int* const batch = wide_lds;
+    int* const row_info = batch + p.batch_cap;
+    const int tid = threadIdx.x, lane = tid & 63, j = lane & 15, g = lane >> 4;
+    const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int K = UP ? p.H : p.I, N = UP ? p.I : p.H;
+    const int nb = K / 32, zb = (nb + 1) / 2, tiles = (N + (UP ? 31 : 63)) / (UP ? 32 : 64);
+    const uint8_t* const wq = UP ? p.w1 : p.w2;
+    const uint16_t* const sq = UP ? p.s1 : p.s2;
+    const uint8_t* const zq = UP ? p.z1 : p.z2;
+    const uint32_t row_bytes = (uint32_t)K / 2, zdef = zq ? 0u : 0x8888u;   // zero points of four blocks
+    const uint32_t magic = vgpr_constant(0x64006400u, p.zero);
+    const int64_t units = (int64_t)p.head[0] * tiles;
+    for (int i = tid; i < p.batch_cap; i += 64 * W) batch[i] = p.batch_e[i];
+    for (int i = tid; i < p.batch_cap * R; i += 64 * W) row_info[i] = UP ? p.row_token[i] : __float_as_int(p.hs[i]);
+    __syncthreads();
+    const int per = (int)((units + gridDim.x - 1) / gridDim.x);
+    const int u0 = std::min<int>((int)blockIdx.x * per, (int)units), u1 = std::min<int>(u0 + per, (int)units);
+    // K in steps of four blocks; a wave takes two neighbours of every 16, whose
+    // weights share 128-byte lines.
+    const int quads = (nb + 3) / 4, steps = (quads + 2 * W - 1) / (2 * W) * 2;
+    // Column of this lane's weights in tile ct, and of its scales: UP tiles 0
+    // and 1 are gate columns, 2 and 3 the up columns of the same h.
+    const uint32_t up = (uint32_t)p.I;
+    const uint32_t scol = UP ? (uint32_t)(lane & 31) + (lane >> 5) * up : (uint32_t)lane;
+
+    struct Step {
+        u32x4 w[CT], a[RT][4];
+    };
+    // Scales and zero points of this lane's column for two steps, eight
+    // blocks, in as few loads as the rows' length and alignment allow: VEC
+    // blocks at a time (every load touches 64 lines, one per column).
+    struct Scales {
+        uint32_t s[VEC > 1 ? 4 : 8], z[VEC == 8 ? 1 : VEC == 4 ? 2 : 4];
+    };
+    int left = (u1 - u0) * steps, nbatch = u0 / tiles, ntile = u0 - nbatch * tiles, nstep = 0;
+    uint32_t wo[CT];                                 // this lane's weights
+#pragma unroll
+    for (int ct = 0; ct < CT; ++ct)
+        wo[ct] = (UP ? (uint32_t)(16 * (ct & 1) + j) + (ct >> 1) * up : (uint32_t)(16 * ct + j)) * row_bytes + 16 * (uint32_t)g;
+    const uint32_t so = 2 * scol * (uint32_t)nb, zo = scol * (uint32_t)zb;
+    uint32_t arow[RT];                               // and its rows of activations, or kPastRows
+    __amdgpu_buffer_rsrc_t rW, rS, rZ, rA;
+    auto enter = [&] {                               // the unit (nbatch, ntile)
+        const bool live = left > 0;
+        const int entry = live ? __builtin_amdgcn_readfirstlane(batch[nbatch]) : 0, rows = entry >> 16;
+        const int64_t e = entry & 0xFFFF;
+        const int64_t row0 = e * (UP ? 2 : 1) * N + (live ? ntile * (UP ? 32 : 64) : 0);
+        const uint32_t cols = !live ? 0u : UP ? up + 32u : (uint32_t)std::min<int>(64, N - ntile * 64);
+        rW = make_rsrc_small(wq + row0 * row_bytes, cols * row_bytes);
+        rS = make_rsrc_small(sq + row0 * nb, 2 * cols * (uint32_t)nb);
+        rZ = make_rsrc_small(zq ? zq + row0 * zb : wq, zq ? cols * (uint32_t)zb : 0u);
+        rA = UP ? make_rsrc_small(p.xs, (uint32_t)p.T * (uint32_t)K * 2)
+                : make_rsrc_small(p.hq + (int64_t)nbatch * R * K, live ? (uint32_t)R * (uint32_t)K * 2 : 0u);
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) {
+            const int r = 16 * rt + j;
+            arow[rt] = r >= rows ? kPastRows
+                                 : 16 * (uint32_t)g + 2 * (uint32_t)K * (uint32_t)(UP ? row_info[nbatch * R + r] : r);
+        }
+    };
+    auto next = [&](Step& st, Scales* sz) {
+        if (nstep == 0) enter();
+        // Lane offsets stay; the step's is uniform.  Blocks past K load zeros
+        // (whole steps of them where rows come in steps, VEC).
+        const int quad = 2 * (wv + W * (nstep >> 1)) + (nstep & 1);
+        const uint32_t at = 64 * (uint32_t)quad;
+        const bool in = VEC > 1 ? 4 * quad < nb : 4 * quad + g < nb;
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct)
+            st.w[ct] = __builtin_amdgcn_raw_buffer_load_b128(rW, in ? wo[ct] : kOutOfRange, at, 0);
+        if (sz) {                                    // the first of two steps
+            const uint32_t ss = 8 * (uint32_t)quad, zs = 2 * (uint32_t)quad;
+            auto here = [&](uint32_t off, int blk) { return 4 * quad + blk < nb ? off : kOutOfRange; };
+            if constexpr (VEC == 8) {
+                const u32x4 t = __builtin_amdgcn_raw_buffer_load_b128(rS, here(so, 0), ss, 0);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) sz->s[VEC > 1 ? i : 0] = t[i];
+                sz->z[0] = __builtin_amdgcn_raw_buffer_load_b32(rZ, here(zo, 0), zs, 0);
+            } else if constexpr (VEC == 4) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const u32x2 t = __builtin_amdgcn_raw_buffer_load_b64(rS, here(so + 8 * i, 4 * i), ss, 0);
+                    sz->s[2 * i] = t[0];
+                    sz->s[2 * i + 1] = t[1];
+                    sz->z[VEC == 8 ? 0 : i] = __builtin_amdgcn_raw_buffer_load_b16(rZ, here(zo + 2 * i, 4 * i), zs, 0);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    sz->s[VEC > 1 ? 0 : i] = __builtin_amdgcn_raw_buffer_load_b16(rS, here(so + 2 * i, i), ss, 0);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    sz->z[VEC > 1 ? 0 : i] = __builtin_amdgcn_raw_buffer_load_b8(rZ, here(zo + i, 2 * i), zs, 0);
+            }
+        }
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) {
+            const uint32_t row = arow[rt] | (VEC > 1 && !in ? kPastRows : 0u);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                st.a[rt][i] = __builtin_amdgcn_raw_buffer_load_b128(
+                    rA, (VEC > 1 || 4 * quad + i < nb ? row : kPastRows) + 64 * i, 4 * at, 0);
+        }
+        --left;
+        if (++nstep == steps) {
+            nstep = 0;
+            if (left > 0 && ++ntile == tiles) {
+                ntile = 0;
+                ++nbatch;
+            }
+        }
+    };
+    Step ring[2];                                    // two steps ahead; steps of a unit are even
+    Scales scales;
+    next(ring[0], &scales);
+    __builtin_amdgcn_sched_barrier(0);
+    next(ring[1], nullptr);
+    __builtin_amdgcn_sched_barrier(0);
+
+    float4_t acc[CT][RT] = {};
+    int todo = (u1 - u0) * steps, step = 0, b = u0 / tiles, tile = u0 - b * tiles;
+    uint8_t* const sl = reinterpret_cast<uint8_t*>(scale_lds[wv]);
+    auto run = [&](Step& st, bool odd) {
+        // The wave's scales and zero points of two steps, column by lane, to
+        // the lanes of the column.
+        if (!odd) {
+            __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
+            u32x4 s8;
+            uint32_t z8;
+            if constexpr (VEC > 1) {
+                s8 = u32x4{scales.s[0], scales.s[1], scales.s[2], scales.s[3]};
+                z8 = VEC == 8 ? scales.z[0] : scales.z[0] | (scales.z[VEC == 8 ? 0 : 1] << 16);
+            } else {
+                for (int i = 0; i < 4; ++i) s8[i] = scales.s[VEC > 1 ? 0 : 2 * i] | (scales.s[VEC > 1 ? 0 : 2 * i + 1] << 16);
+                z8 = scales.z[0] | (scales.z[VEC > 1 ? 0 : 1] << 8) | (scales.z[VEC > 1 ? 0 : 2] << 16) | (scales.z[VEC > 1 ? 0 : 3] << 24);
+            }
+            *reinterpret_cast<u32x4*>(sl + 16 * lane) = s8;
+            *reinterpret_cast<uint32_t*>(sl + 1024 + 4 * lane) = z8;
+            __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
+        }
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct) {
+            const u32x2 s4 = *reinterpret_cast<const u32x2*>(sl + 16 * (16 * ct + j) + 8 * odd);
+            const uint32_t z4 = *reinterpret_cast<const uint16_t*>(sl + 1024 + 4 * (16 * ct + j) + 2 * odd) | zdef;
+            uint32_t d[4] = {st.w[ct][0], st.w[ct][1], st.w[ct][2], st.w[ct][3]};
+            transpose_rows(d);                       // d[i]: dword g of block i
+            // Zero points of the blocks, one to a byte (block i in byte i / 2
+            // of the even or odd word), low and shifted by four: the fields of
+            // zero_point_pairs are those bytes under the constants' upper
+            // bytes, one permute each.
+            const uint32_t zlo[2] = {z4 & 0x0F0Fu, (z4 >> 4) & 0x0F0Fu}, zhi[2] = {(z4 << 4) & 0xF0F0u, z4 & 0xF0F0u};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                uint32_t pr[4];
+                const uint32_t pick = i < 2 ? 0x04000400u : 0x04010401u;
+                const ZeroPoint zp{__builtin_amdgcn_perm(0xE4E4E4E4u, zlo[i & 1], pick),
+                                   __builtin_amdgcn_perm(0xD4D4D4D4u, zhi[i & 1], pick)};
+                unpack_dword(d[i], zp, magic, pr);
+                const half8_t bv = __builtin_bit_cast(half8_t, u32x4{pr[0], pr[1], pr[2], pr[3]});
+                const uint32_t sw = s4[i >> 1];
+                const float sf = (float)__builtin_bit_cast(_Float16, (uint16_t)(i & 1 ? sw >> 16 : sw));
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt) {
+                    const float4_t zero = {0.f, 0.f, 0.f, 0.f};
+                    const float4_t v = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8_t, st.a[rt][i]), bv, zero, 0, 0, 0);
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) acc[ct][rt][r] = fmaf(v[r], sf, acc[ct][rt][r]);
+                }
+            }
+        }
+        const bool live = todo-- > 0;
+        next(st, odd ? nullptr : &scales);
+        if (++step < steps) return;
+        step = 0;
+        // The waves' sums, rows 16 rt + 4 g + r of column 16 ct + j.
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    part[wv][(ct * RT + rt) * 4 + r][lane] = acc[ct][rt][r];
+                    acc[ct][rt][r] = 0.f;
+                }
+        __syncthreads();
+        auto total = [&](int row, int c) {
+            const float* at = &part[0][((c >> 4) * RT + (row >> 4)) * 4 + (row & 3)][16 * ((row >> 2) & 3) + (c & 15)];
+            float v = 0.f;
+#pragma unroll
+            for (int w = 0; w < W; ++w) v += at[w * CT * RT * 4 * 64];
+            return v;
+        };
+        const int rows = batch[b] >> 16;
+        if constexpr (UP) {
+            for (int o = tid; o < 32 * rows && live; o += 64 * W) {
+                const int row = o >> 5, c = o & 31;
+                const float gate = total(row, c), u = total(row, 32 + c);
+                p.hf[((int64_t)b * R + row) * N + 32 * tile + c] = gate / (1.f + __expf(-gate)) * u;
+            }
+        } else {
+            for (int o = tid; o < 64 * rows && live; o += 64 * W) {
+                const int row = o >> 6, c = o & 63;
+                if (64 * tile + c < N)
+                    p.y[((int64_t)b * R + row) * N + 64 * tile + c] = total(row, c) * __int_as_float(row_info[b * R + row]);
+            }
+        }
+        __syncthreads();                             // part is written again by the next unit
+        if (todo > 0 && ++tile == tiles) {
+            tile = 0;
+            ++b;
+        }
+    };
+    while (todo > 0) {
+        run(ring[0], false);
+        run(ring[1], true);
+    }
+}
+
+// Launch 3: each row's h as fp16, its largest at 2^13 .. 2^14, in the unpack's
+// order; hs: the power of two taken out, times the row's weight.
+template <int RT>
+__global__ __launch_bounds__(1024) void mnb_moe_scale_rows_kernel(MoeParams p)
+{
+    __shared__ uint32_t tops[16];
+    const int row = blockIdx.x, tid = threadIdx.x;
+    if (row >= p.head[0] * 16 * RT || p.row_token[row] < 0) return;
+    const float4_t* const h = reinterpret_cast<const float4_t*>(p.hf + (int64_t)row * p.I);
+    const int pieces = p.I / 8;
+    uint32_t top = 0;
+    for (int i = tid; i < 2 * pieces; i += 1024)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const uint32_t m = __float_as_uint(h[i][k]) & 0x7FFFFFFFu;
+            top = m > top ? m : top;
+        }
+    top = wave_max(top);
+    if ((tid & 63) == 0) tops[tid >> 6] = top;
+    __syncthreads();
+    for (int w = 0; w < 16; ++w) top = tops[w] > top ? tops[w] : top;
+    int ex = (int)(top >> 23) - 127 - 13;
+    ex = top == 0 || top >= 0x7F800000u ? 0 : ex < -110 ? -110 : ex;
+    if (tid == 0) p.hs[row] = ldexpf(p.row_p[row], ex);
+    u32x4* const out = reinterpret_cast<u32x4*>(p.hq + (int64_t)row * p.I);
+    for (int i = tid; i < pieces; i += 1024) {
+        const float4_t lo = h[2 * i], hi = h[2 * i + 1];
+        u32x4 o;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) o[k] = f16_pair(ldexpf(lo[k], -ex), ldexpf(hi[k], -ex));
+        out[i] = o;
+    }
+}
+
+// Launch 5: each token's rows, in the order of its slots.
+__global__ __launch_bounds__(256) void mnb_moe_combine_kernel(MoeParams p)
+{
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= (int64_t)p.T * p.H) return;
+    const int t = (int)(i / p.H), c = (int)(i - (int64_t)t * p.H);
+    float v = 0.f;
+    for (int s = 0; s < p.top_k; ++s) {
+        const int row = p.pair_row[t * p.top_k + s];
+        if (row >= 0) v += p.y[(int64_t)row * p.H + c];
+    }
+    if (p.head[1 + t]) v = __uint_as_float(0x7FC00000u);
+    p.out[i] = narrow16(v, p.out_bf16);
+}
+
 // Whether a matrix's scales and zero points can be loaded for `blocks`
 // consecutive blocks at a time.
 bool vec_ok(int64_t K, const uint16_t* scales, const uint8_t* zp, int blocks)
@@ -779,6 +1102,43 @@ hipError_t queue_down(const MoeParams& p, hipStream_t s)
     return queue(fn, p, (unsigned)(p.H / (4 * NC)), 64 * W, lds, s);
 }
 
+template <int RT, bool UP>
+const void* wide_kernel(int64_t K, const uint16_t* scales, const uint8_t* zp)
+{
+    return vec_ok(K, scales, zp, 8)   ? reinterpret_cast<const void*>(mnb_moe_wide_kernel<RT, UP, 8>)
+           : vec_ok(K, scales, zp, 4) ? reinterpret_cast<const void*>(mnb_moe_wide_kernel<RT, UP, 4>)
+                                      : reinterpret_cast<const void*>(mnb_moe_wide_kernel<RT, UP, 1>);
+}
+
+template <int RT>
+hipError_t queue_wide(const MoeParams& p, int cus, int* launches, hipStream_t s)
+{
+    const int64_t pieces = (int64_t)p.T * p.H / 8, rows = (int64_t)p.batch_cap * 16 * RT;
+    const void* const prepare = reinterpret_cast<const void*>(mnb_moe_prepare_kernel<RT>);
+    const void* const up = wide_kernel<RT, true>(p.H, p.s1, p.z1);
+    const void* const scale = reinterpret_cast<const void*>(mnb_moe_scale_rows_kernel<RT>);
+    const void* const down = wide_kernel<RT, false>(p.I, p.s2, p.z2);
+    const void* const combine = reinterpret_cast<const void*>(mnb_moe_combine_kernel);
+    const size_t tables = (size_t)p.batch_cap * (16 * RT + 1) * 4;
+    struct Launch {
+        const void* fn;
+        int64_t grid;
+        int threads;
+        size_t lds;
+    } const all[] = {{prepare, std::min<int64_t>((pieces + 511) / 512, cus), 512,
+                      routing_bytes(p.E, p.T * p.top_k, p.batch_cap, 4 * RT)},
+                     {up, cus, 64 * kWideWaves, tables},
+                     {scale, rows, 1024, 0},
+                     {down, cus, 64 * kWideWaves, tables},
+                     {combine, ((int64_t)p.T * p.H + 255) / 256, 256, 0}};
+    for (const Launch& l : all) {
+        const hipError_t e = queue(l.fn, p, (unsigned)l.grid, l.threads, l.lds, s);
+        if (e != hipSuccess) return e;
+        ++*launches;
+    }
+    return hipSuccess;
+}
+
 }  // namespace
 
 int launch_moe(const MoeArgs& a, void* stream, int* launches)
@@ -806,6 +1166,11 @@ int launch_moe(const MoeArgs& a, void* stream, int* launches)
     p.row_p = reinterpret_cast<float*>(ws + lay.row_p);
     p.hs = reinterpret_cast<float*>(ws + lay.hs);
     p.h = reinterpret_cast<uint16_t*>(ws + lay.h);
+    p.pair_row = lay.wide ? reinterpret_cast<int32_t*>(ws + lay.pair_row) : nullptr;
+    p.xs = reinterpret_cast<uint16_t*>(ws + lay.xs);
+    p.hf = reinterpret_cast<float*>(ws + lay.hf);
+    p.hq = p.h;
+    p.y = reinterpret_cast<float*>(ws + lay.y);
     p.T = a.T;
     p.H = (int32_t)a.w.hidden;
     p.I = (int32_t)a.w.inter;
@@ -818,10 +1183,13 @@ int launch_moe(const MoeArgs& a, void* stream, int* launches)
     p.zero = 0;
     p.batch_cap = lay.batches;
     p.h_quad = 128 * ((p.I / 32 + 15) / 16 * 16);
-    // The first launch stages whole rows where they fit, else spans of K.
-    const int blocks = (p.H / 32 + 63) / 64 * 64, most = lay.rq == 1 ? 448 : 192;
-    p.stage_blocks = blocks < most ? blocks : most;
     const hipStream_t s = static_cast<hipStream_t>(stream);
+    if (lay.wide) return (int)(lay.wide == 1 ? queue_wide<1>(p, cus, launches, s) : queue_wide<2>(p, cus, launches, s));
+    // The first launch stages whole rows where they fit, else spans of K.
+    const int blocks = (p.H / 32 + 31) / 32 * 32;
+    const int most = (int)((kLdsBytes - up_static_lds(lay.rq) - routing_bytes(p.E, p.T * p.top_k, p.batch_cap, lay.rq)) /
+                           (4 * lay.rq * 16) - 1) / 4 / 32 * 32;
+    p.stage_blocks = blocks < most ? blocks : most;
     hipError_t he = lay.rq == 1 ? queue_up<1>(p, cus, s) : queue_up<2>(p, cus, s);
     if (he != hipSuccess) return (int)he;
     ++*launches;

@@ -404,15 +404,16 @@ typedef struct {
  * in its weights and its output row.
  * Numerics: products of fp16 activations with the exact q - z, summed in fp32
  * per block and scaled by the block's scale in fp32; softmax, silu and the
- * sum over the experts in fp32 (in the order of the experts' numbers), one
- * rounding to fp16 or bf16 (RNE).  The activations between the two products
- * are held in fp16 with a power-of-two scale per token, expert and block of
- * 32, so they neither overflow nor lose more than fp16's half step (2^-11)
- * of the block's largest.
+ * sum over the experts in fp32, one rounding to fp16 or bf16 (RNE).  The
+ * activations between the two products are held in fp16 with a power-of-two
+ * scale per token and expert (and block of 32, where the experts see few
+ * tokens), so they do not overflow and lose fp16's half step (2^-11, relative)
+ * at most.
  * A token's results depend on the batch only through the order in which
- * fp32 sums run.  Equal calls give equal bits.  out, expert_ids, expert_weights
- * and workspace must not overlap the inputs or each other.  Asynchronous;
- * allocates nothing; two launches.
+ * fp32 sums run.  Equal calls give equal bits on the same device.  out,
+ * expert_ids, expert_weights and workspace must not overlap the inputs or each
+ * other.  Asynchronous; allocates nothing; two launches, or five where an
+ * expert sees eight tokens or more on average (tokens * top_k >= 8 * experts).
  */
 int moe_nbits(const void* x, int x_dtype, int64_t tokens, const void* router_logits, int logits_dtype,
               int top_k, int renormalize, const mnb_moe_weights* weights, void* out, int out_dtype,
@@ -428,7 +429,7 @@ size_t mnb_moe_workspace(int64_t tokens, int64_t hidden, int64_t inter, int64_t 
  * prints one line per call to stderr, once its plan is fixed and before
  * its launches: the shape, the types, whether the plan was explicit or the
  * default, every plan field, and the number of launches (the 8-bit and expert
- * calls: the operator's name, shape, types and number of launches).
+ * calls, once queued: the operator's name, shape, types and launches).
  */
 
 /*

@@ -137,6 +137,21 @@ def test_product_of_integers(m, K, N):
         _check(out, A, a, W, b, bias if use_bias else None, out_dtype)
 
 
+@pytest.mark.parametrize("m,K,N", [(300, 48, 50000), (1025, 144, 9001), (700, 272, 9001), (200, 400, 9000),
+                                   (250, 1040, 7003), (1000, 400, 600), (60, 2064, 8003), (255, 144, 300)])
+def test_every_tile_and_the_rows_kernel_give_the_same_bits(m, K, N):
+    """Shapes that the choice by cost gives each of the seven tiles, with ragged
+    edges, and the first rows of each alone (the kernel for few rows)."""
+    G.require_gpu()
+    A, a, W, b, bias = _inputs(m, K, N, m + K + N, full=True)
+    dev = [t.cuda() for t in (A, a, W, b, bias)]
+    for out_dtype in (F16, BF16):
+        out = _product(*dev, out_dtype)
+        _check(out, A, a, W, b, bias, out_dtype)
+        few = _product(dev[0][:5].contiguous(), dev[1][:5].contiguous(), *dev[2:], out_dtype)
+        assert torch.equal(few.view(torch.int16), out[:5].view(torch.int16))
+
+
 @pytest.mark.parametrize("dtype", [F16, BF16])
 @pytest.mark.parametrize("m,K,N", SHAPES)
 def test_product_of_activations(m, K, N, dtype):

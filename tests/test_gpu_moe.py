@@ -153,7 +153,7 @@ CASES = [  # T, H, I, E, k
     (4, 2048, 768, 8, 2), (5, 544, 64, 512, 16), (7, 160, 1120, 6, 4), (8, 4096, 96, 4, 1), (9, 128, 2080, 5, 5),
     (12, 256, 4128, 3, 2), (16, 512, 256, 4, 4), (17, 288, 160, 2, 1), (31, 800, 96, 12, 6), (33, 128, 544, 5, 5),
     (48, 192, 128, 1, 1), (64, 256, 160, 8, 2), (64, 64, 32, 128, 8), (64, 480, 1024, 2, 2), (40, 32, 64, 3, 1),
-    (3, 65536, 32, 2, 1), (3, 32, 65536, 2, 2),
+    (3, 65536, 32, 2, 1), (3, 32, 65536, 2, 2), (20, 65536, 32, 2, 1), (34, 32, 65536, 2, 2), (26, 1408, 2048, 4, 2),
 ]
 
 
@@ -208,9 +208,9 @@ def test_every_token_at_one_expert():
 def test_intermediate_past_fp16():
     """silu(g) u far above fp16's largest number, and far below its smallest."""
     G.require_gpu()
-    for factor, out_dtype in ((6.0, BF16), (2.0 ** -13, BF16)):
+    for factor, out_dtype, T in ((6.0, BF16, 5), (2.0 ** -13, BF16, 5), (6.0, BF16, 30), (2.0 ** -13, BF16, 30)):
         w1, w2 = _layer(2, 256, 128, True, 1, lo=0.1 * factor, hi=1.0 * factor)
-        x, logits = _tokens(5, 256, 2, F16, F32, 2)
+        x, logits = _tokens(T, 256, 2, F16, F32, 2)
         x = x * (8 if factor > 1 else 2.0 ** -4)
         out, ids, p = _run(x.cuda(), logits.cuda(), _cuda(w1), _cuda(w2), 1, True, out_dtype)
         rids, rp = _route_ref(logits, 1, True)
@@ -224,7 +224,8 @@ def test_poison_behind_every_array():
     """NaN scales and 0xFF bytes in front of and behind every array and in the
     experts that no token selects: nothing of it may show."""
     G.require_gpu()
-    for T, H, I, E, k in ((3, 96, 160, 5, 2), (1, 1056, 416, 3, 1), (9, 352, 96, 4, 2)):
+    for T, H, I, E, k in ((3, 96, 160, 5, 2), (1, 1056, 416, 3, 1), (9, 352, 96, 4, 2), (20, 352, 96, 4, 2),
+                          (40, 1056, 416, 3, 1)):
         w1, w2 = _layer(E, H, I, True, 8)
         x, logits = _tokens(T, H, E, F16, F32, 9)
         logits[:, E - 1] = -INF
@@ -248,12 +249,12 @@ def test_poison_behind_every_array():
         _check(x, logits, w1, w2, k, True, F16, got)
 
 
-def test_streams_graph_and_workspace():
+@pytest.mark.parametrize("T,H,I,E,k", [(6, 512, 256, 16, 4), (24, 512, 256, 16, 4), (33, 512, 256, 4, 2)])
+def test_streams_graph_and_workspace(T, H, I, E, k):
     """Two streams at once, two graphs (each with its own workspace) replayed
     together with changing tokens between eager calls, a dirty workspace of
     exactly the stated size."""
     G.require_gpu()
-    T, H, I, E, k = 6, 512, 256, 16, 4
     w1, w2 = (_cuda(w) for w in _layer(E, H, I, True, 1))
     data = [tuple(t.cuda() for t in _tokens(T, H, E, BF16, F32, 30 + i)) for i in range(4)]
     want = [_run(x, l, w1, w2, k, True, F16) for x, l in data]
