@@ -154,6 +154,7 @@ CASES = [  # T, H, I, E, k
     (12, 256, 4128, 3, 2), (16, 512, 256, 4, 4), (17, 288, 160, 2, 1), (31, 800, 96, 12, 6), (33, 128, 544, 5, 5),
     (48, 192, 128, 1, 1), (64, 256, 160, 8, 2), (64, 64, 32, 128, 8), (64, 480, 1024, 2, 2), (40, 32, 64, 3, 1),
     (3, 65536, 32, 2, 1), (3, 32, 65536, 2, 2), (20, 65536, 32, 2, 1), (34, 32, 65536, 2, 2), (26, 1408, 2048, 4, 2),
+    (64, 32, 32, 512, 16),
 ]
 
 
@@ -192,6 +193,24 @@ def test_routing_ties_masks_and_bad_logits(T, E, k):
                 logits[5, E - 1] = torch.finfo(ldtype).min
             got = _run(x.cuda(), logits.cuda(), _cuda(w1), _cuda(w2), k, renorm, F16)
             _check(x, logits, w1, w2, k, renorm, F16, got)
+
+
+def test_zeros_of_both_signs_tie():
+    """-0 and +0 are equal logits: the lower expert goes first."""
+    G.require_gpu()
+    E, k, T = 70, 3, 4
+    w1, w2 = _layer(E, 64, 32, True, 3)
+    x, _ = _tokens(T, 64, E, F16, F32, 4)
+    for ldtype in (F32, F16, BF16):
+        logits = torch.full((T, E), -1.0)
+        logits[0, [5, 9, 68]] = torch.tensor([-0.0, 0.0, 0.0])
+        logits[1, [5, 9, 68]] = torch.tensor([0.0, -0.0, 0.0])
+        logits[2, [2, 66, 67, 69]] = torch.tensor([0.0, -0.0, 0.0, -0.0])
+        logits[3] = -0.0
+        logits = logits.to(ldtype)
+        got = _run(x.cuda(), logits.cuda(), _cuda(w1), _cuda(w2), k, True, F16)
+        assert got[1].tolist() == [[5, 9, 68], [5, 9, 68], [2, 66, 67], [0, 1, 2]]
+        _check(x, logits, w1, w2, k, True, F16, got)
 
 
 def test_every_token_at_one_expert():
