@@ -24,6 +24,7 @@ MNB_MAX_M = 8            # decode kernels; prefill up to MNB_MAX_ROWS
 MNB_MAX_ROWS = 1 << 20
 MNB_MAX_SPLIT_WORKSPACE = 32 << 20   # bytes of K-split partial sums a default plan may take
 MNB_MAX_K_INT8 = 131056
+MNB_MAX_N_INT8 = 2147483136
 MNB_MOE_MAX_TOKENS = 64
 MNB_MOE_MAX_EXPERTS = 512
 MNB_MOE_MAX_TOP_K = 16

@@ -144,7 +144,7 @@ int finish_launches(int e, int launches)
 int check_int8_shape(int a_dtype, int64_t m, int64_t K, int64_t N)
 {
     if (m < 0 || m > MNB_MAX_ROWS) return MNB_ERR_M_RANGE;
-    if (K < 0 || N < 0 || K % 16 || K > MNB_MAX_K_INT8 || N > INT32_MAX) return MNB_ERR_SHAPE;
+    if (K < 0 || N < 0 || K % 16 || K > MNB_MAX_K_INT8 || N > MNB_MAX_N_INT8) return MNB_ERR_SHAPE;
     if (a_dtype != MNB_F16 && a_dtype != MNB_BF16 && a_dtype != MNB_I8) return MNB_ERR_DTYPE;
     return MNB_OK;
 }

@@ -1,4 +1,4 @@
-// Device helpers shared by the gfx950 GEMV kernels.  Internal header: HIP
+// Device helpers shared by the gfx950 kernels.  Internal header: HIP
 // device code only.
 #pragma once
 
@@ -29,6 +29,17 @@ __device__ __forceinline__ float dot2(uint32_t a, uint32_t w, float c)
 {
     return __builtin_amdgcn_fdot2(__builtin_bit_cast(half2_t, a),
                                   __builtin_bit_cast(half2_t, w), c, false);
+}
+
+// fp16 or bf16 bits as fp32 (exact), and back (RNE).
+__device__ __forceinline__ float widen16(uint32_t bits, int bf16)
+{
+    return bf16 ? __uint_as_float(bits << 16) : (float)__builtin_bit_cast(_Float16, (uint16_t)bits);
+}
+__device__ __forceinline__ uint16_t narrow16(float v, int bf16)
+{
+    if (!bf16) return __builtin_bit_cast(uint16_t, (_Float16)v);
+    return __builtin_bit_cast(uint16_t, (__bf16)v);
 }
 
 // Two values -> one fp16 pair, round to nearest even (v_cvt_pk_f16_f32):

@@ -22,12 +22,6 @@ namespace {
 
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 
-// fp16 or bf16 bits as fp32 (exact).
-__device__ __forceinline__ float widen16(uint32_t bits, int bf16)
-{
-    return bf16 ? __uint_as_float(bits << 16) : (float)__builtin_bit_cast(_Float16, (uint16_t)bits);
-}
-
 // Quantising a row: L threads hold it in P pieces of eight elements each
 // (rows longer than 8 L P are walked in such chunks and read twice), the row's
 // largest magnitude is found on the bit patterns (for fp16 and bf16 alike the
@@ -164,13 +158,6 @@ void queue_quantize(const QuantizeParams& p, hipStream_t stream)
                        dim3(L < 256 ? 256 : L), 0, stream, p);
 }
 
-// fp32 -> fp16 or bf16 bits (RNE).
-__device__ __forceinline__ uint16_t narrow16(float v, int bf16)
-{
-    if (!bf16) return __builtin_bit_cast(uint16_t, (_Float16)v);
-    return __builtin_bit_cast(uint16_t, (__bf16)v);
-}
-
 struct Int8Params {
     const int8_t* A;        // [M][K]
     const uint16_t* A16;    // the rows as fp16 or bf16, quantised by the kernel
@@ -184,10 +171,11 @@ struct Int8Params {
     int32_t a_bf16, out_bf16;
 };
 
-// The result of one output from its exact sum.
+// The result of one output from its exact sum.  (The FMA is spelled out: the
+// kernels must give the same bits.)
 __device__ __forceinline__ uint16_t finish(int sum, float a_scale, float b_scale, float bias, int out_bf16)
 {
-    return narrow16((float)sum * b_scale * a_scale + bias, out_bf16);
+    return narrow16(fmaf((float)sum * b_scale, a_scale, bias), out_bf16);
 }
 
 // Few rows (m <= 16, K <= 16384): one pass over the weights, which HBM bounds.
@@ -358,9 +346,9 @@ struct __attribute__((packed, aligned(2))) Loose16 {
 
 // A workgroup tile of BM rows by BN columns: WM x WN waves of (BM / WM) x (BN /
 // WN) each, and KS such sets that split each stage's K.  A stage is KB (64 or
-// 128) bytes of every row and column for each set, NS of them in LDS.  Rows lie KB bytes apart; 16-byte piece c of row r in
-// slot c ^ swizzle(r), so that the eight rows that one LDS access of a fragment
-// covers lie in distinct banks.
+// 128) bytes of every row and column for each set, NS of them in LDS.  Rows lie
+// KB bytes apart, 16-byte piece c of row r in slot c ^ swizzle(r), so that the
+// eight rows that one LDS access of a fragment covers lie in distinct banks.
 template <int BM, int BN, int WM, int WN, int KS, int NS, int KB>
 __global__ __launch_bounds__(64 * WM * WN * KS) void mnb_int8_tile_kernel(Int8Params p)
 {
@@ -599,7 +587,8 @@ int cheapest_tile(int64_t m, int64_t K, int64_t N, int cus)
         const TileCost& c = kTiles[t];
         const int64_t tiles = ((m + c.bm - 1) / c.bm) * ((N + c.bn - 1) / c.bn), rounds = (tiles + cus - 1) / cus;
         const double us = (double)rounds * (c.fixed + c.per_k * (double)K / 1024);
-        if (t == 0 || us < least) {
+        // (A grid holds 2^32 threads; the largest tile fits for every N there is.)
+        if (t == 0 || (tiles < (1 << 23) && us < least)) {
             best = t;
             least = us;
         }

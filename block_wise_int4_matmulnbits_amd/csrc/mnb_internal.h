@@ -128,9 +128,11 @@ constexpr int64_t kInt8RowsK = 16 * 8 * 128;
 constexpr size_t kInt8RowsLds = 160 * 1024 - 128;
 // Whether it also quantises fp16 or bf16 rows itself, in one launch: every
 // workgroup then reads all of them.
+constexpr int64_t kInt8FusedElements = 32768;
+static_assert(kInt8FusedElements + 16 * 16 + 16 * 2048 <= kInt8RowsLds, "fused rows always go to the kernel for few rows");
 inline bool int8_fused(int a_dtype, int64_t m, int64_t K)
 {
-    return a_dtype != MNB_I8 && m <= 16 && K <= kInt8RowsK && m * K <= 32768;
+    return a_dtype != MNB_I8 && m <= 16 && K <= kInt8RowsK && m * K <= kInt8FusedElements;
 }
 
 // Workspace of an 8-bit product: the quantised rows and their scales where the

@@ -82,17 +82,6 @@ struct MoeParams {
     uint32_t zero;          // always 0 (see vgpr_constant)
 };
 
-__device__ __forceinline__ float widen16(uint32_t bits, int bf16)
-{
-    return bf16 ? __uint_as_float(bits << 16) : (float)__builtin_bit_cast(_Float16, (uint16_t)bits);
-}
-
-__device__ __forceinline__ uint16_t narrow16(float v, int bf16)
-{
-    if (!bf16) return __builtin_bit_cast(uint16_t, (_Float16)v);
-    return __builtin_bit_cast(uint16_t, (__bf16)v);
-}
-
 // Maximum and sum over a wave, the same in every lane (DPP: four row shifts,
 // two row broadcasts; lane 63 ends with the result).
 template <int CTRL, int ROWS>
@@ -254,8 +243,8 @@ __device__ __forceinline__ int place_batches(const MoeParams& p, int rows, const
 }
 
 // All tokens, the batches in the order of the experts' numbers, and each
-// batch's rows in the order of the tokens; the count of batches.  Workgroup 0 writes the tables for
-// the second launch and the caller's ids and weights.  `meanwhile` is run by
+// batch's rows in the order of the tokens; the count of batches.  Workgroup 0
+// writes the tables for the next launches and the caller's ids and weights.  `meanwhile` is run by
 // the waves that have no token to route, before the routing is complete.
 template <int RQ, typename F>
 __device__ __forceinline__ int route(const MoeParams& p, const Routing& r, F meanwhile)
@@ -388,14 +377,14 @@ __device__ __forceinline__ void spread_scales(const StepScales<NC, VEC>& v, uint
 //   acc[n][rq][r] += s * sum_k a[4 rq + r][k] (q[k] - z)
 // w: the packed block of column 4n + i; s, z: its scale (fp16 bits) and the
 // byte of its zero point; act: the block's activations of row 4 rq + i (pairs in the
-// unpack's order).  ROWSCALE: acc[r] += s * f[rq][r] * ... with a scale per row.
+// unpack's order).  ROWSCALE: the rows' powers of two f[rq][r] are applied with s.
 template <int NC, int RQ, bool ROWSCALE>
 __device__ __forceinline__ void block_products(const u32x4 (&w)[NC], const uint32_t (&s)[NC], const uint32_t (&z)[NC],
                                                int zshift, uint32_t zdef, uint32_t magic, const u32x4 (&act)[RQ][4],
                                                const float4_t (&f)[RQ], float4_t (&acc)[NC][RQ])
 {
     // Column quads taken together, so that four chains of MFMAs run at once.
-    constexpr int NI = RQ >= 4 ? 1 : 4 / RQ < NC ? 4 / RQ : NC;
+    constexpr int NI = 4 / RQ < NC ? 4 / RQ : NC;
 #pragma unroll
     for (int n0 = 0; n0 < NC; n0 += NI) {
         float4_t d4[NI][RQ];
@@ -1148,7 +1137,7 @@ int launch_moe(const MoeArgs& a, void* stream, int* launches)
     if (e != 0) return e;
     const MoeLayout lay = moe_layout(a.T, a.w.hidden, a.w.inter, a.w.experts, a.top_k);
     uint8_t* ws = static_cast<uint8_t*>(a.ws);
-    MoeParams p;
+    MoeParams p{};
     p.x = static_cast<const uint16_t*>(a.x);
     p.logits = a.logits;
     p.w1 = a.w.gate_up;

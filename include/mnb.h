@@ -309,6 +309,8 @@ int quantize_rows_int8(const void* A, int a_dtype, int64_t m, int64_t K, int8_t*
  * 8-bit integers stays below 2^31 (K * 128 * 128 < 2^31; K is a multiple of
  * 16). */
 #define MNB_MAX_K_INT8 131056
+/* Largest N of the 8-bit product (2^31 - 512: its grids hold 2^32 threads). */
+#define MNB_MAX_N_INT8 2147483136
 
 /*
  * matmul_int8 -- product of 8-bit rows and 8-bit weights:
@@ -322,7 +324,7 @@ int quantize_rows_int8(const void* A, int a_dtype, int64_t m, int64_t K, int8_t*
  *   a_scales     device, [m] fp32, 4-byte aligned, with MNB_I8; NULL otherwise
  *                (the call derives the scales).
  *   m, K, N      0 <= m <= MNB_MAX_ROWS; K a multiple of 16, 0 <= K <=
- *                MNB_MAX_K_INT8; 0 <= N <= INT32_MAX.
+ *                MNB_MAX_K_INT8; 0 <= N <= MNB_MAX_N_INT8.
  *   B            device, [N][K] int8, row-major; 16-byte aligned.  All 256
  *                values are taken, here and in A.
  *   b_scales     device, [N] fp32; 4-byte aligned.
@@ -337,8 +339,8 @@ int quantize_rows_int8(const void* A, int a_dtype, int64_t m, int64_t K, int8_t*
  *   stream       hipStream_t, or NULL for the default stream.
  *
  * Numerics: the integer sum is exact (int32), converted to fp32 (one
- * rounding), multiplied by b_scales[n] and then a_scales[r] in fp32, the bias
- * added in fp32, and the result rounded once to fp16 or bf16 (RNE).  The bits
+ * rounding), multiplied by b_scales[n] in fp32, then by a_scales[r] with the
+ * bias added in one FMA, and the result rounded once to fp16 or bf16 (RNE).  The bits
  * do not depend on m, N, the plan or the device.  out and workspace must not
  * overlap the inputs or each other.  Asynchronous; allocates nothing; one or
  * two launches.
@@ -408,7 +410,9 @@ typedef struct {
  * activations between the two products are held in fp16 with a power-of-two
  * scale per token and expert (and block of 32, where the experts see few
  * tokens), so they do not overflow and lose fp16's half step (2^-11, relative)
- * at most.
+ * at most; those below 2^-27 of the largest one under the same scale lose up
+ * to 2^-38 of that one.  A token's x that is not finite in fp16 spoils that
+ * token's row alone.
  * A token's results depend on the batch only through the order in which
  * fp32 sums run.  Equal calls give equal bits on the same device.  out,
  * expert_ids, expert_weights and workspace must not overlap the inputs or each

@@ -213,6 +213,26 @@ def test_zeros_of_both_signs_tie():
         _check(x, logits, w1, w2, k, True, F16, got)
 
 
+@pytest.mark.parametrize("T,E,k", [(3, 6, 2), (7, 6, 2), (30, 6, 2), (64, 6, 2)])
+def test_tokens_that_are_not_finite_stay_alone(T, E, k):
+    """Padding tokens (no expert) of NaN give zeros, a routed token of infinities
+    a row that is not finite, and every other token the bits it has without
+    them."""
+    G.require_gpu()
+    w1, w2 = (_cuda(w) for w in _layer(E, 96, 160, True, T))
+    for dtype in (F16, BF16):
+        x, logits = _tokens(T, 96, E, dtype, F32, T + 1)
+        pads, hot = [0, T // 2], T - 1
+        logits[pads] = -INF
+        plain = _run(x.cuda(), logits.cuda(), w1, w2, k, True, BF16)
+        x[pads], x[hot] = float("nan"), INF
+        got = _run(x.cuda(), logits.cuda(), w1, w2, k, True, BF16)
+        others = [t for t in range(T) if t != hot]
+        assert torch.equal(got[0][others], plain[0][others]) and bool((got[0][pads] == 0).all())
+        assert not bool(got[0][hot].isfinite().any())
+        assert torch.equal(got[1], plain[1]) and torch.equal(got[2], plain[2])
+
+
 def test_every_token_at_one_expert():
     """All tokens select the same experts: 64 rows at one expert."""
     G.require_gpu()

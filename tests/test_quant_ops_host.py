@@ -42,7 +42,7 @@ F16 = dict(a=mnb.MNB_F16, sa=None, ws=6 * P, size=1 << 24)
 
 @pytest.mark.parametrize("args,status", [
     (dict(m=-1), 6), (dict(m=(1 << 20) + 1), 6), (dict(K=-16), 2), (dict(K=24), 2), (dict(K=131072), 2),
-    (dict(N=-1), 2), (dict(N=1 << 31), 2), (dict(a=mnb.MNB_F32), 4), (dict(a=4), 4), (dict(o=mnb.MNB_F32), 4),
+    (dict(N=-1), 2), (dict(N=1 << 31), 2), (dict(N=mnb.MNB_MAX_N_INT8 + 1), 2), (dict(a=mnb.MNB_F32), 4), (dict(a=4), 4), (dict(o=mnb.MNB_F32), 4),
     (dict(o=mnb.MNB_I8), 4), (dict(A=None), 1), (dict(sa=None), 1), (dict(B=None), 1), (dict(sb=None), 1),
     (dict(out=None), 1), (dict(A=P + 1), 5), (dict(B=3 * P + 8), 5), (dict(sa=2 * P + 2), 5),
     (dict(sb=4 * P + 1), 5), (dict(bias=7 * P + 2), 5), (dict(out=5 * P + 1), 5),
