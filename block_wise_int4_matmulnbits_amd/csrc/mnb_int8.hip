@@ -610,20 +610,20 @@ int launch_quantize_rows(const void* A, int a_bf16, int64_t m, int64_t K, int8_t
 {
     const QuantizeParams p{static_cast<const uint16_t*>(A), q, scales, m, K, a_bf16};
     const hipStream_t s = static_cast<hipStream_t>(stream);
-    // Threads per row: where the rows fill the device, as few as hold the row
-    // in eight pieces each; few rows are spread over one workgroup each.
+    // Threads per row and pieces per thread: rows that fill the device take no
+    // more waves than hold them, few rows are spread wide (us, 64 x 1, 256 x 1, 256
+    // x 8, 1024 x 1, 1024 x 4): 4096 rows of 512 4.2, 6.2, 9.4, 17.1, 20.9; of 2048
+    // 10.0, 8.8, 11.6, 18.3, 21.9; of 8192 34.3, 25.8, 20.1, 26.7, 30.4; 2048 rows of
+    // 16384 50.3, 27.8, 22.1, 26.2, 23.8, of 32768 101, 59, 61, 50, 38.5; 16 rows of
+    // 2048 5.6, 3.3, 3.5, 3.3, 3.6; of 8192 15.1, 5.9, 4.8, 3.8, 4.2; of 16384
+    // 28.3, 9.2, 6.5, 4.8, 4.7.  At 512 rows of 4096 (10.5, 5.0, 5.0, 4.8, 5.6) and 1024
+    // (11.2, 6.3, 6.5, 7.5, 8.5) the order turns.
     const bool many = m >= 1024;
-    if (K <= (many ? 4096 : 512)) {
-        if (K <= 512) queue_quantize<64, 1>(p, s);
-        else queue_quantize<64, 8>(p, s);
-    } else if (K <= (many ? 16384 : 2048)) {
-        if (K <= 2048) queue_quantize<256, 1>(p, s);
-        else queue_quantize<256, 8>(p, s);
-    } else if (K <= 8192) {
-        queue_quantize<1024, 1>(p, s);
-    } else {
-        queue_quantize<1024, 4>(p, s);
-    }
+    if (K <= 512) queue_quantize<64, 1>(p, s);
+    else if (K <= (many ? 4096 : 2048)) queue_quantize<256, 1>(p, s);
+    else if (many && K <= 16384) queue_quantize<256, 8>(p, s);
+    else if (K <= 8192) queue_quantize<1024, 1>(p, s);
+    else queue_quantize<1024, 4>(p, s);
     return (int)hipGetLastError();
 }
 
@@ -659,10 +659,16 @@ int launch_int8(const Int8Args& a, void* stream, int* launches)
     const int64_t units = std::max<int64_t>((a.K + 127) / 128, 1);
     hipError_t he;
     if (a.m <= 16 && a.K <= kInt8RowsK && rows_lds(a.m, a.K, 16) <= kInt8RowsLds) {
-        // Eight waves, two workgroups a CU, where eight units a wave cover K,
-        // both fit LDS and there is work for them; sixteen otherwise.
+        // Sixteen waves, or eight in two workgroups a CU where both fit LDS:
+        // with K <= 2048, where sixteen would have one unit each under way
+        // (2048 x 28672, one row: 15.2 us against 17.2), and up to 4096 with so
+        // many columns that an odd tile does not count (4096 x 151936: 111
+        // against 119; 4096 x 28672: 25.8 against 24.6; 8192 x 28672: 47.4
+        // against 42.7).
         const int64_t tiles = (a.N + 15) / 16;
-        int64_t w = units <= 64 && tiles > cus && 2 * rows_lds(a.m, a.K, 8) <= kInt8RowsLds ? 8 : 16;
+        const bool eight = 2 * rows_lds(a.m, a.K, 8) <= kInt8RowsLds &&
+                           ((units <= 16 && tiles > cus) || (units <= 32 && tiles > 16 * (int64_t)cus));
+        int64_t w = eight ? 8 : 16;
         if (w > units) w = units;
         const int nu = (int)((units + w - 1) / w);
         w = (units + nu - 1) / nu;

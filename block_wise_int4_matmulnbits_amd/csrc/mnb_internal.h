@@ -127,7 +127,10 @@ int launch_int8(const Int8Args& args, void* stream, int* launches) MNB_WEAK;
 constexpr int64_t kInt8RowsK = 16 * 8 * 128;
 constexpr size_t kInt8RowsLds = 160 * 1024 - 128;
 // Whether it also quantises fp16 or bf16 rows itself, in one launch: every
-// workgroup then reads all of them.
+// workgroup then reads all of them.  One launch against two (us of kernels; a
+// launch more costs 2 or 3 us besides): 4096 x 4096 with 1 row 8.6 against 2.5 +
+// 6.4, with 8 rows 11.1 against 3.4 + 7.2, with 16 12.4 against 3.4 + 7.7; 14336
+// x 4096 with 1 row 21.5 against 4.1 + 15.6, with 4 rows 23.9 against 4.1 + 16.3.
 constexpr int64_t kInt8FusedElements = 32768;
 static_assert(kInt8FusedElements + 16 * 16 + 16 * 2048 <= kInt8RowsLds, "fused rows always go to the kernel for few rows");
 inline bool int8_fused(int a_dtype, int64_t m, int64_t K)

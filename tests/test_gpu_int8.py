@@ -63,7 +63,8 @@ def _check_quantize(x):
 
 @pytest.mark.parametrize("dtype", [F16, BF16])
 @pytest.mark.parametrize("m,K", [(1, 16), (1, 4096), (3, 48), (7, 1040), (2, 16400), (5, 14336), (300, 272),
-                                 (2, 70000), (1, 131056), (4100, 64), (33, 8208), (1, 0)])
+                                 (2, 70000), (1, 131056), (4100, 64), (33, 8208), (1, 0),
+                                 (1100, 2064), (1031, 4112), (1025, 8400), (1024, 16400)])
 def test_quantize(m, K, dtype):
     G.require_gpu()
     _check_quantize(_rows(m, K, dtype, 7 * m + K))
