@@ -428,11 +428,12 @@ MoeLayout moe_layout(int64_t T, int64_t H, int64_t I, int64_t E, int top_k)
     const int64_t pairs = T * top_k;
     MoeLayout l{};
     // The kernels and the rows of a batch, by the tokens an expert sees on
-    // average (us, narrow with 4 or 8 rows against wide with 16 or 32): 6
-    // tokens (24 tokens, 2 of 8 experts of 4096, 14336) 219 against 248 and
-    // 286; 8 (32 tokens) 312 against 252 and 293, (64 tokens, 8 of 64 of 2048,
-    // 768) 97 against 101 and 125; 16 (64 tokens, 2 of 8) 451 against 400 and
-    // 337, (64 tokens, 8 of 32 of 2048, 768) 87 against 86 and 84.
+    // average (us, narrow with 8 rows against wide with 16 and with 32): 6 tokens
+    // (24 tokens, 2 of 8 experts of 4096, 14336) 217 against 238 and 265; 8 (32
+    // tokens) 314 against 245 and 275, (64 tokens, 8 of 64 of 2048, 768) 97 against 97
+    // and 113; 16 (64 tokens, 2 of 8) 535 against 390 and 328, (64 tokens, 8 of 32
+    // of 2048, 768) 87 against 84 and 77; 32 (64 tokens, 2 of 4 of 4096, 4096) 133
+    // against 98 and 89.
     l.wide = pairs > 12 * E ? 2 : pairs >= 8 * E ? 1 : 0;
     l.rq = l.wide ? 4 * l.wide : pairs > 4 * E ? 2 : 1;
     // Every expert has at most one batch that is not full.

@@ -760,7 +760,6 @@ __global__ __launch_bounds__(64 * W) void mnb_moe_down_kernel(MoeParams p)
 // scale per block, as in the narrow kernels, every product would need the
 // scales of its four rows.
 constexpr int kWideWaves = 8;
-constexpr uint32_t kPastRows = 0xF0000000u;   // out of range, also with a small offset added
 
 // Launch 1: the tables (workgroup 0) and x as fp16 in the unpack's order.
 template <int RT>
@@ -794,7 +793,7 @@ __global__ __launch_bounds__(64 * kWideWaves) void mnb_moe_wide_kernel(MoeParams
     const uint8_t* const wq = UP ? p.w1 : p.w2;
     const uint16_t* const sq = UP ? p.s1 : p.s2;
     const uint8_t* const zq = UP ? p.z1 : p.z2;
-    const uint32_t row_bytes = (uint32_t)K / 2, zdef = zq ? 0u : 0x8888u;   // zero points of four blocks
+    const uint32_t row_bytes = (uint32_t)K / 2, zdef = zq ? 0u : 0x88u;   // zero points of two blocks
     const uint32_t magic = vgpr_constant(0x64006400u, p.zero);
     const int64_t units = (int64_t)p.head[0] * tiles;
     for (int i = tid; i < p.batch_cap; i += 64 * W) batch[i] = p.batch_e[i];
@@ -810,9 +809,6 @@ __global__ __launch_bounds__(64 * kWideWaves) void mnb_moe_wide_kernel(MoeParams
     const uint32_t up = (uint32_t)p.I;
     const uint32_t scol = UP ? (uint32_t)(lane & 31) + (lane >> 5) * up : (uint32_t)lane;
 
-    struct Step {
-        u32x4 w[CT], a[RT][4];
-    };
     // Scales and zero points of this lane's column for two steps, eight
     // blocks, in as few loads as the rows' length and alignment allow: VEC
     // blocks at a time (every load touches 64 lines, one per column).
@@ -825,36 +821,27 @@ __global__ __launch_bounds__(64 * kWideWaves) void mnb_moe_wide_kernel(MoeParams
     for (int ct = 0; ct < CT; ++ct)
         wo[ct] = (UP ? (uint32_t)(16 * (ct & 1) + j) + (ct >> 1) * up : (uint32_t)(16 * ct + j)) * row_bytes + 16 * (uint32_t)g;
     const uint32_t so = 2 * scol * (uint32_t)nb, zo = scol * (uint32_t)zb;
-    uint32_t arow[RT];                               // and its rows of activations, or kPastRows
     __amdgpu_buffer_rsrc_t rW, rS, rZ, rA;
     auto enter = [&] {                               // the unit (nbatch, ntile)
         const bool live = left > 0;
-        const int entry = live ? __builtin_amdgcn_readfirstlane(batch[nbatch]) : 0, rows = entry >> 16;
-        const int64_t e = entry & 0xFFFF;
+        const int64_t e = (live ? __builtin_amdgcn_readfirstlane(batch[nbatch]) : 0) & 0xFFFF;
         const int64_t row0 = e * (UP ? 2 : 1) * N + (live ? ntile * (UP ? 32 : 64) : 0);
         const uint32_t cols = !live ? 0u : UP ? up + 32u : (uint32_t)std::min<int>(64, N - ntile * 64);
         rW = make_rsrc_small(wq + row0 * row_bytes, cols * row_bytes);
         rS = make_rsrc_small(sq + row0 * nb, 2 * cols * (uint32_t)nb);
         rZ = make_rsrc_small(zq ? zq + row0 * zb : wq, zq ? cols * (uint32_t)zb : 0u);
-        rA = UP ? make_rsrc_small(p.xs, (uint32_t)p.T * (uint32_t)K * 2)
-                : make_rsrc_small(p.hq + (int64_t)nbatch * R * K, live ? (uint32_t)R * (uint32_t)K * 2 : 0u);
-#pragma unroll
-        for (int rt = 0; rt < RT; ++rt) {
-            const int r = 16 * rt + j;
-            arow[rt] = r >= rows ? kPastRows
-                                 : 16 * (uint32_t)g + 2 * (uint32_t)K * (uint32_t)(UP ? row_info[nbatch * R + r] : r);
-        }
     };
-    auto next = [&](Step& st, Scales* sz) {
+    auto quad_of = [&](int step) { return 2 * (wv + W * (step >> 1)) + (step & 1); };
+    auto next = [&](u32x4 (&w)[CT], Scales* sz) {
         if (nstep == 0) enter();
         // Lane offsets stay; the step's is uniform.  Blocks past K load zeros
         // (whole steps of them where rows come in steps, VEC).
-        const int quad = 2 * (wv + W * (nstep >> 1)) + (nstep & 1);
+        const int quad = quad_of(nstep);
         const uint32_t at = 64 * (uint32_t)quad;
         const bool in = VEC > 1 ? 4 * quad < nb : 4 * quad + g < nb;
 #pragma unroll
         for (int ct = 0; ct < CT; ++ct)
-            st.w[ct] = __builtin_amdgcn_raw_buffer_load_b128(rW, in ? wo[ct] : kOutOfRange, at, 0);
+            w[ct] = __builtin_amdgcn_raw_buffer_load_b128(rW, in ? wo[ct] : kOutOfRange, at, 0);
         if (sz) {                                    // the first of two steps
             const uint32_t ss = 8 * (uint32_t)quad, zs = 2 * (uint32_t)quad;
             auto here = [&](uint32_t off, int blk) { return 4 * quad + blk < nb ? off : kOutOfRange; };
@@ -880,14 +867,6 @@ __global__ __launch_bounds__(64 * kWideWaves) void mnb_moe_wide_kernel(MoeParams
                     sz->z[VEC > 1 ? 0 : i] = __builtin_amdgcn_raw_buffer_load_b8(rZ, here(zo + i, 2 * i), zs, 0);
             }
         }
-#pragma unroll
-        for (int rt = 0; rt < RT; ++rt) {
-            const uint32_t row = arow[rt] | (VEC > 1 && !in ? kPastRows : 0u);
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                st.a[rt][i] = __builtin_amdgcn_raw_buffer_load_b128(
-                    rA, (VEC > 1 || 4 * quad + i < nb ? row : kPastRows) + 64 * i, 4 * at, 0);
-        }
         --left;
         if (++nstep == steps) {
             nstep = 0;
@@ -897,17 +876,47 @@ __global__ __launch_bounds__(64 * kWideWaves) void mnb_moe_wide_kernel(MoeParams
             }
         }
     };
-    Step ring[2];                                    // two steps ahead; steps of a unit are even
+    // Activations, one step ahead: blocks 2 ip, 2 ip + 1 of this lane's rows take
+    // the place of the ones just used.  (They come from L2; two steps ahead the
+    // kernel for 32 rows spilled, and the spills' reloads waited for the weights:
+    // 64 tokens, 2 of 8 of 4096, 14336: 208 -> 189 us for launch 2.)
+    uint32_t arow[RT];                               // this lane's rows, or kOutOfRange
+    auto rows_of = [&](int b, bool live) {           // of batch b
+        const int rows = live ? __builtin_amdgcn_readfirstlane(batch[b]) >> 16 : 0;
+        rA = UP ? make_rsrc_small(p.xs, (uint32_t)p.T * (uint32_t)K * 2)
+                : make_rsrc_small(p.hq + (int64_t)(live ? b : 0) * R * K, live ? (uint32_t)R * (uint32_t)K * 2 : 0u);
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) {
+            const int r = 16 * rt + j;
+            arow[rt] = r >= rows ? kOutOfRange
+                                 : 16 * (uint32_t)g + 2 * (uint32_t)K * (uint32_t)(UP ? row_info[b * R + r] : r);
+        }
+    };
+    u32x4 act[RT][4];
+    auto next_rows = [&](int step, int ip) {
+        const int quad = quad_of(step);
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+            for (int i = 2 * ip; i < 2 * ip + 2; ++i)
+                act[rt][i] = __builtin_amdgcn_raw_buffer_load_b128(
+                    rA, 4 * quad + (VEC > 1 ? 0 : i) < nb ? arow[rt] : kOutOfRange, 256 * (uint32_t)quad + 64 * i, 0);
+    };
+
+    float4_t acc[CT][RT] = {};
+    int todo = (u1 - u0) * steps, step = 0, b = u0 / tiles, tile = u0 - b * tiles;
+    u32x4 ring[2][CT];                               // weights, two steps ahead; steps of a unit are even
     Scales scales;
     next(ring[0], &scales);
+    rows_of(b, todo > 0);
+    next_rows(0, 0);
+    next_rows(0, 1);
     __builtin_amdgcn_sched_barrier(0);
     next(ring[1], nullptr);
     __builtin_amdgcn_sched_barrier(0);
 
-    float4_t acc[CT][RT] = {};
-    int todo = (u1 - u0) * steps, step = 0, b = u0 / tiles, tile = u0 - b * tiles;
     uint8_t* const sl = reinterpret_cast<uint8_t*>(scale_lds[wv]);
-    auto run = [&](Step& st, bool odd) {
+    auto run = [&](u32x4 (&w)[CT], bool odd) {
         // The wave's scales and zero points of two steps, column by lane, to
         // the lanes of the column.
         if (!odd) {
@@ -925,38 +934,54 @@ __global__ __launch_bounds__(64 * kWideWaves) void mnb_moe_wide_kernel(MoeParams
             *reinterpret_cast<uint32_t*>(sl + 1024 + 4 * lane) = z8;
             __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
         }
+        uint32_t d[CT][4];                           // d[ct][i]: dword g of block i
 #pragma unroll
         for (int ct = 0; ct < CT; ++ct) {
-            const u32x2 s4 = *reinterpret_cast<const u32x2*>(sl + 16 * (16 * ct + j) + 8 * odd);
-            const uint32_t z4 = *reinterpret_cast<const uint16_t*>(sl + 1024 + 4 * (16 * ct + j) + 2 * odd) | zdef;
-            uint32_t d[4] = {st.w[ct][0], st.w[ct][1], st.w[ct][2], st.w[ct][3]};
-            transpose_rows(d);                       // d[i]: dword g of block i
-            // Zero points of the blocks, one to a byte (block i in byte i / 2
-            // of the even or odd word), low and shifted by four: the fields of
-            // zero_point_pairs are those bytes under the constants' upper
-            // bytes, one permute each.
-            const uint32_t zlo[2] = {z4 & 0x0F0Fu, (z4 >> 4) & 0x0F0Fu}, zhi[2] = {(z4 << 4) & 0xF0F0u, z4 & 0xF0F0u};
+            // (Kept whole until here: taken apart across the loop's end, the
+            // loaded words would be copied there, and the copies would wait for
+            // every load under way.)
+            u32x4 v = w[ct];
+            asm("" : "+v"(v));
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                uint32_t pr[4];
-                const uint32_t pick = i < 2 ? 0x04000400u : 0x04010401u;
-                const ZeroPoint zp{__builtin_amdgcn_perm(0xE4E4E4E4u, zlo[i & 1], pick),
-                                   __builtin_amdgcn_perm(0xD4D4D4D4u, zhi[i & 1], pick)};
-                unpack_dword(d[i], zp, magic, pr);
-                const half8_t bv = __builtin_bit_cast(half8_t, u32x4{pr[0], pr[1], pr[2], pr[3]});
-                const uint32_t sw = s4[i >> 1];
-                const float sf = (float)__builtin_bit_cast(_Float16, (uint16_t)(i & 1 ? sw >> 16 : sw));
+            for (int i = 0; i < 4; ++i) d[ct][i] = v[i];
+            transpose_rows(d[ct]);
+        }
+        const bool last = step + 1 == steps;
 #pragma unroll
-                for (int rt = 0; rt < RT; ++rt) {
-                    const float4_t zero = {0.f, 0.f, 0.f, 0.f};
-                    const float4_t v = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8_t, st.a[rt][i]), bv, zero, 0, 0, 0);
+        for (int ip = 0; ip < 2; ++ip) {
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) acc[ct][rt][r] = fmaf(v[r], sf, acc[ct][rt][r]);
+            for (int ct = 0; ct < CT; ++ct) {
+                const uint32_t s2 = *reinterpret_cast<const uint32_t*>(sl + 16 * (16 * ct + j) + 8 * odd + 4 * ip);
+                const uint32_t z2 = *(sl + 1024 + 4 * (16 * ct + j) + 2 * odd + ip) | zdef;
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    // The fields of zero_point_pairs: the zero point, plain and
+                    // shifted by four, under the constants' upper bytes.
+                    uint32_t pr[4];
+                    const uint32_t lo = k ? z2 >> 4 : z2 & 0xFu, hi = k ? z2 & 0xF0u : z2 << 4;
+                    const ZeroPoint zp{__builtin_amdgcn_perm(0xE4E4E4E4u, lo, 0x04000400u),
+                                       __builtin_amdgcn_perm(0xD4D4D4D4u, hi, 0x04000400u)};
+                    unpack_dword(d[ct][2 * ip + k], zp, magic, pr);
+                    const half8_t bv = __builtin_bit_cast(half8_t, u32x4{pr[0], pr[1], pr[2], pr[3]});
+                    const float sf = (float)__builtin_bit_cast(_Float16, (uint16_t)(k ? s2 >> 16 : s2));
+#pragma unroll
+                    for (int rt = 0; rt < RT; ++rt) {
+                        const float4_t zero = {0.f, 0.f, 0.f, 0.f};
+                        const float4_t v = __builtin_amdgcn_mfma_f32_16x16x32_f16(
+                            __builtin_bit_cast(half8_t, act[rt][2 * ip + k]), bv, zero, 0, 0, 0);
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) acc[ct][rt][r] = fmaf(v[r], sf, acc[ct][rt][r]);
+                    }
                 }
             }
+            if (ip == 0 && last) {
+                const bool turn = tile + 1 == tiles;
+                if (turn || todo == 1) rows_of(b + turn, todo > 1);
+            }
+            next_rows(last ? 0 : step + 1, ip);
         }
         const bool live = todo-- > 0;
-        next(st, odd ? nullptr : &scales);
+        next(w, odd ? nullptr : &scales);
         if (++step < steps) return;
         step = 0;
         // The waves' sums, rows 16 rt + 4 g + r of column 16 ct + j.
