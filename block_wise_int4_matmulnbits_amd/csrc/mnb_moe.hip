@@ -761,13 +761,15 @@ __global__ __launch_bounds__(64 * W) void mnb_moe_down_kernel(MoeParams p)
 // scales of its four rows.
 constexpr int kWideWaves = 8;
 
-// Launch 1: the tables (workgroup 0) and x as fp16 in the unpack's order.
+// Launch 1: the tables (workgroup 0) and x as fp16 in the unpack's order.  Sixteen
+// waves: each routes its tokens one after another.
+constexpr int kPrepareThreads = 1024;
 template <int RT>
-__global__ __launch_bounds__(512) void mnb_moe_prepare_kernel(MoeParams p)
+__global__ __launch_bounds__(kPrepareThreads) void mnb_moe_prepare_kernel(MoeParams p)
 {
     extern __shared__ u32x4 prepare_lds[];
     const int64_t pieces = (int64_t)p.T * p.H / 8;
-    for (int64_t i = (int64_t)blockIdx.x * 512 + threadIdx.x; i < pieces; i += (int64_t)gridDim.x * 512)
+    for (int64_t i = (int64_t)blockIdx.x * kPrepareThreads + threadIdx.x; i < pieces; i += (int64_t)gridDim.x * kPrepareThreads)
         reinterpret_cast<u32x4*>(p.xs)[i] = f16_pairs(reinterpret_cast<const u32x4*>(p.x)[i], p.x_bf16, 0);
     if (blockIdx.x != 0) return;
     const Routing rt = routing_tables(reinterpret_cast<uint8_t*>(prepare_lds), p.E, p.T * p.top_k, p.batch_cap, 4 * RT);
@@ -1038,11 +1040,19 @@ __global__ __launch_bounds__(1024) void mnb_moe_scale_rows_kernel(MoeParams p)
     if (row >= p.head[0] * 16 * RT || p.row_token[row] < 0) return;
     const float4_t* const h = reinterpret_cast<const float4_t*>(p.hf + (int64_t)row * p.I);
     const int pieces = p.I / 8;
-    uint32_t top = 0;
-    for (int i = tid; i < 2 * pieces; i += 1024)
+    constexpr int P = MNB_MOE_MAX_WIDTH / 8 / 1024;   // the whole row in registers
+    float4_t v[P][2] = {};
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const uint32_t m = __float_as_uint(h[i][k]) & 0x7FFFFFFFu;
+    for (int i = 0; i < P; ++i)
+        if (tid + 1024 * i < pieces)
+#pragma unroll
+            for (int q = 0; q < 2; ++q) v[i][q] = h[2 * (tid + 1024 * i) + q];
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < P; ++i)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const uint32_t m = __float_as_uint(v[i][k >> 2][k & 3]) & 0x7FFFFFFFu;
             top = m > top ? m : top;
         }
     top = wave_max(top);
@@ -1053,28 +1063,32 @@ __global__ __launch_bounds__(1024) void mnb_moe_scale_rows_kernel(MoeParams p)
     ex = top == 0 || top >= 0x7F800000u ? 0 : ex < -110 ? -110 : ex;
     if (tid == 0) p.hs[row] = ldexpf(p.row_p[row], ex);
     u32x4* const out = reinterpret_cast<u32x4*>(p.hq + (int64_t)row * p.I);
-    for (int i = tid; i < pieces; i += 1024) {
-        const float4_t lo = h[2 * i], hi = h[2 * i + 1];
-        u32x4 o;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) o[k] = f16_pair(ldexpf(lo[k], -ex), ldexpf(hi[k], -ex));
-        out[i] = o;
-    }
+    for (int i = 0; i < P; ++i)
+        if (tid + 1024 * i < pieces) {
+            u32x4 o;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) o[k] = f16_pair(ldexpf(v[i][0][k], -ex), ldexpf(v[i][1][k], -ex));
+            out[tid + 1024 * i] = o;
+        }
 }
 
-// Launch 5: each token's rows, in the order of its slots.
+// Launch 5: each token's rows, in the order of its slots; four columns a thread.
 __global__ __launch_bounds__(256) void mnb_moe_combine_kernel(MoeParams p)
 {
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (i >= (int64_t)p.T * p.H) return;
-    const int t = (int)(i / p.H), c = (int)(i - (int64_t)t * p.H);
-    float v = 0.f;
+    const int quads = p.H / 4;
+    const int i = blockIdx.x * 256 + threadIdx.x;    // at most 2^20 of them
+    if (i >= p.T * quads) return;
+    const int t = i / quads, c = 4 * (i - t * quads);
+    float4_t v = {0.f, 0.f, 0.f, 0.f};
     for (int s = 0; s < p.top_k; ++s) {
         const int row = p.pair_row[t * p.top_k + s];
-        if (row >= 0) v += p.y[(int64_t)row * p.H + c];
+        if (row >= 0) v += *reinterpret_cast<const float4_t*>(p.y + (int64_t)row * p.H + c);
     }
-    if (p.head[1 + t]) v = __uint_as_float(0x7FC00000u);
-    p.out[i] = narrow16(v, p.out_bf16);
+    const bool bad = p.head[1 + t];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        p.out[(int64_t)t * p.H + c + k] = narrow16(bad ? __uint_as_float(0x7FC00000u) : v[k], p.out_bf16);
 }
 
 // Whether a matrix's scales and zero points can be loaded for `blocks`
@@ -1139,12 +1153,12 @@ hipError_t queue_wide(const MoeParams& p, int cus, int* launches, hipStream_t s)
         int64_t grid;
         int threads;
         size_t lds;
-    } const all[] = {{prepare, std::min<int64_t>((pieces + 511) / 512, cus), 512,
+    } const all[] = {{prepare, std::min<int64_t>((pieces + kPrepareThreads - 1) / kPrepareThreads, cus), kPrepareThreads,
                       routing_bytes(p.E, p.T * p.top_k, p.batch_cap, 4 * RT)},
                      {up, cus, 64 * kWideWaves, tables},
                      {scale, rows, 1024, 0},
                      {down, cus, 64 * kWideWaves, tables},
-                     {combine, ((int64_t)p.T * p.H + 255) / 256, 256, 0}};
+                     {combine, ((int64_t)p.T * p.H / 4 + 255) / 256, 256, 0}};
     for (const Launch& l : all) {
         const hipError_t e = queue(l.fn, p, (unsigned)l.grid, l.threads, l.lds, s);
         if (e != hipSuccess) return e;
