@@ -183,7 +183,7 @@ __device__ __forceinline__ void route_token(const MoeParams& p, int t, const Rou
             if (!p.renormalize) {
                 float m = 0.f;
 #pragma unroll
-                for (int i = 0; i < NS; ++i) m += key[i] > kNegInf ? __expf(value(key[i]) - peak) : 0.f;
+                for (int i = 0; i < NS; ++i) m += key[i] > kNegInf ? expf(value(key[i]) - peak) : 0.f;
                 mass = wave_sum(m);
             }
         }
@@ -198,7 +198,7 @@ __device__ __forceinline__ void route_token(const MoeParams& p, int t, const Rou
             key[i] = take && lane == bit ? 0u : key[i];
             found |= take;
         }
-        const float w = __expf(value(top) - peak);
+        const float w = expf(value(top) - peak);
         if (p.renormalize) mass += w;
         mine_e = lane == j ? e : mine_e;
         mine_w = lane == j ? w : mine_w;
@@ -575,7 +575,7 @@ __global__ __launch_bounds__(64 * kUpWaves) void mnb_moe_up_kernel(MoeParams p)
                 gate += part[buf][4 * k + (c >> 3)][at];
                 up += part[buf][4 * k + (c >> 3)][at + 2 * RQ * 16];
             }
-            const float h = gate / (1.f + __expf(-gate)) * up;
+            const float h = gate / (1.f + expf(-gate)) * up;
             uint32_t top = __float_as_uint(h) & 0x7FFFFFFFu;
 #pragma unroll
             for (int d = 16; d; d >>= 1) {
@@ -1009,7 +1009,7 @@ __global__ __launch_bounds__(64 * kWideWaves) void mnb_moe_wide_kernel(MoeParams
             for (int o = tid; o < 32 * rows && live; o += 64 * W) {
                 const int row = o >> 5, c = o & 31;
                 const float gate = total(row, c), u = total(row, 32 + c);
-                p.hf[((int64_t)b * R + row) * N + 32 * tile + c] = gate / (1.f + __expf(-gate)) * u;
+                p.hf[((int64_t)b * R + row) * N + 32 * tile + c] = gate / (1.f + expf(-gate)) * u;
             }
         } else {
             for (int o = tid; o < 64 * rows && live; o += 64 * W) {
