@@ -170,8 +170,9 @@ __device__ __forceinline__ void route_token(const MoeParams& p, int t, const Rou
     }
     bad = __any(bad);
     auto value = [](uint32_t k) { return __uint_as_float(k ^ (~(uint32_t)((int32_t)k >> 31) | 0x80000000u)); };
-    float peak = 0.f, mass = 0.f, mine_w = 0.f;
-    int mine_e = -1;                             // lane j: slot j
+    float peak = 0.f, mass = 0.f;
+    int mine_e = -1;                             // lane j: slot j, and its logit's key
+    uint32_t mine_key = 0;
     for (int j = 0; j < p.top_k && !bad; ++j) {
         uint32_t top = key[0];
 #pragma unroll
@@ -198,11 +199,11 @@ __device__ __forceinline__ void route_token(const MoeParams& p, int t, const Rou
             key[i] = take && lane == bit ? 0u : key[i];
             found |= take;
         }
-        const float w = expf(value(top) - peak);
-        if (p.renormalize) mass += w;
         mine_e = lane == j ? e : mine_e;
-        mine_w = lane == j ? w : mine_w;
+        mine_key = lane == j ? top : mine_key;
     }
+    const float mine_w = mine_e < 0 ? 0.f : expf(value(mine_key) - peak);
+    if (p.renormalize) mass = wave_sum(mine_w);
     if (lane < p.top_k) {
         const int s = t * p.top_k + lane;
         r.sel[s] = (int16_t)mine_e;
