@@ -456,6 +456,7 @@ MoeLayout moe_layout(int64_t T, int64_t H, int64_t I, int64_t E, int top_k)
         l.h = take(batches * rows * I * 2);
         l.pair_row = take(pairs * 4);
         l.xs = take(T * H * 2);
+        l.xe = take(T * 4);
         l.hf = take(batches * rows * I * 4);
         l.y = take(batches * rows * H * 4);
     } else {

@@ -42,6 +42,13 @@ __device__ __forceinline__ uint16_t narrow16(float v, int bf16)
     return __builtin_bit_cast(uint16_t, (__bf16)v);
 }
 
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b)
+{
+    typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2, a),
+                                                                  __builtin_bit_cast(u16x2, b)));
+}
+
 // Two values -> one fp16 pair, round to nearest even (v_cvt_pk_f16_f32):
 // the fp32 values are exact (bf16 halves widened by a shift or a mask).
 __device__ __forceinline__ uint32_t f16_pair(float lo, float hi)

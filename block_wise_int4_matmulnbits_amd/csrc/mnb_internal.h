@@ -162,7 +162,7 @@ int launch_moe(const MoeArgs& args, void* stream, int* launches) MNB_WEAK;
 struct MoeLayout {
     int wide;                // 0: the narrow kernels; 1, 2: the wide ones with 16 or 32 rows
     int rq, batches;         // row quads of a batch; the most batches there can be
-    size_t batch_e, row_token, row_p, hs, h, pair_row, xs, hf, y, bytes;
+    size_t batch_e, row_token, row_p, hs, h, pair_row, xs, xe, hf, y, bytes;
 };
 MoeLayout moe_layout(int64_t T, int64_t H, int64_t I, int64_t E, int top_k);
 

@@ -22,6 +22,13 @@
 // scale are paid once per lane and 32 weights for four rows (16x16x32
 // products, a quarter block of every column per lane, pay them four times).
 //
+// Activations.  The products take fp16, whose exponents are fewer than bf16's:
+// a bf16 token is multiplied by a power of two, which its sums take back.  Its
+// largest element lands at 2^14 .. 2^15, so that elements down to 2^-31 of it
+// are exact and those below lose at most 2^-39 of it.  (A power per block of 32
+// would cost the first launch a product more per block, row and column: 20
+// tokens, 2 of 8 of 4096, 14336: 244 us against 211.)
+//
 // Between the launches the activations h = silu(g) u lie in the workspace as
 // fp16, scaled by a power of two per row and block of 32 (so that no h
 // overflows and small ones keep their precision), in the order in which the
@@ -49,8 +56,9 @@ constexpr int kMaxSlots = MNB_MOE_MAX_EXPERTS / 64;   // experts per lane of a r
 // 40%, 4 waves with 4 steps ahead 20%.
 constexpr int kUpWaves = 8, kUpRing = 2;
 constexpr size_t kLdsBytes = 160 * 1024;
-// Static LDS of the first launch: two units' partial sums, the waves' scales.
-constexpr size_t up_static_lds(int rq) { return (size_t)2 * kUpWaves * 64 * rq * 4 + kUpWaves * 640; }
+// Static LDS of the first launch: two units' partial sums, the waves' scales, the
+// rows' powers of two.
+constexpr size_t up_static_lds(int rq) { return (size_t)2 * kUpWaves * 64 * rq * 4 + kUpWaves * 640 + 16 * rq; }
 constexpr int kPadToken = 255;                        // a batch's unused rows
 
 struct MoeParams {
@@ -71,6 +79,7 @@ struct MoeParams {
     // Workspace of the wide kernels.
     int32_t* pair_row;   // [T][top_k]: row of the batches, or -1
     uint16_t* xs;        // [T][H]: activations as fp16, in the unpack's order
+    float* xe;           // [T]: the power of two taken out of them
     float* hf;           // [row][I]: silu(g) u
     uint16_t* hq;        // [row][I]: its fp16 form, in the unpack's order
     float* y;            // [row][H]: weighted outputs of the rows
@@ -423,19 +432,49 @@ __device__ __forceinline__ void block_products(const u32x4 (&w)[NC], const uint3
     }
 }
 
+// The power of two that brings bf16 numbers, the largest of whose magnitudes has
+// these bits, to at most 2^15 (`to`), and its inverse; 1 where an infinity or a
+// NaN is among them.  (Rows below 2^-96 keep less than all their bits: their
+// h lies below every number of bf16.)
+struct Power {
+    float to, back;
+};
+__device__ __forceinline__ Power fp16_power(uint32_t top)
+{
+    const int e = (int)(top >> 7) - 127 - 14, ex = top >= 0x7F80u ? 0 : e < -110 ? -110 : e;
+    return Power{__uint_as_float((uint32_t)(127 - ex) << 23), __uint_as_float((uint32_t)(127 + ex) << 23)};
+}
+// Bits of the largest magnitude of eight bf16 numbers.
+__device__ __forceinline__ uint32_t top_of_piece(u32x4 v)
+{
+    uint32_t m = 0;
+#pragma unroll
+    for (int d = 0; d < 4; ++d) m = max_u16x2(m, v[d] & 0x7FFF7FFFu);
+    return (m & 0xFFFFu) > (m >> 16) ? m & 0xFFFFu : m >> 16;
+}
+// Eight bf16 numbers times f as fp16 pairs in the unpack's order (f16_pairs).
+__device__ __forceinline__ u32x4 scaled_pairs(u32x4 v, float f)
+{
+    const uint32_t x = v[0], y = v[1], z = v[2], w = v[3];
+    return u32x4{f16_pair(bf16_lo(x) * f, bf16_lo(z) * f), f16_pair(bf16_hi(x) * f, bf16_hi(z) * f),
+                 f16_pair(bf16_lo(y) * f, bf16_lo(w) * f), f16_pair(bf16_hi(y) * f, bf16_hi(w) * f)};
+}
+
 // First launch: routing, gate and up products, h.  A unit is one batch by 32
 // columns of h; a workgroup takes a contiguous range of units.  Wave (cw, ks)
 // owns columns 8 cw .. 8 cw + 7 of the unit (two gate quads and the two up
 // quads of the same columns) and, of every 4 W blocks of K, the 16 from 16 ks.
 // The rows' activations are staged in LDS as fp16 in the unpack's order, rows
 // 16 bytes apart modulo 128 so that eight lanes' reads fall on distinct banks.
-template <int RQ, bool VEC>
+// BF16: each with its token's power of two.
+template <int RQ, bool VEC, bool BF16>
 __global__ __launch_bounds__(64 * kUpWaves) void mnb_moe_up_kernel(MoeParams p)
 {
     constexpr int NC = 4, R = 4 * RQ, W = kUpWaves, P = kUpRing;
     constexpr int SB = 16 * (W / 4);                 // blocks of K of a step, 16 per slice
     __shared__ float part[2][W][NC * RQ * 16];
     __shared__ u32x2 scale_lds[W][kScaleBytes<NC> / 8];
+    __shared__ float powers[R];                      // BF16: of the staged rows
     extern __shared__ u32x4 up_lds[];                // routing tables, then the stage
     const int tid = threadIdx.x, lane = tid & 63;
     const int wv = __builtin_amdgcn_readfirstlane(tid >> 6), cw = wv & 3, ks = wv >> 2;
@@ -451,19 +490,53 @@ __global__ __launch_bounds__(64 * kUpWaves) void mnb_moe_up_kernel(MoeParams p)
     u32x4* const stage = up_lds + routing_bytes(p.E, pairs, p.batch_cap, RQ) / 16;   // [rows][4 stage_blocks + 1]
 
     // Rows [0, n) of the stage from tokens tok(row), blocks [b0, b0 +
-    // stage_blocks) of K, by threads tid0, tid0 + 1, ...
-    auto fill = [&](int n, int b0, int tid0, auto tok) {
+    // stage_blocks) of K, by the waves from wave0 on.  BF16: a row is the work of
+    // one wave, or of several that each look for its largest element by
+    // themselves, and is then read once more (against plain rounding to fp16: one
+    // token, 8 of 64 of 2048, 768 17.2 us against 16.9; 16 tokens, 6 of 64 of 2048,
+    // 1408 67.2 against 65.4); `fresh`: the rows' powers are not in LDS yet.
+    auto fill = [&](int n, int b0, int wave0, bool fresh, auto tok) {
         const int per_row = 4 * p.stage_blocks;
-        for (int i = tid - tid0; i < n * per_row; i += 64 * W - tid0) {
-            const int row = i / per_row, pc = i - row * per_row, t = tok(row);
-            u32x4 v = {0, 0, 0, 0};
-            if (t != kPadToken && b0 + pc / 4 < nb)
-                v = *reinterpret_cast<const u32x4*>(p.x + (int64_t)t * p.H + 32 * b0 + 8 * pc);
-            stage[row * row_pieces + pc] = f16_pairs(v, p.x_bf16, 0);
+        if constexpr (BF16) {
+            const int nw = W - wave0, w = wv - wave0, wpr = n < nw ? nw / n : 1, groups = nw / wpr;
+            const int part = w % wpr;
+            for (int row = w / wpr < groups ? w / wpr : n; row < n; row += groups) {
+                const int t = tok(row);
+                const bool used = t != kPadToken;
+                const __amdgpu_buffer_rsrc_t rX = make_rsrc_small(p.x + (int64_t)(used ? t : 0) * p.H, used ? 2 * (uint32_t)p.H : 0u);
+                auto load = [&](uint32_t piece) { return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rX, 16 * piece, 0, 0)); };
+                Power pw;
+                if (fresh) {
+                    uint32_t top = 0;
+                    for (int pc = lane; pc < p.H / 8; pc += 64 * 8) {
+                        u32x4 v[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) v[i] = load(pc + 64 * i);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) top = std::max(top, top_of_piece(v[i]));
+                    }
+                    pw = fp16_power(wave_max(top));
+                    if (part == 0 && lane == 0) powers[row] = pw.back;
+                } else {
+                    pw.to = 1.f / powers[row];       // exact
+                }
+#pragma unroll 4
+                for (int pc = 64 * part + lane; pc < per_row; pc += 64 * wpr)
+                    stage[row * row_pieces + pc] = scaled_pairs(load(4 * b0 + pc), pw.to);
+            }
+        } else {
+            const int tid0 = 64 * wave0;
+            for (int i = tid - tid0; i < n * per_row; i += 64 * W - tid0) {
+                const int row = i / per_row, pc = i - row * per_row, t = tok(row);
+                u32x4 v = {0, 0, 0, 0};
+                if (t != kPadToken && b0 + pc / 4 < nb)
+                    v = *reinterpret_cast<const u32x4*>(p.x + (int64_t)t * p.H + 32 * b0 + 8 * pc);
+                stage[row * row_pieces + pc] = f16_pairs(v, 0, 0);
+            }
         }
     };
     const int batches = route<RQ>(p, rt, [&] {
-        if (all && chunks == 1 && wv >= W / 4) fill(p.T, 0, 16 * W, [](int row) { return row; });
+        if (all && chunks == 1 && wv >= W / 4) fill(p.T, 0, W / 4, true, [](int row) { return row; });
     });
 
     const int64_t units = (int64_t)batches * hblocks;   // at most 2^21
@@ -532,7 +605,7 @@ __global__ __launch_bounds__(64 * kUpWaves) void mnb_moe_up_kernel(MoeParams p)
     auto run = [&](Step& st) {
         if (staged != -2 && step % chunk_steps == 0 && (chunks > 1 || staged != b)) {
             __syncthreads();
-            fill(R, SB * step, 0, [&](int row) { return (int)rt.token()[b * R + row]; });
+            fill(R, SB * step, 0, staged != b, [&](int row) { return (int)rt.token()[b * R + row]; });
             __syncthreads();
             staged = b;
         }
@@ -576,6 +649,12 @@ __global__ __launch_bounds__(64 * kUpWaves) void mnb_moe_up_kernel(MoeParams p)
                 gate += part[buf][4 * k + (c >> 3)][at];
                 up += part[buf][4 * k + (c >> 3)][at + 2 * RQ * 16];
             }
+            const int token = rt.token()[b * R + row];
+            if constexpr (BF16) {                    // (unused rows: any value)
+                const float f = powers[staged != -2 ? row : token == kPadToken ? 0 : token];
+                gate *= f;
+                up *= f;
+            }
             const float h = gate / (1.f + expf(-gate)) * up;
             uint32_t top = __float_as_uint(h) & 0x7FFFFFFFu;
 #pragma unroll
@@ -587,7 +666,7 @@ __global__ __launch_bounds__(64 * kUpWaves) void mnb_moe_up_kernel(MoeParams p)
             // or not finite).
             int ex = (int)(top >> 23) - 127 - 13;
             ex = top == 0 || top >= 0x7F800000u ? 0 : ex < -110 ? -110 : ex;
-            if (live && rt.token()[b * R + row] != kPadToken) {
+            if (live && token != kPadToken) {
                 const int64_t quad = (int64_t)b * RQ + (row >> 2);
                 // Its rows: a prefix of the four (tokens are below 64, unused rows 255).
                 const int rows = 4 - __popc(rt.token4[quad] & 0x80808080u);
@@ -762,17 +841,39 @@ __global__ __launch_bounds__(64 * W) void mnb_moe_down_kernel(MoeParams p)
 // scales of its four rows.
 constexpr int kWideWaves = 8;
 
-// Launch 1: the tables (workgroup 0) and x as fp16 in the unpack's order.  Sixteen
-// waves: each routes its tokens one after another.
+// Launch 1: the tables (workgroup 0; sixteen waves, each routes its tokens one
+// after another) and x as fp16 in the unpack's order (a token for each of the
+// others), bf16 with one power of two per token.
 constexpr int kPrepareThreads = 1024;
 template <int RT>
 __global__ __launch_bounds__(kPrepareThreads) void mnb_moe_prepare_kernel(MoeParams p)
 {
     extern __shared__ u32x4 prepare_lds[];
-    const int64_t pieces = (int64_t)p.T * p.H / 8;
-    for (int64_t i = (int64_t)blockIdx.x * kPrepareThreads + threadIdx.x; i < pieces; i += (int64_t)gridDim.x * kPrepareThreads)
-        reinterpret_cast<u32x4*>(p.xs)[i] = f16_pairs(reinterpret_cast<const u32x4*>(p.x)[i], p.x_bf16, 0);
-    if (blockIdx.x != 0) return;
+    if (blockIdx.x != 0) {
+        __shared__ uint32_t tops[kPrepareThreads / 64];
+        constexpr int P = MNB_MOE_MAX_WIDTH / 8 / kPrepareThreads;   // the whole token in registers
+        const int t = blockIdx.x - 1, tid = threadIdx.x, pieces = p.H / 8;
+        const u32x4* const x = reinterpret_cast<const u32x4*>(p.x + (int64_t)t * p.H);
+        u32x4* const out = reinterpret_cast<u32x4*>(p.xs + (int64_t)t * p.H);
+        u32x4 v[P];
+        uint32_t top = 0;
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            v[i] = tid + kPrepareThreads * i < pieces ? x[tid + kPrepareThreads * i] : u32x4{0, 0, 0, 0};
+            top = std::max(top, top_of_piece(v[i]));
+        }
+        top = wave_max(top);
+        if ((tid & 63) == 0) tops[tid >> 6] = top;
+        __syncthreads();
+        for (int w = 0; w < kPrepareThreads / 64; ++w) top = std::max(top, tops[w]);
+        const Power pw = p.x_bf16 ? fp16_power(top) : Power{1.f, 1.f};
+        if (tid == 0) p.xe[t] = pw.back;
+#pragma unroll
+        for (int i = 0; i < P; ++i)
+            if (tid + kPrepareThreads * i < pieces)
+                out[tid + kPrepareThreads * i] = p.x_bf16 ? scaled_pairs(v[i], pw.to) : f16_pairs(v[i], 0, 0);
+        return;
+    }
     const Routing rt = routing_tables(reinterpret_cast<uint8_t*>(prepare_lds), p.E, p.T * p.top_k, p.batch_cap, 4 * RT);
     route<4 * RT>(p, rt, [] {});
 }
@@ -784,6 +885,7 @@ __global__ __launch_bounds__(64 * kWideWaves) void mnb_moe_wide_kernel(MoeParams
     constexpr int R = 16 * RT, CT = 4, W = kWideWaves;
     __shared__ float part[W][CT * RT * 4][64];
     __shared__ u32x4 scale_lds[W][64 * 20 / 16];    // of two steps: [64 columns][8 fp16], then [64][4]
+    __shared__ float powers[UP ? MNB_MOE_MAX_TOKENS : 1];   // the tokens' (xe)
     // The tables, so that the loop reads none from memory (it would wait for
     // its own loads ahead): the batches, then each row's token (UP) or scale.
     extern __shared__ int wide_lds[];
@@ -801,6 +903,7 @@ __global__ __launch_bounds__(64 * kWideWaves) void mnb_moe_wide_kernel(MoeParams
     const int64_t units = (int64_t)p.head[0] * tiles;
     for (int i = tid; i < p.batch_cap; i += 64 * W) batch[i] = p.batch_e[i];
     for (int i = tid; i < p.batch_cap * R; i += 64 * W) row_info[i] = UP ? p.row_token[i] : __float_as_int(p.hs[i]);
+    if (UP && tid < p.T) powers[tid] = p.xe[tid];
     __syncthreads();
     const int per = (int)((units + gridDim.x - 1) / gridDim.x);
     const int u0 = std::min<int>((int)blockIdx.x * per, (int)units), u1 = std::min<int>(u0 + per, (int)units);
@@ -1009,7 +1112,7 @@ __global__ __launch_bounds__(64 * kWideWaves) void mnb_moe_wide_kernel(MoeParams
         if constexpr (UP) {
             for (int o = tid; o < 32 * rows && live; o += 64 * W) {
                 const int row = o >> 5, c = o & 31;
-                const float gate = total(row, c), u = total(row, 32 + c);
+                const float f = powers[row_info[b * R + row]], gate = total(row, c) * f, u = total(row, 32 + c) * f;
                 p.hf[((int64_t)b * R + row) * N + 32 * tile + c] = gate / (1.f + expf(-gate)) * u;
             }
         } else {
@@ -1116,8 +1219,10 @@ hipError_t queue_up(const MoeParams& p, int cus, hipStream_t s)
     const size_t lds = routing_bytes(p.E, p.T * p.top_k, p.batch_cap, RQ) + (size_t)rows * (4 * p.stage_blocks + 1) * 16;
     const int64_t units = (int64_t)p.T * p.top_k * (p.I / 32);
     const bool vec = vec_ok(p.H, p.s1, p.z1, 4);
-    const void* fn = vec ? reinterpret_cast<const void*>(mnb_moe_up_kernel<RQ, true>)
-                         : reinterpret_cast<const void*>(mnb_moe_up_kernel<RQ, false>);
+    const void* fn = p.x_bf16 ? (vec ? reinterpret_cast<const void*>(mnb_moe_up_kernel<RQ, true, true>)
+                                     : reinterpret_cast<const void*>(mnb_moe_up_kernel<RQ, false, true>))
+                              : (vec ? reinterpret_cast<const void*>(mnb_moe_up_kernel<RQ, true, false>)
+                                     : reinterpret_cast<const void*>(mnb_moe_up_kernel<RQ, false, false>));
     return queue(fn, p, (unsigned)(units < cus ? units : cus), 64 * kUpWaves, lds, s);
 }
 
@@ -1142,7 +1247,7 @@ const void* wide_kernel(int64_t K, const uint16_t* scales, const uint8_t* zp)
 template <int RT>
 hipError_t queue_wide(const MoeParams& p, int cus, int* launches, hipStream_t s)
 {
-    const int64_t pieces = (int64_t)p.T * p.H / 8, rows = (int64_t)p.batch_cap * 16 * RT;
+    const int64_t rows = (int64_t)p.batch_cap * 16 * RT;
     const void* const prepare = reinterpret_cast<const void*>(mnb_moe_prepare_kernel<RT>);
     const void* const up = wide_kernel<RT, true>(p.H, p.s1, p.z1);
     const void* const scale = reinterpret_cast<const void*>(mnb_moe_scale_rows_kernel<RT>);
@@ -1154,8 +1259,7 @@ hipError_t queue_wide(const MoeParams& p, int cus, int* launches, hipStream_t s)
         int64_t grid;
         int threads;
         size_t lds;
-    } const all[] = {{prepare, std::min<int64_t>((pieces + kPrepareThreads - 1) / kPrepareThreads, cus), kPrepareThreads,
-                      routing_bytes(p.E, p.T * p.top_k, p.batch_cap, 4 * RT)},
+    } const all[] = {{prepare, p.T + 1, kPrepareThreads, routing_bytes(p.E, p.T * p.top_k, p.batch_cap, 4 * RT)},
                      {up, cus, 64 * kWideWaves, tables},
                      {scale, rows, 1024, 0},
                      {down, cus, 64 * kWideWaves, tables},
@@ -1197,6 +1301,7 @@ int launch_moe(const MoeArgs& a, void* stream, int* launches)
     p.h = reinterpret_cast<uint16_t*>(ws + lay.h);
     p.pair_row = lay.wide ? reinterpret_cast<int32_t*>(ws + lay.pair_row) : nullptr;
     p.xs = reinterpret_cast<uint16_t*>(ws + lay.xs);
+    p.xe = reinterpret_cast<float*>(ws + lay.xe);
     p.hf = reinterpret_cast<float*>(ws + lay.hf);
     p.hq = p.h;
     p.y = reinterpret_cast<float*>(ws + lay.y);

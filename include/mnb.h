@@ -384,8 +384,8 @@ typedef struct {
  *
  *   out[t] = sum_j p[t][j] * Down_e( silu(Gate_e x[t]) * (Up_e x[t]) ),  e = ids[t][j]
  *
- *   x              device, [tokens][H] row-major, fp16 or bf16; 16-byte aligned;
- *                  finite in fp16 (bf16 is rounded to fp16, as in matmul_nbits).
+ *   x              device, [tokens][H] row-major, fp16 or bf16; 16-byte aligned.
+ *                  (bf16 keeps its range here: see Numerics.)
  *   tokens         0 .. MNB_MOE_MAX_TOKENS.
  *   router_logits  device, [tokens][experts], MNB_F32, MNB_F16 or MNB_BF16;
  *                  aligned to its element.
@@ -405,14 +405,16 @@ typedef struct {
  * of zeros.  A token whose logits hold a NaN or +infinity gets ids -1 and NaN
  * in its weights and its output row.
  * Numerics: products of fp16 activations with the exact q - z, summed in fp32
- * per block and scaled by the block's scale in fp32; softmax, silu and the
+ * per block and scaled by the block's scale in fp32.  fp16 x is taken as it
+ * is; a bf16 token is held in fp16 under a power of two of its own, which its
+ * sums take back: exact, but for elements below 2^-31 of the token's largest,
+ * which lose up to 2^-39 of that one.  Softmax, silu and the
  * sum over the experts in fp32, one rounding to fp16 or bf16 (RNE).  The
  * activations between the two products are held in fp16 with a power-of-two
  * scale per token and expert (and block of 32, where the experts see few
  * tokens), so they do not overflow and lose fp16's half step (2^-11, relative)
  * at most; those below 2^-27 of the largest one under the same scale lose up
- * to 2^-38 of that one.  A token's x that is not finite in fp16 spoils that
- * token's row alone.
+ * to 2^-38 of that one.  An x that is not finite spoils its token's row alone.
  * A token's results depend on the batch only through the order in which
  * fp32 sums run.  Equal calls give equal bits on the same device.  out,
  * expert_ids, expert_weights and workspace must not overlap the inputs or each
