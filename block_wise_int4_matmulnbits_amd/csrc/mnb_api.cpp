@@ -423,6 +423,64 @@ size_t int8_workspace_bytes(int a_dtype, int64_t m, int64_t K, int64_t)
     return (size_t)(m * K) + (size_t)(m * 4);   // rows (a multiple of 16 bytes), then scales
 }
 
+// The tile with the least time: rounds of one tile per CU, each a fixed part
+// (filling the stages, the epilogue) and one that grows with K, us and us per
+// 1024 of K.  Fitted to the seven tiles' times on 72 shapes (m = 17 .. 2048; K
+// x N = 4096 x 4096, 4096 x 28672, 14336 x 4096, 4112 x 5999, 1024 x 8192, 8192 x
+// 1024); its choice is 0.4% slower than the fastest tile on average, at most
+// 12% (8.1 against 7.3 us, 32 x 1024 x 8192).  256 x 256 against 256 x 128 on 2048 x
+// 4096 x 28672: 250 and 260 us, on 2048 x 14336 x 4096: 158 and 113; 32 x 32
+// against 64 x 64 on 32 x 14336 x 4096: 21 and 38, on 256 x 4096 x 4096: 24 and 14.
+struct Int8TileCost {
+    int bm, bn;
+    double fixed, per_k;
+};
+constexpr Int8TileCost kInt8Tiles[] = {{256, 256, 8.0, 13.4}, {256, 128, 8.0, 7.2}, {128, 128, 4.5, 4.4},
+                                       {128, 64, 5.5, 2.85},  {64, 64, 5.0, 2.33},  {64, 32, 4.8, 1.42},
+                                       {32, 32, 4.5, 0.98}};
+
+int int8_cheapest_tile(int64_t m, int64_t K, int64_t N, int cus)
+{
+    int best = 0;
+    double least = 0;
+    for (int t = 0; t < (int)(sizeof(kInt8Tiles) / sizeof(kInt8Tiles[0])); ++t) {
+        const Int8TileCost& c = kInt8Tiles[t];
+        const int64_t tiles = ((m + c.bm - 1) / c.bm) * ((N + c.bn - 1) / c.bn), rounds = (tiles + cus - 1) / cus;
+        const double us = (double)rounds * (c.fixed + c.per_k * (double)K / 1024);
+        // (A grid holds 2^32 threads; the largest tile fits for every N there is.)
+        if (t == 0 || (tiles < (1 << 23) && us < least)) {
+            best = t;
+            least = us;
+        }
+    }
+    return best;
+}
+
+Int8Route int8_route(int a_dtype, int64_t m, int64_t K, int64_t N, int cus)
+{
+    Int8Route r{};
+    r.fused = int8_fused(a_dtype, m, K);
+    if (m > 16 || K > kInt8RowsK || int8_rows_lds(m, K, 16) > kInt8RowsLds) {
+        r.tile = int8_cheapest_tile(m, K, N, cus);
+        return r;
+    }
+    r.tile = -1;
+    // Sixteen waves, or eight in two workgroups a CU where both fit LDS:
+    // with K <= 2048, where sixteen would have one unit each under way
+    // (2048 x 28672, one row: 15.2 us against 17.2), and up to 4096 with so
+    // many columns that an odd tile does not count (4096 x 151936: 111
+    // against 119; 4096 x 28672: 25.8 against 24.6; 8192 x 28672: 47.4
+    // against 42.7).
+    const int64_t units = std::max<int64_t>((K + 127) / 128, 1), tiles = (N + 15) / 16;
+    const bool eight = 2 * int8_rows_lds(m, K, 8) <= kInt8RowsLds &&
+                       ((units <= 16 && tiles > cus) || (units <= 32 && tiles > 16 * (int64_t)cus));
+    const int64_t w = std::min<int64_t>(eight ? 8 : 16, units);
+    r.nu = (int)((units + w - 1) / w);
+    r.waves = (int)((units + r.nu - 1) / r.nu);
+    r.workgroups = std::min(tiles, (r.waves <= 8 ? 2 : 1) * (int64_t)cus);
+    return r;
+}
+
 MoeLayout moe_layout(int64_t T, int64_t H, int64_t I, int64_t E, int top_k)
 {
     const int64_t pairs = T * top_k;
@@ -465,6 +523,38 @@ MoeLayout moe_layout(int64_t T, int64_t H, int64_t I, int64_t E, int top_k)
     }
     l.bytes = at;
     return l;
+}
+
+MoeRoute moe_route(const MoeArgs& a, const MoeLayout& l, int cus)
+{
+    const mnb_moe_weights& w = a.w;
+    // Whether a matrix's scales and zero points can be loaded for `blocks`
+    // consecutive blocks at a time.
+    auto vec_ok = [](int64_t K, const uint16_t* scales, const uint8_t* zp, int blocks) {
+        return (K / 32) % blocks == 0 && ((uintptr_t)scales & (2 * blocks - 1)) == 0 &&
+               (blocks < 4 || ((uintptr_t)zp & (blocks / 2 - 1)) == 0);
+    };
+    MoeRoute r{};
+    if (l.wide) {
+        auto vec = [&](int64_t K, const uint16_t* s, const uint8_t* z) { return vec_ok(K, s, z, 8) ? 8 : vec_ok(K, s, z, 4) ? 4 : 1; };
+        r.up_vec = vec(w.hidden, w.gate_up_scales, w.gate_up_zero_points);
+        r.down_vec = vec(w.inter, w.down_scales, w.down_zero_points);
+        return r;
+    }
+    r.up_vec = vec_ok(w.hidden, w.gate_up_scales, w.gate_up_zero_points, 4) ? 4 : 1;
+    // The first launch stages whole rows where they fit, else spans of K.
+    const int blocks = (int)(w.hidden / 32 + 31) / 32 * 32, rows = 4 * l.rq;
+    const int64_t lds = kMoeLds - (int64_t)moe_up_static_lds(l.rq) -
+                        moe_routing_bytes((int)w.experts, a.T * a.top_k, l.batches, l.rq);
+    const int most = (int)(lds / (rows * 16) - 1) / 4 / 32 * 32;
+    r.stage_blocks = std::min(blocks, most);
+    // Columns of a workgroup of the second: as many (16, 8, 4) as leave one for
+    // every CU (us of this launch with 4, 8 and 16): 2 of 8 experts of 4096,
+    // 14336, 1 token 36, 25, 19; 8 of 64 of 2048, 768, 4 tokens 17.6, 11.8, 15.9;
+    // 8 of 32 of 1024, 512, 4 tokens 6.9, 7.8, 8.9.
+    r.down_quads = w.hidden / 16 >= cus ? 4 : w.hidden / 8 >= cus ? 2 : 1;
+    r.down_vec = vec_ok(w.inter, w.down_scales, w.down_zero_points, r.down_quads) ? r.down_quads : 1;
+    return r;
 }
 
 }  // namespace mnb

@@ -182,8 +182,6 @@ __device__ __forceinline__ uint16_t finish(int sum, float a_scale, float b_scale
 //
 // LDS: rows [M][K + 16] (lanes j read rows 16 bytes apart modulo 128), then the
 // sums of two tiles [2][W][64] x 16 bytes.
-inline size_t rows_lds(int64_t m, int64_t K, int waves) { return (size_t)(m * (K + 16)) + (size_t)waves * 2048; }
-
 template <int NU, bool FUSE>
 __global__ __launch_bounds__(1024) void mnb_int8_rows_kernel(Int8Params p)
 {
@@ -557,38 +555,6 @@ hipError_t queue(Int8Fn fn, const Int8Params& p, int64_t grid, int threads, size
     return e != hipSuccess ? e : hipGetLastError();
 }
 
-// The tile with the least time: rounds of one tile per CU, each a fixed part
-// (filling the stages, the epilogue) and one that grows with K, us and us per
-// 1024 of K.  Fitted to the seven tiles' times on 72 shapes (m = 17 .. 2048; K
-// x N = 4096 x 4096, 4096 x 28672, 14336 x 4096, 4112 x 5999, 1024 x 8192, 8192 x
-// 1024); its choice is 0.4% slower than the fastest tile on average, at most
-// 12% (8.1 against 7.3 us, 32 x 1024 x 8192).  256 x 256 against 256 x 128 on 2048 x
-// 4096 x 28672: 250 and 260 us, on 2048 x 14336 x 4096: 158 and 113; 32 x 32
-// against 64 x 64 on 32 x 14336 x 4096: 21 and 38, on 256 x 4096 x 4096: 24 and 14.
-struct TileCost {
-    int bm, bn;
-    double fixed, per_k;
-};
-constexpr TileCost kTiles[] = {{256, 256, 8.0, 13.4}, {256, 128, 8.0, 7.2}, {128, 128, 4.5, 4.4}, {128, 64, 5.5, 2.85},
-                               {64, 64, 5.0, 2.33},   {64, 32, 4.8, 1.42},  {32, 32, 4.5, 0.98}};
-
-int cheapest_tile(int64_t m, int64_t K, int64_t N, int cus)
-{
-    int best = 0;
-    double least = 0;
-    for (int t = 0; t < (int)(sizeof(kTiles) / sizeof(kTiles[0])); ++t) {
-        const TileCost& c = kTiles[t];
-        const int64_t tiles = ((m + c.bm - 1) / c.bm) * ((N + c.bn - 1) / c.bn), rounds = (tiles + cus - 1) / cus;
-        const double us = (double)rounds * (c.fixed + c.per_k * (double)K / 1024);
-        // (A grid holds 2^32 threads; the largest tile fits for every N there is.)
-        if (t == 0 || (tiles < (1 << 23) && us < least)) {
-            best = t;
-            least = us;
-        }
-    }
-    return best;
-}
-
 template <int BM, int BN, int WM, int WN, int KS, int NS, int KB>
 hipError_t queue_tile(const Int8Params& p, hipStream_t s)
 {
@@ -626,13 +592,13 @@ int launch_int8(const Int8Args& a, void* stream, int* launches)
     int e = current_device_cus(&cus);
     if (e != 0) return e;
     const hipStream_t s = static_cast<hipStream_t>(stream);
-    const bool fuse = int8_fused(a.a_dtype, a.m, a.K);
+    const Int8Route route = int8_route(a.a_dtype, a.m, a.K, a.N, cus);
     Int8Params p{};
     p.A = static_cast<const int8_t*>(a.A);
     p.A16 = static_cast<const uint16_t*>(a.A);
     p.a_scales = a.a_scales;
     p.a_bf16 = a.a_dtype == MNB_BF16;
-    if (a.a_dtype != MNB_I8 && !fuse) {
+    if (a.a_dtype != MNB_I8 && !route.fused) {
         int8_t* q = static_cast<int8_t*>(a.ws);
         float* scales = reinterpret_cast<float*>(q + a.m * a.K);
         e = launch_quantize_rows(a.A, p.a_bf16, a.m, a.K, q, scales, stream);
@@ -649,27 +615,12 @@ int launch_int8(const Int8Args& a, void* stream, int* launches)
     p.N = a.N;
     p.K = (int32_t)a.K;
     p.out_bf16 = a.out_bf16;
-    const int64_t units = std::max<int64_t>((a.K + 127) / 128, 1);
     hipError_t he;
-    if (a.m <= 16 && a.K <= kInt8RowsK && rows_lds(a.m, a.K, 16) <= kInt8RowsLds) {
-        // Sixteen waves, or eight in two workgroups a CU where both fit LDS:
-        // with K <= 2048, where sixteen would have one unit each under way
-        // (2048 x 28672, one row: 15.2 us against 17.2), and up to 4096 with so
-        // many columns that an odd tile does not count (4096 x 151936: 111
-        // against 119; 4096 x 28672: 25.8 against 24.6; 8192 x 28672: 47.4
-        // against 42.7).
-        const int64_t tiles = (a.N + 15) / 16;
-        const bool eight = 2 * rows_lds(a.m, a.K, 8) <= kInt8RowsLds &&
-                           ((units <= 16 && tiles > cus) || (units <= 32 && tiles > 16 * (int64_t)cus));
-        int64_t w = eight ? 8 : 16;
-        if (w > units) w = units;
-        const int nu = (int)((units + w - 1) / w);
-        w = (units + nu - 1) / nu;
-        const int64_t slots = (w <= 8 ? 2 : 1) * (int64_t)cus;
-        he = queue(fuse ? rows_kernel<true>(nu) : rows_kernel<false>(nu), p, tiles < slots ? tiles : slots,
-                   (int)(64 * w), rows_lds(a.m, a.K, (int)w), s);
+    if (route.tile < 0) {
+        he = queue(route.fused ? rows_kernel<true>(route.nu) : rows_kernel<false>(route.nu), p, route.workgroups,
+                   64 * route.waves, int8_rows_lds(a.m, a.K, route.waves), s);
     } else {
-        switch (cheapest_tile(a.m, a.K, a.N, cus)) {
+        switch (route.tile) {
         case 0: he = queue_tile<256, 256, 2, 4, 1, 4, 64>(p, s); break;
         case 1: he = queue_tile<256, 128, 4, 2, 1, 3, 128>(p, s); break;
         case 2: he = queue_tile<128, 128, 2, 4, 1, 4, 128>(p, s); break;

@@ -133,10 +133,21 @@ constexpr size_t kInt8RowsLds = 160 * 1024 - 128;
 // x 4096 with 1 row 21.5 against 4.1 + 15.6, with 4 rows 23.9 against 4.1 + 16.3.
 constexpr int64_t kInt8FusedElements = 32768;
 static_assert(kInt8FusedElements + 16 * 16 + 16 * 2048 <= kInt8RowsLds, "fused rows always go to the kernel for few rows");
+inline size_t int8_rows_lds(int64_t m, int64_t K, int waves) { return (size_t)(m * (K + 16)) + (size_t)waves * 2048; }
 inline bool int8_fused(int a_dtype, int64_t m, int64_t K)
 {
     return a_dtype != MNB_I8 && m <= 16 && K <= kInt8RowsK && m * K <= kInt8FusedElements;
 }
+
+// The kernel of an 8-bit product on a device of `cus` compute units.
+// Host-only arithmetic (mnb_api.cpp).
+struct Int8Route {
+    int tile;             // number of the tile (launch_int8), or -1: few rows
+    int waves, nu;        // few rows: waves, and 128-byte units of K of each
+    int64_t workgroups;   // few rows
+    bool fused;           // the kernel quantises the rows itself
+};
+Int8Route int8_route(int a_dtype, int64_t m, int64_t K, int64_t N, int cus);
 
 // Workspace of an 8-bit product: the quantised rows and their scales where the
 // rows come as fp16 or bf16.  Host-only arithmetic (mnb_api.cpp).
@@ -165,5 +176,25 @@ struct MoeLayout {
     size_t batch_e, row_token, row_p, hs, h, pair_row, xs, xe, hf, y, bytes;
 };
 MoeLayout moe_layout(int64_t T, int64_t H, int64_t I, int64_t E, int top_k);
+
+// LDS of a workgroup, of the first narrow launch that the kernel declares (two
+// units' partial sums, the waves' scales, the rows' powers of two), and of the
+// routing tables.
+constexpr int64_t kMoeLds = 160 * 1024;
+constexpr int kMoeUpWaves = 8;
+constexpr uint32_t moe_up_static_lds(int rq) { return 2 * kMoeUpWaves * 64 * rq * 4 + kMoeUpWaves * 640 + 16 * rq; }
+constexpr uint32_t moe_routing_bytes(int E, int pairs, int cap, int rq)
+{
+    return (uint32_t)(8 * E + 4 * pairs + 4 * cap * rq + 2 * E + 2 * pairs + 2 * cap + 15) & ~15u;
+}
+
+// The variants of its kernels on a device of `cus` compute units.  Host-only
+// arithmetic (mnb_api.cpp).
+struct MoeRoute {
+    int up_vec, down_vec;   // blocks whose scales one load brings
+    int stage_blocks;       // narrow: blocks of K staged in LDS at a time
+    int down_quads;         // narrow: column quads of a workgroup of the second launch
+};
+MoeRoute moe_route(const MoeArgs& args, const MoeLayout& layout, int cus);
 
 }  // namespace mnb

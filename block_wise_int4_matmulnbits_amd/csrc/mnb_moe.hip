@@ -54,11 +54,7 @@ constexpr int kMaxSlots = MNB_MOE_MAX_EXPERTS / 64;   // experts per lane of a r
 // the pace of its loop (5.8 TB/s, 64 KB in flight per CU): 12 waves or three or
 // four steps ahead gained nothing, 16 waves (128 registers) spilled and cost
 // 40%, 4 waves with 4 steps ahead 20%.
-constexpr int kUpWaves = 8, kUpRing = 2;
-constexpr size_t kLdsBytes = 160 * 1024;
-// Static LDS of the first launch: two units' partial sums, the waves' scales, the
-// rows' powers of two.
-constexpr size_t up_static_lds(int rq) { return (size_t)2 * kUpWaves * 64 * rq * 4 + kUpWaves * 640 + 16 * rq; }
+constexpr int kUpWaves = kMoeUpWaves, kUpRing = 2;
 constexpr int kPadToken = 255;                        // a batch's unused rows
 
 struct MoeParams {
@@ -131,10 +127,6 @@ struct Routing {
     uint16_t* batch_e;   // [batch]
     __device__ uint8_t* token() const { return reinterpret_cast<uint8_t*>(token4); }   // [batch][4 RQ]
 };
-__host__ __device__ inline uint32_t routing_bytes(int E, int pairs, int cap, int rq)
-{
-    return (uint32_t)(8 * E + 4 * pairs + 4 * cap * rq + 2 * E + 2 * pairs + 2 * cap + 15) & ~15u;
-}
 __device__ __forceinline__ Routing routing_tables(uint8_t* lds, int E, int pairs, int cap, int rq)
 {
     Routing r;
@@ -487,7 +479,7 @@ __global__ __launch_bounds__(64 * kUpWaves) void mnb_moe_up_kernel(MoeParams p)
     const bool all = p.T <= R;                       // every token staged once, rows by token
     const int pairs = p.T * p.top_k;
     const Routing rt = routing_tables(reinterpret_cast<uint8_t*>(up_lds), p.E, pairs, p.batch_cap, RQ);
-    u32x4* const stage = up_lds + routing_bytes(p.E, pairs, p.batch_cap, RQ) / 16;   // [rows][4 stage_blocks + 1]
+    u32x4* const stage = up_lds + moe_routing_bytes(p.E, pairs, p.batch_cap, RQ) / 16;   // [rows][4 stage_blocks + 1]
 
     // Rows [0, n) of the stage from tokens tok(row), blocks [b0, b0 +
     // stage_blocks) of K, by the waves from wave0 on.  BF16: a row is the work of
@@ -1195,14 +1187,6 @@ __global__ __launch_bounds__(256) void mnb_moe_combine_kernel(MoeParams p)
         p.out[(int64_t)t * p.H + c + k] = narrow16(bad ? __uint_as_float(0x7FC00000u) : v[k], p.out_bf16);
 }
 
-// Whether a matrix's scales and zero points can be loaded for `blocks`
-// consecutive blocks at a time.
-bool vec_ok(int64_t K, const uint16_t* scales, const uint8_t* zp, int blocks)
-{
-    return (K / 32) % blocks == 0 && ((uintptr_t)scales & (2 * blocks - 1)) == 0 &&
-           (blocks < 4 || ((uintptr_t)zp & (blocks / 2 - 1)) == 0);
-}
-
 hipError_t queue(const void* fn, const MoeParams& p, unsigned grid, int threads, size_t lds, hipStream_t s)
 {
     MoeParams q = p;
@@ -1212,13 +1196,13 @@ hipError_t queue(const void* fn, const MoeParams& p, unsigned grid, int threads,
 }
 
 template <int RQ>
-hipError_t queue_up(const MoeParams& p, int cus, hipStream_t s)
+hipError_t queue_up(const MoeParams& p, const MoeRoute& r, int cus, hipStream_t s)
 {
     // Every token, where they are few and K is staged whole; else one batch.
     const int rows = p.T < 4 * RQ && p.H <= 32 * p.stage_blocks ? p.T : 4 * RQ;
-    const size_t lds = routing_bytes(p.E, p.T * p.top_k, p.batch_cap, RQ) + (size_t)rows * (4 * p.stage_blocks + 1) * 16;
+    const size_t lds = moe_routing_bytes(p.E, p.T * p.top_k, p.batch_cap, RQ) + (size_t)rows * (4 * p.stage_blocks + 1) * 16;
     const int64_t units = (int64_t)p.T * p.top_k * (p.I / 32);
-    const bool vec = vec_ok(p.H, p.s1, p.z1, 4);
+    const bool vec = r.up_vec > 1;
     const void* fn = p.x_bf16 ? (vec ? reinterpret_cast<const void*>(mnb_moe_up_kernel<RQ, true, true>)
                                      : reinterpret_cast<const void*>(mnb_moe_up_kernel<RQ, false, true>))
                               : (vec ? reinterpret_cast<const void*>(mnb_moe_up_kernel<RQ, true, false>)
@@ -1227,31 +1211,30 @@ hipError_t queue_up(const MoeParams& p, int cus, hipStream_t s)
 }
 
 template <int RQ, int NC, int W>
-hipError_t queue_down(const MoeParams& p, hipStream_t s)
+hipError_t queue_down(const MoeParams& p, const MoeRoute& r, hipStream_t s)
 {
     const size_t lds = ((size_t)W * p.T * 4 * NC + (size_t)p.batch_cap * (8 * RQ + 1)) * 4;
-    const bool vec = vec_ok(p.I, p.s2, p.z2, NC);
-    const void* fn = vec ? reinterpret_cast<const void*>(mnb_moe_down_kernel<RQ, NC, W, true>)
-                         : reinterpret_cast<const void*>(mnb_moe_down_kernel<RQ, NC, W, false>);
+    const void* fn = r.down_vec == NC ? reinterpret_cast<const void*>(mnb_moe_down_kernel<RQ, NC, W, true>)
+                                      : reinterpret_cast<const void*>(mnb_moe_down_kernel<RQ, NC, W, false>);
     return queue(fn, p, (unsigned)(p.H / (4 * NC)), 64 * W, lds, s);
 }
 
 template <int RT, bool UP>
-const void* wide_kernel(int64_t K, const uint16_t* scales, const uint8_t* zp)
+const void* wide_kernel(int vec)
 {
-    return vec_ok(K, scales, zp, 8)   ? reinterpret_cast<const void*>(mnb_moe_wide_kernel<RT, UP, 8>)
-           : vec_ok(K, scales, zp, 4) ? reinterpret_cast<const void*>(mnb_moe_wide_kernel<RT, UP, 4>)
-                                      : reinterpret_cast<const void*>(mnb_moe_wide_kernel<RT, UP, 1>);
+    return vec == 8   ? reinterpret_cast<const void*>(mnb_moe_wide_kernel<RT, UP, 8>)
+           : vec == 4 ? reinterpret_cast<const void*>(mnb_moe_wide_kernel<RT, UP, 4>)
+                      : reinterpret_cast<const void*>(mnb_moe_wide_kernel<RT, UP, 1>);
 }
 
 template <int RT>
-hipError_t queue_wide(const MoeParams& p, int cus, int* launches, hipStream_t s)
+hipError_t queue_wide(const MoeParams& p, const MoeRoute& r, int cus, int* launches, hipStream_t s)
 {
     const int64_t rows = (int64_t)p.batch_cap * 16 * RT;
     const void* const prepare = reinterpret_cast<const void*>(mnb_moe_prepare_kernel<RT>);
-    const void* const up = wide_kernel<RT, true>(p.H, p.s1, p.z1);
+    const void* const up = wide_kernel<RT, true>(r.up_vec);
     const void* const scale = reinterpret_cast<const void*>(mnb_moe_scale_rows_kernel<RT>);
-    const void* const down = wide_kernel<RT, false>(p.I, p.s2, p.z2);
+    const void* const down = wide_kernel<RT, false>(r.down_vec);
     const void* const combine = reinterpret_cast<const void*>(mnb_moe_combine_kernel);
     const size_t tables = (size_t)p.batch_cap * (16 * RT + 1) * 4;
     struct Launch {
@@ -1259,7 +1242,7 @@ hipError_t queue_wide(const MoeParams& p, int cus, int* launches, hipStream_t s)
         int64_t grid;
         int threads;
         size_t lds;
-    } const all[] = {{prepare, p.T + 1, kPrepareThreads, routing_bytes(p.E, p.T * p.top_k, p.batch_cap, 4 * RT)},
+    } const all[] = {{prepare, p.T + 1, kPrepareThreads, moe_routing_bytes(p.E, p.T * p.top_k, p.batch_cap, 4 * RT)},
                      {up, cus, 64 * kWideWaves, tables},
                      {scale, rows, 1024, 0},
                      {down, cus, 64 * kWideWaves, tables},
@@ -1280,6 +1263,7 @@ int launch_moe(const MoeArgs& a, void* stream, int* launches)
     int e = current_device_cus(&cus);
     if (e != 0) return e;
     const MoeLayout lay = moe_layout(a.T, a.w.hidden, a.w.inter, a.w.experts, a.top_k);
+    const MoeRoute route = moe_route(a, lay, cus);
     uint8_t* ws = static_cast<uint8_t*>(a.ws);
     MoeParams p{};
     p.x = static_cast<const uint16_t*>(a.x);
@@ -1318,24 +1302,21 @@ int launch_moe(const MoeArgs& a, void* stream, int* launches)
     p.batch_cap = lay.batches;
     p.h_quad = 128 * ((p.I / 32 + 15) / 16 * 16);
     const hipStream_t s = static_cast<hipStream_t>(stream);
-    if (lay.wide) return (int)(lay.wide == 1 ? queue_wide<1>(p, cus, launches, s) : queue_wide<2>(p, cus, launches, s));
-    // The first launch stages whole rows where they fit, else spans of K.
-    const int blocks = (p.H / 32 + 31) / 32 * 32;
-    const int most = (int)((kLdsBytes - up_static_lds(lay.rq) - routing_bytes(p.E, p.T * p.top_k, p.batch_cap, lay.rq)) /
-                           (4 * lay.rq * 16) - 1) / 4 / 32 * 32;
-    p.stage_blocks = blocks < most ? blocks : most;
-    hipError_t he = lay.rq == 1 ? queue_up<1>(p, cus, s) : queue_up<2>(p, cus, s);
+    if (lay.wide)
+        return (int)(lay.wide == 1 ? queue_wide<1>(p, route, cus, launches, s) : queue_wide<2>(p, route, cus, launches, s));
+    p.stage_blocks = route.stage_blocks;
+    hipError_t he = lay.rq == 1 ? queue_up<1>(p, route, cus, s) : queue_up<2>(p, route, cus, s);
     if (he != hipSuccess) return (int)he;
     ++*launches;
-    // Columns of a workgroup: as many (16, 8, 4) as leave one for every CU (us of
-    // this launch with 4, 8 and 16): 2 of 8 experts of 4096, 14336, 1 token 36, 25,
-    // 19; 8 of 64 of 2048, 768, 4 tokens 17.6, 11.8, 15.9; 8 of 32 of 1024, 512, 4
-    // tokens 6.9, 7.8, 8.9.
-    const int nc = p.H / 16 >= cus ? 4 : p.H / 8 >= cus ? 2 : 1;
+    const int nc = route.down_quads;
     if (lay.rq == 1)
-        he = nc == 4 ? queue_down<1, 4, 12>(p, s) : nc == 2 ? queue_down<1, 2, 16>(p, s) : queue_down<1, 1, 16>(p, s);
+        he = nc == 4   ? queue_down<1, 4, 12>(p, route, s)
+             : nc == 2 ? queue_down<1, 2, 16>(p, route, s)
+                       : queue_down<1, 1, 16>(p, route, s);
     else
-        he = nc == 4 ? queue_down<2, 4, 8>(p, s) : nc == 2 ? queue_down<2, 2, 8>(p, s) : queue_down<2, 1, 8>(p, s);
+        he = nc == 4   ? queue_down<2, 4, 8>(p, route, s)
+             : nc == 2 ? queue_down<2, 2, 8>(p, route, s)
+                       : queue_down<2, 1, 8>(p, route, s);
     if (he == hipSuccess) ++*launches;
     return (int)he;
 }
