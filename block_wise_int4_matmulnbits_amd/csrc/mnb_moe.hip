@@ -1214,8 +1214,9 @@ template <int RQ, int NC, int W>
 hipError_t queue_down(const MoeParams& p, const MoeRoute& r, hipStream_t s)
 {
     const size_t lds = ((size_t)W * p.T * 4 * NC + (size_t)p.batch_cap * (8 * RQ + 1)) * 4;
+    // (Of one quad a load brings one block either way.)
     const void* fn = r.down_vec == NC ? reinterpret_cast<const void*>(mnb_moe_down_kernel<RQ, NC, W, true>)
-                                      : reinterpret_cast<const void*>(mnb_moe_down_kernel<RQ, NC, W, false>);
+                                      : reinterpret_cast<const void*>(mnb_moe_down_kernel<RQ, NC, W, NC == 1>);
     return queue(fn, p, (unsigned)(p.H / (4 * NC)), 64 * W, lds, s);
 }
 
