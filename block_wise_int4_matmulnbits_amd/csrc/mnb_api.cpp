@@ -423,14 +423,30 @@ size_t int8_workspace_bytes(int a_dtype, int64_t m, int64_t K, int64_t)
     return (size_t)(m * K) + (size_t)(m * 4);   // rows (a multiple of 16 bytes), then scales
 }
 
+int quantize_variant(int64_t m, int64_t K)
+{
+    // Rows that fill the device take no more waves than hold them, few rows are
+    // spread wide (us, 64 x 1, 256 x 1, 256 x 8, 1024 x 1, 1024 x 4): 4096 rows of 512
+    // 4.2, 6.2, 9.4, 17.1, 20.9; of 2048 10.0, 8.8, 11.6, 18.3, 21.9; of 8192 34.3,
+    // 25.8, 20.1, 26.7, 30.4; 2048 rows of 16384 50.3, 27.8, 22.1, 26.2, 23.8, of
+    // 32768 101, 59, 61, 50, 38.5; 16 rows of 2048 5.6, 3.3, 3.5, 3.3, 3.6; of 8192
+    // 15.1, 5.9, 4.8, 3.8, 4.2; of 16384 28.3, 9.2, 6.5, 4.8, 4.7.  At 512 rows of 4096
+    // (10.5, 5.0, 5.0, 4.8, 5.6) and 1024 (11.2, 6.3, 6.5, 7.5, 8.5) the order turns.
+    const bool many = m >= 1024;
+    if (K <= 512) return 0;
+    if (K <= (many ? 4096 : 2048)) return 1;
+    if (many && K <= 16384) return 2;
+    return K <= 8192 ? 3 : 4;
+}
+
 // The tile with the least time: rounds of one tile per CU, each a fixed part
 // (filling the stages, the epilogue) and one that grows with K, us and us per
 // 1024 of K.  Fitted to the seven tiles' times on 72 shapes (m = 17 .. 2048; K
 // x N = 4096 x 4096, 4096 x 28672, 14336 x 4096, 4112 x 5999, 1024 x 8192, 8192 x
-// 1024); its choice is 0.4% slower than the fastest tile on average, at most
-// 12% (8.1 against 7.3 us, 32 x 1024 x 8192).  256 x 256 against 256 x 128 on 2048 x
-// 4096 x 28672: 250 and 260 us, on 2048 x 14336 x 4096: 158 and 113; 32 x 32
-// against 64 x 64 on 32 x 14336 x 4096: 21 and 38, on 256 x 4096 x 4096: 24 and 14.
+// 1024); its choice is 0.2% slower than the fastest tile on average, at most
+// 4%.  256 x 256 against 256 x 128 on 2048 x
+// 4096 x 28672: 258 and 275 us, on 2048 x 14336 x 4096: 154 and 116; 32 x 32
+// against 64 x 64 on 32 x 14336 x 4096: 21 and 38, on 256 x 4096 x 4096: 20 and 10.
 struct Int8TileCost {
     int bm, bn;
     double fixed, per_k;
@@ -467,10 +483,10 @@ Int8Route int8_route(int a_dtype, int64_t m, int64_t K, int64_t N, int cus)
     r.tile = -1;
     // Sixteen waves, or eight in two workgroups a CU where both fit LDS:
     // with K <= 2048, where sixteen would have one unit each under way
-    // (2048 x 28672, one row: 15.2 us against 17.2), and up to 4096 with so
-    // many columns that an odd tile does not count (4096 x 151936: 111
-    // against 119; 4096 x 28672: 25.8 against 24.6; 8192 x 28672: 47.4
-    // against 42.7).
+    // (us, eight against sixteen: 2048 x 28672, 4 rows 14.8 and 16.1; 2048 x
+    // 151936, one row 60.4 and 75.4), and up to 4096 with so many columns that
+    // an odd tile does not count (4096 x 151936 111 and 119, but with 16 rows 117
+    // and 111; 4096 x 28672 25.9 and 24.6; 8192 x 28672 47.0 and 42.2).
     const int64_t units = std::max<int64_t>((K + 127) / 128, 1), tiles = (N + 15) / 16;
     const bool eight = 2 * int8_rows_lds(m, K, 8) <= kInt8RowsLds &&
                        ((units <= 16 && tiles > cus) || (units <= 32 && tiles > 16 * (int64_t)cus));
@@ -487,11 +503,13 @@ MoeLayout moe_layout(int64_t T, int64_t H, int64_t I, int64_t E, int top_k)
     MoeLayout l{};
     // The kernels and the rows of a batch, by the tokens an expert sees on
     // average (us, narrow with 8 rows against wide with 16 and with 32): 6 tokens
-    // (24 tokens, 2 of 8 experts of 4096, 14336) 217 against 238 and 265; 8 (32
-    // tokens) 314 against 245 and 275, (64 tokens, 8 of 64 of 2048, 768) 97 against 97
-    // and 113; 16 (64 tokens, 2 of 8) 535 against 390 and 328, (64 tokens, 8 of 32
-    // of 2048, 768) 87 against 84 and 77; 32 (64 tokens, 2 of 4 of 4096, 4096) 133
-    // against 98 and 89.
+    // (24 tokens, 2 of 8 experts of 4096, 14336) 218 against 237 and 262; 8 (32
+    // tokens) 269 against 253 and 279, (64 tokens, 8 of 64 of 2048, 768) 98 against
+    // 100 and 119; 16 (64 tokens, 2 of 8) 451 against 354 and 295, (64 tokens, 8 of
+    // 32 of 2048, 768) 89 against 85 and 76; 32 (64 tokens, 2 of 4 of 4096, 4096) 145
+    // against 102 and 88.  Narrow with 4 rows against 8 (2 of 8 of 4096, 14336):
+    // 3 tokens for an expert 156 against 171, 4 214 against 199, 5 228 against 200.
+    // (Kernel times; three more launches cost the wide form about 5 us besides.)
     l.wide = pairs > 12 * E ? 2 : pairs >= 8 * E ? 1 : 0;
     l.rq = l.wide ? 4 * l.wide : pairs > 4 * E ? 2 : 1;
     // Every expert has at most one batch that is not full.

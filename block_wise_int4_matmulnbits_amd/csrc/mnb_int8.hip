@@ -569,20 +569,13 @@ int launch_quantize_rows(const void* A, int a_bf16, int64_t m, int64_t K, int8_t
 {
     const QuantizeParams p{static_cast<const uint16_t*>(A), q, scales, m, K, a_bf16};
     const hipStream_t s = static_cast<hipStream_t>(stream);
-    // Threads per row and pieces per thread: rows that fill the device take no
-    // more waves than hold them, few rows are spread wide (us, 64 x 1, 256 x 1, 256
-    // x 8, 1024 x 1, 1024 x 4): 4096 rows of 512 4.2, 6.2, 9.4, 17.1, 20.9; of 2048
-    // 10.0, 8.8, 11.6, 18.3, 21.9; of 8192 34.3, 25.8, 20.1, 26.7, 30.4; 2048 rows of
-    // 16384 50.3, 27.8, 22.1, 26.2, 23.8, of 32768 101, 59, 61, 50, 38.5; 16 rows of
-    // 2048 5.6, 3.3, 3.5, 3.3, 3.6; of 8192 15.1, 5.9, 4.8, 3.8, 4.2; of 16384
-    // 28.3, 9.2, 6.5, 4.8, 4.7.  At 512 rows of 4096 (10.5, 5.0, 5.0, 4.8, 5.6) and 1024
-    // (11.2, 6.3, 6.5, 7.5, 8.5) the order turns.
-    const bool many = m >= 1024;
-    if (K <= 512) queue_quantize<64, 1>(p, s);
-    else if (K <= (many ? 4096 : 2048)) queue_quantize<256, 1>(p, s);
-    else if (many && K <= 16384) queue_quantize<256, 8>(p, s);
-    else if (K <= 8192) queue_quantize<1024, 1>(p, s);
-    else queue_quantize<1024, 4>(p, s);
+    switch (quantize_variant(m, K)) {
+    case 0: queue_quantize<64, 1>(p, s); break;
+    case 1: queue_quantize<256, 1>(p, s); break;
+    case 2: queue_quantize<256, 8>(p, s); break;
+    case 3: queue_quantize<1024, 1>(p, s); break;
+    default: queue_quantize<1024, 4>(p, s); break;
+    }
     return (int)hipGetLastError();
 }
 

@@ -121,6 +121,10 @@ int launch_quantize_rows(const void* A, int a_bf16, int64_t m, int64_t K, int8_t
     MNB_WEAK;
 int launch_int8(const Int8Args& args, void* stream, int* launches) MNB_WEAK;
 
+// Threads of a row and pieces of each when rows are quantised: 64 x 1, 256 x 1,
+// 256 x 8, 1024 x 1 or 1024 x 4.  Host-only arithmetic (mnb_api.cpp).
+int quantize_variant(int64_t m, int64_t K);
+
 // The kernel for few rows takes up to 16 of them where they fit its LDS with
 // the sums of its (at most 16) waves, and K up to 16 waves of eight 128-byte
 // units.

@@ -1,4 +1,4 @@
-"""Which kernels the 8-bit products and the expert layer run, from the
+"""Which kernels the 8-bit operators and the expert layer run, from the
 library's own host code: a small program built from csrc/mnb_api.cpp and the
 host-only stand-ins for the HIP side prints the choice for each shape, as on a
 device of 256 compute units."""
@@ -25,6 +25,8 @@ int main()
         if (!strcmp(op, "int8")) {
             const mnb::Int8Route r = mnb::int8_route((int)a, m, K, N, CUS);
             printf("%d %d %d %d\n", r.tile, r.waves, r.nu, (int)r.fused);
+        } else if (!strcmp(op, "quantize")) {
+            printf("%d\n", mnb::quantize_variant(m, K));
         } else {                       // moe T H I E k; arrays on 256 bytes
             const mnb::MoeLayout l = mnb::moe_layout(a, m, K, N, (int)k);
             mnb::MoeArgs args{};
@@ -62,6 +64,16 @@ class Routes:
         names = list(TILES)
         return [(names[t] if t >= 0 else None, w, nu, bool(f))
                 for t, w, nu, f in self._ask(["int8 %d %d %d %d 0" % s for s in shapes])]
+
+    def quantize(self, shapes):
+        """Threads of a row x pieces of each for (m, K)."""
+        names = ("64x1", "256x1", "256x8", "1024x1", "1024x4")
+        return [names[v] for v, in self._ask(["quantize 0 %d %d 0 0" % s for s in shapes])]
+
+    def moe_choice(self, shapes):
+        """(kernels, column quads of the second narrow launch) of (T, H, I, E, k)."""
+        return [("wide%d" % (16 * wide) if wide else "narrow%d" % (4 * rq), str(quads))
+                for wide, rq, _, _, _, quads in self._ask(["moe %d %d %d %d %d" % s for s in shapes])]
 
     def moe(self, shapes):
         """The kernel instances of (T, H, I, E, k) with fp16 and with bf16 rows."""
