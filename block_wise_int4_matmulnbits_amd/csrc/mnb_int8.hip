@@ -317,7 +317,8 @@ __global__ __launch_bounds__(1024) void mnb_int8_rows_kernel(Int8Params p)
 // Sixteen bytes per lane from global memory straight into LDS (lane l to lds +
 // 16 l).  Written as assembly because the compiler makes every LDS read that
 // follows the builtin wait for the transfer; here the caller waits, once per
-// stage (wait_stage).  It has no result registers.
+// stage (turn_over).  It has no result registers, and M0, which it sets, is
+// read by nothing else in these kernels (the compiler reserves it).
 __device__ __forceinline__ void load_to_lds(i32x4 rsrc, uint32_t voffset, uint32_t soffset, uint32_t lds)
 {
     asm volatile("s_mov_b32 m0, %3\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds"

@@ -43,16 +43,21 @@ typedef enum { MNB_F16 = 0, MNB_BF16 = 1, MNB_F32 = 2, MNB_I8 = 3 } mnb_dtype;
 typedef enum {
     MNB_OK = 0,
     MNB_ERR_NULL = 1,     /* a required pointer is NULL                      */
-    MNB_ERR_SHAPE = 2,    /* K < 0, N < 0, K not a multiple of 32, too large  */
+    MNB_ERR_SHAPE = 2,    /* a size that is negative, too large or not a
+                             multiple of what the call needs (matmul_nbits:
+                             K of 32; 8-bit calls: K of 16; expert layer: hidden
+                             and inter of 32), or experts or top_k out of range */
     MNB_ERR_BLOCK = 3,    /* block != 32                                     */
     MNB_ERR_DTYPE = 4,    /* an element type the call does not take           */
-    MNB_ERR_ALIGN = 5,    /* A or Bpacked not 16-byte aligned, scales or out
-                             not 2-byte aligned                              */
+    MNB_ERR_ALIGN = 5,    /* a buffer is not aligned as its call states
+                             (matmul_nbits: A and Bpacked to 16 bytes, scales
+                             and out to 2)                                   */
     MNB_ERR_M_RANGE = 6,  /* m < 0 or m > MNB_MAX_ROWS (tokens of the expert
                              layer: > MNB_MOE_MAX_TOKENS)                     */
     MNB_ERR_HIP = 7,      /* the HIP runtime reported an error; see
                              mnb_last_hip_error()                            */
-    MNB_ERR_ALIAS = 8,    /* out overlaps an input buffer                    */
+    MNB_ERR_ALIAS = 8,    /* a written buffer (out, and whatever else the call
+                             writes) overlaps an input or another of them    */
     MNB_ERR_PLAN = 9,     /* an explicit plan is not one the library runs   */
     MNB_ERR_LAYOUT = 10,  /* unknown weight layout                            */
     MNB_ERR_WORKSPACE = 11 /* matmul_nbits_noalloc: the plan needs more than its
@@ -408,15 +413,17 @@ typedef struct {
  * per block and scaled by the block's scale in fp32.  fp16 x is taken as it
  * is; a bf16 token is held in fp16 under a power of two of its own, which its
  * sums take back: exact, but for elements below 2^-31 of the token's largest,
- * which lose up to 2^-39 of that one.  Softmax, silu and the
- * sum over the experts in fp32, one rounding to fp16 or bf16 (RNE).  The
- * activations between the two products are held in fp16 with a power-of-two
- * scale per token and expert (and block of 32, where the experts see few
- * tokens), so they do not overflow and lose fp16's half step (2^-11, relative)
+ * which lose up to 2^-39 of that one.  Softmax, silu and the sum over the
+ * experts in fp32, one rounding to fp16 or bf16 (RNE).  The activations between
+ * the two products are held in fp16 with a power-of-two scale per token and
+ * expert, and block of 32 where the experts see fewer than eight tokens on
+ * average; so they do not overflow and lose fp16's half step (2^-11, relative)
  * at most; those below 2^-27 of the largest one under the same scale lose up
  * to 2^-38 of that one.  An x that is not finite spoils its token's row alone.
- * A token's results depend on the batch only through the order in which
- * fp32 sums run.  Equal calls give equal bits on the same device.  out,
+ * A token's bits depend on the other tokens' routing and on the number of
+ * tokens, which set that scale's grain and the order in which fp32 sums run,
+ * but never on the values of their x; each form keeps within the roundings
+ * stated here.  Equal calls give equal bits on the same device.  out,
  * expert_ids, expert_weights and workspace must not overlap the inputs or each
  * other.  Asynchronous; allocates nothing; two launches, or five where an
  * expert sees eight tokens or more on average (tokens * top_k >= 8 * experts).
