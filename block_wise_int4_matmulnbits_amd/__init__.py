@@ -1,5 +1,6 @@
 """Python binding of libmnb, the block-wise INT4 MatMulNBits products, 8-bit
-products and 4-bit expert layers for MI355X (gfx950).
+products, 4-bit expert layers, attention over an 8-bit cache and low-rank
+adapters for MI355X (gfx950).
 
 Argument marshalling only: every step of the computation runs in the HIP
 kernels of ``libmnb.so`` (built in-tree by ``build.py``).  Functions carry the
@@ -29,6 +30,12 @@ MNB_MOE_MAX_TOKENS = 64
 MNB_MOE_MAX_EXPERTS = 512
 MNB_MOE_MAX_TOP_K = 16
 MNB_MOE_MAX_WIDTH = 65536
+MNB_KV_MAX_SEQUENCES = 65536
+MNB_KV_MAX_HEADS = 256
+MNB_KV_MAX_GROUP = 64
+MNB_KV_MAX_LENGTH = 1 << 30
+MNB_LORA_MAX_RANK = 256
+MNB_LORA_MAX_ADAPTERS = 65536
 MNB_LAYOUT_NATURAL = 0   # stored weight layouts (mnb_repack_weights)
 MNB_LAYOUT_EVEN_ODD = 1
 
@@ -97,6 +104,17 @@ class mnb_moe_weights(ctypes.Structure):
                 ("down_zero_points", ctypes.c_void_p), ("block", ctypes.c_int32)]
 
 
+class mnb_kv_cache(ctypes.Structure):
+    _fields_ = [("pages", ctypes.c_int64), ("page_size", ctypes.c_int64), ("kv_heads", ctypes.c_int64),
+                ("head_dim", ctypes.c_int64), ("k_pages", ctypes.c_void_p), ("v_pages", ctypes.c_void_p),
+                ("k_scales", ctypes.c_void_p), ("v_scales", ctypes.c_void_p)]
+
+
+class mnb_kv_batch(ctypes.Structure):
+    _fields_ = [("sequences", ctypes.c_int64), ("tokens", ctypes.c_int64), ("max_pages", ctypes.c_int64),
+                ("starts", ctypes.c_void_p), ("lengths", ctypes.c_void_p), ("page_table", ctypes.c_void_p)]
+
+
 _lock = threading.Lock()
 _lib = None
 
@@ -104,7 +122,8 @@ EXPORTS = ("matmul_nbits", "matmul_nbits_planned", "matmul_nbits_noalloc", "mnb_
            "mnb_plan_check", "mnb_counters_get", "mnb_counters_reset",
            "mnb_get_kernel_info", "mnb_status_string", "mnb_last_hip_error",
            "mnb_abi_version", "mnb_repack_weights", "quantize_rows_int8", "matmul_int8",
-           "mnb_int8_workspace", "moe_nbits", "mnb_moe_workspace")
+           "mnb_int8_workspace", "moe_nbits", "mnb_moe_workspace", "append_kv_int8", "attention_int8",
+           "mnb_attention_workspace", "matmul_lora", "mnb_lora_workspace")
 
 
 def lib():
@@ -158,6 +177,18 @@ def lib():
                                 vp, i32, vp, vp, vp, ctypes.c_size_t, vp]
         L.mnb_moe_workspace.restype = ctypes.c_size_t
         L.mnb_moe_workspace.argtypes = [i64, i64, i64, i64, i32]
+        cp, bp = ctypes.POINTER(mnb_kv_cache), ctypes.POINTER(mnb_kv_batch)
+        L.append_kv_int8.restype = i32
+        L.append_kv_int8.argtypes = [cp, bp, i32, vp, i64, vp, i64, vp, i64, vp, i64, i64, vp, vp, i64, i64, i32, vp]
+        L.attention_int8.restype = i32
+        L.attention_int8.argtypes = [cp, bp, i32, vp, i64, i64, ctypes.c_float, vp, i64, i64, vp, ctypes.c_size_t, vp]
+        L.mnb_attention_workspace.restype = ctypes.c_size_t
+        L.mnb_attention_workspace.argtypes = [i64, i64, i64, i64]
+        L.matmul_lora.restype = i32
+        L.matmul_lora.argtypes = [vp, i32, i64, i64, i64, i64, i64, i64, vp, vp, vp, vp, vp, i64, vp, i64, i32, vp,
+                                  ctypes.c_size_t, vp]
+        L.mnb_lora_workspace.restype = ctypes.c_size_t
+        L.mnb_lora_workspace.argtypes = [i64, i64, i64, i64, i64]
         _lib = L
         return L
 
@@ -458,6 +489,189 @@ def moe_nbits(x, router_logits, gate_up, gate_up_scales, gate_up_zero_points, do
 def mnb_moe_workspace(tokens, hidden, inter, experts, top_k):
     """Workspace bytes of moe_nbits."""
     return lib().mnb_moe_workspace(tokens, hidden, inter, experts, top_k)
+
+
+# ------------------------------------- 8-bit cache, attention and adapters
+def _strided(name, t, shape, dtype, index):
+    """t has this shape and type, is on GPU ``index`` and dense but for its
+    first dimension; returns the elements from one row to the next."""
+    if t.dtype != dtype:
+        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if t.shape != shape:
+        raise ValueError("%s must be %s, got %s" % (name, list(shape), list(t.shape)))
+    if t.get_device() != index:
+        raise ValueError("%s must be on the GPU of the first argument, got %s" % (name, t.device))
+    width = 1
+    for d in range(len(shape) - 1, 0, -1):
+        if shape[d] != 1 and t.stride(d) != width:
+            raise ValueError("%s must be contiguous but for its first dimension" % name)
+        width *= shape[d]
+    return t.stride(0) if shape[0] > 1 else width
+
+
+def _kv(x, starts, lengths, page_table, k_pages, v_pages, k_scales, v_scales, index):
+    """The cache and the batch of a call as the library takes them."""
+    import torch
+    if k_pages.dim() != 4 or page_table.dim() != 2 or lengths.dim() != 1:
+        raise ValueError("k_pages must be 4-D, page_table 2-D, lengths 1-D")
+    pages, heads, P, D = k_pages.shape
+    S = lengths.shape[0]
+    _expect("k_pages", k_pages, (pages, heads, P, D), torch.int8, index)
+    _expect("v_pages", v_pages, (pages, heads, D, P), torch.int8, index)
+    _expect("k_scales", k_scales, (pages, heads), torch.float32, index)
+    _expect("v_scales", v_scales, (pages, heads), torch.float32, index)
+    _expect("starts", starts, (S + 1,), torch.int32, index)
+    _expect("lengths", lengths, (S,), torch.int32, index)
+    _expect("page_table", page_table, (S, page_table.shape[1]), torch.int32, index)
+    cache = mnb_kv_cache(pages, P, heads, D, k_pages.data_ptr(), v_pages.data_ptr(), k_scales.data_ptr(),
+                         v_scales.data_ptr())
+    batch = mnb_kv_batch(S, x.shape[0], page_table.shape[1], starts.data_ptr(), lengths.data_ptr(),
+                         page_table.data_ptr())
+    return cache, batch
+
+
+def _on_gpu(name, t, dim):
+    if t.dim() != dim:
+        raise ValueError("%s must be %d-D" % (name, dim))
+    index = t.get_device()
+    if index < 0:
+        raise ValueError("%s must be on the GPU" % name)
+    return index
+
+
+def append_kv_int8(k, v, cos, sin, starts, lengths, page_table, k_pages, v_pages, k_scales, v_scales, q=None,
+                   q_out=None, interleaved=False, stream=None):
+    """New tokens' keys and values into a paged cache of 8-bit integers, the
+    keys rotated by their positions; with q, the rotated queries into q_out.
+
+    k, v: fp16/bf16 [tokens, heads, D], dense but for their first dimension
+    (parts of one buffer, say); cos, sin: fp32 [positions, rotated / 2] with a
+    row for every position that the page table reaches, or None for no
+    rotation; starts: int32 [S + 1], the rows of each sequence; lengths: int32
+    [S], its tokens with the new ones; page_table: int32 [S, pages of a
+    sequence]; k_pages: int8 [pages, heads, P, D]; v_pages: int8 [pages, heads,
+    D, P]; k_scales, v_scales: fp32 [pages, heads].  q, q_out: [tokens, query
+    heads, D]; q_out may be q.  An integer n of the cache stands for (n + 1/2)
+    * scale.  interleaved: pairs are neighbours, not half the rotated width
+    apart.  Queued on ``stream``; returns q_out.
+    """
+    L = _lib or lib()
+    index = _on_gpu("k", k, 3)
+    T, heads, D = k.shape
+    dtype = _dtype_code(k)
+    cache, batch = _kv(k, starts, lengths, page_table, k_pages, v_pages, k_scales, v_scales, index)
+    if (heads, D) != (cache.kv_heads, cache.head_dim):
+        raise ValueError("k must be [tokens, %d, %d]" % (cache.kv_heads, cache.head_dim))
+    ks = _strided("k", k, (T, heads, D), k.dtype, index)
+    vs = _strided("v", v, (T, heads, D), k.dtype, index)
+    qp = op = None
+    qs = os_ = q_heads = 0
+    if (q is None) != (q_out is None):
+        raise ValueError("q and q_out go together")
+    if q is not None:
+        _on_gpu("q", q, 3)
+        q_heads = q.shape[1]
+        qs = _strided("q", q, (T, q_heads, D), k.dtype, index)
+        os_ = _strided("q_out", q_out, (T, q_heads, D), k.dtype, index)
+        qp, op = q.data_ptr(), q_out.data_ptr()
+    cp = sp = None
+    rot = rows = 0
+    if (cos is None) != (sin is None):
+        raise ValueError("cos and sin go together")
+    if cos is not None:
+        import torch
+        if cos.dim() != 2:
+            raise ValueError("cos must be 2-D")
+        rows, rot = cos.shape[0], 2 * cos.shape[1]
+        _expect("cos", cos, (rows, rot // 2), torch.float32, index)
+        _expect("sin", sin, (rows, rot // 2), torch.float32, index)
+        cp, sp = cos.data_ptr(), sin.data_ptr()
+    _on_device(index, stream, L.append_kv_int8, ctypes.byref(cache), ctypes.byref(batch), dtype, k.data_ptr(), ks,
+               v.data_ptr(), vs, qp, qs, op, os_, q_heads, cp, sp, rot, rows, 1 if interleaved else 0)
+    return q_out
+
+
+def attention_int8(q, starts, lengths, page_table, k_pages, v_pages, k_scales, v_scales, out, scale=None,
+                   max_tokens=None, workspace=None, stream=None):
+    """Causal attention of a batch's new tokens over the 8-bit paged cache
+    (append_kv_int8), which holds their own keys and values already.
+
+    q, out: fp16/bf16 [tokens, query heads, D], dense but for their first
+    dimension; query head i reads key head i // (query heads / heads).  The
+    cache and the batch as for append_kv_int8.  scale: of the scores, D^-1/2
+    by default.  max_tokens: the most new tokens of a sequence, where known;
+    it only chooses kernels.  Rows behind the last sequence are left as they
+    are, rows that see no key are zero.  workspace: a tensor of at least
+    mnb_attention_workspace(...) bytes, or None for one of torch's allocator.
+    Queued on ``stream``; returns ``out``.
+    """
+    L = _lib or lib()
+    index = _on_gpu("q", q, 3)
+    T, heads, D = q.shape
+    dtype = _dtype_code(q)
+    cache, batch = _kv(q, starts, lengths, page_table, k_pages, v_pages, k_scales, v_scales, index)
+    if D != cache.head_dim:
+        raise ValueError("q must be [tokens, query heads, %d]" % cache.head_dim)
+    qs = _strided("q", q, (T, heads, D), q.dtype, index)
+    os_ = _strided("out", out, (T, heads, D), q.dtype, index)
+    need = L.mnb_attention_workspace(T, heads, cache.kv_heads, D) if workspace is None else 0
+    ws = _workspace(q, need, workspace, stream, index) if need or workspace is not None else None
+    _on_device(index, stream, L.attention_int8, ctypes.byref(cache), ctypes.byref(batch), dtype, q.data_ptr(), qs, heads,
+               D ** -0.5 if scale is None else scale, out.data_ptr(), os_, max_tokens or 0,
+               None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel() * ws.element_size())
+    return out
+
+
+def mnb_attention_workspace(tokens, q_heads, kv_heads, head_dim):
+    """Workspace bytes of attention_int8."""
+    return lib().mnb_attention_workspace(tokens, q_heads, kv_heads, head_dim)
+
+
+def matmul_lora(x, ids, A, B, base, out, scaling=None, workspace=None, stream=None):
+    """out[r] = base[r] + scaling[a] * B[a] @ (A[a] @ x[r]) with a = ids[r]: the
+    low-rank adapters of many requests beside a shared projection.
+
+    x: fp16/bf16 [m, K], K a multiple of 16; ids: int32 [m] (a number outside 0
+    .. n - 1: no adapter); A: [n, R, K] and B: [n, N, R] of x's type, R a
+    multiple of 8 up to MNB_LORA_MAX_RANK; base, out: fp16/bf16 [m, N] of one
+    type, out may be base, base None for zeros; scaling: fp32 [n] or None.  x,
+    base and out may have rows further apart than their width.  workspace: a
+    tensor of at least mnb_lora_workspace(...) bytes, or None for one of
+    torch's allocator.  Queued on ``stream``; returns ``out``.
+    """
+    import torch
+    L = _lib or lib()
+    index = _on_gpu("x", x, 2)
+    m, K = x.shape
+    if A.dim() != 3 or B.dim() != 3 or out.dim() != 2:
+        raise ValueError("A and B must be 3-D, out 2-D")
+    n, R = A.shape[0], A.shape[1]
+    N = B.shape[1]
+    x_dt, o_dt = _dtype_code(x), _dtype_code(out)
+    xs = _strided("x", x, (m, K), x.dtype, index)
+    os_ = _strided("out", out, (m, N), out.dtype, index)
+    _expect("ids", ids, (m,), torch.int32, index)
+    _expect("A", A, (n, R, K), x.dtype, index)
+    _expect("B", B, (n, N, R), x.dtype, index)
+    sp = bp = None
+    bs = 0
+    if scaling is not None:
+        _expect("scaling", scaling, (n,), torch.float32, index)
+        sp = scaling.data_ptr()
+    if base is not None:
+        bs = _strided("base", base, (m, N), out.dtype, index)
+        bp = base.data_ptr()
+    need = L.mnb_lora_workspace(m, K, N, R, n) if workspace is None else 0
+    ws = _workspace(x, need, workspace, stream, index) if need or workspace is not None else None
+    _on_device(index, stream, L.matmul_lora, x.data_ptr(), x_dt, xs, m, K, N, R, n, ids.data_ptr(), A.data_ptr(),
+               B.data_ptr(), sp, bp, bs, out.data_ptr(), os_, o_dt, None if ws is None else ws.data_ptr(),
+               0 if ws is None else ws.numel() * ws.element_size())
+    return out
+
+
+def mnb_lora_workspace(m, K, N, rank, adapters):
+    """Workspace bytes of matmul_lora."""
+    return lib().mnb_lora_workspace(m, K, N, rank, adapters)
 
 
 def mnb_plan_default(m, K, N, num_cus, wgs_per_cu=0):

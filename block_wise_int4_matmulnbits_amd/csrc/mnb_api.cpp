@@ -141,6 +141,68 @@ int finish_launches(int e, int launches)
     return MNB_OK;
 }
 
+// Rows of a buffer: `rows` of `width` bytes, `stride` bytes apart.
+struct Rows {
+    const void* p;
+    int64_t rows, width, stride;
+};
+
+Span span_of(const Rows& r) { return Span{r.p, r.rows > 0 ? (r.rows - 1) * r.stride + r.width : 0}; }
+
+// Whether two sets of rows share a byte.  Rows of one stride may lie between
+// each other (parts of one buffer); others must not overlap as a whole.
+bool rows_overlap(const Rows& a, const Rows& b)
+{
+    const Span x = span_of(a), y = span_of(b);
+    if (!overlaps(x.p, x.bytes, y.p, y.bytes)) return false;
+    if (a.stride != b.stride || a.stride <= 0) return true;
+    int64_t d = ((int64_t)((uintptr_t)b.p - (uintptr_t)a.p)) % a.stride;
+    if (d < 0) d += a.stride;
+    return d < a.width || d + b.width > a.stride;
+}
+
+int check_kv(const mnb_kv_cache& c, const mnb_kv_batch& b)
+{
+    if (b.tokens < 0 || b.tokens > MNB_MAX_ROWS) return MNB_ERR_M_RANGE;
+    if (c.pages < 0 || c.pages > INT32_MAX || !is_pow2_in(c.page_size, 16, 256) || c.kv_heads < 1 ||
+        c.kv_heads > MNB_KV_MAX_HEADS || !is_pow2_in(c.head_dim, 64, 256) || b.sequences < 0 ||
+        b.sequences > MNB_KV_MAX_SEQUENCES || b.max_pages < 0 || b.max_pages > MNB_KV_MAX_LENGTH / c.page_size)
+        return MNB_ERR_SHAPE;
+    return MNB_OK;
+}
+
+int check_kv_pointers(const mnb_kv_cache& c, const mnb_kv_batch& b)
+{
+    if (!b.starts || !b.lengths || (b.max_pages > 0 && !b.page_table)) return MNB_ERR_NULL;
+    if (c.pages > 0 && (!c.k_pages || !c.v_pages || !c.k_scales || !c.v_scales)) return MNB_ERR_NULL;
+    if (((uintptr_t)b.starts & 3) || ((uintptr_t)b.lengths & 3) || ((uintptr_t)b.page_table & 3) ||
+        ((uintptr_t)c.k_pages & 15) || ((uintptr_t)c.v_pages & 15) || ((uintptr_t)c.k_scales & 3) ||
+        ((uintptr_t)c.v_scales & 3))
+        return MNB_ERR_ALIGN;
+    return MNB_OK;
+}
+
+// Whether q_heads query heads can share kv_heads key heads.
+bool good_group(int64_t q_heads, int64_t kv_heads)
+{
+    return q_heads > 0 && q_heads % kv_heads == 0 && q_heads / kv_heads <= MNB_KV_MAX_GROUP;
+}
+
+// A strided operand [tokens][heads][D]: its row stride in elements.
+bool bad_stride(int64_t stride, int64_t heads, int64_t D, int64_t tokens)
+{
+    return tokens > 1 && (stride < heads * D || stride % 8 || stride > ((int64_t)1 << 40));
+}
+
+int check_lora_shape(int64_t m, int64_t K, int64_t N, int64_t rank, int64_t adapters)
+{
+    if (m < 0 || m > MNB_MAX_ROWS) return MNB_ERR_M_RANGE;
+    if (K < 0 || K % 16 || K > MNB_MAX_K || N < 0 || N > MNB_MAX_N_INT8 || rank < 8 || rank % 8 ||
+        rank > MNB_LORA_MAX_RANK || adapters < 0 || adapters > MNB_LORA_MAX_ADAPTERS)
+        return MNB_ERR_SHAPE;
+    return MNB_OK;
+}
+
 int check_int8_shape(int a_dtype, int64_t m, int64_t K, int64_t N)
 {
     if (m < 0 || m > MNB_MAX_ROWS) return MNB_ERR_M_RANGE;
@@ -573,6 +635,34 @@ MoeRoute moe_route(const MoeArgs& a, const MoeLayout& l, int cus)
     r.down_quads = w.hidden / 16 >= cus ? 4 : w.hidden / 8 >= cus ? 2 : 1;
     r.down_vec = vec_ok(w.inter, w.down_scales, w.down_zero_points, r.down_quads) ? r.down_quads : 1;
     return r;
+}
+
+}  // namespace mnb
+
+namespace mnb {
+
+AttentionLayout attention_layout(int64_t head_dim)
+{
+    AttentionLayout l;
+    l.workgroups = 512;
+    const size_t tiles = 2 * (size_t)l.workgroups;
+    l.o = tiles * 16 * 2 * 4;
+    l.bytes = l.o + tiles * 16 * (size_t)head_dim * 4;
+    return l;
+}
+
+LoraLayout lora_layout(int64_t m, int64_t K, int64_t R)
+{
+    LoraLayout l;
+    l.row_tiles = m <= 64 ? 1 : R <= 128 ? 4 : 2;
+    const int64_t tiles = ceil_div(m, 16 * l.row_tiles);
+    int64_t splits = ceil_div(512, tiles);
+    splits = std::min<int64_t>(splits, std::min<int64_t>(16, std::max<int64_t>(1, K / 256)));
+    const int64_t slice = ceil_div(ceil_div(K, splits), 128) * 128;
+    l.k_slice = (int)std::max<int64_t>(128, slice);
+    l.splits = (int)std::max<int64_t>(1, ceil_div(K, l.k_slice));
+    l.bytes = (size_t)l.splits * (size_t)m * (size_t)R * 4;
+    return l;
 }
 
 }  // namespace mnb
@@ -1012,6 +1102,148 @@ int moe_nbits(const void* x, int x_dtype, int64_t tokens, const void* router_log
     return finish_launches(e, launches);
 }
 
+int append_kv_int8(const mnb_kv_cache* cache, const mnb_kv_batch* batch, int dtype, const void* k, int64_t k_stride,
+                   const void* v, int64_t v_stride, const void* q, int64_t q_stride, void* q_out,
+                   int64_t q_out_stride, int64_t q_heads, const float* cos, const float* sin, int64_t rot_dim,
+                   int64_t table_rows, int interleaved, void* stream)
+{
+    if (!cache || !batch) return MNB_ERR_NULL;
+    const mnb_kv_cache& c = *cache;
+    const mnb_kv_batch& b = *batch;
+    int st = check_kv(c, b);
+    if (st != MNB_OK) return st;
+    const int64_t H = c.kv_heads, D = c.head_dim, P = c.page_size, T = b.tokens;
+    if (rot_dim < 0 || rot_dim > D || rot_dim % 16 || q_heads < 0 || q_heads > MNB_KV_MAX_HEADS * MNB_KV_MAX_GROUP ||
+        (rot_dim > 0 && table_rows < b.max_pages * P) || bad_stride(k_stride, H, D, T) ||
+        bad_stride(v_stride, H, D, T) || (q_heads && (bad_stride(q_stride, q_heads, D, T) ||
+                                                      bad_stride(q_out_stride, q_heads, D, T))))
+        return MNB_ERR_SHAPE;
+    if (dtype != MNB_F16 && dtype != MNB_BF16) return MNB_ERR_DTYPE;
+    if (T == 0 || b.sequences == 0 || b.max_pages == 0) return finish_launches(0, 0);
+    st = check_kv_pointers(c, b);
+    if (st == MNB_ERR_NULL || !k || !v || (q_heads > 0) != (q != nullptr) || (q != nullptr) != (q_out != nullptr) ||
+        (rot_dim > 0 && (!cos || !sin)))
+        return MNB_ERR_NULL;
+    if (st != MNB_OK || ((uintptr_t)k & 15) || ((uintptr_t)v & 15) || ((uintptr_t)q & 15) || ((uintptr_t)q_out & 15) ||
+        (rot_dim > 0 && (((uintptr_t)cos & 15) || ((uintptr_t)sin & 15))))
+        return MNB_ERR_ALIGN;
+    const Rows kr{k, T, H * D * 2, k_stride * 2}, vr{v, T, H * D * 2, v_stride * 2},
+        qr{q, T, q_heads * D * 2, q_stride * 2}, qo{q_out, T, q_heads * D * 2, q_out_stride * 2};
+    const Span tables = {rot_dim ? cos : nullptr, table_rows * (rot_dim / 2) * 4},
+               tables2 = {rot_dim ? sin : nullptr, table_rows * (rot_dim / 2) * 4};
+    const Span in[] = {span_of(kr), span_of(vr), span_of(qr), tables, tables2, {b.starts, (b.sequences + 1) * 4},
+                       {b.lengths, b.sequences * 4}, {b.page_table, b.sequences * b.max_pages * 4}};
+    const int64_t each = c.pages * H;
+    const Span wr[] = {{c.k_pages, each * P * D}, {c.v_pages, each * P * D}, {c.k_scales, each * 4},
+                       {c.v_scales, each * 4}};
+    const Span qw[] = {span_of(qo)};
+    if (aliased(in, 8, wr, 4) || aliased(in + 3, 5, qw, 1) || aliased(wr, 4, qw, 1)) return MNB_ERR_ALIAS;
+    const bool in_place = q && q_out == q && (T == 1 || q_out_stride == q_stride);
+    if (q && (rows_overlap(qo, kr) || rows_overlap(qo, vr) || (!in_place && rows_overlap(qo, qr)))) return MNB_ERR_ALIAS;
+    if (log_enabled())
+        fprintf(stderr, "mnb: append_kv_int8 sequences=%lld tokens=%lld heads=%lld q_heads=%lld dim=%lld page=%lld "
+                "rot=%lld type=%s launches=1\n", (long long)b.sequences, (long long)T, (long long)H,
+                (long long)q_heads, (long long)D, (long long)P, (long long)rot_dim, dtype_name(dtype));
+    if (!mnb::launch_append) return finish_launches(kNoDevice, 0);
+    const mnb::AppendArgs args{c, b, k, v, q, q_out, k_stride, v_stride, q_stride, q_out_stride, q_heads, rot_dim,
+                               cos, sin, dtype == MNB_BF16, interleaved != 0};
+    return finish_launches(mnb::launch_append(args, stream), 1);
+}
+
+size_t mnb_attention_workspace(int64_t tokens, int64_t q_heads, int64_t kv_heads, int64_t head_dim)
+{
+    const mnb_kv_cache c{0, 16, kv_heads, head_dim, nullptr, nullptr, nullptr, nullptr};
+    const mnb_kv_batch b{0, tokens, 0, nullptr, nullptr, nullptr};
+    if (check_kv(c, b) != MNB_OK || !good_group(q_heads, kv_heads) || tokens == 0) return 0;
+    return mnb::attention_layout(head_dim).bytes;
+}
+
+int attention_int8(const mnb_kv_cache* cache, const mnb_kv_batch* batch, int dtype, const void* q, int64_t q_stride,
+                   int64_t q_heads, float scale, void* out, int64_t out_stride, int64_t max_tokens, void* workspace,
+                   size_t workspace_bytes, void* stream)
+{
+    if (!cache || !batch) return MNB_ERR_NULL;
+    const mnb_kv_cache& c = *cache;
+    const mnb_kv_batch& b = *batch;
+    int st = check_kv(c, b);
+    if (st != MNB_OK) return st;
+    const int64_t H = c.kv_heads, D = c.head_dim, P = c.page_size, T = b.tokens;
+    if (!good_group(q_heads, H) || bad_stride(q_stride, q_heads, D, T) || bad_stride(out_stride, q_heads, D, T) ||
+        max_tokens < 0 || !std::isfinite(scale))
+        return MNB_ERR_SHAPE;
+    if (dtype != MNB_F16 && dtype != MNB_BF16) return MNB_ERR_DTYPE;
+    if (T == 0 || b.sequences == 0) return finish_launches(0, 0);
+    st = check_kv_pointers(c, b);
+    if (st == MNB_ERR_NULL || !q || !out || !workspace) return MNB_ERR_NULL;
+    if (st != MNB_OK || ((uintptr_t)q & 15) || ((uintptr_t)out & 15) || ((uintptr_t)workspace & 15))
+        return MNB_ERR_ALIGN;
+    const size_t need = mnb::attention_layout(D).bytes;
+    if (need > workspace_bytes) return MNB_ERR_WORKSPACE;
+    const int64_t each = c.pages * H;
+    const Rows qr{q, T, q_heads * D * 2, q_stride * 2}, orow{out, T, q_heads * D * 2, out_stride * 2};
+    const Span in[] = {{c.k_pages, each * P * D}, {c.v_pages, each * P * D}, {c.k_scales, each * 4},
+                       {c.v_scales, each * 4}, {b.starts, (b.sequences + 1) * 4}, {b.lengths, b.sequences * 4},
+                       {b.page_table, b.sequences * b.max_pages * 4}};
+    const Span wr[] = {span_of(orow), {workspace, (int64_t)need}}, qs[] = {span_of(qr)};
+    if (aliased(in, 7, wr, 2) || aliased(qs, 1, wr + 1, 1) || rows_overlap(orow, qr)) return MNB_ERR_ALIAS;
+    if (!mnb::launch_attention) return finish_launches(kNoDevice, 0);
+    const mnb::AttentionArgs args{c, b, q, out, q_stride, out_stride, q_heads, max_tokens, scale, dtype == MNB_BF16,
+                                  workspace};
+    int launches = 0;
+    const int e = mnb::launch_attention(args, stream, &launches);
+    if (log_enabled())
+        fprintf(stderr, "mnb: attention_int8 sequences=%lld tokens=%lld heads=%lld q_heads=%lld dim=%lld page=%lld "
+                "type=%s launches=%d\n", (long long)b.sequences, (long long)T, (long long)H, (long long)q_heads,
+                (long long)D, (long long)P, dtype_name(dtype), launches);
+    return finish_launches(e, launches);
+}
+
+size_t mnb_lora_workspace(int64_t m, int64_t K, int64_t N, int64_t rank, int64_t adapters)
+{
+    if (check_lora_shape(m, K, N, rank, adapters) != MNB_OK || m == 0 || N == 0) return 0;
+    return mnb::lora_layout(m, K, rank).bytes;
+}
+
+int matmul_lora(const void* x, int x_dtype, int64_t x_stride, int64_t m, int64_t K, int64_t N, int64_t rank,
+                int64_t adapters, const int32_t* ids, const void* A, const void* B, const float* scaling,
+                const void* base, int64_t base_stride, void* out, int64_t out_stride, int out_dtype, void* workspace,
+                size_t workspace_bytes, void* stream)
+{
+    int st = check_lora_shape(m, K, N, rank, adapters);
+    if (st != MNB_OK) return st;
+    const int64_t most = (int64_t)1 << 40;
+    if (m > 1 && (x_stride < K || x_stride % 8 || x_stride > most || out_stride < N || out_stride > most ||
+                  (base && (base_stride < N || base_stride > most))))
+        return MNB_ERR_SHAPE;
+    if ((x_dtype != MNB_F16 && x_dtype != MNB_BF16) || (out_dtype != MNB_F16 && out_dtype != MNB_BF16))
+        return MNB_ERR_DTYPE;
+    if (m == 0 || N == 0) return finish_launches(0, 0);
+    if (!out || !ids || !workspace || (adapters > 0 && (!B || (K > 0 && (!x || !A))))) return MNB_ERR_NULL;
+    if (((uintptr_t)x & 15) || ((uintptr_t)A & 15) || ((uintptr_t)B & 15) || ((uintptr_t)ids & 3) ||
+        ((uintptr_t)scaling & 3) || ((uintptr_t)base & 1) || ((uintptr_t)out & 1) || ((uintptr_t)workspace & 15))
+        return MNB_ERR_ALIGN;
+    const size_t need = mnb::lora_layout(m, K, rank).bytes;
+    if (need > workspace_bytes) return MNB_ERR_WORKSPACE;
+    const Rows xr{x, m, K * 2, x_stride * 2}, br{base, m, N * 2, base_stride * 2}, orow{out, m, N * 2, out_stride * 2};
+    const Span in[] = {{ids, m * 4}, {A, adapters * rank * K * 2}, {B, adapters * N * rank * 2}, {scaling, adapters * 4},
+                       span_of(xr), span_of(br)};
+    const Span wr[] = {span_of(orow), {workspace, (int64_t)need}};
+    const bool in_place = base == out && (m == 1 || base_stride == out_stride);
+    if (aliased(in, 4, wr, 2) || aliased(in + 4, 2, wr + 1, 1) || rows_overlap(orow, xr) ||
+        (base && !in_place && rows_overlap(orow, br)))
+        return MNB_ERR_ALIAS;
+    if (!mnb::launch_lora) return finish_launches(kNoDevice, 0);
+    const mnb::LoraArgs args{x, ids, A, B, scaling, base, out, x_stride, base_stride, out_stride, m, K, N, rank,
+                             adapters, x_dtype == MNB_BF16, out_dtype == MNB_BF16, workspace};
+    int launches = 0;
+    const int e = mnb::launch_lora(args, stream, &launches);
+    if (log_enabled())
+        fprintf(stderr, "mnb: matmul_lora m=%lld K=%lld N=%lld rank=%lld adapters=%lld x=%s out=%s launches=%d\n",
+                (long long)m, (long long)K, (long long)N, (long long)rank, (long long)adapters, dtype_name(x_dtype),
+                dtype_name(out_dtype), launches);
+    return finish_launches(e, launches);
+}
+
 void mnb_counters_get(mnb_counters* out)
 {
     if (!out) return;
@@ -1055,7 +1287,7 @@ const char* mnb_status_string(int status)
     case MNB_ERR_BLOCK: return "block size must be 32";
     case MNB_ERR_DTYPE: return "an element type the call does not take (matmul_nbits: MNB_F16 or MNB_BF16)";
     case MNB_ERR_ALIGN: return "a buffer is not aligned (matmul_nbits: A and Bpacked to 16 bytes, scales and out to 2)";
-    case MNB_ERR_M_RANGE: return "m must be in [0, MNB_MAX_ROWS], tokens of the expert layer in [0, MNB_MOE_MAX_TOKENS]";
+    case MNB_ERR_M_RANGE: return "m (or the tokens of a batch) must be in [0, MNB_MAX_ROWS], tokens of the expert layer in [0, MNB_MOE_MAX_TOKENS]";
     case MNB_ERR_HIP: return "HIP runtime error (see mnb_last_hip_error)";
     case MNB_ERR_ALIAS: return "a written buffer overlaps an input or another written buffer";
     case MNB_ERR_PLAN: return "launch plan not supported";

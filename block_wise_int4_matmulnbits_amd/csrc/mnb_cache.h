@@ -1,0 +1,68 @@
+// What the kernels over the paged 8-bit cache share: its sizes, the batch of
+// sequences, and how a wave finds its sequence.  Internal header: HIP device
+// code only.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "mnb_internal.h"
+
+namespace mnb {
+
+// The batch as the device reads it.  Its numbers come from device memory and
+// are not trusted: every use below is clamped to the buffers.
+struct CacheBatch {
+    const int32_t* starts;    // [S + 1]
+    const int32_t* lengths;   // [S]
+    const int32_t* table;     // [S][max_pages]
+    int32_t S, T;
+    int32_t max_pages, page_bits;   // pages of 1 << page_bits tokens
+    int32_t pages;
+};
+
+// One sequence: its rows t0 .. t0 + n - 1 of the packed tokens and its length
+// with them; token i stands at position length - n + i.
+struct Sequence {
+    int32_t t0, n, length;
+};
+
+__device__ __forceinline__ int32_t clamp32(int32_t v, int32_t lo, int32_t hi)
+{
+    return v < lo ? lo : v > hi ? hi : v;
+}
+
+// A length beyond the page table's width keeps its value (positions count from
+// it); what reads the table checks the width.
+__device__ __forceinline__ Sequence sequence(const CacheBatch& b, int32_t s)
+{
+    Sequence q;
+    q.t0 = clamp32(b.starts[s], 0, b.T);
+    q.n = clamp32(b.starts[s + 1], q.t0, b.T) - q.t0;
+    q.length = b.lengths[s] < 0 ? 0 : b.lengths[s];
+    return q;
+}
+
+// The largest s < count with f(s) <= v for a rising f with f(0) <= v, sixty-four
+// candidates at a time (every lane gets the answer).  f is called with 0 <= s <
+// count only, so any f gives some s in range.
+template <class F>
+__device__ __forceinline__ int32_t wave_search(int32_t count, int64_t v, F f)
+{
+    const int32_t lane = threadIdx.x & 63;
+    int32_t lo = 0, n = count;
+    while (n > 1) {
+        const int32_t step = (n + 63) >> 6;
+        const int32_t at = lo + lane * step;
+        const bool below = lane * step < n && f(at) <= v;
+        const uint64_t m = __builtin_amdgcn_ballot_w64(below);
+        // Candidates below v come first; the last of them starts the range.
+        const int32_t k = m ? 63 - __builtin_clzll(m) : 0;
+        const int32_t left = n - k * step;
+        lo += k * step;
+        n = left < step ? left : step;
+    }
+    return __builtin_amdgcn_readfirstlane(lo);
+}
+
+}  // namespace mnb

@@ -201,4 +201,67 @@ struct MoeRoute {
 };
 MoeRoute moe_route(const MoeArgs& args, const MoeLayout& layout, int cus);
 
+// The paged 8-bit cache: appending (mnb_append.hip) and attention over it
+// (mnb_attention.hip).  Arguments have passed the front end's checks; tokens,
+// sequences, max_pages > 0.
+struct AppendArgs {
+    mnb_kv_cache cache;
+    mnb_kv_batch batch;
+    const void* k;
+    const void* v;
+    const void* q;           // or null
+    void* q_out;
+    int64_t k_stride, v_stride, q_stride, q_out_stride, q_heads, rot_dim;
+    const float* cos;
+    const float* sin;
+    int bf16, interleaved;
+};
+int launch_append(const AppendArgs& args, void* stream) MNB_WEAK;
+
+struct AttentionArgs {
+    mnb_kv_cache cache;
+    mnb_kv_batch batch;
+    const void* q;
+    void* out;
+    int64_t q_stride, out_stride, q_heads, max_tokens;
+    float scale;
+    int bf16;
+    void* ws;                // attention_layout().bytes
+};
+int launch_attention(const AttentionArgs& args, void* stream, int* launches) MNB_WEAK;
+
+// Workgroups of the attention's first launch, and its workspace: for each of
+// them the sums of two row tiles that it shares with others, behind their
+// maxima and weights.  Host-only arithmetic (mnb_api.cpp).
+struct AttentionLayout {
+    int workgroups;
+    size_t o, bytes;
+};
+AttentionLayout attention_layout(int64_t head_dim);
+
+// Low-rank adapters (mnb_lora.hip).  Arguments have passed the front end's
+// checks; m, N > 0.
+struct LoraArgs {
+    const void* x;           // [m][K]
+    const int32_t* ids;      // [m]
+    const void* A;           // [adapters][R][K]
+    const void* B;           // [adapters][N][R]
+    const float* scaling;    // [adapters] or null
+    const void* base;        // [m][N] or null
+    void* out;               // [m][N]
+    int64_t x_stride, base_stride, out_stride, m, K, N, R, adapters;
+    int bf16, out_bf16;
+    void* ws;                // lora_layout().bytes
+};
+int launch_lora(const LoraArgs& args, void* stream, int* launches) MNB_WEAK;
+
+// Row tiles of 16 of a workgroup, slices of K of the first launch and their
+// length, and the workspace that holds the slices' sums.  Host-only arithmetic
+// (mnb_api.cpp).
+struct LoraLayout {
+    int row_tiles, splits, k_slice;
+    size_t bytes;
+};
+LoraLayout lora_layout(int64_t m, int64_t K, int64_t R);
+
 }  // namespace mnb

@@ -32,7 +32,7 @@
 extern "C" {
 #endif
 
-#define MNB_ABI_VERSION 7
+#define MNB_ABI_VERSION 8
 
 /* Element types.  matmul_nbits takes MNB_F16 and MNB_BF16; the 8-bit product
  * also takes MNB_I8 rows and the expert layer MNB_F32 router logits. */
@@ -52,8 +52,9 @@ typedef enum {
     MNB_ERR_ALIGN = 5,    /* a buffer is not aligned as its call states
                              (matmul_nbits: A and Bpacked to 16 bytes, scales
                              and out to 2)                                   */
-    MNB_ERR_M_RANGE = 6,  /* m < 0 or m > MNB_MAX_ROWS (tokens of the expert
-                             layer: > MNB_MOE_MAX_TOKENS)                     */
+    MNB_ERR_M_RANGE = 6,  /* m (or the tokens of a batch) < 0 or > MNB_MAX_ROWS
+                             (tokens of the expert layer: >
+                             MNB_MOE_MAX_TOKENS)                              */
     MNB_ERR_HIP = 7,      /* the HIP runtime reported an error; see
                              mnb_last_hip_error()                            */
     MNB_ERR_ALIAS = 8,    /* a written buffer (out, and whatever else the call
@@ -436,6 +437,179 @@ int moe_nbits(const void* x, int x_dtype, int64_t tokens, const void* router_log
 /* Workspace bytes moe_nbits needs (0 where it would reject the sizes).
  * Host-only. */
 size_t mnb_moe_workspace(int64_t tokens, int64_t hidden, int64_t inter, int64_t experts, int top_k);
+
+/* Bounds of the 8-bit cache and of the attention over it. */
+#define MNB_KV_MAX_SEQUENCES 65536
+#define MNB_KV_MAX_HEADS 256              /* key heads */
+#define MNB_KV_MAX_GROUP 64               /* query heads of a key head */
+#define MNB_KV_MAX_LENGTH ((int64_t)1 << 30)   /* tokens that a row of the page table names */
+
+/*
+ * A paged cache of keys and values in 8-bit integers.  A page holds page_size
+ * tokens of every head; page p and head h have one scale for the keys and one
+ * for the values.  An integer q stands for (q + 1/2) * scale, and under
+ *
+ *   scale = 2^e,  e = min { e >= -126 : -128 <= x / 2^e < 128 for every value x },
+ *   q = floor(x / 2^e)
+ *
+ * (scale 0 and q 0 where every value is 0) no value is off by more than half a
+ * step, and a page whose scale grows keeps its tokens by an arithmetic shift,
+ * which is the floor again: the page's bits depend on the values that it holds,
+ * not on how many calls brought them.
+ */
+typedef struct {
+    int64_t pages;        /* 0 .. 2^31 - 1                                              */
+    int64_t page_size;    /* P: 16, 32, 64, 128 or 256 tokens                           */
+    int64_t kv_heads;     /* 1 .. MNB_KV_MAX_HEADS                                      */
+    int64_t head_dim;     /* D: 64, 128 or 256                                          */
+    int8_t* k_pages;      /* device, [pages][kv_heads][P][D]; 16-byte aligned           */
+    int8_t* v_pages;      /* device, [pages][kv_heads][D][P] (tokens last); 16-byte aligned */
+    float* k_scales;      /* device, [pages][kv_heads]; 4-byte aligned                  */
+    float* v_scales;      /* device, [pages][kv_heads]; 4-byte aligned                  */
+} mnb_kv_cache;
+
+/*
+ * A batch of sequences.  Their new tokens are packed: sequence s has rows
+ * starts[s] .. starts[s + 1] - 1 (none, one or many), lengths[s] counts its
+ * tokens with the new ones, which are its last, and page_table[s] names the
+ * pages of its tokens 0 .. P - 1, P .. 2P - 1, and so on.  starts begins at 0
+ * and does not fall; rows behind starts[sequences] belong to no sequence and
+ * are neither read nor written.
+ *
+ * These numbers are read on the device when the work runs (a captured graph
+ * reads them at each replay), so no call can refuse them.  Wrong ones read and
+ * write nothing outside the buffers: a page outside 0 .. pages - 1, or a
+ * position that the page table does not reach, holds no token (nothing is
+ * stored there, and attention passes over it); a token that would stand before
+ * position 0 (more rows than lengths[s]) is not stored and sees no key.
+ */
+typedef struct {
+    int64_t sequences;            /* 0 .. MNB_KV_MAX_SEQUENCES                             */
+    int64_t tokens;               /* rows of the packed buffers, 0 .. MNB_MAX_ROWS         */
+    int64_t max_pages;            /* width of the page table; max_pages * P <= MNB_KV_MAX_LENGTH */
+    const int32_t* starts;        /* device, [sequences + 1]; 4-byte aligned               */
+    const int32_t* lengths;       /* device, [sequences]; 4-byte aligned                   */
+    const int32_t* page_table;    /* device, [sequences][max_pages]; 4-byte aligned        */
+} mnb_kv_batch;
+
+/*
+ * append_kv_int8 -- the keys and values of a batch's new tokens into the cache,
+ * the position rotation applied on the way, one launch on `stream`.
+ *
+ *   dtype          MNB_F16 or MNB_BF16: of k, v, q and q_out.
+ *   k, v           device, [tokens][kv_heads][D], k_stride and v_stride elements
+ *                  from one token to the next (at least kv_heads * D, a multiple
+ *                  of 8); 16-byte aligned.  They may be parts of one buffer.
+ *   q, q_out       device, [tokens][q_heads][D], likewise: the queries, and where
+ *                  the rotated ones go (q_out == q with equal strides rotates in
+ *                  place); both NULL with q_heads 0 for none.
+ *   cos, sin       device, [table_rows][rot_dim / 2] fp32, 16-byte aligned, row =
+ *                  position; table_rows >= max_pages * P.  NULL with rot_dim 0:
+ *                  no rotation (q_out gets q).
+ *   rot_dim        0 .. D, a multiple of 16: the first elements of a head that are
+ *                  rotated.
+ *   interleaved    0: element i and i + rot_dim / 2 are a pair; nonzero: elements
+ *                  2 i and 2 i + 1.  A pair (a, b) becomes (a c - b s, b c + a s).
+ *
+ * A page whose first token is among the new ones holds nothing else; any other
+ * page must hold what these calls stored there for its earlier tokens.  The
+ * pages that one call stores into must each belong to one sequence.  Bytes of a
+ * page behind the sequence's last token are left as they are.  Rows of q_out
+ * whose token has no position within the page table are left as they are.
+ * Numerics: rotated values in 64 bits, quantised from there; q_out rounded once
+ * (RNE).  A value that is not finite makes its page's scale NaN, until the page
+ * is begun anew.  q_out and the cache must not overlap the inputs or each
+ * other, but for q_out == q.  Asynchronous; allocates nothing.
+ */
+int append_kv_int8(const mnb_kv_cache* cache, const mnb_kv_batch* batch, int dtype, const void* k, int64_t k_stride,
+                   const void* v, int64_t v_stride, const void* q, int64_t q_stride, void* q_out,
+                   int64_t q_out_stride, int64_t q_heads, const float* cos, const float* sin, int64_t rot_dim,
+                   int64_t table_rows, int interleaved, void* stream);
+
+/*
+ * attention_int8 -- causal attention of a batch's new tokens over the cache:
+ *
+ *   out[t][i] = sum_j w[j] v[j][h],   w = softmax_j(scale * q[t][i] . k[j][h]),
+ *
+ * over the positions j of t's sequence from 0 to t's own, with key head h =
+ * i / (q_heads / kv_heads).  The new tokens' own keys are read from the cache
+ * (append them first).
+ *
+ *   q              device, [tokens][q_heads][D], fp16 or bf16 per dtype, q_stride
+ *                  elements from one token to the next (at least q_heads * D, a
+ *                  multiple of 8); 16-byte aligned.
+ *   q_heads        a multiple of kv_heads, at most MNB_KV_MAX_GROUP times as many.
+ *   scale          finite.
+ *   out            device, like q, same type, out_stride; 16-byte aligned.
+ *   max_tokens     no sequence has more new tokens than this (0: not known).
+ *                  It only chooses kernels: results hold for any value.
+ *   workspace      device, mnb_attention_workspace(...) bytes at least, 16-byte
+ *                  aligned; rules as for matmul_int8.
+ *
+ * Rows that see no key (an empty sequence, or no usable page) are zero.
+ * Numerics: scores of the integers exact but for what lies below 2^-22 of a
+ * query's largest element, softmax with the running maximum and sum in fp32,
+ * weights held in 16 bits against the largest of 64 keys, sums in fp32, one
+ * rounding (RNE).  A query that is not finite, or a NaN scale of a page that a
+ * row sees, gives NaN in that row.  The order of fp32 sums depends on the
+ * lengths of the whole batch; equal calls give equal bits.  out and workspace
+ * must not overlap the inputs or each other.  Asynchronous; allocates nothing;
+ * two launches.
+ */
+int attention_int8(const mnb_kv_cache* cache, const mnb_kv_batch* batch, int dtype, const void* q, int64_t q_stride,
+                   int64_t q_heads, float scale, void* out, int64_t out_stride, int64_t max_tokens, void* workspace,
+                   size_t workspace_bytes, void* stream);
+
+/* Workspace bytes attention_int8 needs (0 for none, or where it would reject
+ * the sizes).  Host-only. */
+size_t mnb_attention_workspace(int64_t tokens, int64_t q_heads, int64_t kv_heads, int64_t head_dim);
+
+/* Bounds of the adapters. */
+#define MNB_LORA_MAX_RANK 256
+#define MNB_LORA_MAX_ADAPTERS 65536
+
+/*
+ * matmul_lora -- low-rank adapters of many requests at once, beside a shared
+ * projection whose result is `base`:
+ *
+ *   out[r] = base[r] + scaling[a] * B[a] (A[a] x[r]),   a = ids[r]
+ *
+ *   x             device, [m][K] fp16 or bf16 per x_dtype, x_stride elements from
+ *                 one row to the next (at least K, a multiple of 8); 16-byte
+ *                 aligned.
+ *   m, K, N       0 <= m <= MNB_MAX_ROWS; K a multiple of 16, 0 <= K <= MNB_MAX_K;
+ *                 0 <= N <= MNB_MAX_N_INT8.
+ *   rank          R: a multiple of 8, 8 .. MNB_LORA_MAX_RANK (an adapter of a
+ *                 smaller one is filled up with zeros).
+ *   adapters      0 .. MNB_LORA_MAX_ADAPTERS.
+ *   ids           device, [m] int32; 4-byte aligned.  A row whose number is not
+ *                 one of 0 .. adapters - 1 has no adapter: it gets its base.
+ *   A, B          device, [adapters][R][K] and [adapters][N][R], x's type;
+ *                 16-byte aligned.
+ *   scaling       device, [adapters] fp32, 4-byte aligned; NULL for 1.
+ *   base, out     device, [m][N], fp16 or bf16 per out_dtype, base_stride and
+ *                 out_stride elements from one row to the next (at least N);
+ *                 2-byte aligned.  base may be NULL (zeros), or out itself with
+ *                 equal strides (the adapters are added in place).
+ *   workspace     device, mnb_lora_workspace(...) bytes at least, 16-byte aligned;
+ *                 rules as for matmul_int8.
+ *
+ * Numerics: A x summed in fp32; scaled in fp32; held for the second product in
+ * two pieces of x's type (16 bits of a bf16 value, 21 of an fp16 one, whose row
+ * is under a power of two of its own); B's sums and the base in fp32, one
+ * rounding (RNE).  A row that is not finite spoils itself alone.  A row's bits
+ * depend on its own values and adapter and on (m, K, R).  out and workspace
+ * must not overlap the inputs or each other, but for out == base.
+ * Asynchronous; allocates nothing; two launches.
+ */
+int matmul_lora(const void* x, int x_dtype, int64_t x_stride, int64_t m, int64_t K, int64_t N, int64_t rank,
+                int64_t adapters, const int32_t* ids, const void* A, const void* B, const float* scaling,
+                const void* base, int64_t base_stride, void* out, int64_t out_stride, int out_dtype, void* workspace,
+                size_t workspace_bytes, void* stream);
+
+/* Workspace bytes matmul_lora needs (0 for none, or where it would reject the
+ * sizes).  Host-only. */
+size_t mnb_lora_workspace(int64_t m, int64_t K, int64_t N, int64_t rank, int64_t adapters);
 
 /*
  * Environment: MNB_LOG set to anything but "0" (read once per process)

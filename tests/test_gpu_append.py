@@ -1,0 +1,277 @@
+"""append_kv_int8 against the cache's definition in 64 bits: every integer,
+scale and untouched byte has to be equal."""
+import pytest
+import torch
+
+import block_wise_int4_matmulnbits_amd as mnb
+from tests import gpu_util as G
+from tests import kv_ref as R
+
+pytestmark = pytest.mark.gpu
+
+F16, BF16 = torch.float16, torch.bfloat16
+
+
+def _tables(rows, rot, seed=3):
+    g = torch.Generator().manual_seed(seed)
+    angle = torch.rand(rows, rot // 2, generator=g, dtype=torch.float64) * 6.3
+    return angle.cos().float(), angle.sin().float()
+
+
+def _values(T, hq, heads, D, dtype, seed, spread=True):
+    g = torch.Generator().manual_seed(seed)
+    x = torch.randn(T, hq + 2 * heads, D, generator=g)
+    if spread:   # tokens of very different size: scales that grow within a page
+        x = x * torch.exp2(torch.randint(-6, 7, (T, 1, 1), generator=g).float())
+    x = x.to(dtype)
+    return x[:, :hq], x[:, hq:hq + heads], x[:, hq + heads:]
+
+
+def _bits(t):
+    return t.contiguous().view(torch.int32 if t.element_size() == 4 else torch.int16 if t.element_size() == 2 else torch.int8)
+
+
+def _same(got, want, name):
+    a, b = got.cpu(), want
+    if a.is_floating_point():
+        assert bool((torch.isnan(a) == torch.isnan(b)).all()), name
+        a, b = torch.nan_to_num(a), torch.nan_to_num(b)
+    assert torch.equal(a, b), "%s: %d of %d differ" % (name, int((a != b).sum()), a.numel())
+
+
+def _run(b, q, k, v, cos, sin, interleaved=False, stream=None):
+    """The call on copies of b's cache; b is updated by the reference; both are
+    compared.  q, k and v are parts of one buffer on the GPU."""
+    T, hq, heads = b.T, q.shape[1], b.heads
+    fused = torch.cat((q, k, v), dim=1).cuda()
+    gq, gk, gv = fused[:, :hq], fused[:, hq:hq + heads], fused[:, hq + heads:]
+    args = b.cuda()
+    q_out = torch.full((T, hq, b.D), 7.0, dtype=q.dtype, device="cuda")
+    mnb.append_kv_int8(gk, gv, None if cos is None else cos.cuda(), None if sin is None else sin.cuda(), *args,
+                       q=gq if hq else None, q_out=q_out if hq else None, interleaved=interleaved, stream=stream)
+    torch.cuda.synchronize()
+    want = R.append(b, k, v, cos, sin, q if hq else None, interleaved)
+    for got, ref, name in zip(args[3:], b.cache(), ("k_pages", "v_pages", "k_scales", "v_scales")):
+        _same(got, ref, name)
+    if hq:
+        rows = torch.isnan(want).all(dim=2).all(dim=1)
+        exact = _round(want, q.dtype)
+        got = q_out.cpu()
+        assert bool((got[rows] == 7.0).all())
+        _same(_bits(got[~rows]), _bits(exact[~rows]), "q_out")
+    return args
+
+
+def _round(x, dtype):
+    """64 bits to dtype, rounded once (to nearest even): numpy rounds fp64 to fp16
+    so; to bf16 by hand."""
+    import numpy as np
+    if dtype == F16:
+        return torch.from_numpy(x.numpy().astype(np.float16))
+    y = torch.nan_to_num(x)
+    m, e = torch.frexp(y)
+    e = e.clamp(min=-125)
+    step = torch.ldexp(torch.ones_like(y), e - 8)
+    r = torch.round(y / step) * step      # torch.round: ties to even
+    out = r.to(torch.float32).to(BF16)
+    return out
+
+
+SHAPES = [
+    # new, before, P, query heads, heads, D, rot
+    ([1], [0], 16, 2, 1, 64, 64),
+    ([1], [17], 16, 4, 2, 64, 32),
+    ([1], [1000], 64, 32, 8, 128, 128),
+    ([1, 1, 1, 1, 1], [0, 15, 16, 31, 63], 32, 4, 2, 128, 64),
+    ([3, 0, 1, 5, 0, 2], [14, 9, 0, 62, 0, 127], 16, 3, 3, 64, 16),
+    ([200, 1, 77], [0, 300, 13], 64, 6, 2, 128, 128),
+    ([130, 0, 259], [127, 5, 1], 128, 2, 2, 256, 240),
+    ([300], [250], 256, 1, 1, 64, 0),
+    ([65], [0], 64, 16, 1, 256, 256),
+    ([33, 31, 32], [0, 1, 32], 32, 0, 5, 64, 48),
+]
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16], ids=["f16", "bf16"])
+@pytest.mark.parametrize("interleaved", [False, True], ids=["halves", "neighbours"])
+@pytest.mark.parametrize("shape", SHAPES, ids=[str(i) for i in range(len(SHAPES))])
+def test_integers(shape, interleaved, dtype):
+    G.require_gpu()
+    new, before, P, hq, heads, D, rot = shape
+    b = R.Batch(new, before, P, heads, D, seed=len(new) + P)
+    q, k, v = _values(b.T, hq, heads, D, dtype, 11 + P)
+    cos, sin = _tables(b.width * P, rot) if rot else (None, None)
+    _run(b, q, k, v, cos, sin, interleaved)
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16], ids=["f16", "bf16"])
+def test_pieces_give_the_same_page(dtype):
+    """A prompt at once, or in pieces that end inside pages, or token by token."""
+    G.require_gpu()
+    P, heads, D, n = 32, 2, 64, 90
+    q, k, v = _values(n, 2, heads, D, dtype, 5)
+    cos, sin = (t.cuda() for t in _tables(128, D))
+    found = []
+    for cuts in ([0, n], [0, 7, 8, 40, 41, 64, n], list(range(n + 1))):
+        b = R.Batch([n], [0], P, heads, D, seed=1, width=4)
+        args = b.cuda()
+        for a, z in zip(cuts, cuts[1:]):
+            args[0] = torch.tensor([0, z - a], dtype=torch.int32, device="cuda")
+            args[1] = torch.tensor([z], dtype=torch.int32, device="cuda")
+            mnb.append_kv_int8(k[a:z].cuda(), v[a:z].cuda(), cos, sin, *args)
+        torch.cuda.synchronize()
+        found.append([t.cpu() for t in args[3:]])
+    for other in found[1:]:
+        for x, y in zip(found[0], other):
+            assert torch.equal(x, y)
+    # and each value is within half a step of the rotated one
+    want = R.Batch([n], [0], P, heads, D, seed=1, width=4)
+    R.append(want, k, v, cos.cpu(), sin.cpu())
+    for x, y in zip(found[0], want.cache()):
+        assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16], ids=["f16", "bf16"])
+def test_borders_of_the_range(dtype):
+    """Values at powers of two and one step around them, of both signs; zeros;
+    the smallest and largest of the type."""
+    G.require_gpu()
+    info = torch.finfo(dtype)
+    P, heads, D = 16, 1, 64
+    edges = []
+    for e in (-3, 0, 6, 7):
+        one = 2.0 ** e
+        edges += [one, -one, one * (1 - info.eps / 2), -one * (1 - info.eps / 2), one * (1 + info.eps), -one * (1 + info.eps)]
+    edges += [info.smallest_normal * info.eps, -info.smallest_normal * info.eps, info.smallest_normal, -info.smallest_normal,
+              info.max, info.min]
+    for i, e in enumerate(edges):
+        b = R.Batch([2], [0], P, heads, D, seed=i)
+        x = torch.zeros(2, heads, D, dtype=torch.float64)
+        x[0, 0, 3] = e
+        x[1, 0, 5] = e / 128
+        x[1, 0, 7] = -e / 256
+        x = x.to(dtype)
+        _run(b, x[:, :0], x, x.flip(2), None, None)
+    b = R.Batch([5], [0], P, heads, D, seed=99)
+    z = torch.zeros(5, heads, D, dtype=dtype)
+    _run(b, z[:, :0], z, -z, None, None)
+    assert float(b.k_scales[int(b.table[0, 0]), 0]) == 0.0
+
+
+def test_zeros_then_values_and_growth():
+    """A page of zeros that gets values; a page whose scale grows past seven bits."""
+    G.require_gpu()
+    P, heads, D = 64, 2, 64
+    for sizes in ([0, 0, 1e-3], [1e-3, 1, 300], [0, 1e-4, 0, 60000]):
+        b = R.Batch([0], [0], P, heads, D, width=1, spare=3)
+        b.table[0, 0] = 1
+        args = b.cuda()
+        at = 0
+        for size in sizes:
+            n = 3
+            at += n
+            x = (torch.randn(n, heads, D) * size).clamp(-6e4, 6e4).to(F16)
+            b.T, b.starts[1], b.lengths[0] = n, n, at
+            dev = [b.starts.cuda(), b.lengths.cuda(), b.table.cuda()] + args[3:]
+            mnb.append_kv_int8(x.cuda(), x.flip(0).cuda(), None, None, *dev)
+            torch.cuda.synchronize()
+            R.append(b, x, x.flip(0), None, None)
+            for got, ref, name in zip(args[3:], b.cache(), ("k_pages", "v_pages", "k_scales", "v_scales")):
+                _same(got, ref, name)
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+def test_values_that_are_not_finite(bad):
+    """They spoil their page and head, also for what comes later, until the page
+    is begun anew."""
+    G.require_gpu()
+    P, heads, D = 16, 3, 64
+    b = R.Batch([20], [3], P, heads, D, seed=4)
+    q, k, v = _values(20, 0, heads, D, BF16, 8)
+    k[4, 1, 9] = bad
+    v[15, 2, 0] = bad
+    args = _run(b, q, k, v, None, None)
+    assert int(torch.isnan(args[5]).sum()) == 1 and int(torch.isnan(args[6]).sum()) == 1
+    b.new, b.before = [2], [23]
+    b.starts = torch.tensor([0, 2], dtype=torch.int32)
+    b.lengths = torch.tensor([25], dtype=torch.int32)
+    b.T = 2
+    q, k, v = _values(2, 0, heads, D, BF16, 9)
+    _run(b, q, k, v, None, None)
+    b.starts, b.lengths = torch.tensor([0, 2], dtype=torch.int32), torch.tensor([2], dtype=torch.int32)
+    _run(b, q, k, v, None, None)
+    assert not bool(torch.isnan(b.k_scales[int(b.table[0, 0])]).any())
+
+
+def test_tokens_without_a_place():
+    """Rows behind the last sequence, tokens before position 0 or behind the page
+    table, pages that are none: nothing is stored and no other byte changes."""
+    G.require_gpu()
+    P, heads, D = 16, 2, 64
+    b = R.Batch([5, 4, 6, 3], [0, 30, 20, 10], P, heads, D, seed=6, extra=9)
+    b.lengths[0] = 3                       # two tokens before position 0
+    b.lengths[1] = b.width * P + 2         # the last two behind the table
+    b.table[2, 1] = b.pages                # one past the last page
+    b.table[3, 0] = -1
+    q, k, v = _values(b.T, 4, heads, D, F16, 10)
+    cos, sin = _tables(b.width * P, 32)
+    _run(b, q, k, v, cos, sin)
+    # lengths and starts without sense: nothing outside the buffers is touched
+    b = R.Batch([5, 4], [0, 30], P, heads, D, seed=6)
+    for lengths, starts in (([-5, 2 ** 31 - 1], [0, 5, 9]), ([40, 40], [0, 10 ** 6, 5]), ([0, 0], [-3, 4, 9])):
+        args = b.cuda()
+        args[0] = torch.tensor(starts, dtype=torch.int32, device="cuda")
+        args[1] = torch.tensor(lengths, dtype=torch.int32, device="cuda")
+        q, k, v = _values(9, 2, heads, D, F16, 3)
+        guard = [torch.cat((t.reshape(-1), t.new_ones(64))) for t in args[3:]]
+        views = [g[:-64].view(t.shape) for g, t in zip(guard, args[3:])]
+        tails = [g[-64:].clone() for g in guard]
+        mnb.append_kv_int8(k.contiguous().cuda(), v.contiguous().cuda(), None, None, *args[:3], *views,
+                           q=q.contiguous().cuda(), q_out=torch.empty(9, 2, D, dtype=F16, device="cuda"))
+        torch.cuda.synchronize()
+        for g, t in zip(guard, tails):
+            assert torch.equal(g[-64:], t)
+
+
+def test_in_place_and_streams():
+    """q_out is q within the fused buffer; on another stream; a captured call
+    replayed with other lengths."""
+    G.require_gpu()
+    P, hq, heads, D = 32, 4, 2, 128
+    new, before = [3, 1, 9], [0, 40, 31]
+    b = R.Batch(new, before, P, heads, D, seed=2, width=4)
+    q, k, v = _values(b.T, hq, heads, D, BF16, 21)
+    cos, sin = _tables(b.width * P, 128)
+    _run(b, q, k, v, cos, sin, stream=torch.cuda.Stream())
+    b = R.Batch(new, before, P, heads, D, seed=2, width=4)
+    fused = torch.cat((q, k, v), dim=1).cuda()
+    args = b.cuda()
+    gc, gs = cos.cuda(), sin.cuda()
+    keep = fused.clone()
+
+    def call():
+        mnb.append_kv_int8(fused[:, hq:hq + heads], fused[:, hq + heads:], gc, gs, *args, q=fused[:, :hq], q_out=fused[:, :hq])
+
+    call()
+    torch.cuda.synchronize()
+    want = R.append(b, k, v, cos, sin, q)
+    assert torch.equal(_bits(fused[:, :hq].cpu()), _bits(_round(want, BF16)))
+    assert torch.equal(fused[:, hq:], keep[:, hq:])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    for lengths in ([3, 41, 40], [12, 64, 128], [100, 2, 9]):
+        b2 = R.Batch(new, before, P, heads, D, seed=2, width=4)
+        b2.table[:] = torch.arange(12).reshape(3, 4) % b2.pages
+        b2.table[2] = torch.tensor([-1, b2.pages, -1, -1])
+        b2.lengths[:] = torch.tensor(lengths)
+        b2.table[0], b2.table[1] = torch.tensor([0, 1, 2, 3]), torch.tensor([4, 5, 6, -1])
+        fused.copy_(keep)
+        for dst, src in zip(args, b2.index() + b2.cache()):
+            dst.copy_(src)
+        graph.replay()
+        torch.cuda.synchronize()
+        want = R.append(b2, k, v, cos, sin, q)
+        for got, ref, name in zip(args[3:], b2.cache(), ("k_pages", "v_pages", "k_scales", "v_scales")):
+            _same(got, ref, name)
+        assert torch.equal(_bits(fused[:, :hq].cpu()), _bits(_round(want, BF16)))

@@ -1,0 +1,234 @@
+"""attention_int8 against its formula in 64 bits."""
+import pytest
+import torch
+
+import block_wise_int4_matmulnbits_amd as mnb
+from tests import gpu_util as G
+from tests import kv_ref as R
+
+pytestmark = pytest.mark.gpu
+
+F16, BF16 = torch.float16, torch.bfloat16
+
+
+def _queries(T, hq, D, dtype, seed, size=1.0):
+    g = torch.Generator().manual_seed(seed)
+    x = torch.randn(T, hq, D, generator=g)
+    channels = torch.rand(hq, D, generator=g)
+    return (x * torch.where(channels > 0.97, 8.0, 1.0) * size).to(dtype)
+
+
+def _call(b, q, scale=None, out=None, **kw):
+    args = b.cuda()
+    if out is None:
+        out = torch.full(q.shape, 9.0, dtype=q.dtype, device="cuda")
+    got = mnb.attention_int8(q.cuda(), *args, out, scale=scale, **kw)
+    torch.cuda.synchronize()
+    assert got is out
+    return out.cpu()
+
+
+def _check(b, q, scale=None, **kw):
+    got = _call(b, q, scale, **kw)
+    want, tol = R.attention(b, q, q.shape[2] ** -0.5 if scale is None else scale)
+    used = int(b.starts[-1])
+    R.check_rows(got[:used], want[:used], tol[:used], q.dtype)
+    assert bool((got[used:] == 9.0).all())
+    return got
+
+
+SHAPES = [
+    # new, before, P, query heads, heads, D
+    ([1], [0], 16, 1, 1, 64),
+    ([1], [62], 64, 4, 1, 128),
+    ([1], [63], 64, 8, 2, 128),
+    ([1], [64], 64, 8, 2, 128),
+    ([1], [2048], 64, 8, 2, 128),
+    ([1], [1500], 16, 5, 1, 256),
+    ([1, 1, 1, 1, 1, 1], [0, 1, 15, 16, 200, 999], 16, 6, 3, 64),
+    ([1, 0, 1, 0], [40, 40, 0, 0], 32, 2, 2, 128),
+    ([3, 1, 5, 0, 2], [0, 700, 61, 13, 126], 32, 8, 2, 128),
+    ([7], [250], 128, 16, 1, 64),
+    ([2, 9], [10, 300], 256, 24, 2, 128),
+    ([40, 1, 17], [0, 100, 33], 64, 4, 2, 128),
+    ([130], [70], 16, 3, 3, 64),
+    ([33, 65], [500, 0], 32, 8, 1, 256),
+    ([300], [0], 64, 4, 1, 128),
+]
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16], ids=["f16", "bf16"])
+@pytest.mark.parametrize("shape", SHAPES, ids=[str(i) for i in range(len(SHAPES))])
+def test_rows(shape, dtype):
+    G.require_gpu()
+    new, before, P, hq, heads, D = shape
+    b = R.Batch(new, before, P, heads, D, seed=P + D + len(new), extra=3)
+    _check(b, _queries(b.T, hq, D, dtype, 7 * P + hq), max_tokens=max(new))
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_long(D):
+    """A length that many workgroups share, joined in the order of the keys."""
+    G.require_gpu()
+    b = R.Batch([1, 2], [33333, 4099], 64, 1, D, seed=D)
+    _check(b, _queries(b.T, 4, D, BF16, D))
+
+
+def test_large_scores():
+    """Weights that all but one key lose, and the scale's sign."""
+    G.require_gpu()
+    for scale in (2.0, -0.5, 0.0, 1e-3):
+        for dtype in (F16, BF16):
+            b = R.Batch([2, 1], [90, 700], 16, 2, 64, seed=5)
+            b.k_scales = torch.full_like(b.k_scales, 2.0 ** -4)
+            _check(b, _queries(b.T, 4, 64, dtype, 3), scale=scale)
+
+
+def test_scales_far_apart():
+    """Pages whose scales differ by up to 2^60, pages of zeros, zero queries."""
+    G.require_gpu()
+    for P in (16, 64):
+        b = R.Batch([1, 2], [190, 333], P, 2, 128, seed=8)
+        g = torch.Generator().manual_seed(1)
+        b.v_scales = torch.exp2(torch.randint(-40, 20, b.v_scales.shape, generator=g).float())
+        b.k_scales = torch.exp2(torch.randint(-30, -5, b.k_scales.shape, generator=g).float())
+        b.v_scales[int(b.table[0, 0])] = 0
+        b.k_scales[int(b.table[1, 1])] = 0
+        q = _queries(b.T, 4, 128, BF16, 4)
+        q[1] = 0
+        _check(b, q)
+        b.v_scales[:] = 0
+        got = _call(b, q)
+        assert bool((got == 0).all())
+
+
+def test_sizes_of_queries():
+    """Queries at both ends of their type's range."""
+    G.require_gpu()
+    for dtype, sizes in ((F16, (6e-8, 1e-4, 3000.0)), (BF16, (1e-38, 1e-10, 1e15))):
+        for size in sizes:
+            b = R.Batch([1, 1], [100, 7], 32, 1, 64, seed=3)
+            b.k_scales = torch.full_like(b.k_scales, 2.0 ** -10)
+            q = _queries(2, 2, 64, F16 if dtype is F16 else torch.float32, 6, size if dtype is BF16 else 1.0)
+            q = (q * size).to(dtype) if dtype is F16 else q.to(dtype)
+            _check(b, q, scale=min(1.0, 0.1 / size))
+
+
+def test_not_finite():
+    """A query that is not finite spoils its row; a NaN scale the rows that see a
+    token of its page; keys behind a row's position do not matter."""
+    G.require_gpu()
+    for P in (16, 64):
+        b = R.Batch([4, 1], [61, 40], P, 2, 64, seed=2)
+        q = _queries(b.T, 4, 64, F16, 1)
+        clean = _call(b, q)
+        for bad in (float("nan"), float("inf")):
+            q2 = q.clone()
+            q2[2, 3, 5] = bad
+            got = _call(b, q2)
+            assert bool(torch.isnan(got[2, 3]).all())
+            got[2, 3] = clean[2, 3]
+            assert torch.equal(got, clean)
+        # the last page holds positions 64 and up: the last row alone sees it
+        for scales in (b.k_scales, b.v_scales):
+            page = int(b.table[0, 64 // P])
+            was = scales[page, 1].clone()
+            scales[page, 1] = float("nan")
+            got = _call(b, q)
+            assert bool(torch.isnan(got[3, 2:]).all())
+            got[3, 2:] = clean[3, 2:]
+            assert torch.equal(got, clean)
+            scales[page, 1] = was
+        # bytes and scales behind the last token: pages of the table that no token has reached
+        wide = R.Batch([4, 1], [61, 40], P, 2, 64, seed=2, width=9, spare=2)
+        for s in range(2):
+            for i in range(-(-int(wide.lengths[s]) // P), 9):
+                wide.table[s, i] = wide.pages - 1
+        used = {int(p) for s in range(2) for p in wide.table[s, :-(-int(wide.lengths[s]) // P)]}
+        free = [p for p in range(wide.pages) if p not in used]
+        wide.table[wide.table == wide.pages - 1] = free[-1]
+        if wide.pages - 1 in used:
+            for s in range(2):
+                for i in range(-(-int(wide.lengths[s]) // P)):
+                    if wide.table[s, i] == free[-1]:
+                        wide.table[s, i] = wide.pages - 1
+        wide.k_scales[free], wide.v_scales[free] = float("nan"), float("inf")
+        want, tol = R.attention(wide, q, 64 ** -0.5)
+        R.check_rows(_call(wide, q), want, tol, F16)
+
+
+def test_pages_and_lengths_without_sense():
+    G.require_gpu()
+    P = 16
+    b = R.Batch([2, 3, 1, 2], [100, 50, 0, 30], P, 2, 64, seed=9, extra=2)
+    b.table[0, 2] = -1                    # passed over
+    b.table[1, 0] = b.pages
+    b.table[1, 3] = 2 ** 31 - 1
+    b.table[3] = -5                       # no usable page: rows of zeros
+    b.lengths[2] = 0                      # its token stands before position 0
+    q = _queries(b.T, 4, 64, BF16, 2)
+    got = _check(b, q)
+    assert bool((got[5] == 0).all()) and bool((got[6:8] == 0).all())
+    b = R.Batch([2, 3], [100, 50], P, 2, 64, seed=9)
+    b.lengths[0] = b.width * P + 50       # behind the table: what it names is read
+    _check(b, _queries(b.T, 4, 64, F16, 3))
+    q = _queries(b.T, 4, 64, F16, 3)
+    for lengths, starts in (([-3, 2 ** 31 - 1], [0, 2, 5]), ([90, 50], [0, 10 ** 6, 1]), ([0, 0], [-9, 3, 4])):
+        b.lengths[:], b.starts[:] = torch.tensor(lengths), torch.tensor(starts)
+        _call(b, q)
+
+
+def test_strides_streams_and_workspaces():
+    """Rows further apart than their width, in both directions; raw stream
+    handles; a workspace of the caller's; equal calls give equal bits."""
+    G.require_gpu()
+    b = R.Batch([1, 3, 1], [700, 20, 64], 32, 2, 128, seed=3)
+    q = _queries(b.T, 8, 128, BF16, 9)
+    want = _check(b, q)
+    args = b.cuda()
+    big = torch.full((b.T, 20, 128), 5.0, dtype=BF16, device="cuda")
+    big[:, 3:11] = q.cuda()
+    ws = torch.empty(mnb.mnb_attention_workspace(b.T, 8, 2, 128), dtype=torch.uint8, device="cuda")
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for stream in (None, side, side.cuda_stream):
+        big[:, 11:19] = 5.0
+        torch.cuda.synchronize()
+        mnb.attention_int8(big[:, 3:11], *args, big[:, 11:19], workspace=ws, stream=stream)
+        torch.cuda.synchronize()
+        assert torch.equal(big[:, 11:19].cpu(), want)
+        assert bool((big[:, :3] == 5.0).all()) and bool((big[:, 19:] == 5.0).all())
+        assert torch.equal(big[:, 3:11].cpu(), q)
+
+
+def test_captured():
+    """A captured call replayed with other lengths, pages and queries, eager calls
+    between the replays."""
+    G.require_gpu()
+    new = [1, 2, 1, 0]
+    sets = []
+    for i, before in enumerate(([500, 3, 60, 9], [0, 0, 0, 0], [1, 2500, 64, 0])):
+        b = R.Batch(new, before, 16, 2, 64, seed=i, width=160, spare=2)
+        pages = 400
+        for name in ("k_pages", "v_pages", "k_scales", "v_scales"):
+            t = getattr(b, name)
+            setattr(b, name, torch.cat((t, t.new_zeros((pages - t.shape[0],) + t.shape[1:]))))
+        b.pages = pages
+        sets.append((b, _queries(b.T, 6, 64, F16, i)))
+    args, q = sets[0][0].cuda(), sets[0][1].cuda()
+    out = torch.empty_like(q)
+    mnb.attention_int8(q, *args, out)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        mnb.attention_int8(q, *args, out)
+    for i in (1, 2, 0, 2):
+        b, x = sets[i]
+        for dst, src in zip(args, b.index() + b.cache()):
+            dst.copy_(src)
+        q.copy_(x)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out.cpu(), _call(b, x))
+        want, tol = R.attention(b, x, 64 ** -0.5)
+        R.check_rows(out.cpu(), want, tol, F16)
