@@ -33,7 +33,7 @@ MNB_MOE_MAX_WIDTH = 65536
 MNB_KV_MAX_SEQUENCES = 65536
 MNB_KV_MAX_HEADS = 256
 MNB_KV_MAX_GROUP = 64
-MNB_KV_MAX_LENGTH = 1 << 30
+MNB_KV_MAX_LENGTH = 1 << 24
 MNB_LORA_MAX_RANK = 256
 MNB_LORA_MAX_ADAPTERS = 65536
 MNB_LAYOUT_NATURAL = 0   # stored weight layouts (mnb_repack_weights)

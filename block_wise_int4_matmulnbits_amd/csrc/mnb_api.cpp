@@ -644,8 +644,7 @@ namespace mnb {
 AttentionLayout attention_layout(int64_t head_dim)
 {
     AttentionLayout l;
-    l.workgroups = 512;
-    const size_t tiles = 2 * (size_t)l.workgroups;
+    const size_t tiles = 2 * (size_t)kAttentionWorkgroups;
     l.o = tiles * 16 * 2 * 4;
     l.bytes = l.o + tiles * 16 * (size_t)head_dim * 4;
     return l;

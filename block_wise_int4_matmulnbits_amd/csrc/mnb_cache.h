@@ -32,6 +32,13 @@ __device__ __forceinline__ int32_t clamp32(int32_t v, int32_t lo, int32_t hi)
     return v < lo ? lo : v > hi ? hi : v;
 }
 
+// A value that every lane of the wave holds alike, in scalar registers.
+__device__ __forceinline__ int32_t uniform(int32_t v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ __forceinline__ int64_t uniform64(int64_t v)
+{
+    return (int64_t)((uint64_t)(uint32_t)uniform((int32_t)(v >> 32)) << 32 | (uint32_t)uniform((int32_t)v));
+}
+
 // A length beyond the page table's width keeps its value (positions count from
 // it); what reads the table checks the width.
 __device__ __forceinline__ Sequence sequence(const CacheBatch& b, int32_t s)
@@ -41,6 +48,12 @@ __device__ __forceinline__ Sequence sequence(const CacheBatch& b, int32_t s)
     q.n = clamp32(b.starts[s + 1], q.t0, b.T) - q.t0;
     q.length = b.lengths[s] < 0 ? 0 : b.lengths[s];
     return q;
+}
+
+__device__ __forceinline__ Sequence uniform_sequence(const CacheBatch& b, int32_t s)
+{
+    const Sequence q = sequence(b, s);
+    return Sequence{uniform(q.t0), uniform(q.n), uniform(q.length)};
 }
 
 // The largest s < count with f(s) <= v for a rising f with f(0) <= v, sixty-four

@@ -233,8 +233,8 @@ int launch_attention(const AttentionArgs& args, void* stream, int* launches) MNB
 // Workgroups of the attention's first launch, and its workspace: for each of
 // them the sums of two row tiles that it shares with others, behind their
 // maxima and weights.  Host-only arithmetic (mnb_api.cpp).
+constexpr int kAttentionWorkgroups = 512;
 struct AttentionLayout {
-    int workgroups;
     size_t o, bytes;
 };
 AttentionLayout attention_layout(int64_t head_dim);

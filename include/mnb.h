@@ -442,7 +442,7 @@ size_t mnb_moe_workspace(int64_t tokens, int64_t hidden, int64_t inter, int64_t 
 #define MNB_KV_MAX_SEQUENCES 65536
 #define MNB_KV_MAX_HEADS 256              /* key heads */
 #define MNB_KV_MAX_GROUP 64               /* query heads of a key head */
-#define MNB_KV_MAX_LENGTH ((int64_t)1 << 30)   /* tokens that a row of the page table names */
+#define MNB_KV_MAX_LENGTH (1 << 24)       /* tokens that a row of the page table names */
 
 /*
  * A paged cache of keys and values in 8-bit integers.  A page holds page_size

@@ -46,7 +46,7 @@ SHARED = [
     (dict(null_cache=True), 1), (dict(null_batch=True), 1), (dict(T=-1), 6), (dict(T=(1 << 20) + 1), 6),
     (dict(pages=-1), 2), (dict(pages=1 << 31), 2), (dict(size=8), 2), (dict(size=48), 2), (dict(size=512), 2),
     (dict(heads=0), 2), (dict(heads=257), 2), (dict(D=32), 2), (dict(D=96), 2), (dict(D=512), 2), (dict(S=-1), 2),
-    (dict(S=65537), 2), (dict(width=-1), 2), (dict(width=(1 << 26) + 1), 2), (dict(dtype=mnb.MNB_F32), 4),
+    (dict(S=65537), 2), (dict(width=-1), 2), (dict(width=(1 << 20) + 1), 2), (dict(dtype=mnb.MNB_F32), 4),
     (dict(dtype=mnb.MNB_I8), 4), (dict(dtype=-1), 4), (dict(starts=None), 1), (dict(lengths=None), 1),
     (dict(table=None), 1), (dict(kp=None), 1), (dict(vp=None), 1), (dict(ks=None), 1), (dict(vs=None), 1),
     (dict(starts=5 * P + 2), 5), (dict(lengths=6 * P + 1), 5), (dict(table=7 * P + 2), 5), (dict(kp=P + 8), 5),
