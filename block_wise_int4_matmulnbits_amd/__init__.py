@@ -183,7 +183,7 @@ def lib():
         L.attention_int8.restype = i32
         L.attention_int8.argtypes = [cp, bp, i32, vp, i64, i64, ctypes.c_float, vp, i64, i64, vp, ctypes.c_size_t, vp]
         L.mnb_attention_workspace.restype = ctypes.c_size_t
-        L.mnb_attention_workspace.argtypes = [i64, i64, i64, i64]
+        L.mnb_attention_workspace.argtypes = [i64, i64, i64, i64, i64]
         L.matmul_lora.restype = i32
         L.matmul_lora.argtypes = [vp, i32, i64, i64, i64, i64, i64, i64, vp, vp, vp, vp, vp, i64, vp, i64, i32, vp,
                                   ctypes.c_size_t, vp]
@@ -614,7 +614,7 @@ def attention_int8(q, starts, lengths, page_table, k_pages, v_pages, k_scales, v
         raise ValueError("q must be [tokens, query heads, %d]" % cache.head_dim)
     qs = _strided("q", q, (T, heads, D), q.dtype, index)
     os_ = _strided("out", out, (T, heads, D), q.dtype, index)
-    need = L.mnb_attention_workspace(T, heads, cache.kv_heads, D) if workspace is None else 0
+    need = L.mnb_attention_workspace(T, batch.sequences, heads, cache.kv_heads, D) if workspace is None else 0
     ws = _workspace(q, need, workspace, stream, index) if need or workspace is not None else None
     _on_device(index, stream, L.attention_int8, ctypes.byref(cache), ctypes.byref(batch), dtype, q.data_ptr(), qs, heads,
                D ** -0.5 if scale is None else scale, out.data_ptr(), os_, max_tokens or 0,
@@ -622,9 +622,9 @@ def attention_int8(q, starts, lengths, page_table, k_pages, v_pages, k_scales, v
     return out
 
 
-def mnb_attention_workspace(tokens, q_heads, kv_heads, head_dim):
+def mnb_attention_workspace(tokens, sequences, q_heads, kv_heads, head_dim):
     """Workspace bytes of attention_int8."""
-    return lib().mnb_attention_workspace(tokens, q_heads, kv_heads, head_dim)
+    return lib().mnb_attention_workspace(tokens, sequences, q_heads, kv_heads, head_dim)
 
 
 def matmul_lora(x, ids, A, B, base, out, scaling=None, workspace=None, stream=None):

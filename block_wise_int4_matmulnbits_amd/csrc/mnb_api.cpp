@@ -641,12 +641,22 @@ MoeRoute moe_route(const MoeArgs& a, const MoeLayout& l, int cus)
 
 namespace mnb {
 
-AttentionLayout attention_layout(int64_t head_dim)
+AttentionLayout attention_layout(int64_t tokens, int64_t sequences, int64_t q_heads, int64_t kv_heads, int64_t head_dim)
 {
     AttentionLayout l;
-    const size_t tiles = 2 * (size_t)kAttentionWorkgroups;
-    l.o = tiles * 16 * 2 * 4;
-    l.bytes = l.o + tiles * 16 * (size_t)head_dim * 4;
+    const size_t parts = 2 * (size_t)kAttentionWorkgroups, D = (size_t)head_dim;
+    l.o = parts * 16 * 2 * 4;
+    l.tile_ml = l.o + parts * 16 * D * 4;
+    const int64_t rows = tokens * (q_heads / kv_heads), tile = 32 * tile_waves(head_dim);
+    // Full tiles, and one more for each sequence that can have many rows.
+    l.tile_slots = rows > kAttentionManyRows
+                       ? (int)(rows / tile + std::min<int64_t>(sequences, rows / (kAttentionManyRows + 1))) : 0;
+    const int64_t tiles = std::max<int64_t>(1, rows / tile) * kv_heads;
+    l.splits = (int)std::max<int64_t>(1, std::min<int64_t>(16, ceil_div(512, tiles)));
+    if (tiles >= 256) l.splits = 1;
+    const size_t each = l.splits > 1 ? (size_t)l.tile_slots * (size_t)kv_heads * (size_t)l.splits * (size_t)tile : 0;
+    l.tile_o = l.tile_ml + each * 2 * 4;
+    l.bytes = l.tile_o + each * D * 4;
     return l;
 }
 
@@ -1149,12 +1159,12 @@ int append_kv_int8(const mnb_kv_cache* cache, const mnb_kv_batch* batch, int dty
     return finish_launches(mnb::launch_append(args, stream), 1);
 }
 
-size_t mnb_attention_workspace(int64_t tokens, int64_t q_heads, int64_t kv_heads, int64_t head_dim)
+size_t mnb_attention_workspace(int64_t tokens, int64_t sequences, int64_t q_heads, int64_t kv_heads, int64_t head_dim)
 {
     const mnb_kv_cache c{0, 16, kv_heads, head_dim, nullptr, nullptr, nullptr, nullptr};
-    const mnb_kv_batch b{0, tokens, 0, nullptr, nullptr, nullptr};
-    if (check_kv(c, b) != MNB_OK || !good_group(q_heads, kv_heads) || tokens == 0) return 0;
-    return mnb::attention_layout(head_dim).bytes;
+    const mnb_kv_batch b{sequences, tokens, 0, nullptr, nullptr, nullptr};
+    if (check_kv(c, b) != MNB_OK || !good_group(q_heads, kv_heads) || tokens == 0 || sequences == 0) return 0;
+    return mnb::attention_layout(tokens, sequences, q_heads, kv_heads, head_dim).bytes;
 }
 
 int attention_int8(const mnb_kv_cache* cache, const mnb_kv_batch* batch, int dtype, const void* q, int64_t q_stride,
@@ -1176,7 +1186,7 @@ int attention_int8(const mnb_kv_cache* cache, const mnb_kv_batch* batch, int dty
     if (st == MNB_ERR_NULL || !q || !out || !workspace) return MNB_ERR_NULL;
     if (st != MNB_OK || ((uintptr_t)q & 15) || ((uintptr_t)out & 15) || ((uintptr_t)workspace & 15))
         return MNB_ERR_ALIGN;
-    const size_t need = mnb::attention_layout(D).bytes;
+    const size_t need = mnb::attention_layout(T, b.sequences, q_heads, H, D).bytes;
     if (need > workspace_bytes) return MNB_ERR_WORKSPACE;
     const int64_t each = c.pages * H;
     const Rows qr{q, T, q_heads * D * 2, q_stride * 2}, orow{out, T, q_heads * D * 2, out_stride * 2};

@@ -191,6 +191,42 @@ __device__ __forceinline__ uint32_t pack_bytes(uint32_t a, uint32_t b, uint32_t 
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }   // v_exp_f32: one step off at most
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
 
+// The y-th tile of BR rows, counted from the last one, among the sequences of
+// many rows (b.S: none); its number from the first.
+struct Tile {
+    int32_t s, rt, slot;
+};
+__device__ __forceinline__ int32_t tiles_of(const AttentionParams& p, int32_t s, int BR)
+{
+    const Sequence q = sequence(p.b, s);
+    const int32_t rows = q.n * p.G;
+    return rows > p.many ? (rows + BR - 1) / BR : 0;
+}
+__device__ __forceinline__ Tile tile_of(const AttentionParams& p, int32_t y, int BR)
+{
+    const int lane = threadIdx.x & 63;
+    int64_t all = 0;
+    for (int32_t s0 = 0; s0 < p.b.S; s0 += 64) all += s0 + lane < p.b.S ? tiles_of(p, s0 + lane, BR) : 0;
+    all = uniform64(wave_sum(all));
+    const int64_t v = all - 1 - y;
+    Tile t{p.b.S, 0, 0};
+    if (v < 0) return t;
+    int64_t base = 0;
+    for (int32_t s0 = 0; s0 < p.b.S; s0 += 64) {
+        const int64_t mine = s0 + lane < p.b.S ? tiles_of(p, s0 + lane, BR) : 0, upto = wave_prefix(mine);
+        const uint64_t past = __builtin_amdgcn_ballot_w64(base + upto > v);
+        if (past) {
+            const int l = __builtin_ctzll(past);
+            t.s = uniform(s0 + l);
+            t.rt = (int32_t)(v - uniform64(base + __shfl(upto - mine, l)));
+            t.slot = (int32_t)v;
+            return t;
+        }
+        base += uniform64(__shfl(upto, 63));
+    }
+    return t;
+}
+
 template <int D, bool BF16>
 __global__ __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) void mnb_attention_rows_kernel(AttentionParams p)
 {
@@ -545,15 +581,404 @@ __global__ __launch_bounds__(256) void mnb_attention_join_kernel(AttentionParams
     }
 }
 
-template <int D, bool BF16>
-int queue(AttentionParams& p, hipStream_t stream)
+// ---------------------------------------------------------------- many rows
+//
+// Tiles of 32 rows a wave, kTileWaves waves, over the keys in units of 64, the
+// running maximum and sum in registers; matrix products and the exponentials
+// share the time.  The workgroup stages a unit once for all its waves: integers
+// as fp16 (q + 1/2 for the keys, (q + 1/2) r for the values; exact) in LDS, two
+// units in turn, the next one's loads under way during the products.  Both
+// products run on v_mfma_f32_32x32x16_f16:
+//
+// * scores: 32 keys (A) x 32 rows (B, in registers: fp16 as they are, bf16 under a
+//   power of two of the row's own, exact but for what lies below 2^-39 of its
+//   largest).  Result lane (row, half) holds keys 8 q + 4 half + j; row m of A
+//   carries key 16 (q / 2) + 8 half + 4 (q % 2) + j for m = 8 q + 4 half + j, so that
+//   a lane ends with eight neighbouring keys of each 16: the B operand of the
+//   second product.
+// * outputs: 32 elements (A) x 32 rows, 16 keys deep, the same order, so that a
+//   lane stores eight neighbouring elements.  Weights in fp16 (2^-11 of each).
+//
+// Sixteen keys (a run) have one value scale.  The sums stand in units of `unit`: the
+// value scale of the run, or the largest of the 64 keys' where the run's is within
+// 2^-10 of it (r, at most 1, is what remains), so that no weight times scale falls
+// out of fp16's range, whatever the pages before it held.
+typedef _Float16 half8_t __attribute__((ext_vector_type(8)));
+typedef float float16_t __attribute__((ext_vector_type(16)));
+
+// What a unit's runs need: the factor of the scores, 0 or -infinity to add, and
+// the units of the values.
+struct Runs {
+    float ks[4], bias[4], ref[4];
+};
+
+__device__ __forceinline__ uint32_t half_pair(float lo, float hi) { return f16_pair(lo, hi); }
+
+// Sixteen integers to fp16: (q + 1/2) r.  1024 + (q + 128) has the byte in its low
+// mantissa bits.
+__device__ __forceinline__ void widen_bytes(i32x4 w, uint32_t r2, uint32_t half_r2, u32x4* out)
 {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t u = (uint32_t)w[i] ^ 0x80808080u;
+        const uint32_t a = hadd2(__builtin_amdgcn_perm(0x64646464u, u, 0x04010400u), 0xE480E480u);   // - 1152
+        const uint32_t b = hadd2(__builtin_amdgcn_perm(0x64646464u, u, 0x04030402u), 0xE480E480u);
+        out[i >> 1][(i & 1) * 2] = hfma2(a, r2, half_r2);
+        out[i >> 1][(i & 1) * 2 + 1] = hfma2(b, r2, half_r2);
+    }
+}
+
+template <int D, bool BF16>
+__global__ __launch_bounds__(64 * tile_waves(D), 1) void mnb_attention_tile_kernel(AttentionParams p)
+{
+    constexpr int NW = tile_waves(D), BR = 32 * NW, THREADS = 64 * NW;
+    constexpr int KQ = D / 16, DB = D / 32;
+    constexpr int KROW = D + 8, VROW = 64 + 8;             // fp16; the rows of LDS start 4 banks apart
+    constexpr int CHUNKS = 64 * D / 16 / THREADS;          // 16-byte pieces of the keys (and of the values) a thread
+    extern __shared__ uint16_t tile_lds[];                 // [2][64][KROW], [2][D][VROW]
+    uint16_t* const k_lds = tile_lds;
+    uint16_t* const v_lds = tile_lds + 2 * 64 * KROW;
+    const int tid = threadIdx.x, lane = tid & 63, r = lane & 31, hh = lane >> 5;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int32_t h = blockIdx.x, z = blockIdx.z;
+
+    // The tile: counted from the last one, whose rows see the most keys.
+    const Tile at = tile_of(p, blockIdx.y, BR);
+    if (at.s >= p.b.S) return;
+    const int32_t s = at.s, row0 = at.rt * BR;
+    const Sequence q = uniform_sequence(p.b, s);
+    const int32_t rows = q.n * p.G, start = q.length - q.n;
+    const int32_t wave0 = row0 + 32 * wave, mine = wave0 + r < rows ? wave0 + r : rows - 1;
+    const Row me = row_of(p, mine, h);
+    const int32_t position = start + me.token;
+    // Positions of the tile's last row and of the wave's first and last one.
+    const int32_t last = start + row_of(p, row0 + BR < rows ? row0 + BR - 1 : rows - 1, h).token;
+    const int32_t lowest = start + row_of(p, wave0 < rows ? wave0 : rows - 1, h).token;
+    const int32_t highest = start + row_of(p, wave0 + 31 < rows ? wave0 + 31 : rows - 1, h).token;
+    const int32_t cap = p.b.max_pages << p.b.page_bits;
+    const int32_t keys = last < 0 ? 0 : last + 1 < cap ? last + 1 : cap;
+    const int32_t units = (keys + 63) / 64;
+    const int32_t c0 = (int32_t)((int64_t)units * z / p.splits), c1 = (int32_t)((int64_t)units * (z + 1) / p.splits);
+
+    half8_t qv[KQ];
+    float q_scale;
+    {
+        const uint16_t* src = p.q + (q.t0 + me.token) * p.q_stride + (int64_t)me.head * D + 8 * hh;
+        u32x4 raw[KQ];
+        uint32_t top = 0;
+#pragma unroll
+        for (int k = 0; k < KQ; ++k) raw[k] = *reinterpret_cast<const u32x4*>(src + 16 * k);
+#pragma unroll
+        for (int k = 0; k < KQ; ++k)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) top = max_u16x2(top, raw[k][i] & 0x7FFF7FFFu);
+        top = (top & 0xFFFFu) > (top >> 16) ? top & 0xFFFFu : top >> 16;
+        const uint32_t o = __shfl_xor(top, 32);
+        top = o > top ? o : top;
+        const bool finite = top < (BF16 ? 0x7F80u : 0x7C00u);
+        // The factor of the scores is kept positive: the scale's sign goes to the row.
+        const float size = fabsf(p.scale_log2);
+        const uint32_t sign = p.scale_log2 < 0.f ? 0x80008000u : 0u;
+        q_scale = size;
+        if constexpr (BF16) {
+            const int ex = (int)(__float_as_uint(widen16(top, 1)) >> 23) - 126;       // |x| < 2^ex
+            const float pre = ex < -64 ? pow2(64) : 1.f, up = pow2((ex < -64 ? -49 : 15) - ex);
+            q_scale = size * pow2(ex < -64 ? -64 : ex) * pow2(ex < -64 ? ex + 49 : -15);
+#pragma unroll
+            for (int k = 0; k < KQ; ++k)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    raw[k][i] = half_pair(bf16_lo(raw[k][i]) * pre * up, bf16_hi(raw[k][i]) * pre * up);
+        }
+        if (!finite) q_scale = __uint_as_float(0x7FC00000u);
+#pragma unroll
+        for (int k = 0; k < KQ; ++k) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) raw[k][i] ^= sign;
+            qv[k] = __builtin_bit_cast(half8_t, raw[k]);
+        }
+    }
+
+    // Staging.  Piece i of a thread: key k_token of the unit, elements k_elem ..; and
+    // element v_elem, run tid % 4.
+    const int32_t* table = p.b.table + (int64_t)s * p.b.max_pages;
+    const int P = 1 << p.b.page_bits;
+    auto entry = [&](int c) {            // lane: the page of run lane % 4 of unit c
+        const int32_t index = (c * 64 + 16 * (lane & 3)) >> p.b.page_bits;
+        return index < p.b.max_pages ? table[index] : -1;
+    };
+    auto usable = [&](int32_t page) { return page >= 0 && page < p.b.pages; };
+    i32x4 raw_k[CHUNKS], raw_v[CHUNKS];
+    float lane_ks, lane_vs;              // of run lane % 4
+    bool lane_ok;
+    auto load = [&](int c, int32_t page) {
+        const int32_t safe = usable(page) ? page : 0;
+#pragma unroll
+        for (int i = 0; i < CHUNKS; ++i) {
+            const int id = tid + i * THREADS, token = id / (D / 16), elem = 16 * (id % (D / 16));
+            const int64_t pk = __shfl(safe, token >> 4);
+            raw_k[i] = *reinterpret_cast<const i32x4*>(
+                p.k_pages + (((pk * p.heads + h) << p.b.page_bits) + ((c * 64 + token) & (P - 1))) * D + elem);
+            const int ve = id >> 2, run = id & 3;
+            raw_v[i] = *reinterpret_cast<const i32x4*>(
+                p.v_pages + (((int64_t)safe * p.heads + h) << p.b.page_bits) * D + (int64_t)ve * P +
+                ((c * 64 + 16 * run) & (P - 1)));
+        }
+        lane_ok = usable(page);
+        // Scales of a run behind the last key mean nothing.
+        const bool live = lane_ok && c * 64 + 16 * (lane & 3) < keys;
+        const int64_t at_scale = (int64_t)safe * p.heads + h;
+        lane_ks = live ? p.k_scales[at_scale] : 0.f;
+        lane_vs = live ? fabsf(p.v_scales[at_scale]) : 0.f;
+    };
+    Runs now;
+    float lane_r;                        // what remains of run lane % 4's value scale
+    auto settle = [&](Runs& n) {
+        const bool fine = lane_vs < __builtin_inff();      // false for NaN
+        const float vs = fine ? lane_vs : 0.f;
+        float most = fmaxf(vs, __shfl_xor(vs, 1));
+        most = fmaxf(most, __shfl_xor(most, 2));
+        const float ref = most == 0.f ? 1.f : vs >= most * 0x1p-10f || vs == 0.f ? most : vs;
+        lane_r = vs / ref;
+        const float ks = fine ? lane_ks : __uint_as_float(0x7FC00000u), bias = lane_ok ? 0.f : -__builtin_inff();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            n.ks[i] = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(ks), i));
+            n.bias[i] = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(bias), i));
+            n.ref[i] = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(ref), i));
+        }
+    };
+    auto store = [&](int buffer) {
+        const uint32_t r2 = f16_pair(lane_r, lane_r), half_r2 = f16_pair(0.5f * lane_r, 0.5f * lane_r);
+#pragma unroll
+        for (int i = 0; i < CHUNKS; ++i) {
+            const int id = tid + i * THREADS, token = id / (D / 16), elem = 16 * (id % (D / 16));
+            u32x4 w[2];
+            widen_bytes(raw_k[i], 0x3C003C00u, 0x38003800u, w);      // 1, 1/2
+            u32x4* to = reinterpret_cast<u32x4*>(k_lds + (buffer * 64 + token) * KROW + elem);
+            to[0] = w[0];
+            to[1] = w[1];
+            widen_bytes(raw_v[i], r2, half_r2, w);
+            to = reinterpret_cast<u32x4*>(v_lds + (buffer * D + (id >> 2)) * VROW + 16 * (id & 3));
+            to[0] = w[0];
+            to[1] = w[1];
+        }
+    };
+
+    float16_t o[DB];
+#pragma unroll
+    for (int d = 0; d < DB; ++d)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[d][i] = 0.f;
+    float top = kLowest, weight = 0.f, unit = 0.f;
+    // Row m of A: key (or element) order(m) of its 32.
+    const int order = 16 * (r >> 4) + 8 * ((r >> 2) & 1) + 4 * ((r >> 3) & 1) + (r & 3);
+
+    if (c0 < c1) {
+        int32_t page = entry(c0);
+        load(c0, page);
+        page = c0 + 1 < c1 ? entry(c0 + 1) : 0;
+        settle(now);
+        store(0);
+        __syncthreads();
+        for (int c = c0; c < c1; ++c) {
+            const int buffer = (c - c0) & 1;
+            const bool more = c + 1 < c1;
+            if (more) {
+                load(c + 1, page);
+                if (c + 2 < c1) page = entry(c + 2);
+            }
+            const int32_t key0 = c * 64;
+            if (key0 <= highest) {
+                float16_t x[2];
+#pragma unroll
+                for (int b = 0; b < 2; ++b)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) x[b][i] = 0.f;
+                const uint16_t* kl = k_lds + (buffer * 64 + order) * KROW + 8 * hh;
+#pragma unroll
+                for (int k = 0; k < KQ; ++k)
+#pragma unroll
+                    for (int b = 0; b < 2; ++b)
+                        x[b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
+                            *reinterpret_cast<const half8_t*>(kl + 32 * b * KROW + 16 * k), qv[k], x[b], 0, 0, 0);
+                // x[b][8 e + j]: key 32 b + 16 e + 8 hh + j, of run 2 b + e.
+                float factor[4], add[4], m = -__builtin_inff();
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    factor[e] = q_scale * now.ks[e];
+                    add[e] = now.bias[e];
+                }
+                if (key0 + 63 > lowest) {       // (a key that is not seen has no factor: 0 times infinity)
+#pragma unroll
+                    for (int b = 0; b < 2; ++b)
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            const int e = 2 * b + (i >> 3);
+                            x[b][i] = key0 + 16 * e + 8 * hh + (i & 7) <= position ? fmaf(x[b][i], factor[e], add[e])
+                                                                                   : -__builtin_inff();
+                        }
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        factor[e] = 1.f;
+                        add[e] = 0.f;
+                    }
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    float most = x[e >> 1][8 * (e & 1)];
+#pragma unroll
+                    for (int j = 1; j < 8; ++j) most = fmaxf(most, x[e >> 1][8 * (e & 1) + j]);
+                    m = fmaxf(m, fmaf(most, factor[e], add[e]));
+                }
+                m = fmaxf(m, __shfl_xor(m, 32));
+                // The maximum is followed in steps of 2^6 at least: weights stay below
+                // 2^6, and the sums are scaled again in few units.
+                if (__builtin_amdgcn_ballot_w64(m > top + 6.f)) {
+                    const float next = fmaxf(top, m), keep = exp2_fast(top - next);
+                    top = next;
+                    weight *= keep;
+#pragma unroll
+                    for (int d = 0; d < DB; ++d) o[d] *= keep;
+                }
+                half8_t w[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float from = add[e] - top;
+                    u32x4 pairs;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float a = exp2_fast(fmaf(x[e >> 1][8 * (e & 1) + 2 * j], factor[e], from));
+                        const float b = exp2_fast(fmaf(x[e >> 1][8 * (e & 1) + 2 * j + 1], factor[e], from));
+                        pairs[j] = half_pair(a, b);
+                        weight = dot2(pairs[j], 0x3C003C00u, weight);
+                    }
+                    w[e] = __builtin_bit_cast(half8_t, pairs);
+                }
+                const uint16_t* vl = v_lds + (buffer * D + order) * VROW + 8 * hh;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    if (now.ref[e] != unit) {
+                        // Sums past 2^90 of the new unit keep theirs: what is added then
+                        // lies below their last bit, unless nothing has been added yet.
+                        const float by = unit == 0.f ? 1.f : unit / now.ref[e];
+                        if (by > 0x1p90f) continue;
+                        unit = now.ref[e];
+#pragma unroll
+                        for (int d = 0; d < DB; ++d) o[d] *= by;
+                    }
+#pragma unroll
+                    for (int d = 0; d < DB; ++d)
+                        o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
+                            *reinterpret_cast<const half8_t*>(vl + 32 * d * VROW + 16 * e), w[e], o[d], 0, 0, 0);
+                }
+            }
+            if (more) {
+                settle(now);
+                store(buffer ^ 1);
+            }
+            __syncthreads();
+        }
+    }
+
+    weight += __shfl_xor(weight, 32);
+    if (wave0 + r >= rows) return;
+    // o[d][8 e + j]: element 32 d + 16 e + 8 hh + j.
+    if (p.splits == 1) {
+        const float by = weight == 0.f ? 0.f : unit / weight;
+        uint16_t* dst = p.out + (q.t0 + me.token) * p.out_stride + (int64_t)me.head * D + 8 * hh;
+#pragma unroll
+        for (int d = 0; d < DB; ++d)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                u32x4 w;
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    w[j] = (uint32_t)narrow16(o[d][8 * e + 2 * j] * by, BF16) |
+                           (uint32_t)narrow16(o[d][8 * e + 2 * j + 1] * by, BF16) << 16;
+                *reinterpret_cast<u32x4*>(dst + 32 * d + 16 * e) = w;
+            }
+        return;
+    }
+    const int64_t part = (((int64_t)at.slot * p.heads + h) * p.splits + z) * BR + 32 * wave + r;
+    float* dst = p.tile_o + part * D + 8 * hh;
+#pragma unroll
+    for (int d = 0; d < DB; ++d)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+                *reinterpret_cast<float4_t*>(dst + 32 * d + 16 * e + 4 * j) =
+                    float4_t{o[d][8 * e + 4 * j] * unit, o[d][8 * e + 4 * j + 1] * unit, o[d][8 * e + 4 * j + 2] * unit,
+                             o[d][8 * e + 4 * j + 3] * unit};
+    if (hh == 0) {
+        p.tile_ml[part * 2] = top;
+        p.tile_ml[part * 2 + 1] = weight;
+    }
+}
+
+// The splits of a tile's keys, in order.  Grid: (heads, tiles, rows of a tile / 16).
+template <int D, bool BF16>
+__global__ __launch_bounds__(256) void mnb_attention_tile_join_kernel(AttentionParams p)
+{
+    constexpr int BR = 32 * tile_waves(D);
+    const int32_t h = blockIdx.x;
+    const Tile at = tile_of(p, blockIdx.y, BR);
+    if (at.s >= p.b.S) return;
+    const Sequence q = uniform_sequence(p.b, at.s);
+    const int32_t in = 16 * (int)blockIdx.z + (threadIdx.x >> 4), row = at.rt * BR + in, e0 = 4 * (threadIdx.x & 15);
+    if (row >= q.n * p.G) return;
+    const int64_t first = ((int64_t)at.slot * p.heads + h) * p.splits * BR + in;
+    float m = kLowest, l = 0.f;
+    for (int z = 0; z < p.splits; ++z) m = fmaxf(m, p.tile_ml[(first + z * BR) * 2]);
+    float4_t y[D / 64];
+#pragma unroll
+    for (int i = 0; i < D / 64; ++i) y[i] = float4_t{0.f, 0.f, 0.f, 0.f};
+    for (int z = 0; z < p.splits; ++z) {
+        const int64_t part = first + z * BR;
+        const float f = exp2_fast(p.tile_ml[part * 2] - m);
+        l += p.tile_ml[part * 2 + 1] * f;
+#pragma unroll
+        for (int i = 0; i < D / 64; ++i) y[i] += *reinterpret_cast<const float4_t*>(p.tile_o + part * D + 64 * i + e0) * f;
+    }
+    const Row to = row_of(p, row, h);
+    const float by = l == 0.f ? 0.f : 1.f / l;
+    uint16_t* dst = p.out + (q.t0 + to.token) * p.out_stride + (int64_t)to.head * D + e0;
+#pragma unroll
+    for (int i = 0; i < D / 64; ++i) {
+        uint32_t* w = reinterpret_cast<uint32_t*>(dst + 64 * i);
+        w[0] = (uint32_t)narrow16(y[i][0] * by, BF16) | (uint32_t)narrow16(y[i][1] * by, BF16) << 16;
+        w[1] = (uint32_t)narrow16(y[i][2] * by, BF16) | (uint32_t)narrow16(y[i][3] * by, BF16) << 16;
+    }
+}
+
+template <int D, bool BF16>
+int queue(const AttentionParams& p, const AttentionLayout& lay, hipStream_t stream, int* launches)
+{
+    const dim3 tiles((unsigned)p.heads, (unsigned)p.tile_slots, (unsigned)p.splits);
+    if (p.tile_slots) {
+        constexpr size_t lds = (size_t)4 * (64 * (D + 8) + D * 72);
+        hipLaunchKernelGGL((mnb_attention_tile_kernel<D, BF16>), tiles, dim3(64 * tile_waves(D)), lds, stream, p);
+        const int e = (int)hipGetLastError();
+        if (e != 0) return e;
+        ++*launches;
+    }
+    if (p.tile_slots && p.splits > 1) {
+        hipLaunchKernelGGL((mnb_attention_tile_join_kernel<D, BF16>),
+                           dim3((unsigned)p.heads, (unsigned)p.tile_slots, 2 * tile_waves(D)), dim3(256), 0, stream, p);
+        const int e = (int)hipGetLastError();
+        if (e != 0) return e;
+        ++*launches;
+    }
     hipLaunchKernelGGL((mnb_attention_rows_kernel<D, BF16>), dim3(kWorkgroups), dim3(64 * kWaves), 0, stream, p);
     int e = (int)hipGetLastError();
     if (e != 0) return e;
-    hipLaunchKernelGGL((mnb_attention_join_kernel<D, BF16>), dim3((unsigned)p.slots, (unsigned)p.heads, D / 64), dim3(256), 0,
-                       stream, p);
-    return (int)hipGetLastError();
+    ++*launches;
+    hipLaunchKernelGGL((mnb_attention_join_kernel<D, BF16>), dim3((unsigned)p.slots, (unsigned)p.heads, D / 64), dim3(256),
+                       0, stream, p);
+    e = (int)hipGetLastError();
+    if (e == 0) ++*launches;
+    return e;
 }
 
 }  // namespace
@@ -575,18 +1000,26 @@ int launch_attention(const AttentionArgs& a, void* stream, int* launches)
     p.heads = (int32_t)a.cache.kv_heads;
     p.G = (int32_t)(a.q_heads / a.cache.kv_heads);
     p.scale_log2 = a.scale * 1.44269504088896340736f;
-    const AttentionLayout lay = attention_layout(a.cache.head_dim);
+    const AttentionLayout lay = attention_layout(a.batch.tokens, a.batch.sequences, a.q_heads, a.cache.kv_heads,
+                                                a.cache.head_dim);
     uint8_t* ws = static_cast<uint8_t*>(a.ws);
     p.part_ml = reinterpret_cast<float*>(ws);
     p.part_o = reinterpret_cast<float*>(ws + lay.o);
-    p.many = INT32_MAX;
+    p.tile_ml = reinterpret_cast<float*>(ws + lay.tile_ml);
+    p.tile_o = reinterpret_cast<float*>(ws + lay.tile_o);
     p.slots = (int32_t)(a.batch.tokens * p.G / 16 + a.batch.sequences);
+    p.many = kAttentionManyRows;
+    // No sequence can have many rows where max_tokens says so.
+    const bool few = a.max_tokens > 0 && a.max_tokens * p.G <= p.many;
+    p.tile_slots = few ? 0 : lay.tile_slots;
+    if (few) p.many = INT32_MAX;
+    p.splits = lay.splits;
     const hipStream_t s = static_cast<hipStream_t>(stream);
-    *launches = 2;
+    *launches = 0;
     switch (a.cache.head_dim) {
-    case 64: return a.bf16 ? queue<64, true>(p, s) : queue<64, false>(p, s);
-    case 128: return a.bf16 ? queue<128, true>(p, s) : queue<128, false>(p, s);
-    default: return a.bf16 ? queue<256, true>(p, s) : queue<256, false>(p, s);
+    case 64: return a.bf16 ? queue<64, true>(p, lay, s, launches) : queue<64, false>(p, lay, s, launches);
+    case 128: return a.bf16 ? queue<128, true>(p, lay, s, launches) : queue<128, false>(p, lay, s, launches);
+    default: return a.bf16 ? queue<256, true>(p, lay, s, launches) : queue<256, false>(p, lay, s, launches);
     }
 }
 

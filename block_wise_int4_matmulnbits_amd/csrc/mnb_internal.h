@@ -230,14 +230,21 @@ struct AttentionArgs {
 };
 int launch_attention(const AttentionArgs& args, void* stream, int* launches) MNB_WEAK;
 
-// Workgroups of the attention's first launch, and its workspace: for each of
-// them the sums of two row tiles that it shares with others, behind their
-// maxima and weights.  Host-only arithmetic (mnb_api.cpp).
+// Sequences of more rows (tokens times query heads of a key head) than this go
+// to tiles of 32 tile_waves() rows, the others to a fixed number of workgroups.
+constexpr int kAttentionManyRows = 64;
 constexpr int kAttentionWorkgroups = 512;
+constexpr int tile_waves(int64_t head_dim) { return head_dim == 128 ? 8 : 4; }
+
+// The attention's workspace.  Few rows: for each workgroup the sums of two row
+// tiles that it shares with others, behind their maxima and weights.  Many: the
+// tiles there can be, and the sums of the splits of their keys, where few tiles
+// leave the device empty.  Host-only arithmetic (mnb_api.cpp).
 struct AttentionLayout {
-    size_t o, bytes;
+    int tile_slots, splits;
+    size_t o, tile_ml, tile_o, bytes;
 };
-AttentionLayout attention_layout(int64_t head_dim);
+AttentionLayout attention_layout(int64_t tokens, int64_t sequences, int64_t q_heads, int64_t kv_heads, int64_t head_dim);
 
 // Low-rank adapters (mnb_lora.hip).  Arguments have passed the front end's
 // checks; m, N > 0.

@@ -562,7 +562,7 @@ int attention_int8(const mnb_kv_cache* cache, const mnb_kv_batch* batch, int dty
 
 /* Workspace bytes attention_int8 needs (0 for none, or where it would reject
  * the sizes).  Host-only. */
-size_t mnb_attention_workspace(int64_t tokens, int64_t q_heads, int64_t kv_heads, int64_t head_dim);
+size_t mnb_attention_workspace(int64_t tokens, int64_t sequences, int64_t q_heads, int64_t kv_heads, int64_t head_dim);
 
 /* Bounds of the adapters. */
 #define MNB_LORA_MAX_RANK 256

@@ -151,33 +151,36 @@ def attention(b, q, scale):
     for s in range(b.S):
         t0, n = int(b.starts[s]), int(b.starts[s + 1] - b.starts[s])
         length = int(b.lengths[s])
+        upto = min(max(length, 0), b.width * b.P)
         for h in range(b.heads if n else 0):
-            k, v, vs, held = keys_of(b, s, h, max(length, 0))
-            for i in range(n):
-                seen = held.clone()
-                seen[max(0, length - n + i + 1):] = False
-                for g in range(G):
-                    row = q[t0 + i, h * G + g].double()
-                    at = (t0 + i, h * G + g)
-                    if not bool(seen.any()):
-                        out[at] = 0
-                        continue
-                    kk, vv, ss = k[seen], v[seen], vs[seen]
-                    z = kk @ row * scale
-                    w = torch.softmax(z, dim=0)
-                    y = w @ vv
-                    out[at] = y
-                    mag = abs(scale) * (kk.abs() @ row.abs() + 0.5 * 0)
-                    d = abs(scale) * 2.0 ** -22 * float(row.abs().max()) * kk.abs().sum(dim=1)
-                    d = d + 16 * 2.0 ** -24 * (mag + float(z.abs().max()))
-                    size = w @ vv.abs()
-                    moved = 2 * float(d.max()) * (size + y.abs())
-                    units = (torch.nonzero(seen)[:, 0] // 64)
-                    top = torch.zeros(int(units.max()) + 1, dtype=F64).scatter_reduce(0, units, w * ss, "amax")
-                    held16 = 2.0 ** -16 * (top[units] * 128).sum()
-                    heldf = 2.0 ** -11 * size + 2.0 ** -24 * float((w * ss).max()) * 128 * len(ss)
-                    sums = (len(top) + 64) * 2.0 ** -24 * 2 * (size + 128 * float((w * ss).sum()))
-                    tol[at] = moved + torch.maximum(held16 * torch.ones_like(y), heldf) + sums
+            k, v, vs, held = keys_of(b, s, h, upto)
+            rows = q[t0:t0 + n, h * G:(h + 1) * G].double().reshape(n * G, D)
+            last = (length - n + torch.arange(n)).repeat_interleave(G)
+            seen = held[None] & (torch.arange(upto)[None] <= last[:, None])
+            some = seen.any(dim=1)
+            y = torch.zeros(n * G, D, dtype=F64)
+            e = torch.zeros(n * G, D, dtype=F64)
+            if bool(some.any()):
+                z = (rows @ k.t() * scale).masked_fill(~seen, float("-inf"))
+                w = torch.softmax(z[some], dim=1)
+                y[some] = w @ v
+                m = seen[some]
+                kmag = k.abs().sum(dim=1)[None].masked_fill(~m, 0)
+                mag = abs(scale) * (rows[some].abs() @ k.abs().t()).masked_fill(~m, 0)
+                largest = z[some].masked_fill(~m, 0).abs().amax(dim=1)
+                d = abs(scale) * 2.0 ** -22 * rows[some].abs().amax(dim=1) * kmag.amax(dim=1)
+                d = d + 16 * 2.0 ** -24 * (mag.amax(dim=1) + largest)
+                size = w @ v.abs()
+                moved = 2 * d[:, None] * (size + y[some].abs())
+                pad = -upto % 64
+                ws = torch.nn.functional.pad(w * vs[None], (0, pad)).reshape(w.shape[0], -1, 64)
+                held16 = 2.0 ** -16 * 128 * 64 * ws.amax(dim=2).sum(dim=1)[:, None]
+                total = (m * vs[None]).sum(dim=1)[:, None]
+                heldf = 2.0 ** -11 * size + 2.0 ** -24 * 128 * w.amax(dim=1)[:, None] * total
+                sums = (ws.shape[1] + 64) * 2.0 ** -24 * 2 * (size + 128 * (w @ vs)[:, None])
+                e[some] = moved + torch.maximum(held16.expand_as(size), heldf) + sums
+            out[t0:t0 + n, h * G:(h + 1) * G] = y.reshape(n, G, D)
+            tol[t0:t0 + n, h * G:(h + 1) * G] = e.reshape(n, G, D)
     return out, tol
 
 

@@ -54,6 +54,15 @@ SHAPES = [
     ([130], [70], 16, 3, 3, 64),
     ([33, 65], [500, 0], 32, 8, 1, 256),
     ([300], [0], 64, 4, 1, 128),
+    # many rows: tiles, with and without their keys split over workgroups
+    ([65], [0], 64, 1, 1, 128),
+    ([1, 200, 3, 90], [500, 0, 70, 1000], 32, 8, 2, 128),
+    ([257, 70], [3, 64], 16, 2, 2, 128),
+    ([120, 0, 121], [0, 9, 700], 16, 2, 1, 256),
+    ([600], [130], 128, 64, 16, 64),
+    ([1100], [0], 64, 60, 30, 128),
+    ([9], [4000], 64, 64, 1, 128),
+    ([90, 333], [2000, 1], 256, 5, 5, 64),
 ]
 
 
@@ -100,6 +109,80 @@ def test_scales_far_apart():
         b.v_scales[:] = 0
         got = _call(b, q)
         assert bool((got == 0).all())
+
+
+def test_scales_far_apart_many_rows():
+    """The same for tiles: value scales that differ within a unit and from page to
+    page, pages of zeros, rows that see only some of them."""
+    G.require_gpu()
+    for P in (16, 32, 64):
+        for D in (64, 128):
+            b = R.Batch([150], [40], P, 1, D, seed=8)
+            g = torch.Generator().manual_seed(P)
+            b.v_scales = torch.exp2(torch.randint(-20, 10, b.v_scales.shape, generator=g).float())
+            b.k_scales = torch.exp2(torch.randint(-30, -5, b.k_scales.shape, generator=g).float())
+            b.v_scales[int(b.table[0, 0])] = 0
+            b.k_scales[int(b.table[0, 1])] = 0
+            q = _queries(b.T, 3, D, BF16, 4)
+            q[1] = 0
+            _check(b, q)
+            b.v_scales[:] = 0
+            assert bool((_call(b, q) == 0).all())
+
+
+def test_large_scores_many_rows():
+    G.require_gpu()
+    for scale in (2.0, -0.5, 0.0, 1e-3):
+        for dtype in (F16, BF16):
+            b = R.Batch([100, 70], [90, 300], 16, 2, 64, seed=5)
+            b.k_scales = torch.full_like(b.k_scales, 2.0 ** -4)
+            _check(b, _queries(b.T, 4, 64, dtype, 3), scale=scale)
+
+
+def test_not_finite_many_rows():
+    """Rows of tiles that do not see a page whose scale is NaN, or a query that is
+    not finite, keep their bits."""
+    G.require_gpu()
+    for P in (16, 64):
+        for D in (64, 128, 256):
+            b = R.Batch([100], [61], P, 1, D, seed=2)
+            q = _queries(b.T, 2, D, BF16, 1)
+            clean = _call(b, q)
+            for bad in (float("nan"), float("inf"), float("-inf")):
+                q2 = q.clone()
+                q2[70, 1, 5] = bad
+                got = _call(b, q2)
+                assert bool(torch.isnan(got[70, 1]).all())
+                got[70, 1] = clean[70, 1]
+                assert torch.equal(got, clean)
+            for scales in (b.k_scales, b.v_scales):
+                page = int(b.table[0, 128 // P])
+                was = scales[page, 0].clone()
+                scales[page, 0] = float("nan")
+                got = _call(b, q)
+                first = 128 - 61               # the first row that sees position 128
+                assert bool(torch.isnan(got[first:]).all())
+                assert torch.equal(got[:first], clean[:first])
+                scales[page, 0] = was
+
+
+def test_sizes_of_queries_many_rows():
+    G.require_gpu()
+    for dtype, sizes in ((F16, (6e-8, 1e-4, 3000.0)), (BF16, (1e-38, 1e-10, 1e15))):
+        for size in sizes:
+            b = R.Batch([70], [100], 32, 1, 64, seed=3)
+            b.k_scales = torch.full_like(b.k_scales, 2.0 ** -10)
+            q = (_queries(70, 2, 64, torch.float32, 6) * size).to(dtype)
+            _check(b, q, scale=min(1.0, 0.1 / size))
+
+
+def test_max_tokens_only_chooses():
+    """Wrong bounds of the tokens give other kernels, not other rows."""
+    G.require_gpu()
+    b = R.Batch([90, 1, 20], [100, 300, 0], 32, 2, 64, seed=4)
+    q = _queries(b.T, 4, 64, BF16, 2)
+    for most in (None, 1, 90, 10 ** 6):
+        _check(b, q, max_tokens=most)
 
 
 def test_sizes_of_queries():
@@ -188,7 +271,7 @@ def test_strides_streams_and_workspaces():
     args = b.cuda()
     big = torch.full((b.T, 20, 128), 5.0, dtype=BF16, device="cuda")
     big[:, 3:11] = q.cuda()
-    ws = torch.empty(mnb.mnb_attention_workspace(b.T, 8, 2, 128), dtype=torch.uint8, device="cuda")
+    ws = torch.empty(mnb.mnb_attention_workspace(b.T, b.S, 8, 2, 128), dtype=torch.uint8, device="cuda")
     side = torch.cuda.Stream()
     torch.cuda.synchronize()
     for stream in (None, side, side.cuda_stream):
@@ -201,11 +284,11 @@ def test_strides_streams_and_workspaces():
         assert torch.equal(big[:, 3:11].cpu(), q)
 
 
-def test_captured():
+@pytest.mark.parametrize("new", [[1, 2, 1, 0], [1, 40, 3, 30]], ids=["few", "many"])
+def test_captured(new):
     """A captured call replayed with other lengths, pages and queries, eager calls
     between the replays."""
     G.require_gpu()
-    new = [1, 2, 1, 0]
     sets = []
     for i, before in enumerate(([500, 3, 60, 9], [0, 0, 0, 0], [1, 2500, 64, 0])):
         b = R.Batch(new, before, 16, 2, 64, seed=i, width=160, spare=2)

@@ -106,11 +106,11 @@ def test_attention_refusals(args, status):
 
 
 def test_attention_workspace():
-    need = mnb.mnb_attention_workspace(5, 4, 2, 64)
+    need = mnb.mnb_attention_workspace(5, 3, 4, 2, 64)
     assert need > 0
     _status(_attention, dict(room=need - 1), 11)
-    for bad in ((-1, 4, 2, 64), ((1 << 20) + 1, 4, 2, 64), (0, 4, 2, 64), (5, 3, 2, 64), (5, 4, 0, 64), (5, 4, 2, 80),
-                (5, 130, 2, 64)):
+    for bad in ((-1, 3, 4, 2, 64), ((1 << 20) + 1, 3, 4, 2, 64), (0, 3, 4, 2, 64), (5, 0, 4, 2, 64), (5, -1, 4, 2, 64),
+                (5, 3, 3, 2, 64), (5, 3, 4, 0, 64), (5, 3, 4, 2, 80), (5, 3, 130, 2, 64)):
         assert mnb.mnb_attention_workspace(*bad) == 0
 
 
