@@ -609,7 +609,8 @@ typedef float float16_t __attribute__((ext_vector_type(16)));
 // What a unit's runs need: the factor of the scores, 0 or -infinity to add, and
 // the units of the values.
 struct Runs {
-    float ks[4], bias[4], ref[4];
+    float ks[4], bias[4];
+    uint32_t ref[4];          // bits
 };
 
 __device__ __forceinline__ uint32_t half_pair(float lo, float hi) { return f16_pair(lo, hi); }
@@ -629,7 +630,7 @@ __device__ __forceinline__ void widen_bytes(i32x4 w, uint32_t r2, uint32_t half_
 }
 
 template <int D, bool BF16>
-__global__ __launch_bounds__(64 * tile_waves(D), 1) void mnb_attention_tile_kernel(AttentionParams p)
+__global__ __launch_bounds__(64 * tile_waves(D), D == 64 ? 2 : 1) void mnb_attention_tile_kernel(AttentionParams p)
 {
     constexpr int NW = tile_waves(D), BR = 32 * NW, THREADS = 64 * NW;
     constexpr int KQ = D / 16, DB = D / 32;
@@ -731,6 +732,7 @@ __global__ __launch_bounds__(64 * tile_waves(D), 1) void mnb_attention_tile_kern
         lane_ks = live ? p.k_scales[at_scale] : 0.f;
         lane_vs = live ? fabsf(p.v_scales[at_scale]) : 0.f;
     };
+    uint32_t unit_bits = 0;              // bits of the sums' unit, alike in every lane; 0: no sums yet
     Runs now;
     float lane_r;                        // what remains of run lane % 4's value scale
     auto settle = [&](Runs& n) {
@@ -738,14 +740,16 @@ __global__ __launch_bounds__(64 * tile_waves(D), 1) void mnb_attention_tile_kern
         const float vs = fine ? lane_vs : 0.f;
         float most = fmaxf(vs, __shfl_xor(vs, 1));
         most = fmaxf(most, __shfl_xor(most, 2));
-        const float ref = most == 0.f ? 1.f : vs >= most * 0x1p-10f || vs == 0.f ? most : vs;
+        // (Sums of a unit 2^90 larger have their last bit above what they would lose.)
+        float ref = most == 0.f ? 1.f : vs >= most * 0x1p-10f || vs == 0.f ? most : vs;
+        ref = fmaxf(ref, fmaxf(most, __uint_as_float(unit_bits)) * 0x1p-90f);
         lane_r = vs / ref;
         const float ks = fine ? lane_ks : __uint_as_float(0x7FC00000u), bias = lane_ok ? 0.f : -__builtin_inff();
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             n.ks[i] = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(ks), i));
             n.bias[i] = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(bias), i));
-            n.ref[i] = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(ref), i));
+            n.ref[i] = __builtin_amdgcn_readlane(__float_as_uint(ref), i);
         }
     };
     auto store = [&](int buffer) {
@@ -770,7 +774,7 @@ __global__ __launch_bounds__(64 * tile_waves(D), 1) void mnb_attention_tile_kern
     for (int d = 0; d < DB; ++d)
 #pragma unroll
         for (int i = 0; i < 16; ++i) o[d][i] = 0.f;
-    float top = kLowest, weight = 0.f, unit = 0.f;
+    float top = kLowest, weight = 0.f;
     // Row m of A: key (or element) order(m) of its 32.
     const int order = 16 * (r >> 4) + 8 * ((r >> 2) & 1) + 4 * ((r >> 3) & 1) + (r & 3);
 
@@ -790,18 +794,29 @@ __global__ __launch_bounds__(64 * tile_waves(D), 1) void mnb_attention_tile_kern
             }
             const int32_t key0 = c * 64;
             if (key0 <= highest) {
+                // The pieces of A come two steps ahead of their products.
                 float16_t x[2];
 #pragma unroll
                 for (int b = 0; b < 2; ++b)
 #pragma unroll
                     for (int i = 0; i < 16; ++i) x[b][i] = 0.f;
                 const uint16_t* kl = k_lds + (buffer * 64 + order) * KROW + 8 * hh;
+                half8_t ka[2][4];
 #pragma unroll
-                for (int k = 0; k < KQ; ++k)
+                for (int k = 0; k < 4; ++k)
+                    ka[0][k] = *reinterpret_cast<const half8_t*>(kl + 32 * (k & 1) * KROW + 16 * (k >> 1));
 #pragma unroll
-                    for (int b = 0; b < 2; ++b)
-                        x[b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
-                            *reinterpret_cast<const half8_t*>(kl + 32 * b * KROW + 16 * k), qv[k], x[b], 0, 0, 0);
+                for (int n = 0; n < KQ / 2; ++n) {
+                    if (n + 1 < KQ / 2)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            ka[(n + 1) & 1][k] = *reinterpret_cast<const half8_t*>(kl + 32 * (k & 1) * KROW +
+                                                                                   32 * (n + 1) + 16 * (k >> 1));
+                    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        x[k & 1] = __builtin_amdgcn_mfma_f32_32x32x16_f16(ka[n & 1][k], qv[2 * n + (k >> 1)], x[k & 1], 0, 0, 0);
+                }
                 // x[b][8 e + j]: key 32 b + 16 e + 8 hh + j, of run 2 b + e.
                 float factor[4], add[4], m = -__builtin_inff();
 #pragma unroll
@@ -841,10 +856,12 @@ __global__ __launch_bounds__(64 * tile_waves(D), 1) void mnb_attention_tile_kern
 #pragma unroll
                     for (int d = 0; d < DB; ++d) o[d] *= keep;
                 }
-                half8_t w[4];
+                int from_v = (buffer * D + order) * VROW + 8 * hh;
+                auto values = [&](int e, half8_t (&f)[DB]) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float from = add[e] - top;
+                    for (int d = 0; d < DB; ++d) f[d] = *reinterpret_cast<const half8_t*>(v_lds + from_v + 32 * d * VROW + 16 * e);
+                };
+                auto weights = [&](int e, float from) {
                     u32x4 pairs;
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
@@ -853,25 +870,38 @@ __global__ __launch_bounds__(64 * tile_waves(D), 1) void mnb_attention_tile_kern
                         pairs[j] = half_pair(a, b);
                         weight = dot2(pairs[j], 0x3C003C00u, weight);
                     }
-                    w[e] = __builtin_bit_cast(half8_t, pairs);
-                }
-                const uint16_t* vl = v_lds + (buffer * D + order) * VROW + 8 * hh;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    if (now.ref[e] != unit) {
-                        // Sums past 2^90 of the new unit keep theirs: what is added then
-                        // lies below their last bit, unless nothing has been added yet.
-                        const float by = unit == 0.f ? 1.f : unit / now.ref[e];
-                        if (by > 0x1p90f) continue;
-                        unit = now.ref[e];
+                    return __builtin_bit_cast(half8_t, pairs);
+                };
+                // The runs of one unit of the sums at a time: all of them, but where their
+                // scales lie far apart.
+                uint32_t left = 15;
+                do {
+                    const uint32_t ref = left & 1 ? now.ref[0] : left & 2 ? now.ref[1] : left & 4 ? now.ref[2] : now.ref[3];
+                    if (ref != unit_bits) {
+                        const float by = unit_bits ? __uint_as_float(unit_bits) / __uint_as_float(ref) : 1.f;
+                        unit_bits = ref;
 #pragma unroll
                         for (int d = 0; d < DB; ++d) o[d] *= by;
                     }
+                    float from[4];
 #pragma unroll
-                    for (int d = 0; d < DB; ++d)
-                        o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
-                            *reinterpret_cast<const half8_t*>(vl + 32 * d * VROW + 16 * e), w[e], o[d], 0, 0, 0);
-                }
+                    for (int e = 0; e < 4; ++e) {
+                        const bool in = (left >> e & 1) && now.ref[e] == ref;
+                        from[e] = in ? add[e] - top : -__builtin_inff();
+                        left &= in ? ~(1u << e) : ~0u;
+                    }
+                    asm("" : "+v"(from_v));       // the loop's own loads: 16 pieces are too many to keep
+                    half8_t va[2][DB];
+                    values(0, va[0]);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        if (e < 3) values(e + 1, va[(e + 1) & 1]);
+                        const half8_t w = weights(e, from[e]);
+#pragma unroll
+                        for (int d = 0; d < DB; ++d)
+                            o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(va[e & 1][d], w, o[d], 0, 0, 0);
+                    }
+                } while (left);
             }
             if (more) {
                 settle(now);
@@ -881,6 +911,7 @@ __global__ __launch_bounds__(64 * tile_waves(D), 1) void mnb_attention_tile_kern
         }
     }
 
+    const float unit = __uint_as_float(unit_bits);
     weight += __shfl_xor(weight, 32);
     if (wave0 + r >= rows) return;
     // o[d][8 e + j]: element 32 d + 16 e + 8 hh + j.
