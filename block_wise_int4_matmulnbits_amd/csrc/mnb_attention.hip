@@ -54,6 +54,7 @@ struct AttentionParams {
     int64_t q_stride, out_stride;
     int32_t heads, G;         // key heads, rows a token has for each
     int32_t slots;            // row tiles of the joining launch's grid
+    int32_t tiles_each;       // of a sequence in it, or 0
     int32_t many;             // sequences of more rows than this go to the tiles
     int32_t tile_slots, splits;   // of the tiles' grid
     float scale_log2;         // scale * log2(e)
@@ -163,10 +164,16 @@ __device__ __forceinline__ Start start_of(const AttentionParams& p)
     return r;
 }
 
+// The larger of the lanes l and l ^ 32, and of the four lanes that share l % 16.
+__device__ __forceinline__ float xor32_max(float v)
+{
+    const auto h = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return fmaxf(__uint_as_float(h[0]), __uint_as_float(h[1]));
+}
 __device__ __forceinline__ float xor16_max(float v)
 {
-    v = fmaxf(v, __shfl_xor(v, 16));
-    return fmaxf(v, __shfl_xor(v, 32));
+    const auto h = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return xor32_max(fmaxf(__uint_as_float(h[0]), __uint_as_float(h[1])));
 }
 
 // A row's place: its token (of the sequence) and its head of q.  (A sequence
@@ -251,9 +258,9 @@ __global__ __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) void mnb_attention_r
             q = uniform_sequence(p.b, s);
             w = work_of(p, q);
         }
-        // (At most 2^2 tiles, 2^18 units and 2^8 heads.)
-        const uint32_t in = (uint32_t)(u - before), each = (uint32_t)(w.units + kBegin), pair = in / each;
-        const int from = (int)(in - pair * each) - kBegin, to = end - u < w.units - from ? from + (int)(end - u) : w.units;
+        const int64_t in = u - before, pair64 = divide(in, w.units + kBegin);
+        const uint32_t pair = (uint32_t)pair64;      // tiles and heads: at most 2^22 and 2^8
+        const int from = (int)(in - pair64 * (w.units + kBegin)) - kBegin, to = end - u < w.units - from ? from + (int)(end - u) : w.units;
         const int32_t h = (int32_t)(pair / (uint32_t)w.tiles), rt = (int32_t)(pair - h * w.tiles);
         u += to - from;
         const int c0 = from < 0 ? 0 : from, c1 = to;
@@ -525,8 +532,11 @@ __global__ __launch_bounds__(256) void mnb_attention_join_kernel(AttentionParams
     __shared__ float4_t meet[256];
     const int64_t slot = blockIdx.x;
     const int32_t h = blockIdx.y;
-    // A sequence's first slot: floor(t0 G / 16) + s leaves room for its tiles.
-    auto base = [&](int32_t i) { return (int64_t)clamp32(p.b.starts[i], 0, p.b.T) * p.G / 16 + i; };
+    // A sequence's first slot: the most tiles that the ones before it can have, or
+    // floor(t0 G / 16) + s, which leaves room for what they have.
+    auto base = [&](int32_t i) {
+        return p.tiles_each ? (int64_t)i * p.tiles_each : (int64_t)clamp32(p.b.starts[i], 0, p.b.T) * p.G / 16 + i;
+    };
     const int32_t s = wave_search(p.b.S, slot, base);
     const Sequence q = sequence(p.b, s);
     const Work w = work_of(p, q);
@@ -611,6 +621,7 @@ typedef float float16_t __attribute__((ext_vector_type(16)));
 struct Runs {
     float ks[4], bias[4];
     uint32_t ref[4];          // bits
+    uint32_t spoilt;          // runs with a scale that is not finite
 };
 
 __device__ __forceinline__ uint32_t half_pair(float lo, float hi) { return f16_pair(lo, hi); }
@@ -663,6 +674,7 @@ __global__ __launch_bounds__(64 * tile_waves(D), D == 64 ? 2 : 1) void mnb_atten
 
     half8_t qv[KQ];
     float q_scale;
+    bool q_finite;
     {
         const uint16_t* src = p.q + (q.t0 + me.token) * p.q_stride + (int64_t)me.head * D + 8 * hh;
         u32x4 raw[KQ];
@@ -677,6 +689,7 @@ __global__ __launch_bounds__(64 * tile_waves(D), D == 64 ? 2 : 1) void mnb_atten
         const uint32_t o = __shfl_xor(top, 32);
         top = o > top ? o : top;
         const bool finite = top < (BF16 ? 0x7F80u : 0x7C00u);
+        q_finite = finite;
         // The factor of the scores is kept positive: the scale's sign goes to the row.
         const float size = fabsf(p.scale_log2);
         const uint32_t sign = p.scale_log2 < 0.f ? 0x80008000u : 0u;
@@ -691,11 +704,12 @@ __global__ __launch_bounds__(64 * tile_waves(D), D == 64 ? 2 : 1) void mnb_atten
                 for (int i = 0; i < 4; ++i)
                     raw[k][i] = half_pair(bf16_lo(raw[k][i]) * pre * up, bf16_hi(raw[k][i]) * pre * up);
         }
-        if (!finite) q_scale = __uint_as_float(0x7FC00000u);
+        // (Its products are done with zeros; it gets its NaN at the end.)
+        if (!finite) q_scale = size;
 #pragma unroll
         for (int k = 0; k < KQ; ++k) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) raw[k][i] ^= sign;
+            for (int i = 0; i < 4; ++i) raw[k][i] = finite ? raw[k][i] ^ sign : 0u;
             qv[k] = __builtin_bit_cast(half8_t, raw[k]);
         }
     }
@@ -727,9 +741,9 @@ __global__ __launch_bounds__(64 * tile_waves(D), D == 64 ? 2 : 1) void mnb_atten
         }
         lane_ok = usable(page);
         // Scales of a run behind the last key mean nothing.
-        const bool live = lane_ok && c * 64 + 16 * (lane & 3) < keys;
+        const bool live = lane_ok && (P >= 64 || c * 64 + 16 * (lane & 3) < keys);
         const int64_t at_scale = (int64_t)safe * p.heads + h;
-        lane_ks = live ? p.k_scales[at_scale] : 0.f;
+        lane_ks = live ? fabsf(p.k_scales[at_scale]) : 0.f;
         lane_vs = live ? fabsf(p.v_scales[at_scale]) : 0.f;
     };
     uint32_t unit_bits = 0;              // bits of the sums' unit, alike in every lane; 0: no sums yet
@@ -738,13 +752,32 @@ __global__ __launch_bounds__(64 * tile_waves(D), D == 64 ? 2 : 1) void mnb_atten
     auto settle = [&](Runs& n) {
         const bool fine = lane_vs < __builtin_inff();      // false for NaN
         const float vs = fine ? lane_vs : 0.f;
+        const bool spoilt = !(lane_ks < __builtin_inff()) || !fine;
+        const float ks = spoilt ? 1.f : lane_ks, bias = lane_ok ? 0.f : -__builtin_inff();
+        // Zeros keep the sums' unit.  (Sums of a unit 2^90 larger have their last bit above
+        // what they would lose.)
+        n.spoilt = (uint32_t)__builtin_amdgcn_ballot_w64(spoilt) & 15u;
+        const bool none_yet = unit_bits == 0;
+        const float none = none_yet ? 1.f : __uint_as_float(unit_bits);
+        if (P >= 64) {                   // one page: the lanes of run 0 have it all
+            const float ref = vs == 0.f ? none : fmaxf(vs, none_yet ? 0.f : none * 0x1p-90f);
+            lane_r = vs == ref ? 1.f : vs / ref;
+            const float ks0 = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(ks), 0));
+            const float bias0 = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(bias), 0));
+            const uint32_t ref0 = __builtin_amdgcn_readlane(__float_as_uint(ref), 0);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                n.ks[i] = ks0;
+                n.bias[i] = bias0;
+                n.ref[i] = ref0;
+            }
+            return;
+        }
         float most = fmaxf(vs, __shfl_xor(vs, 1));
         most = fmaxf(most, __shfl_xor(most, 2));
-        // (Sums of a unit 2^90 larger have their last bit above what they would lose.)
-        float ref = most == 0.f ? 1.f : vs >= most * 0x1p-10f || vs == 0.f ? most : vs;
-        ref = fmaxf(ref, fmaxf(most, __uint_as_float(unit_bits)) * 0x1p-90f);
+        float ref = most == 0.f ? none : vs >= most * 0x1p-10f || vs == 0.f ? most : vs;
+        ref = fmaxf(ref, fmaxf(most, none_yet ? 0.f : none) * 0x1p-90f);
         lane_r = vs / ref;
-        const float ks = fine ? lane_ks : __uint_as_float(0x7FC00000u), bias = lane_ok ? 0.f : -__builtin_inff();
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             n.ks[i] = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(ks), i));
@@ -818,35 +851,26 @@ __global__ __launch_bounds__(64 * tile_waves(D), D == 64 ? 2 : 1) void mnb_atten
                         x[k & 1] = __builtin_amdgcn_mfma_f32_32x32x16_f16(ka[n & 1][k], qv[2 * n + (k >> 1)], x[k & 1], 0, 0, 0);
                 }
                 // x[b][8 e + j]: key 32 b + 16 e + 8 hh + j, of run 2 b + e.
-                float factor[4], add[4], m = -__builtin_inff();
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    factor[e] = q_scale * now.ks[e];
-                    add[e] = now.bias[e];
-                }
-                if (key0 + 63 > lowest) {       // (a key that is not seen has no factor: 0 times infinity)
+                if (key0 + 63 > lowest || now.spoilt) {
 #pragma unroll
                     for (int b = 0; b < 2; ++b)
 #pragma unroll
                         for (int i = 0; i < 16; ++i) {
-                            const int e = 2 * b + (i >> 3);
-                            x[b][i] = key0 + 16 * e + 8 * hh + (i & 7) <= position ? fmaf(x[b][i], factor[e], add[e])
-                                                                                   : -__builtin_inff();
+                            const float y = now.spoilt >> (2 * b + (i >> 3)) & 1 ? __uint_as_float(0x7FC00000u) : x[b][i];
+                            x[b][i] = key0 + 32 * b + 16 * (i >> 3) + 8 * hh + (i & 7) <= position ? y : -__builtin_inff();
                         }
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        factor[e] = 1.f;
-                        add[e] = 0.f;
-                    }
                 }
+                float factor[4], m = -__builtin_inff();
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
+                    const float f = q_scale * now.ks[e];
+                    factor[e] = f == 0.f ? 1e-37f : f;      // (a key that is not seen stands at -infinity)
                     float most = x[e >> 1][8 * (e & 1)];
 #pragma unroll
                     for (int j = 1; j < 8; ++j) most = fmaxf(most, x[e >> 1][8 * (e & 1) + j]);
-                    m = fmaxf(m, fmaf(most, factor[e], add[e]));
+                    m = fmaxf(m, fmaf(most, factor[e], now.bias[e]));
                 }
-                m = fmaxf(m, __shfl_xor(m, 32));
+                m = xor32_max(m);
                 // The maximum is followed in steps of 2^6 at least: weights stay below
                 // 2^6, and the sums are scaled again in few units.
                 if (__builtin_amdgcn_ballot_w64(m > top + 6.f)) {
@@ -887,7 +911,7 @@ __global__ __launch_bounds__(64 * tile_waves(D), D == 64 ? 2 : 1) void mnb_atten
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         const bool in = (left >> e & 1) && now.ref[e] == ref;
-                        from[e] = in ? add[e] - top : -__builtin_inff();
+                        from[e] = in ? now.bias[e] - top : -__builtin_inff();
                         left &= in ? ~(1u << e) : ~0u;
                     }
                     asm("" : "+v"(from_v));       // the loop's own loads: 16 pieces are too many to keep
@@ -913,6 +937,7 @@ __global__ __launch_bounds__(64 * tile_waves(D), D == 64 ? 2 : 1) void mnb_atten
 
     const float unit = __uint_as_float(unit_bits);
     weight += __shfl_xor(weight, 32);
+    if (!q_finite && weight > 0.f) weight = __uint_as_float(0x7FC00000u);
     if (wave0 + r >= rows) return;
     // o[d][8 e + j]: element 32 d + 16 e + 8 hh + j.
     if (p.splits == 1) {
@@ -1038,12 +1063,15 @@ int launch_attention(const AttentionArgs& a, void* stream, int* launches)
     p.part_o = reinterpret_cast<float*>(ws + lay.o);
     p.tile_ml = reinterpret_cast<float*>(ws + lay.tile_ml);
     p.tile_o = reinterpret_cast<float*>(ws + lay.tile_o);
-    p.slots = (int32_t)(a.batch.tokens * p.G / 16 + a.batch.sequences);
     p.many = kAttentionManyRows;
     // No sequence can have many rows where max_tokens says so.
     const bool few = a.max_tokens > 0 && a.max_tokens * p.G <= p.many;
     p.tile_slots = few ? 0 : lay.tile_slots;
     if (few) p.many = INT32_MAX;
+    // (max_tokens is not trusted with the place of a row tile.)
+    const int64_t loose = a.batch.tokens * p.G / 16 + a.batch.sequences, each = (kAttentionManyRows + 15) / 16;
+    p.tiles_each = !few && each * a.batch.sequences <= loose ? (int32_t)each : 0;
+    p.slots = (int32_t)(p.tiles_each ? each * a.batch.sequences : loose);
     p.splits = lay.splits;
     const hipStream_t s = static_cast<hipStream_t>(stream);
     *launches = 0;
