@@ -11,6 +11,7 @@ no fallback: if the library is missing, importing the entry points raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -492,6 +493,8 @@ def mnb_moe_workspace(tokens, hidden, inter, experts, top_k):
 
 
 # ------------------------------------- 8-bit cache, attention and adapters
+# Called once per layer and token too: each call's tensors pass one condition,
+# and only where it fails are they looked at one by one for what is wrong.
 def _strided(name, t, shape, dtype, index):
     """t has this shape and type, is on GPU ``index`` and dense but for its
     first dimension; returns the elements from one row to the next."""
@@ -501,33 +504,52 @@ def _strided(name, t, shape, dtype, index):
         raise ValueError("%s must be %s, got %s" % (name, list(shape), list(t.shape)))
     if t.get_device() != index:
         raise ValueError("%s must be on the GPU of the first argument, got %s" % (name, t.device))
-    width = 1
+    strides, width = t.stride(), 1
     for d in range(len(shape) - 1, 0, -1):
-        if shape[d] != 1 and t.stride(d) != width:
+        if shape[d] != 1 and strides[d] != width:
             raise ValueError("%s must be contiguous but for its first dimension" % name)
         width *= shape[d]
-    return t.stride(0) if shape[0] > 1 else width
+    return strides[0] if shape[0] > 1 else width
 
 
 def _kv(x, starts, lengths, page_table, k_pages, v_pages, k_scales, v_scales, index):
     """The cache and the batch of a call as the library takes them."""
-    import torch
     if k_pages.dim() != 4 or page_table.dim() != 2 or lengths.dim() != 1:
         raise ValueError("k_pages must be 4-D, page_table 2-D, lengths 1-D")
+    i8, i32, f32 = _types or _load_types()
     pages, heads, P, D = k_pages.shape
-    S = lengths.shape[0]
-    _expect("k_pages", k_pages, (pages, heads, P, D), torch.int8, index)
-    _expect("v_pages", v_pages, (pages, heads, D, P), torch.int8, index)
-    _expect("k_scales", k_scales, (pages, heads), torch.float32, index)
-    _expect("v_scales", v_scales, (pages, heads), torch.float32, index)
-    _expect("starts", starts, (S + 1,), torch.int32, index)
-    _expect("lengths", lengths, (S,), torch.int32, index)
-    _expect("page_table", page_table, (S, page_table.shape[1]), torch.int32, index)
-    cache = mnb_kv_cache(pages, P, heads, D, k_pages.data_ptr(), v_pages.data_ptr(), k_scales.data_ptr(),
-                         v_scales.data_ptr())
-    batch = mnb_kv_batch(S, x.shape[0], page_table.shape[1], starts.data_ptr(), lengths.data_ptr(),
-                         page_table.data_ptr())
-    return cache, batch
+    S, width = page_table.shape
+    if not (k_pages.dtype is v_pages.dtype is i8 and k_scales.dtype is v_scales.dtype is f32
+            and starts.dtype is lengths.dtype is page_table.dtype is i32
+            and v_pages.shape == (pages, heads, D, P) and k_scales.shape == v_scales.shape == (pages, heads)
+            and lengths.shape[0] == S and starts.shape == (S + 1,)
+            and k_pages.get_device() == v_pages.get_device() == k_scales.get_device() == v_scales.get_device()
+            == starts.get_device() == lengths.get_device() == page_table.get_device() == index
+            and k_pages.is_contiguous() and v_pages.is_contiguous() and k_scales.is_contiguous()
+            and v_scales.is_contiguous() and starts.is_contiguous() and lengths.is_contiguous()
+            and page_table.is_contiguous()):
+        S = lengths.shape[0]
+        _expect("k_pages", k_pages, (pages, heads, P, D), i8, index)
+        _expect("v_pages", v_pages, (pages, heads, D, P), i8, index)
+        _expect("k_scales", k_scales, (pages, heads), f32, index)
+        _expect("v_scales", v_scales, (pages, heads), f32, index)
+        _expect("starts", starts, (S + 1,), i32, index)
+        _expect("lengths", lengths, (S,), i32, index)
+        _expect("page_table", page_table, (S, width), i32, index)
+    return (mnb_kv_cache(pages, P, heads, D, k_pages.data_ptr(), v_pages.data_ptr(), k_scales.data_ptr(),
+                         v_scales.data_ptr()),
+            mnb_kv_batch(S, x.shape[0], width, starts.data_ptr(), lengths.data_ptr(), page_table.data_ptr()),
+            heads, D)
+
+
+_types = None
+
+
+def _load_types():
+    global _types
+    import torch
+    _types = (torch.int8, torch.int32, torch.float32)
+    return _types
 
 
 def _on_gpu(name, t, dim):
@@ -537,6 +559,16 @@ def _on_gpu(name, t, dim):
     if index < 0:
         raise ValueError("%s must be on the GPU" % name)
     return index
+
+
+@functools.lru_cache(maxsize=4096)
+def _attention_bytes(tokens, sequences, q_heads, kv_heads, head_dim):
+    return lib().mnb_attention_workspace(tokens, sequences, q_heads, kv_heads, head_dim)
+
+
+@functools.lru_cache(maxsize=4096)
+def _lora_bytes(m, K, N, rank, adapters):
+    return lib().mnb_lora_workspace(m, K, N, rank, adapters)
 
 
 def append_kv_int8(k, v, cos, sin, starts, lengths, page_table, k_pages, v_pages, k_scales, v_scales, q=None,
@@ -557,37 +589,35 @@ def append_kv_int8(k, v, cos, sin, starts, lengths, page_table, k_pages, v_pages
     """
     L = _lib or lib()
     index = _on_gpu("k", k, 3)
-    T, heads, D = k.shape
-    dtype = _dtype_code(k)
-    cache, batch = _kv(k, starts, lengths, page_table, k_pages, v_pages, k_scales, v_scales, index)
-    if (heads, D) != (cache.kv_heads, cache.head_dim):
-        raise ValueError("k must be [tokens, %d, %d]" % (cache.kv_heads, cache.head_dim))
-    ks = _strided("k", k, (T, heads, D), k.dtype, index)
-    vs = _strided("v", v, (T, heads, D), k.dtype, index)
-    qp = op = None
-    qs = os_ = q_heads = 0
-    if (q is None) != (q_out is None):
-        raise ValueError("q and q_out go together")
-    if q is not None:
+    T = k.shape[0]
+    dtype = k.dtype
+    code = _dtype_code(k)
+    cache, batch, heads, D = _kv(k, starts, lengths, page_table, k_pages, v_pages, k_scales, v_scales, index)
+    shape = (T, heads, D)
+    ks = _strided("k", k, shape, dtype, index)
+    vs = _strided("v", v, shape, dtype, index)
+    qp = op = cp = sp = None
+    qs = os_ = q_heads = rot = rows = 0
+    if q is not None and q_out is not None:
         _on_gpu("q", q, 3)
         q_heads = q.shape[1]
-        qs = _strided("q", q, (T, q_heads, D), k.dtype, index)
-        os_ = _strided("q_out", q_out, (T, q_heads, D), k.dtype, index)
+        shape = (T, q_heads, D)
+        qs = _strided("q", q, shape, dtype, index)
+        os_ = _strided("q_out", q_out, shape, dtype, index)
         qp, op = q.data_ptr(), q_out.data_ptr()
-    cp = sp = None
-    rot = rows = 0
-    if (cos is None) != (sin is None):
-        raise ValueError("cos and sin go together")
-    if cos is not None:
-        import torch
+    elif q is not q_out:
+        raise ValueError("q and q_out go together")
+    if cos is not None and sin is not None:
         if cos.dim() != 2:
             raise ValueError("cos must be 2-D")
-        rows, rot = cos.shape[0], 2 * cos.shape[1]
-        _expect("cos", cos, (rows, rot // 2), torch.float32, index)
-        _expect("sin", sin, (rows, rot // 2), torch.float32, index)
-        cp, sp = cos.data_ptr(), sin.data_ptr()
-    _on_device(index, stream, L.append_kv_int8, ctypes.byref(cache), ctypes.byref(batch), dtype, k.data_ptr(), ks,
-               v.data_ptr(), vs, qp, qs, op, os_, q_heads, cp, sp, rot, rows, 1 if interleaved else 0)
+        rows, half = shape = cos.shape
+        _expect("cos", cos, shape, _types[2], index)
+        _expect("sin", sin, shape, _types[2], index)
+        rot, cp, sp = 2 * half, cos.data_ptr(), sin.data_ptr()
+    elif cos is not sin:
+        raise ValueError("cos and sin go together")
+    _on_device(index, stream, L.append_kv_int8, cache, batch, code, k.data_ptr(), ks, v.data_ptr(), vs, qp, qs, op, os_,
+               q_heads, cp, sp, rot, rows, 1 if interleaved else 0)
     return q_out
 
 
@@ -607,16 +637,17 @@ def attention_int8(q, starts, lengths, page_table, k_pages, v_pages, k_scales, v
     """
     L = _lib or lib()
     index = _on_gpu("q", q, 3)
-    T, heads, D = q.shape
-    dtype = _dtype_code(q)
-    cache, batch = _kv(q, starts, lengths, page_table, k_pages, v_pages, k_scales, v_scales, index)
-    if D != cache.head_dim:
-        raise ValueError("q must be [tokens, query heads, %d]" % cache.head_dim)
-    qs = _strided("q", q, (T, heads, D), q.dtype, index)
-    os_ = _strided("out", out, (T, heads, D), q.dtype, index)
-    need = L.mnb_attention_workspace(T, batch.sequences, heads, cache.kv_heads, D) if workspace is None else 0
+    shape = T, q_heads, D = q.shape
+    dtype = q.dtype
+    code = _dtype_code(q)
+    cache, batch, heads, head_dim = _kv(q, starts, lengths, page_table, k_pages, v_pages, k_scales, v_scales, index)
+    if D != head_dim:
+        raise ValueError("q must be [tokens, query heads, %d]" % head_dim)
+    qs = _strided("q", q, shape, dtype, index)
+    os_ = _strided("out", out, shape, dtype, index)
+    need = _attention_bytes(T, batch.sequences, q_heads, heads, D) if workspace is None else 0
     ws = _workspace(q, need, workspace, stream, index) if need or workspace is not None else None
-    _on_device(index, stream, L.attention_int8, ctypes.byref(cache), ctypes.byref(batch), dtype, q.data_ptr(), qs, heads,
+    _on_device(index, stream, L.attention_int8, cache, batch, code, q.data_ptr(), qs, q_heads,
                D ** -0.5 if scale is None else scale, out.data_ptr(), os_, max_tokens or 0,
                None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel() * ws.element_size())
     return out
@@ -661,7 +692,7 @@ def matmul_lora(x, ids, A, B, base, out, scaling=None, workspace=None, stream=No
     if base is not None:
         bs = _strided("base", base, (m, N), out.dtype, index)
         bp = base.data_ptr()
-    need = L.mnb_lora_workspace(m, K, N, R, n) if workspace is None else 0
+    need = _lora_bytes(m, K, N, R, n) if workspace is None else 0
     ws = _workspace(x, need, workspace, stream, index) if need or workspace is not None else None
     _on_device(index, stream, L.matmul_lora, x.data_ptr(), x_dt, xs, m, K, N, R, n, ids.data_ptr(), A.data_ptr(),
                B.data_ptr(), sp, bp, bs, out.data_ptr(), os_, o_dt, None if ws is None else ws.data_ptr(),

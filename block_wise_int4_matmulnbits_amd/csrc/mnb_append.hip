@@ -32,6 +32,8 @@ namespace {
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
 constexpr int kThreads = 256;
+constexpr int kKeyUnits = 4;     // units of sixteen keys' elements that a thread keeps between its two looks at them
+constexpr int kValueUnits = 2;   // the same of 8 elements of four tokens
 
 struct AppendParams {
     CacheBatch b;
@@ -46,18 +48,16 @@ struct AppendParams {
     float* k_scales;          // [pages][heads]
     float* v_scales;
     int64_t k_stride, v_stride, q_stride, q_out_stride;   // elements between tokens
-    int32_t heads, q_heads, D, rot;
+    int32_t heads, q_heads, rot;
     int32_t slots;            // page slots of the grid
     int32_t by_token;         // slot of a sequence's first page: its first token, else see slot_base
-    int32_t bf16, interleaved;
 };
 
 // A sequence of n tokens touches at most n pages, and at most floor((n - 1) /
 // P) + 2.  Its slots start at its first token, or at floor(t0 / P) + 2 s, which
 // leaves room for that many whatever the sequences before it hold.
-__device__ __forceinline__ int64_t slot_base(const AppendParams& p, int32_t s)
+__device__ __forceinline__ int64_t slot_base(const AppendParams& p, int32_t t0, int32_t s)
 {
-    const int32_t t0 = clamp32(p.b.starts[s], 0, p.b.T);
     return p.by_token ? t0 : (int64_t)(t0 >> p.b.page_bits) + 2 * (int64_t)s;
 }
 
@@ -102,54 +102,54 @@ __device__ __forceinline__ uint32_t shift_bytes(uint32_t w, int d)
 }
 
 // Sixteen elements, unit j of a token's head: two pieces of eight, rotated
-// where the unit lies in the first rot elements.  Piece 0 starts at element
-// unit_first(), piece 1 at unit_second().
-struct Unit {
-    int first, second;
-    bool turned;
-};
-__device__ __forceinline__ Unit unit_of(int j, int rot, int interleaved)
+// where the unit lies in the first rot elements.
+template <bool NEAR>
+__device__ __forceinline__ void unit_of(int j, int rot, int* first, int* second)
 {
-    const bool turned = 16 * j < rot;
-    if (turned && !interleaved) return Unit{8 * j, rot / 2 + 8 * j, true};
-    return Unit{16 * j, 16 * j + 8, turned};
+    const bool halves = !NEAR && 16 * j < rot;
+    *first = halves ? 8 * j : 16 * j;
+    *second = halves ? rot / 2 + 8 * j : 16 * j + 8;
 }
 
-__device__ __forceinline__ float element(const u32x4& a, int i, int bf16)
+template <bool BF16>
+__device__ __forceinline__ float element(const u32x4& a, int i)
 {
     const uint32_t w = a[i >> 1];
-    return widen16(i & 1 ? w >> 16 : w & 0xFFFFu, bf16);
+    return widen16(i & 1 ? w >> 16 : w & 0xFFFFu, BF16);
 }
 
-// The unit's values in 64 bits, pieces 0 and 1 after each other.
-__device__ __forceinline__ void load_unit(const AppendParams& p, const uint16_t* src, int64_t position, int j,
-                                          const Unit& u, double (&x)[16])
+// The cosines and sines of unit j at a position: 1 and 0 where it is not rotated.
+__device__ __forceinline__ void load_turn(const AppendParams& p, int64_t position, int j, float4_t (&c)[2], float4_t (&s)[2])
 {
-    const u32x4 a = *reinterpret_cast<const u32x4*>(src + u.first);
-    const u32x4 b = *reinterpret_cast<const u32x4*>(src + u.second);
-    if (!u.turned) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            x[i] = element(a, i, p.bf16);
-            x[8 + i] = element(b, i, p.bf16);
-        }
-        return;
+    c[0] = c[1] = float4_t{1.f, 1.f, 1.f, 1.f};
+    s[0] = s[1] = float4_t{0.f, 0.f, 0.f, 0.f};
+    if (16 * j < p.rot) {
+        const float4_t* cp = reinterpret_cast<const float4_t*>(p.cos + position * (p.rot / 2) + 8 * j);
+        const float4_t* sp = reinterpret_cast<const float4_t*>(p.sin + position * (p.rot / 2) + 8 * j);
+        c[0] = cp[0];
+        c[1] = cp[1];
+        s[0] = sp[0];
+        s[1] = sp[1];
     }
-    const float4_t* cp = reinterpret_cast<const float4_t*>(p.cos + position * (p.rot / 2) + 8 * j);
-    const float4_t* sp = reinterpret_cast<const float4_t*>(p.sin + position * (p.rot / 2) + 8 * j);
-    const float4_t c0 = cp[0], c1 = cp[1], s0 = sp[0], s1 = sp[1];
+}
+
+// The pieces a and b turned, value(n, x) called with each of the sixteen in 64 bits,
+// n = 0 .. 7 of the first piece, then the second's.  A unit that is not rotated keeps
+// its values whatever they are (0 times infinity would not).
+template <bool BF16, bool NEAR, class F>
+__device__ __forceinline__ void turn(const u32x4& a, const u32x4& b, const float4_t (&c)[2], const float4_t (&s)[2],
+                                     bool turned, F value)
+{
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const double c = i < 4 ? c0[i & 3] : c1[i & 3], s = i < 4 ? s0[i & 3] : s1[i & 3];
-        if (p.interleaved) {       // pairs of neighbours: elements 2 i and 2 i + 1 of the sixteen
-            const double e = element(i < 4 ? a : b, 2 * (i & 3), p.bf16), o = element(i < 4 ? a : b, 2 * (i & 3) + 1, p.bf16);
-            x[2 * i] = e * c - o * s;
-            x[2 * i + 1] = o * c + e * s;
-        } else {
-            const double e = element(a, i, p.bf16), o = element(b, i, p.bf16);
-            x[i] = e * c - o * s;
-            x[8 + i] = o * c + e * s;
-        }
+        const int e0 = NEAR ? 2 * i : i, e1 = NEAR ? 2 * i + 1 : 8 + i;
+        const float x0 = NEAR ? (i < 4 ? element<BF16>(a, 2 * (i & 3)) : element<BF16>(b, 2 * (i & 3))) : element<BF16>(a, i);
+        const float x1 = NEAR ? (i < 4 ? element<BF16>(a, 2 * (i & 3) + 1) : element<BF16>(b, 2 * (i & 3) + 1))
+                              : element<BF16>(b, i);
+        const double co = c[i >> 2][i & 3], si = s[i >> 2][i & 3];
+        const double y0 = (double)x0 * co - (double)x1 * si, y1 = (double)x1 * co + (double)x0 * si;
+        value(e0, turned ? y0 : (double)x0);
+        value(e1, turned ? y1 : (double)x1);
     }
 }
 
@@ -184,111 +184,201 @@ __device__ __forceinline__ OldScale old_scale(float scale)
     return OldScale{e + 133 < 255 ? (uint32_t)(e + 133) << 23 : 0x7F7FFFFFu, e};
 }
 
-// One page of one head: the tokens of positions first + a .. first + b - 1.
-// tokens == the row of position first (rows follow each other).
-__device__ __forceinline__ void store_keys(const AppendParams& p, int64_t page, int head, int64_t first, int a, int b,
+// One page of one head: the tokens of positions first + a .. first + b - 1, whose
+// rows follow each other; `row` is that of position first.  page is looked at
+// only once the new values are on their way.
+template <int D, bool BF16, bool NEAR>
+__device__ __forceinline__ void store_keys(const AppendParams& p, int32_t page, int head, int64_t first, int a, int b,
                                            int64_t row, uint32_t* part)
 {
-    const int D = p.D, units = D / 16, count = (b - a) * units;
+    constexpr int UNITS = D / 16;
+    const int count = (b - a) * UNITS;
     const uint16_t* src = p.k + row * p.k_stride + (int64_t)head * D;
-    float* scale = p.k_scales + page * p.heads + head;
-    int8_t* dst = p.k_pages + ((page * p.heads + head) << p.b.page_bits) * D;
-    const OldScale old = a > 0 ? old_scale(*scale) : OldScale{0, 0};
-    uint32_t top = old.bits;
-    double x[16];
-    for (int i = threadIdx.x; i < count; i += kThreads) {
-        const int off = a + i / units, j = i % units;
-        load_unit(p, src + off * p.k_stride, first + off, j, unit_of(j, p.rot, p.interleaved), x);
+    // Units i, i + 256, ... of a thread share their place in the head.
+    const int j = threadIdx.x % UNITS;
+    int piece0, piece1;
+    unit_of<NEAR>(j, p.rot, &piece0, &piece1);
+    const bool turned = 16 * j < p.rot;
+    uint32_t top = 0;
+    float kept[kKeyUnits][16];
+    auto look = [&](int i, float (&x)[16]) {
+        const int off = a + i / UNITS;
+        const u32x4 va = *reinterpret_cast<const u32x4*>(src + off * p.k_stride + piece0);
+        const u32x4 vb = *reinterpret_cast<const u32x4*>(src + off * p.k_stride + piece1);
+        float4_t c[2], s[2];
+        load_turn(p, first + off, j, c, s);
+        turn<BF16, NEAR>(va, vb, c, s, turned, [&](int n, double y) { x[n] = round_down(y); });
+    };
+    const bool keep = count <= kKeyUnits * kThreads;
+    if (keep) {
 #pragma unroll
-        for (int n = 0; n < 16; ++n) {
-            const uint32_t r = range_bits(round_down(x[n]));
-            top = r > top ? r : top;
+        for (int u = 0; u < kKeyUnits; ++u) {
+            const int i = threadIdx.x + u * kThreads;
+            if (i < count) {
+                look(i, kept[u]);
+#pragma unroll
+                for (int n = 0; n < 16; ++n) top = max(top, range_bits(kept[u][n]));
+            }
+        }
+    } else {
+        for (int i = threadIdx.x; i < count; i += kThreads) {
+            look(i, kept[0]);
+#pragma unroll
+            for (int n = 0; n < 16; ++n) top = max(top, range_bits(kept[0][n]));
         }
     }
-    top = workgroup_max(top, part);
+    if (page < 0 || page >= p.b.pages) return;
+    const int64_t at = (int64_t)page * p.heads + head;
+    int8_t* dst = p.k_pages + (at << p.b.page_bits) * D;
+    const OldScale old = a > 0 ? old_scale(p.k_scales[at]) : OldScale{0, 0};
+    top = workgroup_max(max(top, old.bits), part);
     const bool finite = top < 0x7F800000u;
     const int e = exponent_of(top);
     const float down = power_of_two(-e);
-    if (threadIdx.x == 0) *scale = !finite ? __uint_as_float(0x7FC00000u) : top == 0 ? 0.f : power_of_two(e);
+    if (threadIdx.x == 0) p.k_scales[at] = !finite ? __uint_as_float(0x7FC00000u) : top == 0 ? 0.f : power_of_two(e);
     if (old.bits && finite && e > old.e) {
         const int d = e - old.e < 7 ? e - old.e : 7;
         uint32_t* w = reinterpret_cast<uint32_t*>(dst);
         for (int i = threadIdx.x; i < a * D / 4; i += kThreads) w[i] = shift_bytes(w[i], d);
     }
-    for (int i = threadIdx.x; i < count; i += kThreads) {
-        const int off = a + i / units, j = i % units;
-        const Unit u = unit_of(j, p.rot, p.interleaved);
-        load_unit(p, src + off * p.k_stride, first + off, j, u, x);
+    auto store = [&](int i, const float (&x)[16]) {
         uint32_t w[4];
 #pragma unroll
         for (int n = 0; n < 4; ++n) {
             uint32_t r = 0;
 #pragma unroll
-            for (int m = 0; m < 4; ++m) r |= (uint32_t)(quantize(round_down(x[4 * n + m]), down) & 255) << (8 * m);
+            for (int m = 0; m < 4; ++m) r |= (uint32_t)(quantize(x[4 * n + m], down) & 255) << (8 * m);
             w[n] = finite ? r : 0;
         }
-        *reinterpret_cast<u32x2*>(dst + off * D + u.first) = u32x2{w[0], w[1]};
-        *reinterpret_cast<u32x2*>(dst + off * D + u.second) = u32x2{w[2], w[3]};
+        int8_t* to = dst + (a + i / UNITS) * D;
+        *reinterpret_cast<u32x2*>(to + piece0) = u32x2{w[0], w[1]};
+        *reinterpret_cast<u32x2*>(to + piece1) = u32x2{w[2], w[3]};
+    };
+    if (keep) {
+#pragma unroll
+        for (int u = 0; u < kKeyUnits; ++u)
+            if ((int)threadIdx.x + u * kThreads < count) store(threadIdx.x + u * kThreads, kept[u]);
+    } else {
+        for (int i = threadIdx.x; i < count; i += kThreads) {
+            look(i, kept[0]);
+            store(i, kept[0]);
+        }
     }
+}
+
+// The largest of |x|, and of |x| less a step where x is negative, of pairs of 16-bit
+// values.  (Their bits are in the order of their size; a step less takes a power of
+// two into the range below, as range_bits does.)
+__device__ __forceinline__ void range16(uint32_t w, uint32_t& most, uint32_t& less)
+{
+    typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+    const uint32_t m = w & 0x7FFF7FFFu;
+    const u16x2 sign = __builtin_bit_cast(u16x2, w) >> (uint16_t)15;
+    most = max_u16x2(most, m);
+    less = max_u16x2(less, __builtin_bit_cast(uint32_t, __builtin_elementwise_sub_sat(__builtin_bit_cast(u16x2, m), sign)));
+}
+
+__device__ __forceinline__ uint32_t range_of(uint32_t most, uint32_t less, int bf16)
+{
+    most = max(most & 0xFFFFu, most >> 16);
+    less = max(less & 0xFFFFu, less >> 16);
+    if (most >= (bf16 ? 0x7F80u : 0x7C00u)) return 0x7F800000u;
+    // (A step below the type's smallest value is zero, which says nothing of its range.)
+    return most == 0 ? 0u : max(__float_as_uint(0.5f * widen16(1, bf16)), __float_as_uint(widen16(less, bf16)));
 }
 
 // The values lie with their tokens last: a thread holds eight elements of four
 // neighbouring tokens and writes a word for each element.
-__device__ __forceinline__ void store_values(const AppendParams& p, int64_t page, int head, int a, int b, int64_t row,
+template <int D, bool BF16>
+__device__ __forceinline__ void store_values(const AppendParams& p, int32_t page, int head, int a, int b, int64_t row,
                                              uint32_t* part)
 {
-    const int D = p.D, P = 1 << p.b.page_bits, pieces = D / 8;
+    constexpr int PIECES = D / 8;
+    const int P = 1 << p.b.page_bits;
     const uint16_t* src = p.v + row * p.v_stride + (int64_t)head * D;
-    float* scale = p.v_scales + page * p.heads + head;
-    int8_t* dst = p.v_pages + ((page * p.heads + head) << p.b.page_bits) * D;
-    const OldScale old = a > 0 ? old_scale(*scale) : OldScale{0, 0};
-    uint32_t top = old.bits;
-    for (int i = threadIdx.x; i < (b - a) * pieces; i += kThreads) {
-        const u32x4 x = *reinterpret_cast<const u32x4*>(src + (a + i / pieces) * p.v_stride + 8 * (i % pieces));
-#pragma unroll
-        for (int n = 0; n < 8; ++n) {
-            const uint32_t r = range_bits(element(x, n, p.bf16));
-            top = r > top ? r : top;
-        }
-    }
-    top = workgroup_max(top, part);
-    const bool finite = top < 0x7F800000u;
-    const int e = exponent_of(top);
-    const float down = power_of_two(-e);
-    if (threadIdx.x == 0) *scale = !finite ? __uint_as_float(0x7FC00000u) : top == 0 ? 0.f : power_of_two(e);
-    const int d = old.bits && finite && e > old.e ? (e - old.e < 7 ? e - old.e : 7) : 0;
-    // Groups of four tokens; those before the first new one only where they are shifted.
-    const int g0 = d ? 0 : a / 4, g1 = (b + 3) / 4;
-    for (int i = threadIdx.x; i < (g1 - g0) * pieces; i += kThreads) {
-        const int off = 4 * (g0 + i % (g1 - g0)), c = 8 * (i / (g1 - g0));
-        uint32_t w[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    // Groups of four tokens with a new one; unit i is group g0 + i % groups, piece i / groups.
+    const int g0 = a / 4, groups = (b + 3) / 4 - g0, count = groups * PIECES;
+    uint32_t most = 0, less = 0;
+    u32x4 kept[kValueUnits][4];
+    auto look = [&](int i, u32x4 (&x)[4]) {
+        const int off = 4 * (g0 + i % groups), c = 8 * (i / groups);
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
             const bool mine = off + m >= a && off + m < b;
-            if (!mine) continue;
-            const u32x4 x = *reinterpret_cast<const u32x4*>(src + (off + m) * p.v_stride + c);
-#pragma unroll
-            for (int n = 0; n < 8; ++n)
-                w[n] |= finite ? (uint32_t)(quantize(element(x, n, p.bf16), down) & 255) << (8 * m) : 0u;
+            x[m] = mine ? *reinterpret_cast<const u32x4*>(src + (off + m) * p.v_stride + c) : u32x4{0, 0, 0, 0};
         }
+    };
+    const bool keep = count <= kValueUnits * kThreads;
+    if (keep) {
+#pragma unroll
+        for (int u = 0; u < kValueUnits; ++u) {
+            const int i = threadIdx.x + u * kThreads;
+            if (i < count) {
+                look(i, kept[u]);
+#pragma unroll
+                for (int m = 0; m < 4; ++m)
+#pragma unroll
+                    for (int n = 0; n < 4; ++n) range16(kept[u][m][n], most, less);
+            }
+        }
+    } else {
+        for (int i = threadIdx.x; i < count; i += kThreads) {
+            look(i, kept[0]);
+#pragma unroll
+            for (int m = 0; m < 4; ++m)
+#pragma unroll
+                for (int n = 0; n < 4; ++n) range16(kept[0][m][n], most, less);
+        }
+    }
+    if (page < 0 || page >= p.b.pages) return;
+    const int64_t at = (int64_t)page * p.heads + head;
+    int8_t* dst = p.v_pages + (at << p.b.page_bits) * D;
+    const OldScale old = a > 0 ? old_scale(p.v_scales[at]) : OldScale{0, 0};
+    const uint32_t top = workgroup_max(max(range_of(most, less, BF16), old.bits), part);
+    const bool finite = top < 0x7F800000u;
+    const int e = exponent_of(top);
+    const float down = power_of_two(-e);
+    if (threadIdx.x == 0) p.v_scales[at] = !finite ? __uint_as_float(0x7FC00000u) : top == 0 ? 0.f : power_of_two(e);
+    const int d = old.bits && finite && e > old.e ? (e - old.e < 7 ? e - old.e : 7) : 0;
+    if (d) {      // groups of old tokens only
+        for (int i = threadIdx.x; i < g0 * D; i += kThreads) {
+            uint32_t* w = reinterpret_cast<uint32_t*>(dst + (int64_t)(i / g0) * P) + i % g0;
+            *w = shift_bytes(*w, d);
+        }
+    }
+    auto store = [&](int i, const u32x4 (&x)[4]) {
+        const int off = 4 * (g0 + i % groups), c = 8 * (i / groups);
         uint32_t* to = reinterpret_cast<uint32_t*>(dst + (int64_t)c * P + off);
         const bool whole = off >= a && off + 4 <= b;
-        uint32_t fresh = 0, kept = 0;     // bytes that are new, and old ones of this sequence
+        uint32_t fresh = 0, mine = 0;     // bytes that are new, and old ones of this sequence
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
-            if (off + m >= a && off + m < b) fresh |= 255u << (8 * m);
-            if (off + m < a) kept |= 255u << (8 * m);
+            fresh |= off + m >= a && off + m < b ? 255u << (8 * m) : 0u;
+            mine |= off + m < a ? 255u << (8 * m) : 0u;
         }
 #pragma unroll
         for (int n = 0; n < 8; ++n) {
+            uint32_t w = 0;
+#pragma unroll
+            for (int m = 0; m < 4; ++m) w |= (uint32_t)(quantize(element<BF16>(x[m], n), down) & 255) << (8 * m);
+            w = finite ? w : 0;
             uint32_t* word = to + n * (P / 4);
             if (whole) {
-                *word = w[n];
+                *word = w;
                 continue;
             }
-            const uint32_t was = *word;
-            const uint32_t moved = d ? shift_bytes(was, d) : was;
-            *word = (w[n] & fresh) | (moved & kept) | (was & ~(fresh | kept));
+            const uint32_t was = *word, moved = d ? shift_bytes(was, d) : was;
+            *word = (w & fresh) | (moved & mine) | (was & ~(fresh | mine));
+        }
+    };
+    if (keep) {
+#pragma unroll
+        for (int u = 0; u < kValueUnits; ++u)
+            if ((int)threadIdx.x + u * kThreads < count) store(threadIdx.x + u * kThreads, kept[u]);
+    } else {
+        for (int i = threadIdx.x; i < count; i += kThreads) {
+            look(i, kept[0]);
+            store(i, kept[0]);
         }
     }
 }
@@ -305,32 +395,48 @@ __device__ __forceinline__ float round_to_odd(double x)
     return __uint_as_float(b | 1u);
 }
 
+template <int D, bool BF16, bool NEAR>
 __device__ __forceinline__ void turn_queries(const AppendParams& p, int64_t t)
 {
-    const int lane = threadIdx.x & 63;
-    const int32_t s = wave_search(p.b.S, t, [&](int32_t i) { return (int64_t)clamp32(p.b.starts[i], 0, p.b.T); });
-    const Sequence q = sequence(p.b, s);
-    const int64_t i = t - q.t0, position = (int64_t)q.length - q.n + i;
-    if (i < 0 || i >= q.n || position < 0 || position >= ((int64_t)p.b.max_pages << p.b.page_bits)) return;
-    const int units = p.D / 16;
+    constexpr int UNITS = D / 16, EACH = 64 / UNITS;     // units of a head, heads of a wave at a time
+    const int lane = threadIdx.x & 63, j = lane % UNITS;
+    const Found f = find_sequence(p.b, t, [](int32_t t0, int32_t) { return (int64_t)t0; });
+    const int64_t i = t - f.q.t0, position = (int64_t)f.q.length - f.q.n + i;
+    if (i < 0 || i >= f.q.n || position < 0 || position >= ((int64_t)p.b.max_pages << p.b.page_bits)) return;
+    int piece0, piece1;
+    unit_of<NEAR>(j, p.rot, &piece0, &piece1);
     const uint16_t* src = p.q + t * p.q_stride;
     uint16_t* dst = p.q_out + t * p.q_out_stride;
-    double x[16];
-    for (int n = lane; n < p.q_heads * units; n += 64) {
-        const int j = n % units;
-        const int64_t at = (int64_t)(n / units) * p.D;
-        const Unit u = unit_of(j, p.rot, p.interleaved);
-        load_unit(p, src + at, position, j, u, x);
-        u32x4 out[2];
+    float4_t c[2], s[2];
+    load_turn(p, position, j, c, s);
+    constexpr int AHEAD = 4;
+    for (int h0 = 0; h0 < p.q_heads; h0 += AHEAD * EACH) {
+        u32x4 va[AHEAD], vb[AHEAD];
 #pragma unroll
-        for (int m = 0; m < 8; ++m)
-            out[m >> 2][m & 3] = (uint32_t)narrow16(round_to_odd(x[2 * m]), p.bf16) |
-                                 (uint32_t)narrow16(round_to_odd(x[2 * m + 1]), p.bf16) << 16;
-        *reinterpret_cast<u32x4*>(dst + at + u.first) = out[0];
-        *reinterpret_cast<u32x4*>(dst + at + u.second) = out[1];
+        for (int u = 0; u < AHEAD; ++u) {
+            const int h = h0 + u * EACH + lane / UNITS;
+            if (h < p.q_heads) {
+                va[u] = *reinterpret_cast<const u32x4*>(src + h * D + piece0);
+                vb[u] = *reinterpret_cast<const u32x4*>(src + h * D + piece1);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < AHEAD; ++u) {
+            const int h = h0 + u * EACH + lane / UNITS;
+            if (h >= p.q_heads) continue;
+            uint32_t out[16];
+            turn<BF16, NEAR>(va[u], vb[u], c, s, 16 * j < p.rot,
+                             [&](int n, double y) { out[n] = narrow16(round_to_odd(y), BF16); });
+            u32x4 w[2];
+#pragma unroll
+            for (int m = 0; m < 8; ++m) w[m >> 2][m & 3] = out[2 * m] | out[2 * m + 1] << 16;
+            *reinterpret_cast<u32x4*>(dst + h * D + piece0) = w[0];
+            *reinterpret_cast<u32x4*>(dst + h * D + piece1) = w[1];
+        }
     }
 }
 
+template <int D, bool BF16, bool NEAR>
 __global__ __launch_bounds__(kThreads) void mnb_append_kernel(AppendParams p)
 {
     __shared__ uint32_t part[kThreads / 64];
@@ -340,25 +446,31 @@ __global__ __launch_bounds__(kThreads) void mnb_append_kernel(AppendParams p)
     if (blockIdx.x >= (uint32_t)p.slots) {
         const int64_t id = (int64_t)(blockIdx.x - p.slots) * gridDim.y + kind;
         const int64_t t = id * (kThreads / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-        if (t < p.b.T) turn_queries(p, t);
+        if (t < p.b.T) turn_queries<D, BF16, NEAR>(p, t);
         return;
     }
     const int64_t slot = blockIdx.x;
-    const int32_t s = wave_search(p.b.S, slot, [&](int32_t i) { return slot_base(p, i); });
-    const Sequence q = sequence(p.b, s);
+    const Found f = find_sequence(p.b, slot, [&](int32_t t0, int32_t i) { return slot_base(p, t0, i); });
     // Tokens before position 0 (a length shorter than its tokens) are passed over.
-    const int64_t start = (int64_t)q.length - q.n, from = start < 0 ? 0 : start;
-    const int64_t index = (from >> p.b.page_bits) + (slot - slot_base(p, s));
+    const int64_t start = (int64_t)f.q.length - f.q.n, from = start < 0 ? 0 : start;
+    const int64_t index = (from >> p.b.page_bits) + (slot - slot_base(p, f.q.t0, f.s));
     const int64_t first = index << p.b.page_bits;
-    if (index < 0 || first >= q.length || index >= p.b.max_pages || q.n == 0) return;
-    const int32_t page = p.b.table[(int64_t)s * p.b.max_pages + index];
-    if (page < 0 || page >= p.b.pages) return;
+    if (index < 0 || first >= f.q.length || index >= p.b.max_pages || f.q.n == 0) return;
+    const int32_t page = p.b.table[(int64_t)f.s * p.b.max_pages + index];
     const int P = 1 << p.b.page_bits;
     const int a = from > first ? (int)(from - first) : 0;
-    const int b = q.length - first < P ? (int)(q.length - first) : P;
-    const int64_t row = q.t0 + (first - start);   // of position first; negative only where a > 0
-    if (kind < p.heads) store_keys(p, page, kind, first, a, b, row, part);
-    else store_values(p, page, kind - p.heads, a, b, row, part);
+    const int b = f.q.length - first < P ? (int)(f.q.length - first) : P;
+    const int64_t row = f.q.t0 + (first - start);   // of position first; negative only where a > 0
+    if (kind < p.heads) store_keys<D, BF16, NEAR>(p, page, kind, first, a, b, row, part);
+    else store_values<D, BF16>(p, page, kind - p.heads, a, b, row, part);
+}
+
+template <int D, bool BF16>
+int queue(const AppendParams& p, bool near, dim3 grid, hipStream_t stream)
+{
+    if (near) hipLaunchKernelGGL((mnb_append_kernel<D, BF16, true>), grid, dim3(kThreads), 0, stream, p);
+    else hipLaunchKernelGGL((mnb_append_kernel<D, BF16, false>), grid, dim3(kThreads), 0, stream, p);
+    return (int)hipGetLastError();
 }
 
 }  // namespace
@@ -385,17 +497,20 @@ int launch_append(const AppendArgs& a, void* stream)
     p.q_out_stride = a.q_out_stride;
     p.heads = (int32_t)a.cache.kv_heads;
     p.q_heads = (int32_t)a.q_heads;
-    p.D = (int32_t)a.cache.head_dim;
     p.rot = (int32_t)a.rot_dim;
-    p.bf16 = a.bf16;
-    p.interleaved = a.interleaved;
     const int64_t T = a.batch.tokens, loose = T / a.cache.page_size + 2 * a.batch.sequences;
     p.by_token = T <= loose;
     p.slots = (int32_t)(p.by_token ? T : loose);
     const int64_t rows = 2 * a.cache.kv_heads, waves = kThreads / 64;
     const int64_t columns = p.slots + (p.q ? (T + rows * waves - 1) / (rows * waves) : 0);
-    hipLaunchKernelGGL(mnb_append_kernel, dim3((unsigned)columns, (unsigned)rows), dim3(kThreads), 0, static_cast<hipStream_t>(stream), p);
-    return (int)hipGetLastError();
+    const dim3 grid((unsigned)columns, (unsigned)rows);
+    const hipStream_t st = static_cast<hipStream_t>(stream);
+    const bool near = a.interleaved != 0;
+    switch (a.cache.head_dim) {
+    case 64: return a.bf16 ? queue<64, true>(p, near, grid, st) : queue<64, false>(p, near, grid, st);
+    case 128: return a.bf16 ? queue<128, true>(p, near, grid, st) : queue<128, false>(p, near, grid, st);
+    default: return a.bf16 ? queue<256, true>(p, near, grid, st) : queue<256, false>(p, near, grid, st);
+    }
 }
 
 }  // namespace mnb

@@ -78,4 +78,25 @@ __device__ __forceinline__ int32_t wave_search(int32_t count, int64_t v, F f)
     return __builtin_amdgcn_readfirstlane(lo);
 }
 
+// Sequence s = the largest with f(its first row, s) <= v, for a rising f.  Up to 64
+// sequences are read at once, lane s the s-th.
+struct Found {
+    int32_t s;
+    Sequence q;
+};
+template <class F>
+__device__ __forceinline__ Found find_sequence(const CacheBatch& b, int64_t v, F f)
+{
+    if (b.S > 64) {
+        const int32_t s = wave_search(b.S, v, [&](int32_t i) { return f(clamp32(b.starts[i], 0, b.T), i); });
+        return Found{s, uniform_sequence(b, s)};
+    }
+    const int32_t lane = threadIdx.x & 63, i = lane < b.S ? lane : b.S - 1;
+    const Sequence q = sequence(b, i);
+    const uint64_t m = __builtin_amdgcn_ballot_w64(lane < b.S && f(q.t0, i) <= v);
+    const int32_t s = m ? 63 - __builtin_clzll(m) : 0;
+    return Found{s, Sequence{__builtin_amdgcn_readlane(q.t0, s), __builtin_amdgcn_readlane(q.n, s),
+                             __builtin_amdgcn_readlane(q.length, s)}};
+}
+
 }  // namespace mnb
