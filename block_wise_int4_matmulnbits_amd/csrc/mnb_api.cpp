@@ -660,16 +660,19 @@ AttentionLayout attention_layout(int64_t tokens, int64_t sequences, int64_t q_he
     return l;
 }
 
-LoraLayout lora_layout(int64_t m, int64_t K, int64_t R)
+LoraLayout lora_layout(int64_t m, int64_t K, int64_t N, int64_t R, int64_t adapters)
 {
     LoraLayout l;
-    l.row_tiles = m <= 64 ? 1 : R <= 128 ? 4 : 2;
-    const int64_t tiles = ceil_div(m, 16 * l.row_tiles);
-    int64_t splits = ceil_div(512, tiles);
-    splits = std::min<int64_t>(splits, std::min<int64_t>(16, std::max<int64_t>(1, K / 256)));
+    l.row_tiles = m <= 16 ? 1 : R <= 128 ? 4 : 2;
+    const int64_t rows = 16 * l.row_tiles, tiles = ceil_div(m, rows);
+    // Few rows may have an adapter each; many rows come in runs of one.
+    l.ways = (int)std::max<int64_t>(1, std::min<int64_t>(tiles == 1 ? 64 : 1, std::min(adapters, std::min(m, rows))));
+    int64_t splits = ceil_div(512, tiles * l.ways);
+    splits = std::min<int64_t>(splits, std::min<int64_t>(m <= 16 ? 16 : 8, std::max<int64_t>(1, K / 256)));
     const int64_t slice = ceil_div(ceil_div(K, splits), 128) * 128;
     l.k_slice = (int)std::max<int64_t>(128, slice);
     l.splits = (int)std::max<int64_t>(1, ceil_div(K, l.k_slice));
+    l.wide = ceil_div(N, 512) * tiles >= 256;
     l.bytes = (size_t)l.splits * (size_t)m * (size_t)R * 4;
     return l;
 }
@@ -1210,7 +1213,7 @@ int attention_int8(const mnb_kv_cache* cache, const mnb_kv_batch* batch, int dty
 size_t mnb_lora_workspace(int64_t m, int64_t K, int64_t N, int64_t rank, int64_t adapters)
 {
     if (check_lora_shape(m, K, N, rank, adapters) != MNB_OK || m == 0 || N == 0) return 0;
-    return mnb::lora_layout(m, K, rank).bytes;
+    return mnb::lora_layout(m, K, N, rank, adapters).bytes;
 }
 
 int matmul_lora(const void* x, int x_dtype, int64_t x_stride, int64_t m, int64_t K, int64_t N, int64_t rank,
@@ -1231,7 +1234,7 @@ int matmul_lora(const void* x, int x_dtype, int64_t x_stride, int64_t m, int64_t
     if (((uintptr_t)x & 15) || ((uintptr_t)A & 15) || ((uintptr_t)B & 15) || ((uintptr_t)ids & 3) ||
         ((uintptr_t)scaling & 3) || ((uintptr_t)base & 1) || ((uintptr_t)out & 1) || ((uintptr_t)workspace & 15))
         return MNB_ERR_ALIGN;
-    const size_t need = mnb::lora_layout(m, K, rank).bytes;
+    const size_t need = mnb::lora_layout(m, K, N, rank, adapters).bytes;
     if (need > workspace_bytes) return MNB_ERR_WORKSPACE;
     const Rows xr{x, m, K * 2, x_stride * 2}, br{base, m, N * 2, base_stride * 2}, orow{out, m, N * 2, out_stride * 2};
     const Span in[] = {{ids, m * 4}, {A, adapters * rank * K * 2}, {B, adapters * N * rank * 2}, {scaling, adapters * 4},

@@ -263,12 +263,14 @@ struct LoraArgs {
 int launch_lora(const LoraArgs& args, void* stream, int* launches) MNB_WEAK;
 
 // Row tiles of 16 of a workgroup, slices of K of the first launch and their
-// length, and the workspace that holds the slices' sums.  Host-only arithmetic
-// (mnb_api.cpp).
+// length, workgroups that share the adapters of a tile in it, whether the second
+// launch takes 64 columns a wave (or 16), and the workspace that holds the
+// slices' sums.  Host-only arithmetic (mnb_api.cpp).
 struct LoraLayout {
-    int row_tiles, splits, k_slice;
+    int row_tiles, splits, k_slice, ways;
+    bool wide;
     size_t bytes;
 };
-LoraLayout lora_layout(int64_t m, int64_t K, int64_t R);
+LoraLayout lora_layout(int64_t m, int64_t K, int64_t N, int64_t R, int64_t adapters);
 
 }  // namespace mnb

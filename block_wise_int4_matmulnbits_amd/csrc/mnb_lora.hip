@@ -23,7 +23,7 @@ namespace {
 typedef _Float16 half8_t __attribute__((ext_vector_type(8)));
 typedef __bf16 bhalf8_t __attribute__((ext_vector_type(8)));
 
-constexpr int kWaves = 4;
+constexpr int kDownWaves = 4;
 
 struct LoraParams {
     const uint16_t* x;        // [m][K]
@@ -36,7 +36,7 @@ struct LoraParams {
     float* t;                 // [splits][m][R]
     int64_t m, x_stride, base_stride, out_stride;
     int32_t K, N, R, adapters, splits;
-    int32_t k_slice;          // K of a slice: a multiple of 32 * kWaves
+    int32_t k_slice;          // K of a slice: a multiple of 32 * kDownWaves
     int32_t out_bf16;
 };
 
@@ -59,19 +59,33 @@ __device__ __forceinline__ int32_t tile_id(const LoraParams& p, int64_t row0)
     return a >= 0 && a < p.adapters ? a : -1;
 }
 
+// The adapters of a tile one after another, by their first row; rows: a bit each.
+struct Adapters {
+    uint64_t left;
+    int32_t id;               // of this lane's row
+    __device__ __forceinline__ int32_t next(uint64_t* rows)
+    {
+        const int32_t a = __builtin_amdgcn_readlane(id, __builtin_ctzll(left));
+        *rows = __builtin_amdgcn_ballot_w64(id == a);
+        left &= ~*rows;
+        return a;
+    }
+};
+
 // Rows to rank: a workgroup takes RT = 16 NRT rows, one slice of K and, of the
-// adapters that its rows use, every gridDim.z-th; its waves split the slice.
-// RKT tiles of 16 ranks at a time.
+// adapters that its rows use, every gridDim.z-th; its waves split the slice, two
+// steps of 32 in flight.  RKT tiles of 16 ranks at a time.
 template <bool BF16, int NRT, int RKT>
-__global__ __launch_bounds__(64 * kWaves) void mnb_lora_down_kernel(LoraParams p)
+__global__ __launch_bounds__(64 * kDownWaves) void mnb_lora_down_kernel(LoraParams p)
 {
-    constexpr int RT = 16 * NRT;
-    __shared__ float4_t part[kWaves - 1][NRT * RKT][64];
+    constexpr int RT = 16 * NRT, STEP = 32 * kDownWaves;
+    __shared__ float4_t part[kDownWaves - 1][NRT * RKT][64];
     const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t row0 = (int64_t)blockIdx.x * RT;
-    const int32_t id = tile_id<RT>(p, row0);
-    uint64_t left = __builtin_amdgcn_ballot_w64(id >= 0);
+    Adapters list;
+    list.id = tile_id<RT>(p, row0);
+    list.left = __builtin_amdgcn_ballot_w64(list.id >= 0);
     const int32_t k0 = (int32_t)blockIdx.y * p.k_slice, k1 = k0 + p.k_slice < p.K ? k0 + p.k_slice : p.K;
     const uint16_t* xr[NRT];
 #pragma unroll
@@ -79,10 +93,9 @@ __global__ __launch_bounds__(64 * kWaves) void mnb_lora_down_kernel(LoraParams p
         const int64_t row = row0 + 16 * n + r < p.m ? row0 + 16 * n + r : p.m - 1;
         xr[n] = p.x + row * p.x_stride + 8 * g;
     }
-    for (int j = 0; left; ++j) {
-        const int32_t a = __shfl(id, __builtin_ctzll(left));
-        const uint64_t mine = __builtin_amdgcn_ballot_w64(id == a);
-        left &= ~mine;
+    for (uint32_t j = 0; list.left; ++j) {
+        uint64_t mine;
+        const int32_t a = list.next(&mine);
         if (j % gridDim.z != blockIdx.z) continue;
         for (int c0 = 0; c0 < p.R; c0 += 16 * RKT) {
             const uint16_t* ar[RKT];
@@ -96,18 +109,28 @@ __global__ __launch_bounds__(64 * kWaves) void mnb_lora_down_kernel(LoraParams p
             for (int n = 0; n < NRT; ++n)
 #pragma unroll
                 for (int c = 0; c < RKT; ++c) acc[n][c] = float4_t{0.f, 0.f, 0.f, 0.f};
-            for (int k = k0 + 32 * wave; k < k1; k += 32 * kWaves) {
-                u32x4 av[RKT], xv[NRT];
-                const bool in = k + 8 * g < k1;      // K is a multiple of 8
-                const u32x4 zero = u32x4{0, 0, 0, 0};
+            const u32x4 zero = u32x4{0, 0, 0, 0};
+            for (int k = k0 + 32 * wave; k < k1; k += 2 * STEP) {
+                u32x4 av[2][RKT], xv[2][NRT];
 #pragma unroll
-                for (int c = 0; c < RKT; ++c) av[c] = in ? *reinterpret_cast<const u32x4*>(ar[c] + k) : zero;
+                for (int i = 0; i < 2; ++i) {
+                    const bool in = k + i * STEP + 8 * g < k1;      // K is a multiple of 8
 #pragma unroll
-                for (int n = 0; n < NRT; ++n) xv[n] = in ? *reinterpret_cast<const u32x4*>(xr[n] + k) : zero;
+                    for (int n = 0; n < NRT; ++n) {
+                        const bool some = (mine >> (16 * n)) & 0xFFFF;
+                        xv[i][n] = in && some ? *reinterpret_cast<const u32x4*>(xr[n] + k + i * STEP) : zero;
+                    }
 #pragma unroll
-                for (int n = 0; n < NRT; ++n)
+                    for (int c = 0; c < RKT; ++c)
+                        av[i][c] = in ? *reinterpret_cast<const u32x4*>(ar[c] + k + i * STEP) : zero;
+                }
 #pragma unroll
-                    for (int c = 0; c < RKT; ++c) acc[n][c] = mfma<BF16>(av[c], xv[n], acc[n][c]);
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int n = 0; n < NRT; ++n)
+                        if ((mine >> (16 * n)) & 0xFFFF)
+#pragma unroll
+                            for (int c = 0; c < RKT; ++c) acc[n][c] = mfma<BF16>(av[i][c], xv[i][n], acc[n][c]);
             }
             if (wave) {
 #pragma unroll
@@ -125,7 +148,7 @@ __global__ __launch_bounds__(64 * kWaves) void mnb_lora_down_kernel(LoraParams p
                     for (int c = 0; c < RKT; ++c) {
                         float4_t sum = acc[n][c];
 #pragma unroll
-                        for (int w = 0; w < kWaves - 1; ++w) sum += part[w][n * RKT + c][lane];
+                        for (int w = 0; w < kDownWaves - 1; ++w) sum += part[w][n * RKT + c][lane];
                         const int rank = c0 + 16 * c + 4 * g;
                         if (rank < p.R) *reinterpret_cast<float4_t*>(dst + rank) = sum;   // R is a multiple of 8
                     }
@@ -136,35 +159,134 @@ __global__ __launch_bounds__(64 * kWaves) void mnb_lora_down_kernel(LoraParams p
     }
 }
 
-// Rank to columns: a workgroup takes RT rows and 256 columns, 64 a wave.  The
-// rows' sums are scaled, split and kept in LDS.  fp16: under a power of two of
-// the row's own, so that they neither overflow nor fall below fp16's range.
-template <bool BF16, int NRT>
-__global__ __launch_bounds__(64 * kWaves) void mnb_lora_up_kernel(LoraParams p)
+// Sixteen or eight bytes at any even address.
+struct __attribute__((packed, aligned(2))) Loose16 {
+    u32x4 v;
+};
+struct __attribute__((packed, aligned(2))) Loose8 {
+    uint32_t v[2];
+};
+
+// C columns (4 or 16) of a row: base + acc * unit.
+template <int CT>
+__device__ __forceinline__ void finish(const LoraParams& p, int64_t row, int32_t col, const float4_t (&acc)[CT], float unit)
 {
-    constexpr int RT = 16 * NRT;
-    extern __shared__ uint16_t t_lds[];          // [2][RT][R32 + 8]
+    constexpr int C = 4 * CT;
+    const uint16_t* src = p.base ? p.base + row * p.base_stride + col : nullptr;
+    uint16_t* dst = p.out + row * p.out_stride + col;
+    if (col + C <= p.N) {
+        uint32_t b[C / 2] = {}, w[C / 2];
+        if (src) {
+            if constexpr (CT == 1) {
+                const Loose8 t = *reinterpret_cast<const Loose8*>(src);
+                b[0] = t.v[0];
+                b[1] = t.v[1];
+            } else {
+#pragma unroll
+                for (int i = 0; i < C / 8; ++i) {
+                    const u32x4 t = reinterpret_cast<const Loose16*>(src)[i].v;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) b[4 * i + e] = t[e];
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < C / 2; ++i) {
+            const float lo = fmaf(acc[i >> 1][2 * (i & 1)], unit, widen16(b[i] & 0xFFFFu, p.out_bf16));
+            const float hi = fmaf(acc[i >> 1][2 * (i & 1) + 1], unit, widen16(b[i] >> 16, p.out_bf16));
+            w[i] = (uint32_t)narrow16(lo, p.out_bf16) | (uint32_t)narrow16(hi, p.out_bf16) << 16;
+        }
+        if constexpr (CT == 1) {
+            *reinterpret_cast<Loose8*>(dst) = Loose8{{w[0], w[1]}};
+        } else {
+#pragma unroll
+            for (int i = 0; i < C / 8; ++i)
+                reinterpret_cast<Loose16*>(dst)[i].v = u32x4{w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]};
+        }
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+        if (col + i < p.N)
+            dst[i] = narrow16(fmaf(acc[i >> 2][i & 3], unit, src ? widen16(src[i], p.out_bf16) : 0.f), p.out_bf16);
+    }
+}
+
+// Rank to columns: a workgroup of W waves takes RT rows and 16 CT columns a wave.
+// The rows' sums are added over the slices, scaled, split and kept in LDS.  fp16:
+// under a power of two of the row's own, so that they neither overflow nor fall
+// below fp16's range.  The pieces of B, an adapter's 64 ranks at a time, come
+// up to three ahead of their products.
+template <bool BF16, int NRT, int CT, int W>
+__global__ __launch_bounds__(64 * W) void mnb_lora_up_kernel(LoraParams p)
+{
+    constexpr int RT = 16 * NRT, AHEAD = CT == 1 ? 3 : 1;
+    extern __shared__ uint16_t t_lds[];          // [2][RT][R64 + 8]
     __shared__ float t_unit[RT];
     const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t row0 = (int64_t)blockIdx.y * RT;
-    const int R32 = (p.R + 31) / 32 * 32, stride = R32 + 8;
-    const int32_t id = tile_id<RT>(p, row0);
-    // Each row by 16 neighbouring threads.
-    for (int i = threadIdx.x >> 4; i < RT; i += 64 * kWaves / 16) {
-        const int32_t a = __shfl(id, i);         // RT <= 64: the lane that holds row i
-        const int64_t row = row0 + i;
-        const float s = a >= 0 ? (p.scaling ? p.scaling[a] : 1.f) : 0.f;
+    const int R64 = (p.R + 63) / 64 * 64, stride = R64 + 8;
+    Adapters list;
+    list.id = tile_id<RT>(p, row0);
+    list.left = __builtin_amdgcn_ballot_w64(list.id >= 0);
+    // Row j of tile t of A carries column CT * 4 * (j / 4) + 4 t + j % 4, so that lane
+    // (r, g) ends with 4 CT neighbouring columns of row r.
+    const int32_t n0 = ((int32_t)blockIdx.x * W + wave) * 16 * CT;
+    const int32_t chunks = R64 / 64;
+    struct Item {
+        u32x4 b[2][CT];
+        uint64_t rows;
+    };
+    int32_t a = 0, chunk = chunks;               // of the last item fetched
+    uint64_t rows = 0;
+    const u32x4 zero = u32x4{0, 0, 0, 0};
+    auto fetch = [&](Item& it) {                 // the next item; rows 0: no more
+        if (++chunk >= chunks) {
+            chunk = 0;
+            rows = 0;
+            if (list.left) a = list.next(&rows);
+        }
+        it.rows = rows;
+        if (!rows || n0 >= p.N) {
+            it.rows = 0;
+            return;
+        }
+#pragma unroll
+        for (int t = 0; t < CT; ++t) {
+            int32_t col = n0 + 4 * CT * (r >> 2) + 4 * t + (r & 3);
+            if (col >= p.N) col = p.N - 1;
+            const uint16_t* src = p.B + ((int64_t)a * p.N + col) * p.R + 64 * chunk + 8 * g;
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+                it.b[k][t] = 64 * chunk + 32 * k + 8 * g < p.R ? *reinterpret_cast<const u32x4*>(src + 32 * k) : zero;
+        }
+    };
+    Item items[AHEAD + 1];
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) fetch(items[i]);
+
+    // Each row by 16 neighbouring threads, four ranks a time: at most 256 ranks.
+    for (int i = threadIdx.x >> 4; i < RT; i += 4 * W) {
+        const int32_t own = __shfl(list.id, i);  // RT <= 64: the lane that holds row i
+        const float s = own >= 0 ? (p.scaling ? p.scaling[own] : 1.f) : 0.f;
+        const float* src = p.t + (row0 + i) * p.R;
+        float4_t v[4];
         float top = 0.f;
-        auto value = [&](int c) {
-            if (a < 0 || c >= p.R) return 0.f;
-            float sum = 0.f;
-            for (int n = 0; n < p.splits; ++n) sum += p.t[((int64_t)n * p.m + row) * p.R + c];
-            return sum * s;
-        };
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            const int rank = 64 * c + 4 * (threadIdx.x & 15);
+            v[c] = float4_t{0.f, 0.f, 0.f, 0.f};
+            if (own >= 0 && rank < p.R) {
+#pragma unroll 8
+                for (int n = 0; n < p.splits; ++n) v[c] += *reinterpret_cast<const float4_t*>(src + (int64_t)n * p.m * p.R + rank);
+                v[c] *= s;
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) top = fmaxf(top, fabsf(v[c][e]));
+        }
         float unit = 1.f, down = 1.f;
         if constexpr (!BF16) {
-            for (int c = threadIdx.x & 15; c < R32; c += 16) top = fmaxf(top, fabsf(value(c)));
 #pragma unroll
             for (int d = 8; d; d >>= 1) top = fmaxf(top, __shfl_xor(top, d));
             // A sum that is not finite spoils its row through fp16 as it is.
@@ -173,71 +295,71 @@ __global__ __launch_bounds__(64 * kWaves) void mnb_lora_up_kernel(LoraParams p)
             unit = ldexpf(1.f, e2);
             down = ldexpf(1.f, -e2);
         }
-        for (int c = threadIdx.x & 15; c < R32; c += 16) {
-            const float v = value(c) * down;
-            const uint16_t hi = narrow16(v, BF16);
-            t_lds[i * stride + c] = hi;
-            const float rest = v - widen16(hi, BF16);
-            t_lds[(RT + i) * stride + c] = narrow16(rest, BF16);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            const int rank = 64 * c + 4 * (threadIdx.x & 15);
+            if (rank >= R64) continue;
+            uint32_t hi[2], lo[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const float x = v[c][2 * e] * down, y = v[c][2 * e + 1] * down;
+                const uint16_t xh = narrow16(x, BF16), yh = narrow16(y, BF16);
+                hi[e] = (uint32_t)xh | (uint32_t)yh << 16;
+                lo[e] = (uint32_t)narrow16(x - widen16(xh, BF16), BF16) |
+                        (uint32_t)narrow16(y - widen16(yh, BF16), BF16) << 16;
+            }
+            uint32_t* to = reinterpret_cast<uint32_t*>(t_lds + i * stride + rank);
+            to[0] = hi[0];
+            to[1] = hi[1];
+            to = reinterpret_cast<uint32_t*>(t_lds + (RT + i) * stride + rank);
+            to[0] = lo[0];
+            to[1] = lo[1];
         }
         if ((threadIdx.x & 15) == 0) t_unit[i] = unit;
     }
     __syncthreads();
-    // Row j of tile t of A carries column 16 (j / 4) + 4 t + j % 4, so that lane
-    // (r, g) ends with columns 16 g .. 16 g + 15 of row r.
-    const int32_t n0 = (int32_t)blockIdx.x * 256 + 64 * wave;
     if (n0 >= p.N) return;
-    float4_t acc[NRT][4];
+    float4_t acc[NRT][CT];
 #pragma unroll
     for (int n = 0; n < NRT; ++n)
 #pragma unroll
-        for (int t = 0; t < 4; ++t) acc[n][t] = float4_t{0.f, 0.f, 0.f, 0.f};
-    uint64_t left = __builtin_amdgcn_ballot_w64(id >= 0);
-    const u32x4 zero = u32x4{0, 0, 0, 0};
-    while (left) {
-        const int32_t a = __shfl(id, __builtin_ctzll(left));
-        const uint64_t mine = __builtin_amdgcn_ballot_w64(id == a);
-        left &= ~mine;
-        const uint16_t* br[4];
+        for (int t = 0; t < CT; ++t) acc[n][t] = float4_t{0.f, 0.f, 0.f, 0.f};
+    int at = 0;                                  // chunk of the item in hand
+    auto multiply = [&](const Item& it) {
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
-            int32_t col = n0 + 16 * (r >> 2) + 4 * t + (r & 3);
-            if (col >= p.N) col = p.N - 1;
-            br[t] = p.B + ((int64_t)a * p.N + col) * p.R + 8 * g;
-        }
-        for (int k = 0; k < p.R; k += 32) {
-            u32x4 bv[4];
-            const bool in = k + 8 * g < p.R;
-#pragma unroll
-            for (int t = 0; t < 4; ++t) bv[t] = in ? *reinterpret_cast<const u32x4*>(br[t] + k) : zero;
+        for (int k = 0; k < 2; ++k) {
+            if (64 * at + 32 * k >= p.R) continue;
 #pragma unroll
             for (int n = 0; n < NRT; ++n) {
-                if (!((mine >> (16 * n)) & 0xFFFF)) continue;
-                const bool own = (mine >> (16 * n + r)) & 1;
-                const u32x4 hi = own ? *reinterpret_cast<const u32x4*>(t_lds + (16 * n + r) * stride + k + 8 * g) : zero;
-                const u32x4 lo = own ? *reinterpret_cast<const u32x4*>(t_lds + (RT + 16 * n + r) * stride + k + 8 * g) : zero;
+                if (!((it.rows >> (16 * n)) & 0xFFFF)) continue;
+                const bool own = (it.rows >> (16 * n + r)) & 1;
+                const int from = (16 * n + r) * stride + 64 * at + 32 * k + 8 * g;
+                const u32x4 hi = own ? *reinterpret_cast<const u32x4*>(t_lds + from) : zero;
+                const u32x4 lo = own ? *reinterpret_cast<const u32x4*>(t_lds + RT * stride + from) : zero;
 #pragma unroll
-                for (int t = 0; t < 4; ++t) {
-                    acc[n][t] = mfma<BF16>(bv[t], hi, acc[n][t]);
-                    acc[n][t] = mfma<BF16>(bv[t], lo, acc[n][t]);
+                for (int t = 0; t < CT; ++t) {
+                    acc[n][t] = mfma<BF16>(it.b[k][t], hi, acc[n][t]);
+                    acc[n][t] = mfma<BF16>(it.b[k][t], lo, acc[n][t]);
                 }
             }
+        }
+        at = at + 1 < chunks ? at + 1 : 0;
+    };
+    bool more = true;
+    while (more) {
+#pragma unroll
+        for (int i = 0; i <= AHEAD; ++i) {
+            if (!more) continue;
+            more = items[i].rows != 0;
+            if (!more) continue;
+            fetch(items[(i + AHEAD) % (AHEAD + 1)]);
+            multiply(items[i]);
         }
     }
 #pragma unroll
     for (int n = 0; n < NRT; ++n) {
         const int64_t row = row0 + 16 * n + r;
-        if (row >= p.m) continue;
-        const float unit = t_unit[16 * n + r];
-        const int32_t col = n0 + 16 * g;
-        const uint16_t* src = p.base ? p.base + row * p.base_stride + col : nullptr;
-        uint16_t* dst = p.out + row * p.out_stride + col;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            if (col + i >= p.N) break;
-            const float b = src ? widen16(src[i], p.out_bf16) : 0.f;
-            dst[i] = narrow16(fmaf(acc[n][i >> 2][i & 3], unit, b), p.out_bf16);
-        }
+        if (row < p.m && n0 + 4 * CT * g < p.N) finish<CT>(p, row, n0 + 4 * CT * g, acc[n], t_unit[16 * n + r]);
     }
 }
 
@@ -245,28 +367,36 @@ template <bool BF16, int NRT, int RKT>
 int queue_down(const LoraParams& p, unsigned ways, hipStream_t s)
 {
     hipLaunchKernelGGL((mnb_lora_down_kernel<BF16, NRT, RKT>),
-                       dim3((unsigned)((p.m + 16 * NRT - 1) / (16 * NRT)), (unsigned)p.splits, ways), dim3(64 * kWaves), 0, s, p);
+                       dim3((unsigned)((p.m + 16 * NRT - 1) / (16 * NRT)), (unsigned)p.splits, ways), dim3(64 * kDownWaves), 0, s, p);
+    return (int)hipGetLastError();
+}
+
+template <bool BF16, int NRT, int CT, int W>
+int queue_up(const LoraParams& p, hipStream_t s)
+{
+    constexpr int COLS = 16 * CT * W;
+    const size_t lds = (size_t)2 * 16 * NRT * ((p.R + 63) / 64 * 64 + 8) * 2;
+    hipLaunchKernelGGL((mnb_lora_up_kernel<BF16, NRT, CT, W>),
+                       dim3((unsigned)((p.N + COLS - 1) / COLS), (unsigned)((p.m + 16 * NRT - 1) / (16 * NRT))),
+                       dim3(64 * W), lds, s, p);
     return (int)hipGetLastError();
 }
 
 template <bool BF16, int NRT>
-int queue(const LoraParams& p, unsigned ways, hipStream_t s)
+int queue(const LoraParams& p, const LoraLayout& lay, hipStream_t s)
 {
-    const int e = p.R <= 16 ? queue_down<BF16, NRT, 1>(p, ways, s)
-                : p.R <= 32 ? queue_down<BF16, NRT, 2>(p, ways, s) : queue_down<BF16, NRT, 4>(p, ways, s);
+    const unsigned ways = (unsigned)lay.ways;
+    const int e = p.R <= 16 ? queue_down<BF16, NRT, 1>(p, ways, s) : p.R <= 32 ? queue_down<BF16, NRT, 2>(p, ways, s)
+                : p.R <= 48 ? queue_down<BF16, NRT, 3>(p, ways, s) : queue_down<BF16, NRT, 4>(p, ways, s);
     if (e != 0) return e;
-    const size_t lds = (size_t)2 * 16 * NRT * ((p.R + 31) / 32 * 32 + 8) * 2;
-    hipLaunchKernelGGL((mnb_lora_up_kernel<BF16, NRT>),
-                       dim3((unsigned)((p.N + 255) / 256), (unsigned)((p.m + 16 * NRT - 1) / (16 * NRT))),
-                       dim3(64 * kWaves), lds, s, p);
-    return (int)hipGetLastError();
+    return lay.wide ? queue_up<BF16, NRT, 4, 8>(p, s) : queue_up<BF16, NRT, 1, 4>(p, s);
 }
 
 }  // namespace
 
 int launch_lora(const LoraArgs& a, void* stream, int* launches)
 {
-    const LoraLayout lay = lora_layout(a.m, a.K, a.R);
+    const LoraLayout lay = lora_layout(a.m, a.K, a.N, a.R, a.adapters);
     LoraParams p{};
     p.x = static_cast<const uint16_t*>(a.x);
     p.ids = a.ids;
@@ -289,12 +419,9 @@ int launch_lora(const LoraArgs& a, void* stream, int* launches)
     p.out_bf16 = a.out_bf16;
     const hipStream_t s = static_cast<hipStream_t>(stream);
     *launches = 2;
-    if (lay.row_tiles == 1) {
-        const unsigned ways = (unsigned)(a.adapters < 1 ? 1 : a.adapters < 16 ? a.adapters : 16);
-        return a.bf16 ? queue<true, 1>(p, ways, s) : queue<false, 1>(p, ways, s);
-    }
-    if (lay.row_tiles == 2) return a.bf16 ? queue<true, 2>(p, 1, s) : queue<false, 2>(p, 1, s);
-    return a.bf16 ? queue<true, 4>(p, 1, s) : queue<false, 4>(p, 1, s);
+    if (lay.row_tiles == 1) return a.bf16 ? queue<true, 1>(p, lay, s) : queue<false, 1>(p, lay, s);
+    if (lay.row_tiles == 2) return a.bf16 ? queue<true, 2>(p, lay, s) : queue<false, 2>(p, lay, s);
+    return a.bf16 ? queue<true, 4>(p, lay, s) : queue<false, 4>(p, lay, s);
 }
 
 }  // namespace mnb
