@@ -110,27 +110,32 @@ __global__ __launch_bounds__(64 * kDownWaves) void mnb_lora_down_kernel(LoraPara
 #pragma unroll
                 for (int c = 0; c < RKT; ++c) acc[n][c] = float4_t{0.f, 0.f, 0.f, 0.f};
             const u32x4 zero = u32x4{0, 0, 0, 0};
-            for (int k = k0 + 32 * wave; k < k1; k += 2 * STEP) {
-                u32x4 av[2][RKT], xv[2][NRT];
+            u32x4 av[2][RKT], xv[2][NRT];
+            auto load = [&](int k, u32x4 (&a2)[RKT], u32x4 (&x2)[NRT]) {
+                const bool in = k + 8 * g < k1;              // K is a multiple of 8
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const bool in = k + i * STEP + 8 * g < k1;      // K is a multiple of 8
+                for (int n = 0; n < NRT; ++n)
+                    x2[n] = in && ((mine >> (16 * n)) & 0xFFFF) ? *reinterpret_cast<const u32x4*>(xr[n] + k) : zero;
 #pragma unroll
-                    for (int n = 0; n < NRT; ++n) {
-                        const bool some = (mine >> (16 * n)) & 0xFFFF;
-                        xv[i][n] = in && some ? *reinterpret_cast<const u32x4*>(xr[n] + k + i * STEP) : zero;
-                    }
+                for (int c = 0; c < RKT; ++c) a2[c] = in ? *reinterpret_cast<const u32x4*>(ar[c] + k) : zero;
+            };
+            auto multiply = [&](const u32x4 (&a2)[RKT], const u32x4 (&x2)[NRT]) {
 #pragma unroll
-                    for (int c = 0; c < RKT; ++c)
-                        av[i][c] = in ? *reinterpret_cast<const u32x4*>(ar[c] + k + i * STEP) : zero;
-                }
+                for (int n = 0; n < NRT; ++n)
+                    if ((mine >> (16 * n)) & 0xFFFF)
 #pragma unroll
-                for (int i = 0; i < 2; ++i)
-#pragma unroll
-                    for (int n = 0; n < NRT; ++n)
-                        if ((mine >> (16 * n)) & 0xFFFF)
-#pragma unroll
-                            for (int c = 0; c < RKT; ++c) acc[n][c] = mfma<BF16>(av[i][c], xv[i][n], acc[n][c]);
+                        for (int c = 0; c < RKT; ++c) acc[n][c] = mfma<BF16>(a2[c], x2[n], acc[n][c]);
+            };
+            int k = k0 + 32 * wave;
+            load(k, av[0], xv[0]);
+            load(k + STEP, av[1], xv[1]);
+            for (; k < k1; k += 2 * STEP) {
+                multiply(av[0], xv[0]);
+                load(k + 2 * STEP, av[0], xv[0]);
+                __builtin_amdgcn_sched_barrier(0);
+                multiply(av[1], xv[1]);
+                load(k + 3 * STEP, av[1], xv[1]);
+                __builtin_amdgcn_sched_barrier(0);
             }
             if (wave) {
 #pragma unroll
@@ -167,29 +172,33 @@ struct __attribute__((packed, aligned(2))) Loose8 {
     uint32_t v[2];
 };
 
-// C columns (4 or 16) of a row: base + acc * unit.
+// C = 4 CT columns of a row's base; whole: none lies behind the last one.
 template <int CT>
-__device__ __forceinline__ void finish(const LoraParams& p, int64_t row, int32_t col, const float4_t (&acc)[CT], float unit)
+__device__ __forceinline__ void load_base(const uint16_t* src, uint32_t (&b)[2 * CT])
+{
+    if constexpr (CT == 1) {
+        const Loose8 t = *reinterpret_cast<const Loose8*>(src);
+        b[0] = t.v[0];
+        b[1] = t.v[1];
+    } else {
+#pragma unroll
+        for (int i = 0; i < CT / 2; ++i) {
+            const u32x4 t = reinterpret_cast<const Loose16*>(src)[i].v;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) b[4 * i + e] = t[e];
+        }
+    }
+}
+
+// base + acc * unit.
+template <int CT>
+__device__ __forceinline__ void finish(const LoraParams& p, int64_t row, int32_t col, bool whole, const uint32_t (&b)[2 * CT],
+                                       const float4_t (&acc)[CT], float unit)
 {
     constexpr int C = 4 * CT;
-    const uint16_t* src = p.base ? p.base + row * p.base_stride + col : nullptr;
     uint16_t* dst = p.out + row * p.out_stride + col;
-    if (col + C <= p.N) {
-        uint32_t b[C / 2] = {}, w[C / 2];
-        if (src) {
-            if constexpr (CT == 1) {
-                const Loose8 t = *reinterpret_cast<const Loose8*>(src);
-                b[0] = t.v[0];
-                b[1] = t.v[1];
-            } else {
-#pragma unroll
-                for (int i = 0; i < C / 8; ++i) {
-                    const u32x4 t = reinterpret_cast<const Loose16*>(src)[i].v;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) b[4 * i + e] = t[e];
-                }
-            }
-        }
+    if (whole) {
+        uint32_t w[C / 2];
 #pragma unroll
         for (int i = 0; i < C / 2; ++i) {
             const float lo = fmaf(acc[i >> 1][2 * (i & 1)], unit, widen16(b[i] & 0xFFFFu, p.out_bf16));
@@ -200,11 +209,12 @@ __device__ __forceinline__ void finish(const LoraParams& p, int64_t row, int32_t
             *reinterpret_cast<Loose8*>(dst) = Loose8{{w[0], w[1]}};
         } else {
 #pragma unroll
-            for (int i = 0; i < C / 8; ++i)
+            for (int i = 0; i < CT / 2; ++i)
                 reinterpret_cast<Loose16*>(dst)[i].v = u32x4{w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]};
         }
         return;
     }
+    const uint16_t* src = p.base ? p.base + row * p.base_stride + col : nullptr;
 #pragma unroll
     for (int i = 0; i < C; ++i) {
         if (col + i < p.N)
@@ -265,6 +275,17 @@ __global__ __launch_bounds__(64 * W) void mnb_lora_up_kernel(LoraParams p)
     Item items[AHEAD + 1];
 #pragma unroll
     for (int i = 0; i < AHEAD; ++i) fetch(items[i]);
+
+    // The base of this lane's columns.
+    const int32_t mine0 = n0 + 4 * CT * g;
+    const bool whole = mine0 + 4 * CT <= p.N;
+    uint32_t base[NRT][2 * CT];
+#pragma unroll
+    for (int n = 0; n < NRT; ++n) {
+#pragma unroll
+        for (int i = 0; i < 2 * CT; ++i) base[n][i] = 0;
+        if (p.base && whole && row0 + 16 * n + r < p.m) load_base<CT>(p.base + (row0 + 16 * n + r) * p.base_stride + mine0, base[n]);
+    }
 
     // Each row by 16 neighbouring threads, four ranks a time: at most 256 ranks.
     for (int i = threadIdx.x >> 4; i < RT; i += 4 * W) {
@@ -359,7 +380,7 @@ __global__ __launch_bounds__(64 * W) void mnb_lora_up_kernel(LoraParams p)
 #pragma unroll
     for (int n = 0; n < NRT; ++n) {
         const int64_t row = row0 + 16 * n + r;
-        if (row < p.m && n0 + 4 * CT * g < p.N) finish<CT>(p, row, n0 + 4 * CT * g, acc[n], t_unit[16 * n + r]);
+        if (row < p.m && mine0 < p.N) finish<CT>(p, row, mine0, whole, base[n], acc[n], t_unit[16 * n + r]);
     }
 }
 
