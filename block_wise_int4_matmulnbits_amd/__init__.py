@@ -11,7 +11,6 @@ no fallback: if the library is missing, importing the entry points raises.
 from __future__ import annotations
 
 import ctypes
-import functools
 import os
 import threading
 
@@ -493,82 +492,35 @@ def mnb_moe_workspace(tokens, hidden, inter, experts, top_k):
 
 
 # ------------------------------------- 8-bit cache, attention and adapters
-# Called once per layer and token too: each call's tensors pass one condition,
-# and only where it fails are they looked at one by one for what is wrong.
-def _strided(name, t, shape, dtype, index):
-    """t has this shape and type, is on GPU ``index`` and dense but for its
-    first dimension; returns the elements from one row to the next."""
-    if t.dtype != dtype:
-        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
-    if t.shape != shape:
-        raise ValueError("%s must be %s, got %s" % (name, list(shape), list(t.shape)))
-    if t.get_device() != index:
-        raise ValueError("%s must be on the GPU of the first argument, got %s" % (name, t.device))
-    strides, width = t.stride(), 1
-    for d in range(len(shape) - 1, 0, -1):
-        if shape[d] != 1 and strides[d] != width:
-            raise ValueError("%s must be contiguous but for its first dimension" % name)
-        width *= shape[d]
-    return strides[0] if shape[0] > 1 else width
+# Their arguments are checked and handed on by the module mnb_torch.so
+# (csrc/mnb_torch.cpp, built with the library): in Python that takes longer than
+# the kernels of a single token.
+_native = None
 
 
-def _kv(x, starts, lengths, page_table, k_pages, v_pages, k_scales, v_scales, index):
-    """The cache and the batch of a call as the library takes them."""
-    if k_pages.dim() != 4 or page_table.dim() != 2 or lengths.dim() != 1:
-        raise ValueError("k_pages must be 4-D, page_table 2-D, lengths 1-D")
-    i8, i32, f32 = _types or _load_types()
-    pages, heads, P, D = k_pages.shape
-    S, width = page_table.shape
-    if not (k_pages.dtype is v_pages.dtype is i8 and k_scales.dtype is v_scales.dtype is f32
-            and starts.dtype is lengths.dtype is page_table.dtype is i32
-            and v_pages.shape == (pages, heads, D, P) and k_scales.shape == v_scales.shape == (pages, heads)
-            and lengths.shape[0] == S and starts.shape == (S + 1,)
-            and k_pages.get_device() == v_pages.get_device() == k_scales.get_device() == v_scales.get_device()
-            == starts.get_device() == lengths.get_device() == page_table.get_device() == index
-            and k_pages.is_contiguous() and v_pages.is_contiguous() and k_scales.is_contiguous()
-            and v_scales.is_contiguous() and starts.is_contiguous() and lengths.is_contiguous()
-            and page_table.is_contiguous()):
-        S = lengths.shape[0]
-        _expect("k_pages", k_pages, (pages, heads, P, D), i8, index)
-        _expect("v_pages", v_pages, (pages, heads, D, P), i8, index)
-        _expect("k_scales", k_scales, (pages, heads), f32, index)
-        _expect("v_scales", v_scales, (pages, heads), f32, index)
-        _expect("starts", starts, (S + 1,), i32, index)
-        _expect("lengths", lengths, (S,), i32, index)
-        _expect("page_table", page_table, (S, width), i32, index)
-    return (mnb_kv_cache(pages, P, heads, D, k_pages.data_ptr(), v_pages.data_ptr(), k_scales.data_ptr(),
-                         v_scales.data_ptr()),
-            mnb_kv_batch(S, x.shape[0], width, starts.data_ptr(), lengths.data_ptr(), page_table.data_ptr()),
-            heads, D)
+def _load_native():
+    """The module mnb_torch.so (raises if it has not been built), bound to the
+    loaded library."""
+    global _native
+    import torch    # noqa: F401 (the module links with it)
+    L = lib()
+    path = os.path.join(_HERE, "mnb_torch.so")
+    if not os.path.exists(path):
+        raise ImportError("mnb_torch.so is not built (%s); run __graft_entry__.build() or "
+                          "python block_wise_int4_matmulnbits_amd/build.py" % path)
+    from . import mnb_torch
+    with _lock:
+        mnb_torch.bind(*[ctypes.cast(f, ctypes.c_void_p).value for f in (
+            L.append_kv_int8, L.attention_int8, L.mnb_attention_workspace, L.matmul_lora, L.mnb_lora_workspace)])
+        _native = mnb_torch
+    return mnb_torch
 
 
-_types = None
-
-
-def _load_types():
-    global _types
-    import torch
-    _types = (torch.int8, torch.int32, torch.float32)
-    return _types
-
-
-def _on_gpu(name, t, dim):
-    if t.dim() != dim:
-        raise ValueError("%s must be %d-D" % (name, dim))
+def _gpu_of(name, t):
     index = t.get_device()
     if index < 0:
         raise ValueError("%s must be on the GPU" % name)
     return index
-
-
-@functools.lru_cache(maxsize=4096)
-def _attention_bytes(tokens, sequences, q_heads, kv_heads, head_dim):
-    return lib().mnb_attention_workspace(tokens, sequences, q_heads, kv_heads, head_dim)
-
-
-@functools.lru_cache(maxsize=4096)
-def _lora_bytes(m, K, N, rank, adapters):
-    return lib().mnb_lora_workspace(m, K, N, rank, adapters)
 
 
 def append_kv_int8(k, v, cos, sin, starts, lengths, page_table, k_pages, v_pages, k_scales, v_scales, q=None,
@@ -587,37 +539,9 @@ def append_kv_int8(k, v, cos, sin, starts, lengths, page_table, k_pages, v_pages
     * scale.  interleaved: pairs are neighbours, not half the rotated width
     apart.  Queued on ``stream``; returns q_out.
     """
-    L = _lib or lib()
-    index = _on_gpu("k", k, 3)
-    T = k.shape[0]
-    dtype = k.dtype
-    code = _dtype_code(k)
-    cache, batch, heads, D = _kv(k, starts, lengths, page_table, k_pages, v_pages, k_scales, v_scales, index)
-    shape = (T, heads, D)
-    ks = _strided("k", k, shape, dtype, index)
-    vs = _strided("v", v, shape, dtype, index)
-    qp = op = cp = sp = None
-    qs = os_ = q_heads = rot = rows = 0
-    if q is not None and q_out is not None:
-        _on_gpu("q", q, 3)
-        q_heads = q.shape[1]
-        shape = (T, q_heads, D)
-        qs = _strided("q", q, shape, dtype, index)
-        os_ = _strided("q_out", q_out, shape, dtype, index)
-        qp, op = q.data_ptr(), q_out.data_ptr()
-    elif q is not q_out:
-        raise ValueError("q and q_out go together")
-    if cos is not None and sin is not None:
-        if cos.dim() != 2:
-            raise ValueError("cos must be 2-D")
-        rows, half = shape = cos.shape
-        _expect("cos", cos, shape, _types[2], index)
-        _expect("sin", sin, shape, _types[2], index)
-        rot, cp, sp = 2 * half, cos.data_ptr(), sin.data_ptr()
-    elif cos is not sin:
-        raise ValueError("cos and sin go together")
-    _on_device(index, stream, L.append_kv_int8, cache, batch, code, k.data_ptr(), ks, v.data_ptr(), vs, qp, qs, op, os_,
-               q_heads, cp, sp, rot, rows, 1 if interleaved else 0)
+    N = _native or _load_native()
+    _on_device(_gpu_of("k", k), stream, N.append_kv_int8, k, v, cos, sin, starts, lengths, page_table, k_pages, v_pages,
+               k_scales, v_scales, q, q_out, interleaved)
     return q_out
 
 
@@ -635,21 +559,13 @@ def attention_int8(q, starts, lengths, page_table, k_pages, v_pages, k_scales, v
     mnb_attention_workspace(...) bytes, or None for one of torch's allocator.
     Queued on ``stream``; returns ``out``.
     """
-    L = _lib or lib()
-    index = _on_gpu("q", q, 3)
-    shape = T, q_heads, D = q.shape
-    dtype = q.dtype
-    code = _dtype_code(q)
-    cache, batch, heads, head_dim = _kv(q, starts, lengths, page_table, k_pages, v_pages, k_scales, v_scales, index)
-    if D != head_dim:
-        raise ValueError("q must be [tokens, query heads, %d]" % head_dim)
-    qs = _strided("q", q, shape, dtype, index)
-    os_ = _strided("out", out, shape, dtype, index)
-    need = _attention_bytes(T, batch.sequences, q_heads, heads, D) if workspace is None else 0
-    ws = _workspace(q, need, workspace, stream, index) if need or workspace is not None else None
-    _on_device(index, stream, L.attention_int8, cache, batch, code, q.data_ptr(), qs, q_heads,
-               D ** -0.5 if scale is None else scale, out.data_ptr(), os_, max_tokens or 0,
-               None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel() * ws.element_size())
+    N = _native or _load_native()
+    index = _gpu_of("q", q)
+    if stream is not None and workspace is None:
+        need = _lib.mnb_attention_workspace(q.shape[0], lengths.shape[0], q.shape[1], k_pages.shape[1], q.shape[2])
+        workspace = _workspace(q, need, None, stream, index)
+    _on_device(index, stream, N.attention_int8, q, starts, lengths, page_table, k_pages, v_pages, k_scales, v_scales, out,
+               scale, max_tokens, workspace)
     return out
 
 
@@ -670,33 +586,12 @@ def matmul_lora(x, ids, A, B, base, out, scaling=None, workspace=None, stream=No
     tensor of at least mnb_lora_workspace(...) bytes, or None for one of
     torch's allocator.  Queued on ``stream``; returns ``out``.
     """
-    import torch
-    L = _lib or lib()
-    index = _on_gpu("x", x, 2)
-    m, K = x.shape
-    if A.dim() != 3 or B.dim() != 3 or out.dim() != 2:
-        raise ValueError("A and B must be 3-D, out 2-D")
-    n, R = A.shape[0], A.shape[1]
-    N = B.shape[1]
-    x_dt, o_dt = _dtype_code(x), _dtype_code(out)
-    xs = _strided("x", x, (m, K), x.dtype, index)
-    os_ = _strided("out", out, (m, N), out.dtype, index)
-    _expect("ids", ids, (m,), torch.int32, index)
-    _expect("A", A, (n, R, K), x.dtype, index)
-    _expect("B", B, (n, N, R), x.dtype, index)
-    sp = bp = None
-    bs = 0
-    if scaling is not None:
-        _expect("scaling", scaling, (n,), torch.float32, index)
-        sp = scaling.data_ptr()
-    if base is not None:
-        bs = _strided("base", base, (m, N), out.dtype, index)
-        bp = base.data_ptr()
-    need = _lora_bytes(m, K, N, R, n) if workspace is None else 0
-    ws = _workspace(x, need, workspace, stream, index) if need or workspace is not None else None
-    _on_device(index, stream, L.matmul_lora, x.data_ptr(), x_dt, xs, m, K, N, R, n, ids.data_ptr(), A.data_ptr(),
-               B.data_ptr(), sp, bp, bs, out.data_ptr(), os_, o_dt, None if ws is None else ws.data_ptr(),
-               0 if ws is None else ws.numel() * ws.element_size())
+    N = _native or _load_native()
+    index = _gpu_of("x", x)
+    if stream is not None and workspace is None:
+        need = _lib.mnb_lora_workspace(x.shape[0], x.shape[1], B.shape[1], A.shape[1], A.shape[0])
+        workspace = _workspace(x, need, None, stream, index)
+    _on_device(index, stream, N.matmul_lora, x, ids, A, B, base, out, scaling, workspace)
     return out
 
 

@@ -4,7 +4,8 @@ hipcc compiles the kernels (mnb_gemv.hip, mnb_gemv_mfma4.hip,
 mnb_gemm_mfma.hip, mnb_layout.hip, mnb_int8.hip, mnb_moe.hip,
 mnb_append.hip, mnb_attention.hip, mnb_lora.hip); the host front end
 (mnb_api.cpp) is plain C++ built with g++; hipcc links both into one shared
-library next to this file.
+library next to this file.  mnb_torch.cpp, the part of the Python binding that is
+compiled, becomes a module of its own there.
 """
 from __future__ import annotations
 
@@ -18,6 +19,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmnb.so")
 PROBE_LIB = os.path.join(HERE, "libmnb_probe.so")
+TORCH_MODULE = os.path.join(HERE, "mnb_torch.so")
 ARCH = "gfx950"
 
 HIP_FLAGS = [
@@ -28,6 +30,22 @@ HIP_FLAGS = [
 ]
 CXX_FLAGS = ["-O2", "-std=c++17", "-fPIC", "-Wall", "-Wextra", "-I", INCLUDE,
              "-I", CSRC]
+
+
+def _torch_flags():
+    """Compiler and linker flags of the binding's module, which uses torch's
+    tensors (no GPU code)."""
+    import sysconfig
+    import torch
+    root = os.path.dirname(torch.__file__)
+    abi = int(torch._C._GLIBCXX_USE_CXX11_ABI)
+    include = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+               sysconfig.get_paths()["include"]]
+    # (torch's headers warn under -Wextra)
+    flags = ["-O2", "-std=c++17", "-fPIC", "-Wall", "-D_GLIBCXX_USE_CXX11_ABI=%d" % abi, "-I", INCLUDE]
+    for path in include:
+        flags += ["-isystem", path]
+    return flags, ["-L" + os.path.join(root, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10"]
 
 
 def _run(cmd, verbose):
@@ -51,11 +69,16 @@ def build(verbose: bool = False, save_temps: bool = False) -> str:
     api_o = os.path.join(BUILD, "mnb_api.o")
     objs.append(api_o)
     jobs.append(["g++", "-c", os.path.join(CSRC, "mnb_api.cpp"), "-o", api_o] + CXX_FLAGS)
+    # The binding's module: named only when it is whole.
+    flags, libs = _torch_flags()
+    module = TORCH_MODULE + ".tmp%d" % os.getpid()
+    jobs.append(["g++", "-shared", os.path.join(CSRC, "mnb_torch.cpp"), "-o", module] + flags + libs)
     # The translation units are independent: compile them side by side.
     from concurrent.futures import ThreadPoolExecutor
     with ThreadPoolExecutor(max_workers=len(jobs)) as ex:
         for f in [ex.submit(_run, cmd, verbose) for cmd in jobs]:
             f.result()
+    os.replace(module, TORCH_MODULE)
     tmp = LIB + ".tmp%d" % os.getpid()
     _run(["hipcc", "-shared", "-fPIC", "--offload-arch=" + ARCH, "-o", tmp] + objs, verbose)
     os.replace(tmp, LIB)

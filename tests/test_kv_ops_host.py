@@ -177,16 +177,26 @@ def test_binding_refuses_cpu_tensors_and_shapes():
         mnb.matmul_lora(x, i, x, x, None, x[0])
 
 
-def test_rows_are_dense_but_for_the_first_dimension():
-    """The stride that the binding passes on, on CPU tensors."""
+def test_module_refuses_what_is_no_gpu_tensor():
+    """The compiled part of the binding on CPU tensors and other objects: errors in
+    Python's manner, nothing launched."""
     import torch
-    from block_wise_int4_matmulnbits_amd import _strided
-    f = torch.zeros(5, 10, 64, dtype=torch.float16)
-    assert _strided("x", f[:, 2:6], (5, 4, 64), torch.float16, -1) == 640
-    assert _strided("x", f[:1, 2:6], (1, 4, 64), torch.float16, -1) == 256
-    assert _strided("x", f[:, 3:4], (5, 1, 64), torch.float16, -1) == 640
-    for bad in (f[:, ::2], f.transpose(0, 1), f[..., ::2]):
-        with pytest.raises(ValueError):
-            _strided("x", bad, tuple(bad.shape), torch.float16, -1)
-    with pytest.raises(TypeError):
-        _strided("x", f, (5, 10, 64), torch.bfloat16, -1)
+    N = mnb._load_native()
+    x = torch.zeros(2, 4, 64, dtype=torch.float16)
+    i = torch.zeros(3, dtype=torch.int32)
+    k = torch.zeros(3, 4, 16, 64, dtype=torch.int8)
+    s = torch.zeros(3, 4)
+    cache = (i, i[:2], i[None], k, k, s, s)
+    c0 = mnb.mnb_counters_get()
+    for call, error in ((lambda: N.append_kv_int8(x), TypeError), (lambda: N.attention_int8(), TypeError),
+                        (lambda: N.matmul_lora(1, 2, 3, 4, 5, 6, 7, 8, 9), TypeError),
+                        (lambda: N.append_kv_int8(x, x, None, None, *cache, None, None, False, 0), ValueError),
+                        (lambda: N.append_kv_int8(x[0], x, None, None, *cache, None, None, False, 0), ValueError),
+                        (lambda: N.append_kv_int8(x.float(), x, None, None, *cache, None, None, False, 0), TypeError),
+                        (lambda: N.append_kv_int8(x, None, None, None, *cache, None, None, False, 0), ValueError),
+                        (lambda: N.attention_int8(x, *cache, x, None, None, None, 0), ValueError),
+                        (lambda: N.attention_int8("x", *cache, x, None, None, None, 0), TypeError),
+                        (lambda: N.matmul_lora(x[0], i, x, x, None, x[0], None, None, 0), ValueError)):
+        with pytest.raises(error):
+            call()
+    assert mnb.mnb_counters_get() == c0
