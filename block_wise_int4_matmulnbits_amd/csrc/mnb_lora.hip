@@ -276,16 +276,21 @@ __global__ __launch_bounds__(64 * W) void mnb_lora_up_kernel(LoraParams p)
 #pragma unroll
     for (int i = 0; i < AHEAD; ++i) fetch(items[i]);
 
-    // The base of this lane's columns.
+    // The base of this lane's columns; with few rows and many adapters, behind their
+    // weights.
     const int32_t mine0 = n0 + 4 * CT * g;
     const bool whole = mine0 + 4 * CT <= p.N;
     uint32_t base[NRT][2 * CT];
+    auto read_base = [&] {
 #pragma unroll
-    for (int n = 0; n < NRT; ++n) {
+        for (int n = 0; n < NRT; ++n) {
 #pragma unroll
-        for (int i = 0; i < 2 * CT; ++i) base[n][i] = 0;
-        if (p.base && whole && row0 + 16 * n + r < p.m) load_base<CT>(p.base + (row0 + 16 * n + r) * p.base_stride + mine0, base[n]);
-    }
+            for (int i = 0; i < 2 * CT; ++i) base[n][i] = 0;
+            if (p.base && whole && row0 + 16 * n + r < p.m)
+                load_base<CT>(p.base + (row0 + 16 * n + r) * p.base_stride + mine0, base[n]);
+        }
+    };
+    if (CT > 1) read_base();
 
     // Each row by 16 neighbouring threads, four ranks a time: at most 256 ranks.
     for (int i = threadIdx.x >> 4; i < RT; i += 4 * W) {
@@ -377,6 +382,7 @@ __global__ __launch_bounds__(64 * W) void mnb_lora_up_kernel(LoraParams p)
             multiply(items[i]);
         }
     }
+    if (CT == 1) read_base();
 #pragma unroll
     for (int n = 0; n < NRT; ++n) {
         const int64_t row = row0 + 16 * n + r;
