@@ -647,7 +647,7 @@ AttentionLayout attention_layout(int64_t tokens, int64_t sequences, int64_t q_he
     const size_t parts = 2 * (size_t)kAttentionWorkgroups, D = (size_t)head_dim;
     l.o = parts * 16 * 2 * 4;
     l.tile_ml = l.o + parts * 16 * D * 4;
-    const int64_t rows = tokens * (q_heads / kv_heads), tile = 32 * tile_waves(head_dim);
+    const int64_t rows = tokens * (q_heads / kv_heads), tile = tile_rows(head_dim);
     // Full tiles, and one more for each sequence that can have many rows.
     l.tile_slots = rows > kAttentionManyRows
                        ? (int)(rows / tile + std::min<int64_t>(sequences, rows / (kAttentionManyRows + 1))) : 0;

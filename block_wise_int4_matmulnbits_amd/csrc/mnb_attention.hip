@@ -643,8 +643,9 @@ __device__ __forceinline__ void widen_bytes(i32x4 w, uint32_t r2, uint32_t half_
 template <int D, bool BF16>
 __global__ __launch_bounds__(64 * tile_waves(D), D == 64 ? 2 : 1) void mnb_attention_tile_kernel(AttentionParams p)
 {
-    constexpr int NW = tile_waves(D), BR = 32 * NW, THREADS = 64 * NW;
-    constexpr int KQ = D / 16, DB = D / 32;
+    constexpr int NW = tile_waves(D), BR = tile_rows(D), THREADS = 64 * NW;
+    constexpr int SHARE = 32 * NW / BR;                    // waves that share rows, an equal part of the output each
+    constexpr int KQ = D / 16, DB = D / 32 / SHARE;
     constexpr int KROW = D + 8, VROW = 64 + 8;             // fp16; the rows of LDS start 4 banks apart
     constexpr int CHUNKS = 64 * D / 16 / THREADS;          // 16-byte pieces of the keys (and of the values) a thread
     extern __shared__ uint16_t tile_lds[];                 // [2][64][KROW], [2][D][VROW]
@@ -652,6 +653,7 @@ __global__ __launch_bounds__(64 * tile_waves(D), D == 64 ? 2 : 1) void mnb_atten
     uint16_t* const v_lds = tile_lds + 2 * 64 * KROW;
     const int tid = threadIdx.x, lane = tid & 63, r = lane & 31, hh = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int part_of_row = wave % SHARE, elem0 = 32 * DB * part_of_row;
     const int32_t h = blockIdx.x, z = blockIdx.z;
 
     // The tile: counted from the last one, whose rows see the most keys.
@@ -660,7 +662,7 @@ __global__ __launch_bounds__(64 * tile_waves(D), D == 64 ? 2 : 1) void mnb_atten
     const int32_t s = at.s, row0 = at.rt * BR;
     const Sequence q = uniform_sequence(p.b, s);
     const int32_t rows = q.n * p.G, start = q.length - q.n;
-    const int32_t wave0 = row0 + 32 * wave, mine = wave0 + r < rows ? wave0 + r : rows - 1;
+    const int32_t wave0 = row0 + 32 * (wave / SHARE), mine = wave0 + r < rows ? wave0 + r : rows - 1;
     const Row me = row_of(p, mine, h);
     const int32_t position = start + me.token;
     // Positions of the tile's last row and of the wave's first and last one.
@@ -880,7 +882,7 @@ __global__ __launch_bounds__(64 * tile_waves(D), D == 64 ? 2 : 1) void mnb_atten
 #pragma unroll
                     for (int d = 0; d < DB; ++d) o[d] *= keep;
                 }
-                int from_v = (buffer * D + order) * VROW + 8 * hh;
+                int from_v = (buffer * D + elem0 + order) * VROW + 8 * hh;
                 auto values = [&](int e, half8_t (&f)[DB]) {
 #pragma unroll
                     for (int d = 0; d < DB; ++d) f[d] = *reinterpret_cast<const half8_t*>(v_lds + from_v + 32 * d * VROW + 16 * e);
@@ -939,10 +941,10 @@ __global__ __launch_bounds__(64 * tile_waves(D), D == 64 ? 2 : 1) void mnb_atten
     weight += __shfl_xor(weight, 32);
     if (!q_finite && weight > 0.f) weight = __uint_as_float(0x7FC00000u);
     if (wave0 + r >= rows) return;
-    // o[d][8 e + j]: element 32 d + 16 e + 8 hh + j.
+    // o[d][8 e + j]: element elem0 + 32 d + 16 e + 8 hh + j.
     if (p.splits == 1) {
         const float by = weight == 0.f ? 0.f : unit / weight;
-        uint16_t* dst = p.out + (q.t0 + me.token) * p.out_stride + (int64_t)me.head * D + 8 * hh;
+        uint16_t* dst = p.out + (q.t0 + me.token) * p.out_stride + (int64_t)me.head * D + elem0 + 8 * hh;
 #pragma unroll
         for (int d = 0; d < DB; ++d)
 #pragma unroll
@@ -956,8 +958,8 @@ __global__ __launch_bounds__(64 * tile_waves(D), D == 64 ? 2 : 1) void mnb_atten
             }
         return;
     }
-    const int64_t part = (((int64_t)at.slot * p.heads + h) * p.splits + z) * BR + 32 * wave + r;
-    float* dst = p.tile_o + part * D + 8 * hh;
+    const int64_t part = (((int64_t)at.slot * p.heads + h) * p.splits + z) * BR + 32 * (wave / SHARE) + r;
+    float* dst = p.tile_o + part * D + elem0 + 8 * hh;
 #pragma unroll
     for (int d = 0; d < DB; ++d)
 #pragma unroll
@@ -967,7 +969,7 @@ __global__ __launch_bounds__(64 * tile_waves(D), D == 64 ? 2 : 1) void mnb_atten
                 *reinterpret_cast<float4_t*>(dst + 32 * d + 16 * e + 4 * j) =
                     float4_t{o[d][8 * e + 4 * j] * unit, o[d][8 * e + 4 * j + 1] * unit, o[d][8 * e + 4 * j + 2] * unit,
                              o[d][8 * e + 4 * j + 3] * unit};
-    if (hh == 0) {
+    if (hh == 0 && part_of_row == 0) {
         p.tile_ml[part * 2] = top;
         p.tile_ml[part * 2 + 1] = weight;
     }
@@ -977,7 +979,7 @@ __global__ __launch_bounds__(64 * tile_waves(D), D == 64 ? 2 : 1) void mnb_atten
 template <int D, bool BF16>
 __global__ __launch_bounds__(256) void mnb_attention_tile_join_kernel(AttentionParams p)
 {
-    constexpr int BR = 32 * tile_waves(D);
+    constexpr int BR = tile_rows(D);
     const int32_t h = blockIdx.x;
     const Tile at = tile_of(p, blockIdx.y, BR);
     if (at.s >= p.b.S) return;
@@ -1021,7 +1023,7 @@ int queue(const AttentionParams& p, const AttentionLayout& lay, hipStream_t stre
     }
     if (p.tile_slots && p.splits > 1) {
         hipLaunchKernelGGL((mnb_attention_tile_join_kernel<D, BF16>),
-                           dim3((unsigned)p.heads, (unsigned)p.tile_slots, 2 * tile_waves(D)), dim3(256), 0, stream, p);
+                           dim3((unsigned)p.heads, (unsigned)p.tile_slots, tile_rows(D) / 16), dim3(256), 0, stream, p);
         const int e = (int)hipGetLastError();
         if (e != 0) return e;
         ++*launches;

@@ -231,10 +231,11 @@ struct AttentionArgs {
 int launch_attention(const AttentionArgs& args, void* stream, int* launches) MNB_WEAK;
 
 // Sequences of more rows (tokens times query heads of a key head) than this go
-// to tiles of 32 tile_waves() rows, the others to a fixed number of workgroups.
+// to tiles of tile_rows() rows, the others to a fixed number of workgroups.
 constexpr int kAttentionManyRows = 64;
 constexpr int kAttentionWorkgroups = 512;
-constexpr int tile_waves(int64_t head_dim) { return head_dim == 128 ? 8 : 4; }
+constexpr int tile_waves(int64_t head_dim) { return head_dim >= 128 ? 8 : 4; }
+constexpr int tile_rows(int64_t head_dim) { return head_dim == 128 ? 256 : 128; }
 
 // The attention's workspace.  Few rows: for each workgroup the sums of two row
 // tiles that it shares with others, behind their maxima and weights.  Many: the
