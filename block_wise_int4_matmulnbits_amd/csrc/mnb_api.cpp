@@ -651,9 +651,12 @@ AttentionLayout attention_layout(int64_t tokens, int64_t sequences, int64_t q_he
     // Full tiles, and one more for each sequence that can have many rows.
     l.tile_slots = rows > kAttentionManyRows
                        ? (int)(rows / tile + std::min<int64_t>(sequences, rows / (kAttentionManyRows + 1))) : 0;
-    const int64_t tiles = std::max<int64_t>(1, rows / tile) * kv_heads;
-    l.splits = (int)std::max<int64_t>(1, std::min<int64_t>(16, ceil_div(512, tiles)));
-    if (tiles >= 256) l.splits = 1;
+    // Tiles that leave compute units (256) empty have their keys split so that whole
+    // rounds of them are full.
+    const int64_t tiles = (rows / tile + 1) * kv_heads, cus = 256;
+    l.splits = 1;
+    for (int z = 2; z <= 16 && tiles < 2 * cus; ++z)
+        if (ceil_div(tiles * z, cus) * l.splits < ceil_div(tiles * l.splits, cus) * z) l.splits = z;
     const size_t each = l.splits > 1 ? (size_t)l.tile_slots * (size_t)kv_heads * (size_t)l.splits * (size_t)tile : 0;
     l.tile_o = l.tile_ml + each * 2 * 4;
     l.bytes = l.tile_o + each * D * 4;

@@ -609,10 +609,10 @@ __global__ __launch_bounds__(256) void mnb_attention_join_kernel(AttentionParams
 // * outputs: 32 elements (A) x 32 rows, 16 keys deep, the same order, so that a
 //   lane stores eight neighbouring elements.  Weights in fp16 (2^-11 of each).
 //
-// Sixteen keys (a run) have one value scale.  The sums stand in units of `unit`: the
-// value scale of the run, or the largest of the 64 keys' where the run's is within
-// 2^-10 of it (r, at most 1, is what remains), so that no weight times scale falls
-// out of fp16's range, whatever the pages before it held.
+// Sixteen keys (a run) have one value scale, which stands as a multiple r of the
+// sums' unit.  The unit changes, and the sums with it, only where r would leave
+// 2^-10 .. 2^8, so that no weight times scale falls out of fp16's range, whatever
+// the pages before it held, and pages of differing scales cost nothing.
 typedef _Float16 half8_t __attribute__((ext_vector_type(8)));
 typedef float float16_t __attribute__((ext_vector_type(16)));
 
@@ -756,30 +756,20 @@ __global__ __launch_bounds__(64 * tile_waves(D), D == 64 ? 2 : 1) void mnb_atten
         const float vs = fine ? lane_vs : 0.f;
         const bool spoilt = !(lane_ks < __builtin_inff()) || !fine;
         const float ks = spoilt ? 1.f : lane_ks, bias = lane_ok ? 0.f : -__builtin_inff();
-        // Zeros keep the sums' unit.  (Sums of a unit 2^90 larger have their last bit above
-        // what they would lose.)
         n.spoilt = (uint32_t)__builtin_amdgcn_ballot_w64(spoilt) & 15u;
-        const bool none_yet = unit_bits == 0;
-        const float none = none_yet ? 1.f : __uint_as_float(unit_bits);
-        if (P >= 64) {                   // one page: the lanes of run 0 have it all
-            const float ref = vs == 0.f ? none : fmaxf(vs, none_yet ? 0.f : none * 0x1p-90f);
-            lane_r = vs == ref ? 1.f : vs / ref;
-            const float ks0 = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(ks), 0));
-            const float bias0 = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(bias), 0));
-            const uint32_t ref0 = __builtin_amdgcn_readlane(__float_as_uint(ref), 0);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                n.ks[i] = ks0;
-                n.bias[i] = bias0;
-                n.ref[i] = ref0;
-            }
-            return;
+        // A run whose scale is zero, or from 2^-10 to 2^8 of the sums' unit, keeps that
+        // unit (128 times 2^8 is within fp16's range); another one has its own.  (Sums of
+        // a unit 2^90 larger have their last bit above what they would lose.)
+        const bool none = unit_bits == 0;
+        float most = vs;
+        if (P < 64) {
+            most = fmaxf(most, __shfl_xor(most, 1));
+            most = fmaxf(most, __shfl_xor(most, 2));
         }
-        float most = fmaxf(vs, __shfl_xor(vs, 1));
-        most = fmaxf(most, __shfl_xor(most, 2));
-        float ref = most == 0.f ? none : vs >= most * 0x1p-10f || vs == 0.f ? most : vs;
-        ref = fmaxf(ref, fmaxf(most, none_yet ? 0.f : none) * 0x1p-90f);
-        lane_r = vs / ref;
+        const float base = !none ? __uint_as_float(unit_bits) : most == 0.f ? 1.f : most;
+        const bool near = vs == 0.f || (vs >= base * 0x1p-10f && vs <= base * 0x1p8f);
+        const float ref = near ? base : fmaxf(vs, fmaxf(most, base) * 0x1p-90f);
+        lane_r = vs == ref ? 1.f : vs / ref;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             n.ks[i] = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(ks), i));
