@@ -57,6 +57,7 @@ struct AttentionParams {
     int32_t tiles_each;       // of a sequence in it, or 0
     int32_t many;             // sequences of more rows than this go to the tiles
     int32_t tile_slots, splits;   // of the tiles' grid
+    int32_t small;            // up to 64 sequences, whose work (but for the heads) fits 32 bits
     float scale_log2;         // scale * log2(e)
 };
 
@@ -77,6 +78,12 @@ __device__ __forceinline__ Work work_of(const AttentionParams& p, const Sequence
 __device__ __forceinline__ int64_t count_of(const AttentionParams& p, const Work& w)
 {
     return w.units ? (int64_t)w.tiles * (w.units + kBegin) * p.heads : 0;
+}
+// The same without the heads, of this lane's sequence (p.small).
+__device__ __forceinline__ int32_t small_count(const AttentionParams& p, const Sequences& all)
+{
+    const Work w = work_of(p, all.mine);
+    return (int)(threadIdx.x & 63) < p.b.S && w.units ? w.tiles * (w.units + kBegin) : 0;
 }
 
 __device__ __forceinline__ int64_t units_of(const AttentionParams& p, int32_t s)
@@ -135,10 +142,22 @@ struct Start {
     int64_t share, all, unit, before;
     int32_t s;
 };
-__device__ __forceinline__ Start start_of(const AttentionParams& p)
+__device__ __forceinline__ Start start_of(const AttentionParams& p, const Sequences& seqs)
 {
     const int lane = threadIdx.x & 63;
     Start r;
+    if (p.small) {
+        const int32_t mine = small_count(p, seqs), upto = wave_prefix32(mine);
+        r.all = (int64_t)__builtin_amdgcn_readlane(upto, 63) * p.heads;
+        r.share = share_of(r.all);
+        r.unit = (int64_t)blockIdx.x * r.share;
+        r.before = 0;
+        r.s = p.b.S;
+        if (r.unit >= r.all) return r;
+        r.s = __builtin_ctzll(__builtin_amdgcn_ballot_w64((int64_t)upto * p.heads > r.unit));
+        r.before = (int64_t)__builtin_amdgcn_readlane(upto - mine, r.s) * p.heads;
+        return r;
+    }
     int64_t mine = lane < p.b.S ? units_of(p, lane) : 0, upto = wave_prefix(mine), base = 0;
     r.all = uniform64(__shfl(upto, 63));
     for (int32_t s0 = 64; s0 < p.b.S; s0 += 64) r.all += uniform64(wave_sum(s0 + lane < p.b.S ? units_of(p, s0 + lane) : 0));
@@ -202,34 +221,38 @@ __device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)
 // many rows (b.S: none); its number from the first.
 struct Tile {
     int32_t s, rt, slot;
+    Sequence q;
 };
-__device__ __forceinline__ int32_t tiles_of(const AttentionParams& p, int32_t s, int BR)
+__device__ __forceinline__ int32_t tiles_of(const AttentionParams& p, const Sequence& q, int BR)
 {
-    const Sequence q = sequence(p.b, s);
     const int32_t rows = q.n * p.G;
     return rows > p.many ? (rows + BR - 1) / BR : 0;
 }
 __device__ __forceinline__ Tile tile_of(const AttentionParams& p, int32_t y, int BR)
 {
     const int lane = threadIdx.x & 63;
-    int64_t all = 0;
-    for (int32_t s0 = 0; s0 < p.b.S; s0 += 64) all += s0 + lane < p.b.S ? tiles_of(p, s0 + lane, BR) : 0;
-    all = uniform64(wave_sum(all));
-    const int64_t v = all - 1 - y;
-    Tile t{p.b.S, 0, 0};
-    if (v < 0) return t;
-    int64_t base = 0;
+    const Sequences seqs(p.b);
+    int32_t all = 0, base = 0;            // (at most 2^26 rows, and a tile more for each sequence)
     for (int32_t s0 = 0; s0 < p.b.S; s0 += 64) {
-        const int64_t mine = s0 + lane < p.b.S ? tiles_of(p, s0 + lane, BR) : 0, upto = wave_prefix(mine);
-        const uint64_t past = __builtin_amdgcn_ballot_w64(base + upto > v);
+        const Sequence q = p.b.S <= 64 ? seqs.mine : sequence(p.b, s0 + lane < p.b.S ? s0 + lane : 0);
+        all += __builtin_amdgcn_readlane(wave_prefix32(s0 + lane < p.b.S ? tiles_of(p, q, BR) : 0), 63);
+    }
+    const int32_t v = all - 1 - y;
+    Tile t{p.b.S, 0, 0, Sequence{0, 0, 0}};
+    if (v < 0) return t;
+    for (int32_t s0 = 0; s0 < p.b.S; s0 += 64) {
+        const Sequence q = p.b.S <= 64 ? seqs.mine : sequence(p.b, s0 + lane < p.b.S ? s0 + lane : 0);
+        const int32_t mine = s0 + lane < p.b.S ? tiles_of(p, q, BR) : 0, upto = base + wave_prefix32(mine);
+        const uint64_t past = __builtin_amdgcn_ballot_w64(upto > v);
         if (past) {
             const int l = __builtin_ctzll(past);
-            t.s = uniform(s0 + l);
-            t.rt = (int32_t)(v - uniform64(base + __shfl(upto - mine, l)));
-            t.slot = (int32_t)v;
+            t.s = s0 + l;
+            t.rt = v - __builtin_amdgcn_readlane(upto - mine, l);
+            t.slot = v;
+            t.q = seqs.at(t.s);
             return t;
         }
-        base += uniform64(__shfl(upto, 63));
+        base = __builtin_amdgcn_readlane(upto, 63);
     }
     return t;
 }
@@ -242,7 +265,8 @@ __global__ __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) void mnb_attention_r
     __shared__ float lds_m[kWaves][16], lds_l[kWaves][16];
     const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const Start start = start_of(p);
+    const Sequences seqs(p.b);
+    const Start start = start_of(p, seqs);
     int64_t u = start.unit, before = start.before;
     const int64_t end = u + start.share < start.all ? u + start.share : start.all;
     int32_t s = start.s;
@@ -250,12 +274,12 @@ __global__ __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) void mnb_attention_r
     const int P = 1 << p.b.page_bits;
     for (; u < end; ) {
         // The segment: units c0 .. c1 - 1 of sequence s, head h, row tile rt.
-        Sequence q = uniform_sequence(p.b, s);
+        Sequence q = seqs.at(s);
         Work w = work_of(p, q);
         while (u - before >= count_of(p, w)) {   // on to the next sequence with work
             before += count_of(p, w);
             if (++s >= p.b.S) return;
-            q = uniform_sequence(p.b, s);
+            q = seqs.at(s);
             w = work_of(p, q);
         }
         const int64_t in = u - before, pair64 = divide(in, w.units + kBegin);
@@ -537,13 +561,31 @@ __global__ __launch_bounds__(256) void mnb_attention_join_kernel(AttentionParams
     auto base = [&](int32_t i) {
         return p.tiles_each ? (int64_t)i * p.tiles_each : (int64_t)clamp32(p.b.starts[i], 0, p.b.T) * p.G / 16 + i;
     };
-    const int32_t s = wave_search(p.b.S, slot, base);
-    const Sequence q = sequence(p.b, s);
-    const Work w = work_of(p, q);
-    const int64_t rt = slot - base(s);
-    if (rt < 0 || rt >= w.tiles) return;
-    int64_t all, before;
-    count_units(p, s, &all, &before);
+    int32_t s;
+    Sequence q;
+    int64_t all, before, rt;
+    Work w;
+    if (p.small) {
+        const Sequences seqs(p.b);
+        const int lane = threadIdx.x & 63;
+        auto first = [&](int32_t t0) { return p.tiles_each ? lane * p.tiles_each : (int32_t)((int64_t)t0 * p.G / 16) + lane; };
+        const int32_t mine = small_count(p, seqs), upto = wave_prefix32(mine), at = first(seqs.mine.t0);
+        const uint64_t m = __builtin_amdgcn_ballot_w64(lane < p.b.S && at <= (int32_t)slot);
+        s = m ? 63 - __builtin_clzll(m) : 0;
+        q = seqs.at(s);
+        w = work_of(p, q);
+        rt = slot - __builtin_amdgcn_readlane(at, s);
+        if (rt < 0 || rt >= w.tiles) return;
+        all = (int64_t)__builtin_amdgcn_readlane(upto, 63) * p.heads;
+        before = (int64_t)__builtin_amdgcn_readlane(upto - mine, s) * p.heads;
+    } else {
+        s = wave_search(p.b.S, slot, base);
+        q = sequence(p.b, s);
+        w = work_of(p, q);
+        rt = slot - base(s);
+        if (rt < 0 || rt >= w.tiles) return;
+        count_units(p, s, &all, &before);
+    }
     const int64_t share = share_of(all);
     const int64_t u0 = before + ((int64_t)h * w.tiles + rt) * (w.units + kBegin) + kBegin, u1 = u0 + w.units;
     const int64_t w0 = divide(u0, share);
@@ -660,7 +702,7 @@ __global__ __launch_bounds__(64 * tile_waves(D), D == 64 ? 2 : 1) void mnb_atten
     const Tile at = tile_of(p, blockIdx.y, BR);
     if (at.s >= p.b.S) return;
     const int32_t s = at.s, row0 = at.rt * BR;
-    const Sequence q = uniform_sequence(p.b, s);
+    const Sequence q = at.q;
     const int32_t rows = q.n * p.G, start = q.length - q.n;
     const int32_t wave0 = row0 + 32 * (wave / SHARE), mine = wave0 + r < rows ? wave0 + r : rows - 1;
     const Row me = row_of(p, mine, h);
@@ -973,7 +1015,7 @@ __global__ __launch_bounds__(256) void mnb_attention_tile_join_kernel(AttentionP
     const int32_t h = blockIdx.x;
     const Tile at = tile_of(p, blockIdx.y, BR);
     if (at.s >= p.b.S) return;
-    const Sequence q = uniform_sequence(p.b, at.s);
+    const Sequence q = at.q;
     const int32_t in = 16 * (int)blockIdx.z + (threadIdx.x >> 4), row = at.rt * BR + in, e0 = 4 * (threadIdx.x & 15);
     if (row >= q.n * p.G) return;
     const int64_t first = ((int64_t)at.slot * p.heads + h) * p.splits * BR + in;
@@ -1065,6 +1107,8 @@ int launch_attention(const AttentionArgs& a, void* stream, int* launches)
     p.tiles_each = !few && each * a.batch.sequences <= loose ? (int32_t)each : 0;
     p.slots = (int32_t)(p.tiles_each ? each * a.batch.sequences : loose);
     p.splits = lay.splits;
+    // Tiles of few rows: at most tokens G / 16 and one for each sequence, of 2^18 units.
+    p.small = a.batch.sequences <= 64 && a.batch.tokens * p.G / 16 + a.batch.sequences < (1 << 12);
     const hipStream_t s = static_cast<hipStream_t>(stream);
     *launches = 0;
     switch (a.cache.head_dim) {

@@ -78,6 +78,36 @@ __device__ __forceinline__ int32_t wave_search(int32_t count, int64_t v, F f)
     return __builtin_amdgcn_readfirstlane(lo);
 }
 
+// Sum over the lanes up to this one.
+__device__ __forceinline__ int32_t wave_prefix32(int32_t v)
+{
+    v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false);   // row_shr:1
+    v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false);   // row_shr:2
+    v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false);   // row_shr:4
+    v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false);   // row_shr:8
+    v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);   // row_bcast:15 into rows 1 and 3
+    v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);   // row_bcast:31 into rows 2 and 3
+    return v;
+}
+
+// The sequences of a batch, lane s holding the s-th where there are up to 64 of
+// them (read once, together).
+struct Sequences {
+    const CacheBatch& b;
+    Sequence mine;
+    __device__ __forceinline__ explicit Sequences(const CacheBatch& batch) : b(batch), mine{0, 0, 0}
+    {
+        const int32_t lane = threadIdx.x & 63;
+        if (b.S <= 64) mine = sequence(b, lane < b.S ? lane : b.S - 1);
+    }
+    __device__ __forceinline__ Sequence at(int32_t s) const      // s alike in every lane
+    {
+        if (b.S > 64) return uniform_sequence(b, s);
+        return Sequence{__builtin_amdgcn_readlane(mine.t0, s), __builtin_amdgcn_readlane(mine.n, s),
+                        __builtin_amdgcn_readlane(mine.length, s)};
+    }
+};
+
 // Sequence s = the largest with f(its first row, s) <= v, for a rising f.  Up to 64
 // sequences are read at once, lane s the s-th.
 struct Found {
@@ -91,12 +121,11 @@ __device__ __forceinline__ Found find_sequence(const CacheBatch& b, int64_t v, F
         const int32_t s = wave_search(b.S, v, [&](int32_t i) { return f(clamp32(b.starts[i], 0, b.T), i); });
         return Found{s, uniform_sequence(b, s)};
     }
-    const int32_t lane = threadIdx.x & 63, i = lane < b.S ? lane : b.S - 1;
-    const Sequence q = sequence(b, i);
-    const uint64_t m = __builtin_amdgcn_ballot_w64(lane < b.S && f(q.t0, i) <= v);
+    const Sequences all(b);
+    const int32_t lane = threadIdx.x & 63;
+    const uint64_t m = __builtin_amdgcn_ballot_w64(lane < b.S && f(all.mine.t0, lane) <= v);
     const int32_t s = m ? 63 - __builtin_clzll(m) : 0;
-    return Found{s, Sequence{__builtin_amdgcn_readlane(q.t0, s), __builtin_amdgcn_readlane(q.n, s),
-                             __builtin_amdgcn_readlane(q.length, s)}};
+    return Found{s, all.at(s)};
 }
 
 }  // namespace mnb
