@@ -31,7 +31,6 @@ namespace {
 
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
-constexpr int kThreads = 256;
 constexpr int kKeyUnits = 4;     // units of sixteen keys' elements that a thread keeps between its two looks at them
 constexpr int kValueUnits = 2;   // the same of 8 elements of four tokens
 
@@ -154,6 +153,7 @@ __device__ __forceinline__ void turn(const u32x4& a, const u32x4& b, const float
 }
 
 // The largest of a workgroup's values, in every thread.
+template <int kThreads>
 __device__ __forceinline__ uint32_t workgroup_max(uint32_t v, uint32_t* part)
 {
 #pragma unroll
@@ -161,6 +161,7 @@ __device__ __forceinline__ uint32_t workgroup_max(uint32_t v, uint32_t* part)
         const uint32_t o = __shfl_xor(v, d);
         v = o > v ? o : v;
     }
+    if (kThreads == 64) return v;
     if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = v;
     __syncthreads();
 #pragma unroll
@@ -187,7 +188,7 @@ __device__ __forceinline__ OldScale old_scale(float scale)
 // One page of one head: the tokens of positions first + a .. first + b - 1, whose
 // rows follow each other; `row` is that of position first.  page is looked at
 // only once the new values are on their way.
-template <int D, bool BF16, bool NEAR>
+template <int D, bool BF16, bool NEAR, int kThreads>
 __device__ __forceinline__ void store_keys(const AppendParams& p, int32_t page, int head, int64_t first, int a, int b,
                                            int64_t row, uint32_t* part)
 {
@@ -231,7 +232,7 @@ __device__ __forceinline__ void store_keys(const AppendParams& p, int32_t page, 
     const int64_t at = (int64_t)page * p.heads + head;
     int8_t* dst = p.k_pages + (at << p.b.page_bits) * D;
     const OldScale old = a > 0 ? old_scale(p.k_scales[at]) : OldScale{0, 0};
-    top = workgroup_max(max(top, old.bits), part);
+    top = workgroup_max<kThreads>(max(top, old.bits), part);
     const bool finite = top < 0x7F800000u;
     const int e = exponent_of(top);
     const float down = power_of_two(-e);
@@ -289,7 +290,7 @@ __device__ __forceinline__ uint32_t range_of(uint32_t most, uint32_t less, int b
 
 // The values lie with their tokens last: a thread holds eight elements of four
 // neighbouring tokens and writes a word for each element.
-template <int D, bool BF16>
+template <int D, bool BF16, int kThreads>
 __device__ __forceinline__ void store_values(const AppendParams& p, int32_t page, int head, int a, int b, int64_t row,
                                              uint32_t* part)
 {
@@ -334,7 +335,7 @@ __device__ __forceinline__ void store_values(const AppendParams& p, int32_t page
     const int64_t at = (int64_t)page * p.heads + head;
     int8_t* dst = p.v_pages + (at << p.b.page_bits) * D;
     const OldScale old = a > 0 ? old_scale(p.v_scales[at]) : OldScale{0, 0};
-    const uint32_t top = workgroup_max(max(range_of(most, less, BF16), old.bits), part);
+    const uint32_t top = workgroup_max<kThreads>(max(range_of(most, less, BF16), old.bits), part);
     const bool finite = top < 0x7F800000u;
     const int e = exponent_of(top);
     const float down = power_of_two(-e);
@@ -436,7 +437,10 @@ __device__ __forceinline__ void turn_queries(const AppendParams& p, int64_t t)
     }
 }
 
-template <int D, bool BF16, bool NEAR>
+// Workgroups of four waves, or of one where the sequences have a token or two each:
+// of a page's few units the other waves would get none (64 sequences of one to three
+// tokens).
+template <int D, bool BF16, bool NEAR, int kThreads>
 __global__ __launch_bounds__(kThreads) void mnb_append_kernel(AppendParams p)
 {
     __shared__ uint32_t part[kThreads / 64];
@@ -461,16 +465,27 @@ __global__ __launch_bounds__(kThreads) void mnb_append_kernel(AppendParams p)
     const int a = from > first ? (int)(from - first) : 0;
     const int b = f.q.length - first < P ? (int)(f.q.length - first) : P;
     const int64_t row = f.q.t0 + (first - start);   // of position first; negative only where a > 0
-    if (kind < p.heads) store_keys<D, BF16, NEAR>(p, page, kind, first, a, b, row, part);
-    else store_values<D, BF16>(p, page, kind - p.heads, a, b, row, part);
+    if (kind < p.heads) store_keys<D, BF16, NEAR, kThreads>(p, page, kind, first, a, b, row, part);
+    else store_values<D, BF16, kThreads>(p, page, kind - p.heads, a, b, row, part);
 }
 
-template <int D, bool BF16>
-int queue(const AppendParams& p, bool near, dim3 grid, hipStream_t stream)
+template <int D, bool BF16, bool NEAR>
+int queue(const AppendParams& p, int64_t tokens, hipStream_t stream)
 {
-    if (near) hipLaunchKernelGGL((mnb_append_kernel<D, BF16, true>), grid, dim3(kThreads), 0, stream, p);
-    else hipLaunchKernelGGL((mnb_append_kernel<D, BF16, false>), grid, dim3(kThreads), 0, stream, p);
+    const int threads = p.by_token ? 64 : 256;
+    const int64_t rows = 2 * p.heads, each = rows * (threads / 64);      // queries of a column: a token a wave
+    const dim3 grid((unsigned)(p.slots + (p.q ? (tokens + each - 1) / each : 0)), (unsigned)rows);
+    if (threads == 64) hipLaunchKernelGGL((mnb_append_kernel<D, BF16, NEAR, 64>), grid, dim3(64), 0, stream, p);
+    else hipLaunchKernelGGL((mnb_append_kernel<D, BF16, NEAR, 256>), grid, dim3(256), 0, stream, p);
     return (int)hipGetLastError();
+}
+
+template <int D>
+int queue(const AppendParams& p, const AppendArgs& a, hipStream_t s)
+{
+    const int64_t T = a.batch.tokens;
+    if (a.bf16) return a.interleaved ? queue<D, true, true>(p, T, s) : queue<D, true, false>(p, T, s);
+    return a.interleaved ? queue<D, false, true>(p, T, s) : queue<D, false, false>(p, T, s);
 }
 
 }  // namespace
@@ -501,16 +516,8 @@ int launch_append(const AppendArgs& a, void* stream)
     const int64_t T = a.batch.tokens, loose = T / a.cache.page_size + 2 * a.batch.sequences;
     p.by_token = T <= loose;
     p.slots = (int32_t)(p.by_token ? T : loose);
-    const int64_t rows = 2 * a.cache.kv_heads, waves = kThreads / 64;
-    const int64_t columns = p.slots + (p.q ? (T + rows * waves - 1) / (rows * waves) : 0);
-    const dim3 grid((unsigned)columns, (unsigned)rows);
     const hipStream_t st = static_cast<hipStream_t>(stream);
-    const bool near = a.interleaved != 0;
-    switch (a.cache.head_dim) {
-    case 64: return a.bf16 ? queue<64, true>(p, near, grid, st) : queue<64, false>(p, near, grid, st);
-    case 128: return a.bf16 ? queue<128, true>(p, near, grid, st) : queue<128, false>(p, near, grid, st);
-    default: return a.bf16 ? queue<256, true>(p, near, grid, st) : queue<256, false>(p, near, grid, st);
-    }
+    return a.cache.head_dim == 64 ? queue<64>(p, a, st) : a.cache.head_dim == 128 ? queue<128>(p, a, st) : queue<256>(p, a, st);
 }
 
 }  // namespace mnb
