@@ -416,7 +416,8 @@ int queue(const LoraParams& p, const LoraLayout& lay, hipStream_t s)
     const int e = p.R <= 16 ? queue_down<BF16, NRT, 1>(p, ways, s) : p.R <= 32 ? queue_down<BF16, NRT, 2>(p, ways, s)
                 : p.R <= 48 ? queue_down<BF16, NRT, 3>(p, ways, s) : queue_down<BF16, NRT, 4>(p, ways, s);
     if (e != 0) return e;
-    return lay.wide ? queue_up<BF16, NRT, 4, 8>(p, s) : queue_up<BF16, NRT, 1, 4>(p, s);
+    // Wide: 32 rows a workgroup (4091 x 4097 columns, rank 40: 61 us with 64, 53 with 32).
+    return lay.wide ? queue_up<BF16, NRT == 1 ? 1 : 2, 4, 8>(p, s) : queue_up<BF16, NRT, 1, 4>(p, s);
 }
 
 }  // namespace
