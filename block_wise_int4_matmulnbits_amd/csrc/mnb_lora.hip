@@ -353,21 +353,30 @@ __global__ __launch_bounds__(64 * W) void mnb_lora_up_kernel(LoraParams p)
     int at = 0;                                  // chunk of the item in hand
     auto multiply = [&](const Item& it) {
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            if (64 * at + 32 * k >= p.R) continue;
+        for (int n = 0; n < NRT; ++n) {
+            if (!((it.rows >> (16 * n)) & 0xFFFF)) continue;
+            // Rows of other adapters keep their sums (0 times a weight that is not finite
+            // would not).
+            const bool own = (it.rows >> (16 * n + r)) & 1;
+            float4_t sum[CT];
 #pragma unroll
-            for (int n = 0; n < NRT; ++n) {
-                if (!((it.rows >> (16 * n)) & 0xFFFF)) continue;
-                const bool own = (it.rows >> (16 * n + r)) & 1;
+            for (int t = 0; t < CT; ++t) sum[t] = acc[n][t];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                if (64 * at + 32 * k >= p.R) continue;
                 const int from = (16 * n + r) * stride + 64 * at + 32 * k + 8 * g;
-                const u32x4 hi = own ? *reinterpret_cast<const u32x4*>(t_lds + from) : zero;
-                const u32x4 lo = own ? *reinterpret_cast<const u32x4*>(t_lds + RT * stride + from) : zero;
+                const u32x4 hi = *reinterpret_cast<const u32x4*>(t_lds + from);
+                const u32x4 lo = *reinterpret_cast<const u32x4*>(t_lds + RT * stride + from);
 #pragma unroll
                 for (int t = 0; t < CT; ++t) {
-                    acc[n][t] = mfma<BF16>(it.b[k][t], hi, acc[n][t]);
-                    acc[n][t] = mfma<BF16>(it.b[k][t], lo, acc[n][t]);
+                    sum[t] = mfma<BF16>(it.b[k][t], hi, sum[t]);
+                    sum[t] = mfma<BF16>(it.b[k][t], lo, sum[t]);
                 }
             }
+#pragma unroll
+            for (int t = 0; t < CT; ++t)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[n][t][i] = own ? sum[t][i] : acc[n][t][i];
         }
         at = at + 1 < chunks ? at + 1 : 0;
     };

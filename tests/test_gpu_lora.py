@@ -158,3 +158,76 @@ def test_captured():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(out.cpu(), _call(*sets[i]))
+
+
+WIDE = [
+    # m, K, N, rank, adapters, run: enough columns and rows for the wide second launch
+    (300, 48, 27136, 16, 9, 40), (300, 48, 27137, 16, 9, 7), (9, 32, 130571, 8, 3, 1), (70, 32, 65539, 136, 3, 30),
+    (40, 96, 131073, 72, 2, 5), (4099, 16, 2049, 24, 5, 600),
+]
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16], ids=["f16", "bf16"])
+@pytest.mark.parametrize("shape", WIDE, ids=["x".join(map(str, s)) for s in WIDE])
+def test_wide(shape, dtype):
+    G.require_gpu()
+    m, K, N, rank, n, run = shape
+    x, ids, A, B, scaling, base = _make(m, K, N, rank, n, dtype, dtype, m + N, run)
+    dev = [t.cuda() for t in (x, ids, A, B, base)]
+    out = torch.full((m, N), 9.0, dtype=dtype, device="cuda")
+    mnb.matmul_lora(*dev, out, scaling=scaling.cuda())
+    torch.cuda.synchronize()
+    none = (ids < 0) | (ids >= n)
+    out = out.cpu()
+    assert torch.equal(out[none], base[none])
+    some = torch.arange(0, m, max(1, m // 40))          # rows against 64 bits
+    want, tol = R.lora(x[some], ids[some], A, B, scaling, base[some])
+    R.check_rows(out[some], want, tol, dtype)
+    # the other rows: the same values as alone
+    got = torch.empty(m, N, dtype=dtype, device="cuda")
+    mnb.matmul_lora(*dev[:4], None, got, scaling=scaling.cuda())
+    torch.cuda.synchronize()
+    got = got.cpu()
+    assert bool((got[none] == 0).all())
+    want, tol = R.lora(x[some], ids[some], A, B, scaling, None)
+    R.check_rows(got[some], want, tol, dtype)
+    size = 2.0 ** -6 * (got.float().abs() + base.float().abs() + 1)
+    assert bool(((out.float() - base.float() - got.float()).abs() <= size).all())
+
+
+def test_adapters_that_are_not_finite():
+    """An adapter whose weights or scaling are not finite spoils its own rows alone."""
+    G.require_gpu()
+    for m, N, dtype in ((12, 130, F16), (70, 130, BF16), (300, 27137, BF16)):
+        x, ids, A, B, scaling, base = _make(m, 64, N, 24, 5, dtype, dtype, 8, none=0.1)
+        clean = _call(x, ids, A, B, scaling, base)
+        for bad in (float("nan"), float("inf")):
+            for which in range(3):
+                w = [A.clone(), B.clone(), scaling.clone()]
+                w[which][2] = bad
+                got = _call(x, ids, *w, base)
+                assert torch.equal(got[ids != 2], clean[ids != 2])
+                assert not bool(torch.isfinite(got[ids == 2]).any())
+
+
+def test_two_graphs_of_one_workspace():
+    G.require_gpu()
+    sets = [_make(m, 512, 300, 16, 5, BF16, BF16, m) for m in (24, 130)]
+    ws = torch.empty(max(mnb.mnb_lora_workspace(m, 512, 300, 16, 5) for m in (24, 130)), dtype=torch.uint8, device="cuda")
+    work = []
+    for s in sets:
+        x, ids, A, B, scaling, base = [t.cuda() for t in s]
+        out = torch.empty_like(base)
+        mnb.matmul_lora(x, ids, A, B, base, out, scaling=scaling, workspace=ws)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            mnb.matmul_lora(x, ids, A, B, base, out, scaling=scaling, workspace=ws)
+        work.append((graph, (x, ids, A, B, scaling, base), out, _call(*s)))
+    for i in (0, 1, 1, 0, 1, 0):
+        graph, _, out, want = work[i]
+        out.fill_(3.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out.cpu(), want)
+        _call(*sets[1 - i])
