@@ -1202,7 +1202,9 @@ int attention_int8(const mnb_kv_cache* cache, const mnb_kv_batch* batch, int dty
     const Span wr[] = {span_of(orow), {workspace, (int64_t)need}}, qs[] = {span_of(qr)};
     if (aliased(in, 7, wr, 2) || aliased(qs, 1, wr + 1, 1) || rows_overlap(orow, qr)) return MNB_ERR_ALIAS;
     if (!mnb::launch_attention) return finish_launches(kNoDevice, 0);
-    const mnb::AttentionArgs args{c, b, q, out, q_stride, out_stride, q_heads, max_tokens, scale, dtype == MNB_BF16,
+    mnb_kv_batch seen = b;
+    if (c.pages == 0) seen.max_pages = 0;      // no token stands anywhere: nothing of the cache is read
+    const mnb::AttentionArgs args{c, seen, q, out, q_stride, out_stride, q_heads, max_tokens, scale, dtype == MNB_BF16,
                                   workspace};
     int launches = 0;
     const int e = mnb::launch_attention(args, stream, &launches);

@@ -37,6 +37,7 @@ typedef int i32x4 __attribute__((ext_vector_type(4)));
 constexpr int kWaves = 4;
 constexpr int kWorkgroups = kAttentionWorkgroups, kMostParts = kAttentionWorkgroups;
 constexpr int kBegin = 4;
+constexpr int kGridTiles = 32768;     // tiles of a grid's y
 constexpr float kLowest = -3.0e38f;   // a running maximum before any key
 
 struct AttentionParams {
@@ -218,9 +219,9 @@ __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_ex
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
 
 // The y-th tile of BR rows, counted from the last one, among the sequences of
-// many rows (b.S: none); its number from the first.
+// many rows (b.S: none).
 struct Tile {
-    int32_t s, rt, slot;
+    int32_t s, rt;
     Sequence q;
 };
 __device__ __forceinline__ int32_t tiles_of(const AttentionParams& p, const Sequence& q, int BR)
@@ -238,8 +239,8 @@ __device__ __forceinline__ Tile tile_of(const AttentionParams& p, int32_t y, int
         all += __builtin_amdgcn_readlane(wave_prefix32(s0 + lane < p.b.S ? tiles_of(p, q, BR) : 0), 63);
     }
     const int32_t v = all - 1 - y;
-    Tile t{p.b.S, 0, 0, Sequence{0, 0, 0}};
-    if (v < 0) return t;
+    Tile t{p.b.S, 0, Sequence{0, 0, 0}};
+    if (v < 0 || y >= p.tile_slots) return t;
     for (int32_t s0 = 0; s0 < p.b.S; s0 += 64) {
         const Sequence q = p.b.S <= 64 ? seqs.mine : sequence(p.b, s0 + lane < p.b.S ? s0 + lane : 0);
         const int32_t mine = s0 + lane < p.b.S ? tiles_of(p, q, BR) : 0, upto = base + wave_prefix32(mine);
@@ -248,7 +249,6 @@ __device__ __forceinline__ Tile tile_of(const AttentionParams& p, int32_t y, int
             const int l = __builtin_ctzll(past);
             t.s = s0 + l;
             t.rt = v - __builtin_amdgcn_readlane(upto - mine, l);
-            t.slot = v;
             t.q = seqs.at(t.s);
             return t;
         }
@@ -320,8 +320,9 @@ __global__ __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) void mnb_attention_r
             // |x| < 2^ex, and n = rint(x 2^(22 - ex)) in the low bits of n + 1.5 * 2^23.
             // The three signed digits of n are the bytes of n + 0x808080, each with
             // its top bit turned.
-            const int ex = (int)(__float_as_uint(widen16(top, BF16)) >> 23) - 126;
-            const float pre = ex < -64 ? pow2(64) : 1.f, up = finite ? pow2((ex < -64 ? -42 : 22) - ex) : 0.f;
+            // (At least 2^-80: the factor of the scores stays a normal number.)
+            const int ex = max((int)(__float_as_uint(widen16(top, BF16)) >> 23), 46) - 126;
+            const float up = finite ? pow2(22 - ex) : 0.f;
             uint32_t sum = 0;
 #pragma unroll
             for (int k = 0; k < KS; ++k)
@@ -332,7 +333,7 @@ __global__ __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) void mnb_attention_r
                     for (int j = 0; j < 4; ++j) {
                         const uint32_t pair2 = raw[k][i >> 1][(i & 1) * 2 + (j >> 1)];
                         const float x = widen16(j & 1 ? pair2 >> 16 : pair2 & 0xFFFFu, BF16);
-                        const uint32_t n = __float_as_uint(fmaf(x * pre, up, 12582912.f)) - 0x4B400000u;
+                        const uint32_t n = __float_as_uint(fmaf(x, up, 12582912.f)) - 0x4B400000u;
                         sum += n;
                         w[j] = n + 0x808080u;
                     }
@@ -343,8 +344,7 @@ __global__ __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) void mnb_attention_r
             sum += __shfl_xor(sum, 16);
             sum += __shfl_xor(sum, 32);
             half = (int)sum >> 1;
-            q_scale = finite ? p.scale_log2 * pow2(ex < -64 ? -64 : ex) * pow2(ex < -64 ? ex + 42 : -22)
-                             : __uint_as_float(0x7FC00000u);
+            q_scale = finite ? p.scale_log2 * pow2(ex - 22) : __uint_as_float(0x7FC00000u);
         }
 
         float4_t o[DT];
@@ -591,6 +591,8 @@ __global__ __launch_bounds__(256) void mnb_attention_join_kernel(AttentionParams
     const int64_t w0 = divide(u0, share);
     const int parts = w.units ? (int)(divide(u1 - 1, share) - w0) + 1 : 0;
     if (parts == 1) return;              // stored by that workgroup
+    // (Only numbers of the batch that overflow the counts lead beyond the last one.)
+    if (u0 < 0 || parts < 0 || w0 + parts > kWorkgroups) return;
     const int rows = q.n * p.G - (int)rt * 16, count = rows < 16 ? rows : 16;
     auto part_of = [&](int i) { return (2 * (w0 + i) + (i == 0 ? 1 : 0)) * 16; };
     {
@@ -696,10 +698,11 @@ __global__ __launch_bounds__(64 * tile_waves(D), D == 64 ? 2 : 1) void mnb_atten
     const int tid = threadIdx.x, lane = tid & 63, r = lane & 31, hh = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int part_of_row = wave % SHARE, elem0 = 32 * DB * part_of_row;
-    const int32_t h = blockIdx.x, z = blockIdx.z;
+    const int32_t h = blockIdx.x, z = p.splits > 1 ? (int32_t)blockIdx.z : 0;
 
     // The tile: counted from the last one, whose rows see the most keys.
-    const Tile at = tile_of(p, blockIdx.y, BR);
+    const int32_t slot = (int32_t)blockIdx.y + (p.splits > 1 ? 0 : kGridTiles * (int32_t)blockIdx.z);
+    const Tile at = tile_of(p, slot, BR);
     if (at.s >= p.b.S) return;
     const int32_t s = at.s, row0 = at.rt * BR;
     const Sequence q = at.q;
@@ -739,17 +742,17 @@ __global__ __launch_bounds__(64 * tile_waves(D), D == 64 ? 2 : 1) void mnb_atten
         const uint32_t sign = p.scale_log2 < 0.f ? 0x80008000u : 0u;
         q_scale = size;
         if constexpr (BF16) {
-            const int ex = (int)(__float_as_uint(widen16(top, 1)) >> 23) - 126;       // |x| < 2^ex
-            const float pre = ex < -64 ? pow2(64) : 1.f, up = pow2((ex < -64 ? -49 : 15) - ex);
-            q_scale = size * pow2(ex < -64 ? -64 : ex) * pow2(ex < -64 ? ex + 49 : -15);
+            const int ex = max((int)(__float_as_uint(widen16(top, 1)) >> 23), 46) - 126;    // |x| < 2^ex, as above
+            const float up = pow2(15 - ex);
+            q_scale = finite ? size * pow2(ex - 15) : size;
 #pragma unroll
             for (int k = 0; k < KQ; ++k)
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    raw[k][i] = half_pair(bf16_lo(raw[k][i]) * pre * up, bf16_hi(raw[k][i]) * pre * up);
+                    raw[k][i] = half_pair(bf16_lo(raw[k][i]) * up, bf16_hi(raw[k][i]) * up);
         }
-        // (Its products are done with zeros; it gets its NaN at the end.)
-        if (!finite) q_scale = size;
+        // (The products of a row that is not finite are done with zeros; it gets its NaN
+        // at the end.)
 #pragma unroll
         for (int k = 0; k < KQ; ++k) {
 #pragma unroll
@@ -801,7 +804,7 @@ __global__ __launch_bounds__(64 * tile_waves(D), D == 64 ? 2 : 1) void mnb_atten
         n.spoilt = (uint32_t)__builtin_amdgcn_ballot_w64(spoilt) & 15u;
         // A run whose scale is zero, or from 2^-10 to 2^8 of the sums' unit, keeps that
         // unit (128 times 2^8 is within fp16's range); another one has its own.  (Sums of
-        // a unit 2^90 larger have their last bit above what they would lose.)
+        // a unit 2^80 larger have their last bit above what they would lose.)
         const bool none = unit_bits == 0;
         float most = vs;
         if (P < 64) {
@@ -810,7 +813,7 @@ __global__ __launch_bounds__(64 * tile_waves(D), D == 64 ? 2 : 1) void mnb_atten
         }
         const float base = !none ? __uint_as_float(unit_bits) : most == 0.f ? 1.f : most;
         const bool near = vs == 0.f || (vs >= base * 0x1p-10f && vs <= base * 0x1p8f);
-        const float ref = near ? base : fmaxf(vs, fmaxf(most, base) * 0x1p-90f);
+        const float ref = near ? base : fmaxf(vs, fmaxf(most, base) * 0x1p-80f);
         lane_r = vs == ref ? 1.f : vs / ref;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -990,7 +993,7 @@ __global__ __launch_bounds__(64 * tile_waves(D), D == 64 ? 2 : 1) void mnb_atten
             }
         return;
     }
-    const int64_t part = (((int64_t)at.slot * p.heads + h) * p.splits + z) * BR + 32 * (wave / SHARE) + r;
+    const int64_t part = (((int64_t)slot * p.heads + h) * p.splits + z) * BR + 32 * (wave / SHARE) + r;
     float* dst = p.tile_o + part * D + elem0 + 8 * hh;
 #pragma unroll
     for (int d = 0; d < DB; ++d)
@@ -1018,7 +1021,7 @@ __global__ __launch_bounds__(256) void mnb_attention_tile_join_kernel(AttentionP
     const Sequence q = at.q;
     const int32_t in = 16 * (int)blockIdx.z + (threadIdx.x >> 4), row = at.rt * BR + in, e0 = 4 * (threadIdx.x & 15);
     if (row >= q.n * p.G) return;
-    const int64_t first = ((int64_t)at.slot * p.heads + h) * p.splits * BR + in;
+    const int64_t first = ((int64_t)blockIdx.y * p.heads + h) * p.splits * BR + in;
     float m = kLowest, l = 0.f;
     for (int z = 0; z < p.splits; ++z) m = fmaxf(m, p.tile_ml[(first + z * BR) * 2]);
     float4_t y[D / 64];
@@ -1045,7 +1048,9 @@ __global__ __launch_bounds__(256) void mnb_attention_tile_join_kernel(AttentionP
 template <int D, bool BF16>
 int queue(const AttentionParams& p, const AttentionLayout& lay, hipStream_t stream, int* launches)
 {
-    const dim3 tiles((unsigned)p.heads, (unsigned)p.tile_slots, (unsigned)p.splits);
+    // (Keys are split where tiles are few, far fewer than kGridTiles.)
+    const dim3 tiles((unsigned)p.heads, (unsigned)(p.tile_slots < kGridTiles ? p.tile_slots : kGridTiles),
+                     (unsigned)(p.splits > 1 ? p.splits : (p.tile_slots + kGridTiles - 1) / kGridTiles));
     if (p.tile_slots) {
         constexpr size_t lds = (size_t)4 * (64 * (D + 8) + D * 72);
         hipLaunchKernelGGL((mnb_attention_tile_kernel<D, BF16>), tiles, dim3(64 * tile_waves(D)), lds, stream, p);

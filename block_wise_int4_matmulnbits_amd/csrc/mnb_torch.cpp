@@ -199,8 +199,10 @@ PyObject* py_append(PyObject*, PyObject* const* a, Py_ssize_t n)
             cp = static_cast<float*>(dense("cos", a[2], {rows, rot / 2}, at::kFloat, index));
             sp = static_cast<float*>(dense("sin", a[3], {rows, rot / 2}, at::kFloat, index));
         }
+        const int near = PyObject_IsTrue(a[13]);
+        if (near < 0) throw python_error();
         return g_append(&c.cache, &c.batch, code, kp, ks, vp, vs, qp, qs, op, os, heads, cp, sp, rot, rows,
-                        PyObject_IsTrue(a[13]) == 1, address(a[14]));
+                        near, address(a[14]));
     });
 }
 

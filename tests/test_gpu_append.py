@@ -275,3 +275,64 @@ def test_in_place_and_streams():
         for got, ref, name in zip(args[3:], b2.cache(), ("k_pages", "v_pages", "k_scales", "v_scales")):
             _same(got, ref, name)
         assert torch.equal(_bits(fused[:, :hq].cpu()), _bits(_round(want, BF16)))
+
+
+@pytest.mark.parametrize("new", [[1 + i % 3 for i in range(90)], [(11 * i) % 40 for i in range(66)]], ids=["few", "more"])
+def test_many_sequences(new):
+    """More sequences than a wave has lanes."""
+    G.require_gpu()
+    b = R.Batch(new, [(7 * i) % 50 for i in range(len(new))], 16, 2, 64, seed=13, extra=3)
+    q, k, v = _values(b.T, 4, 2, 64, BF16, 14)
+    cos, sin = _tables(b.width * 16, 64)
+    _run(b, q, k, v, cos, sin)
+
+
+def test_no_pages():
+    """A cache of no pages stores nothing; the queries are rotated all the same."""
+    G.require_gpu()
+    b = R.Batch([2, 5], [10, 3], 16, 1, 64, seed=1)
+    b.pages = 0
+    for name in ("k_pages", "v_pages", "k_scales", "v_scales"):
+        setattr(b, name, getattr(b, name)[:0])
+    q, k, v = _values(b.T, 3, 1, 64, F16, 2)
+    cos, sin = _tables(b.width * 16, 32)
+    _run(b, q, k, v, cos, sin)
+
+
+def test_starts_that_overlap():
+    """Sequences that claim the same rows: nothing outside the cache's pages."""
+    G.require_gpu()
+    T, P, heads, D = 40, 16, 2, 64
+    b = R.Batch([T], [20], P, heads, D, seed=6, extra=2)
+    args = b.cuda()
+    args[0] = torch.tensor([0, T, 0, T, 0, T], dtype=torch.int32, device="cuda")
+    args[1], args[2] = args[1].repeat(5), args[2].repeat(5, 1).contiguous()
+    q, k, v = _values(b.T, 2, heads, D, F16, 3)
+    guard = [torch.cat((t.reshape(-1), t.new_ones(64))) for t in args[3:]]
+    views = [g[:-64].view(t.shape) for g, t in zip(guard, args[3:])]
+    q_out = torch.full((b.T, 2, D), 7.0, dtype=F16, device="cuda")
+    mnb.append_kv_int8(k.contiguous().cuda(), v.contiguous().cuda(), None, None, *args[:3], *views,
+                       q=q.contiguous().cuda(), q_out=q_out)
+    torch.cuda.synchronize()
+    for g in guard:
+        assert bool((g[-64:] == 1).all())
+    assert bool((q_out[T:] == 7.0).all())
+
+
+def test_offsets_past_32_bits():
+    """Pages more than 4 GiB into the cache."""
+    G.require_gpu()
+    pages, P, heads, D = 70000, 64, 8, 128
+    b = R.Batch([1, 70], [63, 100], P, heads, D, seed=3)
+    q, k, v = _values(b.T, 0, heads, D, BF16, 3)
+    where = torch.tensor([pages - 1 - 7 * i for i in range(b.pages)])
+    dev = b.cuda()
+    far = [torch.zeros((pages,) + t.shape[1:], dtype=t.dtype, device="cuda") for t in dev[3:]]
+    for dst, src in zip(far, dev[3:]):
+        dst[where.cuda()] = src
+    table = torch.where(b.table >= 0, where[b.table.clamp(min=0).long()], b.table.long()).to(torch.int32)
+    mnb.append_kv_int8(k.contiguous().cuda(), v.contiguous().cuda(), None, None, dev[0], dev[1], table.cuda(), *far)
+    torch.cuda.synchronize()
+    R.append(b, k, v, None, None)
+    for got, ref, name in zip(far, b.cache(), ("k_pages", "v_pages", "k_scales", "v_scales")):
+        _same(got[where.cuda()], ref, name)

@@ -315,3 +315,133 @@ def test_captured(new):
         assert torch.equal(out.cpu(), _call(b, x))
         want, tol = R.attention(b, x, 64 ** -0.5)
         R.check_rows(out.cpu(), want, tol, F16)
+
+
+def test_queries_of_every_size():
+    """Queries up to bf16's largest value, and the smallest ones that scores can show."""
+    G.require_gpu()
+    for size, step in ((1e38, -124), (1e-28, 100)):
+        for new in ([1, 2], [70]):
+            b = R.Batch(new, [40] * len(new), 32, 1, 64, seed=5)
+            b.k_scales = torch.full_like(b.k_scales, 2.0 ** step)
+            q = (_queries(b.T, 2, 64, torch.float32, 6).clamp(-3, 3) * size).to(BF16)
+            mean = size * 2.0 ** step * 64 * 8      # of a score's magnitude
+            _check(b, q, scale=3.0 / mean)
+
+
+def test_starts_that_overlap():
+    """Sequences that claim the same rows, more of them than the sizes of the call
+    can hold: nothing behind the workspace, no row outside the sequences."""
+    G.require_gpu()
+    for T, G_ in ((150, 2), (40, 1)):
+        b = R.Batch([T], [100], 32, 1, 64, seed=6, extra=4)
+        b.S, b.table = 5, b.table.repeat(5, 1).contiguous()
+        b.lengths = b.lengths.repeat(5)
+        b.starts = torch.tensor([0, T, 0, T, 0, T], dtype=torch.int32)
+        need = mnb.mnb_attention_workspace(b.T, b.S, G_, 1, 64)
+        ws = torch.full((need + 65536,), 0x5A, dtype=torch.uint8, device="cuda")
+        got = _call(b, _queries(b.T, G_, 64, BF16, 1), workspace=ws)
+        assert bool((ws[need:] == 0x5A).all())
+        assert bool((got[T:] == 9.0).all())
+
+
+def test_no_pages():
+    """A cache of no pages, a page table of no width: rows of zeros."""
+    G.require_gpu()
+    for new in ([1, 3], [90, 1]):
+        for width in (0, 2):
+            b = R.Batch(new, [10, 10], 16, 1, 64, seed=1)
+            b.pages, b.width = 0, width
+            b.table = torch.zeros(2, width, dtype=torch.int32)
+            for name in ("k_pages", "v_pages", "k_scales", "v_scales"):
+                setattr(b, name, getattr(b, name)[:0])
+            assert bool((_call(b, _queries(b.T, 2, 64, F16, 1)) == 0).all())
+
+
+MANY = [
+    # new, before, P, query heads, heads, D
+    ([1 + i % 2 for i in range(70)], [3 * i for i in range(70)], 16, 4, 2, 64),
+    ([i % 3 for i in range(131)], [(17 * i) % 90 for i in range(131)], 32, 8, 1, 128),
+    ([66 if i % 9 == 0 else 1 for i in range(80)], [i for i in range(80)], 16, 2, 1, 64),
+    ([1100, 1, 2], [0, 300, 7], 64, 64, 1, 64),      # row tiles enough for 64-bit counts
+]
+
+
+@pytest.mark.parametrize("shape", MANY, ids=[str(i) for i in range(len(MANY))])
+def test_many_sequences(shape):
+    """More sequences than a wave has lanes, or more work than 32 bits count."""
+    G.require_gpu()
+    new, before, P, hq, heads, D = shape
+    b = R.Batch(new, before, P, heads, D, seed=11, extra=2)
+    q = _queries(b.T, hq, D, BF16, 5)
+    for most in (None, max(new)):
+        _check(b, q, max_tokens=most)
+
+
+def test_more_tiles_than_a_grid_row():
+    """2049 sequences of 64 tokens with 64 rows each: 65568 tiles."""
+    G.require_gpu()
+    b = R.Batch([64, 64, 64], [0, 0, 0], 64, 1, 64, seed=12)
+    q = _queries(b.T, 64, 64, F16, 3)
+    want = _check(b, q)
+    times = 683
+    big = R.Batch([64, 64, 64], [0, 0, 0], 64, 1, 64, seed=12)
+    big.S, big.table, big.lengths = 3 * times, b.table.repeat(times, 1), b.lengths.repeat(times)
+    big.starts = torch.arange(0, 64 * (3 * times + 1), 64, dtype=torch.int32)
+    x = q.cuda().repeat(times, 1, 1)
+    out = torch.full_like(x, 9.0)
+    mnb.attention_int8(x, *big.cuda(), out)
+    torch.cuda.synchronize()
+    assert bool((out.view(times, 192, 64, 64) == out[:192]).all())
+    exact, tol = R.attention(b, q, 64 ** -0.5)
+    R.check_rows(out[:192].cpu(), exact, tol, F16)
+    assert want.shape == out[:192].shape
+
+
+def test_offsets_past_32_bits():
+    """Pages more than 4 GiB into the cache."""
+    G.require_gpu()
+    pages, P, heads, D = 70000, 64, 8, 128
+    for new in ([1, 2], [70, 1]):
+        b = R.Batch(new, [200, 90], P, heads, D, seed=3)
+        q = _queries(b.T, 16, D, BF16, 3)
+        want = _call(b, q)
+        where = torch.tensor([pages - 1 - 7 * i for i in range(b.pages)])
+        dev = b.cuda()
+        far = [torch.zeros((pages,) + t.shape[1:], dtype=t.dtype, device="cuda") for t in dev[3:]]
+        for dst, src in zip(far, dev[3:]):
+            dst[where.cuda()] = src
+        table = torch.where(b.table >= 0, where[b.table.clamp(min=0).long()], b.table.long()).to(torch.int32)
+        out = torch.empty_like(q).cuda()
+        mnb.attention_int8(q.cuda(), dev[0], dev[1], table.cuda(), *far, out)
+        torch.cuda.synchronize()
+        assert torch.equal(out.cpu(), want)
+
+
+def test_two_graphs_of_one_workspace():
+    """Two captured calls of different batches that share a workspace, replayed in
+    turn with eager calls between them."""
+    G.require_gpu()
+    sets = []
+    for i, new in enumerate(([1, 2, 1], [1, 90, 3])):
+        b = R.Batch(new, [500, 30, 9], 16, 2, 64, seed=i)
+        sets.append((b, _queries(b.T, 6, 64, F16, i)))
+    need = max(mnb.mnb_attention_workspace(b.T, b.S, 6, 2, 64) for b, _ in sets)
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    work = []
+    for b, q in sets:
+        args, x = b.cuda(), q.cuda()
+        out = torch.empty_like(x)
+        mnb.attention_int8(x, *args, out, workspace=ws)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            mnb.attention_int8(x, *args, out, workspace=ws)
+        work.append((graph, args, x, out, _call(b, q)))
+    for i in (0, 1, 1, 0, 1, 0):
+        graph, args, x, out, want = work[i]
+        out.fill_(3.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out.cpu(), want)
+        _call(*sets[1 - i])
