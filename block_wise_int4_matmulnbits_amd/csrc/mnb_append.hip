@@ -49,6 +49,7 @@ struct AppendParams {
     int64_t k_stride, v_stride, q_stride, q_out_stride;   // elements between tokens
     int32_t heads, q_heads, rot;
     int32_t slots;            // page slots of the grid
+    int32_t narrow;           // workgroups of one wave
     int32_t by_token;         // slot of a sequence's first page: its first token, else see slot_base
 };
 
@@ -437,9 +438,10 @@ __device__ __forceinline__ void turn_queries(const AppendParams& p, int64_t t)
     }
 }
 
-// Workgroups of four waves, or of one where the sequences have a token or two each:
-// of a page's few units the other waves would get none (64 sequences of one to three
-// tokens).
+// Workgroups of four waves, or of one where a page gets 16 tokens or fewer on average:
+// of its few units the other waves would get few or none (8 heads of 128: 64
+// sequences of one token 9.7 -> 7.8 us, 200 of 16 33.8 -> 23.3, 200 of 32 on pages of 16
+// 70.6 -> 42.9; but one of 32 on a page of 64 7.2 -> 8.4 and of 256 wide 11.9 -> 19.7).
 template <int D, bool BF16, bool NEAR, int kThreads>
 __global__ __launch_bounds__(kThreads) void mnb_append_kernel(AppendParams p)
 {
@@ -472,7 +474,7 @@ __global__ __launch_bounds__(kThreads) void mnb_append_kernel(AppendParams p)
 template <int D, bool BF16, bool NEAR>
 int queue(const AppendParams& p, int64_t tokens, hipStream_t stream)
 {
-    const int threads = p.by_token ? 64 : 256;
+    const int threads = p.narrow ? 64 : 256;
     const int64_t rows = 2 * p.heads, each = rows * (threads / 64);      // queries of a column: a token a wave
     const dim3 grid((unsigned)(p.slots + (p.q ? (tokens + each - 1) / each : 0)), (unsigned)rows);
     if (threads == 64) hipLaunchKernelGGL((mnb_append_kernel<D, BF16, NEAR, 64>), grid, dim3(64), 0, stream, p);
@@ -516,6 +518,7 @@ int launch_append(const AppendArgs& a, void* stream)
     const int64_t T = a.batch.tokens, loose = T / a.cache.page_size + 2 * a.batch.sequences;
     p.by_token = T <= loose;
     p.slots = (int32_t)(p.by_token ? T : loose);
+    p.narrow = a.cache.page_size <= 16 || T <= 16 * a.batch.sequences;
     const hipStream_t st = static_cast<hipStream_t>(stream);
     return a.cache.head_dim == 64 ? queue<64>(p, a, st) : a.cache.head_dim == 128 ? queue<128>(p, a, st) : queue<256>(p, a, st);
 }
