@@ -649,15 +649,10 @@ AttentionLayout attention_layout(int64_t tokens, int64_t sequences, int64_t q_he
     l.tile_ml = l.o + parts * 16 * D * 4;
     const int64_t rows = tokens * (q_heads / kv_heads), tile = tile_rows(head_dim);
     // Full tiles, and one more for each sequence that can have many rows.
-    l.tile_slots = rows > kAttentionManyRows
-                       ? (int)(rows / tile + std::min<int64_t>(sequences, rows / (kAttentionManyRows + 1))) : 0;
-    // Tiles that leave compute units (256) empty have their keys split so that whole
-    // rounds of them are full.
-    const int64_t tiles = (rows / tile + 1) * kv_heads, cus = 256;
-    l.splits = 1;
-    for (int z = 2; z <= 16 && tiles < 2 * cus; ++z)
-        if (ceil_div(tiles * z, cus) * l.splits < ceil_div(tiles * l.splits, cus) * z) l.splits = z;
-    const size_t each = l.splits > 1 ? (size_t)l.tile_slots * (size_t)kv_heads * (size_t)l.splits * (size_t)tile : 0;
+    l.many = attention_many_rows(tokens, q_heads, head_dim);
+    l.tile_slots = rows > l.many ? (int)(rows / tile + std::min<int64_t>(sequences, rows / (l.many + 1))) : 0;
+    l.shares = l.tile_slots && (rows / tile + 1) * kv_heads < 512 ? tile_shares(head_dim) : 0;
+    const size_t each = 2 * (size_t)l.shares * (size_t)tile;
     l.tile_o = l.tile_ml + each * 2 * 4;
     l.bytes = l.tile_o + each * D * 4;
     return l;
@@ -666,16 +661,28 @@ AttentionLayout attention_layout(int64_t tokens, int64_t sequences, int64_t q_he
 LoraLayout lora_layout(int64_t m, int64_t K, int64_t N, int64_t R, int64_t adapters)
 {
     LoraLayout l;
-    l.row_tiles = m <= 16 ? 1 : R <= 128 ? 4 : 2;
-    const int64_t rows = 16 * l.row_tiles, tiles = ceil_div(m, rows);
-    // Few rows may have an adapter each; many rows come in runs of one.
-    l.ways = (int)std::max<int64_t>(1, std::min<int64_t>(tiles == 1 ? 64 : 1, std::min(adapters, std::min(m, rows))));
-    int64_t splits = ceil_div(512, tiles * l.ways);
-    splits = std::min<int64_t>(splits, std::min<int64_t>(m <= 16 ? 16 : 8, std::max<int64_t>(1, K / 256)));
+    // 64 columns a wave, or 16 where that leaves compute units empty: 512 rows x 6144
+    // columns 20.7 -> 12.6 us; 64 rows x 14336, 32 adapters 71.3 wide, 33.2 narrow; 128 rows
+    // x 14336, 100 adapters 78.8, 65.4 (112 workgroups both).
+    l.wide = ceil_div(N, 512) * ceil_div(m, m <= 16 ? 16 : 32) >= 128;
+    // Tiles of 32 rows, whose adapters are read for one tile after another, or of 64 where
+    // those fill the device (narrow): 64 rows x 28672, 32 adapters, rank 64 58.0 -> 43.5 us;
+    // 40 rows x 16384 32.5 -> 36.5.
+    l.up_tiles = m <= 16 ? 1 : !l.wide && m > 32 && m <= 64 && R <= 128 && N > 64 * 384 ? 4 : 2;
+    // The first launch: 512 rows, 14336 -> 16 15.8 us with 32, 17.9 with 64; 1024 rows of 8
+    // adapters, 4096 -> 64 50.7 with 32, 44.7 with 64.
+    l.down_tiles = m <= 16 ? 1 : m < 1024 || R > 128 ? 2 : 4;
+    const int64_t rows = 16 * l.down_tiles, tiles = ceil_div(m, rows);
+    // Two workgroups a compute unit (256), of 256 or more of K each; slices cost the second
+    // launch their sums.  (Half or twice as many: within 4%.)
+    const int64_t splits = std::min<int64_t>(ceil_div(512, tiles), std::min<int64_t>(m <= 16 ? 16 : 8, std::max<int64_t>(1, K / 256)));
     const int64_t slice = ceil_div(ceil_div(K, splits), 128) * 128;
     l.k_slice = (int)std::max<int64_t>(128, slice);
     l.splits = (int)std::max<int64_t>(1, ceil_div(K, l.k_slice));
-    l.wide = ceil_div(N, 512) * tiles >= 256;
+    // Rows may have an adapter each: workgroups that share a tile's adapters (64 rows of
+    // 32 adapters, rank 64: one workgroup 188 us, these 33); those that get none end at
+    // once (4096 rows in runs of 500: 90 us with or without them).
+    l.ways = (int)std::max<int64_t>(1, std::min<int64_t>(std::min(adapters, std::min(m, rows)), 512 / (tiles * l.splits)));
     l.bytes = (size_t)l.splits * (size_t)m * (size_t)R * 4;
     return l;
 }

@@ -38,6 +38,7 @@ constexpr int kWaves = 4;
 constexpr int kWorkgroups = kAttentionWorkgroups, kMostParts = kAttentionWorkgroups;
 constexpr int kBegin = 4;
 constexpr int kGridTiles = 32768;     // tiles of a grid's y
+constexpr int kTileBegin = 4, kTileLeast = 2, kTileMore = 6, kTileJoin = 10;
 constexpr float kLowest = -3.0e38f;   // a running maximum before any key
 
 struct AttentionParams {
@@ -50,14 +51,14 @@ struct AttentionParams {
     const float* v_scales;
     float* part_o;            // [2 workgroups][16][D]: sums of split rows
     float* part_ml;           // [2 workgroups][16][2]: their maximum and weight
-    float* tile_o;            // [slots of tiles][heads][splits][tile rows][D]
-    float* tile_ml;           // the same without D, two each
+    float* tile_o;            // [2 shares][tile rows][D]: sums of tiles that workgroups share
+    float* tile_ml;           // [2 shares][tile rows][2]
     int64_t q_stride, out_stride;
     int32_t heads, G;         // key heads, rows a token has for each
     int32_t slots;            // row tiles of the joining launch's grid
     int32_t tiles_each;       // of a sequence in it, or 0
     int32_t many;             // sequences of more rows than this go to the tiles
-    int32_t tile_slots, splits;   // of the tiles' grid
+    int32_t tile_slots, shares;   // of the tiles' grid
     int32_t small;            // up to 64 sequences, whose work (but for the heads) fits 32 bits
     float scale_log2;         // scale * log2(e)
 };
@@ -92,24 +93,41 @@ __device__ __forceinline__ int64_t units_of(const AttentionParams& p, int32_t s)
     return count_of(p, work_of(p, sequence(p.b, s)));
 }
 
-// Sum over the wave, in every lane.
-__device__ __forceinline__ int64_t wave_sum(int64_t v)
+// Sum over the lanes up to this one, in the manner of wave_prefix32; and over all.
+template <int kControl, int kRows>
+__device__ __forceinline__ int64_t from_lane(int64_t v)
 {
-#pragma unroll
-    for (int d = 32; d; d >>= 1) v += __shfl_xor(v, d);
-    return v;
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int32_t)v, kControl, kRows, 0xF, false);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int32_t)(v >> 32), kControl, kRows, 0xF, false);
+    return (int64_t)((uint64_t)hi << 32 | lo);
 }
-
-// Sum over the lanes up to this one.
 __device__ __forceinline__ int64_t wave_prefix(int64_t v)
 {
-    const int lane = threadIdx.x & 63;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-        const int64_t o = __shfl_up(v, d);
-        if (lane >= d) v += o;
-    }
+    v += from_lane<0x111, 0xF>(v);
+    v += from_lane<0x112, 0xF>(v);
+    v += from_lane<0x114, 0xF>(v);
+    v += from_lane<0x118, 0xF>(v);
+    v += from_lane<0x142, 0xA>(v);
+    v += from_lane<0x143, 0xC>(v);
     return v;
+}
+__device__ __forceinline__ int64_t read_lane(int64_t v, int lane)
+{
+    return (int64_t)((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int32_t)(v >> 32), lane) << 32 |
+                     (uint32_t)__builtin_amdgcn_readlane((int32_t)v, lane));
+}
+__device__ __forceinline__ int64_t wave_sum(int64_t v) { return read_lane(wave_prefix(v), 63); }
+
+// The largest of the wave.
+__device__ __forceinline__ uint32_t wave_max(uint32_t v)
+{
+    v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int32_t)v, 0x111, 0xF, 0xF, false));
+    v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int32_t)v, 0x112, 0xF, 0xF, false));
+    v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int32_t)v, 0x114, 0xF, 0xF, false));
+    v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int32_t)v, 0x118, 0xF, 0xF, false));
+    v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int32_t)v, 0x142, 0xA, 0xF, false));
+    v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int32_t)v, 0x143, 0xC, 0xF, false));
+    return (uint32_t)__builtin_amdgcn_readlane((int32_t)v, 63);
 }
 
 // Units of every sequence, and of those before sequence s.
@@ -160,8 +178,8 @@ __device__ __forceinline__ Start start_of(const AttentionParams& p, const Sequen
         return r;
     }
     int64_t mine = lane < p.b.S ? units_of(p, lane) : 0, upto = wave_prefix(mine), base = 0;
-    r.all = uniform64(__shfl(upto, 63));
-    for (int32_t s0 = 64; s0 < p.b.S; s0 += 64) r.all += uniform64(wave_sum(s0 + lane < p.b.S ? units_of(p, s0 + lane) : 0));
+    r.all = read_lane(upto, 63);
+    for (int32_t s0 = 64; s0 < p.b.S; s0 += 64) r.all += wave_sum(s0 + lane < p.b.S ? units_of(p, s0 + lane) : 0);
     r.share = share_of(r.all);
     r.unit = (int64_t)blockIdx.x * r.share;
     r.before = 0;
@@ -175,11 +193,11 @@ __device__ __forceinline__ Start start_of(const AttentionParams& p, const Sequen
         const uint64_t past = __builtin_amdgcn_ballot_w64(base + upto > r.unit);
         if (past) {
             const int l = __builtin_ctzll(past);
-            r.before = uniform64(base + __shfl(upto - mine, l));
+            r.before = base + read_lane(upto - mine, l);
             r.s = uniform(s0 + l);
             return r;
         }
-        base += uniform64(__shfl(upto, 63));
+        base += read_lane(upto, 63);
     }
     return r;
 }
@@ -229,10 +247,9 @@ __device__ __forceinline__ int32_t tiles_of(const AttentionParams& p, const Sequ
     const int32_t rows = q.n * p.G;
     return rows > p.many ? (rows + BR - 1) / BR : 0;
 }
-__device__ __forceinline__ Tile tile_of(const AttentionParams& p, int32_t y, int BR)
+__device__ __forceinline__ Tile tile_of(const AttentionParams& p, const Sequences& seqs, int32_t y, int BR)
 {
     const int lane = threadIdx.x & 63;
-    const Sequences seqs(p.b);
     int32_t all = 0, base = 0;            // (at most 2^26 rows, and a tile more for each sequence)
     for (int32_t s0 = 0; s0 < p.b.S; s0 += 64) {
         const Sequence q = p.b.S <= 64 ? seqs.mine : sequence(p.b, s0 + lane < p.b.S ? s0 + lane : 0);
@@ -255,6 +272,84 @@ __device__ __forceinline__ Tile tile_of(const AttentionParams& p, int32_t y, int
         base = __builtin_amdgcn_readlane(upto, 63);
     }
     return t;
+}
+
+// Few tiles of many rows are cut into equal shares of the whole batch's work, a
+// workgroup each.  Tile i of a sequence sees about start + (i + 1) BR / G keys, and
+// counts as that and as kTileBegin units (64 keys) more; counts are in 1 / G of a key,
+// so that those of the tiles before i have a closed form.
+struct Count {
+    int64_t first, tiles;     // of a tile but for its own rows; tiles of the sequence
+    int32_t BR;
+    __device__ __forceinline__ int64_t upto(int64_t i) const { return i * first + BR * (i * (i + 1) / 2); }
+    __device__ __forceinline__ int64_t all() const { return upto(tiles); }
+};
+__device__ __forceinline__ Count count_tiles(const AttentionParams& p, const Sequence& q, int BR)
+{
+    const int32_t cap = p.b.max_pages << p.b.page_bits;
+    return Count{(int64_t)p.G * (clamp32(q.length - q.n, 0, cap) + 64 * kTileBegin), tiles_of(p, q, BR), BR};
+}
+
+// Where a border between shares lies: sequence s, key head h, tile rt, and how far
+// into its count (s: b.S where the batch ends before).  cut: false where whole tiles
+// take no longer than shares.
+struct Place {
+    int64_t all, share, in;
+    int32_t s, h, rt;
+    bool cut;
+    Sequence q;
+    Count c;
+};
+__device__ __forceinline__ Place place_of(const AttentionParams& p, const Sequences& seqs, int64_t border, int BR)
+{
+    const int lane = threadIdx.x & 63;
+    auto get = [&](int32_t s0) { return p.b.S <= 64 ? seqs.mine : sequence(p.b, s0 + lane < p.b.S ? s0 + lane : 0); };
+    auto count = [&](int32_t s0, const Count& c) { return s0 + lane < p.b.S ? c.all() * p.heads : 0; };
+    Place r;
+    r.all = 0;
+    int64_t tiles = 0;
+    uint32_t longest = 0;                 // count of a tile: 64 heads of 2^24 keys at most, and its own rows
+    for (int32_t s0 = 0; s0 < p.b.S; s0 += 64) {
+        const Count c = count_tiles(p, get(s0), BR);
+        r.all += wave_sum(count(s0, c));
+        const bool any = s0 + lane < p.b.S && c.tiles > 0;
+        tiles += __builtin_amdgcn_readlane(wave_prefix32(any ? (int32_t)c.tiles : 0), 63);
+        longest = max(longest, wave_max(any ? (uint32_t)(c.first + c.tiles * BR) : 0u));
+    }
+    const int64_t unit = (int64_t)p.G * 64, least = unit * kTileLeast;
+    r.share = divide(r.all + p.shares - 1, p.shares);
+    r.share = uniform64(r.share < least ? least : r.share);
+    r.cut = tiles * p.heads > 2 * p.shares ||
+            (tiles * p.heads > p.shares ? 3 : 2) * (int64_t)longest >
+                2 * (r.share + unit * kTileMore + divide(unit * kTileJoin * r.all, r.share * p.shares));
+    const int64_t at = border * r.share;
+    r.s = p.b.S;
+    r.h = r.rt = 0;
+    r.in = 0;
+    if (!r.cut || at >= r.all) return r;
+    int64_t base = 0;
+    for (int32_t s0 = 0; s0 < p.b.S; s0 += 64) {
+        const int64_t mine = count(s0, count_tiles(p, get(s0), BR)), upto = base + wave_prefix(mine);
+        const uint64_t past = __builtin_amdgcn_ballot_w64(upto > at);
+        if (past) {
+            const int l = __builtin_ctzll(past);
+            r.s = s0 + l;
+            r.q = seqs.at(r.s);
+            r.c = count_tiles(p, r.q, BR);
+            r.in = at - read_lane(upto - mine, l);
+            break;
+        }
+        base = read_lane(upto, 63);
+    }
+    if (r.s >= p.b.S || r.in < 0) {       // (numbers of the batch that overflow)
+        r.s = p.b.S;
+        return r;
+    }
+    r.h = uniform((int32_t)divide(r.in, r.c.all()));
+    r.in -= r.h * r.c.all();
+    r.rt = wave_search((int32_t)r.c.tiles, r.in, [&](int32_t i) { return r.c.upto(i); });
+    r.in -= r.c.upto(r.rt);
+    return r;
 }
 
 template <int D, bool BF16>
@@ -545,15 +640,114 @@ __global__ __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) void mnb_attention_r
     }
 }
 
+// Tiles that several workgroups shared: their sums, in the order of the keys.  A
+// workgroup for every kJoinEach-th of the rows that a border between shares has to
+// itself: the borders within a tile divide its rows, D / 4 threads a row, those that
+// few rows leave over every so many of the parts.
+constexpr int kJoinThreads = 256, kJoinEach = 4;
+template <int D>
+struct TileJoin {
+    Place place;
+    float4_t y[kJoinThreads];
+    float m[kJoinThreads * 4 / D], l[kJoinThreads * 4 / D];
+};
+template <int D, bool BF16>
+__device__ __forceinline__ void join_tiles(const AttentionParams& p, int32_t id, TileJoin<D>& meet)
+{
+    constexpr int BR = tile_rows(D), LANES = D / 4, GROUPS = kJoinThreads / LANES;
+    const int64_t border = id / kJoinEach + 1;
+    if (border >= p.shares) return;
+    if (threadIdx.x < 64) {
+        const Place found = place_of(p, Sequences(p.b), border, BR);
+        if (threadIdx.x == 0) meet.place = found;
+    }
+    __syncthreads();
+    const Place at = meet.place;
+    if (at.s >= p.b.S || at.in == 0) return;
+    // The shares w0 .. w1 of the tile.
+    const int64_t begin = border * at.share - at.in, w0 = divide(begin, at.share);
+    const int64_t w1 = divide(begin + at.c.upto(at.rt + 1) - at.c.upto(at.rt) - 1, at.share);
+    const int parts = (int)(w1 - w0) + 1;
+    if (w0 + parts > p.shares || parts < 2) return;      // (numbers of the batch that overflow)
+    const Sequence q = at.q;
+    const int rows = min(BR, q.n * p.G - at.rt * BR), workers = (parts - 1) * kJoinEach;
+    const int worker = (int)(border - w0 - 1) * kJoinEach + id % kJoinEach;
+    const int first = rows * worker / workers, count = rows * (worker + 1) / workers - first;
+    int ways = GROUPS;
+    while (ways > 1 && count > GROUPS / ways) ways >>= 1;
+    const int group = threadIdx.x / LANES, lane = threadIdx.x % LANES, way = group % ways;
+    for (int i0 = 0; i0 < count; i0 += GROUPS / ways) {
+        const int i = i0 + group / ways;
+        const bool mine = i < count;
+        const int in = first + (mine ? i : 0);
+        float m = kLowest, l = 0.f;
+        float4_t y = float4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll 8
+        for (int n = way; n < parts; n += ways) {
+            const int64_t part = (2 * (w0 + n) + (n == 0 ? 1 : 0)) * BR + in;
+            const float its = p.tile_ml[part * 2], own = p.tile_ml[part * 2 + 1];
+            const float4_t sums = *reinterpret_cast<const float4_t*>(p.tile_o + part * D + 4 * lane);
+            const float now = fmaxf(m, its), keep = exp2_fast(m - now), f = exp2_fast(its - now);
+            m = now;
+            l = l * keep + own * f;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) y[e] = y[e] * keep + (own == 0.f ? 0.f : sums[e] * f);   // 0: no sums stored
+        }
+        if (ways > 1) {
+            if (lane == 0) {
+                meet.m[group] = m;
+                meet.l[group] = l;
+            }
+            meet.y[threadIdx.x] = y;
+            __syncthreads();
+            if (way == 0) {
+                float m_all = m;
+                for (int w = 1; w < ways; ++w) m_all = fmaxf(m_all, meet.m[group + w]);
+                float f = exp2_fast(m - m_all);
+                l *= f;
+                y *= f;
+                for (int w = 1; w < ways; ++w) {
+                    f = exp2_fast(meet.m[group + w] - m_all);
+                    l += meet.l[group + w] * f;
+                    y += meet.y[threadIdx.x + w * LANES] * f;
+                }
+            }
+            __syncthreads();
+        }
+        if (way == 0 && mine) {
+            const Row to = row_of(p, at.rt * BR + in, at.h);
+            const float by = l == 0.f ? 0.f : 1.f / l;
+            uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + (q.t0 + to.token) * p.out_stride + (int64_t)to.head * D + 4 * lane);
+            dst[0] = (uint32_t)narrow16(y[0] * by, BF16) | (uint32_t)narrow16(y[1] * by, BF16) << 16;
+            dst[1] = (uint32_t)narrow16(y[2] * by, BF16) | (uint32_t)narrow16(y[3] * by, BF16) << 16;
+        }
+    }
+}
+
 // Row tiles whose keys several workgroups shared: their sums, in the order of
 // the keys.  Sequences without keys get rows of zeros.  Grid: (row tiles, heads,
-// D / 64); a workgroup takes 64 elements of each of 16 rows.
+// D / 64); a workgroup takes 64 elements of each of 16 rows.  Behind the row tiles, the
+// borders between the shares of tiles.
 template <int D, bool BF16>
 __global__ __launch_bounds__(256) void mnb_attention_join_kernel(AttentionParams p)
 {
-    __shared__ float factor[16][kMostParts + 1];
-    __shared__ float inverse[16];
-    __shared__ float4_t meet[256];
+    struct RowJoin {
+        float factor[16][kMostParts + 1];
+        float inverse[16];
+        float4_t meet[256];
+    };
+    __shared__ union {
+        TileJoin<D> tiles;
+        RowJoin rows;
+    } lds;
+    if ((int32_t)blockIdx.x >= p.slots) {
+        const int32_t id = (((int32_t)blockIdx.x - p.slots) * (int32_t)gridDim.y + (int32_t)blockIdx.y) * (int32_t)gridDim.z + (int32_t)blockIdx.z;
+        join_tiles<D, BF16>(p, id, lds.tiles);
+        return;
+    }
+    auto& factor = lds.rows.factor;
+    auto& inverse = lds.rows.inverse;
+    auto& meet = lds.rows.meet;
     const int64_t slot = blockIdx.x;
     const int32_t h = blockIdx.y;
     // A sequence's first slot: the most tiles that the ones before it can have, or
@@ -698,13 +892,32 @@ __global__ __launch_bounds__(64 * tile_waves(D), D == 64 ? 2 : 1) void mnb_atten
     const int tid = threadIdx.x, lane = tid & 63, r = lane & 31, hh = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int part_of_row = wave % SHARE, elem0 = 32 * DB * part_of_row;
-    const int32_t h = blockIdx.x, z = p.splits > 1 ? (int32_t)blockIdx.z : 0;
+    const int32_t cap = p.b.max_pages << p.b.page_bits, P = 1 << p.b.page_bits;
 
-    // The tile: counted from the last one, whose rows see the most keys.
-    const int32_t slot = (int32_t)blockIdx.y + (p.splits > 1 ? 0 : kGridTiles * (int32_t)blockIdx.z);
-    const Tile at = tile_of(p, slot, BR);
+    // Whole tiles, counted from the last one, whose rows see the most keys; or those of
+    // a share, the first and the last perhaps in part.
+    Place at;
+    int64_t left = 0;                                      // of the share
+    int32_t number = p.shares ? (int32_t)blockIdx.x
+                              : ((int32_t)blockIdx.y + kGridTiles * (int32_t)blockIdx.z) * p.heads + (int32_t)blockIdx.x;
+    auto pick = [&](const Sequences& seqs) {
+        const int32_t y = uniform((int32_t)((uint32_t)number / (uint32_t)p.heads));
+        const Tile t = tile_of(p, seqs, y, BR);
+        at.s = t.s;
+        at.h = number - y * p.heads;
+        at.rt = t.rt;
+        at.q = t.q;
+    };
+    {
+        const Sequences seqs(p.b);
+        at.cut = false;
+        if (p.shares) at = place_of(p, seqs, blockIdx.x, BR);
+        if (at.cut) left = at.all - blockIdx.x * at.share < at.share ? at.all - blockIdx.x * at.share : at.share;
+        else pick(seqs);
+    }
     if (at.s >= p.b.S) return;
-    const int32_t s = at.s, row0 = at.rt * BR;
+    for (;;) {
+    const int32_t s = at.s, h = at.h, row0 = at.rt * BR;
     const Sequence q = at.q;
     const int32_t rows = q.n * p.G, start = q.length - q.n;
     const int32_t wave0 = row0 + 32 * (wave / SHARE), mine = wave0 + r < rows ? wave0 + r : rows - 1;
@@ -714,10 +927,19 @@ __global__ __launch_bounds__(64 * tile_waves(D), D == 64 ? 2 : 1) void mnb_atten
     const int32_t last = start + row_of(p, row0 + BR < rows ? row0 + BR - 1 : rows - 1, h).token;
     const int32_t lowest = start + row_of(p, wave0 < rows ? wave0 : rows - 1, h).token;
     const int32_t highest = start + row_of(p, wave0 + 31 < rows ? wave0 + 31 : rows - 1, h).token;
-    const int32_t cap = p.b.max_pages << p.b.page_bits;
     const int32_t keys = last < 0 ? 0 : last + 1 < cap ? last + 1 : cap;
     const int32_t units = (keys + 63) / 64;
-    const int32_t c0 = (int32_t)((int64_t)units * z / p.splits), c1 = (int32_t)((int64_t)units * (z + 1) / p.splits);
+    int32_t c0 = 0, c1 = units;
+    bool whole = true;
+    int64_t slot = 0;
+    if (at.cut) {
+        const int64_t count = at.c.upto(at.rt + 1) - at.c.upto(at.rt), end = count - at.in < left ? count : at.in + left;
+        whole = at.in == 0 && end == count;
+        slot = 2 * (int64_t)blockIdx.x + (at.in ? 0 : 1);
+        c0 = uniform((int32_t)divide(units * at.in, count));
+        c1 = uniform((int32_t)divide(units * end, count));
+        left -= end - at.in;
+    }
 
     half8_t qv[KQ];
     float q_scale;
@@ -764,7 +986,6 @@ __global__ __launch_bounds__(64 * tile_waves(D), D == 64 ? 2 : 1) void mnb_atten
     // Staging.  Piece i of a thread: key k_token of the unit, elements k_elem ..; and
     // element v_elem, run tid % 4.
     const int32_t* table = p.b.table + (int64_t)s * p.b.max_pages;
-    const int P = 1 << p.b.page_bits;
     auto entry = [&](int c) {            // lane: the page of run lane % 4 of unit c
         const int32_t index = (c * 64 + 16 * (lane & 3)) >> p.b.page_bits;
         return index < p.b.max_pages ? table[index] : -1;
@@ -793,7 +1014,8 @@ __global__ __launch_bounds__(64 * tile_waves(D), D == 64 ? 2 : 1) void mnb_atten
         lane_ks = live ? fabsf(p.k_scales[at_scale]) : 0.f;
         lane_vs = live ? fabsf(p.v_scales[at_scale]) : 0.f;
     };
-    uint32_t unit_bits = 0;              // bits of the sums' unit, alike in every lane; 0: no sums yet
+    uint32_t unit_bits = 0;              // bits of the unit of this wave's sums; 0: no sums yet
+    uint32_t staged = 0;                 // of a wave that multiplies every unit: alike in all waves
     Runs now;
     float lane_r;                        // what remains of run lane % 4's value scale
     auto settle = [&](Runs& n) {
@@ -805,13 +1027,13 @@ __global__ __launch_bounds__(64 * tile_waves(D), D == 64 ? 2 : 1) void mnb_atten
         // A run whose scale is zero, or from 2^-10 to 2^8 of the sums' unit, keeps that
         // unit (128 times 2^8 is within fp16's range); another one has its own.  (Sums of
         // a unit 2^80 larger have their last bit above what they would lose.)
-        const bool none = unit_bits == 0;
+        const bool none = staged == 0;
         float most = vs;
         if (P < 64) {
             most = fmaxf(most, __shfl_xor(most, 1));
             most = fmaxf(most, __shfl_xor(most, 2));
         }
-        const float base = !none ? __uint_as_float(unit_bits) : most == 0.f ? 1.f : most;
+        const float base = !none ? __uint_as_float(staged) : most == 0.f ? 1.f : most;
         const bool near = vs == 0.f || (vs >= base * 0x1p-10f && vs <= base * 0x1p8f);
         const float ref = near ? base : fmaxf(vs, fmaxf(most, base) * 0x1p-80f);
         lane_r = vs == ref ? 1.f : vs / ref;
@@ -821,6 +1043,12 @@ __global__ __launch_bounds__(64 * tile_waves(D), D == 64 ? 2 : 1) void mnb_atten
             n.bias[i] = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(bias), i));
             n.ref[i] = __builtin_amdgcn_readlane(__float_as_uint(ref), i);
         }
+        // The runs are multiplied a unit of the sums at a time, in the order of the units'
+        // first runs.
+        staged = n.ref[0];
+        staged = n.ref[1] != n.ref[0] ? n.ref[1] : staged;
+        staged = n.ref[2] != n.ref[0] && n.ref[2] != n.ref[1] ? n.ref[2] : staged;
+        staged = n.ref[3] != n.ref[0] && n.ref[3] != n.ref[1] && n.ref[3] != n.ref[2] ? n.ref[3] : staged;
     };
     auto store = [&](int buffer) {
         const uint32_t r2 = f16_pair(lane_r, lane_r), half_r2 = f16_pair(0.5f * lane_r, 0.5f * lane_r);
@@ -975,9 +1203,8 @@ __global__ __launch_bounds__(64 * tile_waves(D), D == 64 ? 2 : 1) void mnb_atten
     const float unit = __uint_as_float(unit_bits);
     weight += __shfl_xor(weight, 32);
     if (!q_finite && weight > 0.f) weight = __uint_as_float(0x7FC00000u);
-    if (wave0 + r >= rows) return;
     // o[d][8 e + j]: element elem0 + 32 d + 16 e + 8 hh + j.
-    if (p.splits == 1) {
+    if (wave0 + r < rows && whole) {
         const float by = weight == 0.f ? 0.f : unit / weight;
         uint16_t* dst = p.out + (q.t0 + me.token) * p.out_stride + (int64_t)me.head * D + elem0 + 8 * hh;
 #pragma unroll
@@ -991,76 +1218,58 @@ __global__ __launch_bounds__(64 * tile_waves(D), D == 64 ? 2 : 1) void mnb_atten
                            (uint32_t)narrow16(o[d][8 * e + 2 * j + 1] * by, BF16) << 16;
                 *reinterpret_cast<u32x4*>(dst + 32 * d + 16 * e) = w;
             }
-        return;
+    } else if (wave0 + r < rows) {
+        const int64_t part = slot * BR + 32 * (wave / SHARE) + r;
+        float* dst = p.tile_o + part * D + elem0 + 8 * hh;
+        if (c0 < c1)
+#pragma unroll
+            for (int d = 0; d < DB; ++d)
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+                        *reinterpret_cast<float4_t*>(dst + 32 * d + 16 * e + 4 * j) =
+                            float4_t{o[d][8 * e + 4 * j] * unit, o[d][8 * e + 4 * j + 1] * unit,
+                                     o[d][8 * e + 4 * j + 2] * unit, o[d][8 * e + 4 * j + 3] * unit};
+        if (hh == 0 && part_of_row == 0) {
+            p.tile_ml[part * 2] = top;
+            p.tile_ml[part * 2 + 1] = weight;
+        }
     }
-    const int64_t part = (((int64_t)slot * p.heads + h) * p.splits + z) * BR + 32 * (wave / SHARE) + r;
-    float* dst = p.tile_o + part * D + elem0 + 8 * hh;
-#pragma unroll
-    for (int d = 0; d < DB; ++d)
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-                *reinterpret_cast<float4_t*>(dst + 32 * d + 16 * e + 4 * j) =
-                    float4_t{o[d][8 * e + 4 * j] * unit, o[d][8 * e + 4 * j + 1] * unit, o[d][8 * e + 4 * j + 2] * unit,
-                             o[d][8 * e + 4 * j + 3] * unit};
-    if (hh == 0 && part_of_row == 0) {
-        p.tile_ml[part * 2] = top;
-        p.tile_ml[part * 2 + 1] = weight;
-    }
-}
 
-// The splits of a tile's keys, in order.  Grid: (heads, tiles, rows of a tile / 16).
-template <int D, bool BF16>
-__global__ __launch_bounds__(256) void mnb_attention_tile_join_kernel(AttentionParams p)
-{
-    constexpr int BR = tile_rows(D);
-    const int32_t h = blockIdx.x;
-    const Tile at = tile_of(p, blockIdx.y, BR);
-    if (at.s >= p.b.S) return;
-    const Sequence q = at.q;
-    const int32_t in = 16 * (int)blockIdx.z + (threadIdx.x >> 4), row = at.rt * BR + in, e0 = 4 * (threadIdx.x & 15);
-    if (row >= q.n * p.G) return;
-    const int64_t first = ((int64_t)blockIdx.y * p.heads + h) * p.splits * BR + in;
-    float m = kLowest, l = 0.f;
-    for (int z = 0; z < p.splits; ++z) m = fmaxf(m, p.tile_ml[(first + z * BR) * 2]);
-    float4_t y[D / 64];
-#pragma unroll
-    for (int i = 0; i < D / 64; ++i) y[i] = float4_t{0.f, 0.f, 0.f, 0.f};
-    for (int z = 0; z < p.splits; ++z) {
-        const int64_t part = first + z * BR;
-        const float f = exp2_fast(p.tile_ml[part * 2] - m);
-        l += p.tile_ml[part * 2 + 1] * f;
-#pragma unroll
-        for (int i = 0; i < D / 64; ++i) y[i] += *reinterpret_cast<const float4_t*>(p.tile_o + part * D + 64 * i + e0) * f;
+    // On to the next tile.
+    if (!at.cut) {
+        number += p.shares;
+        if (p.shares == 0 || number >= p.tile_slots * p.heads) return;
+        pick(Sequences(p.b));
+        if (at.s >= p.b.S) return;
+        continue;
     }
-    const Row to = row_of(p, row, h);
-    const float by = l == 0.f ? 0.f : 1.f / l;
-    uint16_t* dst = p.out + (q.t0 + to.token) * p.out_stride + (int64_t)to.head * D + e0;
-#pragma unroll
-    for (int i = 0; i < D / 64; ++i) {
-        uint32_t* w = reinterpret_cast<uint32_t*>(dst + 64 * i);
-        w[0] = (uint32_t)narrow16(y[i][0] * by, BF16) | (uint32_t)narrow16(y[i][1] * by, BF16) << 16;
-        w[1] = (uint32_t)narrow16(y[i][2] * by, BF16) | (uint32_t)narrow16(y[i][3] * by, BF16) << 16;
+    if (left <= 0) return;
+    at.in = 0;
+    if (++at.rt >= at.c.tiles) {
+        at.rt = 0;
+        if (++at.h >= p.heads) {
+            at.h = 0;
+            do {
+                if (++at.s >= p.b.S) return;
+                at.q = uniform_sequence(p.b, at.s);
+                at.c = count_tiles(p, at.q, BR);
+            } while (at.c.tiles == 0);
+        }
+    }
     }
 }
 
 template <int D, bool BF16>
 int queue(const AttentionParams& p, const AttentionLayout& lay, hipStream_t stream, int* launches)
 {
-    // (Keys are split where tiles are few, far fewer than kGridTiles.)
-    const dim3 tiles((unsigned)p.heads, (unsigned)(p.tile_slots < kGridTiles ? p.tile_slots : kGridTiles),
-                     (unsigned)(p.splits > 1 ? p.splits : (p.tile_slots + kGridTiles - 1) / kGridTiles));
+    const dim3 tiles = p.shares ? dim3((unsigned)p.shares)
+                                : dim3((unsigned)p.heads, (unsigned)(p.tile_slots < kGridTiles ? p.tile_slots : kGridTiles),
+                                       (unsigned)((p.tile_slots + kGridTiles - 1) / kGridTiles));
     if (p.tile_slots) {
         constexpr size_t lds = (size_t)4 * (64 * (D + 8) + D * 72);
         hipLaunchKernelGGL((mnb_attention_tile_kernel<D, BF16>), tiles, dim3(64 * tile_waves(D)), lds, stream, p);
-        const int e = (int)hipGetLastError();
-        if (e != 0) return e;
-        ++*launches;
-    }
-    if (p.tile_slots && p.splits > 1) {
-        hipLaunchKernelGGL((mnb_attention_tile_join_kernel<D, BF16>),
-                           dim3((unsigned)p.heads, (unsigned)p.tile_slots, tile_rows(D) / 16), dim3(256), 0, stream, p);
         const int e = (int)hipGetLastError();
         if (e != 0) return e;
         ++*launches;
@@ -1069,8 +1278,10 @@ int queue(const AttentionParams& p, const AttentionLayout& lay, hipStream_t stre
     int e = (int)hipGetLastError();
     if (e != 0) return e;
     ++*launches;
-    hipLaunchKernelGGL((mnb_attention_join_kernel<D, BF16>), dim3((unsigned)p.slots, (unsigned)p.heads, D / 64), dim3(256),
-                       0, stream, p);
+    const int each = p.heads * (D / 64), borders = p.shares ? (p.shares - 1) * kJoinEach : 0;
+    hipLaunchKernelGGL((mnb_attention_join_kernel<D, BF16>),
+                       dim3((unsigned)(p.slots + (borders + each - 1) / each), (unsigned)p.heads, D / 64), dim3(256), 0,
+                       stream, p);
     e = (int)hipGetLastError();
     if (e == 0) ++*launches;
     return e;
@@ -1102,16 +1313,16 @@ int launch_attention(const AttentionArgs& a, void* stream, int* launches)
     p.part_o = reinterpret_cast<float*>(ws + lay.o);
     p.tile_ml = reinterpret_cast<float*>(ws + lay.tile_ml);
     p.tile_o = reinterpret_cast<float*>(ws + lay.tile_o);
-    p.many = kAttentionManyRows;
+    p.many = lay.many;
     // No sequence can have many rows where max_tokens says so.
     const bool few = a.max_tokens > 0 && a.max_tokens * p.G <= p.many;
     p.tile_slots = few ? 0 : lay.tile_slots;
     if (few) p.many = INT32_MAX;
     // (max_tokens is not trusted with the place of a row tile.)
-    const int64_t loose = a.batch.tokens * p.G / 16 + a.batch.sequences, each = (kAttentionManyRows + 15) / 16;
+    const int64_t loose = a.batch.tokens * p.G / 16 + a.batch.sequences, each = (lay.many + 15) / 16;
     p.tiles_each = !few && each * a.batch.sequences <= loose ? (int32_t)each : 0;
     p.slots = (int32_t)(p.tiles_each ? each * a.batch.sequences : loose);
-    p.splits = lay.splits;
+    p.shares = few ? 0 : lay.shares;
     // Tiles of few rows: at most tokens G / 16 and one for each sequence, of 2^18 units.
     p.small = a.batch.sequences <= 64 && a.batch.tokens * p.G / 16 + a.batch.sequences < (1 << 12);
     const hipStream_t s = static_cast<hipStream_t>(stream);

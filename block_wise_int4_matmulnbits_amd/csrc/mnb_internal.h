@@ -230,19 +230,28 @@ struct AttentionArgs {
 };
 int launch_attention(const AttentionArgs& args, void* stream, int* launches) MNB_WEAK;
 
-// Sequences of more rows (tokens times query heads of a key head) than this go
-// to tiles of tile_rows() rows, the others to a fixed number of workgroups.
-constexpr int kAttentionManyRows = 64;
+// Sequences of more rows (tokens times query heads of a key head) than this go to
+// tiles of tile_rows() rows, the others to a fixed number of workgroups.  The tiles'
+// workgroups take long to begin and end; the others read the keys once for every 16
+// rows.  (8 heads of 128, one sequence of 256 rows over 1024 / 8192 / 32768 keys: 16 /
+// 36 / 102 us against tiles' 29 / 38 / 70, of 128 rows 13 / 26 / 61 against 27 / 34 /
+// 65; 16 sequences of 96 rows 48 / 242 / 904 against 55 / 205 / 785.  Heads of 256, 96
+// rows over 8192 keys: 69 against 55.)
+constexpr int attention_many_rows(int64_t tokens, int64_t q_heads, int64_t head_dim)
+{
+    return head_dim <= 128 && tokens * q_heads <= 2048 ? 256 : 64;
+}
 constexpr int kAttentionWorkgroups = 512;
 constexpr int tile_waves(int64_t head_dim) { return head_dim >= 128 ? 8 : 4; }
 constexpr int tile_rows(int64_t head_dim) { return head_dim == 128 ? 256 : 128; }
+constexpr int tile_shares(int64_t head_dim) { return head_dim == 64 ? 512 : 256; }   // workgroups that run at a time
 
 // The attention's workspace.  Few rows: for each workgroup the sums of two row
 // tiles that it shares with others, behind their maxima and weights.  Many: the
-// tiles there can be, and the sums of the splits of their keys, where few tiles
-// leave the device empty.  Host-only arithmetic (mnb_api.cpp).
+// tiles there can be; where they are few, the workgroups that share them (else 0)
+// and the same sums of two tiles for each.  Host-only arithmetic (mnb_api.cpp).
 struct AttentionLayout {
-    int tile_slots, splits;
+    int many, tile_slots, shares;
     size_t o, tile_ml, tile_o, bytes;
 };
 AttentionLayout attention_layout(int64_t tokens, int64_t sequences, int64_t q_heads, int64_t kv_heads, int64_t head_dim);
@@ -268,7 +277,8 @@ int launch_lora(const LoraArgs& args, void* stream, int* launches) MNB_WEAK;
 // launch takes 64 columns a wave (or 16), and the workspace that holds the
 // slices' sums.  Host-only arithmetic (mnb_api.cpp).
 struct LoraLayout {
-    int row_tiles, splits, k_slice, ways;
+    int down_tiles, up_tiles;    // of 16 rows, a workgroup's
+    int splits, k_slice, ways;
     bool wide;
     size_t bytes;
 };

@@ -294,7 +294,7 @@ __global__ __launch_bounds__(64 * W) void mnb_lora_up_kernel(LoraParams p)
 
     // Each row by 16 neighbouring threads, four ranks a time: at most 256 ranks.
     for (int i = threadIdx.x >> 4; i < RT; i += 4 * W) {
-        const int32_t own = __shfl(list.id, i);  // RT <= 64: the lane that holds row i
+        const int32_t own = __shfl(list.id, i);  // the lane that holds row i
         const float s = own >= 0 ? (p.scaling ? p.scaling[own] : 1.f) : 0.f;
         const float* src = p.t + (row0 + i) * p.R;
         float4_t v[4];
@@ -419,14 +419,22 @@ int queue_up(const LoraParams& p, hipStream_t s)
 }
 
 template <bool BF16, int NRT>
+int queue_down(const LoraParams& p, unsigned ways, hipStream_t s)
+{
+    return p.R <= 16 ? queue_down<BF16, NRT, 1>(p, ways, s) : p.R <= 32 ? queue_down<BF16, NRT, 2>(p, ways, s)
+         : p.R <= 48 ? queue_down<BF16, NRT, 3>(p, ways, s) : queue_down<BF16, NRT, 4>(p, ways, s);
+}
+
+template <bool BF16>
 int queue(const LoraParams& p, const LoraLayout& lay, hipStream_t s)
 {
     const unsigned ways = (unsigned)lay.ways;
-    const int e = p.R <= 16 ? queue_down<BF16, NRT, 1>(p, ways, s) : p.R <= 32 ? queue_down<BF16, NRT, 2>(p, ways, s)
-                : p.R <= 48 ? queue_down<BF16, NRT, 3>(p, ways, s) : queue_down<BF16, NRT, 4>(p, ways, s);
+    const int e = lay.down_tiles == 1 ? queue_down<BF16, 1>(p, ways, s) : lay.down_tiles == 2 ? queue_down<BF16, 2>(p, ways, s)
+                                      : queue_down<BF16, 4>(p, ways, s);
     if (e != 0) return e;
-    // Wide: 32 rows a workgroup (4091 x 4097 columns, rank 40: 61 us with 64, 53 with 32).
-    return lay.wide ? queue_up<BF16, NRT == 1 ? 1 : 2, 4, 8>(p, s) : queue_up<BF16, NRT, 1, 4>(p, s);
+    if (lay.up_tiles == 1) return lay.wide ? queue_up<BF16, 1, 4, 8>(p, s) : queue_up<BF16, 1, 1, 4>(p, s);
+    if (lay.up_tiles == 4) return queue_up<BF16, 4, 1, 4>(p, s);
+    return lay.wide ? queue_up<BF16, 2, 4, 8>(p, s) : queue_up<BF16, 2, 1, 4>(p, s);
 }
 
 }  // namespace
@@ -456,9 +464,7 @@ int launch_lora(const LoraArgs& a, void* stream, int* launches)
     p.out_bf16 = a.out_bf16;
     const hipStream_t s = static_cast<hipStream_t>(stream);
     *launches = 2;
-    if (lay.row_tiles == 1) return a.bf16 ? queue<true, 1>(p, lay, s) : queue<false, 1>(p, lay, s);
-    if (lay.row_tiles == 2) return a.bf16 ? queue<true, 2>(p, lay, s) : queue<false, 2>(p, lay, s);
-    return a.bf16 ? queue<true, 4>(p, lay, s) : queue<false, 4>(p, lay, s);
+    return a.bf16 ? queue<true>(p, lay, s) : queue<false>(p, lay, s);
 }
 
 }  // namespace mnb

@@ -63,6 +63,14 @@ SHAPES = [
     ([1100], [0], 64, 60, 30, 128),
     ([9], [4000], 64, 64, 1, 128),
     ([90, 333], [2000, 1], 256, 5, 5, 64),
+    ([65], [0], 64, 36, 1, 128),
+    ([1, 200, 3, 90], [500, 0, 70, 1000], 32, 16, 2, 128),
+    ([257, 70], [3, 64], 16, 8, 2, 128),
+    ([66, 65], [4000, 100], 16, 16, 4, 128),
+    ([130, 300], [33, 0], 64, 6, 1, 256),
+    ([9, 9, 9, 9], [5000, 1, 0, 640], 16, 64, 1, 64),
+    ([33], [9000], 32, 64, 1, 128),
+    ([130, 4], [700, 90], 64, 16, 16, 64),
 ]
 
 
@@ -130,23 +138,25 @@ def test_scales_far_apart_many_rows():
             assert bool((_call(b, q) == 0).all())
 
 
-def test_large_scores_many_rows():
+@pytest.mark.parametrize("hq", [4, 30])
+def test_large_scores_many_rows(hq):
     G.require_gpu()
     for scale in (2.0, -0.5, 0.0, 1e-3):
         for dtype in (F16, BF16):
             b = R.Batch([100, 70], [90, 300], 16, 2, 64, seed=5)
             b.k_scales = torch.full_like(b.k_scales, 2.0 ** -4)
-            _check(b, _queries(b.T, 4, 64, dtype, 3), scale=scale)
+            _check(b, _queries(b.T, hq, 64, dtype, 3), scale=scale)
 
 
-def test_not_finite_many_rows():
+@pytest.mark.parametrize("hq", [2, 24])
+def test_not_finite_many_rows(hq):
     """Rows of tiles that do not see a page whose scale is NaN, or a query that is
     not finite, keep their bits."""
     G.require_gpu()
     for P in (16, 64):
         for D in (64, 128, 256):
             b = R.Batch([100], [61], P, 1, D, seed=2)
-            q = _queries(b.T, 2, D, BF16, 1)
+            q = _queries(b.T, hq, D, BF16, 1)
             clean = _call(b, q)
             for bad in (float("nan"), float("inf"), float("-inf")):
                 q2 = q.clone()
@@ -166,13 +176,14 @@ def test_not_finite_many_rows():
                 scales[page, 0] = was
 
 
-def test_sizes_of_queries_many_rows():
+@pytest.mark.parametrize("hq", [2, 32])
+def test_sizes_of_queries_many_rows(hq):
     G.require_gpu()
     for dtype, sizes in ((F16, (6e-8, 1e-4, 3000.0)), (BF16, (1e-38, 1e-10, 1e15))):
         for size in sizes:
             b = R.Batch([70], [100], 32, 1, 64, seed=3)
             b.k_scales = torch.full_like(b.k_scales, 2.0 ** -10)
-            q = (_queries(70, 2, 64, torch.float32, 6) * size).to(dtype)
+            q = (_queries(70, hq, 64, torch.float32, 6) * size).to(dtype)
             _check(b, q, scale=min(1.0, 0.1 / size))
 
 
@@ -284,8 +295,9 @@ def test_strides_streams_and_workspaces():
         assert torch.equal(big[:, 3:11].cpu(), q)
 
 
-@pytest.mark.parametrize("new", [[1, 2, 1, 0], [1, 40, 3, 30]], ids=["few", "many"])
-def test_captured(new):
+@pytest.mark.parametrize("new,hq", [([1, 2, 1, 0], 6), ([1, 40, 3, 30], 6), ([1, 40, 3, 30], 40)],
+                         ids=["few", "more", "many"])
+def test_captured(new, hq):
     """A captured call replayed with other lengths, pages and queries, eager calls
     between the replays."""
     G.require_gpu()
@@ -297,7 +309,7 @@ def test_captured(new):
             t = getattr(b, name)
             setattr(b, name, torch.cat((t, t.new_zeros((pages - t.shape[0],) + t.shape[1:]))))
         b.pages = pages
-        sets.append((b, _queries(b.T, 6, 64, F16, i)))
+        sets.append((b, _queries(b.T, hq, 64, F16, i)))
     args, q = sets[0][0].cuda(), sets[0][1].cuda()
     out = torch.empty_like(q)
     mnb.attention_int8(q, *args, out)
@@ -321,10 +333,10 @@ def test_queries_of_every_size():
     """Queries up to bf16's largest value, and the smallest ones that scores can show."""
     G.require_gpu()
     for size, step in ((1e38, -124), (1e-28, 100)):
-        for new in ([1, 2], [70]):
+        for new, hq in (([1, 2], 2), ([70], 2), ([70], 30)):
             b = R.Batch(new, [40] * len(new), 32, 1, 64, seed=5)
             b.k_scales = torch.full_like(b.k_scales, 2.0 ** step)
-            q = (_queries(b.T, 2, 64, torch.float32, 6).clamp(-3, 3) * size).to(BF16)
+            q = (_queries(b.T, hq, 64, torch.float32, 6).clamp(-3, 3) * size).to(BF16)
             mean = size * 2.0 ** step * 64 * 8      # of a score's magnitude
             _check(b, q, scale=3.0 / mean)
 
@@ -333,7 +345,7 @@ def test_starts_that_overlap():
     """Sequences that claim the same rows, more of them than the sizes of the call
     can hold: nothing behind the workspace, no row outside the sequences."""
     G.require_gpu()
-    for T, G_ in ((150, 2), (40, 1)):
+    for T, G_ in ((150, 2), (40, 1), (150, 16)):
         b = R.Batch([T], [100], 32, 1, 64, seed=6, extra=4)
         b.S, b.table = 5, b.table.repeat(5, 1).contiguous()
         b.lengths = b.lengths.repeat(5)
@@ -348,14 +360,14 @@ def test_starts_that_overlap():
 def test_no_pages():
     """A cache of no pages, a page table of no width: rows of zeros."""
     G.require_gpu()
-    for new in ([1, 3], [90, 1]):
+    for new, hq in (([1, 3], 2), ([90, 1], 2), ([90, 1], 30)):
         for width in (0, 2):
             b = R.Batch(new, [10, 10], 16, 1, 64, seed=1)
             b.pages, b.width = 0, width
             b.table = torch.zeros(2, width, dtype=torch.int32)
             for name in ("k_pages", "v_pages", "k_scales", "v_scales"):
                 setattr(b, name, getattr(b, name)[:0])
-            assert bool((_call(b, _queries(b.T, 2, 64, F16, 1)) == 0).all())
+            assert bool((_call(b, _queries(b.T, hq, 64, F16, 1)) == 0).all())
 
 
 MANY = [
@@ -423,7 +435,7 @@ def test_two_graphs_of_one_workspace():
     turn with eager calls between them."""
     G.require_gpu()
     sets = []
-    for i, new in enumerate(([1, 2, 1], [1, 90, 3])):
+    for i, new in enumerate(([1, 2, 1], [1, 400, 3])):
         b = R.Batch(new, [500, 30, 9], 16, 2, 64, seed=i)
         sets.append((b, _queries(b.T, 6, 64, F16, i)))
     need = max(mnb.mnb_attention_workspace(b.T, b.S, 6, 2, 64) for b, _ in sets)
@@ -445,3 +457,15 @@ def test_two_graphs_of_one_workspace():
         torch.cuda.synchronize()
         assert torch.equal(out.cpu(), want)
         _call(*sets[1 - i])
+
+
+def test_scales_change_under_the_diagonal():
+    """Value scales that change from page to page where some waves of a tile see no
+    key any more: all waves stage the values in the same unit."""
+    G.require_gpu()
+    for D in (64, 128, 256):
+        for P, before in ((16, 5), (16, 700), (64, 1), (64, 37), (256, 1), (256, 130)):
+            b = R.Batch([333], [before], P, 2, D, seed=D + P)      # 1332 rows a key head
+            for i in range(b.width):
+                b.v_scales[int(b.table[0, i])] = 2.0 ** (-4 - 3 * (i % 4))
+            _check(b, _queries(b.T, 8, D, BF16, 4))

@@ -40,7 +40,8 @@ SHAPES = [
     (1, 16, 1, 8, 1, 1), (1, 4096, 4096, 16, 8, 1), (2, 256, 65, 8, 3, 1), (7, 1040, 129, 24, 5, 1),
     (16, 512, 256, 64, 16, 1), (17, 528, 300, 32, 40, 1), (64, 1024, 1000, 64, 32, 1), (65, 272, 257, 16, 3, 9),
     (100, 2064, 511, 40, 6, 1), (300, 144, 64, 128, 7, 50), (129, 512, 320, 200, 4, 20), (70, 96, 33, 256, 2, 1),
-    (1000, 32, 16, 8, 5, 333),
+    (1000, 32, 16, 8, 5, 333), (64, 64, 25001, 40, 20, 1), (1100, 160, 40, 8, 3, 100), (1030, 160, 33, 32, 3, 1),
+    (1024, 144, 17, 48, 2, 7), (1025, 96, 20, 128, 2, 300),
 ]
 
 
