@@ -356,6 +356,10 @@ template <int D, bool BF16>
 __global__ __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) void mnb_attention_rows_kernel(AttentionParams p)
 {
     constexpr int KS = D / 64, DT = D / 16;
+    // Pieces of a unit's keys and values that registers hold: all, or half, each one's
+    // successor loaded as it is multiplied (heads of 256, all: spills, 64 sequences over
+    // 4000 keys 289 -> 213 us; two waves a SIMD on half as many registers: 434).
+    constexpr int KT = D <= 128 ? 4 : 2, VT = D <= 128 ? DT : DT / 2;
     __shared__ float lds_o[kWaves][16][D + 4];
     __shared__ float lds_m[kWaves][16], lds_l[kWaves][16];
     const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
@@ -415,8 +419,8 @@ __global__ __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) void mnb_attention_r
             // |x| < 2^ex, and n = rint(x 2^(22 - ex)) in the low bits of n + 1.5 * 2^23.
             // The three signed digits of n are the bytes of n + 0x808080, each with
             // its top bit turned.
-            // (At least 2^-80: the factor of the scores stays a normal number.)
-            const int ex = max((int)(__float_as_uint(widen16(top, BF16)) >> 23), 46) - 126;
+            // (At least 2^-100: the factor of the scores stays a normal number.)
+            const int ex = max((int)(__float_as_uint(widen16(top, BF16)) >> 23), 26) - 126;
             const float up = finite ? pow2(22 - ex) : 0.f;
             uint32_t sum = 0;
 #pragma unroll
@@ -457,39 +461,44 @@ __global__ __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) void mnb_attention_r
             return index < p.b.max_pages ? table[index] : -1;
         };
         auto usable = [&](int32_t page) { return page >= 0 && page < p.b.pages; };
-        i32x4 a[4][KS], v[DT];
+        i32x4 a[KT][KS], v[VT];
         float ks, vs;
         bool ok;                 // run g lies in a usable page
-        auto load_keys = [&](int c, int32_t page_k, int32_t page_v) {
+        const int8_t *kp, *vp;   // the lane's part of the unit whose pieces are loaded next
+        auto keys_at = [&](int c, int32_t page) {
             const int32_t key = c * 64 + 16 * (r >> 2) + (r & 3);
-            const int8_t* kp = p.k_pages + ((((int64_t)(usable(page_k) ? page_k : 0) * p.heads + h) << p.b.page_bits) +
-                                            (key & (P - 1))) * D + 16 * g;
+            kp = p.k_pages + ((((int64_t)(usable(page) ? page : 0) * p.heads + h) << p.b.page_bits) + (key & (P - 1))) * D + 16 * g;
+        };
+        auto load_keys = [&](int t) {
 #pragma unroll
-            for (int t = 0; t < 4; ++t)
-#pragma unroll
-                for (int k = 0; k < KS; ++k)
-                    a[t][k] = *reinterpret_cast<const i32x4*>(kp + 4 * t * D + 64 * k);
+            for (int k = 0; k < KS; ++k) a[t % KT][k] = *reinterpret_cast<const i32x4*>(kp + 4 * t * D + 64 * k);
+        };
+        auto load_scales = [&](int c, int32_t page) {
             // The scales of a run behind the sequence's last token mean nothing; a page
             // of 64 tokens or more has one value scale for the whole unit.
-            ok = usable(page_v);
-            const int64_t at = (int64_t)(ok ? page_v : 0) * p.heads + h;
+            ok = usable(page);
+            const int64_t at = (int64_t)(ok ? page : 0) * p.heads + h;
             const bool live = ok && c * 64 + 16 * g < q.length;
             ks = live ? p.k_scales[at] : 0.f;
             vs = live || (ok && P >= 64) ? p.v_scales[at] : 0.f;
         };
-        auto load_values = [&](int c, int32_t page_v) {
-            const int8_t* vp = p.v_pages + (((int64_t)(usable(page_v) ? page_v : 0) * p.heads + h) << p.b.page_bits) * D +
-                               (int64_t)r * P + ((c * 64 + 16 * g) & (P - 1));
-#pragma unroll
-            for (int d = 0; d < DT; ++d) v[d] = *reinterpret_cast<const i32x4*>(vp + (int64_t)16 * d * P);
+        auto values_at = [&](int c, int32_t page) {
+            vp = p.v_pages + (((int64_t)(usable(page) ? page : 0) * p.heads + h) << p.b.page_bits) * D + (int64_t)r * P +
+                 ((c * 64 + 16 * g) & (P - 1));
         };
+        auto load_values = [&](int d) { v[d % VT] = *reinterpret_cast<const i32x4*>(vp + (int64_t)16 * d * P); };
         int c = c0 + wave;
         int32_t next_k = 0, next_v = 0;
         if (c < c1) {
             next_k = entry(c, r >> 2);
             next_v = entry(c, g);
-            load_keys(c, next_k, next_v);
-            load_values(c, next_v);
+            keys_at(c, next_k);
+#pragma unroll
+            for (int t = 0; t < KT; ++t) load_keys(t);
+            load_scales(c, next_v);
+            values_at(c, next_v);
+#pragma unroll
+            for (int d = 0; d < VT; ++d) load_values(d);
             if (c + kWaves < c1) {
                 next_k = entry(c + kWaves, r >> 2);
                 next_v = entry(c + kWaves, g);
@@ -506,16 +515,27 @@ __global__ __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) void mnb_attention_r
                 i32x4 c0v = i32x4{half, half, half, half}, c1v = i32x4{0, 0, 0, 0}, c2v = i32x4{0, 0, 0, 0};
 #pragma unroll
                 for (int k = 0; k < KS; ++k) {
-                    c0v = __builtin_amdgcn_mfma_i32_16x16x64_i8(a[t][k], qd[0][k], c0v, 0, 0, 0);
-                    c1v = __builtin_amdgcn_mfma_i32_16x16x64_i8(a[t][k], qd[1][k], c1v, 0, 0, 0);
-                    c2v = __builtin_amdgcn_mfma_i32_16x16x64_i8(a[t][k], qd[2][k], c2v, 0, 0, 0);
+                    c0v = __builtin_amdgcn_mfma_i32_16x16x64_i8(a[t % KT][k], qd[0][k], c0v, 0, 0, 0);
+                    c1v = __builtin_amdgcn_mfma_i32_16x16x64_i8(a[t % KT][k], qd[1][k], c1v, 0, 0, 0);
+                    c2v = __builtin_amdgcn_mfma_i32_16x16x64_i8(a[t % KT][k], qd[2][k], c2v, 0, 0, 0);
                 }
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     x[4 * t + i] = fmaf(fmaf((float)((c2v[i] << 8) + c1v[i]), 256.f, (float)c0v[i]), factor, bias);
-                if (t & 1) __builtin_amdgcn_sched_barrier(0);     // keeps the sums of few tiles live
+                if (KT < 4) {
+                    if (t + KT == 4 && more) keys_at(c + kWaves, next_k);
+                    if (t + KT < 4 || more) load_keys((t + KT) % 4);
+                }
+                if (KT < 4 || (t & 1)) __builtin_amdgcn_sched_barrier(0);     // keeps the sums of few tiles live
             }
-            if (more) load_keys(c + kWaves, next_k, next_v);
+            if (more) {
+                if (KT == 4) {
+                    keys_at(c + kWaves, next_k);
+#pragma unroll
+                    for (int t = 0; t < 4; ++t) load_keys(t);
+                }
+                load_scales(c + kWaves, next_v);
+            }
             __builtin_amdgcn_sched_barrier(0);
             if (key0 + 63 > lowest)
 #pragma unroll
@@ -566,14 +586,22 @@ __global__ __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) void mnb_attention_r
 #pragma unroll
             for (int d = 0; d < DT; ++d) {
                 const i32x4 zero = i32x4{0, 0, 0, 0};
-                const i32x4 sh = __builtin_amdgcn_mfma_i32_16x16x64_i8(v[d], b_hi, zero, 0, 0, 0);
-                const i32x4 sl = __builtin_amdgcn_mfma_i32_16x16x64_i8(v[d], b_lo, zero, 0, 0, 0);
+                const i32x4 sh = __builtin_amdgcn_mfma_i32_16x16x64_i8(v[d % VT], b_hi, zero, 0, 0, 0);
+                const i32x4 sl = __builtin_amdgcn_mfma_i32_16x16x64_i8(v[d % VT], b_lo, zero, 0, 0, 0);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) o[d][i] = fmaf((float)((sh[i] << 8) + sl[i]), f_o, o[d][i]);
+                if (VT < DT) {
+                    if (d + VT == DT && more) values_at(c + kWaves, next_v);
+                    if (d + VT < DT || more) load_values((d + VT) % DT);
+                }
                 if (d & 1) __builtin_amdgcn_sched_barrier(0);
             }
             if (more) {
-                load_values(c + kWaves, next_v);
+                if (VT == DT) {
+                    values_at(c + kWaves, next_v);
+#pragma unroll
+                    for (int d = 0; d < DT; ++d) load_values(d);
+                }
                 if (c + 2 * kWaves < c1) {
                     next_k = entry(c + 2 * kWaves, r >> 2);
                     next_v = entry(c + 2 * kWaves, g);
@@ -964,7 +992,7 @@ __global__ __launch_bounds__(64 * tile_waves(D), D == 64 ? 2 : 1) void mnb_atten
         const uint32_t sign = p.scale_log2 < 0.f ? 0x80008000u : 0u;
         q_scale = size;
         if constexpr (BF16) {
-            const int ex = max((int)(__float_as_uint(widen16(top, 1)) >> 23), 46) - 126;    // |x| < 2^ex, as above
+            const int ex = max((int)(__float_as_uint(widen16(top, 1)) >> 23), 26) - 126;    // |x| < 2^ex, as above
             const float up = pow2(15 - ex);
             q_scale = finite ? size * pow2(ex - 15) : size;
 #pragma unroll

@@ -235,11 +235,12 @@ int launch_attention(const AttentionArgs& args, void* stream, int* launches) MNB
 // workgroups take long to begin and end; the others read the keys once for every 16
 // rows.  (8 heads of 128, one sequence of 256 rows over 1024 / 8192 / 32768 keys: 16 /
 // 36 / 102 us against tiles' 29 / 38 / 70, of 128 rows 13 / 26 / 61 against 27 / 34 /
-// 65; 16 sequences of 96 rows 48 / 242 / 904 against 55 / 205 / 785.  Heads of 256, 96
-// rows over 8192 keys: 69 against 55.)
+// 65; 16 sequences of 96 rows 48 / 242 / 904 against 55 / 205 / 785.  Heads of 256, one
+// sequence over 1024 / 8192 keys: 96 rows 16 / 52 against 39 / 43, 256 rows 31 / 81
+// against 45 / 62.)
 constexpr int attention_many_rows(int64_t tokens, int64_t q_heads, int64_t head_dim)
 {
-    return head_dim <= 128 && tokens * q_heads <= 2048 ? 256 : 64;
+    return tokens * q_heads > 2048 ? 64 : head_dim <= 128 ? 256 : 128;
 }
 constexpr int kAttentionWorkgroups = 512;
 constexpr int tile_waves(int64_t head_dim) { return head_dim >= 128 ? 8 : 4; }
