@@ -164,15 +164,24 @@ __global__ __launch_bounds__(64 * kDownWaves) void mnb_lora_down_kernel(LoraPara
     }
 }
 
-// Sixteen or eight bytes at any even address.
-struct __attribute__((packed, aligned(2))) Loose16 {
-    u32x4 v;
-};
+// Eight bytes at any even address, and whole words.  Sixteen bytes that begin within a
+// word take far longer, so a lane of sixteen columns moves whole words and shifts them
+// (4091 rows, 512 -> 40 -> 4097 columns: 57 -> 43 us; 4098 columns, which need no
+// shift, 39 both ways).
 struct __attribute__((packed, aligned(2))) Loose8 {
     uint32_t v[2];
 };
+struct __attribute__((packed, aligned(4))) Words4 {
+    uint32_t v[4];
+};
+struct __attribute__((packed, aligned(4))) Words3 {
+    uint32_t v[3];
+};
 
-// C = 4 CT columns of a row's base; whole: none lies behind the last one.
+// The pairs of two words' four elements that begin at the first (shift 0) or second (16).
+__device__ __forceinline__ uint32_t shifted(uint32_t hi, uint32_t lo, uint32_t shift) { return __builtin_amdgcn_alignbit(hi, lo, shift); }
+
+// C = 4 CT columns of a row's base, none of them behind the last one.
 template <int CT>
 __device__ __forceinline__ void load_base(const uint16_t* src, uint32_t (&b)[2 * CT])
 {
@@ -181,36 +190,70 @@ __device__ __forceinline__ void load_base(const uint16_t* src, uint32_t (&b)[2 *
         b[0] = t.v[0];
         b[1] = t.v[1];
     } else {
+        // The words that hold these columns: one more where the first begins within one.
+        const bool odd = (uintptr_t)src & 2;
+        const Words4* from = reinterpret_cast<const Words4*>((uintptr_t)src & ~(uintptr_t)3);
+        uint32_t w[2 * CT + 1];
 #pragma unroll
         for (int i = 0; i < CT / 2; ++i) {
-            const u32x4 t = reinterpret_cast<const Loose16*>(src)[i].v;
+            const Words4 t = from[i];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) b[4 * i + e] = t[e];
+            for (int e = 0; e < 4; ++e) w[4 * i + e] = t.v[e];
         }
+        if (!__builtin_amdgcn_ballot_w64(odd)) {
+#pragma unroll
+            for (int i = 0; i < 2 * CT; ++i) b[i] = w[i];
+            return;
+        }
+        w[2 * CT] = reinterpret_cast<const uint32_t*>(from)[odd ? 2 * CT : 2 * CT - 1];
+#pragma unroll
+        for (int i = 0; i < 2 * CT; ++i) b[i] = shifted(w[i + 1], w[i], odd ? 16 : 0);
     }
 }
 
-// base + acc * unit.
+// base + acc * unit, of a row's 4 CT columns from col (the wave's lanes 16 apart hold
+// neighbours of one row; every lane comes here).
 template <int CT>
-__device__ __forceinline__ void finish(const LoraParams& p, int64_t row, int32_t col, bool whole, const uint32_t (&b)[2 * CT],
+__device__ __forceinline__ void finish(const LoraParams& p, int64_t row, int32_t col, const uint32_t (&b)[2 * CT],
                                        const float4_t (&acc)[CT], float unit)
 {
     constexpr int C = 4 * CT;
-    uint16_t* dst = p.out + row * p.out_stride + col;
-    if (whole) {
-        uint32_t w[C / 2];
+    const int g = (threadIdx.x & 63) >> 4;
+    uint32_t w[C / 2];
 #pragma unroll
-        for (int i = 0; i < C / 2; ++i) {
-            const float lo = fmaf(acc[i >> 1][2 * (i & 1)], unit, widen16(b[i] & 0xFFFFu, p.out_bf16));
-            const float hi = fmaf(acc[i >> 1][2 * (i & 1) + 1], unit, widen16(b[i] >> 16, p.out_bf16));
-            w[i] = (uint32_t)narrow16(lo, p.out_bf16) | (uint32_t)narrow16(hi, p.out_bf16) << 16;
-        }
+    for (int i = 0; i < C / 2; ++i) {
+        const float lo = fmaf(acc[i >> 1][2 * (i & 1)], unit, widen16(b[i] & 0xFFFFu, p.out_bf16));
+        const float hi = fmaf(acc[i >> 1][2 * (i & 1) + 1], unit, widen16(b[i] >> 16, p.out_bf16));
+        w[i] = (uint32_t)narrow16(lo, p.out_bf16) | (uint32_t)narrow16(hi, p.out_bf16) << 16;
+    }
+    uint16_t* dst = p.out + row * p.out_stride + col;
+    const bool odd = (uintptr_t)dst & 2;
+    uint32_t before = 0;
+    if (CT > 1 && __builtin_amdgcn_ballot_w64(odd)) before = __shfl_up(w[C / 2 - 1], 16);
+    if (row >= p.m || col >= p.N) return;
+    if (col + C <= p.N) {
         if constexpr (CT == 1) {
             *reinterpret_cast<Loose8*>(dst) = Loose8{{w[0], w[1]}};
-        } else {
+        } else if (!odd) {
 #pragma unroll
             for (int i = 0; i < CT / 2; ++i)
-                reinterpret_cast<Loose16*>(dst)[i].v = u32x4{w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]};
+                reinterpret_cast<Words4*>(dst)[i] = Words4{{w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]}};
+        } else {
+            // Whole words: the first begins with the left neighbour's last column, and this
+            // one's last column goes to the right neighbour, where there is one.
+            uint32_t v[C / 2];
+#pragma unroll
+            for (int i = 0; i < C / 2; ++i) v[i] = shifted(w[i], i ? w[i - 1] : before, 16);
+            if (g == 0) {
+                dst[0] = (uint16_t)w[0];
+                *reinterpret_cast<Words3*>(dst + 1) = Words3{{v[1], v[2], v[3]}};
+            } else {
+                *reinterpret_cast<Words4*>(dst - 1) = Words4{{v[0], v[1], v[2], v[3]}};
+            }
+#pragma unroll
+            for (int i = 1; i < CT / 2; ++i)
+                *reinterpret_cast<Words4*>(dst - 1 + 8 * i) = Words4{{v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]}};
+            if (g == 3 || col + 2 * C > p.N) dst[C - 1] = (uint16_t)(w[C / 2 - 1] >> 16);
         }
         return;
     }
@@ -394,8 +437,7 @@ __global__ __launch_bounds__(64 * W) void mnb_lora_up_kernel(LoraParams p)
     if (CT == 1) read_base();
 #pragma unroll
     for (int n = 0; n < NRT; ++n) {
-        const int64_t row = row0 + 16 * n + r;
-        if (row < p.m && mine0 < p.N) finish<CT>(p, row, mine0, whole, base[n], acc[n], t_unit[16 * n + r]);
+        finish<CT>(p, row0 + 16 * n + r, mine0, base[n], acc[n], t_unit[16 * n + r]);
     }
 }
 
