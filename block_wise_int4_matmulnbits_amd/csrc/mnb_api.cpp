@@ -651,7 +651,9 @@ AttentionLayout attention_layout(int64_t tokens, int64_t sequences, int64_t q_he
     // Full tiles, and one more for each sequence that can have many rows.
     l.many = attention_many_rows(tokens, q_heads, head_dim);
     l.tile_slots = rows > l.many ? (int)(rows / tile + std::min<int64_t>(sequences, rows / (l.many + 1))) : 0;
-    l.shares = l.tile_slots && (rows / tile + 1) * kv_heads < 512 ? tile_shares(head_dim) : 0;
+    // From five rounds of them on, whole tiles leave too little idle for shares to pay.
+    const int64_t shares = tile_shares(head_dim);
+    l.shares = l.tile_slots && (rows / tile + 1) * kv_heads < 5 * shares ? (int)shares : 0;
     const size_t each = 2 * (size_t)l.shares * (size_t)tile;
     l.tile_o = l.tile_ml + each * 2 * 4;
     l.bytes = l.tile_o + each * D * 4;

@@ -21,8 +21,16 @@
 //   The weights of a unit, largest 1 in each row, are held in 16 bits as two
 //   digits: off by 2^-16 of the largest at most, as the 32-bit sums of the
 //   products of two fp16 values would be off by 2^-12 of each.
+//
+// The batch's units are shared out evenly over a fixed number of workgroups, whose
+// sums of the (at most two) row tiles that others share too are joined by a second
+// launch.  64 sequences of one token over 4000 keys, 32 heads on 8, read 5.7 / 5.2 / 4.9
+// TB/s with heads of 64 / 128 / 256 (a large read by itself 4.0 from HBM); one token over
+// 2049 keys takes 11 us, two launches of dependent loads.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
+
+#include <algorithm>
 
 #include "mnb.h"
 #include "mnb_cache.h"
@@ -36,9 +44,11 @@ typedef int i32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kWaves = 4;
 constexpr int kWorkgroups = kAttentionWorkgroups, kMostParts = kAttentionWorkgroups;
-constexpr int kBegin = 4;
+constexpr int kBegin = 4;             // 48 sequences of differing lengths: 4 / 8 / 16 67 / 69 / 74 us
 constexpr int kGridTiles = 32768;     // tiles of a grid's y
-constexpr int kTileBegin = 4, kTileLeast = 2, kTileMore = 6, kTileJoin = 10;
+// Units that a tile's begin and end count as, that a share has at least, that the second
+// tile of a share and the joining launch cost more than whole tiles do.
+constexpr int kTileBegin = 4, kTileLeast = 2, kTileMore = 4, kTileJoin = 10;
 constexpr float kLowest = -3.0e38f;   // a running maximum before any key
 
 struct AttentionParams {
@@ -275,7 +285,9 @@ __device__ __forceinline__ Tile tile_of(const AttentionParams& p, const Sequence
 }
 
 // Few tiles of many rows are cut into equal shares of the whole batch's work, a
-// workgroup each.  Tile i of a sequence sees about start + (i + 1) BR / G keys, and
+// workgroup each, unless whole tiles take no longer (32 heads on 8 of 128: 512 tokens over
+// 17000 keys whole 685 us, cut 207; 5000 over 20000 2109, 1868; 300 over their own 22, 33;
+// 4096 over their own 190, 224).  Tile i of a sequence sees about start + (i + 1) BR / G keys, and
 // counts as that and as kTileBegin units (64 keys) more; counts are in 1 / G of a key,
 // so that those of the tiles before i have a closed form.
 struct Count {
@@ -319,9 +331,14 @@ __device__ __forceinline__ Place place_of(const AttentionParams& p, const Sequen
     const int64_t unit = (int64_t)p.G * 64, least = unit * kTileLeast;
     r.share = divide(r.all + p.shares - 1, p.shares);
     r.share = uniform64(r.share < least ? least : r.share);
-    r.cut = tiles * p.heads > 2 * p.shares ||
-            (tiles * p.heads > p.shares ? 3 : 2) * (int64_t)longest >
-                2 * (r.share + unit * kTileMore + divide(unit * kTileJoin * r.all, r.share * p.shares));
+    // Whole tiles: rounds of them where all are about as long; else the longest first, and
+    // short ones behind them.
+    tiles *= p.heads;
+    const int64_t rounds = divide(tiles + p.shares - 1, p.shares);
+    const int64_t whole = 2 * (int64_t)longest * tiles <= 3 * r.all
+                              ? rounds * longest
+                              : max((int64_t)longest, divide(r.all, p.shares) + (longest >> 3));
+    r.cut = whole > r.share + unit * kTileMore + divide(unit * kTileJoin * r.all, r.share * p.shares);
     const int64_t at = border * r.share;
     r.s = p.b.S;
     r.h = r.rt = 0;
@@ -879,6 +896,15 @@ __global__ __launch_bounds__(256) void mnb_attention_join_kernel(AttentionParams
 // sums' unit.  The unit changes, and the sums with it, only where r would leave
 // 2^-10 .. 2^8, so that no weight times scale falls out of fp16's range, whatever
 // the pages before it held, and pages of differing scales cost nothing.
+//
+// A unit of a tile of 256 rows and heads of 128 takes 2.6 us on its compute unit, of which
+// the products are 1.8 at the rate of a large fp16 library product: the exponentials and
+// the conversion of the integers hide in part only, as the waves of a workgroup meet at
+// a barrier every unit.  2.6 us is 840 TFLOP/s where all units have keys (one sequence of
+// 16384); a prompt's short tiles end sooner than they begin.  Eight waves of 32 rows,
+// because fewer rows convert the integers more often (four waves of 128 rows: the
+// same time); heads of 256 have two waves to 32 rows, as the outputs of one would not
+// fit its registers (458 -> 423 us for 512 tokens over 17000 keys).
 typedef _Float16 half8_t __attribute__((ext_vector_type(8)));
 typedef float float16_t __attribute__((ext_vector_type(16)));
 
@@ -922,26 +948,25 @@ __global__ __launch_bounds__(64 * tile_waves(D), D == 64 ? 2 : 1) void mnb_atten
     const int part_of_row = wave % SHARE, elem0 = 32 * DB * part_of_row;
     const int32_t cap = p.b.max_pages << p.b.page_bits, P = 1 << p.b.page_bits;
 
-    // Whole tiles, counted from the last one, whose rows see the most keys; or those of
+    // A whole tile, counted from the last one, whose rows see the most keys; or those of
     // a share, the first and the last perhaps in part.
     Place at;
     int64_t left = 0;                                      // of the share
-    int32_t number = p.shares ? (int32_t)blockIdx.x
-                              : ((int32_t)blockIdx.y + kGridTiles * (int32_t)blockIdx.z) * p.heads + (int32_t)blockIdx.x;
-    auto pick = [&](const Sequences& seqs) {
-        const int32_t y = uniform((int32_t)((uint32_t)number / (uint32_t)p.heads));
-        const Tile t = tile_of(p, seqs, y, BR);
-        at.s = t.s;
-        at.h = number - y * p.heads;
-        at.rt = t.rt;
-        at.q = t.q;
-    };
+    const int32_t y = (int32_t)blockIdx.y + kGridTiles * (int32_t)blockIdx.z, number = y * p.heads + (int32_t)blockIdx.x;
     {
         const Sequences seqs(p.b);
         at.cut = false;
-        if (p.shares) at = place_of(p, seqs, blockIdx.x, BR);
-        if (at.cut) left = at.all - blockIdx.x * at.share < at.share ? at.all - blockIdx.x * at.share : at.share;
-        else pick(seqs);
+        if (p.shares) at = place_of(p, seqs, number, BR);
+        if (at.cut) {
+            if (number >= p.shares) return;
+            left = at.all - number * at.share < at.share ? at.all - number * at.share : at.share;
+        } else {
+            const Tile t = tile_of(p, seqs, y, BR);
+            at.s = t.s;
+            at.h = blockIdx.x;
+            at.rt = t.rt;
+            at.q = t.q;
+        }
     }
     if (at.s >= p.b.S) return;
     for (;;) {
@@ -963,7 +988,7 @@ __global__ __launch_bounds__(64 * tile_waves(D), D == 64 ? 2 : 1) void mnb_atten
     if (at.cut) {
         const int64_t count = at.c.upto(at.rt + 1) - at.c.upto(at.rt), end = count - at.in < left ? count : at.in + left;
         whole = at.in == 0 && end == count;
-        slot = 2 * (int64_t)blockIdx.x + (at.in ? 0 : 1);
+        slot = 2 * (int64_t)number + (at.in ? 0 : 1);
         c0 = uniform((int32_t)divide(units * at.in, count));
         c1 = uniform((int32_t)divide(units * end, count));
         left -= end - at.in;
@@ -1265,14 +1290,7 @@ __global__ __launch_bounds__(64 * tile_waves(D), D == 64 ? 2 : 1) void mnb_atten
         }
     }
 
-    // On to the next tile.
-    if (!at.cut) {
-        number += p.shares;
-        if (p.shares == 0 || number >= p.tile_slots * p.heads) return;
-        pick(Sequences(p.b));
-        if (at.s >= p.b.S) return;
-        continue;
-    }
+    // On to the share's next tile.
     if (left <= 0) return;
     at.in = 0;
     if (++at.rt >= at.c.tiles) {
@@ -1292,9 +1310,9 @@ __global__ __launch_bounds__(64 * tile_waves(D), D == 64 ? 2 : 1) void mnb_atten
 template <int D, bool BF16>
 int queue(const AttentionParams& p, const AttentionLayout& lay, hipStream_t stream, int* launches)
 {
-    const dim3 tiles = p.shares ? dim3((unsigned)p.shares)
-                                : dim3((unsigned)p.heads, (unsigned)(p.tile_slots < kGridTiles ? p.tile_slots : kGridTiles),
-                                       (unsigned)((p.tile_slots + kGridTiles - 1) / kGridTiles));
+    // A workgroup for every tile, and for every share.
+    const int rows = std::max(p.tile_slots, (p.shares + p.heads - 1) / p.heads);
+    const dim3 tiles((unsigned)p.heads, (unsigned)std::min(rows, kGridTiles), (unsigned)((rows + kGridTiles - 1) / kGridTiles));
     if (p.tile_slots) {
         constexpr size_t lds = (size_t)4 * (64 * (D + 8) + D * 72);
         hipLaunchKernelGGL((mnb_attention_tile_kernel<D, BF16>), tiles, dim3(64 * tile_waves(D)), lds, stream, p);

@@ -242,15 +242,15 @@ constexpr int attention_many_rows(int64_t tokens, int64_t q_heads, int64_t head_
 {
     return tokens * q_heads > 2048 ? 64 : head_dim <= 128 ? 256 : 128;
 }
-constexpr int kAttentionWorkgroups = 512;
+constexpr int kAttentionWorkgroups = 512;     // (256 / 512 / 1024: 64 sequences over 1000 keys 30 / 28 / 38 us, one over 131072 49 / 52 / 58)
 constexpr int tile_waves(int64_t head_dim) { return head_dim >= 128 ? 8 : 4; }
 constexpr int tile_rows(int64_t head_dim) { return head_dim == 128 ? 256 : 128; }
 constexpr int tile_shares(int64_t head_dim) { return head_dim == 64 ? 512 : 256; }   // workgroups that run at a time
 
 // The attention's workspace.  Few rows: for each workgroup the sums of two row
 // tiles that it shares with others, behind their maxima and weights.  Many: the
-// tiles there can be; where they are few, the workgroups that share them (else 0)
-// and the same sums of two tiles for each.  Host-only arithmetic (mnb_api.cpp).
+// tiles there can be; where they are few, the workgroups that may share them (else
+// 0) and the same sums of two tiles for each.  Host-only arithmetic (mnb_api.cpp).
 struct AttentionLayout {
     int many, tile_slots, shares;
     size_t o, tile_ml, tile_o, bytes;

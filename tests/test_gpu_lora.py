@@ -232,3 +232,24 @@ def test_two_graphs_of_one_workspace():
         torch.cuda.synchronize()
         assert torch.equal(out.cpu(), want)
         _call(*sets[1 - i])
+
+
+def test_wide_within_a_buffer():
+    """The wide second launch on rows at odd columns of a wider buffer, in place and
+    not: the columns around them keep their bits."""
+    G.require_gpu()
+    m, K, N, rank = 300, 48, 27137, 16
+    for dtype, at, wide in ((F16, 3, 27150), (BF16, 8, 27145), (F16, 1, 27140)):
+        x, ids, A, B, scaling, base = _make(m, K, N, rank, 5, dtype, dtype, 9, 30)
+        want = _call(x, ids, A, B, scaling, base)
+        buf = torch.full((m, wide), 4.0, dtype=dtype, device="cuda")
+        buf[:, at:at + N] = base.cuda()
+        dev = [t.cuda() for t in (x, ids, A, B)]
+        other = torch.full((m, wide + 1), 4.0, dtype=dtype, device="cuda")
+        mnb.matmul_lora(*dev, buf[:, at:at + N], other[:, at:at + N], scaling=scaling.cuda())
+        mnb.matmul_lora(*dev, buf[:, at:at + N], buf[:, at:at + N], scaling=scaling.cuda())
+        torch.cuda.synchronize()
+        for t in (buf, other):
+            assert torch.equal(t[:, at:at + N].cpu(), want)
+            t[:, at:at + N] = 4.0
+            assert bool((t == 4.0).all())
