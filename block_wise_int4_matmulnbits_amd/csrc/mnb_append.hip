@@ -19,7 +19,7 @@
 // integers n 2^e, |n| <= 128, are fp32 values, so x >= n 2^e exactly when its
 // fp32 value rounded down is.
 //
-// HBM bounds long calls: 6000 tokens of 8 heads of 128 with their 32 query heads move
+// HBM bounds long calls: 7100 tokens of 8 heads of 128 with their 32 query heads move
 // 164 MB in 39 us (4.2 TB/s; a large copy 4.9).  The launch and one dependent chain of
 // loads (batch, page table, tokens, scale) bound short ones: one token 6.5 us.  A
 // workgroup takes the new tokens of one page and head, keys or values: the page's

@@ -11,7 +11,7 @@
 // once.  Both run on v_mfma_f32_16x16x32_{f16,bf16} straight from the loads.
 // HBM bounds both where there are many rows: x, base and out are read or written once
 // (4091 rows, 14336 -> 40 -> 4097: 179 MB in 87 us), and the used adapters once for each
-// tile of rows (64 rows of 32 adapters, 4096 -> 64 -> 28672: 125 MB in 39 to 45 us).  One
+// tile of rows (64 rows of 32 adapters, 4096 -> 64 -> 28672: 125 MB in 38 to 45 us).  One
 // row is bound by the two launches (9 us).
 #include <hip/hip_runtime.h>
 #include <stdint.h>

@@ -21,6 +21,9 @@
  * is narrowed to bf16 (RNE) in the same kernel -- the fp32 -> fp16 -> bf16
  * double rounding of the staged fp16-GEMV-then-cast route, reproduced bit
  * for bit, with no staging buffer and no second launch.
+ *
+ * Beside it: products with 8-bit weights, 4-bit expert layers, a paged cache of
+ * 8-bit keys and values with the attention over it, and low-rank adapters.
  */
 #ifndef MNB_H
 #define MNB_H
@@ -45,8 +48,10 @@ typedef enum {
     MNB_ERR_NULL = 1,     /* a required pointer is NULL                      */
     MNB_ERR_SHAPE = 2,    /* a size that is negative, too large or not a
                              multiple of what the call needs (matmul_nbits:
-                             K of 32; 8-bit calls: K of 16; expert layer: hidden
-                             and inter of 32), or experts or top_k out of range */
+                             K of 32; 8-bit calls and adapters: K of 16; expert
+                             layer: hidden and inter of 32; rank of 8), heads,
+                             pages or strides that do not fit each other, experts
+                             or top_k out of range, a scale that is not finite  */
     MNB_ERR_BLOCK = 3,    /* block != 32                                     */
     MNB_ERR_DTYPE = 4,    /* an element type the call does not take           */
     MNB_ERR_ALIGN = 5,    /* a buffer is not aligned as its call states
@@ -548,20 +553,27 @@ int append_kv_int8(const mnb_kv_cache* cache, const mnb_kv_batch* batch, int dty
  *
  * Rows that see no key (an empty sequence, or no usable page) are zero.
  * Numerics: scores of the integers exact but for what lies below 2^-22 of a
- * query's largest element, softmax with the running maximum and sum in fp32,
- * weights held in 16 bits against the largest of 64 keys, sums in fp32, one
- * rounding (RNE).  A query that is not finite, or a NaN scale of a page that a
- * row sees, gives NaN in that row.  The order of fp32 sums depends on the
- * lengths of the whole batch; equal calls give equal bits.  out and workspace
- * must not overlap the inputs or each other.  Asynchronous; allocates nothing;
- * two launches.
+ * query's largest element (or below 2^-123) and the steps of fp32 sums, softmax
+ * with the running maximum and sum in fp32.  Weights are held in 16 bits: off by
+ * 2^-16 of the largest weight times value scale of 64 keys, or, with many rows,
+ * by 2^-11 of themselves and 2^-24 of the row's largest.  Sums in fp32, one
+ * rounding (RNE); value scales that differ by more than 2^80 within a row's keys
+ * may lose the smaller ones.  Scales are powers of two as append_kv_int8 stores
+ * them, or any numbers that are not negative; q . k and the scores have to lie in
+ * fp32's range.  A query that is not finite, or a NaN scale of a page that a row
+ * sees, gives NaN in that row.  The order of fp32 sums depends on the lengths of
+ * the whole batch; equal calls give equal bits.  out and workspace must not
+ * overlap the inputs or each other.  Asynchronous; allocates nothing; two
+ * launches, three where a sequence may have many rows (tokens times query heads
+ * of a key head: more than 64, or than 128 or 256 in a small batch).
  */
 int attention_int8(const mnb_kv_cache* cache, const mnb_kv_batch* batch, int dtype, const void* q, int64_t q_stride,
                    int64_t q_heads, float scale, void* out, int64_t out_stride, int64_t max_tokens, void* workspace,
                    size_t workspace_bytes, void* stream);
 
 /* Workspace bytes attention_int8 needs (0 for none, or where it would reject
- * the sizes).  Host-only. */
+ * the sizes): 4 MB for heads of 64 to 17 MB for heads of 256, and up to 68 MB
+ * more where a sequence may have many rows.  Host-only. */
 size_t mnb_attention_workspace(int64_t tokens, int64_t sequences, int64_t q_heads, int64_t kv_heads, int64_t head_dim);
 
 /* Bounds of the adapters. */
@@ -597,10 +609,10 @@ size_t mnb_attention_workspace(int64_t tokens, int64_t sequences, int64_t q_head
  * Numerics: A x summed in fp32; scaled in fp32; held for the second product in
  * two pieces of x's type (16 bits of a bf16 value, 21 of an fp16 one, whose row
  * is under a power of two of its own); B's sums and the base in fp32, one
- * rounding (RNE).  A row that is not finite spoils itself alone.  A row's bits
- * depend on its own values and adapter and on (m, K, R).  out and workspace
- * must not overlap the inputs or each other, but for out == base.
- * Asynchronous; allocates nothing; two launches.
+ * rounding (RNE).  A row or an adapter that is not finite spoils its own rows
+ * alone.  A row's bits depend on its own values and adapter and on the sizes of
+ * the call.  out and workspace must not overlap the inputs or each other, but
+ * for out == base.  Asynchronous; allocates nothing; two launches.
  */
 int matmul_lora(const void* x, int x_dtype, int64_t x_stride, int64_t m, int64_t K, int64_t N, int64_t rank,
                 int64_t adapters, const int32_t* ids, const void* A, const void* B, const float* scaling,
@@ -615,8 +627,8 @@ size_t mnb_lora_workspace(int64_t m, int64_t K, int64_t N, int64_t rank, int64_t
  * Environment: MNB_LOG set to anything but "0" (read once per process)
  * prints one line per call to stderr, once its plan is fixed and before
  * its launches: the shape, the types, whether the plan was explicit or the
- * default, every plan field, and the number of launches (the 8-bit and expert
- * calls, once queued: the operator's name, shape, types and launches).
+ * default, every plan field, and the number of launches (the other calls, once
+ * queued or just before: the operator's name, shape, types and launches).
  */
 
 /*
