@@ -31,6 +31,7 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "mnb.h"
 #include "mnb_cache.h"
@@ -43,7 +44,7 @@ namespace {
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kWaves = 4;
-constexpr int kWorkgroups = kAttentionWorkgroups, kMostParts = kAttentionWorkgroups;
+constexpr int kWorkgroups = kAttentionWorkgroups;
 constexpr int kBegin = 4;             // 48 sequences of differing lengths: 4 / 8 / 16 67 / 69 / 74 us
 constexpr int kGridTiles = 32768;     // tiles of a grid's y
 // Units that a tile's begin and end count as, that a share has at least, that the second
@@ -65,8 +66,6 @@ struct AttentionParams {
     float* tile_ml;           // [2 shares][tile rows][2]
     int64_t q_stride, out_stride;
     int32_t heads, G;         // key heads, rows a token has for each
-    int32_t slots;            // row tiles of the joining launch's grid
-    int32_t tiles_each;       // of a sequence in it, or 0
     int32_t many;             // sequences of more rows than this go to the tiles
     int32_t tile_slots, shares;   // of the tiles' grid
     int32_t small;            // up to 64 sequences, whose work (but for the heads) fits 32 bits
@@ -89,18 +88,13 @@ __device__ __forceinline__ Work work_of(const AttentionParams& p, const Sequence
 // end; a workgroup's share of the whole batch is cut by that count, kBegin first.
 __device__ __forceinline__ int64_t count_of(const AttentionParams& p, const Work& w)
 {
-    return w.units ? (int64_t)w.tiles * (w.units + kBegin) * p.heads : 0;
+    return (int64_t)w.tiles * (w.units + kBegin) * p.heads;
 }
 // The same without the heads, of this lane's sequence (p.small).
 __device__ __forceinline__ int32_t small_count(const AttentionParams& p, const Sequences& all)
 {
     const Work w = work_of(p, all.mine);
-    return (int)(threadIdx.x & 63) < p.b.S && w.units ? w.tiles * (w.units + kBegin) : 0;
-}
-
-__device__ __forceinline__ int64_t units_of(const AttentionParams& p, int32_t s)
-{
-    return count_of(p, work_of(p, sequence(p.b, s)));
+    return (int)(threadIdx.x & 63) < p.b.S ? w.tiles * (w.units + kBegin) : 0;
 }
 
 // Sum over the lanes up to this one, in the manner of wave_prefix32; and over all.
@@ -140,17 +134,70 @@ __device__ __forceinline__ uint32_t wave_max(uint32_t v)
     return (uint32_t)__builtin_amdgcn_readlane((int32_t)v, 63);
 }
 
-// Units of every sequence, and of those before sequence s.
-__device__ __forceinline__ void count_units(const AttentionParams& p, int32_t s, int64_t* all, int64_t* before)
+// A count of every sequence, summed: lane l has an equal run of the sequences.  f(q,
+// valid) counts sequence q (0 where it is not valid).
+struct Counts {
+    int64_t mine, upto, all;
+    int32_t each;             // sequences of a lane
+};
+template <class F>
+__device__ __forceinline__ Counts count_sequences(const CacheBatch& b, const Sequences& seqs, F f)
 {
-    int64_t a = 0, b = 0;
-    for (int32_t i = threadIdx.x & 63; i < p.b.S; i += 64) {
-        const int64_t u = units_of(p, i);
-        a += u;
-        if (i < s) b += u;
+    const int32_t lane = threadIdx.x & 63;
+    Counts c;
+    c.each = (b.S + 63) >> 6;
+    if (b.S <= 64) {
+        c.mine = f(seqs.mine, lane < b.S);
+    } else {
+        c.mine = 0;
+#pragma unroll 4
+        for (int32_t i = 0; i < c.each; ++i) {
+            const int32_t s = lane * c.each + i;
+            c.mine += f(sequence(b, s < b.S ? s : b.S - 1), s < b.S);
+        }
     }
-    *all = wave_sum(a);
-    *before = wave_sum(b);
+    c.upto = wave_prefix(c.mine);
+    c.all = read_lane(c.upto, 63);
+    return c;
+}
+
+// The sequence that holds count `at`, and the count of those before it (s: b.S for none).
+struct Holder {
+    int64_t before;
+    int32_t s;
+    Sequence q;
+};
+template <class F>
+__device__ __forceinline__ Holder find_holder(const CacheBatch& b, const Sequences& seqs, const Counts& c, int64_t at, F f)
+{
+    const int32_t lane = threadIdx.x & 63;
+    Holder r{0, b.S, Sequence{0, 0, 0}};
+    const uint64_t past = __builtin_amdgcn_ballot_w64(c.upto > at);
+    if (!past) return r;
+    const int32_t l = __builtin_ctzll(past);
+    r.before = read_lane(c.upto - c.mine, l);
+    if (b.S <= 64) {
+        r.s = l;
+        r.q = seqs.at(l);
+        return r;
+    }
+    for (int32_t j = 0; j < c.each; j += 64) {
+        const int32_t s = l * c.each + j + lane;
+        const bool valid = j + lane < c.each && s < b.S;
+        const Sequence q = sequence(b, valid ? s : b.S - 1);
+        const int64_t mine = f(q, valid), upto = r.before + wave_prefix(mine);
+        const uint64_t here = __builtin_amdgcn_ballot_w64(upto > at);
+        if (here) {
+            const int k = __builtin_ctzll(here);
+            r.s = l * c.each + j + k;
+            r.before = read_lane(upto - mine, k);
+            r.q = Sequence{__builtin_amdgcn_readlane(q.t0, k), __builtin_amdgcn_readlane(q.n, k),
+                           __builtin_amdgcn_readlane(q.length, k)};
+            return r;
+        }
+        r.before = read_lane(upto, 63);
+    }
+    return r;
 }
 
 // Units of a workgroup: an even share, but no fewer than one for each wave.
@@ -165,50 +212,36 @@ __device__ __forceinline__ int64_t divide(int64_t a, int64_t b)
     return ((uint64_t)(a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
 }
 
-// The first unit of this workgroup, the units before its sequence, and the
+// Where share `number` begins: its first unit, the units before its sequence, and the
 // sequence (b.S: no work).
 struct Start {
     int64_t share, all, unit, before;
     int32_t s;
 };
-__device__ __forceinline__ Start start_of(const AttentionParams& p, const Sequences& seqs)
+__device__ __forceinline__ Start start_of(const AttentionParams& p, const Sequences& seqs, int64_t number)
 {
-    const int lane = threadIdx.x & 63;
     Start r;
+    r.before = 0;
+    r.s = p.b.S;
     if (p.small) {
         const int32_t mine = small_count(p, seqs), upto = wave_prefix32(mine);
         r.all = (int64_t)__builtin_amdgcn_readlane(upto, 63) * p.heads;
         r.share = share_of(r.all);
-        r.unit = (int64_t)blockIdx.x * r.share;
-        r.before = 0;
-        r.s = p.b.S;
+        r.unit = number * r.share;
         if (r.unit >= r.all) return r;
         r.s = __builtin_ctzll(__builtin_amdgcn_ballot_w64((int64_t)upto * p.heads > r.unit));
         r.before = (int64_t)__builtin_amdgcn_readlane(upto - mine, r.s) * p.heads;
         return r;
     }
-    int64_t mine = lane < p.b.S ? units_of(p, lane) : 0, upto = wave_prefix(mine), base = 0;
-    r.all = read_lane(upto, 63);
-    for (int32_t s0 = 64; s0 < p.b.S; s0 += 64) r.all += wave_sum(s0 + lane < p.b.S ? units_of(p, s0 + lane) : 0);
+    auto count = [&](const Sequence& q, bool valid) { return valid ? count_of(p, work_of(p, q)) : 0; };
+    const Counts c = count_sequences(p.b, seqs, count);
+    r.all = c.all;
     r.share = share_of(r.all);
-    r.unit = (int64_t)blockIdx.x * r.share;
-    r.before = 0;
-    r.s = p.b.S;
+    r.unit = number * r.share;
     if (r.unit >= r.all) return r;
-    for (int32_t s0 = 0; s0 < p.b.S; s0 += 64) {
-        if (s0) {
-            mine = s0 + lane < p.b.S ? units_of(p, s0 + lane) : 0;
-            upto = wave_prefix(mine);
-        }
-        const uint64_t past = __builtin_amdgcn_ballot_w64(base + upto > r.unit);
-        if (past) {
-            const int l = __builtin_ctzll(past);
-            r.before = base + read_lane(upto - mine, l);
-            r.s = uniform(s0 + l);
-            return r;
-        }
-        base += read_lane(upto, 63);
-    }
+    const Holder at = find_holder(p.b, seqs, c, r.unit, count);
+    r.before = at.before;
+    r.s = at.s;
     return r;
 }
 
@@ -259,28 +292,15 @@ __device__ __forceinline__ int32_t tiles_of(const AttentionParams& p, const Sequ
 }
 __device__ __forceinline__ Tile tile_of(const AttentionParams& p, const Sequences& seqs, int32_t y, int BR)
 {
-    const int lane = threadIdx.x & 63;
-    int32_t all = 0, base = 0;            // (at most 2^26 rows, and a tile more for each sequence)
-    for (int32_t s0 = 0; s0 < p.b.S; s0 += 64) {
-        const Sequence q = p.b.S <= 64 ? seqs.mine : sequence(p.b, s0 + lane < p.b.S ? s0 + lane : 0);
-        all += __builtin_amdgcn_readlane(wave_prefix32(s0 + lane < p.b.S ? tiles_of(p, q, BR) : 0), 63);
-    }
-    const int32_t v = all - 1 - y;
+    auto count = [&](const Sequence& q, bool valid) { return valid ? (int64_t)tiles_of(p, q, BR) : 0; };
+    const Counts c = count_sequences(p.b, seqs, count);
+    const int64_t v = c.all - 1 - y;
     Tile t{p.b.S, 0, Sequence{0, 0, 0}};
     if (v < 0 || y >= p.tile_slots) return t;
-    for (int32_t s0 = 0; s0 < p.b.S; s0 += 64) {
-        const Sequence q = p.b.S <= 64 ? seqs.mine : sequence(p.b, s0 + lane < p.b.S ? s0 + lane : 0);
-        const int32_t mine = s0 + lane < p.b.S ? tiles_of(p, q, BR) : 0, upto = base + wave_prefix32(mine);
-        const uint64_t past = __builtin_amdgcn_ballot_w64(upto > v);
-        if (past) {
-            const int l = __builtin_ctzll(past);
-            t.s = s0 + l;
-            t.rt = v - __builtin_amdgcn_readlane(upto - mine, l);
-            t.q = seqs.at(t.s);
-            return t;
-        }
-        base = __builtin_amdgcn_readlane(upto, 63);
-    }
+    const Holder at = find_holder(p.b, seqs, c, v, count);
+    t.s = at.s;
+    t.rt = (int32_t)(v - at.before);
+    t.q = at.q;
     return t;
 }
 
@@ -314,20 +334,19 @@ struct Place {
 };
 __device__ __forceinline__ Place place_of(const AttentionParams& p, const Sequences& seqs, int64_t border, int BR)
 {
-    const int lane = threadIdx.x & 63;
-    auto get = [&](int32_t s0) { return p.b.S <= 64 ? seqs.mine : sequence(p.b, s0 + lane < p.b.S ? s0 + lane : 0); };
-    auto count = [&](int32_t s0, const Count& c) { return s0 + lane < p.b.S ? c.all() * p.heads : 0; };
     Place r;
-    r.all = 0;
     int64_t tiles = 0;
     uint32_t longest = 0;                 // count of a tile: 64 heads of 2^24 keys at most, and its own rows
-    for (int32_t s0 = 0; s0 < p.b.S; s0 += 64) {
-        const Count c = count_tiles(p, get(s0), BR);
-        r.all += wave_sum(count(s0, c));
-        const bool any = s0 + lane < p.b.S && c.tiles > 0;
-        tiles += __builtin_amdgcn_readlane(wave_prefix32(any ? (int32_t)c.tiles : 0), 63);
-        longest = max(longest, wave_max(any ? (uint32_t)(c.first + c.tiles * BR) : 0u));
-    }
+    const Counts counts = count_sequences(p.b, seqs, [&](const Sequence& q, bool valid) {
+        const Count c = count_tiles(p, q, BR);
+        if (!valid || c.tiles == 0) return (int64_t)0;
+        tiles += c.tiles;
+        longest = max(longest, (uint32_t)(c.first + c.tiles * BR));
+        return c.all() * p.heads;
+    });
+    tiles = wave_sum(tiles);
+    longest = wave_max(longest);
+    r.all = counts.all;
     const int64_t unit = (int64_t)p.G * 64, least = unit * kTileLeast;
     r.share = divide(r.all + p.shares - 1, p.shares);
     r.share = uniform64(r.share < least ? least : r.share);
@@ -344,20 +363,13 @@ __device__ __forceinline__ Place place_of(const AttentionParams& p, const Sequen
     r.h = r.rt = 0;
     r.in = 0;
     if (!r.cut || at >= r.all) return r;
-    int64_t base = 0;
-    for (int32_t s0 = 0; s0 < p.b.S; s0 += 64) {
-        const int64_t mine = count(s0, count_tiles(p, get(s0), BR)), upto = base + wave_prefix(mine);
-        const uint64_t past = __builtin_amdgcn_ballot_w64(upto > at);
-        if (past) {
-            const int l = __builtin_ctzll(past);
-            r.s = s0 + l;
-            r.q = seqs.at(r.s);
-            r.c = count_tiles(p, r.q, BR);
-            r.in = at - read_lane(upto - mine, l);
-            break;
-        }
-        base = read_lane(upto, 63);
-    }
+    const Holder holder = find_holder(p.b, seqs, counts, at, [&](const Sequence& q, bool valid) {
+        return valid ? count_tiles(p, q, BR).all() * p.heads : 0;
+    });
+    r.s = holder.s;
+    r.q = holder.q;
+    r.c = count_tiles(p, r.q, BR);
+    r.in = at - holder.before;
     if (r.s >= p.b.S || r.in < 0) {       // (numbers of the batch that overflow)
         r.s = p.b.S;
         return r;
@@ -382,7 +394,7 @@ __global__ __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) void mnb_attention_r
     const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const Sequences seqs(p.b);
-    const Start start = start_of(p, seqs);
+    const Start start = start_of(p, seqs, blockIdx.x);
     int64_t u = start.unit, before = start.before;
     const int64_t end = u + start.share < start.all ? u + start.share : start.all;
     int32_t s = start.s;
@@ -403,8 +415,8 @@ __global__ __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) void mnb_attention_r
         const int from = (int)(in - pair64 * (w.units + kBegin)) - kBegin, to = end - u < w.units - from ? from + (int)(end - u) : w.units;
         const int32_t h = (int32_t)(pair / (uint32_t)w.tiles), rt = (int32_t)(pair - h * w.tiles);
         u += to - from;
-        const int c0 = from < 0 ? 0 : from, c1 = to;
-        if (c1 <= c0) continue;
+        const int c0 = from < 0 ? 0 : from, c1 = to < 0 ? 0 : to;
+        if (c1 <= c0 && (w.units || from != -kBegin)) continue;      // (no keys at all: zeros)
         const bool first_part = c0 > 0, whole = c0 == 0 && c1 == w.units;
 
         // This lane's row.  Rows past the last one repeat it and are not stored.
@@ -685,38 +697,21 @@ __global__ __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) void mnb_attention_r
     }
 }
 
-// Tiles that several workgroups shared: their sums, in the order of the keys.  A
-// workgroup for every kJoinEach-th of the rows that a border between shares has to
-// itself: the borders within a tile divide its rows, D / 4 threads a row, those that
-// few rows leave over every so many of the parts.
-constexpr int kJoinThreads = 256, kJoinEach = 4;
+// Tiles of rows whose keys several workgroups shared: their sums, in the order of the
+// keys.  The borders between shares that lie within a tile divide its rows among them,
+// D / 4 threads a row; threads that few rows leave take every so many of the parts.
+constexpr int kJoinThreads = 256, kJoinEach = 4;     // kJoinEach: workgroups of a border within a tile of many rows
 template <int D>
-struct TileJoin {
-    Place place;
+struct Meet {
     float4_t y[kJoinThreads];
     float m[kJoinThreads * 4 / D], l[kJoinThreads * 4 / D];
 };
-template <int D, bool BF16>
-__device__ __forceinline__ void join_tiles(const AttentionParams& p, int32_t id, TileJoin<D>& meet)
+template <int D, bool BF16, int BR>
+__device__ __forceinline__ void join_parts(const AttentionParams& p, const float* ml, const float* o, int64_t w0, int parts,
+                                           int worker, int workers, const Sequence& q, int32_t h, int32_t row0, Meet<D>& meet)
 {
-    constexpr int BR = tile_rows(D), LANES = D / 4, GROUPS = kJoinThreads / LANES;
-    const int64_t border = id / kJoinEach + 1;
-    if (border >= p.shares) return;
-    if (threadIdx.x < 64) {
-        const Place found = place_of(p, Sequences(p.b), border, BR);
-        if (threadIdx.x == 0) meet.place = found;
-    }
-    __syncthreads();
-    const Place at = meet.place;
-    if (at.s >= p.b.S || at.in == 0) return;
-    // The shares w0 .. w1 of the tile.
-    const int64_t begin = border * at.share - at.in, w0 = divide(begin, at.share);
-    const int64_t w1 = divide(begin + at.c.upto(at.rt + 1) - at.c.upto(at.rt) - 1, at.share);
-    const int parts = (int)(w1 - w0) + 1;
-    if (w0 + parts > p.shares || parts < 2) return;      // (numbers of the batch that overflow)
-    const Sequence q = at.q;
-    const int rows = min(BR, q.n * p.G - at.rt * BR), workers = (parts - 1) * kJoinEach;
-    const int worker = (int)(border - w0 - 1) * kJoinEach + id % kJoinEach;
+    constexpr int LANES = D / 4, GROUPS = kJoinThreads / LANES;
+    const int rows = min(BR, q.n * p.G - row0);
     const int first = rows * worker / workers, count = rows * (worker + 1) / workers - first;
     int ways = GROUPS;
     while (ways > 1 && count > GROUPS / ways) ways >>= 1;
@@ -727,17 +722,32 @@ __device__ __forceinline__ void join_tiles(const AttentionParams& p, int32_t id,
         const int in = first + (mine ? i : 0);
         float m = kLowest, l = 0.f;
         float4_t y = float4_t{0.f, 0.f, 0.f, 0.f};
-#pragma unroll 8
-        for (int n = way; n < parts; n += ways) {
-            const int64_t part = (2 * (w0 + n) + (n == 0 ? 1 : 0)) * BR + in;
-            const float its = p.tile_ml[part * 2], own = p.tile_ml[part * 2 + 1];
-            const float4_t sums = *reinterpret_cast<const float4_t*>(p.tile_o + part * D + 4 * lane);
-            const float now = fmaxf(m, its), keep = exp2_fast(m - now), f = exp2_fast(its - now);
-            m = now;
-            l = l * keep + own * f;
+        // K parts, all on their way before the first is added.
+        auto add = [&](auto batch, int n0) {
+            constexpr int K = decltype(batch)::value;
+            float its[K], own[K];
+            float4_t sums[K];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) y[e] = y[e] * keep + (own == 0.f ? 0.f : sums[e] * f);   // 0: no sums stored
-        }
+            for (int k = 0; k < K; ++k) {
+                const int n = n0 + k * ways < parts ? n0 + k * ways : parts - 1;
+                const int64_t part = (2 * (w0 + n) + (n == 0 ? 1 : 0)) * BR + in;
+                its[k] = ml[part * 2];
+                own[k] = ml[part * 2 + 1];
+                sums[k] = *reinterpret_cast<const float4_t*>(o + part * D + 4 * lane);
+            }
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                if (n0 + k * ways >= parts) own[k] = 0.f;
+                const float now = own[k] == 0.f ? m : fmaxf(m, its[k]), keep = exp2_fast(m - now), f = exp2_fast(its[k] - now);
+                m = now;
+                l = l * keep + (own[k] == 0.f ? 0.f : own[k] * f);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) y[e] = y[e] * keep + (own[k] == 0.f ? 0.f : sums[k][e] * f);   // 0: no sums stored
+            }
+        };
+        int n0 = 0;
+        for (; parts - n0 > 2 * ways; n0 += 8 * ways) add(std::integral_constant<int, 8>(), n0 + way);
+        if (n0 < parts) add(std::integral_constant<int, 2>(), n0 + way);
         if (ways > 1) {
             if (lane == 0) {
                 meet.m[group] = m;
@@ -760,7 +770,7 @@ __device__ __forceinline__ void join_tiles(const AttentionParams& p, int32_t id,
             __syncthreads();
         }
         if (way == 0 && mine) {
-            const Row to = row_of(p, at.rt * BR + in, at.h);
+            const Row to = row_of(p, row0 + in, h);
             const float by = l == 0.f ? 0.f : 1.f / l;
             uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + (q.t0 + to.token) * p.out_stride + (int64_t)to.head * D + 4 * lane);
             dst[0] = (uint32_t)narrow16(y[0] * by, BF16) | (uint32_t)narrow16(y[1] * by, BF16) << 16;
@@ -769,109 +779,59 @@ __device__ __forceinline__ void join_tiles(const AttentionParams& p, int32_t id,
     }
 }
 
-// Row tiles whose keys several workgroups shared: their sums, in the order of
-// the keys.  Sequences without keys get rows of zeros.  Grid: (row tiles, heads,
-// D / 64); a workgroup takes 64 elements of each of 16 rows.  Behind the row tiles, the
-// borders between the shares of tiles.
+// Grid: the borders between the shares of few rows, then those of tiles.
 template <int D, bool BF16>
-__global__ __launch_bounds__(256) void mnb_attention_join_kernel(AttentionParams p)
+__global__ __launch_bounds__(kJoinThreads) void mnb_attention_join_kernel(AttentionParams p)
 {
-    struct RowJoin {
-        float factor[16][kMostParts + 1];
-        float inverse[16];
-        float4_t meet[256];
-    };
-    __shared__ union {
-        TileJoin<D> tiles;
-        RowJoin rows;
-    } lds;
-    if ((int32_t)blockIdx.x >= p.slots) {
-        const int32_t id = (((int32_t)blockIdx.x - p.slots) * (int32_t)gridDim.y + (int32_t)blockIdx.y) * (int32_t)gridDim.z + (int32_t)blockIdx.z;
-        join_tiles<D, BF16>(p, id, lds.tiles);
+    constexpr int BR = tile_rows(D);
+    __shared__ Meet<D> meet;
+    if ((int32_t)blockIdx.x < kWorkgroups - 1) {
+        __shared__ Start start;
+        __shared__ Sequence sequence_of_start;
+        const int64_t border = (int64_t)blockIdx.x + 1;
+        if (threadIdx.x < 64) {
+            const Sequences seqs(p.b);
+            const Start found = start_of(p, seqs, border);
+            const Sequence its = found.s < p.b.S ? seqs.at(found.s) : Sequence{0, 0, 0};
+            if (threadIdx.x == 0) {
+                start = found;
+                sequence_of_start = its;
+            }
+        }
+        __syncthreads();
+        const Start at = start;
+        if (at.s >= p.b.S) return;
+        const Sequence q = sequence_of_start;
+        const Work w = work_of(p, q);
+        const int64_t in = at.unit - at.before, per = w.units + kBegin, pair = divide(in, per);
+        const int32_t h = (int32_t)((uint32_t)pair / (uint32_t)w.tiles), rt = (int32_t)(pair - (int64_t)h * w.tiles);
+        // The shares w0 .. w1 of the row tile's keys.
+        const int64_t u0 = at.unit - (in - pair * per) + kBegin, w0 = divide(u0, at.share);
+        const int64_t w1 = divide(u0 + w.units - 1, at.share);
+        if (border <= w0 || border > w1) return;
+        if (in < 0 || w0 < 0 || h >= p.heads || w1 >= kWorkgroups) return;      // (numbers of the batch that overflow)
+        join_parts<D, BF16, 16>(p, p.part_ml, p.part_o, w0, (int)(w1 - w0) + 1, (int)(border - w0) - 1, (int)(w1 - w0), q, h,
+                                rt * 16, meet);
         return;
     }
-    auto& factor = lds.rows.factor;
-    auto& inverse = lds.rows.inverse;
-    auto& meet = lds.rows.meet;
-    const int64_t slot = blockIdx.x;
-    const int32_t h = blockIdx.y;
-    // A sequence's first slot: the most tiles that the ones before it can have, or
-    // floor(t0 G / 16) + s, which leaves room for what they have.
-    auto base = [&](int32_t i) {
-        return p.tiles_each ? (int64_t)i * p.tiles_each : (int64_t)clamp32(p.b.starts[i], 0, p.b.T) * p.G / 16 + i;
-    };
-    int32_t s;
-    Sequence q;
-    int64_t all, before, rt;
-    Work w;
-    if (p.small) {
-        const Sequences seqs(p.b);
-        const int lane = threadIdx.x & 63;
-        auto first = [&](int32_t t0) { return p.tiles_each ? lane * p.tiles_each : (int32_t)((int64_t)t0 * p.G / 16) + lane; };
-        const int32_t mine = small_count(p, seqs), upto = wave_prefix32(mine), at = first(seqs.mine.t0);
-        const uint64_t m = __builtin_amdgcn_ballot_w64(lane < p.b.S && at <= (int32_t)slot);
-        s = m ? 63 - __builtin_clzll(m) : 0;
-        q = seqs.at(s);
-        w = work_of(p, q);
-        rt = slot - __builtin_amdgcn_readlane(at, s);
-        if (rt < 0 || rt >= w.tiles) return;
-        all = (int64_t)__builtin_amdgcn_readlane(upto, 63) * p.heads;
-        before = (int64_t)__builtin_amdgcn_readlane(upto - mine, s) * p.heads;
-    } else {
-        s = wave_search(p.b.S, slot, base);
-        q = sequence(p.b, s);
-        w = work_of(p, q);
-        rt = slot - base(s);
-        if (rt < 0 || rt >= w.tiles) return;
-        count_units(p, s, &all, &before);
-    }
-    const int64_t share = share_of(all);
-    const int64_t u0 = before + ((int64_t)h * w.tiles + rt) * (w.units + kBegin) + kBegin, u1 = u0 + w.units;
-    const int64_t w0 = divide(u0, share);
-    const int parts = w.units ? (int)(divide(u1 - 1, share) - w0) + 1 : 0;
-    if (parts == 1) return;              // stored by that workgroup
-    // (Only numbers of the batch that overflow the counts lead beyond the last one.)
-    if (u0 < 0 || parts < 0 || w0 + parts > kWorkgroups) return;
-    const int rows = q.n * p.G - (int)rt * 16, count = rows < 16 ? rows : 16;
-    auto part_of = [&](int i) { return (2 * (w0 + i) + (i == 0 ? 1 : 0)) * 16; };
-    {
-        const int row = threadIdx.x >> 4, j = threadIdx.x & 15;
-        float m = kLowest, l = 0.f;
-        if (row < count)
-            for (int i = j; i < parts; i += 16) m = fmaxf(m, p.part_ml[(part_of(i) + row) * 2]);
-#pragma unroll
-        for (int d = 8; d; d >>= 1) m = fmaxf(m, __shfl_xor(m, d));
-        if (row < count)
-            for (int i = j; i < parts; i += 16) {
-                const float f = exp2_fast(p.part_ml[(part_of(i) + row) * 2] - m);
-                factor[row][i] = f;
-                l += p.part_ml[(part_of(i) + row) * 2 + 1] * f;
-            }
-#pragma unroll
-        for (int d = 8; d; d >>= 1) l += __shfl_xor(l, d);
-        if (j == 0) inverse[row] = l == 0.f ? 0.f : 1.f / l;
+    __shared__ Place place;
+    const int32_t id = (int32_t)blockIdx.x - (kWorkgroups - 1);
+    const int64_t border = id / kJoinEach + 1;
+    if (border >= p.shares) return;
+    if (threadIdx.x < 64) {
+        const Place found = place_of(p, Sequences(p.b), border, BR);
+        if (threadIdx.x == 0) place = found;
     }
     __syncthreads();
-    // Four elements of a row a thread; with few rows, groups of threads take every
-    // so many of the parts.
-    const int ways = count > 8 ? 1 : count > 4 ? 2 : count > 2 ? 4 : count > 1 ? 8 : 16, width = 256 / ways;
-    const int way = threadIdx.x / width, row = (threadIdx.x % width) >> 4, e = (threadIdx.x & 15) * 4 + 64 * (int)blockIdx.z;
-    float4_t y = float4_t{0.f, 0.f, 0.f, 0.f};
-    if (row < count) {
-#pragma unroll 4
-        for (int i = way; i < parts; i += ways)
-            y += *reinterpret_cast<const float4_t*>(p.part_o + (part_of(i) + row) * D + e) * factor[row][i];
-    }
-    meet[threadIdx.x] = y;
-    __syncthreads();
-    if (way == 0 && row < count) {
-        for (int i = 1; i < ways; ++i) y += meet[threadIdx.x + i * width];
-        y *= inverse[row];
-        const Row to = row_of(p, (uint32_t)rt * 16 + row, h);
-        uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + (q.t0 + to.token) * p.out_stride + (int64_t)to.head * D + e);
-        dst[0] = (uint32_t)narrow16(y[0], BF16) | (uint32_t)narrow16(y[1], BF16) << 16;
-        dst[1] = (uint32_t)narrow16(y[2], BF16) | (uint32_t)narrow16(y[3], BF16) << 16;
-    }
+    const Place at = place;
+    if (at.s >= p.b.S || at.in == 0) return;
+    // The shares w0 .. w1 of the tile.
+    const int64_t begin = border * at.share - at.in, w0 = divide(begin, at.share);
+    const int64_t w1 = divide(begin + at.c.upto(at.rt + 1) - at.c.upto(at.rt) - 1, at.share);
+    const int parts = (int)(w1 - w0) + 1;
+    if (w0 < 0 || w0 + parts > p.shares || parts < 2) return;      // (numbers of the batch that overflow)
+    join_parts<D, BF16, BR>(p, p.tile_ml, p.tile_o, w0, parts, (int)(border - w0 - 1) * kJoinEach + id % kJoinEach,
+                            (parts - 1) * kJoinEach, at.q, at.h, at.rt * BR, meet);
 }
 
 // ---------------------------------------------------------------- many rows
@@ -1324,9 +1284,8 @@ int queue(const AttentionParams& p, const AttentionLayout& lay, hipStream_t stre
     int e = (int)hipGetLastError();
     if (e != 0) return e;
     ++*launches;
-    const int each = p.heads * (D / 64), borders = p.shares ? (p.shares - 1) * kJoinEach : 0;
     hipLaunchKernelGGL((mnb_attention_join_kernel<D, BF16>),
-                       dim3((unsigned)(p.slots + (borders + each - 1) / each), (unsigned)p.heads, D / 64), dim3(256), 0,
+                       dim3((unsigned)(kWorkgroups - 1 + (p.shares ? (p.shares - 1) * kJoinEach : 0))), dim3(kJoinThreads), 0,
                        stream, p);
     e = (int)hipGetLastError();
     if (e == 0) ++*launches;
@@ -1364,10 +1323,6 @@ int launch_attention(const AttentionArgs& a, void* stream, int* launches)
     const bool few = a.max_tokens > 0 && a.max_tokens * p.G <= p.many;
     p.tile_slots = few ? 0 : lay.tile_slots;
     if (few) p.many = INT32_MAX;
-    // (max_tokens is not trusted with the place of a row tile.)
-    const int64_t loose = a.batch.tokens * p.G / 16 + a.batch.sequences, each = (lay.many + 15) / 16;
-    p.tiles_each = !few && each * a.batch.sequences <= loose ? (int32_t)each : 0;
-    p.slots = (int32_t)(p.tiles_each ? each * a.batch.sequences : loose);
     p.shares = few ? 0 : lay.shares;
     // Tiles of few rows: at most tokens G / 16 and one for each sequence, of 2^18 units.
     p.small = a.batch.sequences <= 64 && a.batch.tokens * p.G / 16 + a.batch.sequences < (1 << 12);
