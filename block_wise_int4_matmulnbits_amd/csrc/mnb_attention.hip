@@ -24,9 +24,10 @@
 //
 // The batch's units are shared out evenly over a fixed number of workgroups, whose
 // sums of the (at most two) row tiles that others share too are joined by a second
-// launch.  64 sequences of one token over 4000 keys, 32 heads on 8, read 5.7 / 5.2 / 4.9
-// TB/s with heads of 64 / 128 / 256 (a large read by itself 4.0 from HBM); one token over
-// 2049 keys takes 11 us, two launches of dependent loads.
+// launch, a workgroup for each border between two shares.  64 sequences of one token
+// over 4000 keys, 32 heads on 8, read 5.7 / 5.2 / 4.9 TB/s with heads of 64 / 128 / 256
+// (a plain read of as much 7.0); one token over 2049 keys takes 11 us, two launches of
+// dependent loads.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -45,7 +46,8 @@ typedef int i32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kWaves = 4;
 constexpr int kWorkgroups = kAttentionWorkgroups;
-constexpr int kBegin = 4;             // 48 sequences of differing lengths: 4 / 8 / 16 67 / 69 / 74 us
+constexpr int kBegin = 4;             // (2 / 4 / 8: one token over 2049 keys 12.8 / 10.4 / 10.4 us, 64 sequences of
+                                      // differing lengths, 4 / 8 / 16: 67 / 69 / 74)
 constexpr int kGridTiles = 32768;     // tiles of a grid's y
 // Units that a tile's begin and end count as, that a share has at least, that the second
 // tile of a share and the joining launch cost more than whole tiles do.

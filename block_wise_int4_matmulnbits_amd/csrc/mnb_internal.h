@@ -242,7 +242,7 @@ constexpr int attention_many_rows(int64_t tokens, int64_t q_heads, int64_t head_
 {
     return tokens * q_heads > 2048 ? 64 : head_dim <= 128 ? 256 : 128;
 }
-constexpr int kAttentionWorkgroups = 512;     // (256 / 512 / 1024: 64 sequences over 1000 keys 30 / 28 / 38 us, one over 131072 49 / 52 / 58)
+constexpr int kAttentionWorkgroups = 512;     // (256 / 512 / 1024: 64 sequences over 1000 keys 29 / 27 / 34 us, one over 131072 48 / 49 / 54)
 constexpr int tile_waves(int64_t head_dim) { return head_dim >= 128 ? 8 : 4; }
 constexpr int tile_rows(int64_t head_dim) { return head_dim == 128 ? 256 : 128; }
 constexpr int tile_shares(int64_t head_dim) { return head_dim == 64 ? 512 : 256; }   // workgroups that run at a time
