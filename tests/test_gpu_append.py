@@ -277,7 +277,8 @@ def test_in_place_and_streams():
         assert torch.equal(_bits(fused[:, :hq].cpu()), _bits(_round(want, BF16)))
 
 
-@pytest.mark.parametrize("new", [[1 + i % 3 for i in range(90)], [(11 * i) % 40 for i in range(66)]], ids=["few", "more"])
+@pytest.mark.parametrize("new", [[1 + i % 3 for i in range(90)], [(11 * i) % 40 for i in range(66)],
+                                 [i % 2 for i in range(4200)]], ids=["few", "more", "most"])
 def test_many_sequences(new):
     """More sequences than a wave has lanes."""
     G.require_gpu()

@@ -376,6 +376,7 @@ MANY = [
     ([i % 3 for i in range(131)], [(17 * i) % 90 for i in range(131)], 32, 8, 1, 128),
     ([66 if i % 9 == 0 else 1 for i in range(80)], [i for i in range(80)], 16, 2, 1, 64),
     ([1100, 1, 2], [0, 300, 7], 64, 64, 1, 64),      # row tiles enough for 64-bit counts
+    ([70 if i == 4400 else 1 for i in range(4500)], [i % 3 for i in range(4500)], 16, 4, 1, 64),
 ]
 
 
