@@ -581,16 +581,22 @@ __global__ __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) void mnb_attention_r
             const float now = fmaxf(top, m_unit);
             const float keep = exp2_fast(top - now), f_weight = exp2_fast(m_unit - now);
             top = now;
-            // The weights are held against the unit's largest weight times value scale.
-            float step = 32512.f, f_o;
+            // The weights are held against the unit's largest weight times value scale, which
+            // stands 2^up above the unit's largest weight.  A run whose scale is more than
+            // 2^64 above that (its scores lie as far below) has its exponentials taken from
+            // where it would reach it, so that no factor overflows.
+            float step = 32512.f, f_o, from = m_from;
             if (P >= 64) {
                 f_o = any ? f_weight * v_scale * (1.f / 32512.f) : 0.f;
             } else {
-                const bool seen = m_run != -__builtin_inff();
-                const float lvs = seen ? __log2f(v_scale) : -__builtin_inff();
-                const float n_unit = xor16_max(m_run + lvs);
+                const bool seen = m_run != -__builtin_inff() && v_scale > 0.f;
+                const float n_unit = xor16_max(seen ? m_run + __log2f(v_scale) : -__builtin_inff());
                 const bool some = n_unit != -__builtin_inff();
-                step = seen && some ? 32512.f * exp2_fast(m_from + lvs - n_unit) : 0.f;
+                const float up = some ? n_unit - m_from : 0.f;
+                const float over = (float)__builtin_amdgcn_frexp_expf(v_scale) - up;
+                const bool far = seen && over > 64.f;
+                from = far ? m_from - over : m_from;
+                step = seen && some ? 32512.f * __builtin_amdgcn_frexp_mantf(v_scale) * (far ? 1.f : exp2_fast(over)) : 0.f;
                 f_o = some ? exp2_fast(n_unit - now) * (1.f / 32512.f) : 0.f;
             }
             // (A scale that is not finite has no largest: it goes into the sum.)
@@ -598,12 +604,12 @@ __global__ __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) void mnb_attention_r
             uint32_t lo[16], hi[16];
 #pragma unroll
             for (int j = 0; j < 16; ++j) {
-                const float e = exp2_fast(x[j] - m_from);
+                const float e = exp2_fast(x[j] - from);
                 sum += e;
                 lo[j] = __float_as_uint(fmaf(e, step, 12582912.f));
                 hi[j] = __float_as_uint(fmaf(e, step, 12582912.f + 128.f));
             }
-            weight = weight * keep + sum * f_weight;
+            weight = weight * keep + sum * exp2_fast(from - m_from) * f_weight;
             halves = halves * keep + sum * step * f_o;
             i32x4 b_lo, b_hi;
 #pragma unroll

@@ -1,0 +1,104 @@
+"""Calls at the ends of what the cache, the attention over it and the adapters
+take: scores, scales and lengths that lie far apart, values next to a type's
+largest and smallest."""
+import pytest
+import torch
+
+from tests import gpu_util as G
+from tests import kv_ref as R
+from tests import test_gpu_attention as ATT
+
+pytestmark = pytest.mark.gpu
+
+BF16, F64 = torch.bfloat16, torch.float64
+
+
+def _few_rows(b, q, scale):
+    """Rows in 64 bits, and how far those of a sequence of few rows may be from
+    them before their last rounding.
+
+    As R.attention's, with the terms that belong to few rows alone: a score is off
+    by 2^-22 of its query's largest element and 16 steps of 2^-24 of the products'
+    magnitudes and of the largest score, a weight by twice that relative; each
+    weight is off by 1 / 65024 of the largest weight times value scale of its 64
+    keys, an integer of 128 at most, and what lies below 2^-126 of the row's
+    largest may count as zero; a sum by 2^-24 for each unit of 64 keys and 64
+    more, of its magnitudes, and by fp32's smallest step for each unit.
+    """
+    T, hq, D = q.shape
+    G_ = hq // b.heads
+    out, tol = torch.full(q.shape, float("nan"), dtype=F64), torch.zeros(q.shape, dtype=F64)
+    for s in range(b.S):
+        t0, n, length = int(b.starts[s]), int(b.starts[s + 1] - b.starts[s]), int(b.lengths[s])
+        for h in range(b.heads):
+            k, v, vs, held = R.keys_of(b, s, h, length)
+            for i in range(n * G_):
+                t, head = t0 + i // G_, h * G_ + i % G_
+                m = held & (torch.arange(length) <= length - n + i // G_)
+                x = q[t, head].double()
+                z = (k @ x * scale)[m]
+                w = torch.softmax(z, dim=0)
+                y = w @ v[m]
+                mag = abs(scale) * (k.abs() @ x.abs())[m]
+                d = abs(scale) * 2.0 ** -22 * x.abs().max() * k[m].abs().sum(dim=1).max()
+                d = d + 16 * 2.0 ** -24 * (mag.max() + z.abs().max())
+                size = w @ v[m].abs()
+                ws = torch.zeros(-(-length // 64) * 64, dtype=F64)
+                ws[:length][m] = w * vs[m]
+                held16 = 128 * 64 / 65024 * ws.reshape(-1, 64).amax(dim=1).sum()
+                units = ws.numel() // 64
+                sums = (units + 64) * 2.0 ** -24 * 2 * (size + 128 * (w @ vs[m])) + units * 2.0 ** -149
+                below = 2.0 ** -126 * 128 * float(vs[m].sum())
+                out[t, head], tol[t, head] = y, 2 * d * (size + y.abs()) + held16 + sums + below
+    return out, tol
+
+
+def _scored(lengths, P, D, scores, scales, seed=1, new=None):
+    """Sequences whose page i scores scores[i % len] (within one) for a query of one
+    at element 0 and zeros elsewhere, and has the value scale scales[i % len]; the
+    other integers are random."""
+    new = new or [1] * len(lengths)
+    b = R.Batch(new, [n - m for n, m in zip(lengths, new)], P, 1, D, seed=seed)
+    b.k_scales[:] = 2
+    for s in range(b.S):
+        for i in range(-(-int(b.lengths[s]) // P)):
+            p = int(b.table[s, i])
+            b.k_pages[p, :, :, 0] = round(scores[i % len(scores)] / 2)
+            b.v_scales[p] = scales[i % len(scales)]
+    return b
+
+
+def _unit_queries(T, hq, D):
+    q = torch.zeros(T, hq, D)
+    q[:, :, 0] = 1
+    return q.to(BF16)
+
+
+@pytest.mark.parametrize("P", [16, 32])
+@pytest.mark.parametrize("gap", [80, 100, 114, 120, 130, 160, 200])
+def test_largest_score_on_a_page_of_zeros(P, gap):
+    """A page of zeros holds the largest scores, the other pages of the unit score
+    `gap` (log2) lower."""
+    G.require_gpu()
+    low = -round(gap * 0.6931471805599453)
+    b = _scored([64, 64 + 16, 190], P, 64, (0, low, low - 3, low + 2), (0.0, 0.25, 2.0, 1.0))
+    q = _unit_queries(3, 2, 64)
+    got = ATT._call(b, q, scale=1.0)
+    want, tol = _few_rows(b, q, 1.0)
+    R.check_rows(got, want, tol, BF16)
+
+
+@pytest.mark.parametrize("P", [16, 32])
+@pytest.mark.parametrize("far", [(-126, -5, 120), (-126, 0, 80), (-126, -5, 160), (-126, 100, 118), (-100, 20, 114), (-20, 100, 90)])
+def test_scores_and_value_scales_far_apart(P, far):
+    """The largest score under a small value scale, and the other way round."""
+    G.require_gpu()
+    one, two, gap = far
+    low = -round(gap * 0.6931471805599453)
+    for scores, scales in (((0, low), (2.0 ** one, 2.0 ** two)), ((low, 0), (2.0 ** two, 2.0 ** one)),
+                           ((0, low, low - 1), (2.0 ** one, 2.0 ** two, 0.0))):
+        b = _scored([64, 100, 300], P, 64, scores, scales)
+        q = _unit_queries(3, 2, 64)
+        got = ATT._call(b, q, scale=1.0)
+        want, tol = _few_rows(b, q, 1.0)
+        R.check_rows(got, want, tol, BF16)
