@@ -587,7 +587,7 @@ __global__ __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) void mnb_attention_r
             // where it would reach it, so that no factor overflows.
             float step = 32512.f, f_o, from = m_from;
             if (P >= 64) {
-                f_o = any ? f_weight * v_scale * (1.f / 32512.f) : 0.f;
+                f_o = any ? f_weight * v_scale : 0.f;
             } else {
                 const bool seen = m_run != -__builtin_inff() && v_scale > 0.f;
                 const float n_unit = xor16_max(seen ? m_run + __log2f(v_scale) : -__builtin_inff());
@@ -597,7 +597,9 @@ __global__ __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) void mnb_attention_r
                 const bool far = seen && over > 64.f;
                 from = far ? m_from - over : m_from;
                 step = seen && some ? 32512.f * __builtin_amdgcn_frexp_mantf(v_scale) * (far ? 1.f : exp2_fast(over)) : 0.f;
-                f_o = some ? exp2_fast(n_unit - now) * (1.f / 32512.f) : 0.f;
+                // (2^up by its exponent and the rest: it may lie below exp2's range.)
+                const float whole_up = rintf(up);
+                f_o = some ? ldexpf(exp2_fast(up - whole_up) * f_weight, (int)whole_up) : 0.f;
             }
             // (A scale that is not finite has no largest: it goes into the sum.)
             float sum = m_run != -__builtin_inff() ? v_scale - v_scale : 0.f;
@@ -610,7 +612,7 @@ __global__ __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) void mnb_attention_r
                 hi[j] = __float_as_uint(fmaf(e, step, 12582912.f + 128.f));
             }
             weight = weight * keep + sum * exp2_fast(from - m_from) * f_weight;
-            halves = halves * keep + sum * step * f_o;
+            halves = halves * keep + sum * step * (1.f / 32512.f) * f_o;
             i32x4 b_lo, b_hi;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -625,8 +627,9 @@ __global__ __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) void mnb_attention_r
                 const i32x4 zero = i32x4{0, 0, 0, 0};
                 const i32x4 sh = __builtin_amdgcn_mfma_i32_16x16x64_i8(v[d % VT], b_hi, zero, 0, 0, 0);
                 const i32x4 sl = __builtin_amdgcn_mfma_i32_16x16x64_i8(v[d % VT], b_lo, zero, 0, 0, 0);
+                // (1 / 32512 goes to the products: f_o may be next to fp32's smallest.)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) o[d][i] = fmaf((float)((sh[i] << 8) + sl[i]), f_o, o[d][i]);
+                for (int i = 0; i < 4; ++i) o[d][i] = fmaf((float)((sh[i] << 8) + sl[i]) * (1.f / 32512.f), f_o, o[d][i]);
                 if (VT < DT) {
                     if (d + VT == DT && more) values_at(c + kWaves, next_v);
                     if (d + VT < DT || more) load_values((d + VT) % DT);

@@ -102,3 +102,20 @@ def test_scores_and_value_scales_far_apart(P, far):
         got = ATT._call(b, q, scale=1.0)
         want, tol = _few_rows(b, q, 1.0)
         R.check_rows(got, want, tol, BF16)
+
+
+@pytest.mark.parametrize("P", [16, 64])
+@pytest.mark.parametrize("first", [0, 2, 4, 8])
+@pytest.mark.parametrize("e", [-126, -122, -112])
+def test_small_value_scales(e, first, P):
+    """Value scales down to the smallest, behind a page of zeros whose scores are
+    larger: what the weights leave of them keeps its bits."""
+    G.require_gpu()
+    ahead = 1 if P < 64 else 4         # units of 64 keys go to four waves in turn
+    b = _scored([128, 333] if P < 64 else [512, 1111], P, 64, (0,) * ahead + (-first,) * (4 * ahead - ahead),
+                (0.0,) * ahead + (2.0 ** e, 2.0 ** (e + 2), 2.0 ** e) * ahead)
+    b.v_pages[:] = b.v_pages.abs().clamp(min=64, max=127)         # no sum is near zero
+    q = _unit_queries(2, 2, 64)
+    got = ATT._call(b, q, scale=1.0)
+    want, tol = _few_rows(b, q, 1.0)
+    R.check_rows(got, want, tol, BF16)
