@@ -866,7 +866,9 @@ __global__ __launch_bounds__(kJoinThreads) void mnb_attention_join_kernel(Attent
 // Sixteen keys (a run) have one value scale, which stands as a multiple r of the
 // sums' unit.  The unit changes, and the sums with it, only where r would leave
 // 2^-10 .. 2^8, so that no weight times scale falls out of fp16's range, whatever
-// the pages before it held, and pages of differing scales cost nothing.
+// the pages before it held, and pages of differing scales cost nothing.  A row's
+// unit follows the keys that it sees: scales of later ones, which rows further down
+// see, take nothing from it.
 //
 // A unit of a tile of 256 rows and heads of 128 takes 2.6 us on its compute unit, of which
 // the products are 1.8 at the rate of a large fp16 library product: the exponentials and
@@ -883,8 +885,9 @@ typedef float float16_t __attribute__((ext_vector_type(16)));
 // the units of the values.
 struct Runs {
     float ks[4], bias[4];
-    uint32_t ref[4];          // bits
     uint32_t spoilt;          // runs with a scale that is not finite
+    uint32_t valued;          // runs with a value scale above zero
+    uint32_t ref, group;      // the unit of the first run's sums (bits), and the runs that have it
 };
 
 __device__ __forceinline__ uint32_t half_pair(float lo, float hi) { return f16_pair(lo, hi); }
@@ -1038,41 +1041,49 @@ __global__ __launch_bounds__(64 * tile_waves(D), D == 64 ? 2 : 1) void mnb_atten
         lane_ks = live ? fabsf(p.k_scales[at_scale]) : 0.f;
         lane_vs = live ? fabsf(p.v_scales[at_scale]) : 0.f;
     };
-    uint32_t unit_bits = 0;              // bits of the unit of this wave's sums; 0: no sums yet
-    uint32_t staged = 0;                 // of a wave that multiplies every unit: alike in all waves
+    uint32_t unit_bits = 0;              // bits of the unit of this row's sums; 0: no sums yet
+    uint32_t unit_of_all = 0;            // the same, where all rows of the wave have one
+    uint32_t staged = 0, peak = 0;       // bits of the unit to go on with and of the largest so far: alike in all waves
     Runs now;
-    float lane_r;                        // what remains of run lane % 4's value scale
+    float lane_r, lane_ref;              // of run lane % 4: its value scale as a multiple of its sums' unit, and that
     auto settle = [&](Runs& n) {
         const bool fine = lane_vs < __builtin_inff();      // false for NaN
         const float vs = fine ? lane_vs : 0.f;
         const bool spoilt = !(lane_ks < __builtin_inff()) || !fine;
         const float ks = spoilt ? 1.f : lane_ks, bias = lane_ok ? 0.f : -__builtin_inff();
         n.spoilt = (uint32_t)__builtin_amdgcn_ballot_w64(spoilt) & 15u;
+        n.valued = (uint32_t)__builtin_amdgcn_ballot_w64(vs > 0.f) & 15u;
         // A run whose scale is zero, or from 2^-10 to 2^8 of the sums' unit, keeps that
-        // unit (128 times 2^8 is within fp16's range); another one has its own.  (Sums of
-        // a unit 2^80 larger have their last bit above what they would lose.)
-        const bool none = staged == 0;
-        float most = vs;
-        if (P < 64) {
-            most = fmaxf(most, __shfl_xor(most, 1));
-            most = fmaxf(most, __shfl_xor(most, 2));
-        }
-        const float base = !none ? __uint_as_float(staged) : most == 0.f ? 1.f : most;
+        // unit (128 times 2^8 is within fp16's range); another one has its own, but no less
+        // than 2^-80 of the largest one of the keys up to it: so no sum grows by more than
+        // that as its unit falls.  (Sums of a unit 2^80 larger have their last bit above what
+        // they would lose.  Keys behind a run do not count: rows may not see them.)
+        if (!staged && n.valued) staged = __builtin_amdgcn_readlane(__float_as_uint(vs), __builtin_ctz(n.valued));
+        const float base = staged ? __uint_as_float(staged) : 1.f;
         const bool near = vs == 0.f || (vs >= base * 0x1p-10f && vs <= base * 0x1p8f);
-        const float ref = near ? base : fmaxf(vs, fmaxf(most, base) * 0x1p-80f);
-        lane_r = vs == ref ? 1.f : vs / ref;
+        lane_ref = base;
+        if (__builtin_amdgcn_ballot_w64(!near)) {
+            const uint32_t own = __float_as_uint(near ? base : vs);
+            uint32_t upto = peak;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t its = __builtin_amdgcn_readlane(own, i);
+                upto = (lane & 3) > i ? max(upto, its) : upto;
+                peak = max(peak, its);
+            }
+            lane_ref = fmaxf(__uint_as_float(own), __uint_as_float(upto) * 0x1p-80f);
+            staged = __builtin_amdgcn_readlane(__float_as_uint(fmaxf(lane_ref, __uint_as_float(peak) * 0x1p-80f)), 3);
+        } else {
+            peak = max(peak, staged);
+        }
+        lane_r = vs == lane_ref ? 1.f : vs / lane_ref;
+        n.ref = __builtin_amdgcn_readlane(__float_as_uint(lane_ref), 0);
+        n.group = (uint32_t)__builtin_amdgcn_ballot_w64(__float_as_uint(lane_ref) == n.ref) & 15u;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             n.ks[i] = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(ks), i));
             n.bias[i] = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(bias), i));
-            n.ref[i] = __builtin_amdgcn_readlane(__float_as_uint(ref), i);
         }
-        // The runs are multiplied a unit of the sums at a time, in the order of the units'
-        // first runs.
-        staged = n.ref[0];
-        staged = n.ref[1] != n.ref[0] ? n.ref[1] : staged;
-        staged = n.ref[2] != n.ref[0] && n.ref[2] != n.ref[1] ? n.ref[2] : staged;
-        staged = n.ref[3] != n.ref[0] && n.ref[3] != n.ref[1] && n.ref[3] != n.ref[2] ? n.ref[3] : staged;
     };
     auto store = [&](int buffer) {
         const uint32_t r2 = f16_pair(lane_r, lane_r), half_r2 = f16_pair(0.5f * lane_r, 0.5f * lane_r);
@@ -1187,21 +1198,21 @@ __global__ __launch_bounds__(64 * tile_waves(D), D == 64 ? 2 : 1) void mnb_atten
                 };
                 // The runs of one unit of the sums at a time: all of them, but where their
                 // scales lie far apart.
-                uint32_t left = 15;
-                do {
-                    const uint32_t ref = left & 1 ? now.ref[0] : left & 2 ? now.ref[1] : left & 4 ? now.ref[2] : now.ref[3];
-                    if (ref != unit_bits) {
-                        const float by = unit_bits ? __uint_as_float(unit_bits) / __uint_as_float(ref) : 1.f;
-                        unit_bits = ref;
-#pragma unroll
-                        for (int d = 0; d < DB; ++d) o[d] *= by;
-                    }
+                uint32_t left = 15, group = now.group, ref = now.ref;
+                for (;;) {
+                    left &= ~group;
                     float from[4];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const bool in = (left >> e & 1) && now.ref[e] == ref;
-                        from[e] = in ? now.bias[e] - top : -__builtin_inff();
-                        left &= in ? ~(1u << e) : ~0u;
+                    for (int e = 0; e < 4; ++e) from[e] = group >> e & 1 ? now.bias[e] - top : -__builtin_inff();
+                    // A row's unit changes where it sees a value of the new one only.
+                    const uint32_t valued = group & now.valued;
+                    if (valued && ref != unit_of_all) {
+                        const bool turns = unit_bits != ref && key0 + 16 * __builtin_ctz(valued) <= position;
+                        const float by = turns && unit_bits ? __uint_as_float(unit_bits) / __uint_as_float(ref) : 1.f;
+                        unit_bits = turns ? ref : unit_bits;
+                        unit_of_all = __builtin_amdgcn_ballot_w64(unit_bits != ref) ? 0 : ref;
+#pragma unroll
+                        for (int d = 0; d < DB; ++d) o[d] *= by;
                     }
                     asm("" : "+v"(from_v));       // the loop's own loads: 16 pieces are too many to keep
                     half8_t va[2][DB];
@@ -1214,7 +1225,10 @@ __global__ __launch_bounds__(64 * tile_waves(D), D == 64 ? 2 : 1) void mnb_atten
                         for (int d = 0; d < DB; ++d)
                             o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(va[e & 1][d], w, o[d], 0, 0, 0);
                     }
-                } while (left);
+                    if (!left) break;
+                    ref = __builtin_amdgcn_readlane(__float_as_uint(lane_ref), __builtin_ctz(left));
+                    group = (uint32_t)__builtin_amdgcn_ballot_w64(__float_as_uint(lane_ref) == ref) & left;
+                }
             }
             if (more) {
                 settle(now);
@@ -1229,7 +1243,7 @@ __global__ __launch_bounds__(64 * tile_waves(D), D == 64 ? 2 : 1) void mnb_atten
     if (!q_finite && weight > 0.f) weight = __uint_as_float(0x7FC00000u);
     // o[d][8 e + j]: element elem0 + 32 d + 16 e + 8 hh + j.
     if (wave0 + r < rows && whole) {
-        const float by = weight == 0.f ? 0.f : unit / weight;
+        const float by = weight == 0.f ? 0.f : 1.f / weight;      // (unit / weight may lie below fp32's range)
         uint16_t* dst = p.out + (q.t0 + me.token) * p.out_stride + (int64_t)me.head * D + elem0 + 8 * hh;
 #pragma unroll
         for (int d = 0; d < DB; ++d)
@@ -1238,8 +1252,8 @@ __global__ __launch_bounds__(64 * tile_waves(D), D == 64 ? 2 : 1) void mnb_atten
                 u32x4 w;
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-                    w[j] = (uint32_t)narrow16(o[d][8 * e + 2 * j] * by, BF16) |
-                           (uint32_t)narrow16(o[d][8 * e + 2 * j + 1] * by, BF16) << 16;
+                    w[j] = (uint32_t)narrow16(o[d][8 * e + 2 * j] * by * unit, BF16) |
+                           (uint32_t)narrow16(o[d][8 * e + 2 * j + 1] * by * unit, BF16) << 16;
                 *reinterpret_cast<u32x4*>(dst + 32 * d + 16 * e) = w;
             }
     } else if (wave0 + r < rows) {

@@ -119,3 +119,28 @@ def test_small_value_scales(e, first, P):
     got = ATT._call(b, q, scale=1.0)
     want, tol = _few_rows(b, q, 1.0)
     R.check_rows(got, want, tol, BF16)
+
+
+@pytest.mark.parametrize("hq,new", [(16, 40), (64, 70)], ids=["shares", "tiles"])
+@pytest.mark.parametrize("P", [16, 32, 64])
+@pytest.mark.parametrize("es", [(-5, -70, -126), (0, -80, -126), (100, 30, -40, -110), (-126, -60, 10, 90), (-126, 0),
+                                (0, -126, 100), (-30, -126, -126, 60)], ids=str)
+def test_value_scales_fall_and_rise(es, P, hq, new):
+    """Tiles: value scales that fall and rise by 2^200 in all, rows that see the
+    first of them only."""
+    G.require_gpu()
+    b = _scored([900], P, 64, (0, 1, -1, 0, 2), tuple(2.0 ** e for e in es), new=[new])
+    for first in (0, 64):
+        if first:                  # rows that begin with the sequence
+            b = _scored([new], P, 64, (0, 1, -1, 0, 2), tuple(2.0 ** e for e in es), new=[new])
+        ATT._check(b, ATT._queries(new, hq, 64, BF16, 3, 0.125), scale=0.02)
+
+
+def test_small_value_scales_many_rows():
+    G.require_gpu()
+    for e in (-126, -121, -114):
+        b = R.Batch([70], [3000], 64, 1, 64, seed=1)
+        b.v_scales[:] = 2.0 ** e
+        b.v_pages[:] = b.v_pages.abs().clamp(min=64, max=127)
+        b.k_scales[:] = 2.0 ** -10
+        ATT._check(b, ATT._queries(70, 16, 64, BF16, 3))
