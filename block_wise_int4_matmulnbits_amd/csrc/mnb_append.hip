@@ -17,7 +17,9 @@
 // a 32-bit one are exact and the one rounding (2^-53) does not show.  floor and
 // the range test need no more than that value rounded down to fp32: the
 // integers n 2^e, |n| <= 128, are fp32 values, so x >= n 2^e exactly when its
-// fp32 value rounded down is.
+// fp32 value rounded down is.  Rotation takes bf16 values past fp32's range, up to
+// whose end, 128 times 2^127, there is a scale for them: so everything below stands
+// 2^8 lower, x 2^-8 for a key x (n 2^(e-8) are fp32 values as well).
 //
 // HBM bounds long calls: 7100 tokens of 8 heads of 128 with their 32 query heads move
 // 164 MB in 39 us (4.2 TB/s; a large copy 4.9).  The launch and one dependent chain of
@@ -68,8 +70,8 @@ __device__ __forceinline__ int64_t slot_base(const AppendParams& p, int32_t t0, 
     return p.by_token ? t0 : (int64_t)(t0 >> p.b.page_bits) + 2 * (int64_t)s;
 }
 
-// The fp32 value at or below x (the finite one next to it where x lies past
-// fp32's range is never asked for: see not_finite).
+// The fp32 value at or below x (where x lies past fp32's range, something past
+// 2^126, which range_bits takes for not finite).
 __device__ __forceinline__ float round_down(double x)
 {
     const float f = (float)x;
@@ -80,23 +82,24 @@ __device__ __forceinline__ float round_down(double x)
 
 // Bits whose maximum over the page gives its exponent: those of |x|, less one
 // step for negative x (-128 * 2^e still fits, 128 * 2^e does not), at least 1
-// where x is not zero; 0x7F800000 and above where x is not finite.
+// where x is not zero; 0x7F800000 where no scale fits (x past 128 * 2^127, or not
+// finite).
 __device__ __forceinline__ uint32_t range_bits(float x)
 {
-    const uint32_t b = __float_as_uint(x), m = b & 0x7FFFFFFFu;
-    if (m >= 0x7F800000u) return 0x7F800000u;
-    return (b >> 31) && m > 1 ? m - 1 : m;
+    const uint32_t b = __float_as_uint(x), m = b & 0x7FFFFFFFu, less = (b >> 31) && m > 1 ? m - 1 : m;
+    return less >= 0x7E800000u ? 0x7F800000u : less;
 }
 
-__device__ __forceinline__ int exponent_of(uint32_t bits) { const int e = (int)(bits >> 23) - 133; return e < -126 ? -126 : e; }
+// (0x00400000 is 2^-127, 2^8 times which is 64 * 2^-125.)
+__device__ __forceinline__ int exponent_of(uint32_t bits) { return bits < 0x00400000u ? -126 : (int)(bits >> 23) - 125; }
 
 __device__ __forceinline__ float power_of_two(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
 
-// floor(x / 2^e) of a value in range, with down = 2^-e.  (The product is exact
-// unless it falls below fp32's range, where only its sign counts.)
-__device__ __forceinline__ int quantize(float x, float down)
+// floor(x 2^by) of a value in range.  (The product is exact unless it falls below
+// fp32's range, where only its sign counts.)
+__device__ __forceinline__ int quantize(float x, int by)
 {
-    const float y = x * down;
+    const float y = __builtin_amdgcn_ldexpf(x, by);
     return (int)floorf(y) - ((__float_as_uint(y) << 1) == 0 && x < 0.f ? 1 : 0);
 }
 
@@ -141,18 +144,20 @@ __device__ __forceinline__ void load_turn(const AppendParams& p, int64_t positio
 }
 
 // The pieces a and b turned, value(n, x) called with each of the sixteen in 64 bits,
-// n = 0 .. 7 of the first piece, then the second's.  A unit that is not rotated keeps
-// its values whatever they are (0 times infinity would not).
-template <bool BF16, bool NEAR, class F>
+// n = 0 .. 7 of the first piece, then the second's; DOWN: times 2^-8.  A unit that is
+// not rotated keeps its values whatever they are (0 times infinity would not).
+template <bool BF16, bool NEAR, bool DOWN, class F>
 __device__ __forceinline__ void turn(const u32x4& a, const u32x4& b, const float4_t (&c)[2], const float4_t (&s)[2],
                                      bool turned, F value)
 {
+    constexpr float by = DOWN ? 0x1p-8f : 1.f;      // (exact: 16-bit values go down to 2^-133)
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const int e0 = NEAR ? 2 * i : i, e1 = NEAR ? 2 * i + 1 : 8 + i;
-        const float x0 = NEAR ? (i < 4 ? element<BF16>(a, 2 * (i & 3)) : element<BF16>(b, 2 * (i & 3))) : element<BF16>(a, i);
-        const float x1 = NEAR ? (i < 4 ? element<BF16>(a, 2 * (i & 3) + 1) : element<BF16>(b, 2 * (i & 3) + 1))
-                              : element<BF16>(b, i);
+        const float x0 = by * (NEAR ? (i < 4 ? element<BF16>(a, 2 * (i & 3)) : element<BF16>(b, 2 * (i & 3)))
+                                    : element<BF16>(a, i));
+        const float x1 = by * (NEAR ? (i < 4 ? element<BF16>(a, 2 * (i & 3) + 1) : element<BF16>(b, 2 * (i & 3) + 1))
+                                    : element<BF16>(b, i));
         const double co = c[i >> 2][i & 3], si = s[i >> 2][i & 3];
         const double y0 = (double)x0 * co - (double)x1 * si, y1 = (double)x1 * co + (double)x0 * si;
         value(e0, turned ? y0 : (double)x0);
@@ -188,9 +193,8 @@ __device__ __forceinline__ OldScale old_scale(float scale)
     const uint32_t b = __float_as_uint(scale) & 0x7FFFFFFFu;
     if (b == 0) return OldScale{0, 0};
     if (b >= 0x7F800000u) return OldScale{0x7F800000u, 0};
-    int e = (int)(b >> 23) - 127;
-    if (e < -126) e = -126;
-    return OldScale{e + 133 < 255 ? (uint32_t)(e + 133) << 23 : 0x7F7FFFFFu, e};
+    const int e = (int)(b >> 23) - 127;
+    return OldScale{max(__float_as_uint(0.25f * __uint_as_float(b)), 1u), e < -126 ? -126 : e};      // 64 * 2^-8
 }
 
 // One page of one head: the tokens of positions first + a .. first + b - 1, whose
@@ -216,7 +220,7 @@ __device__ __forceinline__ void store_keys(const AppendParams& p, int32_t page, 
         const u32x4 vb = *reinterpret_cast<const u32x4*>(src + off * p.k_stride + piece1);
         float4_t c[2], s[2];
         load_turn(p, first + off, j, c, s);
-        turn<BF16, NEAR>(va, vb, c, s, turned, [&](int n, double y) { x[n] = round_down(y); });
+        turn<BF16, NEAR, true>(va, vb, c, s, turned, [&](int n, double y) { x[n] = round_down(y); });
     };
     const bool keep = count <= kKeyUnits * kThreads;
     if (keep) {
@@ -243,7 +247,6 @@ __device__ __forceinline__ void store_keys(const AppendParams& p, int32_t page, 
     top = workgroup_max<kThreads>(max(top, old.bits), part);
     const bool finite = top < 0x7F800000u;
     const int e = exponent_of(top);
-    const float down = power_of_two(-e);
     if (threadIdx.x == 0) p.k_scales[at] = !finite ? __uint_as_float(0x7FC00000u) : top == 0 ? 0.f : power_of_two(e);
     if (old.bits && finite && e > old.e) {
         const int d = e - old.e < 7 ? e - old.e : 7;
@@ -256,7 +259,7 @@ __device__ __forceinline__ void store_keys(const AppendParams& p, int32_t page, 
         for (int n = 0; n < 4; ++n) {
             uint32_t r = 0;
 #pragma unroll
-            for (int m = 0; m < 4; ++m) r |= (uint32_t)(quantize(x[4 * n + m], down) & 255) << (8 * m);
+            for (int m = 0; m < 4; ++m) r |= (uint32_t)(quantize(x[4 * n + m], 8 - e) & 255) << (8 * m);
             w[n] = finite ? r : 0;
         }
         int8_t* to = dst + (a + i / UNITS) * D;
@@ -293,7 +296,7 @@ __device__ __forceinline__ uint32_t range_of(uint32_t most, uint32_t less, int b
     less = max(less & 0xFFFFu, less >> 16);
     if (most >= (bf16 ? 0x7F80u : 0x7C00u)) return 0x7F800000u;
     // (A step below the type's smallest value is zero, which says nothing of its range.)
-    return most == 0 ? 0u : max(__float_as_uint(0.5f * widen16(1, bf16)), __float_as_uint(widen16(less, bf16)));
+    return most == 0 ? 0u : max(__float_as_uint(0x1p-9f * widen16(1, bf16)), __float_as_uint(0x1p-8f * widen16(less, bf16)));
 }
 
 // The values lie with their tokens last: a thread holds eight elements of four
@@ -346,7 +349,6 @@ __device__ __forceinline__ void store_values(const AppendParams& p, int32_t page
     const uint32_t top = workgroup_max<kThreads>(max(range_of(most, less, BF16), old.bits), part);
     const bool finite = top < 0x7F800000u;
     const int e = exponent_of(top);
-    const float down = power_of_two(-e);
     if (threadIdx.x == 0) p.v_scales[at] = !finite ? __uint_as_float(0x7FC00000u) : top == 0 ? 0.f : power_of_two(e);
     const int d = old.bits && finite && e > old.e ? (e - old.e < 7 ? e - old.e : 7) : 0;
     if (d) {      // groups of old tokens only
@@ -369,7 +371,7 @@ __device__ __forceinline__ void store_values(const AppendParams& p, int32_t page
         for (int n = 0; n < 8; ++n) {
             uint32_t w = 0;
 #pragma unroll
-            for (int m = 0; m < 4; ++m) w |= (uint32_t)(quantize(element<BF16>(x[m], n), down) & 255) << (8 * m);
+            for (int m = 0; m < 4; ++m) w |= (uint32_t)(quantize(element<BF16>(x[m], n), -e) & 255) << (8 * m);
             w = finite ? w : 0;
             uint32_t* word = to + n * (P / 4);
             if (whole) {
@@ -434,7 +436,7 @@ __device__ __forceinline__ void turn_queries(const AppendParams& p, int64_t t)
             const int h = h0 + u * EACH + lane / UNITS;
             if (h >= p.q_heads) continue;
             uint32_t out[16];
-            turn<BF16, NEAR>(va[u], vb[u], c, s, 16 * j < p.rot,
+            turn<BF16, NEAR, false>(va[u], vb[u], c, s, 16 * j < p.rot,
                              [&](int n, double y) { out[n] = narrow16(round_to_odd(y), BF16); });
             u32x4 w[2];
 #pragma unroll

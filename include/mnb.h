@@ -522,9 +522,10 @@ typedef struct {
  * page behind the sequence's last token are left as they are.  Rows of q_out
  * whose token has no position within the page table are left as they are.
  * Numerics: rotated values in 64 bits, quantised from there; q_out rounded once
- * (RNE).  A value that is not finite makes its page's scale NaN, until the page
- * is begun anew.  q_out and the cache must not overlap the inputs or each
- * other, but for q_out == q.  Asynchronous; allocates nothing.
+ * (RNE).  A value that is not finite, or a rotated key outside -2^134 .. 2^134 (for
+ * which fp32 has no scale), makes its page's scale NaN, until the page is begun
+ * anew.  q_out and the cache must not overlap the inputs or each other, but for
+ * q_out == q.  Asynchronous; allocates nothing.
  */
 int append_kv_int8(const mnb_kv_cache* cache, const mnb_kv_batch* batch, int dtype, const void* k, int64_t k_stride,
                    const void* v, int64_t v_stride, const void* q, int64_t q_stride, void* q_out,
