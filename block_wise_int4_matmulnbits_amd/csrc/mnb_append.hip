@@ -396,11 +396,12 @@ __device__ __forceinline__ void store_values(const AppendParams& p, int32_t page
 
 // The queries of one token (a wave each), rotated and rounded to their type
 // once: to fp32 towards zero with the last bit holding whatever was cut off,
-// then to nearest even.
+// then to nearest even.  (Past fp32's largest value that gives it, which is infinity
+// in either type.)
 __device__ __forceinline__ float round_to_odd(double x)
 {
     const float f = (float)x;
-    if ((double)f == x || !(fabs(x) < 3.0e38)) return f;
+    if ((double)f == x || !(fabs(x) < (double)__builtin_inff())) return f;
     uint32_t b = __float_as_uint(f);
     if (fabs((double)f) > fabs(x)) b -= 1;
     return __uint_as_float(b | 1u);

@@ -148,6 +148,36 @@ def test_small_value_scales_many_rows():
         ATT._check(b, ATT._queries(70, 16, 64, BF16, 3))
 
 
+def _odd_steps(x, dtype):
+    """64-bit values to dtype, rounded once, wherever they lie."""
+    m, e = torch.frexp(x)
+    step = torch.ldexp(torch.ones_like(x), e.clamp(min=-125) - 8)
+    r = torch.round(x / step) * step
+    return torch.where(r.abs() > torch.finfo(dtype).max, torch.sign(r) * float("inf"), r).to(torch.float32).to(dtype)
+
+
+def test_rotated_queries_rounded_once():
+    """bf16 queries up to the type's largest value and past it, next to the middle
+    between two of them."""
+    G.require_gpu()
+    P, D, T = 16, 64, 512
+    b = R.Batch([T], [0], P, 1, D, seed=1)
+    g = torch.Generator().manual_seed(2)
+    x = (torch.rand(T, 1, D, generator=g) * 0.3 + 0.85).mul(3.2e38).clamp(max=3.38e38).to(BF16)
+    angle = torch.rand(b.width * P, D // 2, generator=g, dtype=F64) * 0.2
+    cos, sin = angle.cos().float(), angle.sin().float()
+    # cosines that put a value next to a middle: x c = (n + 1/2) step (1 + 2^-25 or so)
+    mid = (torch.floor(x[:, 0, :D // 2].double() * 0.95 / 2.0 ** 120) + 0.5) * 2.0 ** 120
+    cos[:T] = (mid / x[:, 0, :D // 2].double()).float()
+    sin[:T] = 1e-8 * torch.randn(T, D // 2, generator=g)
+    args = b.cuda()
+    q_out = torch.empty(T, 1, D, dtype=BF16, device="cuda")
+    mnb.append_kv_int8(x.cuda(), x.cuda(), cos.cuda(), sin.cuda(), *args, q=x.cuda(), q_out=q_out)
+    torch.cuda.synchronize()
+    want = torch.stack([R.rotate(x[t], cos[t], sin[t], False) for t in range(T)])
+    assert torch.equal(q_out.cpu().view(torch.int16), _odd_steps(want, BF16).view(torch.int16))
+
+
 @pytest.mark.parametrize("c,s", [(0.70710677, 0.70710677), (0.70710677, -0.70710677), (-1.0, 0.0), (0.6, 0.8), (8.0, 30.0), (-30.0, 20.0)])
 @pytest.mark.parametrize("interleaved", [False, True])
 def test_rotated_past_the_type(c, s, interleaved):
