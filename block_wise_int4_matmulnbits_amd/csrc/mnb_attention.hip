@@ -540,7 +540,7 @@ __global__ __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) void mnb_attention_r
             const int32_t key0 = c * 64, run0 = key0 + 16 * g;
             const float v_scale = fabsf(vs);
             float x[16];
-            const float factor = q_scale * ks, bias = ok ? 0.f : -__builtin_inff();
+            const float factor = ok ? q_scale * ks : 0.f, bias = ok ? 0.f : -__builtin_inff();
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
                 i32x4 c0v = i32x4{half, half, half, half}, c1v = i32x4{0, 0, 0, 0}, c2v = i32x4{0, 0, 0, 0};

@@ -227,3 +227,27 @@ def test_scales_up_to_the_largest():
                     assert torch.equal(got.cpu(), ref)
             else:
                 assert bool(torch.isnan(args[5][page, 0])) and bool((args[3][page, 0, :2] == 0).all())
+
+
+def test_queries_without_a_usable_page():
+    """A query that is not finite and sees no key: zeros, in every kernel."""
+    G.require_gpu()
+    for P in (16, 64):
+        for new, hq in (([1, 2], 2), ([90, 1], 4), ([90, 1], 30)):
+            b = R.Batch(new, [100] * len(new), P, 1, 64, seed=1)
+            b.table[0] = -1
+            q = ATT._queries(b.T, hq, 64, BF16, 1)
+            clean = ATT._call(b, q)
+            for bad in (float("nan"), float("inf")):
+                q2 = q.clone()
+                q2[0, 1, 3] = bad
+                got = ATT._call(b, q2)
+                assert bool((got[:new[0]] == 0).all())
+                assert torch.equal(got, clean)
+            # some usable pages only: the row is spoilt, and no other
+            b.table[0, 1] = 0
+            clean = ATT._call(b, q)
+            got = ATT._call(b, q2)
+            assert bool(torch.isnan(got[0, 1]).all())
+            got[0, 1] = clean[0, 1]
+            assert torch.equal(got, clean)
