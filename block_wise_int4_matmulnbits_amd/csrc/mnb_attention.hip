@@ -1345,7 +1345,7 @@ int launch_attention(const AttentionArgs& a, void* stream, int* launches)
     p.tile_o = reinterpret_cast<float*>(ws + lay.tile_o);
     p.many = lay.many;
     // No sequence can have many rows where max_tokens says so.
-    const bool few = a.max_tokens > 0 && a.max_tokens * p.G <= p.many;
+    const bool few = a.max_tokens > 0 && a.max_tokens <= p.many / p.G;
     p.tile_slots = few ? 0 : lay.tile_slots;
     if (few) p.many = INT32_MAX;
     p.shares = few ? 0 : lay.shares;

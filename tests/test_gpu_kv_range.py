@@ -251,3 +251,17 @@ def test_queries_without_a_usable_page():
             assert bool(torch.isnan(got[0, 1]).all())
             got[0, 1] = clean[0, 1]
             assert torch.equal(got, clean)
+
+
+def test_max_tokens_past_any_length():
+    """Bounds of the tokens up to the largest integer are bounds like others: the
+    kernels of many rows."""
+    G.require_gpu()
+    b = R.Batch([300], [100], 32, 1, 64, seed=4)
+    q = ATT._queries(b.T, 4, 64, BF16, 2)
+    want = ATT._call(b, q, max_tokens=300)
+    for most in (2 ** 31, 2 ** 62, 2 ** 63 - 1):
+        c0 = mnb.mnb_counters_get()["launches"]
+        got = ATT._call(b, q, max_tokens=most)
+        assert mnb.mnb_counters_get()["launches"] - c0 == 3
+        assert torch.equal(got, want)
