@@ -523,6 +523,17 @@ def _gpu_of(name, t):
     return index
 
 
+def _on_stream(index, stream, workspace, call, *args):
+    """_on_device; where the module takes the call's workspace from torch's
+    allocator, on the call's stream (see _workspace)."""
+    import torch
+    if stream is None or workspace is not None:
+        return _on_device(index, stream, call, *args)
+    on = torch.cuda.ExternalStream(stream, device=index) if isinstance(stream, int) else stream
+    with torch.cuda.stream(on):
+        return _on_device(index, stream, call, *args)
+
+
 def append_kv_int8(k, v, cos, sin, starts, lengths, page_table, k_pages, v_pages, k_scales, v_scales, q=None,
                    q_out=None, interleaved=False, stream=None):
     """New tokens' keys and values into a paged cache of 8-bit integers, the
@@ -560,12 +571,8 @@ def attention_int8(q, starts, lengths, page_table, k_pages, v_pages, k_scales, v
     Queued on ``stream``; returns ``out``.
     """
     N = _native or _load_native()
-    index = _gpu_of("q", q)
-    if stream is not None and workspace is None:
-        need = _lib.mnb_attention_workspace(q.shape[0], lengths.shape[0], q.shape[1], k_pages.shape[1], q.shape[2])
-        workspace = _workspace(q, need, None, stream, index)
-    _on_device(index, stream, N.attention_int8, q, starts, lengths, page_table, k_pages, v_pages, k_scales, v_scales, out,
-               scale, max_tokens, workspace)
+    _on_stream(_gpu_of("q", q), stream, workspace, N.attention_int8, q, starts, lengths, page_table, k_pages, v_pages,
+               k_scales, v_scales, out, scale, max_tokens, workspace)
     return out
 
 
@@ -587,11 +594,7 @@ def matmul_lora(x, ids, A, B, base, out, scaling=None, workspace=None, stream=No
     torch's allocator.  Queued on ``stream``; returns ``out``.
     """
     N = _native or _load_native()
-    index = _gpu_of("x", x)
-    if stream is not None and workspace is None:
-        need = _lib.mnb_lora_workspace(x.shape[0], x.shape[1], B.shape[1], A.shape[1], A.shape[0])
-        workspace = _workspace(x, need, None, stream, index)
-    _on_device(index, stream, N.matmul_lora, x, ids, A, B, base, out, scaling, workspace)
+    _on_stream(_gpu_of("x", x), stream, workspace, N.matmul_lora, x, ids, A, B, base, out, scaling, workspace)
     return out
 
 

@@ -12,7 +12,7 @@ from tests import test_gpu_attention as ATT
 
 pytestmark = pytest.mark.gpu
 
-BF16, F64 = torch.bfloat16, torch.float64
+F16, BF16, F64 = torch.float16, torch.bfloat16, torch.float64
 
 
 def _few_rows(b, q, scale):
@@ -265,3 +265,25 @@ def test_max_tokens_past_any_length():
         got = ATT._call(b, q, max_tokens=most)
         assert mnb.mnb_counters_get()["launches"] - c0 == 3
         assert torch.equal(got, want)
+
+
+def test_refusals_on_another_stream():
+    """Wrong arguments are refused in the same manner where a stream is named."""
+    G.require_gpu()
+    b = R.Batch([3], [20], 16, 2, 64, seed=1)
+    c = b.cuda()
+    q = torch.zeros(3, 4, 64, dtype=F16, device="cuda")
+    x, ids = torch.zeros(5, 64, dtype=F16, device="cuda"), torch.zeros(5, dtype=torch.int32, device="cuda")
+    A, B = torch.zeros(2, 8, 64, dtype=F16, device="cuda"), torch.zeros(2, 30, 8, dtype=F16, device="cuda")
+    y = torch.zeros(5, 30, dtype=F16, device="cuda")
+    side = torch.cuda.Stream()
+    for stream in (side, side.cuda_stream):
+        for error, call in ((ValueError, lambda: mnb.attention_int8(q[0], *c, q[0], stream=stream)),
+                            (TypeError, lambda: mnb.attention_int8(q, c[0], 5, *c[2:], q, stream=stream)),
+                            (TypeError, lambda: mnb.attention_int8(q, *c[:3], None, *c[4:], q, stream=stream)),
+                            (ValueError, lambda: mnb.attention_int8(q, *c[:3], c[5], *c[4:], q, stream=stream)),
+                            (ValueError, lambda: mnb.matmul_lora(x[0], ids, A, B, y, y, stream=stream)),
+                            (ValueError, lambda: mnb.matmul_lora(x, ids, A[0, 0], B, y, y, stream=stream)),
+                            (TypeError, lambda: mnb.matmul_lora(x, ids, A, None, y, y, stream=stream))):
+            with pytest.raises(error):
+                call()
