@@ -5,12 +5,14 @@ mnb_gemm_mfma.hip, mnb_layout.hip, mnb_int8.hip, mnb_moe.hip,
 mnb_append.hip, mnb_attention.hip, mnb_lora.hip); the host front end
 (mnb_api.cpp) is plain C++ built with g++; hipcc links both into one shared
 library next to this file.  mnb_torch.cpp, the part of the Python binding that is
-compiled, becomes a module of its own there.
+compiled, becomes a module of its own there; it alone needs torch and Python's
+headers, and where it cannot be built the library is there without it.
 """
 from __future__ import annotations
 
 import os
 import subprocess
+import sys
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -54,8 +56,25 @@ def _run(cmd, verbose):
     subprocess.run(cmd, check=True)
 
 
+def _build_module(verbose):
+    """Compile mnb_torch.so; returns why there is none, or None.  One of older
+    sources does not stay."""
+    tmp = TORCH_MODULE + ".tmp%d" % os.getpid()
+    try:
+        flags, libs = _torch_flags()
+        _run(["g++", "-shared", os.path.join(CSRC, "mnb_torch.cpp"), "-o", tmp] + flags + libs, verbose)
+        os.replace(tmp, TORCH_MODULE)
+        return None
+    except (ImportError, subprocess.CalledProcessError) as e:
+        for path in (tmp, TORCH_MODULE):
+            if os.path.exists(path):
+                os.remove(path)
+        return str(e)
+
+
 def build(verbose: bool = False, save_temps: bool = False) -> str:
-    """Compile and link libmnb.so (always recompiles). Returns its path."""
+    """Compile and link libmnb.so (always recompiles), and the binding's module
+    where torch is there. Returns the library's path."""
     os.makedirs(BUILD, exist_ok=True)
     extra = ["-save-temps=obj"] if save_temps else []
     objs = []
@@ -69,16 +88,12 @@ def build(verbose: bool = False, save_temps: bool = False) -> str:
     api_o = os.path.join(BUILD, "mnb_api.o")
     objs.append(api_o)
     jobs.append(["g++", "-c", os.path.join(CSRC, "mnb_api.cpp"), "-o", api_o] + CXX_FLAGS)
-    # The binding's module: named only when it is whole.
-    flags, libs = _torch_flags()
-    module = TORCH_MODULE + ".tmp%d" % os.getpid()
-    jobs.append(["g++", "-shared", os.path.join(CSRC, "mnb_torch.cpp"), "-o", module] + flags + libs)
     # The translation units are independent: compile them side by side.
     from concurrent.futures import ThreadPoolExecutor
-    with ThreadPoolExecutor(max_workers=len(jobs)) as ex:
+    with ThreadPoolExecutor(max_workers=len(jobs) + 1) as ex:
+        module = ex.submit(_build_module, verbose)
         for f in [ex.submit(_run, cmd, verbose) for cmd in jobs]:
             f.result()
-    os.replace(module, TORCH_MODULE)
     tmp = LIB + ".tmp%d" % os.getpid()
     _run(["hipcc", "-shared", "-fPIC", "--offload-arch=" + ARCH, "-o", tmp] + objs, verbose)
     os.replace(tmp, LIB)
@@ -87,6 +102,10 @@ def build(verbose: bool = False, save_temps: bool = False) -> str:
     _run(["hipcc", "-shared", os.path.join(CSRC, "mnb_probe.hip"), "-o", tmp] + HIP_FLAGS,
          verbose)
     os.replace(tmp, PROBE_LIB)
+    why = module.result()
+    if why:
+        print("mnb_torch.so (append_kv_int8, attention_int8 and matmul_lora from Python) is not built: " + why,
+              file=sys.stderr, flush=True)
     return LIB
 
 
