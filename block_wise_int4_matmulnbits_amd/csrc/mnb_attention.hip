@@ -887,7 +887,9 @@ struct Runs {
     float ks[4], bias[4];
     uint32_t spoilt;          // runs with a scale that is not finite
     uint32_t valued;          // runs with a value scale above zero
-    uint32_t ref, group;      // the unit of the first run's sums (bits), and the runs that have it
+    uint32_t fractions;       // runs whose value scale is no power of two
+    int32_t ref;              // the unit of the first run's sums (bits), and the runs that have it
+    uint32_t group;
 };
 
 __device__ __forceinline__ uint32_t half_pair(float lo, float hi) { return f16_pair(lo, hi); }
@@ -1041,44 +1043,50 @@ __global__ __launch_bounds__(64 * tile_waves(D), D == 64 ? 2 : 1) void mnb_atten
         lane_ks = live ? fabsf(p.k_scales[at_scale]) : 0.f;
         lane_vs = live ? fabsf(p.v_scales[at_scale]) : 0.f;
     };
-    uint32_t unit_bits = 0;              // bits of the unit of this row's sums; 0: no sums yet
-    uint32_t unit_of_all = 0;            // the same, where all rows of the wave have one
-    uint32_t staged = 0, peak = 0;       // bits of the unit to go on with and of the largest so far: alike in all waves
+    int32_t unit_bits = 0;               // bits of the unit of this row's sums; 0: no sums yet
+    int32_t unit_of_all = 0;             // the same, where all rows of the wave have one
+    int32_t staged = 0, peak = 0;        // bits of the unit to go on with and of the largest so far: alike in all waves
     Runs now;
-    float lane_r, lane_ref;              // of run lane % 4: its value scale as a multiple of its sums' unit, and that
+    int32_t lane_ref;                    // of run lane % 4: bits of its sums' unit,
+    float lane_r, lane_part;             // its value scale as a multiple of that, but for a fraction, and 1 / that
     auto settle = [&](Runs& n) {
+        // The value scale is a power of two, vs, times a fraction from 1 to 2, which goes to
+        // the weights (1 where append_kv_int8 stored it).  Powers of two by their bits.
+        constexpr int32_t kOne = 0x3F800000, kStep = 1 << 23;
         const bool fine = lane_vs < __builtin_inff();      // false for NaN
-        const float vs = fine ? lane_vs : 0.f;
-        const bool spoilt = !(lane_ks < __builtin_inff()) || !fine;
+        const int32_t bits = fine ? __float_as_uint(lane_vs) : 0, vs = bits & 0x7F800000;
+        const bool spoilt = !(lane_ks < __builtin_inff()) || !fine, some = vs != 0;
         const float ks = spoilt ? 1.f : lane_ks, bias = lane_ok ? 0.f : -__builtin_inff();
         n.spoilt = (uint32_t)__builtin_amdgcn_ballot_w64(spoilt) & 15u;
-        n.valued = (uint32_t)__builtin_amdgcn_ballot_w64(vs > 0.f) & 15u;
+        n.valued = (uint32_t)__builtin_amdgcn_ballot_w64(some) & 15u;
+        n.fractions = (uint32_t)__builtin_amdgcn_ballot_w64(bits != vs) & 15u;
+        lane_part = some && bits != vs ? __builtin_amdgcn_rcpf(__uint_as_float((bits & 0x007FFFFF) | kOne)) : 1.f;
         // A run whose scale is zero, or from 2^-10 to 2^8 of the sums' unit, keeps that
         // unit (128 times 2^8 is within fp16's range); another one has its own, but no less
         // than 2^-80 of the largest one of the keys up to it: so no sum grows by more than
         // that as its unit falls.  (Sums of a unit 2^80 larger have their last bit above what
         // they would lose.  Keys behind a run do not count: rows may not see them.)
-        if (!staged && n.valued) staged = __builtin_amdgcn_readlane(__float_as_uint(vs), __builtin_ctz(n.valued));
-        const float base = staged ? __uint_as_float(staged) : 1.f;
-        const bool near = vs == 0.f || (vs >= base * 0x1p-10f && vs <= base * 0x1p8f);
+        if (!staged && n.valued) staged = __builtin_amdgcn_readlane(vs, __builtin_ctz(n.valued));
+        const int32_t base = staged ? staged : kOne;
+        const bool near = !some || (uint32_t)(vs - base + 10 * kStep) <= 18u * kStep;
         lane_ref = base;
         if (__builtin_amdgcn_ballot_w64(!near)) {
-            const uint32_t own = __float_as_uint(near ? base : vs);
-            uint32_t upto = peak;
+            const int32_t own = near ? base : vs;
+            int32_t upto = peak;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const uint32_t its = __builtin_amdgcn_readlane(own, i);
+                const int32_t its = __builtin_amdgcn_readlane(own, i);
                 upto = (lane & 3) > i ? max(upto, its) : upto;
                 peak = max(peak, its);
             }
-            lane_ref = fmaxf(__uint_as_float(own), __uint_as_float(upto) * 0x1p-80f);
-            staged = __builtin_amdgcn_readlane(__float_as_uint(fmaxf(lane_ref, __uint_as_float(peak) * 0x1p-80f)), 3);
+            lane_ref = max(own, upto - 80 * kStep);
+            staged = __builtin_amdgcn_readlane(max(lane_ref, peak - 80 * kStep), 3);
         } else {
             peak = max(peak, staged);
         }
-        lane_r = vs == lane_ref ? 1.f : vs / lane_ref;
-        n.ref = __builtin_amdgcn_readlane(__float_as_uint(lane_ref), 0);
-        n.group = (uint32_t)__builtin_amdgcn_ballot_w64(__float_as_uint(lane_ref) == n.ref) & 15u;
+        lane_r = some ? __uint_as_float(max(vs - lane_ref + kOne, 0)) : 0.f;
+        n.ref = __builtin_amdgcn_readlane(lane_ref, 0);
+        n.group = (uint32_t)__builtin_amdgcn_ballot_w64(lane_ref == n.ref) & 15u;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             n.ks[i] = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(ks), i));
@@ -1185,20 +1193,24 @@ __global__ __launch_bounds__(64 * tile_waves(D), D == 64 ? 2 : 1) void mnb_atten
 #pragma unroll
                     for (int d = 0; d < DB; ++d) f[d] = *reinterpret_cast<const half8_t*>(v_lds + from_v + 32 * d * VROW + 16 * e);
                 };
+                // (Their sum goes without the fraction of the scale.)
                 auto weights = [&](int e, float from) {
                     u32x4 pairs;
+                    float sum = 0.f;
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         const float a = exp2_fast(fmaf(x[e >> 1][8 * (e & 1) + 2 * j], factor[e], from));
                         const float b = exp2_fast(fmaf(x[e >> 1][8 * (e & 1) + 2 * j + 1], factor[e], from));
                         pairs[j] = half_pair(a, b);
-                        weight = dot2(pairs[j], 0x3C003C00u, weight);
+                        sum = dot2(pairs[j], 0x3C003C00u, sum);
                     }
+                    weight = fmaf(sum, __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(lane_part), e)), weight);
                     return __builtin_bit_cast(half8_t, pairs);
                 };
                 // The runs of one unit of the sums at a time: all of them, but where their
                 // scales lie far apart.
-                uint32_t left = 15, group = now.group, ref = now.ref;
+                uint32_t left = 15, group = now.group;
+                int32_t ref = now.ref;
                 for (;;) {
                     left &= ~group;
                     float from[4];
@@ -1214,6 +1226,10 @@ __global__ __launch_bounds__(64 * tile_waves(D), D == 64 ? 2 : 1) void mnb_atten
 #pragma unroll
                         for (int d = 0; d < DB; ++d) o[d] *= by;
                     }
+                    if (now.fractions)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            from[e] -= __log2f(__uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(lane_part), e)));
                     asm("" : "+v"(from_v));       // the loop's own loads: 16 pieces are too many to keep
                     half8_t va[2][DB];
                     values(0, va[0]);
@@ -1226,8 +1242,8 @@ __global__ __launch_bounds__(64 * tile_waves(D), D == 64 ? 2 : 1) void mnb_atten
                             o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(va[e & 1][d], w, o[d], 0, 0, 0);
                     }
                     if (!left) break;
-                    ref = __builtin_amdgcn_readlane(__float_as_uint(lane_ref), __builtin_ctz(left));
-                    group = (uint32_t)__builtin_amdgcn_ballot_w64(__float_as_uint(lane_ref) == ref) & left;
+                    ref = __builtin_amdgcn_readlane(lane_ref, __builtin_ctz(left));
+                    group = (uint32_t)__builtin_amdgcn_ballot_w64(lane_ref == ref) & left;
                 }
             }
             if (more) {

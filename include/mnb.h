@@ -560,8 +560,10 @@ int append_kv_int8(const mnb_kv_cache* cache, const mnb_kv_batch* batch, int dty
  * by 2^-11 of themselves and 2^-24 of the row's largest.  Sums in fp32, one
  * rounding (RNE); value scales that differ by more than 2^80 within a row's keys
  * may lose the smaller ones.  Scales are powers of two as append_kv_int8 stores
- * them, or any numbers that are not negative; q . k and the scores have to lie in
- * fp32's range.  A query that is not finite, or a NaN scale of a page that a row
+ * them, or any numbers that are not negative (those of values below 2^-126 may count
+ * as zero); q . k, the scores and the sums of weights times values, the largest weight
+ * up to 64, have to lie in fp32's range, and weights below 2^-126 of a row's largest
+ * may count as zero.  A query that is not finite, or a NaN scale of a page that a row
  * sees, gives NaN in that row.  The order of fp32 sums depends on the lengths of
  * the whole batch; equal calls give equal bits.  out and workspace must not
  * overlap the inputs or each other.  Asynchronous; allocates nothing; two

@@ -1,6 +1,8 @@
 """Calls at the ends of what the cache, the attention over it and the adapters
 take: scores, scales and lengths that lie far apart, values next to a type's
 largest and smallest."""
+import math
+
 import pytest
 import torch
 
@@ -251,6 +253,49 @@ def test_queries_without_a_usable_page():
             assert bool(torch.isnan(got[0, 1]).all())
             got[0, 1] = clean[0, 1]
             assert torch.equal(got, clean)
+
+
+@pytest.mark.parametrize("P", [16, 32, 64, 256])
+@pytest.mark.parametrize("new,hq", [([1, 2], 4), ([40], 16), ([70, 1], 64)], ids=["few", "shares", "tiles"])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_scales_that_are_no_powers_of_two(D, new, hq, P):
+    G.require_gpu()
+    b = R.Batch(new, [700, 333][:len(new)], P, 1, D, seed=P)
+    g = torch.Generator().manual_seed(D)
+    for i, scales in enumerate((b.k_scales, b.v_scales)):
+        scales.mul_(torch.rand(scales.shape, generator=g) + 1)
+        if i:
+            scales[::3] *= 2.0 ** -12
+    for dtype in (F16, BF16):
+        ATT._check(b, ATT._queries(b.T, hq, D, dtype, 3))
+
+
+def test_fractions_of_scales_are_exact_in_tiles():
+    """One weight of 1 and one next to the middle between two fp16 values, a value
+    scale likewise, integers whose products with it are: none but the weight may
+    be rounded (two roundings more would pass the bound, all three up)."""
+    G.require_gpu()
+    P, D = 16, 64
+    s = 1 + 0.51 * 2.0 ** -10
+    half = lambda x: float(torch.tensor(x, dtype=F64).to(F16))
+    n = [q for q in range(64, 128) if half((q + 0.5) * half(s)) > (q + 0.5) * half(s) * (1 + 2.0 ** -12.5)]
+    assert half(s) > s and len(n) > 3
+    b = R.Batch([5], [43], P, 1, D, seed=1)
+    pages = b.table[0].tolist()
+    b.k_pages[:] = 0
+    b.k_scales[:] = 1
+    b.v_scales[:] = s
+    b.v_scales[pages[0]] = 1
+    for p in pages[1:]:
+        b.k_pages[p, :, :, 0] = -1
+    b.k_pages[:, :, :, 1:] = 0
+    for d in range(D):
+        b.v_pages[pages[0], 0, d] = -n[d % len(n)] - 1      # -(n + 1/2): the sums are near zero
+        for p in pages[1:]:
+            b.v_pages[p, 0, d] = n[d % len(n)]
+    q = torch.zeros(5, 64, D)
+    q[:, :, 0] = 1
+    ATT._check(b, q.to(F16), scale=-math.log(0.5 + 0.51 * 2.0 ** -11))
 
 
 def test_max_tokens_past_any_length():
