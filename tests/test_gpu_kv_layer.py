@@ -121,6 +121,50 @@ def test_layer_as_served(new, before):
         torch.cuda.synchronize()
 
 
+@pytest.mark.parametrize("new,before", [([1], [100]), ([1, 1, 1, 1], [0, 3, 64, 200]), ([2, 70, 1, 9], [30, 0, 128, 55])],
+                         ids=["token", "tokens", "mixed"])
+def test_captured_layer_from_the_cache_before(new, before):
+    """A captured step replayed over caches as they are before it: what it has to
+    store is not there yet, and the eager step's cache and outputs are."""
+    G.require_gpu()
+    L = Layer(512, 8, 2, 64, 16, 3, 11)
+    T = sum(new)
+    steps = []
+    for i in range(3):
+        g = torch.Generator().manual_seed(10 + i)
+        b = R.Batch(new, [c + i for c in before], 32, 2, 64, seed=i, width=16, spare=4)
+        pages = 40
+        for name in ("k_pages", "v_pages", "k_scales", "v_scales"):
+            t = getattr(b, name)
+            setattr(b, name, torch.cat((t, t.new_zeros((pages - t.shape[0],) + t.shape[1:]))))
+        b.pages = pages
+        x, ids = torch.randn(T, 512, generator=g).to(F16).cuda(), torch.randint(-1, 3, (T,), generator=g).to(torch.int32).cuda()
+        cache, bufs = b.cuda(), L.buffers(T)
+        clean = [t.clone() for t in cache]
+        L.step(x, ids, cache, bufs)
+        torch.cuda.synchronize()
+        for t, was in zip(cache[3:5], clean[3:5]):
+            assert not torch.equal(t, was)
+        steps.append((x, ids, clean, cache, bufs))
+    x, ids, dev = steps[0][0].clone(), steps[0][1].clone(), [t.clone() for t in steps[0][2]]
+    bufs = L.buffers(T)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        L.step(x, ids, dev, bufs)
+    for i in (1, 2, 0, 1):
+        sx, sids, clean, after, want = steps[i]
+        for dst, src in zip([x, ids] + dev, [sx, sids] + clean):
+            dst.copy_(src)
+        graph.replay()
+        torch.cuda.synchronize()
+        for got, ref in zip(dev[3:], after[3:]):
+            assert torch.equal(got.view(torch.uint8), ref.view(torch.uint8))
+        for n, t in bufs.items():
+            assert torch.equal(t, want[n]), n
+        L.step(x, ids, [t.clone() for t in clean], L.buffers(T))       # eager work between the replays
+        torch.cuda.synchronize()
+
+
 def _calls(seed):
     """Calls of the three operators on inputs of their own: (call(out, stream), shape)."""
     b = R.Batch([1, 40, 2], [300, 20, 77], 16, 2, 64, seed=seed)
