@@ -184,10 +184,13 @@ struct __attribute__((packed, aligned(4))) Words3 {
 // The pairs of two words' four elements that begin at the first (shift 0) or second (16).
 __device__ __forceinline__ uint32_t shifted(uint32_t hi, uint32_t lo, uint32_t shift) { return __builtin_amdgcn_alignbit(hi, lo, shift); }
 
-// C = 4 CT columns of a row's base, none of them behind the last one.
+// C = 4 CT columns of a row's base, none of them behind the last one; the buffer is
+// what lies from first to last.
 template <int CT>
-__device__ __forceinline__ void load_base(const uint16_t* src, uint32_t (&b)[2 * CT])
+__device__ __forceinline__ void load_base(const uint16_t* src, const uint16_t* first, const uint16_t* last,
+                                          uint32_t (&b)[2 * CT])
 {
+    constexpr int C = 4 * CT;
     if constexpr (CT == 1) {
         const Loose8 t = *reinterpret_cast<const Loose8*>(src);
         b[0] = t.v[0];
@@ -195,6 +198,11 @@ __device__ __forceinline__ void load_base(const uint16_t* src, uint32_t (&b)[2 *
     } else {
         // The words that hold these columns: one more where the first begins within one.
         const bool odd = (uintptr_t)src & 2;
+        if (odd && (src == first || src + C == last)) {      // a word that is in the buffer in half
+#pragma unroll
+            for (int i = 0; i < 2 * CT; ++i) b[i] = (uint32_t)src[2 * i] | (uint32_t)src[2 * i + 1] << 16;
+            return;
+        }
         const Words4* from = reinterpret_cast<const Words4*>((uintptr_t)src & ~(uintptr_t)3);
         uint32_t w[2 * CT + 1];
 #pragma unroll
@@ -333,7 +341,8 @@ __global__ __launch_bounds__(64 * W) void mnb_lora_up_kernel(LoraParams p)
 #pragma unroll
             for (int i = 0; i < 2 * CT; ++i) base[n][i] = 0;
             if (p.base && whole && row0 + 16 * n + r < p.m)
-                load_base<CT>(p.base + (row0 + 16 * n + r) * p.base_stride + mine0, base[n]);
+                load_base<CT>(p.base + (row0 + 16 * n + r) * p.base_stride + mine0, p.base,
+                              p.base + (p.m - 1) * p.base_stride + p.N, base[n]);
         }
     };
     if (CT > 1) read_base();

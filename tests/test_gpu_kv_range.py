@@ -332,3 +332,39 @@ def test_refusals_on_another_stream():
                             (TypeError, lambda: mnb.matmul_lora(x, ids, A, None, y, y, stream=stream))):
             with pytest.raises(error):
                 call()
+
+
+@pytest.mark.parametrize("N,stride", [(4096, 4096), (4096, 4097), (4112, 4113), (4097, 4097), (4100, 4101)])
+@pytest.mark.parametrize("dtype", [F16, BF16], ids=["f16", "bf16"])
+def test_base_at_the_ends_of_a_buffer(dtype, N, stride):
+    """Adapters over a base that begins and ends within a word, next to other
+    values: its first and last columns, and no value beside it."""
+    G.require_gpu()
+    m, K, rank, n = 600, 96, 16, 3
+    g = torch.Generator().manual_seed(N + stride)
+    x = torch.randn(m, K, generator=g).to(dtype)
+    ids = torch.randint(-1, n, (m,), generator=g).to(torch.int32)
+    A = (torch.randn(n, rank, K, generator=g) * 0.1).to(dtype)
+    B = torch.randn(n, N, rank, generator=g).to(dtype)
+    for at in (0, 1, 3):
+        for in_place in (False, True):
+            size = (m - 1) * stride + N
+            around = torch.full((at + size + 2,), float("nan"), dtype=dtype)
+            values = torch.randn(size, generator=g).to(dtype)
+            around[at:at + size] = values
+            dev = around.cuda()
+            base = torch.as_strided(dev, (m, N), (stride, 1), at)
+            room = dev if in_place else torch.full_like(dev, 5.0)
+            out = torch.as_strided(room, (m, N), (stride, 1), at)
+            want = base.clone()
+            plain = torch.empty(m, N, dtype=dtype, device="cuda")
+            mnb.matmul_lora(x.cuda(), ids.cuda(), A.cuda(), B.cuda(), want, plain)
+            before = room.clone()
+            mnb.matmul_lora(x.cuda(), ids.cuda(), A.cuda(), B.cuda(), base, out)
+            torch.cuda.synchronize()
+            assert torch.equal(out, plain)
+            inside = torch.zeros_like(room, dtype=torch.bool)
+            torch.as_strided(inside, (m, N), (stride, 1), at).fill_(True)
+            assert torch.equal(room[~inside].view(torch.int16), before[~inside].view(torch.int16))
+            if not in_place:
+                assert torch.equal(dev.cpu().view(torch.int16), around.view(torch.int16))
