@@ -448,10 +448,7 @@ __device__ __forceinline__ void turn_queries(const AppendParams& p, int64_t t)
     }
 }
 
-// Workgroups of four waves, or of one where a page gets 16 tokens or fewer on average:
-// of its few units the other waves would get few or none (8 heads of 128: 64
-// sequences of one token 9.7 -> 7.8 us, 200 of 16 33.8 -> 23.3, 200 of 32 on pages of 16
-// 70.6 -> 42.9; but one of 32 on a page of 64 7.2 -> 8.4 and of 256 wide 11.9 -> 19.7).
+// (Workgroups of one wave or of four: see append_one_wave.)
 template <int D, bool BF16, bool NEAR, int kThreads>
 __global__ __launch_bounds__(kThreads) void mnb_append_kernel(AppendParams p)
 {
@@ -525,10 +522,10 @@ int launch_append(const AppendArgs& a, void* stream)
     p.heads = (int32_t)a.cache.kv_heads;
     p.q_heads = (int32_t)a.q_heads;
     p.rot = (int32_t)a.rot_dim;
-    const int64_t T = a.batch.tokens, loose = T / a.cache.page_size + 2 * a.batch.sequences;
-    p.by_token = T <= loose;
-    p.slots = (int32_t)(p.by_token ? T : loose);
-    p.narrow = a.cache.page_size <= 16 || T <= 16 * a.batch.sequences;
+    const int64_t T = a.batch.tokens;
+    p.slots = (int32_t)append_slots(a.cache.page_size, T, a.batch.sequences);
+    p.by_token = p.slots == T;
+    p.narrow = append_one_wave(a.cache.page_size, T, a.batch.sequences, a.cache.kv_heads, a.cache.head_dim);
     const hipStream_t st = static_cast<hipStream_t>(stream);
     return a.cache.head_dim == 64 ? queue<64>(p, a, st) : a.cache.head_dim == 128 ? queue<128>(p, a, st) : queue<256>(p, a, st);
 }

@@ -218,6 +218,28 @@ struct AppendArgs {
 };
 int launch_append(const AppendArgs& args, void* stream) MNB_WEAK;
 
+// Page slots of the appending grid: a token touches one page, a sequence of n tokens
+// at most floor((n - 1) / P) + 2 (slot_base in mnb_append.hip).
+constexpr int64_t append_slots(int64_t page_size, int64_t tokens, int64_t sequences)
+{
+    const int64_t loose = tokens / page_size + 2 * sequences;
+    return tokens <= loose ? tokens : loose;
+}
+
+// Workgroups of one wave, or of four.  One where a page gets 16 tokens or fewer on
+// average, whose few units would leave the other waves none; and where there are
+// enough workgroups for two rounds of waves and a wave holds what a page gets (4096
+// elements) between its two looks at it.  8 heads of 128, one / four waves: 64
+// sequences of one token 7.7 / 9.7 us, 200 of 32 on pages of 64 34 / 44, 4 of 1800 43 /
+// 37, one of 64 16.0 / 7.0.  Against the times of both over 341 batches: 0.6% above the
+// faster on average (tests/data/kv_rules_gfx950.json).
+constexpr bool append_one_wave(int64_t page_size, int64_t tokens, int64_t sequences, int64_t heads, int64_t head_dim)
+{
+    const int64_t each = tokens / sequences < page_size ? tokens / sequences : page_size;
+    return page_size <= 16 || tokens <= 16 * sequences ||
+           (append_slots(page_size, tokens, sequences) * 2 * heads >= 1024 && each * head_dim <= 4096);
+}
+
 struct AttentionArgs {
     mnb_kv_cache cache;
     mnb_kv_batch batch;
