@@ -663,28 +663,29 @@ AttentionLayout attention_layout(int64_t tokens, int64_t sequences, int64_t q_he
 LoraLayout lora_layout(int64_t m, int64_t K, int64_t N, int64_t R, int64_t adapters)
 {
     LoraLayout l;
-    // 64 columns a wave, or 16 where that leaves compute units empty: 512 rows x 6144
-    // columns 20.7 -> 12.6 us; 64 rows x 14336, 32 adapters 71.3 wide, 33.2 narrow; 128 rows
-    // x 14336, 100 adapters 78.8, 65.4 (112 workgroups both).
-    l.wide = ceil_div(N, 512) * ceil_div(m, m <= 16 ? 16 : 32) >= 128;
-    // Tiles of 32 rows, whose adapters are read for one tile after another, or of 64 where
-    // those fill the device (narrow): 64 rows x 28672, 32 adapters, rank 64 58.0 -> 43.5 us;
-    // 40 rows x 16384 32.5 -> 36.5.
-    l.up_tiles = m <= 16 ? 1 : !l.wide && m > 32 && m <= 64 && R <= 128 && N > 64 * 384 ? 4 : 2;
+    // 64 columns a wave, or 16 where that leaves half of the compute units empty: 512 rows x
+    // 6144 columns 17.6 us wide, 23.8 narrow; 64 rows x 14336, 32 adapters 71.2, 32.9; 33 rows
+    // x 32768, 32 adapters (128 workgroups) 71.4, 39.0, x 36864, 8 adapters 16.9, 19.5.
+    l.wide = ceil_div(N, 512) * ceil_div(m, m <= 16 ? 16 : 32) > 128;
+    // Narrow: tiles of 32 rows, or of 64 where those, counted by their rows, are more than
+    // two workgroups a compute unit and an adapter would be read for one after another (64
+    // rows, 32 adapters, rank 64: x 16384 33.2 us with 32, 40.4 with 64; x 20480 53.4, 41.9;
+    // 40 rows x 20480 33.9, 38.2, x 28672 41.7, 39.1).  Against the times of all three over
+    // 166 shapes: 2.3% above the fastest on average (tests/data/kv_rules_gfx950.json).
+    l.up_tiles = m <= 16 ? 1 : !l.wide && R <= 128 && m * ceil_div(N, 64) > 32 * 512 ? 4 : 2;
     // The first launch: 512 rows, 14336 -> 16 15.8 us with 32, 17.9 with 64; 1024 rows of 8
     // adapters, 4096 -> 64 50.7 with 32, 44.7 with 64.
     l.down_tiles = m <= 16 ? 1 : m < 1024 || R > 128 ? 2 : 4;
     const int64_t rows = 16 * l.down_tiles, tiles = ceil_div(m, rows);
-    // Two workgroups a compute unit (256), of 256 or more of K each; slices cost the second
-    // launch their sums.  (Half or twice as many: within 4%.)
-    const int64_t splits = std::min<int64_t>(ceil_div(512, tiles), std::min<int64_t>(m <= 16 ? 16 : 8, std::max<int64_t>(1, K / 256)));
+    // Workgroups of 256 or more of K each; slices cost the second launch their sums.
+    const int64_t splits = std::min<int64_t>(ceil_div(kLoraDownWorkgroups, tiles), std::min<int64_t>(m <= 16 ? 16 : 8, std::max<int64_t>(1, K / 256)));
     const int64_t slice = ceil_div(ceil_div(K, splits), 128) * 128;
     l.k_slice = (int)std::max<int64_t>(128, slice);
     l.splits = (int)std::max<int64_t>(1, ceil_div(K, l.k_slice));
     // Rows may have an adapter each: workgroups that share a tile's adapters (64 rows of
     // 32 adapters, rank 64: one workgroup 188 us, these 33); those that get none end at
     // once (4096 rows in runs of 500: 90 us with or without them).
-    l.ways = (int)std::max<int64_t>(1, std::min<int64_t>(std::min(adapters, std::min(m, rows)), 512 / (tiles * l.splits)));
+    l.ways = (int)std::max<int64_t>(1, std::min<int64_t>(std::min(adapters, std::min(m, rows)), kLoraDownWorkgroups / (tiles * l.splits)));
     l.bytes = (size_t)l.splits * (size_t)m * (size_t)R * 4;
     return l;
 }

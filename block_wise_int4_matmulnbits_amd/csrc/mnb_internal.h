@@ -305,6 +305,9 @@ struct LoraLayout {
     bool wide;
     size_t bytes;
 };
+// Workgroups that the first launch is divided into, two a compute unit.  (Half as many
+// 0.2%, these 1.0%, twice as many 1.0% above the fastest on average over 24 shapes.)
+constexpr int kLoraDownWorkgroups = 512;
 LoraLayout lora_layout(int64_t m, int64_t K, int64_t N, int64_t R, int64_t adapters);
 
 }  // namespace mnb
