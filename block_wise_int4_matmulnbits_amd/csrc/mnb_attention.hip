@@ -46,12 +46,8 @@ typedef int i32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kWaves = 4;
 constexpr int kWorkgroups = kAttentionWorkgroups;
-constexpr int kBegin = 4;             // (2 / 4 / 8: one token over 2049 keys 12.8 / 10.4 / 10.4 us, 64 sequences of
-                                      // differing lengths, 4 / 8 / 16: 67 / 69 / 74)
+constexpr int kBegin = kAttentionBegin;
 constexpr int kGridTiles = 32768;     // tiles of a grid's y
-// Units that a tile's begin and end count as, that a share has at least, that the second
-// tile of a share and the joining launch cost more than whole tiles do.
-constexpr int kTileBegin = 4, kTileLeast = 2, kTileMore = 4, kTileJoin = 10;
 constexpr float kLowest = -3.0e38f;   // a running maximum before any key
 
 struct AttentionParams {
@@ -306,12 +302,10 @@ __device__ __forceinline__ Tile tile_of(const AttentionParams& p, const Sequence
     return t;
 }
 
-// Few tiles of many rows are cut into equal shares of the whole batch's work, a
-// workgroup each, unless whole tiles take no longer (32 heads on 8 of 128: 512 tokens over
-// 17000 keys whole 685 us, cut 207; 5000 over 20000 2109, 1868; 300 over their own 22, 33;
-// 4096 over their own 190, 224).  Tile i of a sequence sees about start + (i + 1) BR / G keys, and
-// counts as that and as kTileBegin units (64 keys) more; counts are in 1 / G of a key,
-// so that those of the tiles before i have a closed form.
+// The work of tiles (tiles_cut says when it is shared out).  Tile i of a sequence sees
+// about start + (i + 1) BR / G keys, and counts as that and as kTileBegin units (64 keys)
+// more; counts are in 1 / G of a key, so that those of the tiles before i have a closed
+// form.
 struct Count {
     int64_t first, tiles;     // of a tile but for its own rows; tiles of the sequence
     int32_t BR;
@@ -349,17 +343,8 @@ __device__ __forceinline__ Place place_of(const AttentionParams& p, const Sequen
     tiles = wave_sum(tiles);
     longest = wave_max(longest);
     r.all = counts.all;
-    const int64_t unit = (int64_t)p.G * 64, least = unit * kTileLeast;
-    r.share = divide(r.all + p.shares - 1, p.shares);
-    r.share = uniform64(r.share < least ? least : r.share);
-    // Whole tiles: rounds of them where all are about as long; else the longest first, and
-    // short ones behind them.
-    tiles *= p.heads;
-    const int64_t rounds = divide(tiles + p.shares - 1, p.shares);
-    const int64_t whole = 2 * (int64_t)longest * tiles <= 3 * r.all
-                              ? rounds * longest
-                              : max((int64_t)longest, divide(r.all, p.shares) + (longest >> 3));
-    r.cut = whole > r.share + unit * kTileMore + divide(unit * kTileJoin * r.all, r.share * p.shares);
+    r.share = uniform64(tile_share(divide(r.all + p.shares - 1, p.shares), p.G));
+    r.cut = tiles_cut(r.all, tiles * p.heads, longest, p.G, p.shares, r.share, [](int64_t a, int64_t b) { return divide(a, b); });
     const int64_t at = border * r.share;
     r.s = p.b.S;
     r.h = r.rt = 0;

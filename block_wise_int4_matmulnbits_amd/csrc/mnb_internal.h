@@ -265,9 +265,33 @@ constexpr int attention_many_rows(int64_t tokens, int64_t q_heads, int64_t head_
     return tokens * q_heads > 2048 ? 64 : head_dim <= 128 ? 256 : 128;
 }
 constexpr int kAttentionWorkgroups = 512;     // (256 / 512 / 1024: 64 sequences over 1000 keys 29 / 27 / 34 us, one over 131072 48 / 49 / 54)
+// Units that a row tile's begin and end count as in a share.  (2 / 4 / 8: one token over
+// 2049 keys 13.0 / 10.5 / 10.5 us, 7 sequences over 999 10.7 / 12.4 / 12.5; 11.3 / 3.8 / 5.3%
+// above the fastest of seven on average over 30 batches.)
+constexpr int kAttentionBegin = 4;
 constexpr int tile_waves(int64_t head_dim) { return head_dim >= 128 ? 8 : 4; }
 constexpr int tile_rows(int64_t head_dim) { return head_dim == 128 ? 256 : 128; }
 constexpr int tile_shares(int64_t head_dim) { return head_dim == 64 ? 512 : 256; }   // workgroups that run at a time
+
+// Few tiles of many rows are cut into equal shares of the whole batch's work, a
+// workgroup each, unless whole tiles take no longer (32 heads on 8 of 128: 512 tokens over
+// 17000 keys whole 685 us, cut 207; 5000 over 20000 2109, 1868; 300 over their own 22, 33;
+// 4096 over their own 190, 224).  all: their work, in 1 / G of a key; longest: a tile's.
+// Whole tiles take rounds of them where all are about as long; else the longest first,
+// and short ones behind them.  Units that a tile's begin and end count as, that a share has
+// at least, that the second tile of a share and the joining launch cost more than whole
+// tiles do:
+constexpr int kTileBegin = 4, kTileLeast = 2, kTileMore = 4, kTileJoin = 10;
+constexpr int64_t tile_share(int64_t share, int64_t G) { return share < 64 * G * kTileLeast ? 64 * G * kTileLeast : share; }
+template <class Divide>
+constexpr bool tiles_cut(int64_t all, int64_t tiles, int64_t longest, int64_t G, int64_t shares, int64_t share, Divide divide)
+{
+    const int64_t mixed = divide(all, shares) + (longest >> 3);
+    const int64_t whole = 2 * longest * tiles <= 3 * all ? divide(tiles + shares - 1, shares) * longest
+                          : longest > mixed              ? longest
+                                                         : mixed;
+    return whole > share + 64 * G * kTileMore + divide(64 * G * kTileJoin * all, share * shares);
+}
 
 // The attention's workspace.  Few rows: for each workgroup the sums of two row
 // tiles that it shares with others, behind their maxima and weights.  Many: the
