@@ -1053,7 +1053,7 @@ __global__ __launch_bounds__(64 * tile_waves(D), D == 64 ? 2 : 1) void mnb_atten
         // they would lose.  Keys behind a run do not count: rows may not see them.)
         if (!staged && n.valued) staged = __builtin_amdgcn_readlane(vs, __builtin_ctz(n.valued));
         const int32_t base = staged ? staged : kOne;
-        const bool near = !some || (uint32_t)(vs - base + 10 * kStep) <= 18u * kStep;
+        const bool near = !some || (uint32_t)vs - (uint32_t)base + 10u * kStep <= 18u * kStep;
         lane_ref = base;
         if (__builtin_amdgcn_ballot_w64(!near)) {
             const int32_t own = near ? base : vs;
