@@ -368,7 +368,8 @@ __device__ __forceinline__ Place place_of(const AttentionParams& p, const Sequen
     return r;
 }
 
-template <int D, bool BF16>
+// SMALL: pages of less than 64 tokens, several scales in a unit.
+template <int D, bool BF16, bool SMALL>
 __global__ __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) void mnb_attention_rows_kernel(AttentionParams p)
 {
     constexpr int KS = D / 64, DT = D / 16;
@@ -496,7 +497,7 @@ __global__ __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) void mnb_attention_r
             const int64_t at = (int64_t)(ok ? page : 0) * p.heads + h;
             const bool live = ok && c * 64 + 16 * g < q.length;
             ks = live ? p.k_scales[at] : 0.f;
-            vs = live || (ok && P >= 64) ? p.v_scales[at] : 0.f;
+            vs = live || (ok && !SMALL) ? p.v_scales[at] : 0.f;
         };
         auto values_at = [&](int c, int32_t page) {
             vp = p.v_pages + (((int64_t)(usable(page) ? page : 0) * p.heads + h) << p.b.page_bits) * D + (int64_t)r * P +
@@ -571,7 +572,7 @@ __global__ __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) void mnb_attention_r
             // 2^64 above that (its scores lie as far below) has its exponentials taken from
             // where it would reach it, so that no factor overflows.
             float step = 32512.f, f_o, from = m_from;
-            if (P >= 64) {
+            if constexpr (!SMALL) {
                 f_o = any ? f_weight * v_scale : 0.f;
             } else {
                 const bool seen = m_run != -__builtin_inff() && v_scale > 0.f;
@@ -1306,7 +1307,10 @@ int queue(const AttentionParams& p, const AttentionLayout& lay, hipStream_t stre
         if (e != 0) return e;
         ++*launches;
     }
-    hipLaunchKernelGGL((mnb_attention_rows_kernel<D, BF16>), dim3(kWorkgroups), dim3(64 * kWaves), 0, stream, p);
+    if (p.b.page_bits < 6)
+        hipLaunchKernelGGL((mnb_attention_rows_kernel<D, BF16, true>), dim3(kWorkgroups), dim3(64 * kWaves), 0, stream, p);
+    else
+        hipLaunchKernelGGL((mnb_attention_rows_kernel<D, BF16, false>), dim3(kWorkgroups), dim3(64 * kWaves), 0, stream, p);
     int e = (int)hipGetLastError();
     if (e != 0) return e;
     ++*launches;
