@@ -869,8 +869,9 @@ typedef float float16_t __attribute__((ext_vector_type(16)));
 
 // What a unit's runs need: the factor of the scores, 0 or -infinity to add, and
 // the units of the values.
+template <int RUNS>
 struct Runs {
-    float ks[4], bias[4];
+    float ks[RUNS], bias[RUNS];
     uint32_t spoilt;          // runs with a scale that is not finite
     uint32_t valued;          // runs with a value scale above zero
     uint32_t fractions;       // runs whose value scale is no power of two
@@ -894,9 +895,10 @@ __device__ __forceinline__ void widen_bytes(i32x4 w, uint32_t r2, uint32_t half_
     }
 }
 
-template <int D, bool BF16>
+template <int D, bool BF16, bool SMALL>
 __global__ __launch_bounds__(64 * tile_waves(D), D == 64 ? 2 : 1) void mnb_attention_tile_kernel(AttentionParams p)
 {
+    constexpr int RUNS = SMALL ? 4 : 1;                    // of a unit that differ
     constexpr int NW = tile_waves(D), BR = tile_rows(D), THREADS = 64 * NW;
     constexpr int SHARE = 32 * NW / BR;                    // waves that share rows, an equal part of the output each
     constexpr int KQ = D / 16, DB = D / 32 / SHARE;
@@ -1024,7 +1026,7 @@ __global__ __launch_bounds__(64 * tile_waves(D), D == 64 ? 2 : 1) void mnb_atten
         }
         lane_ok = usable(page);
         // Scales of a run behind the last key mean nothing.
-        const bool live = lane_ok && (P >= 64 || c * 64 + 16 * (lane & 3) < keys);
+        const bool live = lane_ok && (!SMALL || c * 64 + 16 * (lane & 3) < keys);
         const int64_t at_scale = (int64_t)safe * p.heads + h;
         lane_ks = live ? fabsf(p.k_scales[at_scale]) : 0.f;
         lane_vs = live ? fabsf(p.v_scales[at_scale]) : 0.f;
@@ -1032,10 +1034,10 @@ __global__ __launch_bounds__(64 * tile_waves(D), D == 64 ? 2 : 1) void mnb_atten
     int32_t unit_bits = 0;               // bits of the unit of this row's sums; 0: no sums yet
     int32_t unit_of_all = 0;             // the same, where all rows of the wave have one
     int32_t staged = 0, peak = 0;        // bits of the unit to go on with and of the largest so far: alike in all waves
-    Runs now;
+    Runs<RUNS> now;
     int32_t lane_ref;                    // of run lane % 4: bits of its sums' unit,
     float lane_r, lane_part;             // its value scale as a multiple of that, but for a fraction, and 1 / that
-    auto settle = [&](Runs& n) {
+    auto settle = [&](Runs<RUNS>& n) {
         // The value scale is a power of two, vs, times a fraction from 1 to 2, which goes to
         // the weights (1 where append_kv_int8 stored it).  Powers of two by their bits.
         constexpr int32_t kOne = 0x3F800000, kStep = 1 << 23;
@@ -1074,7 +1076,7 @@ __global__ __launch_bounds__(64 * tile_waves(D), D == 64 ? 2 : 1) void mnb_atten
         n.ref = __builtin_amdgcn_readlane(lane_ref, 0);
         n.group = (uint32_t)__builtin_amdgcn_ballot_w64(lane_ref == n.ref) & 15u;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < RUNS; ++i) {
             n.ks[i] = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(ks), i));
             n.bias[i] = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(bias), i));
         }
@@ -1157,12 +1159,12 @@ __global__ __launch_bounds__(64 * tile_waves(D), D == 64 ? 2 : 1) void mnb_atten
                 float factor[4], m = -__builtin_inff();
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const float f = q_scale * now.ks[e];
+                    const float f = q_scale * now.ks[e % RUNS];
                     factor[e] = f == 0.f ? 1e-37f : f;      // (a key that is not seen stands at -infinity)
                     float most = x[e >> 1][8 * (e & 1)];
 #pragma unroll
                     for (int j = 1; j < 8; ++j) most = fmaxf(most, x[e >> 1][8 * (e & 1) + j]);
-                    m = fmaxf(m, fmaf(most, factor[e], now.bias[e]));
+                    m = fmaxf(m, fmaf(most, factor[e], now.bias[e % RUNS]));
                 }
                 m = xor32_max(m);
                 // The maximum is followed in steps of 2^6 at least: weights stay below
@@ -1190,7 +1192,7 @@ __global__ __launch_bounds__(64 * tile_waves(D), D == 64 ? 2 : 1) void mnb_atten
                         pairs[j] = half_pair(a, b);
                         sum = dot2(pairs[j], 0x3C003C00u, sum);
                     }
-                    weight = fmaf(sum, __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(lane_part), e)), weight);
+                    weight = fmaf(sum, __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(lane_part), e % RUNS)), weight);
                     return __builtin_bit_cast(half8_t, pairs);
                 };
                 // The runs of one unit of the sums at a time: all of them, but where their
@@ -1201,7 +1203,7 @@ __global__ __launch_bounds__(64 * tile_waves(D), D == 64 ? 2 : 1) void mnb_atten
                     left &= ~group;
                     float from[4];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) from[e] = group >> e & 1 ? now.bias[e] - top : -__builtin_inff();
+                    for (int e = 0; e < 4; ++e) from[e] = !SMALL || (group >> e & 1) ? now.bias[e % RUNS] - top : -__builtin_inff();
                     // A row's unit changes where it sees a value of the new one only.
                     const uint32_t valued = group & now.valued;
                     if (valued && ref != unit_of_all) {
@@ -1215,7 +1217,7 @@ __global__ __launch_bounds__(64 * tile_waves(D), D == 64 ? 2 : 1) void mnb_atten
                     if (now.fractions)
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
-                            from[e] -= __log2f(__uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(lane_part), e)));
+                            from[e] -= __log2f(__uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(lane_part), e % RUNS)));
                     asm("" : "+v"(from_v));       // the loop's own loads: 16 pieces are too many to keep
                     half8_t va[2][DB];
                     values(0, va[0]);
@@ -1227,7 +1229,7 @@ __global__ __launch_bounds__(64 * tile_waves(D), D == 64 ? 2 : 1) void mnb_atten
                         for (int d = 0; d < DB; ++d)
                             o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(va[e & 1][d], w, o[d], 0, 0, 0);
                     }
-                    if (!left) break;
+                    if (!SMALL || !left) break;
                     ref = __builtin_amdgcn_readlane(lane_ref, __builtin_ctz(left));
                     group = (uint32_t)__builtin_amdgcn_ballot_w64(lane_ref == ref) & left;
                 }
@@ -1302,7 +1304,10 @@ int queue(const AttentionParams& p, const AttentionLayout& lay, hipStream_t stre
     const dim3 tiles((unsigned)p.heads, (unsigned)std::min(rows, kGridTiles), (unsigned)((rows + kGridTiles - 1) / kGridTiles));
     if (p.tile_slots) {
         constexpr size_t lds = (size_t)4 * (64 * (D + 8) + D * 72);
-        hipLaunchKernelGGL((mnb_attention_tile_kernel<D, BF16>), tiles, dim3(64 * tile_waves(D)), lds, stream, p);
+        if (p.b.page_bits < 6)
+            hipLaunchKernelGGL((mnb_attention_tile_kernel<D, BF16, true>), tiles, dim3(64 * tile_waves(D)), lds, stream, p);
+        else
+            hipLaunchKernelGGL((mnb_attention_tile_kernel<D, BF16, false>), tiles, dim3(64 * tile_waves(D)), lds, stream, p);
         const int e = (int)hipGetLastError();
         if (e != 0) return e;
         ++*launches;
