@@ -19,13 +19,14 @@
 //   operand of the second product wants of it.
 // * outputs: 16 elements (A: v with its tokens last) x 16 rows, 64 tokens deep.
 //   The weights of a unit, largest 1 in each row, are held in 16 bits as two
-//   digits: off by 2^-16 of the largest at most, as the 32-bit sums of the
-//   products of two fp16 values would be off by 2^-12 of each.
+//   digits: off by 1 / 65024 of the largest at most, where fp16 weights would be
+//   off by 2^-11 of each.  (A third digit spills: heads of 128 102 -> 144 us in the
+//   batch below, of 256 213 -> 367.)
 //
 // The batch's units are shared out evenly over a fixed number of workgroups, whose
 // sums of the (at most two) row tiles that others share too are joined by a second
 // launch, a workgroup for each border between two shares.  64 sequences of one token
-// over 4000 keys, 32 heads on 8, read 5.7 / 5.2 / 4.9 TB/s with heads of 64 / 128 / 256
+// over 4000 keys, 32 heads on 8, read 5.7 / 5.1 / 4.9 TB/s with heads of 64 / 128 / 256
 // (a plain read of as much 7.0); one token over 2049 keys takes 11 us, two launches of
 // dependent loads.
 #include <hip/hip_runtime.h>
@@ -847,10 +848,12 @@ __global__ __launch_bounds__(kJoinThreads) void mnb_attention_join_kernel(Attent
 //   a lane ends with eight neighbouring keys of each 16: the B operand of the
 //   second product.
 // * outputs: 32 elements (A) x 32 rows, 16 keys deep, the same order, so that a
-//   lane stores eight neighbouring elements.  Weights in fp16 (2^-11 of each).
+//   lane stores eight neighbouring elements.  Weights in fp16 (2^-11 of each, which
+//   goes into their sum as well): a second piece of them would double this product.
 //
-// Sixteen keys (a run) have one value scale, which stands as a multiple r of the
-// sums' unit.  The unit changes, and the sums with it, only where r would leave
+// Sixteen keys (a run), or a unit of pages of 64 and more, have one value scale, which
+// stands as r times the sums' unit, r a power of two; the rest of the scale goes to the
+// weights (not to their sum).  The unit changes, and the sums with it, only where r would leave
 // 2^-10 .. 2^8, so that no weight times scale falls out of fp16's range, whatever
 // the pages before it held, and pages of differing scales cost nothing.  A row's
 // unit follows the keys that it sees: scales of later ones, which rows further down
@@ -859,7 +862,7 @@ __global__ __launch_bounds__(kJoinThreads) void mnb_attention_join_kernel(Attent
 // A unit of a tile of 256 rows and heads of 128 takes 2.6 us on its compute unit, of which
 // the products are 1.8 at the rate of a large fp16 library product: the exponentials and
 // the conversion of the integers hide in part only, as the waves of a workgroup meet at
-// a barrier every unit.  2.6 us is 840 TFLOP/s where all units have keys (one sequence of
+// a barrier every unit.  2.6 us is 836 TFLOP/s where all units have keys (one sequence of
 // 16384); a prompt's short tiles end sooner than they begin.  Eight waves of 32 rows,
 // because fewer rows convert the integers more often (four waves of 128 rows: the
 // same time); heads of 256 have two waves to 32 rows, as the outputs of one would not

@@ -556,7 +556,7 @@ int append_kv_int8(const mnb_kv_cache* cache, const mnb_kv_batch* batch, int dty
  * Numerics: scores of the integers exact but for what lies below 2^-22 of a
  * query's largest element (or below 2^-123) and the steps of fp32 sums, softmax
  * with the running maximum and sum in fp32.  Weights are held in 16 bits: off by
- * 2^-16 of the largest weight times value scale of 64 keys, or, with many rows,
+ * 1 / 65024 of the largest weight times value scale of 64 keys, or, with many rows,
  * by 2^-11 of themselves and 2^-24 of the row's largest.  Sums in fp32, one
  * rounding (RNE); value scales that differ by more than 2^80 within a row's keys
  * may lose the smaller ones.  Scales are powers of two as append_kv_int8 stores
