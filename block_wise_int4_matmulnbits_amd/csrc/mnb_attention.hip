@@ -576,7 +576,7 @@ __global__ __launch_bounds__(64 * kWaves, D <= 128 ? 2 : 1) void mnb_attention_r
             if constexpr (!SMALL) {
                 f_o = any ? f_weight * v_scale : 0.f;
             } else {
-                const bool seen = m_run != -__builtin_inff() && v_scale > 0.f;
+                const bool seen = m_run != -__builtin_inff() && v_scale >= 0x1p-126f;     // (log2 takes no smaller ones)
                 const float n_unit = xor16_max(seen ? m_run + __log2f(v_scale) : -__builtin_inff());
                 const bool some = n_unit != -__builtin_inff();
                 const float up = some ? n_unit - m_from : 0.f;

@@ -125,6 +125,21 @@ def test_small_value_scales(e, first, P):
     R.check_rows(got, want, tol, BF16)
 
 
+def test_value_scales_below_the_normal_range():
+    """Scales under 2^-126 count for something between nothing and what they are."""
+    G.require_gpu()
+    for P in (16, 32, 64):
+        for gap in (0, 10, 40):
+            b = _scored([64, 200], P, 64, (0, -gap, -gap), (2.0 ** -130, 2.0 ** -124, 2.0 ** -149))
+            q = _unit_queries(2, 2, 64)
+            got = ATT._call(b, q, scale=1.0)
+            with_them = _few_rows(b, q, 1.0)
+            b.v_scales[b.v_scales < 2.0 ** -126] = 0
+            without = _few_rows(b, q, 1.0)
+            tol = torch.maximum(with_them[1], without[1]) + (with_them[0] - without[0]).abs() / 2
+            R.check_rows(got, (with_them[0] + without[0]) / 2, tol, BF16)
+
+
 @pytest.mark.parametrize("hq,new", [(16, 40), (64, 70)], ids=["shares", "tiles"])
 @pytest.mark.parametrize("P", [16, 32, 64])
 @pytest.mark.parametrize("es", [(-5, -70, -126), (0, -80, -126), (100, 30, -40, -110), (-126, -60, 10, 90), (-126, 0),
