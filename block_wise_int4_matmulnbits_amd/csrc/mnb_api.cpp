@@ -1239,6 +1239,7 @@ int matmul_lora(const void* x, int x_dtype, int64_t x_stride, int64_t m, int64_t
     int st = check_lora_shape(m, K, N, rank, adapters);
     if (st != MNB_OK) return st;
     const int64_t most = (int64_t)1 << 40;
+    if (K == 0) x_stride = 0;      // rows of nothing, wherever they are said to be
     if (m > 1 && (x_stride < K || x_stride % 8 || x_stride > most || out_stride < N || out_stride > most ||
                   (base && (base_stride < N || base_stride > most))))
         return MNB_ERR_SHAPE;

@@ -590,8 +590,8 @@ size_t mnb_attention_workspace(int64_t tokens, int64_t sequences, int64_t q_head
  *   out[r] = base[r] + scaling[a] * B[a] (A[a] x[r]),   a = ids[r]
  *
  *   x             device, [m][K] fp16 or bf16 per x_dtype, x_stride elements from
- *                 one row to the next (at least K, a multiple of 8); 16-byte
- *                 aligned.
+ *                 one row to the next (at least K, a multiple of 8; any with K 0);
+ *                 16-byte aligned.
  *   m, K, N       0 <= m <= MNB_MAX_ROWS; K a multiple of 16, 0 <= K <= MNB_MAX_K;
  *                 0 <= N <= MNB_MAX_N_INT8.
  *   rank          R: a multiple of 8, 8 .. MNB_LORA_MAX_RANK (an adapter of a

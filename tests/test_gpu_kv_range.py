@@ -349,6 +349,21 @@ def test_refusals_on_another_stream():
                 call()
 
 
+def test_adapters_of_no_columns():
+    """x of no columns, as torch lays it out (its rows one element apart): the base."""
+    G.require_gpu()
+    for m in (1, 2, 70):
+        for n in (0, 3):
+            x, A = torch.zeros(m, 0, dtype=F16, device="cuda"), torch.zeros(n, 8, 0, dtype=F16, device="cuda")
+            B = torch.ones(n, 30, 8, dtype=F16, device="cuda")
+            base = torch.randn(m, 30, device="cuda").to(F16)
+            ids = torch.zeros(m, dtype=torch.int32, device="cuda")
+            out = torch.empty_like(base)
+            mnb.matmul_lora(x, ids, A, B, base, out)
+            torch.cuda.synchronize()
+            assert torch.equal(out, base)
+
+
 @pytest.mark.parametrize("N,stride", [(4096, 4096), (4096, 4097), (4112, 4113), (4097, 4097), (4100, 4101)])
 @pytest.mark.parametrize("dtype", [F16, BF16], ids=["f16", "bf16"])
 def test_base_at_the_ends_of_a_buffer(dtype, N, stride):
