@@ -671,7 +671,7 @@ LoraLayout lora_layout(int64_t m, int64_t K, int64_t N, int64_t R, int64_t adapt
     // two workgroups a compute unit and an adapter would be read for one after another (64
     // rows, 32 adapters, rank 64: x 16384 33.2 us with 32, 40.4 with 64; x 20480 53.4, 41.9;
     // 40 rows x 20480 33.9, 38.2, x 28672 41.7, 39.1).  Against the times of all three over
-    // 166 shapes: 2.3% above the fastest on average (tests/data/kv_rules_gfx950.json).
+    // 160 shapes: 2.4% above the fastest on average (tests/data/kv_rules_gfx950.json).
     l.up_tiles = m <= 16 ? 1 : !l.wide && R <= 128 && m * ceil_div(N, 64) > 32 * 512 ? 4 : 2;
     // The first launch: 512 rows, 14336 -> 16 15.8 us with 32, 17.9 with 64; 1024 rows of 8
     // adapters, 4096 -> 64 50.7 with 32, 44.7 with 64.

@@ -19,12 +19,12 @@ DATA = os.path.join(os.path.dirname(os.path.abspath(__file__)), "data", "kv_rule
 LIMITS = {      # mean, worst
     "append_threads": (1.007, 1.30),
     "attention_many_rows": (1.12, 2.40),
-    "attention_cut": (1.05, 1.30),
+    "attention_cut": (1.02, 1.25),
     "attention_shares": (1.04, 1.26),
     "lora_up": (1.025, 1.31),
     "lora_up_few": (1.002, 1.04),
     "lora_down": (1.02, 1.13),
-    "lora_splits": (1.015, 1.09),
+    "lora_splits": (1.015, 1.08),
 }
 
 
